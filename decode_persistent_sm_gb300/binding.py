@@ -19,7 +19,7 @@ STATUS = {
 }
 
 # Every function declared in include/laneformer.h with its ctypes signature.
-_vp, _ci, _i32, _f32 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int32, ctypes.c_float
+_vp, _ci, _i32, _i64, _f32 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
 _SIGS = {
     "lf_validate_config": (_ci, [_vp]),
     "lf_create": (_ci, [_vp, ctypes.POINTER(_vp)]),
@@ -65,6 +65,12 @@ _SIGS = {
     "lf_batch_generate": (_ci, [_vp, _vp, _ci, ctypes.c_float, ctypes.c_float, ctypes.c_uint64, _vp]),
     "lf_gemv_f16": (_ci, [_vp, _vp, _vp, _ci, _ci, _ci, _vp]),
     "lf_stream_read": (_ci, [_vp, ctypes.c_size_t, _vp, _ci, _vp, _vp]),
+    "lf_kv_append_paged": (_ci, [_vp, _vp, _vp, _vp, _ci, _i64, _i64, _i64, _ci, _vp, _i64, _vp, _vp, _ci, _vp, _ci, _vp,
+                                 _vp]),
+    "lf_attn_paged_shared": (_ci, [_vp, _vp, _i64, _vp, _i64, _vp, _ci, _vp, _ci, _ci, _ci, _f32, _vp, ctypes.c_size_t,
+                                   _vp, _vp]),
+    "lf_attn_paged_shared_workspace": (ctypes.c_size_t, [_vp, _ci]),
+    "lf_sample_filtered": (_ci, [_vp, _ci, _ci, _ci, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
     "lf_debug_canaries": (_ci, [_vp, ctypes.POINTER(_ci)]),
     "lf_debug_corrupt_canary": (_ci, [_vp, _ci, _ci]),
 }
@@ -77,6 +83,14 @@ class LfConfig(ctypes.Structure):
         ("dtp_delay", _ci), ("ctx_cap", _ci), ("rms_eps", _f32), ("rope_theta", _f32),
         ("swa_window", _ci * MAX_LAYERS), ("own_lane_immediate", _ci),
     ]
+
+
+DTYPES = {"f32": 0, "f16": 1, "bf16": 2}  # lf_dtype
+
+
+class LfPagedKV(ctypes.Structure):
+    _fields_ = [("k", _vp), ("v", _vp), ("page_table", _vp), ("n_pages", _ci), ("n_kv_heads", _ci), ("page_size", _ci),
+                ("head_dim", _ci), ("n_seqs", _ci), ("max_pages", _ci), ("dtype", _ci), ("page_stride", _i64)]
 
 
 class LaneformerError(RuntimeError):
@@ -175,6 +189,55 @@ def sample_token(logits_ptr: int, vocab: int, temperature: float, top_p: float, 
     lib = load_library()
     _check("lf_sample", lib.lf_sample(logits_ptr, int(vocab), float(temperature), float(top_p),
                                       int(seed) & (2 ** 64 - 1), int(position), int(sample), token_ptr, stream))
+
+
+def paged_kv(k_ptr: int, v_ptr: int, page_table_ptr: int, *, n_pages: int, n_kv_heads: int, page_size: int,
+             head_dim: int, n_seqs: int, max_pages: int, dtype: str, page_stride: int = 0) -> LfPagedKV:
+    """lf_paged_kv: the description of a paged KV cache (device pointers; dtype
+    "f16" or "bf16"; layout and limits in laneformer.h)."""
+    return LfPagedKV(k_ptr, v_ptr, page_table_ptr, int(n_pages), int(n_kv_heads), int(page_size), int(head_dim),
+                     int(n_seqs), int(max_pages), DTYPES[dtype], int(page_stride))
+
+
+def kv_append_paged(kv: LfPagedKV, q_ptr: int, k_ptr: int, v_ptr: int, in_dtype: str, ld_q: int, ld_k: int, ld_v: int,
+                    n_q_heads: int, q_out_ptr: int, ld_q_out: int, seq_ptr: Optional[int], pos_ptr: int, n_tokens: int,
+                    rope_ptr: Optional[int], rope_len: int, err_ptr: int, stream: Optional[int] = None):
+    """lf_kv_append_paged: enqueue the RoPE of n_tokens tokens' queries and keys
+    and the append of their keys and values to a paged cache."""
+    rc = load_library().lf_kv_append_paged(ctypes.byref(kv), q_ptr, k_ptr, v_ptr, DTYPES[in_dtype], ld_q, ld_k, ld_v,
+                                           n_q_heads, q_out_ptr, ld_q_out, seq_ptr, pos_ptr, n_tokens, rope_ptr,
+                                           rope_len, err_ptr, stream)
+    if rc:
+        _check("lf_kv_append_paged", rc)
+
+
+def attn_paged_shared_workspace(kv: LfPagedKV, n_q_heads: int) -> int:
+    """lf_attn_paged_shared_workspace: bytes of scratch one call needs on the
+    current device (0: the call would refuse the sizes)."""
+    return load_library().lf_attn_paged_shared_workspace(ctypes.byref(kv), n_q_heads)
+
+
+def attn_paged_shared(kv: LfPagedKV, q_ptr: int, ld_q: int, out_ptr: int, ld_out: int, lse_ptr: Optional[int],
+                      n_q_heads: int, lens_ptr: int, max_len: int, shared_len: int, window: int, scale: float,
+                      workspace_ptr: int, workspace_bytes: int, err_ptr: int, stream: Optional[int] = None):
+    """lf_attn_paged_shared: enqueue the decode attention of a batch whose
+    sequences share their first shared_len cached positions."""
+    rc = load_library().lf_attn_paged_shared(ctypes.byref(kv), q_ptr, ld_q, out_ptr, ld_out, lse_ptr, n_q_heads,
+                                             lens_ptr, max_len, shared_len, window, scale, workspace_ptr,
+                                             workspace_bytes, err_ptr, stream)
+    if rc:
+        _check("lf_attn_paged_shared", rc)
+
+
+def sample_filtered(logits_ptr: int, dtype: str, rows: int, vocab: int, ld: int, temperature_ptr: Optional[int],
+                    top_k_ptr: Optional[int], top_p_ptr: Optional[int], min_p_ptr: Optional[int], u_ptr: int,
+                    token_ptr: int, logprob_ptr: Optional[int] = None, stream: Optional[int] = None):
+    """lf_sample_filtered: enqueue one draw per row of device logits under
+    temperature, top-k, top-p and min-p from given uniform numbers."""
+    rc = load_library().lf_sample_filtered(logits_ptr, DTYPES[dtype], rows, vocab, ld, temperature_ptr, top_k_ptr,
+                                           top_p_ptr, min_p_ptr, u_ptr, token_ptr, logprob_ptr, stream)
+    if rc:
+        _check("lf_sample_filtered", rc)
 
 
 def validate_config(cfg: LfConfig) -> int:

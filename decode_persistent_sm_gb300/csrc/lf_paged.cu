@@ -1,0 +1,212 @@
+// Append to a paged KV cache with RoPE on the way: the queries and keys of
+// each token rotated by its position, keys and values written to the page
+// its sequence's table names.
+//
+//   y[c] = x[c] cos - x[c + h] sin,  y[c + h] = x[c] sin + x[c + h] cos,
+//   h = head_dim / 2, (cos, sin) = rope[position][c]
+//
+// in fp32, rounded once to the cache's type (values: rounded, not rotated).
+// A unit of work is 8 pairs of one head of one token: two 16-byte stores (and
+// as wide loads as the input's type gives), the same two pieces that the
+// rotation couples.  A thread keeps one pair range c .. c + 7 of one token and
+// walks the heads, so its cos and sin are read once.  The bound is HBM: every
+// value is read and written once.
+#include "lf_paged.h"
+
+namespace lf {
+namespace {
+
+constexpr int kAppendThreads = 256;
+constexpr int kAppendHeads = 2;  // heads per thread whose loads are in flight together
+
+struct AppendArgs {
+    PagedView kv;
+    const void *q, *k, *v;
+    long long ld_q, ld_k, ld_v, ld_qo;
+    void *qo;
+    int n_q;
+    const int32_t *seq, *pos;
+    int n_tokens;
+    const float *rope;
+    int rope_len;
+    uint32_t *err;
+};
+
+// 8 consecutive values as fp32.
+__device__ __forceinline__ void load8(const float *p, float (&f)[8]) {
+    const float4 a = __ldg(reinterpret_cast<const float4 *>(p)), b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
+    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+}
+// (16-bit inputs may be the output array itself, rotated in place: plain loads)
+__device__ __forceinline__ void load8(const __half *p, float (&f)[8]) {
+    const uint4 u = *reinterpret_cast<const uint4 *>(p);
+    const __half2 *h = reinterpret_cast<const __half2 *>(&u);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 t = __half22float2(h[i]);
+        f[2 * i] = t.x, f[2 * i + 1] = t.y;
+    }
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float (&f)[8]) {
+    const uint4 u = *reinterpret_cast<const uint4 *>(p);
+    const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&u);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 t = __bfloat1622float2(h[i]);
+        f[2 * i] = t.x, f[2 * i + 1] = t.y;
+    }
+}
+__device__ __forceinline__ void store8(__half *p, const float (&f)[8]) {
+    __half2 h[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+    *reinterpret_cast<uint4 *>(p) = *reinterpret_cast<const uint4 *>(h);
+}
+__device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&f)[8]) {
+    __nv_bfloat162 h[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+    *reinterpret_cast<uint4 *>(p) = *reinterpret_cast<const uint4 *>(h);
+}
+
+// Block = head_dim / 16 pair ranges x head slots, blockIdx.x = token,
+// blockIdx.y = share of the token's heads.
+template <typename TI, typename TO>
+__global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendArgs a) {
+    const int DH = a.kv.head_dim, half = DH / 2, pieces = DH / 16;
+    const int piece = threadIdx.x % pieces, slot = threadIdx.x / pieces, slots = blockDim.x / pieces;
+    const int t = blockIdx.x, heads = a.n_q + 2 * a.kv.n_kv;
+    const int seq = a.seq ? a.seq[t] : t;
+    if (seq < 0) return;  // padding
+    const int p = a.pos[t];
+    int page = -1;
+    if (seq < a.kv.n_seqs && p >= 0 && (p >> a.kv.ps_log2) < a.kv.max_pages && (!a.rope || p < a.rope_len))
+        page = a.kv.table[(long long)seq * a.kv.max_pages + (p >> a.kv.ps_log2)];
+    if (page < 0 || page >= a.kv.n_pages) {
+        if (threadIdx.x == 0 && blockIdx.y == 0) atomicExch(a.err, 1u);
+        return;
+    }
+    const int row = p & ((1 << a.kv.ps_log2) - 1), c0 = piece * 8;
+    float cs[8], sn[8];
+    if (a.rope) {
+        const float4 *r = reinterpret_cast<const float4 *>(a.rope + ((long long)p * half + c0) * 2);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float4 x = __ldg(r + i);
+            cs[2 * i] = x.x, sn[2 * i] = x.y, cs[2 * i + 1] = x.z, sn[2 * i + 1] = x.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) cs[i] = 1.f, sn[i] = 0.f;
+    }
+    const int step = slots * gridDim.y;
+    for (int h0 = slot + slots * blockIdx.y; h0 < heads; h0 += kAppendHeads * step) {
+        float lo[kAppendHeads][8], hi[kAppendHeads][8];
+#pragma unroll
+        for (int u = 0; u < kAppendHeads; ++u) {
+            const int h = h0 + u * step;
+            if (h >= heads) break;
+            const TI *src;
+            if (h < a.n_q)
+                src = static_cast<const TI *>(a.q) + (long long)t * a.ld_q + (long long)h * DH;
+            else if (h < a.n_q + a.kv.n_kv)
+                src = static_cast<const TI *>(a.k) + (long long)t * a.ld_k + (long long)(h - a.n_q) * DH;
+            else
+                src = static_cast<const TI *>(a.v) + (long long)t * a.ld_v + (long long)(h - a.n_q - a.kv.n_kv) * DH;
+            load8(src + c0, lo[u]);
+            load8(src + half + c0, hi[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < kAppendHeads; ++u) {
+            const int h = h0 + u * step;
+            if (h >= heads) break;
+            TO *dst;
+            if (h < a.n_q) {
+                dst = static_cast<TO *>(a.qo) + (long long)t * a.ld_qo + (long long)h * DH;
+            } else {
+                const int g = (h - a.n_q) % a.kv.n_kv;
+                TO *base = static_cast<TO *>(h < a.n_q + a.kv.n_kv ? a.kv.k : a.kv.v);
+                dst = base + page * a.kv.page_stride + ((((long long)g << a.kv.ps_log2) + row) * DH);
+            }
+            if (a.rope && h < a.n_q + a.kv.n_kv) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float x = lo[u][i], y = hi[u][i];
+                    lo[u][i] = x * cs[i] - y * sn[i];
+                    hi[u][i] = x * sn[i] + y * cs[i];
+                }
+            }
+            store8(dst + c0, lo[u]);
+            store8(dst + half + c0, hi[u]);
+        }
+    }
+}
+
+template <typename TI, typename TO>
+void launch_append(const AppendArgs &a, cudaStream_t st) {
+    const int pieces = a.kv.head_dim / 16;  // 1 .. 16
+    const int threads = kAppendThreads / pieces * pieces, slots = threads / pieces;
+    const int heads = a.n_q + 2 * a.kv.n_kv;
+    const int y = (heads + slots * kAppendHeads - 1) / (slots * kAppendHeads);
+    kv_append_kernel<TI, TO><<<dim3((unsigned)a.n_tokens, (unsigned)y), threads, 0, st>>>(a);
+}
+
+template <typename TI>
+void launch_append_to(const AppendArgs &a, int dtype, cudaStream_t st) {
+    if (dtype == LF_F16)
+        launch_append<TI, __half>(a, st);
+    else
+        launch_append<TI, __nv_bfloat16>(a, st);
+}
+
+}  // namespace
+}  // namespace lf
+
+extern "C" lf_status lf_kv_append_paged(const lf_paged_kv *kv, const void *q_in, const void *k_in, const void *v_in,
+                                        int in_dtype, int64_t ld_q, int64_t ld_k, int64_t ld_v, int n_q_heads,
+                                        void *q_out, int64_t ld_q_out, const int32_t *seq_device,
+                                        const int32_t *pos_device, int n_tokens, const float *rope_device, int rope_len,
+                                        uint32_t *err_device, void *cuda_stream) {
+    lf::AppendArgs a;
+    const lf_status vs = lf::paged_view(kv, &a.kv);
+    if (vs != LF_OK) return vs;
+    const int bytes = lf::dtype_bytes(in_dtype);
+    if (!bytes || n_tokens < 0 || n_q_heads < 0 || n_q_heads > (1 << 16) || kv->n_kv_heads > (1 << 16) || !k_in ||
+        !v_in || !pos_device || !err_device || (reinterpret_cast<uintptr_t>(err_device) & 3u) ||
+        (reinterpret_cast<uintptr_t>(pos_device) & 3u) || (reinterpret_cast<uintptr_t>(seq_device) & 3u))
+        return LF_ERR_INVALID_ARG;
+    const int64_t q_row = (int64_t)n_q_heads * kv->head_dim, kv_row = (int64_t)kv->n_kv_heads * kv->head_dim;
+    if (ld_k < kv_row || ld_v < kv_row || ld_k * bytes % 16 || ld_v * bytes % 16 || !lf::aligned16(k_in) ||
+        !lf::aligned16(v_in))
+        return LF_ERR_INVALID_ARG;
+    if (n_q_heads > 0 && (!q_in || !q_out || ld_q < q_row || ld_q_out < q_row || ld_q * bytes % 16 ||
+                          ld_q_out % 8 || !lf::aligned16(q_in) || !lf::aligned16(q_out)))
+        return LF_ERR_INVALID_ARG;
+    if (n_q_heads > 0 && q_in == q_out && (in_dtype != kv->dtype || ld_q != ld_q_out)) return LF_ERR_INVALID_ARG;
+    if (rope_device && (rope_len < 1 || !lf::aligned16(rope_device))) return LF_ERR_INVALID_ARG;
+    if (!seq_device && n_tokens > kv->n_seqs) return LF_ERR_INVALID_ARG;
+    if (n_tokens == 0) return LF_OK;
+    a.q = q_in;
+    a.k = k_in;
+    a.v = v_in;
+    a.ld_q = ld_q;
+    a.ld_k = ld_k;
+    a.ld_v = ld_v;
+    a.qo = q_out;
+    a.ld_qo = ld_q_out;
+    a.n_q = n_q_heads;
+    a.seq = seq_device;
+    a.pos = pos_device;
+    a.n_tokens = n_tokens;
+    a.rope = rope_device;
+    a.rope_len = rope_len;
+    a.err = err_device;
+    cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
+    if (in_dtype == LF_F32)
+        lf::launch_append_to<float>(a, kv->dtype, st);
+    else if (in_dtype == LF_F16)
+        lf::launch_append_to<__half>(a, kv->dtype, st);
+    else
+        lf::launch_append_to<__nv_bfloat16>(a, kv->dtype, st);
+    return cudaGetLastError() == cudaSuccess ? LF_OK : LF_ERR_CUDA;
+}

@@ -1,0 +1,761 @@
+// Decode attention over a paged cache for a batch whose sequences share their
+// first positions: o = softmax(scale q K^T) V per query head, one query token
+// per sequence.
+//
+// What bounds it is reading K and V: 4 head_dim bytes per (position, KV head)
+// against 4 head_dim FLOP per (position, query head).  The common positions
+// are therefore read once for all sequences: the rows (sequence, query head)
+// of one KV head are the M side of one product with a tile of common keys,
+// 64 rows at a time.  Only positions that every sharing sequence sees are
+// treated so (from the latest window start to shared_len); what a sequence
+// sees besides goes through its own items, so no masked position ever enters
+// a product.
+//
+// Work is cut into tiles of 64 keys.  An item is (KV head, row tile) of the
+// common range or (sequence, KV head) of the own ranges; all tiles of all
+// items form one list, cut into equal contiguous shares, one per CTA, so ragged
+// lengths and short batches fill the GPU alike.  A CTA walks its share with a
+// two-stage cp.async ring that runs on across item borders, and leaves one
+// partial (unnormalised o, max, sum) per item it touches: slot item + CTA,
+// which is unique because both only grow along the list.  A second kernel,
+// launched to overlap the first one's end, joins each row's partials in list
+// order.
+//
+// One tile: S = Q K^T and O += P V on warp-level MMAs (m16n8k16, fp32
+// accumulators), softmax statistics in registers.  The four warps take 16-row
+// blocks (rows > 16) and 16-key blocks (what is left), each warp its own
+// running maximum; warps that shared rows join in shared memory at the item's
+// end.  P is rounded to the cache's type for the second product (as the other
+// operand is); its sum is taken before the rounding.
+#include <climits>
+
+#include "lf_paged.h"
+#include "lf_ptx.cuh"
+
+namespace lf {
+namespace {
+
+constexpr int PA_THREADS = 128, PA_KT = 64, PA_ROWS = 64, PA_MAX_SEQS = 1024, PA_MAX_GROUP = 16;
+constexpr int PA_CTAS_PER_SM = 2;
+constexpr int PA_MERGE_THREADS = 128;
+constexpr float kLog2e = 1.4426950408889634f;
+
+struct AttnArgs {
+    PagedView kv;
+    const void *q;
+    void *out;
+    float *lse;
+    long long ld_q, ld_out;
+    int n_q, group;  // query heads, query heads per KV head
+    const int32_t *lens;
+    int max_len, shared, window;
+    float scale_log2;  // scale * log2 e
+    int row_tiles;     // tiles of the common rows (n_seqs * group)
+    int grid;          // CTAs of the first kernel
+    // workspace
+    int *plan;         // kPlanWords, then the own tiles before each sequence [n_seqs + 1]
+    float *part_c;     // common partials: [n_kv * row_tiles + grid][PA_ROWS][head_dim + 2]
+    float *part_o;     // own partials: [n_seqs * n_kv + grid][group][head_dim + 2]
+    uint32_t *err;
+};
+
+constexpr int kPlanWords = 4;  // head of the plan: tiles per common item, all tiles (low, high word), unused
+
+// What one sequence sees.
+struct Span {
+    int lo, len;   // positions [lo, len)
+    bool member;   // shares the common range
+};
+__device__ __forceinline__ Span span_of(const AttnArgs &a, int b) {
+    Span s;
+    s.len = a.lens[b];
+    if (s.len < 0 || s.len > a.max_len) s.len = 0;
+    s.lo = a.window > 0 ? max(0, s.len - a.window) : 0;
+    s.member = s.len >= a.shared && s.lo < a.shared;
+    return s;
+}
+// Positions of the sequence outside the common range [clo, shared).
+__device__ __forceinline__ int own_count(const Span &s, int clo, int shared) {
+    return s.member ? (clo - s.lo) + (s.len - shared) : s.len - s.lo;
+}
+
+// CTAs that get a share of the list (each at least one tile), and the CTA that
+// owns tile u of it: the last c with floor(total c / ctas) <= u.
+__device__ __forceinline__ int shares(long long total, int grid) { return total < grid ? (int)total : grid; }
+__device__ __forceinline__ int owner(long long u, long long total, int ctas) {
+    return (int)(((u + 1) * ctas - 1) / total);
+}
+
+template <typename T>
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1);
+template <>
+__device__ __forceinline__ void mma<__half>(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    mma_16816(c, a, b0, b1);
+}
+template <>
+__device__ __forceinline__ void mma<__nv_bfloat16>(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi);
+template <>
+__device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+template <>
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// 16 bytes global -> shared, or 16 zero bytes.
+__device__ __forceinline__ void cp16_or_zero(uint32_t dst, const void *src, bool valid) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
+}
+
+// Byte offset of 16-byte chunk c of row r of a tile: the chunk index is
+// permuted by the row so that the 8 rows of a matrix load lie in 8 different
+// 16-byte bank groups.
+template <int DH>
+__device__ __forceinline__ uint32_t tile_off(int r, int c) {
+    return (uint32_t)(r * DH * 2 + ((c ^ (DH >= 64 ? (r & 7) : ((r >> 1) & 3))) << 4));
+}
+
+// The place of a tile in the list.
+struct Place {
+    int item;   // common: h * row_tiles + rt; own: b * n_kv + h
+    int tile, tiles;
+    bool common;
+    int b, h, rt;
+};
+
+template <typename T, int DH>
+struct Smem {
+    static constexpr int STAGES = DH == 128 ? 2 : 4;
+    static constexpr int TILE = PA_KT * DH * 2;                // bytes of K (or V) of one tile
+    static constexpr int RED_LD = DH + 4;                      // floats per row of the join buffer
+    static constexpr int RED = 4 * 16 * RED_LD * 4;            // [warp][16 rows][DH | max, sum]
+    static constexpr int CUM = (PA_MAX_SEQS + 4) * 4;
+    static constexpr int BYTES = STAGES * 2 * TILE + RED + CUM + 256;
+};
+
+template <typename T, int DH>
+class Walker {
+  public:
+    __device__ Walker(const AttnArgs &args, uint8_t *smem) : a(args) {
+        stage0 = smem;
+        red = reinterpret_cast<float *>(smem + L::STAGES * 2 * L::TILE);
+        cum = reinterpret_cast<int *>(smem + L::STAGES * 2 * L::TILE + L::RED);
+        tid = threadIdx.x;
+        warp = tid >> 5;
+        lane = tid & 31;
+    }
+
+    // The plan from the lengths: the common range and the own tiles before
+    // each sequence.  Every CTA works it out for itself (at most 8 lengths per
+    // thread); CTA 0 leaves it for the join.
+    __device__ void plan() {
+        int *scratch = cum + PA_MAX_SEQS + 1;  // common start
+        if (tid == 0) *scratch = -1;
+        __syncthreads();
+        int lo = -1;
+        bool bad = false;
+        for (int b = tid; b < a.kv.n_seqs; b += PA_THREADS) {
+            const int len = a.lens[b];
+            bad |= len < 0 || len > a.max_len;
+            const Span s = span_of(a, b);
+            if (s.member) lo = max(lo, s.lo);
+        }
+        if (bad && blockIdx.x == 0) atomicExch(a.err, 1u);
+        lo = __reduce_max_sync(0xffffffffu, lo);
+        if (lane == 0) atomicMax(scratch, lo);
+        __syncthreads();
+        clo = *scratch;
+        tiles_c = clo < 0 ? 0 : (a.shared - clo + PA_KT - 1) / PA_KT;
+        if (clo < 0) clo = a.shared;
+        // own tiles: each thread a run of sequences, then a scan over the threads
+        const int per = (a.kv.n_seqs + PA_THREADS - 1) / PA_THREADS, b0 = tid * per;
+        int sum = 0;
+        for (int i = 0; i < per; ++i)
+            if (b0 + i < a.kv.n_seqs) sum += own_tiles(b0 + i);
+        int inc = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += y;
+        }
+        int *wsum = reinterpret_cast<int *>(red);
+        if (lane == 31) wsum[warp] = inc;
+        __syncthreads();
+        int at = inc - sum;
+        for (int w = 0; w < warp; ++w) at += wsum[w];
+        for (int i = 0; i < per; ++i)
+            if (b0 + i < a.kv.n_seqs) {
+                cum[b0 + i] = at;
+                at += own_tiles(b0 + i);
+                if (b0 + i == a.kv.n_seqs - 1) cum[a.kv.n_seqs] = at;
+            }
+        __syncthreads();
+        common_total = (long long)a.kv.n_kv * a.row_tiles * tiles_c;
+        total = common_total + (long long)a.kv.n_kv * cum[a.kv.n_seqs];
+        if (blockIdx.x == 0) {
+            if (tid == 0) {
+                a.plan[0] = tiles_c;
+                a.plan[1] = (int)(total & 0xffffffff);
+                a.plan[2] = (int)(total >> 32);
+            }
+            for (int b = tid; b <= a.kv.n_seqs; b += PA_THREADS) a.plan[kPlanWords + b] = cum[b];
+        }
+    }
+
+    __device__ void run() {
+        const int ctas = shares(total, gridDim.x);
+        if ((int)blockIdx.x >= ctas) return;
+        const long long u0 = total * blockIdx.x / ctas, u1 = total * (blockIdx.x + 1) / ctas;
+        const int n = (int)(u1 - u0);
+        Place load = place(u0), work = load;
+        prepare(load);
+        int loaded = 0;
+        for (; loaded < L::STAGES - 1; ++loaded) {
+            if (loaded < n) {
+                fetch(loaded % L::STAGES);
+                if (loaded + 1 < n) step(load);
+            }
+            cp_async_commit();
+        }
+        bool fresh = true;
+        for (int i = 0; i < n; ++i) {
+            if (loaded < n) {
+                fetch(loaded % L::STAGES);
+                if (loaded + 1 < n) step(load);
+            }
+            ++loaded;
+            cp_async_commit();
+            asm volatile("cp.async.wait_group %0;" ::"n"(L::STAGES - 1) : "memory");
+            __syncthreads();
+            const bool last = i + 1 == n || work.tile + 1 == work.tiles;
+            if (work.common) {
+                const int rows = min(PA_ROWS, a.kv.n_seqs * a.group - work.rt * PA_ROWS);
+                if (rows <= 16)
+                    tile<1>(work, rows, fresh, last, i % L::STAGES);
+                else if (rows <= 32)
+                    tile<2>(work, rows, fresh, last, i % L::STAGES);
+                else
+                    tile<4>(work, rows, fresh, last, i % L::STAGES);
+            } else {
+                tile<1>(work, a.group, fresh, last, i % L::STAGES);
+            }
+            __syncthreads();  // the stage (and the join buffer) may be written again
+            fresh = last;
+            if (i + 1 < n) advance(work);
+        }
+    }
+
+  private:
+    using L = Smem<T, DH>;
+    const AttnArgs &a;
+    uint8_t *stage0;
+    float *red;
+    int *cum;
+    int tid, warp, lane;
+    int clo, tiles_c;
+    long long common_total, total;
+    // pages of the tile to be fetched next: element offsets of rows lane and
+    // lane + 32 (-1: no such key)
+    long long row_off[2];
+
+    // running state of this warp's 16 rows (lane 4 g + t: rows g and g + 8)
+    uint32_t qf[DH / 16][4];
+    float o[DH / 8][4];
+    float m[2], l[2];
+
+    __device__ int own_tiles(int b) const {
+        const Span s = span_of(a, b);
+        return (own_count(s, clo, a.shared) + PA_KT - 1) / PA_KT;
+    }
+
+    __device__ Place place(long long u) const {
+        Place p;
+        if (u < common_total) {
+            p.common = true;
+            p.item = (int)(u / tiles_c);
+            p.tile = (int)(u % tiles_c);
+            p.tiles = tiles_c;
+            p.h = p.item / a.row_tiles;
+            p.rt = p.item % a.row_tiles;
+            p.b = 0;
+            return p;
+        }
+        const long long v = u - common_total;
+        int lo = 0, hi = a.kv.n_seqs;  // the sequence with n_kv cum[b] <= v < n_kv cum[b + 1]
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) / 2;
+            if ((long long)a.kv.n_kv * cum[mid] <= v)
+                lo = mid;
+            else
+                hi = mid;
+        }
+        p.common = false;
+        p.b = lo;
+        p.tiles = cum[lo + 1] - cum[lo];
+        const int r = (int)(v - (long long)a.kv.n_kv * cum[lo]);
+        p.h = r / p.tiles;
+        p.tile = r % p.tiles;
+        p.rt = 0;
+        p.item = p.b * a.kv.n_kv + p.h;
+        return p;
+    }
+
+    // The next tile of the list.
+    __device__ void advance(Place &p) const {
+        if (++p.tile < p.tiles) return;
+        p.tile = 0;
+        if (p.common) {
+            ++p.item;
+            if (++p.rt == a.row_tiles) {
+                p.rt = 0;
+                if (++p.h == a.kv.n_kv) {  // on to the own items
+                    p.common = false;
+                    p.h = 0;
+                    p.b = -1;
+                    next_seq(p);
+                }
+            }
+            return;
+        }
+        if (++p.h == a.kv.n_kv) {
+            p.h = 0;
+            next_seq(p);
+        }
+        p.item = p.b * a.kv.n_kv + p.h;
+    }
+    __device__ void next_seq(Place &p) const {
+        do {
+            ++p.b;
+        } while (p.b < a.kv.n_seqs - 1 && cum[p.b + 1] == cum[p.b]);
+        p.tiles = cum[p.b + 1] - cum[p.b];
+        p.item = p.b * a.kv.n_kv + p.h;
+    }
+
+    // Keys of an item, counted from 0.
+    __device__ int keys_of(const Place &p) const {
+        if (p.common) return a.shared - clo;
+        const Span s = span_of(a, p.b);
+        return own_count(s, clo, a.shared);
+    }
+
+    // Looks up the pages of p's tile (rows lane and lane + 32).
+    __device__ void prepare(const Place &p) {
+        const int n = keys_of(p);
+        int first = clo, gap_at = INT_MAX, gap = 0;
+        if (!p.common) {
+            const Span s = span_of(a, p.b);
+            first = s.lo;
+            if (s.member) {
+                gap_at = clo - s.lo;
+                gap = a.shared - clo;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int k = p.tile * PA_KT + lane + 32 * i;
+            row_off[i] = -1;
+            if (k < n) {
+                const int j = first + k + (k >= gap_at ? gap : 0);
+                const int row = j < a.shared ? 0 : p.b;
+                const int page = __ldg(a.kv.table + (long long)row * a.kv.max_pages + (j >> a.kv.ps_log2));
+                if (page >= 0 && page < a.kv.n_pages)
+                    row_off[i] = page * a.kv.page_stride +
+                                 ((((long long)p.h << a.kv.ps_log2) + (j & ((1 << a.kv.ps_log2) - 1))) * DH);
+                else
+                    atomicExch(a.err, 1u);
+            }
+        }
+    }
+    __device__ void step(Place &p) {
+        advance(p);
+        prepare(p);
+    }
+
+    // Starts the copies of the prepared tile into stage s.
+    __device__ void fetch(int s) {
+        constexpr int CH = DH / 8;                  // 16-byte chunks per row
+        constexpr int RP = PA_THREADS / CH;         // rows per pass
+        const int c = tid % CH, r0 = tid / CH;
+        const uint32_t ks = smem_u32(stage0 + (size_t)s * 2 * L::TILE), vs = ks + L::TILE;
+        const T *k = static_cast<const T *>(a.kv.k), *v = static_cast<const T *>(a.kv.v);
+#pragma unroll
+        for (int i = 0; i < PA_KT / RP; ++i) {
+            const int r = i * RP + r0;
+            const long long o0 = __shfl_sync(0xffffffffu, row_off[0], r & 31);
+            const long long o1 = __shfl_sync(0xffffffffu, row_off[1], r & 31);
+            const long long off = r < 32 ? o0 : o1;
+            const long long at = off < 0 ? 0 : off + c * 8;
+            cp16_or_zero(ks + tile_off<DH>(r, c), k + at, off >= 0);
+            cp16_or_zero(vs + tile_off<DH>(r, c), v + at, off >= 0);
+        }
+    }
+
+    // One tile of an item's rows: WR warps side by side in rows, 4 / WR in keys.
+    template <int WR>
+    __device__ void tile(const Place &p, int rows, bool fresh, bool last, int s) {
+        constexpr int WK = 4 / WR, NB = PA_KT / (16 * WK);  // NB blocks of 16 keys per warp
+        const int wr = warp % WR, wk = warp / WR, t = lane & 3;
+        if (fresh) {
+            begin(p, wr, rows);
+#pragma unroll
+            for (int i = 0; i < DH / 8; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
+            m[0] = m[1] = -INFINITY;
+            l[0] = l[1] = 0.f;
+        }
+        const uint32_t ks = smem_u32(stage0 + (size_t)s * 2 * L::TILE), vs = ks + L::TILE;
+        const int left = keys_of(p) - p.tile * PA_KT;  // keys of this tile (may exceed it)
+        float sc[2 * NB][4];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+            const int key0 = (nb * WK + wk) * 16;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) sc[2 * nb][j] = sc[2 * nb + 1][j] = 0.f;
+#pragma unroll
+            for (int kk = 0; kk < DH / 16; ++kk) {
+                // matrices: keys 0-7 | dims 0-7, keys 0-7 | dims 8-15, keys 8-15 | dims 0-7, keys 8-15 | dims 8-15
+                uint32_t r[4];
+                ldsm_x4(ks + tile_off<DH>(key0 + (lane & 7) + ((lane >> 4) << 3), 2 * kk + ((lane >> 3) & 1)), r);
+                mma<T>(sc[2 * nb], qf[kk], r[0], r[1]);
+                mma<T>(sc[2 * nb + 1], qf[kk], r[2], r[3]);
+            }
+        }
+        if (left < PA_KT) {
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const int key = (nb * WK + wk) * 16 + x * 8 + 2 * t;
+                    if (key >= left) sc[2 * nb + x][0] = sc[2 * nb + x][2] = -INFINITY;
+                    if (key + 1 >= left) sc[2 * nb + x][1] = sc[2 * nb + x][3] = -INFINITY;
+                }
+        }
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {  // rows g, g + 8
+            float mx = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < 2 * NB; ++i) mx = fmaxf(mx, fmaxf(sc[i][2 * r], sc[i][2 * r + 1]));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+            const float mn = fmaxf(m[r], mx * a.scale_log2);
+            const float off = mn == -INFINITY ? 0.f : mn;
+            const float fac = ex2(m[r] - off);
+            m[r] = mn;
+            l[r] *= fac;
+#pragma unroll
+            for (int i = 0; i < DH / 8; ++i) {
+                o[i][2 * r] *= fac;
+                o[i][2 * r + 1] *= fac;
+            }
+            float sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < 2 * NB; ++i)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const float e = ex2(fmaf(sc[i][2 * r + x], a.scale_log2, -off));
+                    sc[i][2 * r + x] = e;
+                    sum += e;
+                }
+            l[r] += sum;  // this lane's keys only: joined at the end
+        }
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+            const int key0 = (nb * WK + wk) * 16;
+            uint32_t pf[4];
+            pf[0] = pack2<T>(sc[2 * nb][0], sc[2 * nb][1]);
+            pf[1] = pack2<T>(sc[2 * nb][2], sc[2 * nb][3]);
+            pf[2] = pack2<T>(sc[2 * nb + 1][0], sc[2 * nb + 1][1]);
+            pf[3] = pack2<T>(sc[2 * nb + 1][2], sc[2 * nb + 1][3]);
+#pragma unroll
+            for (int d = 0; d < DH / 16; ++d) {
+                // transposed matrices: keys 0-7 | dims 0-7, keys 8-15 | dims 0-7, then dims 8-15
+                uint32_t r[4];
+                ldsm_x4_trans(vs + tile_off<DH>(key0 + (lane & 15), 2 * d + (lane >> 4)), r);
+                mma<T>(o[2 * d], pf, r[0], r[1]);
+                mma<T>(o[2 * d + 1], pf, r[2], r[3]);
+            }
+        }
+        if (last) finish<WR>(p, wr, wk, rows);
+    }
+
+    // Q fragments of this warp's 16 rows (rows past the item's are zero).
+    __device__ void begin(const Place &p, int wr, int rows) {
+        const int g = lane >> 2, t = lane & 3;
+        const T *base[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int row = wr * 16 + g + 8 * r;
+            base[r] = nullptr;
+            if (row < rows) {
+                int b = p.b, x = row;
+                if (p.common) {
+                    const int all = p.rt * PA_ROWS + row;
+                    b = all / a.group;
+                    x = all % a.group;
+                }
+                base[r] = static_cast<const T *>(a.q) + (long long)b * a.ld_q + (long long)(p.h * a.group + x) * DH;
+            }
+        }
+#pragma unroll
+        for (int kk = 0; kk < DH / 16; ++kk)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const T *q = base[i & 1];
+                qf[kk][i] = q ? __ldg(reinterpret_cast<const uint32_t *>(q + kk * 16 + (i >> 1) * 8 + 2 * t)) : 0u;
+            }
+    }
+
+    // The item's partial: (o, max, sum) per row, warps with the same rows joined.
+    template <int WR>
+    __device__ void finish(const Place &p, int wr, int wk, int rows) {
+        constexpr int WK = 4 / WR;
+        const int g = lane >> 2, t = lane & 3;
+        float *dst = p.common ? a.part_c + (long long)(p.item + blockIdx.x) * PA_ROWS * (DH + 2)
+                              : a.part_o + (long long)(p.item + blockIdx.x) * a.group * (DH + 2);
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+        }
+        if constexpr (WK == 1) {
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const int row = wr * 16 + g + 8 * r;
+                if (row >= rows) continue;
+                float *d = dst + (long long)row * (DH + 2);
+#pragma unroll
+                for (int i = 0; i < DH / 8; ++i)
+                    *reinterpret_cast<float2 *>(d + 8 * i + 2 * t) = make_float2(o[i][2 * r], o[i][2 * r + 1]);
+                if (t == 0) *reinterpret_cast<float2 *>(d + DH) = make_float2(m[r], l[r]);
+            }
+        } else {
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                float *d = red + (warp * 16 + g + 8 * r) * L::RED_LD;
+#pragma unroll
+                for (int i = 0; i < DH / 8; ++i)
+                    *reinterpret_cast<float2 *>(d + 8 * i + 2 * t) = make_float2(o[i][2 * r], o[i][2 * r + 1]);
+                if (t == 0) *reinterpret_cast<float2 *>(d + DH) = make_float2(m[r], l[r]);
+            }
+            __syncthreads();
+            for (int x = tid; x < rows * (DH / 2); x += PA_THREADS) {
+                const int row = x / (DH / 2), c = (x % (DH / 2)) * 2;
+                const float *s0 = red + ((row / 16) * 16 + row % 16) * L::RED_LD;  // warp of key share 0
+                float mx = -INFINITY;
+#pragma unroll
+                for (int k = 0; k < WK; ++k) mx = fmaxf(mx, s0[k * WR * 16 * L::RED_LD + DH]);
+                const float off = mx == -INFINITY ? 0.f : mx;
+                float sx = 0.f, sy = 0.f, sl = 0.f;
+#pragma unroll
+                for (int k = 0; k < WK; ++k) {
+                    const float *sk = s0 + k * WR * 16 * L::RED_LD;
+                    const float f = ex2(sk[DH] - off);
+                    sx += f * sk[c];
+                    sy += f * sk[c + 1];
+                    sl += f * sk[DH + 1];
+                }
+                float *d = dst + (long long)row * (DH + 2);
+                *reinterpret_cast<float2 *>(d + c) = make_float2(sx, sy);
+                if (c == 0) *reinterpret_cast<float2 *>(d + DH) = make_float2(mx, sl);
+            }
+        }
+    }
+};
+
+template <typename T, int DH>
+__global__ void __launch_bounds__(PA_THREADS, PA_CTAS_PER_SM) paged_attn_kernel(const AttnArgs a) {
+    extern __shared__ __align__(128) uint8_t pa_smem[];
+    Walker<T, DH> w(a, pa_smem);
+    asm volatile("griddepcontrol.launch_dependents;");
+    w.plan();
+    w.run();
+}
+
+
+// One warp per (sequence, query head): the row's partials joined in list
+// order (common item first), normalised and rounded once.
+template <typename T, int DH>
+__global__ void __launch_bounds__(PA_MERGE_THREADS) paged_attn_join(const AttnArgs a) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int x = (int)((blockIdx.x * (long long)PA_MERGE_THREADS + threadIdx.x) >> 5), lane = threadIdx.x & 31;
+    if (x >= a.kv.n_seqs * a.n_q) return;
+    const int b = x / a.n_q, hq = x % a.n_q, h = hq / a.group, r = hq % a.group;
+    const int tiles_c = a.plan[0];
+    const long long total = (long long)(uint32_t)a.plan[1] | ((long long)a.plan[2] << 32);
+    const long long common_total = (long long)a.kv.n_kv * a.row_tiles * tiles_c;
+    const int ctas = shares(total, a.grid);
+    const Span s = span_of(a, b);
+    constexpr int V = DH / 32;  // values per lane
+    float acc[V], mx = -INFINITY, sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[i] = 0.f;
+    auto join = [&](const float *base, long long stride, int n) {
+        for (int k = 0; k < n; ++k) {
+            const float *d = base + k * stride;
+            const float pm = d[DH], pl = d[DH + 1];
+            float v[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) v[i] = d[lane * V + i];
+            const float mn = fmaxf(mx, pm), off = mn == -INFINITY ? 0.f : mn;
+            const float f0 = ex2(mx - off), f1 = ex2(pm - off);
+            mx = mn;
+            sum = sum * f0 + pl * f1;
+#pragma unroll
+            for (int i = 0; i < V; ++i) acc[i] = acc[i] * f0 + v[i] * f1;
+        }
+    };
+    if (s.member && tiles_c > 0) {
+        const int row = b * a.group + r, item = h * a.row_tiles + row / PA_ROWS;
+        const long long u = (long long)item * tiles_c;
+        const int c0 = owner(u, total, ctas), c1 = owner(u + tiles_c - 1, total, ctas);
+        join(a.part_c + ((long long)(item + c0) * PA_ROWS + row % PA_ROWS) * (DH + 2), (long long)PA_ROWS * (DH + 2),
+             c1 - c0 + 1);
+    }
+    const int t0 = a.plan[kPlanWords + b], tiles = a.plan[kPlanWords + b + 1] - t0;
+    if (tiles > 0) {
+        const int item = b * a.kv.n_kv + h;
+        const long long u = common_total + (long long)a.kv.n_kv * t0 + (long long)h * tiles;
+        const int c0 = owner(u, total, ctas), c1 = owner(u + tiles - 1, total, ctas);
+        join(a.part_o + ((long long)(item + c0) * a.group + r) * (DH + 2), (long long)a.group * (DH + 2), c1 - c0 + 1);
+    }
+    const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);  // (a NaN stays one)
+    T *dst = static_cast<T *>(a.out) + (long long)b * a.ld_out + (long long)hq * DH + lane * V;
+#pragma unroll
+    for (int i = 0; i < V; ++i) dst[i] = (T)(acc[i] * inv);
+    if (a.lse && lane == 0) a.lse[(long long)b * a.n_q + hq] = mx * 0.69314718055994530942f + logf(sum);
+}
+
+int sm_count() {
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return 0;
+    }
+    return n;
+}
+
+size_t al256(size_t n) { return (n + 255) & ~size_t(255); }
+
+struct WsLayout {
+    size_t plan, part_c, part_o, bytes;
+};
+WsLayout ws_layout(const PagedView &kv, int group, int row_tiles, int grid) {
+    WsLayout w;
+    const size_t row = (size_t)(kv.head_dim + 2) * sizeof(float);
+    w.plan = 0;
+    w.part_c = al256((size_t)(kPlanWords + kv.n_seqs + 1) * sizeof(int));
+    w.part_o = w.part_c + al256(((size_t)kv.n_kv * row_tiles + grid) * PA_ROWS * row);
+    w.bytes = w.part_o + al256(((size_t)kv.n_seqs * kv.n_kv + grid) * group * row);
+    return w;
+}
+
+lf_status check_shape(const lf_paged_kv *kv, int n_q_heads, PagedView *v) {
+    const lf_status st = paged_view(kv, v);
+    if (st != LF_OK) return st;
+    if (n_q_heads < 1 || n_q_heads % v->n_kv) return LF_ERR_INVALID_ARG;
+    if ((v->head_dim != 32 && v->head_dim != 64 && v->head_dim != 128) || n_q_heads / v->n_kv > PA_MAX_GROUP ||
+        v->n_seqs > PA_MAX_SEQS)
+        return LF_ERR_UNSUPPORTED;
+    if ((long long)v->n_seqs * n_q_heads > (1 << 26)) return LF_ERR_UNSUPPORTED;  // item numbers are 32-bit
+    return LF_OK;
+}
+
+template <typename T, int DH>
+lf_status launch_attn(const AttnArgs &a, cudaStream_t st) {
+    constexpr int smem = Smem<T, DH>::BYTES;
+    if (!set_smem_once<paged_attn_kernel<T, DH>>(smem)) return LF_ERR_CUDA;
+    paged_attn_kernel<T, DH><<<a.grid, PA_THREADS, smem, st>>>(a);
+    if (cudaGetLastError() != cudaSuccess) return LF_ERR_CUDA;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(((long long)a.kv.n_seqs * a.n_q * 32 + PA_MERGE_THREADS - 1) / PA_MERGE_THREADS));
+    cfg.blockDim = dim3(PA_MERGE_THREADS);
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, paged_attn_join<T, DH>, a) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return LF_ERR_CUDA;
+    }
+    return LF_OK;
+}
+
+template <typename T>
+lf_status launch_attn_dim(const AttnArgs &a, cudaStream_t st) {
+    return a.kv.head_dim == 32   ? launch_attn<T, 32>(a, st)
+           : a.kv.head_dim == 64 ? launch_attn<T, 64>(a, st)
+                                 : launch_attn<T, 128>(a, st);
+}
+
+}  // namespace
+}  // namespace lf
+
+extern "C" size_t lf_attn_paged_shared_workspace(const lf_paged_kv *kv, int n_q_heads) {
+    lf::PagedView v;
+    if (lf::check_shape(kv, n_q_heads, &v) != LF_OK) return 0;
+    const int group = n_q_heads / v.n_kv, tiles = (v.n_seqs * group + lf::PA_ROWS - 1) / lf::PA_ROWS;
+    const int n_sm = lf::sm_count();
+    return n_sm ? lf::ws_layout(v, group, tiles, n_sm * lf::PA_CTAS_PER_SM).bytes : 0;
+}
+
+extern "C" lf_status lf_attn_paged_shared(const lf_paged_kv *kv, const void *q_device, int64_t ld_q, void *out_device,
+                                          int64_t ld_out, float *lse_device, int n_q_heads, const int32_t *lens_device,
+                                          int max_len, int shared_len, int window, float scale, void *workspace_device,
+                                          size_t workspace_bytes, uint32_t *err_device, void *cuda_stream) {
+    lf::AttnArgs a = {};
+    const lf_status cs = lf::check_shape(kv, n_q_heads, &a.kv);
+    if (cs != LF_OK) return cs;
+    const int64_t row = (int64_t)n_q_heads * kv->head_dim, cap = (int64_t)kv->max_pages * kv->page_size;
+    auto off4 = [](const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; };
+    if (!q_device || !out_device || !lens_device || !workspace_device || !err_device || !lf::aligned16(q_device) ||
+        !lf::aligned16(out_device) || off4(lse_device) || off4(lens_device) || off4(err_device) ||
+        (reinterpret_cast<uintptr_t>(workspace_device) & 255u) || ld_q < row || ld_out < row || ld_q % 8 ||
+        ld_out % 8 || max_len < 0 || max_len > cap || shared_len < 0 || shared_len > max_len || window < 0 ||
+        !(scale > 0.f && scale < INFINITY))
+        return LF_ERR_INVALID_ARG;
+    a.group = n_q_heads / a.kv.n_kv;
+    a.row_tiles = (a.kv.n_seqs * a.group + lf::PA_ROWS - 1) / lf::PA_ROWS;
+    const int n_sm = lf::sm_count();
+    if (!n_sm) return LF_ERR_CUDA;
+    a.grid = n_sm * lf::PA_CTAS_PER_SM;
+    const lf::WsLayout w = lf::ws_layout(a.kv, a.group, a.row_tiles, a.grid);
+    if (workspace_bytes < w.bytes) return LF_ERR_INVALID_ARG;
+    uint8_t *ws = static_cast<uint8_t *>(workspace_device);
+    a.plan = reinterpret_cast<int *>(ws + w.plan);
+    a.part_c = reinterpret_cast<float *>(ws + w.part_c);
+    a.part_o = reinterpret_cast<float *>(ws + w.part_o);
+    a.q = q_device;
+    a.out = out_device;
+    a.lse = lse_device;
+    a.ld_q = ld_q;
+    a.ld_out = ld_out;
+    a.n_q = n_q_heads;
+    a.lens = lens_device;
+    a.max_len = max_len;
+    a.shared = shared_len;
+    a.window = window;
+    a.scale_log2 = scale * lf::kLog2e;
+    a.err = err_device;
+    cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
+    return kv->dtype == LF_F16 ? lf::launch_attn_dim<__half>(a, st) : lf::launch_attn_dim<__nv_bfloat16>(a, st);
+}

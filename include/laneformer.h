@@ -419,6 +419,138 @@ lf_status lf_gemv_f16(const void *w_device, const void *x_device, float *y_devic
                       void *cuda_stream);
 
 /*
+ * Operators of a serving loop over a paged cache: the append with RoPE, the
+ * decode attention of a batch whose sequences share their first positions,
+ * and the filtered draw.  They stand beside lf_matmul_f16, lf_gemv_f16 and
+ * lf_sample for callers that build their own batched passes (pass@N: several
+ * continuations of one prompt, News, "Performance and infrastructure"), and
+ * lf_batch_begin_shared / lf_batch_generate_filtered run the engine's own
+ * batched decode on them.
+ *
+ * All three are asynchronous: they only enqueue kernels on `cuda_stream`
+ * (NULL = legacy stream), which must belong to the current device, as must
+ * every DEVICE pointer; they allocate nothing and can be captured into a
+ * graph.  What a kernel can only see on the device (a page number, a length,
+ * a position, a filter's value) is checked there, never trusted as an index.
+ */
+typedef enum { LF_F32 = 0, LF_F16 = 1, LF_BF16 = 2 } lf_dtype;
+
+/* A paged KV cache (one layer).  Page g of K holds page_size positions of
+ * every KV head, [n_kv_heads][page_size][head_dim] from k + g * page_stride
+ * elements on, and V likewise; position j of sequence s lives in row
+ * j % page_size of page page_table[s * max_pages + j / page_size].  Sequences
+ * may name the same page (a shared prompt).
+ *   k, v: DEVICE arrays of dtype (LF_F16 or LF_BF16), 16-byte aligned;
+ *   page_table: DEVICE int32 [n_seqs][max_pages];
+ *   page_size: a power of two, 1 .. 1024; head_dim: a multiple of 16, 16 .. 256;
+ *   page_stride: elements from one page to the next, a multiple of 8 and at
+ *   least n_kv_heads * page_size * head_dim; 0 = exactly that. */
+typedef struct {
+    void *k, *v;
+    const int32_t *page_table;
+    int n_pages, n_kv_heads, page_size, head_dim, n_seqs, max_pages;
+    int dtype;
+    int64_t page_stride;
+} lf_paged_kv;
+
+/* Rotates the queries and keys of n_tokens tokens by their positions (pairs
+ * (c, c + head_dim / 2), the engine's RoPE) and appends the keys and values to
+ * the cache.  Token t belongs to sequence seq_device[t] (NULL: sequence t) at
+ * position pos_device[t].
+ *   q_in, k_in, v_in: DEVICE arrays of in_dtype (LF_F32, LF_F16 or LF_BF16),
+ *   token t's heads [n_q_heads or n_kv_heads][head_dim] from ld_q * t (ld_k,
+ *   ld_v) elements on, e.g. three columns of one fused projection's output;
+ *   q_out: DEVICE array of the cache's dtype, row stride ld_q_out; it may be
+ *   q_in itself when the types and strides are equal (rotated in place), and
+ *   otherwise overlaps no input; q_in and q_out are unused when n_q_heads is 0;
+ *   rope_device: DEVICE [rope_len][head_dim / 2] fp32 pairs (cos, sin), row p
+ *   for position p; NULL appends without a rotation.
+ * Pointers and row strides are multiples of 16 bytes.  The rotation is
+ * computed in fp32 and rounded once.  A token whose sequence is negative is
+ * padding: nothing is read for it and nothing is written.  A sequence, position
+ * or page outside the cache (or a position outside rope_device) skips the
+ * token and sets *err_device (DEVICE word, cleared by the caller) to 1.  The
+ * tokens of one call name different slots: of two that name the same slot
+ * either may supply any 16-byte piece of it.  n_tokens 0 does nothing.
+ * LF_ERR_INVALID_ARG for bad sizes, pointers, strides or types. */
+lf_status lf_kv_append_paged(const lf_paged_kv *kv, const void *q_in, const void *k_in, const void *v_in, int in_dtype,
+                             int64_t ld_q, int64_t ld_k, int64_t ld_v, int n_q_heads, void *q_out, int64_t ld_q_out,
+                             const int32_t *seq_device, const int32_t *pos_device, int n_tokens,
+                             const float *rope_device, int rope_len, uint32_t *err_device, void *cuda_stream);
+
+/* Decode attention of one query token per sequence over the paged cache:
+ *   out[b][h] = sum_j p_j v_j,  p = softmax_j(scale * q[b][h] . k_j),
+ * over the positions j of sequence b with len_b - window <= j < len_b (window
+ * 0: all j < len_b), len_b = lens_device[b] counting the current token; query
+ * head h reads KV head h / (n_q_heads / n_kv_heads).  The first `shared_len`
+ * positions are common to the batch and always read through sequence 0's row
+ * of the page table; they are read once for all sequences that reach them
+ * (len_b >= shared_len, and a window that starts before it), each sequence's
+ * other positions through its own row.  shared_len 0 is plain paged
+ * attention.  A position that a sequence does not see never reaches its
+ * result, whatever the cache holds there (NaN included).
+ *   q_device, out_device: DEVICE [n_seqs][n_q_heads][head_dim] of the cache's
+ *   dtype, row strides ld_q and ld_out elements (16-byte multiples);
+ *   lse_device: DEVICE [n_seqs][n_q_heads] fp32, the natural log of the
+ *   softmax's denominator (of sum_j exp(scale * q . k_j)); NULL: not wanted;
+ *   lens_device: DEVICE int32 [n_seqs]; a sequence of length 0 gets zeros and
+ *   lse -inf;
+ *   max_len: upper bound of the lengths (sizes nothing but the check of them);
+ *   scale: finite, above 0;
+ *   workspace_device: DEVICE scratch of at least
+ *   lf_attn_paged_shared_workspace bytes, 256-byte aligned; it needs no
+ *   initial content, holds nothing between calls, and belongs to one call (or
+ *   one replayed graph) at a time.
+ * Scores, softmax statistics and sums are fp32; the softmax weights enter the
+ * second product rounded to the cache's type.  The result does not depend on
+ * timing (sums in a fixed order), only on the arguments and the SM count.  A
+ * length outside [0, max_len] (taken as 0) or a page outside the cache (the
+ * result is then undefined) sets *err_device to 1.
+ * LF_ERR_INVALID_ARG for bad sizes, pointers, strides or types, shared_len or
+ * max_len above max_pages * page_size, or a workspace too small;
+ * LF_ERR_UNSUPPORTED for head_dim other than 32, 64 or 128, more than 16
+ * query heads per KV head or more than 1024 sequences. */
+lf_status lf_attn_paged_shared(const lf_paged_kv *kv, const void *q_device, int64_t ld_q, void *out_device,
+                               int64_t ld_out, float *lse_device, int n_q_heads, const int32_t *lens_device,
+                               int max_len, int shared_len, int window, float scale, void *workspace_device,
+                               size_t workspace_bytes, uint32_t *err_device, void *cuda_stream);
+
+/* Workspace bytes of lf_attn_paged_shared for this cache on the current
+ * device, whatever the lengths; 0 where that call would refuse the sizes. */
+size_t lf_attn_paged_shared_workspace(const lf_paged_kv *kv, int n_q_heads);
+
+/* One draw per row of logits under temperature, top-k, top-p and min-p, from
+ * a given uniform number per row.  For row r with z = its logits, T =
+ * temperature[r] and w_i = exp((z_i - max z) / T), token i is kept when
+ *   z_i >= the top_k[r]-th largest logit (equal logits count each)
+ *                                                 (top_k <= 0 or >= vocab: all),
+ *   z_i >= the largest value t for which the tokens of that set with z >= t
+ *          hold at least top_p[r] of the set's mass (top_p 1: all), and
+ *   z_i >= max z + T ln min_p[r], i.e. w_i >= min_p (min_p 0: all);
+ * logits equal to a bound are all kept.  The token is the first kept index, in
+ * index order, whose running kept mass exceeds u[r] times the kept mass;
+ * logprob is the log of its share of the kept mass.  T = 0 takes the lowest
+ * index among the maxima, logprob 0.  Logits of -inf are never drawn; if some
+ * are +inf, those alone hold the mass, equally.
+ *   logits_device: DEVICE [rows] rows of vocab values of dtype (LF_F32, LF_F16
+ *   or LF_BF16), ld elements apart (ld >= vocab), aligned to the type;
+ *   temperature, top_k, top_p, min_p: DEVICE arrays [rows] (fp32; top_k int32);
+ *   NULL: 1, all, 1 and 0 for every row; u: DEVICE fp32 [rows], in [0, 1);
+ *   token_device: DEVICE int32 [rows]; logprob_device: DEVICE fp32 [rows] or
+ *   NULL.
+ * Masses are 64-bit fixed-point sums of weights that are exact to about 2^-40,
+ * so the draw is the definition's unless u lies that close to a border.  A row
+ * with a NaN, without a logit above -inf, or with a parameter outside its range
+ * (T neither 0 nor in [1e-30, 1e30], top_p outside (0, 1], min_p outside [0, 1],
+ * u outside [0, 1)) gets token -1 and logprob NaN.  rows 0 does nothing.
+ * LF_ERR_INVALID_ARG for bad sizes, types or pointers; LF_ERR_UNSUPPORTED for
+ * a vocabulary above 262144. */
+lf_status lf_sample_filtered(const void *logits_device, int dtype, int rows, int vocab, int64_t ld,
+                             const float *temperature_device, const int32_t *top_k_device, const float *top_p_device,
+                             const float *min_p_device, const float *u_device, int32_t *token_device,
+                             float *logprob_device, void *cuda_stream);
+
+/*
  * Debug build.  liblaneformer_debug.so is the same library compiled with
  * LF_DEBUG: before every weight-tile, KV, q/k/v, partial, lane-sum,
  * attention-partial and logit access the decode kernel checks the index
