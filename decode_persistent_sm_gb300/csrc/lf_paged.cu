@@ -9,16 +9,17 @@
 // A unit of work is 8 pairs of one head of one token: two 16-byte stores (and
 // as wide loads as the input's type gives), the same two pieces that the
 // rotation couples.  A thread keeps one pair range c .. c + 7 of one token and
-// walks the heads, so its cos and sin are read once.  The bound is HBM: every
-// value is read and written once.
+// takes U heads of it, so its cos and sin are read once and U units' loads are
+// in flight together, started before the position, the table entry and the
+// rotation's row (three loads that wait for each other) are looked up.  The
+// bound is HBM: every value is read and written once.
 #include "lf_paged.h"
 
 namespace lf {
 namespace {
 
 constexpr int kAppendThreads = 256;
-constexpr int kAppendHeads = 2;  // heads per thread whose loads are in flight together
-
+constexpr long long kAppendManyUnits = 1 << 18;
 struct AppendArgs {
     PagedView kv;
     const void *q, *k, *v;
@@ -32,30 +33,47 @@ struct AppendArgs {
     uint32_t *err;
 };
 
-// 8 consecutive values as fp32.
-__device__ __forceinline__ void load8(const float *p, float (&f)[8]) {
-    const float4 a = __ldg(reinterpret_cast<const float4 *>(p)), b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
-    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
-}
-// (16-bit inputs may be the output array itself, rotated in place: plain loads)
-__device__ __forceinline__ void load8(const __half *p, float (&f)[8]) {
-    const uint4 u = *reinterpret_cast<const uint4 *>(p);
-    const __half2 *h = reinterpret_cast<const __half2 *>(&u);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 t = __half22float2(h[i]);
-        f[2 * i] = t.x, f[2 * i + 1] = t.y;
+// 8 consecutive values as they lie in memory, and as fp32.  (The input may be
+// the output array itself, rotated in place: no read-only loads.)
+template <typename T>
+struct Eight;
+template <>
+struct Eight<float> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float *p) {
+        a = reinterpret_cast<const float4 *>(p)[0];
+        b = reinterpret_cast<const float4 *>(p)[1];
     }
-}
-__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float (&f)[8]) {
-    const uint4 u = *reinterpret_cast<const uint4 *>(p);
-    const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&u);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 t = __bfloat1622float2(h[i]);
-        f[2 * i] = t.x, f[2 * i + 1] = t.y;
+    __device__ __forceinline__ void get(float (&f)[8]) const {
+        f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
     }
-}
+};
+template <>
+struct Eight<__half> {
+    uint4 u;
+    __device__ __forceinline__ void load(const __half *p) { u = *reinterpret_cast<const uint4 *>(p); }
+    __device__ __forceinline__ void get(float (&f)[8]) const {
+        const __half2 *h = reinterpret_cast<const __half2 *>(&u);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 t = __half22float2(h[i]);
+            f[2 * i] = t.x, f[2 * i + 1] = t.y;
+        }
+    }
+};
+template <>
+struct Eight<__nv_bfloat16> {
+    uint4 u;
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p) { u = *reinterpret_cast<const uint4 *>(p); }
+    __device__ __forceinline__ void get(float (&f)[8]) const {
+        const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&u);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 t = __bfloat1622float2(h[i]);
+            f[2 * i] = t.x, f[2 * i + 1] = t.y;
+        }
+    }
+};
 __device__ __forceinline__ void store8(__half *p, const float (&f)[8]) {
     __half2 h[4];
 #pragma unroll
@@ -69,43 +87,23 @@ __device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&f)[8]) {
     *reinterpret_cast<uint4 *>(p) = *reinterpret_cast<const uint4 *>(h);
 }
 
-// Block = head_dim / 16 pair ranges x head slots, blockIdx.x = token,
-// blockIdx.y = share of the token's heads.
-template <typename TI, typename TO>
-__global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendArgs a) {
-    const int DH = a.kv.head_dim, half = DH / 2, pieces = DH / 16;
-    const int piece = threadIdx.x % pieces, slot = threadIdx.x / pieces, slots = blockDim.x / pieces;
-    const int t = blockIdx.x, heads = a.n_q + 2 * a.kv.n_kv;
+// A token has per_token = pieces * slots threads (pieces = head_dim / 16 pair
+// ranges, slots = heads / U rounded up); a block holds whole tokens.
+template <typename TI, typename TO, int U>
+__global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendArgs a, int slots) {
+    const int DH = a.kv.head_dim, half = DH / 2, pieces = DH / 16, per_token = pieces * slots;
+    const long long t_ll = (long long)blockIdx.x * (blockDim.x / per_token) + threadIdx.x / per_token;
+    if (t_ll >= a.n_tokens) return;
+    const int t = (int)t_ll, x = threadIdx.x % per_token, c0 = x % pieces * 8, slot = x / pieces + slots * blockIdx.y * U;
+    const int heads = a.n_q + 2 * a.kv.n_kv;
     const int seq = a.seq ? a.seq[t] : t;
-    if (seq < 0) return;  // padding
     const int p = a.pos[t];
-    int page = -1;
-    if (seq < a.kv.n_seqs && p >= 0 && (p >> a.kv.ps_log2) < a.kv.max_pages && (!a.rope || p < a.rope_len))
-        page = a.kv.table[(long long)seq * a.kv.max_pages + (p >> a.kv.ps_log2)];
-    if (page < 0 || page >= a.kv.n_pages) {
-        if (threadIdx.x == 0 && blockIdx.y == 0) atomicExch(a.err, 1u);
-        return;
-    }
-    const int row = p & ((1 << a.kv.ps_log2) - 1), c0 = piece * 8;
-    float cs[8], sn[8];
-    if (a.rope) {
-        const float4 *r = reinterpret_cast<const float4 *>(a.rope + ((long long)p * half + c0) * 2);
+    if (seq < 0) return;  // padding
+    Eight<TI> lo[U], hi[U];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float4 x = __ldg(r + i);
-            cs[2 * i] = x.x, sn[2 * i] = x.y, cs[2 * i + 1] = x.z, sn[2 * i + 1] = x.w;
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) cs[i] = 1.f, sn[i] = 0.f;
-    }
-    const int step = slots * gridDim.y;
-    for (int h0 = slot + slots * blockIdx.y; h0 < heads; h0 += kAppendHeads * step) {
-        float lo[kAppendHeads][8], hi[kAppendHeads][8];
-#pragma unroll
-        for (int u = 0; u < kAppendHeads; ++u) {
-            const int h = h0 + u * step;
-            if (h >= heads) break;
+    for (int u = 0; u < U; ++u) {
+        const int h = slot + u * slots;
+        if (h < heads) {
             const TI *src;
             if (h < a.n_q)
                 src = static_cast<const TI *>(a.q) + (long long)t * a.ld_q + (long long)h * DH;
@@ -113,42 +111,74 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendA
                 src = static_cast<const TI *>(a.k) + (long long)t * a.ld_k + (long long)(h - a.n_q) * DH;
             else
                 src = static_cast<const TI *>(a.v) + (long long)t * a.ld_v + (long long)(h - a.n_q - a.kv.n_kv) * DH;
-            load8(src + c0, lo[u]);
-            load8(src + half + c0, hi[u]);
-        }
-#pragma unroll
-        for (int u = 0; u < kAppendHeads; ++u) {
-            const int h = h0 + u * step;
-            if (h >= heads) break;
-            TO *dst;
-            if (h < a.n_q) {
-                dst = static_cast<TO *>(a.qo) + (long long)t * a.ld_qo + (long long)h * DH;
-            } else {
-                const int g = (h - a.n_q) % a.kv.n_kv;
-                TO *base = static_cast<TO *>(h < a.n_q + a.kv.n_kv ? a.kv.k : a.kv.v);
-                dst = base + page * a.kv.page_stride + ((((long long)g << a.kv.ps_log2) + row) * DH);
-            }
-            if (a.rope && h < a.n_q + a.kv.n_kv) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float x = lo[u][i], y = hi[u][i];
-                    lo[u][i] = x * cs[i] - y * sn[i];
-                    hi[u][i] = x * sn[i] + y * cs[i];
-                }
-            }
-            store8(dst + c0, lo[u]);
-            store8(dst + half + c0, hi[u]);
+            lo[u].load(src + c0);
+            hi[u].load(src + half + c0);
         }
     }
+    int page = -1;
+    if (seq < a.kv.n_seqs && p >= 0 && (p >> a.kv.ps_log2) < a.kv.max_pages && (!a.rope || p < a.rope_len))
+        page = a.kv.table[(long long)seq * a.kv.max_pages + (p >> a.kv.ps_log2)];
+    if (page < 0 || page >= a.kv.n_pages) {
+        if (x == 0 && blockIdx.y == 0) atomicExch(a.err, 1u);
+        return;
+    }
+    float cs[8], sn[8];
+    if (a.rope) {
+        const float4 *r = reinterpret_cast<const float4 *>(a.rope + ((long long)p * half + c0) * 2);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float4 y = __ldg(r + i);
+            cs[2 * i] = y.x, sn[2 * i] = y.y, cs[2 * i + 1] = y.z, sn[2 * i + 1] = y.w;
+        }
+    }
+    const int row = p & ((1 << a.kv.ps_log2) - 1);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int h = slot + u * slots;
+        if (h >= heads) break;
+        TO *dst;
+        if (h < a.n_q) {
+            dst = static_cast<TO *>(a.qo) + (long long)t * a.ld_qo + (long long)h * DH;
+        } else {
+            const int g = h < a.n_q + a.kv.n_kv ? h - a.n_q : h - a.n_q - a.kv.n_kv;
+            TO *base = static_cast<TO *>(h < a.n_q + a.kv.n_kv ? a.kv.k : a.kv.v);
+            dst = base + page * a.kv.page_stride + ((((long long)g << a.kv.ps_log2) + row) * DH);
+        }
+        float fl[8], fh[8];
+        lo[u].get(fl);
+        hi[u].get(fh);
+        if (a.rope && h < a.n_q + a.kv.n_kv) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float y = fl[i], z = fh[i];
+                fl[i] = y * cs[i] - z * sn[i];
+                fh[i] = y * sn[i] + z * cs[i];
+            }
+        }
+        store8(dst + c0, fl);
+        store8(dst + half + c0, fh);
+    }
+}
+
+template <typename TI, typename TO, int U>
+void launch_units(const AppendArgs &a, cudaStream_t st) {
+    const int pieces = a.kv.head_dim / 16, heads = a.n_q + 2 * a.kv.n_kv;  // pieces: 1 .. 16
+    const int slots = min((heads + U - 1) / U, kAppendThreads / pieces);
+    const int tokens = kAppendThreads / (pieces * slots);  // per block
+    const int y = (heads + slots * U - 1) / (slots * U);
+    kv_append_kernel<TI, TO, U><<<dim3((unsigned)((a.n_tokens + tokens - 1) / tokens), (unsigned)y),
+                                  pieces * slots * tokens, 0, st>>>(a, slots);
 }
 
 template <typename TI, typename TO>
 void launch_append(const AppendArgs &a, cudaStream_t st) {
-    const int pieces = a.kv.head_dim / 16;  // 1 .. 16
-    const int threads = kAppendThreads / pieces * pieces, slots = threads / pieces;
-    const int heads = a.n_q + 2 * a.kv.n_kv;
-    const int y = (heads + slots * kAppendHeads - 1) / (slots * kAppendHeads);
-    kv_append_kernel<TI, TO><<<dim3((unsigned)a.n_tokens, (unsigned)y), threads, 0, st>>>(a);
+    // four units a thread once that still leaves a few blocks per SM, one unit
+    // for the few tokens of a decode step (a shorter chain in each thread)
+    const long long units = (long long)a.n_tokens * (a.n_q + 2 * a.kv.n_kv) * (a.kv.head_dim / 16);
+    if (units >= kAppendManyUnits)
+        launch_units<TI, TO, 4>(a, st);
+    else
+        launch_units<TI, TO, 1>(a, st);
 }
 
 template <typename TI>
