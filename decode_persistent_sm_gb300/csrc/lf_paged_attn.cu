@@ -15,7 +15,7 @@
 // common range or (sequence, KV head) of the own ranges; all tiles of all
 // items form one list, cut into equal contiguous shares, one per CTA, so ragged
 // lengths and short batches fill the GPU alike.  A CTA walks its share with a
-// two-stage cp.async ring that runs on across item borders, and leaves one
+// cp.async ring of tiles that runs on across item borders, and leaves one
 // partial (unnormalised o, max, sum) per item it touches: slot item + CTA,
 // which is unique because both only grow along the list.  A second kernel,
 // launched to overlap the first one's end, joins each row's partials in list
@@ -139,14 +139,17 @@ struct Place {
     int b, h, rt;
 };
 
+// Three stages of 32 KB at head_dim 128, so that two CTAs share an SM with 128 KB
+// of copies in flight; as many bytes in more stages for smaller heads.
 template <typename T, int DH>
 struct Smem {
-    static constexpr int STAGES = DH == 128 ? 2 : 4;
-    static constexpr int TILE = PA_KT * DH * 2;                // bytes of K (or V) of one tile
-    static constexpr int RED_LD = DH + 4;                      // floats per row of the join buffer
-    static constexpr int RED = 4 * 16 * RED_LD * 4;            // [warp][16 rows][DH | max, sum]
+    static constexpr int TILE = PA_KT * DH * 2;  // bytes of K (or V) of one tile
+    static constexpr int STAGES = DH == 128 ? 3 : DH == 64 ? 6 : 8;
+    static constexpr int ML = 4 * 16 * 2 * 4;  // max and sum of the rows that the warps join
     static constexpr int CUM = (PA_MAX_SEQS + 4) * 4;
-    static constexpr int BYTES = STAGES * 2 * TILE + RED + CUM + 256;
+    static constexpr int BYTES = STAGES * 2 * TILE + ML + CUM + 16 * 4;
+    // the join of the warps' rows uses the stage of the item's last tile
+    static_assert(4 * 16 * DH * 4 <= 2 * TILE, "the joined rows fit the stage");
 };
 
 template <typename T, int DH>
@@ -154,8 +157,8 @@ class Walker {
   public:
     __device__ Walker(const AttnArgs &args, uint8_t *smem) : a(args) {
         stage0 = smem;
-        red = reinterpret_cast<float *>(smem + L::STAGES * 2 * L::TILE);
-        cum = reinterpret_cast<int *>(smem + L::STAGES * 2 * L::TILE + L::RED);
+        ml = reinterpret_cast<float2 *>(smem + L::STAGES * 2 * L::TILE);
+        cum = reinterpret_cast<int *>(smem + L::STAGES * 2 * L::TILE + L::ML);
         tid = threadIdx.x;
         warp = tid >> 5;
         lane = tid & 31;
@@ -194,7 +197,7 @@ class Walker {
             const int y = __shfl_up_sync(0xffffffffu, inc, o);
             if (lane >= o) inc += y;
         }
-        int *wsum = reinterpret_cast<int *>(red);
+        int *wsum = cum + PA_MAX_SEQS + 4;
         if (lane == 31) wsum[warp] = inc;
         __syncthreads();
         int at = inc - sum;
@@ -265,7 +268,7 @@ class Walker {
     using L = Smem<T, DH>;
     const AttnArgs &a;
     uint8_t *stage0;
-    float *red;
+    float2 *ml;
     int *cum;
     int tid, warp, lane;
     int clo, tiles_c;
@@ -492,7 +495,7 @@ class Walker {
                 mma<T>(o[2 * d + 1], pf, r[2], r[3]);
             }
         }
-        if (last) finish<WR>(p, wr, wk, rows);
+        if (last) finish<WR>(p, wr, rows, s);
     }
 
     // Q fragments of this warp's 16 rows (rows past the item's are zero).
@@ -524,7 +527,7 @@ class Walker {
 
     // The item's partial: (o, max, sum) per row, warps with the same rows joined.
     template <int WR>
-    __device__ void finish(const Place &p, int wr, int wk, int rows) {
+    __device__ void finish(const Place &p, int wr, int rows, int s) {
         constexpr int WK = 4 / WR;
         const int g = lane >> 2, t = lane & 3;
         float *dst = p.common ? a.part_c + (long long)(p.item + blockIdx.x) * PA_ROWS * (DH + 2)
@@ -546,30 +549,36 @@ class Walker {
                 if (t == 0) *reinterpret_cast<float2 *>(d + DH) = make_float2(m[r], l[r]);
             }
         } else {
+            __syncthreads();  // every warp has read this stage's keys and values
+            // row r of warp w at (w * 16 + r) * DH, its columns permuted by the row (8 rows of a warp write 8 bank groups)
+            float *red = reinterpret_cast<float *>(stage0 + (size_t)s * 2 * L::TILE);
+            auto col = [](int row, int c) { return c ^ ((row & (DH / 8 - 1) & 7) << 3); };
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                float *d = red + (warp * 16 + g + 8 * r) * L::RED_LD;
+                const int row = g + 8 * r;
+                float *d = red + (warp * 16 + row) * DH;
 #pragma unroll
                 for (int i = 0; i < DH / 8; ++i)
-                    *reinterpret_cast<float2 *>(d + 8 * i + 2 * t) = make_float2(o[i][2 * r], o[i][2 * r + 1]);
-                if (t == 0) *reinterpret_cast<float2 *>(d + DH) = make_float2(m[r], l[r]);
+                    *reinterpret_cast<float2 *>(d + col(row, 8 * i) + 2 * t) = make_float2(o[i][2 * r], o[i][2 * r + 1]);
+                if (t == 0) ml[warp * 16 + row] = make_float2(m[r], l[r]);
             }
             __syncthreads();
             for (int x = tid; x < rows * (DH / 2); x += PA_THREADS) {
                 const int row = x / (DH / 2), c = (x % (DH / 2)) * 2;
-                const float *s0 = red + ((row / 16) * 16 + row % 16) * L::RED_LD;  // warp of key share 0
-                float mx = -INFINITY;
+                float mx = -INFINITY;  // over the key shares k: warp row / 16 + k * WR
 #pragma unroll
-                for (int k = 0; k < WK; ++k) mx = fmaxf(mx, s0[k * WR * 16 * L::RED_LD + DH]);
+                for (int k = 0; k < WK; ++k) mx = fmaxf(mx, ml[row + k * WR * 16].x);
                 const float off = mx == -INFINITY ? 0.f : mx;
                 float sx = 0.f, sy = 0.f, sl = 0.f;
 #pragma unroll
                 for (int k = 0; k < WK; ++k) {
-                    const float *sk = s0 + k * WR * 16 * L::RED_LD;
-                    const float f = ex2(sk[DH] - off);
-                    sx += f * sk[c];
-                    sy += f * sk[c + 1];
-                    sl += f * sk[DH + 1];
+                    const float2 w = ml[row + k * WR * 16];
+                    const float f = ex2(w.x - off);
+                    const float2 v = *reinterpret_cast<const float2 *>(red + (row + k * WR * 16) * DH +
+                                                                       col(row, c & ~7) + (c & 7));
+                    sx += f * v.x;
+                    sy += f * v.y;
+                    sl += f * w.y;
                 }
                 float *d = dst + (long long)row * (DH + 2);
                 *reinterpret_cast<float2 *>(d + c) = make_float2(sx, sy);
@@ -606,19 +615,49 @@ __global__ void __launch_bounds__(PA_MERGE_THREADS) paged_attn_join(const AttnAr
     float acc[V], mx = -INFINITY, sum = 0.f;
 #pragma unroll
     for (int i = 0; i < V; ++i) acc[i] = 0.f;
+    // n partials, the lanes reading the maxima and sums of 32 at once, then the
+    // weighted o's with four loads in flight
     auto join = [&](const float *base, long long stride, int n) {
-        for (int k = 0; k < n; ++k) {
-            const float *d = base + k * stride;
-            const float pm = d[DH], pl = d[DH + 1];
-            float v[V];
+        for (int k0 = 0; k0 < n; k0 += 32) {
+            const int c = min(32, n - k0);
+            float2 w = make_float2(-INFINITY, 0.f);
+            if (lane < c) w = *reinterpret_cast<const float2 *>(base + (k0 + lane) * stride + DH);
+            float mn = w.x;
 #pragma unroll
-            for (int i = 0; i < V; ++i) v[i] = d[lane * V + i];
-            const float mn = fmaxf(mx, pm), off = mn == -INFINITY ? 0.f : mn;
-            const float f0 = ex2(mx - off), f1 = ex2(pm - off);
+            for (int o = 16; o > 0; o >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+            mn = fmaxf(mn, mx);
+            const float off = mn == -INFINITY ? 0.f : mn;
+            const float f0 = ex2(mx - off), f = ex2(w.x - off);
+            float add = w.y * f;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) add += __shfl_xor_sync(0xffffffffu, add, o);
             mx = mn;
-            sum = sum * f0 + pl * f1;
+            sum = sum * f0 + add;
 #pragma unroll
-            for (int i = 0; i < V; ++i) acc[i] = acc[i] * f0 + v[i] * f1;
+            for (int i = 0; i < V; ++i) acc[i] *= f0;
+            for (int k = 0; k < c; k += 4) {
+                float v[4][V], fk[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    fk[j] = __shfl_sync(0xffffffffu, f, min(k + j, 31));
+                    const float *d = base + (k0 + min(k + j, c - 1)) * stride + lane * V;
+#pragma unroll
+                    for (int i = 0; i < V; i += V >= 2 ? 2 : 1) {
+                        if constexpr (V >= 2) {
+                            const float2 x2 = *reinterpret_cast<const float2 *>(d + i);
+                            v[j][i] = x2.x, v[j][i + 1] = x2.y;
+                        } else {
+                            v[j][i] = d[i];
+                        }
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (k + j < c) {
+#pragma unroll
+                        for (int i = 0; i < V; ++i) acc[i] += v[j][i] * fk[j];
+                    }
+            }
         }
     };
     if (s.member && tiles_c > 0) {
