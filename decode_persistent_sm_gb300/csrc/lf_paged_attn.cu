@@ -59,7 +59,7 @@ struct AttnArgs {
     uint32_t *err;
 };
 
-constexpr int kPlanWords = 4;  // head of the plan: tiles per common item, all tiles (low, high word), unused
+constexpr int kPlanWords = 4;  // head of the plan: tiles per common item, all tiles, two unused
 
 // What one sequence sees.
 struct Span {
@@ -79,12 +79,21 @@ __device__ __forceinline__ int own_count(const Span &s, int clo, int shared) {
     return s.member ? (clo - s.lo) + (s.len - shared) : s.len - s.lo;
 }
 
-// CTAs that get a share of the list (each at least one tile), and the CTA that
-// owns tile u of it: the last c with floor(total c / ctas) <= u.
-__device__ __forceinline__ int shares(long long total, int grid) { return total < grid ? (int)total : grid; }
-__device__ __forceinline__ int owner(long long u, long long total, int ctas) {
-    return (int)(((u + 1) * ctas - 1) / total);
-}
+// The list's shares: the first total % ctas CTAs take one tile more.  No share
+// is empty (a list shorter than the grid goes to its first tiles' CTAs).
+struct Shares {
+    int q, r;
+    __device__ Shares(int total, int grid) {
+        const int ctas = min(total, grid);
+        q = ctas ? total / ctas : 0;
+        r = ctas ? total - q * ctas : 0;
+    }
+    __device__ int begin(int c) const { return c * q + min(c, r); }
+    __device__ int owner(int u) const {
+        const int head = r * (q + 1);
+        return u < head ? u / (q + 1) : r + (u - head) / q;
+    }
+};
 
 template <typename T>
 __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1);
@@ -137,6 +146,8 @@ struct Place {
     int tile, tiles;
     bool common;
     int b, h, rt;
+    // the item's keys: key k is position first + k, + gap from key gap_at on
+    int keys, first, gap_at, gap;
 };
 
 // Three stages of 32 KB at head_dim 128, so that two CTAs share an SM with 128 KB
@@ -146,8 +157,9 @@ struct Smem {
     static constexpr int TILE = PA_KT * DH * 2;  // bytes of K (or V) of one tile
     static constexpr int STAGES = DH == 128 ? 3 : DH == 64 ? 6 : 8;
     static constexpr int ML = 4 * 16 * 2 * 4;  // max and sum of the rows that the warps join
+    static constexpr int Q = PA_MAX_GROUP * DH * 2;  // an own item's query rows, one buffer per stage
     static constexpr int CUM = (PA_MAX_SEQS + 4) * 4;
-    static constexpr int BYTES = STAGES * 2 * TILE + ML + CUM + 16 * 4;
+    static constexpr int BYTES = STAGES * (2 * TILE + Q) + ML + CUM;
     // the join of the warps' rows uses the stage of the item's last tile
     static_assert(4 * 16 * DH * 4 <= 2 * TILE, "the joined rows fit the stage");
 };
@@ -157,93 +169,82 @@ class Walker {
   public:
     __device__ Walker(const AttnArgs &args, uint8_t *smem) : a(args) {
         stage0 = smem;
-        ml = reinterpret_cast<float2 *>(smem + L::STAGES * 2 * L::TILE);
-        cum = reinterpret_cast<int *>(smem + L::STAGES * 2 * L::TILE + L::ML);
+        q0 = smem + L::STAGES * 2 * L::TILE;
+        ml = reinterpret_cast<float2 *>(q0 + L::STAGES * L::Q);
+        cum = reinterpret_cast<int *>(q0 + L::STAGES * L::Q + L::ML);
         tid = threadIdx.x;
         warp = tid >> 5;
         lane = tid & 31;
     }
 
     // The plan from the lengths: the common range and the own tiles before
-    // each sequence.  Every CTA works it out for itself (at most 8 lengths per
-    // thread); CTA 0 leaves it for the join.
+    // each sequence.  Every warp works it out for itself, so that only the
+    // table waits for a barrier; CTA 0 leaves it for the join.
     __device__ void plan() {
-        int *scratch = cum + PA_MAX_SEQS + 1;  // common start
-        if (tid == 0) *scratch = -1;
-        __syncthreads();
+        const int n = a.kv.n_seqs;
         int lo = -1;
         bool bad = false;
-        for (int b = tid; b < a.kv.n_seqs; b += PA_THREADS) {
+        for (int b = lane; b < n; b += 32) {
             const int len = a.lens[b];
             bad |= len < 0 || len > a.max_len;
             const Span s = span_of(a, b);
             if (s.member) lo = max(lo, s.lo);
         }
         if (bad && blockIdx.x == 0) atomicExch(a.err, 1u);
-        lo = __reduce_max_sync(0xffffffffu, lo);
-        if (lane == 0) atomicMax(scratch, lo);
-        __syncthreads();
-        clo = *scratch;
+        clo = __reduce_max_sync(0xffffffffu, lo);
         tiles_c = clo < 0 ? 0 : (a.shared - clo + PA_KT - 1) / PA_KT;
         if (clo < 0) clo = a.shared;
-        // own tiles: each thread a run of sequences, then a scan over the threads
-        const int per = (a.kv.n_seqs + PA_THREADS - 1) / PA_THREADS, b0 = tid * per;
-        int sum = 0;
-        for (int i = 0; i < per; ++i)
-            if (b0 + i < a.kv.n_seqs) sum += own_tiles(b0 + i);
-        int inc = sum;
+        int at = 0;
+        for (int b0 = 0; b0 < n; b0 += 32) {
+            const int b = b0 + lane;
+            const int t = b < n ? (own_count(span_of(a, b), clo, a.shared) + PA_KT - 1) / PA_KT : 0;
+            int inc = t;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, inc, o);
-            if (lane >= o) inc += y;
-        }
-        int *wsum = cum + PA_MAX_SEQS + 4;
-        if (lane == 31) wsum[warp] = inc;
-        __syncthreads();
-        int at = inc - sum;
-        for (int w = 0; w < warp; ++w) at += wsum[w];
-        for (int i = 0; i < per; ++i)
-            if (b0 + i < a.kv.n_seqs) {
-                cum[b0 + i] = at;
-                at += own_tiles(b0 + i);
-                if (b0 + i == a.kv.n_seqs - 1) cum[a.kv.n_seqs] = at;
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += y;
             }
-        __syncthreads();
-        common_total = (long long)a.kv.n_kv * a.row_tiles * tiles_c;
-        total = common_total + (long long)a.kv.n_kv * cum[a.kv.n_seqs];
-        if (blockIdx.x == 0) {
-            if (tid == 0) {
-                a.plan[0] = tiles_c;
-                a.plan[1] = (int)(total & 0xffffffff);
-                a.plan[2] = (int)(total >> 32);
+            if (warp == 0 && b < n) {
+                cum[b] = at + inc - t;
+                if (blockIdx.x == 0) a.plan[kPlanWords + b] = at + inc - t;
             }
-            for (int b = tid; b <= a.kv.n_seqs; b += PA_THREADS) a.plan[kPlanWords + b] = cum[b];
+            at += __shfl_sync(0xffffffffu, inc, 31);
         }
+        if (tid == 0) cum[n] = at;
+        common_total = a.kv.n_kv * a.row_tiles * tiles_c;
+        total = common_total + a.kv.n_kv * at;
+        if (blockIdx.x == 0 && tid == 0) {
+            a.plan[0] = tiles_c;
+            a.plan[1] = total;
+            a.plan[kPlanWords + n] = at;
+        }
+        __syncthreads();
     }
 
     __device__ void run() {
-        const int ctas = shares(total, gridDim.x);
-        if ((int)blockIdx.x >= ctas) return;
-        const long long u0 = total * blockIdx.x / ctas, u1 = total * (blockIdx.x + 1) / ctas;
-        const int n = (int)(u1 - u0);
-        Place load = place(u0), work = load;
+        const Shares sh(total, gridDim.x);
+        if ((int)blockIdx.x >= min(total, (int)gridDim.x)) return;
+        const int u0 = sh.begin(blockIdx.x), n = sh.begin(blockIdx.x + 1) - u0;
+        Place work = place(u0), load = work;
         prepare(load);
         int loaded = 0;
-        for (; loaded < L::STAGES - 1; ++loaded) {
+        bool load_fresh = true;  // load is the first tile of its item in this CTA
+        auto fetch_next = [&] {
             if (loaded < n) {
-                fetch(loaded % L::STAGES);
-                if (loaded + 1 < n) step(load);
-            }
-            cp_async_commit();
-        }
-        bool fresh = true;
-        for (int i = 0; i < n; ++i) {
-            if (loaded < n) {
-                fetch(loaded % L::STAGES);
-                if (loaded + 1 < n) step(load);
+                fetch(loaded % L::STAGES, load, load_fresh);
+                if (loaded + 1 < n) {
+                    load_fresh = advance(load);
+                    prepare(load);
+                }
             }
             ++loaded;
             cp_async_commit();
+        };
+        for (int i = 0; i < L::STAGES - 1; ++i) fetch_next();
+        bool fresh = true;
+        for (int i = 0; i < n; ++i) {
+            if (fresh && work.common) common_queries(work);
+            fetch_next();
             asm volatile("cp.async.wait_group %0;" ::"n"(L::STAGES - 1) : "memory");
             __syncthreads();
             const bool last = i + 1 == n || work.tile + 1 == work.tiles;
@@ -258,7 +259,7 @@ class Walker {
             } else {
                 tile<1>(work, a.group, fresh, last, i % L::STAGES);
             }
-            __syncthreads();  // the stage (and the join buffer) may be written again
+            __syncthreads();  // the stage may be written again
             fresh = last;
             if (i + 1 < n) advance(work);
         }
@@ -267,12 +268,12 @@ class Walker {
   private:
     using L = Smem<T, DH>;
     const AttnArgs &a;
-    uint8_t *stage0;
+    uint8_t *stage0, *q0;
     float2 *ml;
     int *cum;
     int tid, warp, lane;
     int clo, tiles_c;
-    long long common_total, total;
+    int common_total, total;
     // pages of the tile to be fetched next: element offsets of rows lane and
     // lane + 32 (-1: no such key)
     long long row_off[2];
@@ -282,99 +283,89 @@ class Walker {
     float o[DH / 8][4];
     float m[2], l[2];
 
-    __device__ int own_tiles(int b) const {
-        const Span s = span_of(a, b);
-        return (own_count(s, clo, a.shared) + PA_KT - 1) / PA_KT;
+    // The keys of p's item.
+    __device__ void set_keys(Place &p) const {
+        p.gap_at = INT_MAX;
+        p.gap = 0;
+        if (p.common) {
+            p.first = clo;
+            p.keys = a.shared - clo;
+            return;
+        }
+        const Span s = span_of(a, p.b);
+        p.first = s.lo;
+        p.keys = own_count(s, clo, a.shared);
+        if (s.member) {
+            p.gap_at = clo - s.lo;
+            p.gap = a.shared - clo;
+        }
     }
 
-    __device__ Place place(long long u) const {
+    __device__ Place place(int u) const {
         Place p;
         if (u < common_total) {
             p.common = true;
-            p.item = (int)(u / tiles_c);
-            p.tile = (int)(u % tiles_c);
+            p.item = u / tiles_c;
+            p.tile = u - p.item * tiles_c;
             p.tiles = tiles_c;
             p.h = p.item / a.row_tiles;
-            p.rt = p.item % a.row_tiles;
+            p.rt = p.item - p.h * a.row_tiles;
             p.b = 0;
-            return p;
+        } else {
+            const int v = u - common_total;
+            int lo = 0, hi = a.kv.n_seqs;  // the sequence with n_kv cum[b] <= v < n_kv cum[b + 1]
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) / 2;
+                if (a.kv.n_kv * cum[mid] <= v)
+                    lo = mid;
+                else
+                    hi = mid;
+            }
+            p.common = false;
+            p.b = lo;
+            p.tiles = cum[lo + 1] - cum[lo];
+            const int r = v - a.kv.n_kv * cum[lo];
+            p.h = r / p.tiles;
+            p.tile = r - p.h * p.tiles;
+            p.rt = 0;
+            p.item = p.b * a.kv.n_kv + p.h;
         }
-        const long long v = u - common_total;
-        int lo = 0, hi = a.kv.n_seqs;  // the sequence with n_kv cum[b] <= v < n_kv cum[b + 1]
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) / 2;
-            if ((long long)a.kv.n_kv * cum[mid] <= v)
-                lo = mid;
-            else
-                hi = mid;
-        }
-        p.common = false;
-        p.b = lo;
-        p.tiles = cum[lo + 1] - cum[lo];
-        const int r = (int)(v - (long long)a.kv.n_kv * cum[lo]);
-        p.h = r / p.tiles;
-        p.tile = r % p.tiles;
-        p.rt = 0;
-        p.item = p.b * a.kv.n_kv + p.h;
+        set_keys(p);
         return p;
     }
 
-    // The next tile of the list.
-    __device__ void advance(Place &p) const {
-        if (++p.tile < p.tiles) return;
+    // The next tile of the list; true if it begins another item.
+    __device__ bool advance(Place &p) const {
+        if (++p.tile < p.tiles) return false;
         p.tile = 0;
+        ++p.item;
         if (p.common) {
-            ++p.item;
-            if (++p.rt == a.row_tiles) {
-                p.rt = 0;
-                if (++p.h == a.kv.n_kv) {  // on to the own items
-                    p.common = false;
-                    p.h = 0;
-                    p.b = -1;
-                    next_seq(p);
-                }
-            }
-            return;
+            if (++p.rt < a.row_tiles) return true;
+            p.rt = 0;
+            if (++p.h < a.kv.n_kv) return true;
+            p.common = false;  // on to the own items
+            p.b = -1;
+        } else {
+            if (++p.h < a.kv.n_kv) return true;
         }
-        if (++p.h == a.kv.n_kv) {
-            p.h = 0;
-            next_seq(p);
-        }
-        p.item = p.b * a.kv.n_kv + p.h;
-    }
-    __device__ void next_seq(Place &p) const {
+        p.h = 0;
         do {
             ++p.b;
         } while (p.b < a.kv.n_seqs - 1 && cum[p.b + 1] == cum[p.b]);
         p.tiles = cum[p.b + 1] - cum[p.b];
-        p.item = p.b * a.kv.n_kv + p.h;
-    }
-
-    // Keys of an item, counted from 0.
-    __device__ int keys_of(const Place &p) const {
-        if (p.common) return a.shared - clo;
-        const Span s = span_of(a, p.b);
-        return own_count(s, clo, a.shared);
+        p.item = p.b * a.kv.n_kv;
+        set_keys(p);
+        return true;
     }
 
     // Looks up the pages of p's tile (rows lane and lane + 32).
     __device__ void prepare(const Place &p) {
-        const int n = keys_of(p);
-        int first = clo, gap_at = INT_MAX, gap = 0;
-        if (!p.common) {
-            const Span s = span_of(a, p.b);
-            first = s.lo;
-            if (s.member) {
-                gap_at = clo - s.lo;
-                gap = a.shared - clo;
-            }
-        }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int k = p.tile * PA_KT + lane + 32 * i;
             row_off[i] = -1;
-            if (k < n) {
-                const int j = first + k + (k >= gap_at ? gap : 0);
+            if (k < p.keys) {
+                const int j = p.first + k + (k >= p.gap_at ? p.gap : 0);
                 const int row = j < a.shared ? 0 : p.b;
                 const int page = __ldg(a.kv.table + (long long)row * a.kv.max_pages + (j >> a.kv.ps_log2));
                 if (page >= 0 && page < a.kv.n_pages)
@@ -385,14 +376,17 @@ class Walker {
             }
         }
     }
-    __device__ void step(Place &p) {
-        advance(p);
-        prepare(p);
-    }
 
-    // Starts the copies of the prepared tile into stage s.
-    __device__ void fetch(int s) {
+    // Starts the copies of the prepared tile into stage s
+    // and, with the first tile of an own item, of the item's query rows.
+    __device__ void fetch(int s, const Place &p, bool first) {
         constexpr int CH = DH / 8;                  // 16-byte chunks per row
+        if (first && !p.common) {
+            const uint32_t qs = smem_u32(q0 + s * L::Q);
+            const T *q = static_cast<const T *>(a.q) + (long long)p.b * a.ld_q + (long long)p.h * a.group * DH;
+            for (int x = tid; x < a.group * CH; x += PA_THREADS)
+                cp16_or_zero(qs + tile_off<DH>(x / CH, x % CH), q + (x / CH) * DH + (x % CH) * 8, true);
+        }
         constexpr int RP = PA_THREADS / CH;         // rows per pass
         const int c = tid % CH, r0 = tid / CH;
         const uint32_t ks = smem_u32(stage0 + (size_t)s * 2 * L::TILE), vs = ks + L::TILE;
@@ -415,7 +409,11 @@ class Walker {
         constexpr int WK = 4 / WR, NB = PA_KT / (16 * WK);  // NB blocks of 16 keys per warp
         const int wr = warp % WR, wk = warp / WR, t = lane & 3;
         if (fresh) {
-            begin(p, wr, rows);
+            if (!p.common) {  // (rows past the group hold anything: their results are dropped)
+                const uint32_t qs = smem_u32(q0 + s * L::Q);
+#pragma unroll
+                for (int kk = 0; kk < DH / 16; ++kk) ldsm_x4(qs + tile_off<DH>(lane & 15, 2 * kk + (lane >> 4)), qf[kk]);
+            }
 #pragma unroll
             for (int i = 0; i < DH / 8; ++i)
 #pragma unroll
@@ -424,7 +422,7 @@ class Walker {
             l[0] = l[1] = 0.f;
         }
         const uint32_t ks = smem_u32(stage0 + (size_t)s * 2 * L::TILE), vs = ks + L::TILE;
-        const int left = keys_of(p) - p.tile * PA_KT;  // keys of this tile (may exceed it)
+        const int left = p.keys - p.tile * PA_KT;  // keys of this tile (may exceed it)
         float sc[2 * NB][4];
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
@@ -498,22 +496,20 @@ class Walker {
         if (last) finish<WR>(p, wr, rows, s);
     }
 
-    // Q fragments of this warp's 16 rows (rows past the item's are zero).
-    __device__ void begin(const Place &p, int wr, int rows) {
-        const int g = lane >> 2, t = lane & 3;
+    // Q fragments of this warp's 16 rows of a common item, straight from global
+    // memory (rows past the item's are zero).
+    __device__ void common_queries(const Place &p) {
+        const int rows = min(PA_ROWS, a.kv.n_seqs * a.group - p.rt * PA_ROWS);
+        const int wr = rows <= 16 ? 0 : rows <= 32 ? warp % 2 : warp, g = lane >> 2, t = lane & 3;
         const T *base[2];
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
             const int row = wr * 16 + g + 8 * r;
             base[r] = nullptr;
             if (row < rows) {
-                int b = p.b, x = row;
-                if (p.common) {
-                    const int all = p.rt * PA_ROWS + row;
-                    b = all / a.group;
-                    x = all % a.group;
-                }
-                base[r] = static_cast<const T *>(a.q) + (long long)b * a.ld_q + (long long)(p.h * a.group + x) * DH;
+                const int all = p.rt * PA_ROWS + row, b = all / a.group;
+                base[r] = static_cast<const T *>(a.q) + (long long)b * a.ld_q +
+                          (long long)(p.h * a.group + all - b * a.group) * DH;
             }
         }
 #pragma unroll
@@ -606,10 +602,9 @@ __global__ void __launch_bounds__(PA_MERGE_THREADS) paged_attn_join(const AttnAr
     const int x = (int)((blockIdx.x * (long long)PA_MERGE_THREADS + threadIdx.x) >> 5), lane = threadIdx.x & 31;
     if (x >= a.kv.n_seqs * a.n_q) return;
     const int b = x / a.n_q, hq = x % a.n_q, h = hq / a.group, r = hq % a.group;
-    const int tiles_c = a.plan[0];
-    const long long total = (long long)(uint32_t)a.plan[1] | ((long long)a.plan[2] << 32);
-    const long long common_total = (long long)a.kv.n_kv * a.row_tiles * tiles_c;
-    const int ctas = shares(total, a.grid);
+    const int tiles_c = a.plan[0], total = a.plan[1], t0 = a.plan[kPlanWords + b];
+    const int tiles = a.plan[kPlanWords + b + 1] - t0, common_total = a.kv.n_kv * a.row_tiles * tiles_c;
+    const Shares sh(total, a.grid);
     const Span s = span_of(a, b);
     constexpr int V = DH / 32;  // values per lane
     float acc[V], mx = -INFINITY, sum = 0.f;
@@ -662,16 +657,13 @@ __global__ void __launch_bounds__(PA_MERGE_THREADS) paged_attn_join(const AttnAr
     };
     if (s.member && tiles_c > 0) {
         const int row = b * a.group + r, item = h * a.row_tiles + row / PA_ROWS;
-        const long long u = (long long)item * tiles_c;
-        const int c0 = owner(u, total, ctas), c1 = owner(u + tiles_c - 1, total, ctas);
+        const int u = item * tiles_c, c0 = sh.owner(u), c1 = sh.owner(u + tiles_c - 1);
         join(a.part_c + ((long long)(item + c0) * PA_ROWS + row % PA_ROWS) * (DH + 2), (long long)PA_ROWS * (DH + 2),
              c1 - c0 + 1);
     }
-    const int t0 = a.plan[kPlanWords + b], tiles = a.plan[kPlanWords + b + 1] - t0;
     if (tiles > 0) {
         const int item = b * a.kv.n_kv + h;
-        const long long u = common_total + (long long)a.kv.n_kv * t0 + (long long)h * tiles;
-        const int c0 = owner(u, total, ctas), c1 = owner(u + tiles - 1, total, ctas);
+        const int u = common_total + a.kv.n_kv * t0 + h * tiles, c0 = sh.owner(u), c1 = sh.owner(u + tiles - 1);
         join(a.part_o + ((long long)(item + c0) * a.group + r) * (DH + 2), (long long)a.group * (DH + 2), c1 - c0 + 1);
     }
     const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);  // (a NaN stays one)
@@ -773,6 +765,10 @@ extern "C" lf_status lf_attn_paged_shared(const lf_paged_kv *kv, const void *q_d
         !(scale > 0.f && scale < INFINITY))
         return LF_ERR_INVALID_ARG;
     a.group = n_q_heads / a.kv.n_kv;
+    // tiles are counted in 32 bits
+    const long long per_head = (long long)(shared_len / lf::PA_KT + 1) * (((long long)kv->n_seqs * a.group) / lf::PA_ROWS + 1) +
+                               (long long)(max_len / lf::PA_KT + 2) * kv->n_seqs;
+    if (per_head * kv->n_kv_heads > INT_MAX) return LF_ERR_UNSUPPORTED;
     a.row_tiles = (a.kv.n_seqs * a.group + lf::PA_ROWS - 1) / lf::PA_ROWS;
     const int n_sm = lf::sm_count();
     if (!n_sm) return LF_ERR_CUDA;

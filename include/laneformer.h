@@ -509,7 +509,8 @@ lf_status lf_kv_append_paged(const lf_paged_kv *kv, const void *q_in, const void
  * LF_ERR_INVALID_ARG for bad sizes, pointers, strides or types, shared_len or
  * max_len above max_pages * page_size, or a workspace too small;
  * LF_ERR_UNSUPPORTED for head_dim other than 32, 64 or 128, more than 16
- * query heads per KV head or more than 1024 sequences. */
+ * query heads per KV head, more than 1024 sequences, or max_len * n_seqs *
+ * n_kv_heads above about 2^37. */
 lf_status lf_attn_paged_shared(const lf_paged_kv *kv, const void *q_device, int64_t ld_q, void *out_device,
                                int64_t ld_out, float *lse_device, int n_q_heads, const int32_t *lens_device,
                                int max_len, int shared_len, int window, float scale, void *workspace_device,
