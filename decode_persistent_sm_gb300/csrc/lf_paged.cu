@@ -96,6 +96,8 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendA
     if (t_ll >= a.n_tokens) return;
     const int t = (int)t_ll, x = threadIdx.x % per_token, c0 = x % pieces * 8, slot = x / pieces + slots * blockIdx.y * U;
     const int heads = a.n_q + 2 * a.kv.n_kv;
+    pdl_wait();
+    pdl_trigger();
     const int seq = a.seq ? a.seq[t] : t;
     const int p = a.pos[t];
     if (seq < 0) return;  // padding
@@ -161,32 +163,26 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendA
 }
 
 template <typename TI, typename TO, int U>
-void launch_units(const AppendArgs &a, cudaStream_t st) {
+bool launch_units(const AppendArgs &a, cudaStream_t st) {
     const int pieces = a.kv.head_dim / 16, heads = a.n_q + 2 * a.kv.n_kv;  // pieces: 1 .. 16
     const int slots = min((heads + U - 1) / U, kAppendThreads / pieces);
     const int tokens = kAppendThreads / (pieces * slots);  // per block
     const int y = (heads + slots * U - 1) / (slots * U);
-    kv_append_kernel<TI, TO, U><<<dim3((unsigned)((a.n_tokens + tokens - 1) / tokens), (unsigned)y),
-                                  pieces * slots * tokens, 0, st>>>(a, slots);
+    return launch_pdl(kv_append_kernel<TI, TO, U>, dim3((unsigned)((a.n_tokens + tokens - 1) / tokens), (unsigned)y),
+                      (unsigned)(pieces * slots * tokens), 0, st, a, slots);
 }
 
 template <typename TI, typename TO>
-void launch_append(const AppendArgs &a, cudaStream_t st) {
+bool launch_append(const AppendArgs &a, cudaStream_t st) {
     // four units a thread once that still leaves a few blocks per SM, one unit
     // for the few tokens of a decode step (a shorter chain in each thread)
     const long long units = (long long)a.n_tokens * (a.n_q + 2 * a.kv.n_kv) * (a.kv.head_dim / 16);
-    if (units >= kAppendManyUnits)
-        launch_units<TI, TO, 4>(a, st);
-    else
-        launch_units<TI, TO, 1>(a, st);
+    return units >= kAppendManyUnits ? launch_units<TI, TO, 4>(a, st) : launch_units<TI, TO, 1>(a, st);
 }
 
 template <typename TI>
-void launch_append_to(const AppendArgs &a, int dtype, cudaStream_t st) {
-    if (dtype == LF_F16)
-        launch_append<TI, __half>(a, st);
-    else
-        launch_append<TI, __nv_bfloat16>(a, st);
+bool launch_append_to(const AppendArgs &a, int dtype, cudaStream_t st) {
+    return dtype == LF_F16 ? launch_append<TI, __half>(a, st) : launch_append<TI, __nv_bfloat16>(a, st);
 }
 
 }  // namespace
@@ -232,11 +228,8 @@ extern "C" lf_status lf_kv_append_paged(const lf_paged_kv *kv, const void *q_in,
     a.rope_len = rope_len;
     a.err = err_device;
     cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
-    if (in_dtype == LF_F32)
-        lf::launch_append_to<float>(a, kv->dtype, st);
-    else if (in_dtype == LF_F16)
-        lf::launch_append_to<__half>(a, kv->dtype, st);
-    else
-        lf::launch_append_to<__nv_bfloat16>(a, kv->dtype, st);
-    return cudaGetLastError() == cudaSuccess ? LF_OK : LF_ERR_CUDA;
+    const bool ok = in_dtype == LF_F32   ? lf::launch_append_to<float>(a, kv->dtype, st)
+                    : in_dtype == LF_F16 ? lf::launch_append_to<__half>(a, kv->dtype, st)
+                                         : lf::launch_append_to<__nv_bfloat16>(a, kv->dtype, st);
+    return ok ? LF_OK : LF_ERR_CUDA;
 }

@@ -45,6 +45,43 @@ inline lf_status paged_view(const lf_paged_kv *kv, PagedView *out) {
     return LF_OK;
 }
 
+// Programmatic dependent launch.  The kernels of these calls are launched so
+// that they may become resident before the stream's previous kernel has
+// finished; pdl_wait is the first thing they do, and returns when that kernel's
+// results are visible.  pdl_trigger lets the next such kernel become resident
+// in turn.  (A kernel launched without the attribute still waits for all of
+// this one.)  It hides about 2 us of launch latency between these kernels.
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+template <typename... P, typename... A>
+inline bool launch_pdl_cluster(void (*kernel)(P...), unsigned cluster, dim3 grid, unsigned threads, size_t smem,
+                               cudaStream_t st, const A &...args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = cluster;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return false;
+    }
+    return true;
+}
+template <typename... P, typename... A>
+inline bool launch_pdl(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t st,
+                       const A &...args) {
+    return launch_pdl_cluster(kernel, 1, grid, threads, smem, st, args...);
+}
+
 // Raises a kernel's dynamic shared-memory limit once per device.
 template <auto Kernel>
 inline bool set_smem_once(int bytes) {

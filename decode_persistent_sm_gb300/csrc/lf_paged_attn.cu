@@ -11,7 +11,7 @@
 // sees besides goes through its own items, so no masked position ever enters
 // a product.
 //
-// Work is cut into tiles of 64 keys.  An item is (KV head, row tile) of the
+// Work is cut into tiles of 64 or 128 keys.  An item is (KV head, row tile) of the
 // common range or (sequence, KV head) of the own ranges; all tiles of all
 // items form one list, cut into equal contiguous shares, one per CTA, so ragged
 // lengths and short batches fill the GPU alike.  A CTA walks its share with a
@@ -35,8 +35,10 @@
 namespace lf {
 namespace {
 
-constexpr int PA_THREADS = 128, PA_KT = 64, PA_ROWS = 64, PA_MAX_SEQS = 1024, PA_MAX_GROUP = 16;
+constexpr int PA_THREADS = 128, PA_ROWS = 64, PA_MAX_SEQS = 1024, PA_MAX_GROUP = 16;
 constexpr int PA_CTAS_PER_SM = 2;
+// keys per tile: 32 KB of K and V at head_dim 64 and 128 (a 16 KB tile's barriers and softmax statistics cost more than its copy)
+__host__ __device__ constexpr int tile_keys(int dim) { return dim == 128 ? 64 : 128; }
 constexpr int PA_MERGE_THREADS = 128;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -54,8 +56,11 @@ struct AttnArgs {
     int grid;          // CTAs of the first kernel
     // workspace
     int *plan;         // kPlanWords, then the own tiles before each sequence [n_seqs + 1]
-    float *part_c;     // common partials: [n_kv * row_tiles + grid][PA_ROWS][head_dim + 2]
-    float *part_o;     // own partials: [n_seqs * n_kv + grid][group][head_dim + 2]
+    // partials, common items' slots first: slots_c = n_kv * row_tiles + grid of PA_ROWS rows, then n_seqs * n_kv + grid
+    // of `group` rows
+    int slots_c;
+    float *part_o;     // [row][head_dim], unnormalised
+    float2 *part_ml;   // [row] (max in the log2 domain, sum)
     uint32_t *err;
 };
 
@@ -150,12 +155,13 @@ struct Place {
     int keys, first, gap_at, gap;
 };
 
-// Three stages of 32 KB at head_dim 128, so that two CTAs share an SM with 128 KB
-// of copies in flight; as many bytes in more stages for smaller heads.
+// Three stages of 32 KB (six of 16 KB at head_dim 32), so that two CTAs share an
+// SM with 128 KB of copies in flight.
 template <typename T, int DH>
 struct Smem {
-    static constexpr int TILE = PA_KT * DH * 2;  // bytes of K (or V) of one tile
-    static constexpr int STAGES = DH == 128 ? 3 : DH == 64 ? 6 : 8;
+    static constexpr int KT = tile_keys(DH);
+    static constexpr int TILE = KT * DH * 2;  // bytes of K (or V) of one tile
+    static constexpr int STAGES = DH == 32 ? 6 : 3;
     static constexpr int ML = 4 * 16 * 2 * 4;  // max and sum of the rows that the warps join
     static constexpr int Q = PA_MAX_GROUP * DH * 2;  // an own item's query rows, one buffer per stage
     static constexpr int CUM = (PA_MAX_SEQS + 4) * 4;
@@ -192,12 +198,12 @@ class Walker {
         }
         if (bad && blockIdx.x == 0) atomicExch(a.err, 1u);
         clo = __reduce_max_sync(0xffffffffu, lo);
-        tiles_c = clo < 0 ? 0 : (a.shared - clo + PA_KT - 1) / PA_KT;
+        tiles_c = clo < 0 ? 0 : (a.shared - clo + KT - 1) / KT;
         if (clo < 0) clo = a.shared;
         int at = 0;
         for (int b0 = 0; b0 < n; b0 += 32) {
             const int b = b0 + lane;
-            const int t = b < n ? (own_count(span_of(a, b), clo, a.shared) + PA_KT - 1) / PA_KT : 0;
+            const int t = b < n ? (own_count(span_of(a, b), clo, a.shared) + KT - 1) / KT : 0;
             int inc = t;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -267,6 +273,7 @@ class Walker {
 
   private:
     using L = Smem<T, DH>;
+    static constexpr int KT = L::KT;
     const AttnArgs &a;
     uint8_t *stage0, *q0;
     float2 *ml;
@@ -274,9 +281,8 @@ class Walker {
     int tid, warp, lane;
     int clo, tiles_c;
     int common_total, total;
-    // pages of the tile to be fetched next: element offsets of rows lane and
-    // lane + 32 (-1: no such key)
-    long long row_off[2];
+    // the tile to be fetched next: element offsets of rows lane + 32 i (-1: no such key)
+    long long row_off[KT / 32];
 
     // running state of this warp's 16 rows (lane 4 g + t: rows g and g + 8)
     uint32_t qf[DH / 16][4];
@@ -358,11 +364,11 @@ class Walker {
         return true;
     }
 
-    // Looks up the pages of p's tile (rows lane and lane + 32).
+    // Looks up the pages of p's tile.
     __device__ void prepare(const Place &p) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int k = p.tile * PA_KT + lane + 32 * i;
+        for (int i = 0; i < KT / 32; ++i) {
+            const int k = p.tile * KT + lane + 32 * i;
             row_off[i] = -1;
             if (k < p.keys) {
                 const int j = p.first + k + (k >= p.gap_at ? p.gap : 0);
@@ -392,11 +398,10 @@ class Walker {
         const uint32_t ks = smem_u32(stage0 + (size_t)s * 2 * L::TILE), vs = ks + L::TILE;
         const T *k = static_cast<const T *>(a.kv.k), *v = static_cast<const T *>(a.kv.v);
 #pragma unroll
-        for (int i = 0; i < PA_KT / RP; ++i) {
+        for (int i = 0; i < KT / RP; ++i) {
             const int r = i * RP + r0;
-            const long long o0 = __shfl_sync(0xffffffffu, row_off[0], r & 31);
-            const long long o1 = __shfl_sync(0xffffffffu, row_off[1], r & 31);
-            const long long off = r < 32 ? o0 : o1;
+            // (the RP rows of a pass lie in one group of 32: RP divides 32)
+            const long long off = __shfl_sync(0xffffffffu, row_off[i * RP / 32], r & 31);
             const long long at = off < 0 ? 0 : off + c * 8;
             cp16_or_zero(ks + tile_off<DH>(r, c), k + at, off >= 0);
             cp16_or_zero(vs + tile_off<DH>(r, c), v + at, off >= 0);
@@ -406,7 +411,7 @@ class Walker {
     // One tile of an item's rows: WR warps side by side in rows, 4 / WR in keys.
     template <int WR>
     __device__ void tile(const Place &p, int rows, bool fresh, bool last, int s) {
-        constexpr int WK = 4 / WR, NB = PA_KT / (16 * WK);  // NB blocks of 16 keys per warp
+        constexpr int WK = 4 / WR, NB = KT / (16 * WK);  // NB blocks of 16 keys per warp
         const int wr = warp % WR, wk = warp / WR, t = lane & 3;
         if (fresh) {
             if (!p.common) {  // (rows past the group hold anything: their results are dropped)
@@ -422,7 +427,7 @@ class Walker {
             l[0] = l[1] = 0.f;
         }
         const uint32_t ks = smem_u32(stage0 + (size_t)s * 2 * L::TILE), vs = ks + L::TILE;
-        const int left = p.keys - p.tile * PA_KT;  // keys of this tile (may exceed it)
+        const int left = p.keys - p.tile * KT;  // keys of this tile (may exceed it)
         float sc[2 * NB][4];
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
@@ -438,7 +443,7 @@ class Walker {
                 mma<T>(sc[2 * nb + 1], qf[kk], r[2], r[3]);
             }
         }
-        if (left < PA_KT) {
+        if (left < KT) {
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -526,8 +531,10 @@ class Walker {
     __device__ void finish(const Place &p, int wr, int rows, int s) {
         constexpr int WK = 4 / WR;
         const int g = lane >> 2, t = lane & 3;
-        float *dst = p.common ? a.part_c + (long long)(p.item + blockIdx.x) * PA_ROWS * (DH + 2)
-                              : a.part_o + (long long)(p.item + blockIdx.x) * a.group * (DH + 2);
+        const long long slot0 = p.common ? (long long)(p.item + blockIdx.x) * PA_ROWS
+                                         : (long long)a.slots_c * PA_ROWS + (long long)(p.item + blockIdx.x) * a.group;
+        float *dst = a.part_o + slot0 * DH;
+        float2 *dst_ml = a.part_ml + slot0;
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
             l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
@@ -538,11 +545,11 @@ class Walker {
             for (int r = 0; r < 2; ++r) {
                 const int row = wr * 16 + g + 8 * r;
                 if (row >= rows) continue;
-                float *d = dst + (long long)row * (DH + 2);
+                float *d = dst + row * DH;
 #pragma unroll
                 for (int i = 0; i < DH / 8; ++i)
                     *reinterpret_cast<float2 *>(d + 8 * i + 2 * t) = make_float2(o[i][2 * r], o[i][2 * r + 1]);
-                if (t == 0) *reinterpret_cast<float2 *>(d + DH) = make_float2(m[r], l[r]);
+                if (t == 0) dst_ml[row] = make_float2(m[r], l[r]);
             }
         } else {
             __syncthreads();  // every warp has read this stage's keys and values
@@ -576,9 +583,9 @@ class Walker {
                     sy += f * v.y;
                     sl += f * w.y;
                 }
-                float *d = dst + (long long)row * (DH + 2);
+                float *d = dst + row * DH;
                 *reinterpret_cast<float2 *>(d + c) = make_float2(sx, sy);
-                if (c == 0) *reinterpret_cast<float2 *>(d + DH) = make_float2(mx, sl);
+                if (c == 0) dst_ml[row] = make_float2(mx, sl);
             }
         }
     }
@@ -588,7 +595,8 @@ template <typename T, int DH>
 __global__ void __launch_bounds__(PA_THREADS, PA_CTAS_PER_SM) paged_attn_kernel(const AttnArgs a) {
     extern __shared__ __align__(128) uint8_t pa_smem[];
     Walker<T, DH> w(a, pa_smem);
-    asm volatile("griddepcontrol.launch_dependents;");
+    pdl_wait();
+    pdl_trigger();
     w.plan();
     w.run();
 }
@@ -598,78 +606,90 @@ __global__ void __launch_bounds__(PA_THREADS, PA_CTAS_PER_SM) paged_attn_kernel(
 // order (common item first), normalised and rounded once.
 template <typename T, int DH>
 __global__ void __launch_bounds__(PA_MERGE_THREADS) paged_attn_join(const AttnArgs a) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    constexpr int V = DH / 32;  // values per lane
+    constexpr int U = 8;        // partials in flight
+    pdl_wait();
+    pdl_trigger();
     const int x = (int)((blockIdx.x * (long long)PA_MERGE_THREADS + threadIdx.x) >> 5), lane = threadIdx.x & 31;
     if (x >= a.kv.n_seqs * a.n_q) return;
     const int b = x / a.n_q, hq = x % a.n_q, h = hq / a.group, r = hq % a.group;
     const int tiles_c = a.plan[0], total = a.plan[1], t0 = a.plan[kPlanWords + b];
     const int tiles = a.plan[kPlanWords + b + 1] - t0, common_total = a.kv.n_kv * a.row_tiles * tiles_c;
     const Shares sh(total, a.grid);
-    const Span s = span_of(a, b);
-    constexpr int V = DH / 32;  // values per lane
+    // partial k < n_c of the common item, then n_o of the own one: their rows in the workspace
+    long long row_c = 0, row_o = 0;
+    int n_c = 0, n_o = 0;
+    if (span_of(a, b).member && tiles_c > 0) {
+        const int row = b * a.group + r, item = h * a.row_tiles + row / PA_ROWS, u = item * tiles_c;
+        const int c0 = sh.owner(u);
+        n_c = sh.owner(u + tiles_c - 1) - c0 + 1;
+        row_c = (long long)(item + c0) * PA_ROWS + row % PA_ROWS;
+    }
+    if (tiles > 0) {
+        const int u = common_total + a.kv.n_kv * t0 + h * tiles, c0 = sh.owner(u);
+        n_o = sh.owner(u + tiles - 1) - c0 + 1;
+        row_o = (long long)a.slots_c * PA_ROWS + (long long)(b * a.kv.n_kv + h + c0) * a.group + r;
+    }
+    auto row_of = [&](int k) {
+        return k < n_c ? row_c + (long long)k * PA_ROWS : row_o + (long long)(k - n_c) * a.group;
+    };
     float acc[V], mx = -INFINITY, sum = 0.f;
 #pragma unroll
     for (int i = 0; i < V; ++i) acc[i] = 0.f;
-    // n partials, the lanes reading the maxima and sums of 32 at once, then the
-    // weighted o's with four loads in flight
-    auto join = [&](const float *base, long long stride, int n) {
-        for (int k0 = 0; k0 < n; k0 += 32) {
-            const int c = min(32, n - k0);
-            float2 w = make_float2(-INFINITY, 0.f);
-            if (lane < c) w = *reinterpret_cast<const float2 *>(base + (k0 + lane) * stride + DH);
-            float mn = w.x;
+    const int n = n_c + n_o;
+    for (int k0 = 0; k0 < n; k0 += 32) {
+        const int c = min(32, n - k0);
+        const long long mine = row_of(k0 + min(lane, c - 1));
+        float2 w = a.part_ml[mine];
+        if (lane >= c) w = make_float2(-INFINITY, 0.f);
+        for (int k = 0; k < c; k += U) {
+            float v[U][V];
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
-            mn = fmaxf(mn, mx);
-            const float off = mn == -INFINITY ? 0.f : mn;
-            const float f0 = ex2(mx - off), f = ex2(w.x - off);
-            float add = w.y * f;
+            for (int j = 0; j < U; ++j) {
+                const float *d = a.part_o + __shfl_sync(0xffffffffu, mine, min(k + j, c - 1)) * DH + lane * V;
+                if constexpr (V == 4)
+                    *reinterpret_cast<float4 *>(v[j]) = *reinterpret_cast<const float4 *>(d);
+                else if constexpr (V == 2)
+                    *reinterpret_cast<float2 *>(v[j]) = *reinterpret_cast<const float2 *>(d);
+                else
+                    v[j][0] = d[0];
+            }
+            // (the statistics arrive with the first of these loads)
+            float f = 0.f;
+            if (k == 0) {
+                float mn = w.x;
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) add += __shfl_xor_sync(0xffffffffu, add, o);
-            mx = mn;
-            sum = sum * f0 + add;
+                for (int o = 16; o > 0; o >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+                mn = fmaxf(mn, mx);
+                const float off = mn == -INFINITY ? 0.f : mn, f0 = ex2(mx - off);
+                w.x = ex2(w.x - off);  // from here on the partial's weight
+                float add = w.y * w.x;
 #pragma unroll
-            for (int i = 0; i < V; ++i) acc[i] *= f0;
-            for (int k = 0; k < c; k += 4) {
-                float v[4][V], fk[4];
+                for (int o = 16; o > 0; o >>= 1) add += __shfl_xor_sync(0xffffffffu, add, o);
+                mx = mn;
+                sum = sum * f0 + add;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    fk[j] = __shfl_sync(0xffffffffu, f, min(k + j, 31));
-                    const float *d = base + (k0 + min(k + j, c - 1)) * stride + lane * V;
+                for (int i = 0; i < V; ++i) acc[i] *= f0;
+            }
 #pragma unroll
-                    for (int i = 0; i < V; i += V >= 2 ? 2 : 1) {
-                        if constexpr (V >= 2) {
-                            const float2 x2 = *reinterpret_cast<const float2 *>(d + i);
-                            v[j][i] = x2.x, v[j][i + 1] = x2.y;
-                        } else {
-                            v[j][i] = d[i];
-                        }
-                    }
+            for (int j = 0; j < U; ++j) {
+                f = __shfl_sync(0xffffffffu, w.x, (k + j) & 31);
+                if (k + j < c) {
+#pragma unroll
+                    for (int i = 0; i < V; ++i) acc[i] += v[j][i] * f;
                 }
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (k + j < c) {
-#pragma unroll
-                        for (int i = 0; i < V; ++i) acc[i] += v[j][i] * fk[j];
-                    }
             }
         }
-    };
-    if (s.member && tiles_c > 0) {
-        const int row = b * a.group + r, item = h * a.row_tiles + row / PA_ROWS;
-        const int u = item * tiles_c, c0 = sh.owner(u), c1 = sh.owner(u + tiles_c - 1);
-        join(a.part_c + ((long long)(item + c0) * PA_ROWS + row % PA_ROWS) * (DH + 2), (long long)PA_ROWS * (DH + 2),
-             c1 - c0 + 1);
-    }
-    if (tiles > 0) {
-        const int item = b * a.kv.n_kv + h;
-        const int u = common_total + a.kv.n_kv * t0 + h * tiles, c0 = sh.owner(u), c1 = sh.owner(u + tiles - 1);
-        join(a.part_o + ((long long)(item + c0) * a.group + r) * (DH + 2), (long long)a.group * (DH + 2), c1 - c0 + 1);
     }
     const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);  // (a NaN stays one)
     T *dst = static_cast<T *>(a.out) + (long long)b * a.ld_out + (long long)hq * DH + lane * V;
+    if constexpr (V == 1) {
+        dst[0] = (T)(acc[0] * inv);
+    } else {
 #pragma unroll
-    for (int i = 0; i < V; ++i) dst[i] = (T)(acc[i] * inv);
+        for (int i = 0; i < V; i += 2)
+            *reinterpret_cast<uint32_t *>(dst + i) = pack2<T>(acc[i] * inv, acc[i + 1] * inv);
+    }
     if (a.lse && lane == 0) a.lse[(long long)b * a.n_q + hq] = mx * 0.69314718055994530942f + logf(sum);
 }
 
@@ -686,15 +706,17 @@ int sm_count() {
 size_t al256(size_t n) { return (n + 255) & ~size_t(255); }
 
 struct WsLayout {
-    size_t plan, part_c, part_o, bytes;
+    size_t plan, ml, o, bytes;
+    int slots_c;
 };
 WsLayout ws_layout(const PagedView &kv, int group, int row_tiles, int grid) {
     WsLayout w;
-    const size_t row = (size_t)(kv.head_dim + 2) * sizeof(float);
+    w.slots_c = kv.n_kv * row_tiles + grid;
+    const size_t rows = (size_t)w.slots_c * PA_ROWS + ((size_t)kv.n_seqs * kv.n_kv + grid) * group;
     w.plan = 0;
-    w.part_c = al256((size_t)(kPlanWords + kv.n_seqs + 1) * sizeof(int));
-    w.part_o = w.part_c + al256(((size_t)kv.n_kv * row_tiles + grid) * PA_ROWS * row);
-    w.bytes = w.part_o + al256(((size_t)kv.n_seqs * kv.n_kv + grid) * group * row);
+    w.ml = al256((size_t)(kPlanWords + kv.n_seqs + 1) * sizeof(int));
+    w.o = w.ml + al256(rows * sizeof(float2));
+    w.bytes = w.o + rows * kv.head_dim * sizeof(float);
     return w;
 }
 
@@ -713,22 +735,10 @@ template <typename T, int DH>
 lf_status launch_attn(const AttnArgs &a, cudaStream_t st) {
     constexpr int smem = Smem<T, DH>::BYTES;
     if (!set_smem_once<paged_attn_kernel<T, DH>>(smem)) return LF_ERR_CUDA;
-    paged_attn_kernel<T, DH><<<a.grid, PA_THREADS, smem, st>>>(a);
-    if (cudaGetLastError() != cudaSuccess) return LF_ERR_CUDA;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(((long long)a.kv.n_seqs * a.n_q * 32 + PA_MERGE_THREADS - 1) / PA_MERGE_THREADS));
-    cfg.blockDim = dim3(PA_MERGE_THREADS);
-    cfg.stream = st;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, paged_attn_join<T, DH>, a) != cudaSuccess) {
-        (void)cudaGetLastError();
-        return LF_ERR_CUDA;
-    }
-    return LF_OK;
+    if (!launch_pdl(paged_attn_kernel<T, DH>, a.grid, PA_THREADS, smem, st, a)) return LF_ERR_CUDA;
+    const long long threads = (long long)a.kv.n_seqs * a.n_q * 32;
+    const unsigned blocks = (unsigned)((threads + PA_MERGE_THREADS - 1) / PA_MERGE_THREADS);
+    return launch_pdl(paged_attn_join<T, DH>, blocks, PA_MERGE_THREADS, 0, st, a) ? LF_OK : LF_ERR_CUDA;
 }
 
 template <typename T>
@@ -766,8 +776,9 @@ extern "C" lf_status lf_attn_paged_shared(const lf_paged_kv *kv, const void *q_d
         return LF_ERR_INVALID_ARG;
     a.group = n_q_heads / a.kv.n_kv;
     // tiles are counted in 32 bits
-    const long long per_head = (long long)(shared_len / lf::PA_KT + 1) * (((long long)kv->n_seqs * a.group) / lf::PA_ROWS + 1) +
-                               (long long)(max_len / lf::PA_KT + 2) * kv->n_seqs;
+    const int kt = lf::tile_keys(kv->head_dim);
+    const long long per_head = (long long)(shared_len / kt + 1) * (((long long)kv->n_seqs * a.group) / lf::PA_ROWS + 1) +
+                               (long long)(max_len / kt + 2) * kv->n_seqs;
     if (per_head * kv->n_kv_heads > INT_MAX) return LF_ERR_UNSUPPORTED;
     a.row_tiles = (a.kv.n_seqs * a.group + lf::PA_ROWS - 1) / lf::PA_ROWS;
     const int n_sm = lf::sm_count();
@@ -777,8 +788,9 @@ extern "C" lf_status lf_attn_paged_shared(const lf_paged_kv *kv, const void *q_d
     if (workspace_bytes < w.bytes) return LF_ERR_INVALID_ARG;
     uint8_t *ws = static_cast<uint8_t *>(workspace_device);
     a.plan = reinterpret_cast<int *>(ws + w.plan);
-    a.part_c = reinterpret_cast<float *>(ws + w.part_c);
-    a.part_o = reinterpret_cast<float *>(ws + w.part_o);
+    a.slots_c = w.slots_c;
+    a.part_ml = reinterpret_cast<float2 *>(ws + w.ml);
+    a.part_o = reinterpret_cast<float *>(ws + w.o);
     a.q = q_device;
     a.out = out_device;
     a.lse = lse_device;

@@ -507,6 +507,9 @@ __global__ void __launch_bounds__(NT) sample_filtered_kernel(const FilterArgs a)
     const int row = blockIdx.x / C, rank = blockIdx.x % C;
     const int i0 = rank * a.per, n = max(0, min(a.per, a.vocab - i0));
     Row<NT, C> R(S, z, n, rank);
+    for (int i = tid; i < 256; i += NT) S.pow2[i] = kPow2.v[i];
+    pdl_wait();
+    pdl_trigger();
 
     const float t = a.temperature ? a.temperature[row] : 1.f, top_p = a.top_p ? a.top_p[row] : 1.f;
     const float min_p = a.min_p ? a.min_p[row] : 0.f, u = a.u[row];
@@ -535,8 +538,6 @@ __global__ void __launch_bounds__(NT) sample_filtered_kernel(const FilterArgs a)
         S.cl = (float)(cd - (double)S.ch);
         if (min_p > 0.f) S.ln_min_p = (double)t * log((double)min_p);
     }
-    for (int i = tid; i < 256; i += NT) S.pow2[i] = kPow2.v[i];
-
     uint32_t kmax = own;
     nan = __syncthreads_or(nan);
     R.block_minmax(kmin, kmax);
@@ -650,22 +651,10 @@ constexpr int kWidePer = 26624;  // above it (one CTA per SM by its shared memor
 template <int NT, int C>
 lf_status launch_row(const FilterArgs &a, cudaStream_t st) {
     if (!set_smem_once<sample_filtered_kernel<NT, C>>(kMaxPer * (int)sizeof(float))) return LF_ERR_CUDA;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(a.rows * C));
-    cfg.blockDim = dim3(NT);
-    cfg.dynamicSmemBytes = (size_t)a.per * sizeof(float);
-    cfg.stream = st;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = (unsigned)C;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, sample_filtered_kernel<NT, C>, a) != cudaSuccess) {
-        (void)cudaGetLastError();
-        return LF_ERR_CUDA;
-    }
-    return LF_OK;
+    return launch_pdl_cluster(sample_filtered_kernel<NT, C>, C, dim3((unsigned)(a.rows * C)), NT,
+                              (size_t)a.per * sizeof(float), st, a)
+               ? LF_OK
+               : LF_ERR_CUDA;
 }
 
 template <int C>
