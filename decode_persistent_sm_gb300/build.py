@@ -25,7 +25,7 @@ BUILD_DEBUG = os.path.join(PKG, "_build_debug")
 LIB_DEBUG = os.path.join(PKG, "liblaneformer_debug.so")
 SOURCES = ["lf_plan.cpp", "lf_kernel.cu", "lf_runtime.cu", "lf_noalloc.cu", "lf_tc_gemm.cu", "lf_prefill.cu",
            "lf_pf_attn_tc.cu", "lf_sample.cu", "lf_gemv_tc.cu", "lf_batch.cu", "lf_stream.cu",
-           "lf_paged.cu", "lf_paged_attn.cu", "lf_sample_filtered.cu"]
+           "lf_paged.cu", "lf_paged_attn.cu", "lf_paged_attn_tc.cu", "lf_sample_filtered.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

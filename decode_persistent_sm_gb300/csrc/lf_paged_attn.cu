@@ -27,9 +27,11 @@
 // running maximum; warps that shared rows join in shared memory at the item's
 // end.  P is rounded to the cache's type for the second product (as the other
 // operand is); its sum is taken before the rounding.
+#include <algorithm>
 #include <climits>
+#include <type_traits>
 
-#include "lf_paged.h"
+#include "lf_paged_attn.h"
 #include "lf_ptx.cuh"
 
 namespace lf {
@@ -40,66 +42,7 @@ constexpr int PA_CTAS_PER_SM = 2;
 // keys per tile: 32 KB of K and V at head_dim 64 and 128 (a 16 KB tile's barriers and softmax statistics cost more than its copy)
 __host__ __device__ constexpr int tile_keys(int dim) { return dim == 128 ? 64 : 128; }
 constexpr int PA_MERGE_THREADS = 128;
-constexpr float kLog2e = 1.4426950408889634f;
-
-struct AttnArgs {
-    PagedView kv;
-    const void *q;
-    void *out;
-    float *lse;
-    long long ld_q, ld_out;
-    int n_q, group;  // query heads, query heads per KV head
-    const int32_t *lens;
-    int max_len, shared, window;
-    float scale_log2;  // scale * log2 e
-    int row_tiles;     // tiles of the common rows (n_seqs * group)
-    int grid;          // CTAs of the first kernel
-    // workspace
-    int *plan;         // kPlanWords, then the own tiles before each sequence [n_seqs + 1]
-    // partials, common items' slots first: slots_c = n_kv * row_tiles + grid of PA_ROWS rows, then n_seqs * n_kv + grid
-    // of `group` rows
-    int slots_c;
-    float *part_o;     // [row][head_dim], unnormalised
-    float2 *part_ml;   // [row] (max in the log2 domain, sum)
-    uint32_t *err;
-};
-
-constexpr int kPlanWords = 4;  // head of the plan: tiles per common item, all tiles, two unused
-
-// What one sequence sees.
-struct Span {
-    int lo, len;   // positions [lo, len)
-    bool member;   // shares the common range
-};
-__device__ __forceinline__ Span span_of(const AttnArgs &a, int b) {
-    Span s;
-    s.len = a.lens[b];
-    if (s.len < 0 || s.len > a.max_len) s.len = 0;
-    s.lo = a.window > 0 ? max(0, s.len - a.window) : 0;
-    s.member = s.len >= a.shared && s.lo < a.shared;
-    return s;
-}
-// Positions of the sequence outside the common range [clo, shared).
-__device__ __forceinline__ int own_count(const Span &s, int clo, int shared) {
-    return s.member ? (clo - s.lo) + (s.len - shared) : s.len - s.lo;
-}
-
-// The list's shares: the first total % ctas CTAs take one tile more.  No share
-// is empty (a list shorter than the grid goes to its first tiles' CTAs).
-struct Shares {
-    int q, r;
-    __device__ Shares(int total, int grid) {
-        const int ctas = min(total, grid);
-        q = ctas ? total / ctas : 0;
-        r = ctas ? total - q * ctas : 0;
-    }
-    __device__ int begin(int c) const { return c * q + min(c, r); }
-    __device__ int owner(int u) const {
-        const int head = r * (q + 1);
-        return u < head ? u / (q + 1) : r + (u - head) / q;
-    }
-};
-
+constexpr int kTcMinRows = 33, kTcMinKeys = 1024;
 template <typename T>
 __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1);
 template <>
@@ -113,25 +56,6 @@ __device__ __forceinline__ void mma<__nv_bfloat16>(float (&c)[4], const uint32_t
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-template <typename T>
-__device__ __forceinline__ uint32_t pack2(float lo, float hi);
-template <>
-__device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
-template <>
-__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
-
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 // 16 bytes global -> shared, or 16 zero bytes.
 __device__ __forceinline__ void cp16_or_zero(uint32_t dst, const void *src, bool valid) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
@@ -173,7 +97,7 @@ struct Smem {
 template <typename T, int DH>
 class Walker {
   public:
-    __device__ Walker(const AttnArgs &args, uint8_t *smem) : a(args) {
+    __device__ Walker(const AttnArgs &args, uint8_t *smem) : a(args), com(args, -1) {
         stage0 = smem;
         q0 = smem + L::STAGES * 2 * L::TILE;
         ml = reinterpret_cast<float2 *>(q0 + L::STAGES * L::Q);
@@ -188,22 +112,16 @@ class Walker {
     // table waits for a barrier; CTA 0 leaves it for the join.
     __device__ void plan() {
         const int n = a.kv.n_seqs;
-        int lo = -1;
-        bool bad = false;
-        for (int b = lane; b < n; b += 32) {
-            const int len = a.lens[b];
-            bad |= len < 0 || len > a.max_len;
-            const Span s = span_of(a, b);
-            if (s.member) lo = max(lo, s.lo);
-        }
-        if (bad && blockIdx.x == 0) atomicExch(a.err, 1u);
-        clo = __reduce_max_sync(0xffffffffu, lo);
-        tiles_c = clo < 0 ? 0 : (a.shared - clo + KT - 1) / KT;
-        if (clo < 0) clo = a.shared;
+        com = Common(a, __reduce_max_sync(0xffffffffu, latest_start(a, lane)));
+        tiles_c = (com.hi - com.lo + a.keys_c - 1) / a.keys_c;
         int at = 0;
         for (int b0 = 0; b0 < n; b0 += 32) {
             const int b = b0 + lane;
-            const int t = b < n ? (own_count(span_of(a, b), clo, a.shared) + KT - 1) / KT : 0;
+            int t = 0;
+            if (b < n) {
+                t = (own_count(span_of(a, b), com) + KT - 1) / KT;
+                if (blockIdx.x == 0 && (a.lens[b] < 0 || a.lens[b] > a.max_len)) atomicExch(a.err, 1u);
+            }
             int inc = t;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -217,11 +135,13 @@ class Walker {
             at += __shfl_sync(0xffffffffu, inc, 31);
         }
         if (tid == 0) cum[n] = at;
-        common_total = a.kv.n_kv * a.row_tiles * tiles_c;
+        const int all_c = a.kv.n_kv * a.row_tiles * tiles_c;
+        common_total = a.tc ? 0 : all_c;
         total = common_total + a.kv.n_kv * at;
         if (blockIdx.x == 0 && tid == 0) {
             a.plan[0] = tiles_c;
             a.plan[1] = total;
+            a.plan[2] = a.tc ? all_c : total;
             a.plan[kPlanWords + n] = at;
         }
         __syncthreads();
@@ -279,7 +199,8 @@ class Walker {
     float2 *ml;
     int *cum;
     int tid, warp, lane;
-    int clo, tiles_c;
+    Common com;
+    int tiles_c;
     int common_total, total;
     // the tile to be fetched next: element offsets of rows lane + 32 i (-1: no such key)
     long long row_off[KT / 32];
@@ -294,16 +215,16 @@ class Walker {
         p.gap_at = INT_MAX;
         p.gap = 0;
         if (p.common) {
-            p.first = clo;
-            p.keys = a.shared - clo;
+            p.first = com.lo;
+            p.keys = com.hi - com.lo;
             return;
         }
         const Span s = span_of(a, p.b);
         p.first = s.lo;
-        p.keys = own_count(s, clo, a.shared);
+        p.keys = own_count(s, com);
         if (s.member) {
-            p.gap_at = clo - s.lo;
-            p.gap = a.shared - clo;
+            p.gap_at = max(0, com.lo - s.lo);
+            p.gap = com.hi - max(com.lo, s.lo);
         }
     }
 
@@ -532,7 +453,7 @@ class Walker {
         constexpr int WK = 4 / WR;
         const int g = lane >> 2, t = lane & 3;
         const long long slot0 = p.common ? (long long)(p.item + blockIdx.x) * PA_ROWS
-                                         : (long long)a.slots_c * PA_ROWS + (long long)(p.item + blockIdx.x) * a.group;
+                                         : (long long)a.slots_c * a.rows_c + (long long)(p.item + blockIdx.x) * a.group;
         float *dst = a.part_o + slot0 * DH;
         float2 *dst_ml = a.part_ml + slot0;
 #pragma unroll
@@ -595,10 +516,15 @@ template <typename T, int DH>
 __global__ void __launch_bounds__(PA_THREADS, PA_CTAS_PER_SM) paged_attn_kernel(const AttnArgs a) {
     extern __shared__ __align__(128) uint8_t pa_smem[];
     Walker<T, DH> w(a, pa_smem);
-    pdl_wait();
+    // With the tensor-core kernel in front, which triggers this one after its own
+    // wait, all that is read here is already there and what is written is apart
+    // from that kernel's partials: this one runs beside it and waits at its end,
+    // so that the join behind it finds both done.
+    if (!a.tc) pdl_wait();
     pdl_trigger();
     w.plan();
     w.run();
+    if (a.tc) pdl_wait();
 }
 
 
@@ -614,24 +540,24 @@ __global__ void __launch_bounds__(PA_MERGE_THREADS) paged_attn_join(const AttnAr
     if (x >= a.kv.n_seqs * a.n_q) return;
     const int b = x / a.n_q, hq = x % a.n_q, h = hq / a.group, r = hq % a.group;
     const int tiles_c = a.plan[0], total = a.plan[1], t0 = a.plan[kPlanWords + b];
-    const int tiles = a.plan[kPlanWords + b + 1] - t0, common_total = a.kv.n_kv * a.row_tiles * tiles_c;
-    const Shares sh(total, a.grid);
+    const int tiles = a.plan[kPlanWords + b + 1] - t0, common_total = a.tc ? 0 : a.kv.n_kv * a.row_tiles * tiles_c;
+    const Shares sh(total, a.grid), sh_c(a.plan[2], a.grid_c);
     // partial k < n_c of the common item, then n_o of the own one: their rows in the workspace
     long long row_c = 0, row_o = 0;
     int n_c = 0, n_o = 0;
     if (span_of(a, b).member && tiles_c > 0) {
-        const int row = b * a.group + r, item = h * a.row_tiles + row / PA_ROWS, u = item * tiles_c;
-        const int c0 = sh.owner(u);
-        n_c = sh.owner(u + tiles_c - 1) - c0 + 1;
-        row_c = (long long)(item + c0) * PA_ROWS + row % PA_ROWS;
+        const int row = b * a.group + r, item = h * a.row_tiles + row / a.rows_c, u = item * tiles_c;
+        const int c0 = sh_c.owner(u);
+        n_c = sh_c.owner(u + tiles_c - 1) - c0 + 1;
+        row_c = (long long)(item + c0) * a.rows_c + row % a.rows_c;
     }
     if (tiles > 0) {
         const int u = common_total + a.kv.n_kv * t0 + h * tiles, c0 = sh.owner(u);
         n_o = sh.owner(u + tiles - 1) - c0 + 1;
-        row_o = (long long)a.slots_c * PA_ROWS + (long long)(b * a.kv.n_kv + h + c0) * a.group + r;
+        row_o = (long long)a.slots_c * a.rows_c + (long long)(b * a.kv.n_kv + h + c0) * a.group + r;
     }
     auto row_of = [&](int k) {
-        return k < n_c ? row_c + (long long)k * PA_ROWS : row_o + (long long)(k - n_c) * a.group;
+        return k < n_c ? row_c + (long long)k * a.rows_c : row_o + (long long)(k - n_c) * a.group;
     };
     float acc[V], mx = -INFINITY, sum = 0.f;
 #pragma unroll
@@ -705,19 +631,45 @@ int sm_count() {
 
 size_t al256(size_t n) { return (n + 255) & ~size_t(255); }
 
+// How the common rows are cut: 64 rows a pass on warp-level MMAs, or 256 on the
+// tensor cores of lf_paged_attn_tc.cu.
+void common_shape(AttnArgs &a, bool tc, int n_sm) {
+    const long long rows = (long long)a.kv.n_seqs * a.group;
+    a.tc = tc;
+    a.rows_c = tc ? kTcRows : PA_ROWS;
+    a.keys_c = tc ? kTcKeys : tile_keys(a.kv.head_dim);
+    a.row_tiles = (int)((rows + a.rows_c - 1) / a.rows_c);
+    a.grid = n_sm * PA_CTAS_PER_SM;
+    a.grid_c = tc ? n_sm : a.grid;
+    a.page_align = tc ? 1 << a.kv.ps_log2 : 1;
+    a.slots_c = a.kv.n_kv * a.row_tiles + a.grid_c;
+}
+
 struct WsLayout {
     size_t plan, ml, o, bytes;
-    int slots_c;
 };
-WsLayout ws_layout(const PagedView &kv, int group, int row_tiles, int grid) {
+WsLayout ws_layout(const AttnArgs &a) {
     WsLayout w;
-    w.slots_c = kv.n_kv * row_tiles + grid;
-    const size_t rows = (size_t)w.slots_c * PA_ROWS + ((size_t)kv.n_seqs * kv.n_kv + grid) * group;
+    const size_t rows = (size_t)a.slots_c * a.rows_c + ((size_t)a.kv.n_seqs * a.kv.n_kv + a.grid) * a.group;
     w.plan = 0;
-    w.ml = al256((size_t)(kPlanWords + kv.n_seqs + 1) * sizeof(int));
+    w.ml = al256((size_t)(kPlanWords + a.kv.n_seqs + 1) * sizeof(int));
     w.o = w.ml + al256(rows * sizeof(float2));
-    w.bytes = w.o + rows * kv.head_dim * sizeof(float);
+    w.bytes = w.o + rows * a.kv.head_dim * sizeof(float);
     return w;
+}
+
+// The tensor-core kernel takes head_dim 64 and 128 and pages of at least 8
+// positions (a TMA box).
+bool tc_possible(const PagedView &v) { return v.head_dim >= 64 && v.ps_log2 >= 3; }
+
+size_t ws_bytes(AttnArgs a, int n_sm) {
+    common_shape(a, false, n_sm);
+    size_t n = ws_layout(a).bytes;
+    if (tc_possible(a.kv)) {
+        common_shape(a, true, n_sm);
+        n = std::max(n, ws_layout(a).bytes);
+    }
+    return n;
 }
 
 lf_status check_shape(const lf_paged_kv *kv, int n_q_heads, PagedView *v) {
@@ -735,6 +687,12 @@ template <typename T, int DH>
 lf_status launch_attn(const AttnArgs &a, cudaStream_t st) {
     constexpr int smem = Smem<T, DH>::BYTES;
     if (!set_smem_once<paged_attn_kernel<T, DH>>(smem)) return LF_ERR_CUDA;
+    if constexpr (DH >= 64) {
+        if (a.tc) {
+            const lf_status ts = paged_attn_tc(a, std::is_same<T, __half>::value ? LF_F16 : LF_BF16, st);
+            if (ts != LF_OK) return ts;
+        }
+    }
     if (!launch_pdl(paged_attn_kernel<T, DH>, a.grid, PA_THREADS, smem, st, a)) return LF_ERR_CUDA;
     const long long threads = (long long)a.kv.n_seqs * a.n_q * 32;
     const unsigned blocks = (unsigned)((threads + PA_MERGE_THREADS - 1) / PA_MERGE_THREADS);
@@ -752,11 +710,11 @@ lf_status launch_attn_dim(const AttnArgs &a, cudaStream_t st) {
 }  // namespace lf
 
 extern "C" size_t lf_attn_paged_shared_workspace(const lf_paged_kv *kv, int n_q_heads) {
-    lf::PagedView v;
-    if (lf::check_shape(kv, n_q_heads, &v) != LF_OK) return 0;
-    const int group = n_q_heads / v.n_kv, tiles = (v.n_seqs * group + lf::PA_ROWS - 1) / lf::PA_ROWS;
+    lf::AttnArgs a = {};
+    if (lf::check_shape(kv, n_q_heads, &a.kv) != LF_OK) return 0;
+    a.group = n_q_heads / a.kv.n_kv;
     const int n_sm = lf::sm_count();
-    return n_sm ? lf::ws_layout(v, group, tiles, n_sm * lf::PA_CTAS_PER_SM).bytes : 0;
+    return n_sm ? lf::ws_bytes(a, n_sm) : 0;
 }
 
 extern "C" lf_status lf_attn_paged_shared(const lf_paged_kv *kv, const void *q_device, int64_t ld_q, void *out_device,
@@ -780,15 +738,14 @@ extern "C" lf_status lf_attn_paged_shared(const lf_paged_kv *kv, const void *q_d
     const long long per_head = (long long)(shared_len / kt + 1) * (((long long)kv->n_seqs * a.group) / lf::PA_ROWS + 1) +
                                (long long)(max_len / kt + 2) * kv->n_seqs;
     if (per_head * kv->n_kv_heads > INT_MAX) return LF_ERR_UNSUPPORTED;
-    a.row_tiles = (a.kv.n_seqs * a.group + lf::PA_ROWS - 1) / lf::PA_ROWS;
     const int n_sm = lf::sm_count();
     if (!n_sm) return LF_ERR_CUDA;
-    a.grid = n_sm * lf::PA_CTAS_PER_SM;
-    const lf::WsLayout w = lf::ws_layout(a.kv, a.group, a.row_tiles, a.grid);
-    if (workspace_bytes < w.bytes) return LF_ERR_INVALID_ARG;
+    if (workspace_bytes < lf::ws_bytes(a, n_sm)) return LF_ERR_INVALID_ARG;
+    const bool tc = lf::tc_possible(a.kv) && (long long)a.kv.n_seqs * a.group >= lf::kTcMinRows && shared_len >= lf::kTcMinKeys;
+    lf::common_shape(a, tc, n_sm);
+    const lf::WsLayout w = lf::ws_layout(a);
     uint8_t *ws = static_cast<uint8_t *>(workspace_device);
     a.plan = reinterpret_cast<int *>(ws + w.plan);
-    a.slots_c = w.slots_c;
     a.part_ml = reinterpret_cast<float2 *>(ws + w.ml);
     a.part_o = reinterpret_cast<float *>(ws + w.o);
     a.q = q_device;

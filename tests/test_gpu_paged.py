@@ -238,6 +238,49 @@ CASES = [
     (lens_of(33, [1000, 1, 2000]), 33, 8, 8, 64, 1024, "f16", 0),
 ]
 
+# batches with many rows over a long common range (the tensor-core kernel): rows of one KV head 33, 64, 128, 129, 256,
+# 257, 640; pages smaller than, equal to and larger than a tile; the common range cut inside pages at both ends
+MANY = [
+    (lens_of(1024, [1 + i for i in range(11)]), 1024, 3, 1, 128, 16, "f16", 0),
+    (lens_of(1500, [5 * i + 1 for i in range(32)]), 1500, 4, 2, 64, 8, "bf16", 0),
+    (lens_of(2049, [1] * 64), 2049, 4, 2, 128, 64, "bf16", 0),
+    (lens_of(1031, [3] * 43), 1031, 6, 2, 128, 32, "f16", 0),
+    (lens_of(1300, [70] * 64), 1300, 8, 2, 64, 128, "f16", 0),
+    (lens_of(1200, [2] * 257), 1200, 2, 2, 128, 16, "bf16", 0),
+    (lens_of(3000, [1 + i % 7 for i in range(80)]), 3000, 16, 2, 64, 512, "bf16", 0),
+    (lens_of(2500, [1 + 3 * i for i in range(50)]), 2500, 5, 5, 128, 1024, "f16", 0),
+    (lens_of(2600, [1 + 11 * i for i in range(40)]), 2600, 4, 2, 128, 16, "f16", 1024),   # windows from inside the prefix
+    (lens_of(1100, [1 + 40 * i for i in range(40)]), 1100, 4, 2, 64, 32, "bf16", 900),    # some start behind it
+    ([0, 500, 1090, 7] + lens_of(1100, [9] * 40), 1100, 2, 2, 128, 16, "bf16", 0),        # some end inside it, one is empty
+    (lens_of(1100, [1 + 400 * i for i in range(34)]), 1100, 1, 1, 64, 64, "f16", 1101),   # one key in common, no whole page
+]
+
+
+@pytest.mark.parametrize("case", range(len(MANY)))
+def test_attention_of_many_rows(case):
+    lens, shared, nq, nkv, dim, page, dtype, window = MANY[case]
+    c = Case(lens, shared, nq, nkv, dim, page, dtype, window, seed=100 + case)
+    c.check(*c.run())
+
+
+def test_attention_of_many_rows_strided_flagged_and_replayed():
+    import torch
+    c = Case(lens_of(1400, [1 + i for i in range(40)]), 1400, 4, 2, 64, 16, "bf16", stride_extra=24)
+    ws, out = c.workspace(), torch.full((40, 4 * 64 + 40), 9.0, dtype=torch.bfloat16, device="cuda")
+    c.run(ws=ws)
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        _, lse = c.run(out=out, ld=4 * 64 + 40, ws=ws, stream=torch.cuda.current_stream().cuda_stream)
+    for _ in range(3):
+        gr.replay()
+    torch.cuda.synchronize()
+    assert (out[:, 4 * 64:] == 9.0).all()
+    c.check(out, lse)
+    c.tb[0, 3] = c.k.shape[0]  # a page of the common range that does not exist
+    c.run(ws=ws)
+    torch.cuda.synchronize()
+    assert c.err.item() == 1
+
 
 @pytest.mark.parametrize("case", range(len(CASES)))
 def test_attention(case):
