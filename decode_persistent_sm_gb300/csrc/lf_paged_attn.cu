@@ -42,7 +42,6 @@ constexpr int PA_CTAS_PER_SM = 2;
 // keys per tile: 32 KB of K and V at head_dim 64 and 128 (a 16 KB tile's barriers and softmax statistics cost more than its copy)
 __host__ __device__ constexpr int tile_keys(int dim) { return dim == 128 ? 64 : 128; }
 constexpr int PA_MERGE_THREADS = 128;
-constexpr int kTcMinRows = 33, kTcMinKeys = 1024;
 template <typename T>
 __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1);
 template <>
@@ -661,6 +660,23 @@ WsLayout ws_layout(const AttnArgs &a) {
 // The tensor-core kernel takes head_dim 64 and 128 and pages of at least 8
 // positions (a TMA box).
 bool tc_possible(const PagedView &v) { return v.head_dim >= 64 && v.ps_log2 >= 3; }
+// It costs one more launch, which leaves the other kernel about 4 us later, and
+// its 128-row tiles idle where there are few rows; it gains as the common
+// products grow.  Both measured (us, warp-level MMAs | tensor cores), 64 own
+// positions at most, by rows of a KV head x common positions:
+//   head_dim 128, 8 KV heads:   64 x 4096 20.9 | 22.9   64 x 16384 36.2 | 30.7
+//                              128 x 4096 25.3 | 28.1  128 x 16384 47.7 | 39.5
+//   head_dim 128, 16 KV heads: 128 x 2048 28.5 | 29.4  128 x 4096  36.9 | 34.6
+//                               32 x 16384 39.8 | 39.5 256 x 16384 132 | 69
+//   head_dim 64, 16 KV heads:   64 x 16384 34.8 | 37.9 128 x 16384 57.1 | 43.3
+// so: by the size of the common products, and not where half of a row tile (a
+// quarter at head_dim 128) would be empty.  With a window at most that many
+// positions are common.
+bool tc_pays(const AttnArgs &a) {
+    const long long rows = (long long)a.kv.n_seqs * a.group, keys = a.window > 0 ? std::min(a.window, a.shared) : a.shared;
+    return rows > (a.kv.head_dim == 128 ? 32 : 64) &&
+           (double)rows * (double)keys * a.kv.n_kv * a.kv.head_dim >= 7.5e8;
+}
 
 size_t ws_bytes(AttnArgs a, int n_sm) {
     common_shape(a, false, n_sm);
@@ -741,8 +757,9 @@ extern "C" lf_status lf_attn_paged_shared(const lf_paged_kv *kv, const void *q_d
     const int n_sm = lf::sm_count();
     if (!n_sm) return LF_ERR_CUDA;
     if (workspace_bytes < lf::ws_bytes(a, n_sm)) return LF_ERR_INVALID_ARG;
-    const bool tc = lf::tc_possible(a.kv) && (long long)a.kv.n_seqs * a.group >= lf::kTcMinRows && shared_len >= lf::kTcMinKeys;
-    lf::common_shape(a, tc, n_sm);
+    a.shared = shared_len;
+    a.window = window;
+    lf::common_shape(a, lf::tc_possible(a.kv) && lf::tc_pays(a), n_sm);
     const lf::WsLayout w = lf::ws_layout(a);
     uint8_t *ws = static_cast<uint8_t *>(workspace_device);
     a.plan = reinterpret_cast<int *>(ws + w.plan);
@@ -756,8 +773,6 @@ extern "C" lf_status lf_attn_paged_shared(const lf_paged_kv *kv, const void *q_d
     a.n_q = n_q_heads;
     a.lens = lens_device;
     a.max_len = max_len;
-    a.shared = shared_len;
-    a.window = window;
     a.scale_log2 = scale * lf::kLog2e;
     a.err = err_device;
     cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);

@@ -31,32 +31,35 @@ def visible(length, window):
 
 
 def attention(q, k, v, table, page, lens, shared, window, scale):
-    """q [seqs][heads][dim], k and v [pages][kv heads][page][dim], all float64.
-    Returns out, lse and the per-value magnitude sum_j p_j |v_j|, the largest
-    sum of |q k| and the largest |v| per row (for error bounds)."""
+    """q [seqs][heads][dim], k and v [pages][kv heads][page][dim], torch tensors,
+    computed in float64 where they are; table and lens: numpy, list.  Returns out,
+    lse and, for error bounds, the per-value magnitude sum_j p_j |v_j| and per
+    row the largest sum of |q k|, the largest |v| and keys / sum of exp."""
+    import torch
     n, nq, d = q.shape
     nkv = k.shape[1]
     g = nq // nkv
-    out, mag = np.zeros_like(q), np.zeros_like(q)
-    lse = np.full((n, nq), -np.inf)
-    qk, vmax, cond = np.zeros((n, nq, 1)), np.zeros((n, nq, 1)), np.ones((n, nq, 1))
+    new = lambda *sh: torch.zeros(*sh, dtype=torch.float64, device=q.device)  # noqa: E731
+    out, mag, lse = new(n, nq, d), new(n, nq, d), new(n, nq) - np.inf
+    qk, vmax, cond = new(n, nq, 1), new(n, nq, 1), new(n, nq, 1) + 1
     for b in range(n):
         j = visible(int(lens[b]), window)
         if not len(j):
             continue
-        pages = np.where(j < shared, table[0][j // page], table[b][j // page])
-        kb, vb = k[pages, :, j % page], v[pages, :, j % page]
-        for h in range(nq):
-            kk, vv = kb[:, h // g], vb[:, h // g]
-            s = scale * (kk @ q[b, h])
-            m = s.max()
-            e = np.exp(s - m)
-            out[b, h] = (e @ vv) / e.sum()
-            mag[b, h] = (e @ np.abs(vv)) / e.sum()
-            lse[b, h] = m + np.log(e.sum())
-            qk[b, h] = scale * (np.abs(kk) @ np.abs(q[b, h])).max()
-            vmax[b, h] = np.abs(vv).max()
-            cond[b, h] = len(j) / e.sum()
+        pages = torch.from_numpy(np.where(j < shared, table[0][j // page], table[b][j // page])).to(q.device).long()
+        row = torch.from_numpy(j % page).to(q.device)
+        kb, vb = k[pages, :, row].double().transpose(0, 1), v[pages, :, row].double().transpose(0, 1)  # [kv heads][keys][dim]
+        qb = q[b].double().view(nkv, g, d)
+        sc = scale * (qb @ kb.transpose(1, 2))
+        m = sc.amax(-1, keepdim=True)
+        e = (sc - m).exp()
+        total = e.sum(-1, keepdim=True)
+        out[b] = ((e @ vb) / total).view(nq, d)
+        mag[b] = ((e @ vb.abs()) / total).view(nq, d)
+        lse[b] = (m + total.log()).view(nq)
+        qk[b, :, 0] = scale * (qb.abs() @ kb.abs().transpose(1, 2)).amax(-1).view(nq)
+        vmax[b, :, 0] = vb.abs().amax((1, 2)).repeat_interleave(g)
+        cond[b, :, 0] = (len(j) / total).view(nq)
     return out, lse, mag, qk, vmax, cond
 
 

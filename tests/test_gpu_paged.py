@@ -139,6 +139,7 @@ class Case:
     def __init__(self, lens, shared, nq, nkv, dim, page, dtype, window=0, seed=0, stride_extra=0, spare=2):
         import torch
         g = np.random.default_rng(seed + dim + page + shared)
+        gen = torch.Generator(device="cuda").manual_seed(seed + dim + page + shared)
         n = len(lens)
         self.lens, self.shared, self.window, self.page, self.dtype, self.nq = lens, shared, window, page, dtype, nq
         max_pages = max(1, -(-(max(max(lens), shared)) // page)) + spare
@@ -155,8 +156,8 @@ class Case:
             j = ref.visible(lens[b], window)
             pg = np.where(j < shared, self.table[0][j // page], self.table[b][j // page])
             for c in (self.k, self.v):
-                c[torch.from_numpy(pg).cuda().long(), :, torch.from_numpy(j % page).cuda()] = torch.from_numpy(
-                    g.standard_normal((len(j), nkv, dim))).cuda().to(dt)
+                c[torch.from_numpy(pg).cuda().long(), :, torch.from_numpy(j % page).cuda()] = torch.randn(
+                    len(j), nkv, dim, device="cuda", generator=gen).to(dt)
         self.q = torch.from_numpy(1.5 * g.standard_normal((n, nq, dim))).cuda().to(dt)
         self.scale = dim ** -0.5
         self.tb = torch.from_numpy(self.table).cuda()
@@ -190,8 +191,8 @@ class Case:
         torch.cuda.synchronize()
         assert self.err.item() == 0
         n, nq, d = self.q.shape
-        want, wl, mag, qk, vmax, cond = ref.attention(f64(self.q), np.nan_to_num(f64(self.k)), np.nan_to_num(f64(self.v)),
-                                                      self.table, self.page, self.lens, self.shared, self.window, self.scale)
+        want, wl, mag, qk, vmax, cond = (x.cpu().numpy() for x in ref.attention(
+            self.q, self.k, self.v, self.table, self.page, self.lens, self.shared, self.window, self.scale))
         eps = ref.EPS[self.dtype]
         keys = np.array([len(ref.visible(x, self.window)) for x in self.lens])[:, None, None]
         ds = 2.0 ** -23 * (d / 16 + 4) * qk
@@ -241,18 +242,19 @@ CASES = [
 # batches with many rows over a long common range (the tensor-core kernel): rows of one KV head 33, 64, 128, 129, 256,
 # 257, 640; pages smaller than, equal to and larger than a tile; the common range cut inside pages at both ends
 MANY = [
-    (lens_of(1024, [1 + i for i in range(11)]), 1024, 3, 1, 128, 16, "f16", 0),
-    (lens_of(1500, [5 * i + 1 for i in range(32)]), 1500, 4, 2, 64, 8, "bf16", 0),
-    (lens_of(2049, [1] * 64), 2049, 4, 2, 128, 64, "bf16", 0),
-    (lens_of(1031, [3] * 43), 1031, 6, 2, 128, 32, "f16", 0),
-    (lens_of(1300, [70] * 64), 1300, 8, 2, 64, 128, "f16", 0),
-    (lens_of(1200, [2] * 257), 1200, 2, 2, 128, 16, "bf16", 0),
-    (lens_of(3000, [1 + i % 7 for i in range(80)]), 3000, 16, 2, 64, 512, "bf16", 0),
-    (lens_of(2500, [1 + 3 * i for i in range(50)]), 2500, 5, 5, 128, 1024, "f16", 0),
-    (lens_of(2600, [1 + 11 * i for i in range(40)]), 2600, 4, 2, 128, 16, "f16", 1024),   # windows from inside the prefix
-    (lens_of(1100, [1 + 40 * i for i in range(40)]), 1100, 4, 2, 64, 32, "bf16", 900),    # some start behind it
-    ([0, 500, 1090, 7] + lens_of(1100, [9] * 40), 1100, 2, 2, 128, 16, "bf16", 0),        # some end inside it, one is empty
-    (lens_of(1100, [1 + 400 * i for i in range(34)]), 1100, 1, 1, 64, 64, "f16", 1101),   # one key in common, no whole page
+    # lens, shared, nq, nkv, dim, page, dtype, window
+    (lens_of(23040, [1 + i for i in range(11)]), 23040, 24, 8, 128, 16, "f16", 0),
+    (lens_of(11500, [5 * i + 1 for i in range(64)]), 11500, 16, 8, 64, 8, "bf16", 0),
+    (lens_of(7001, [1] * 64), 7001, 32, 16, 128, 64, "bf16", 0),
+    (lens_of(5801, [3] * 43), 5801, 24, 8, 128, 32, "f16", 0),
+    (lens_of(6000, [70] * 64), 6000, 32, 8, 64, 128, "f16", 0),
+    (lens_of(2901, [2] * 257), 2901, 8, 8, 128, 16, "bf16", 0),
+    (lens_of(4700, [1 + i % 7 for i in range(80)]), 4700, 64, 8, 64, 512, "bf16", 0),
+    (lens_of(9000, [1 + 3 * i for i in range(50)]), 9000, 48, 16, 128, 1024, "f16", 0),
+    (lens_of(6000, [1 + 11 * i for i in range(64)]), 6000, 16, 8, 128, 16, "f16", 6200),    # windows from inside the prefix
+    (lens_of(6100, [6200 if i % 16 == 5 else i for i in range(64)]), 6100, 32, 8, 64, 32, "bf16", 6000),   # some start behind it
+    ([0, 500, 5990, 7] + lens_of(6000, [9] * 124), 6000, 8, 8, 128, 16, "bf16", 0),  # some end inside it, one is empty
+    (lens_of(5700, [5610, 5000] + [1] * 63), 5700, 16, 16, 128, 64, "f16", 5640),  # 30 positions in common: no page
 ]
 
 
@@ -265,16 +267,16 @@ def test_attention_of_many_rows(case):
 
 def test_attention_of_many_rows_strided_flagged_and_replayed():
     import torch
-    c = Case(lens_of(1400, [1 + i for i in range(40)]), 1400, 4, 2, 64, 16, "bf16", stride_extra=24)
-    ws, out = c.workspace(), torch.full((40, 4 * 64 + 40), 9.0, dtype=torch.bfloat16, device="cuda")
+    c = Case(lens_of(9400, [1 + i for i in range(40)]), 9400, 64, 16, 64, 16, "bf16", stride_extra=24)
+    ws, out = c.workspace(), torch.full((40, 64 * 64 + 40), 9.0, dtype=torch.bfloat16, device="cuda")
     c.run(ws=ws)
     gr = torch.cuda.CUDAGraph()
     with torch.cuda.graph(gr):
-        _, lse = c.run(out=out, ld=4 * 64 + 40, ws=ws, stream=torch.cuda.current_stream().cuda_stream)
+        _, lse = c.run(out=out, ld=64 * 64 + 40, ws=ws, stream=torch.cuda.current_stream().cuda_stream)
     for _ in range(3):
         gr.replay()
     torch.cuda.synchronize()
-    assert (out[:, 4 * 64:] == 9.0).all()
+    assert (out[:, 64 * 64:] == 9.0).all()
     c.check(out, lse)
     c.tb[0, 3] = c.k.shape[0]  # a page of the common range that does not exist
     c.run(ws=ws)
