@@ -18,7 +18,7 @@
 //
 // A row belongs to a cluster of 1, 2, 4 or 8 CTAs, each with a contiguous
 // range of the vocabulary in shared memory as fp32: the logits are read from
-// HBM once.  A bound is found in two stages.  First a histogram over 1024
+// HBM once.  A bound is found in two stages.  First a histogram over 2048
 // equal steps of the logit below the maximum, summed over the cluster through
 // distributed shared memory, leaves few candidates:
 //   top-k: the threads' own maxima are counted; k of them at or above a step
@@ -26,10 +26,14 @@
 //          drops out (for k above half the threads: every logit is counted);
 //   top-p: the masses of all logits (64 bits as two 32-bit shared atomics, the
 //          second only on a carry) name the step that holds the border.
-// The candidates' values are then gathered in every CTA and ranked against
-// each other; a top-k set that was gathered serves top-p as well.  More
-// candidates than the list holds (equal or close logits) are told apart on
-// their float's bits, 10 a level.
+// The candidates' values (up to 1024) are then gathered in every CTA and told
+// apart there, up to 256 by ranking them pairwise, more by their float's bits,
+// 11 a level; a top-k set that was gathered serves top-p as well.  More
+// candidates than the list holds (many equal logits) are told apart on their
+// bits over all logits.
+// No double precision on the way but for one sum per row (its rate here is 1/64
+// of fp32's: a logarithm and a division cost 2 us): targets are exact integer
+// products, log2(e) / T and ln(min_p) come as pairs of floats.
 
 #include <cooperative_groups.h>
 
@@ -44,8 +48,9 @@ namespace cg = cooperative_groups;
 namespace lf {
 namespace {
 
-constexpr int F_BINS = 1024;
-constexpr int F_LIST = 320;  // candidates that are ranked pairwise: 320^2 comparisons take about 1 us of one SM
+constexpr int F_BINS = 2048;
+constexpr int F_LIST = 1024;  // candidates that every CTA of the row gathers
+constexpr int F_RANK = 256;   // candidates that are ranked pairwise
 constexpr int F_MAX_CLUSTER = 8;
 constexpr int F_MAX_VOCAB = 262144;
 constexpr int F_FRAC = 44;          // weights are integers in units of 2^-44
@@ -53,7 +58,7 @@ constexpr float F_MAX_Y = 45.f;     // below 2^-45 a weight rounds to nothing
 
 using u64 = unsigned long long;
 
-// 2^62 * 2^(-f / 256), f = 0 .. 255 (Taylor series of the exponential).
+// 2^61 * 2^(-f / 256), f = 0 .. 255 (Taylor series of the exponential).
 struct Pow2Table {
     u64 v[256];
     constexpr Pow2Table() : v() {
@@ -64,7 +69,7 @@ struct Pow2Table {
                 term *= x / i;
                 sum += term;
             }
-            v[f] = (u64)(sum * 4611686018427387904.0 + 0.5);
+            v[f] = (u64)(sum * 2305843009213693952.0 + 0.5);
         }
     }
 };
@@ -95,13 +100,12 @@ struct FilterShared {
     uint32_t lo[F_BINS], hi[F_BINS];
     float cand[F_LIST];      // this CTA's candidates
     float all[F_LIST];       // the cluster's
-    u64 mass[F_LIST];        // their weights
+    u64 mass[F_RANK];        // weights of those ranked pairwise
     Gather slot[2][F_MAX_CLUSTER];
     u64 wsum[32];
     uint32_t wmin[32], wmax[32];
-    u64 found_before, target;
-    double ln_min_p;         // T ln(min_p)
-    float ch, cl, floor;
+    u64 found_before;
+    float floor;
     uint32_t found_bin, key;
     int found, n_cand;
 };
@@ -117,30 +121,53 @@ __device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
 
 // round(2^44 exp((z - max) / T)), (ch, cl) = log2(e) / T as a pair of floats.
-// y = (max - z) log2(e) / T as a pair (error 2^-46 of it); y = j / 256 + r;
-// 2^-y = 2^(-j / 256) (1 - q), q = 1 - e^(-r ln 2) with r ln 2 = th + tl < 0.0028:
-// q = th + (tl - th^2 (1/2 - th / 6 + th^2 / 24)), its tail below 2^-42.
+// y = (max - z) log2(e) / T as a pair (error 2^-46 of it); y = j / 256 + r, |r| <= 1 / 512;
+// 2^-y = 2^(-j / 256) (1 - q), q = 1 - e^(-t), t = r ln 2 = th + tl, |t| < 0.0014:
+// q = th + (tl - th^2 (1/2 - th / 6)), the rest below 2^-42.  Sums of a large and a
+// small integer are taken after their conversions (the small one by adding 1.5 * 2^23).
 __device__ __forceinline__ u64 weight(float z, float mx, float ch, float cl, const u64 *pow2) {
-    if (z == mx) return 1ull << F_FRAC;
+    if (z == mx) return 1ull << F_FRAC;  // (also +inf)
     const float s = mx - z;
     const float yh = __fmul_rn(s, ch);
     if (!(yh < F_MAX_Y)) return 0;
+    constexpr float kRound = 12582912.f;  // 1.5 * 2^23: adding it leaves the integer part in the low mantissa bits
+    constexpr int kRoundBits = 0x4B400000;
     const float bb = __fsub_rn(s, mx);  // mx - z = s + e exactly
     const float e = __fsub_rn(__fsub_rn(mx, __fsub_rn(s, bb)), __fadd_rn(z, bb));
     const float yl = __fmaf_rn(s, ch, -yh) + __fmaf_rn(s, cl, e * ch);
-    const int j = __float2int_rd(yh * 256.f);
-    const float r = __fmaf_rn((float)j, -1.f / 256.f, yh);
+    const float tj = __fmaf_rn(yh, 256.f, kRound);
+    const int j = __float_as_int(tj) - kRoundBits;
+    const float r = __fmaf_rn(__fsub_rn(tj, kRound), -1.f / 256.f, yh);
     constexpr float kLn2 = 0.693147182464599609375f, kLn2Lo = -1.904654299957767878541e-9f;
     const float th = __fmul_rn(r, kLn2);
     const float tl = __fmaf_rn(r, kLn2, -th) + __fmaf_rn(r, kLn2Lo, yl * kLn2);
-    const float poly = __fmaf_rn(th, __fmaf_rn(th, 1.f / 24.f, -1.f / 6.f), 0.5f);
-    const float c = __fmaf_rn(-th * th, poly, tl);
+    const float c = __fmaf_rn(-th * th, __fmaf_rn(th, -1.f / 6.f, 0.5f), tl);
     constexpr float kScale = 549755813888.f;  // 2^39
-    const int q = __float2int_rn(th * kScale) + __float2int_rn(c * kScale);
+    const int q = __float2int_rn(th * kScale) + (__float_as_int(__fmaf_rn(c, kScale, kRound)) - kRoundBits);
     const u64 t = pow2[j & 255];
-    const u64 w62 = t - (u64)(((long long)(t >> 31) * q) >> 8);
-    const int sh = 62 - F_FRAC + (j >> 8);
-    return (w62 + (1ull << (sh - 1))) >> sh;
+    const u64 w61 = t - (u64)(((long long)(int)(t >> 31) * q) >> 8);
+    const int sh = 61 - F_FRAC + (j >> 8);
+    return ((w61 >> (sh - 1)) + 1) >> 1;
+}
+
+// floor(f * s), or (up) its ceiling, exactly, for 0 <= f < 1.
+__device__ __forceinline__ u64 scaled(float f, u64 s, bool up) {
+    const uint32_t bits = __float_as_uint(f);
+    const int e = (int)(bits >> 23);
+    const u64 m = e ? (bits & 0x7fffffu) | 0x800000u : bits;  // f = m 2^-k
+    const int k = 150 - (e ? e : 1);                          // 24 ..
+    const u64 lo = m * s, hi = __umul64hi(m, s);
+    u64 v = 0;
+    bool rest;
+    if (k < 64) {
+        v = (hi << (64 - k)) | (lo >> k);
+        rest = (lo & ((1ull << k) - 1)) != 0;
+    } else {
+        const int d = k - 64;
+        v = d < 64 ? hi >> d : 0;
+        rest = lo != 0 || (d < 64 ? (hi & ((1ull << d) - 1)) != 0 : hi != 0);
+    }
+    return v + (up && rest ? 1 : 0);
 }
 
 // The step of a logit below the maximum, monotone in it.
@@ -235,14 +262,20 @@ struct Row {
         __syncthreads();
     }
 
-    // Finds, in the cluster's summed histogram (bins in falling order of the
-    // logit), the bin where `above` + the running sum reaches the target, and
-    // `before`, above + the sum of the bins before it.  With frac >= 0 the
-    // target is first set to ceil(frac * total).
+    // Finds, in the summed histogram (bins in falling order of the logit), the
+    // bin where `above` + the running sum reaches the target, and `before`,
+    // above + the sum of the bins before it.  With frac >= 0 the target is first
+    // set to frac of the total, rounded up.  G = C: the sum of the cluster's
+    // histograms; G = 1: this CTA's alone.
+    template <int G>
     __device__ int find_bin(u64 above, u64 &target, float frac, u64 &before) {
-        constexpr int SL = F_BINS / C;            // bins of this CTA's slice
-        constexpr int PT = (SL + NT - 1) / NT;    // bins per thread (1 or 2)
-        sync();  // every CTA's histogram is complete
+        constexpr int SL = F_BINS / G;            // bins of this CTA's slice
+        constexpr int PT = (SL + NT - 1) / NT;    // bins per thread
+        const int part = G == 1 ? 0 : rank;
+        if constexpr (G > 1)
+            sync();  // every CTA's histogram is complete
+        else
+            __syncthreads();
         u64 v[PT], sum = 0;
         const int b0 = tid * PT;
 #pragma unroll
@@ -250,13 +283,13 @@ struct Row {
             v[i] = 0;
             if (b0 + i < SL) {
 #pragma unroll
-                for (int r = 0; r < C; ++r) {
+                for (int r = 0; r < G; ++r) {
                     const uint32_t *lo = S.lo, *hi = S.hi;
-                    if constexpr (C > 1) {
+                    if constexpr (G > 1) {
                         lo = cg::this_cluster().map_shared_rank(S.lo, r);
                         hi = cg::this_cluster().map_shared_rank(S.hi, r);
                     }
-                    v[i] += ((u64)hi[rank * SL + b0 + i] << 32) + lo[rank * SL + b0 + i];
+                    v[i] += ((u64)hi[part * SL + b0 + i] << 32) + lo[part * SL + b0 + i];
                 }
             }
             sum += v[i];
@@ -270,40 +303,48 @@ struct Row {
         if (lane == 31) S.wsum[w] = inc;
         if (tid == 0) S.found = 0;
         __syncthreads();
-        const u64 ws = lane < NW ? S.wsum[lane] : 0;
-        const u64 all = warp_sum(ws);
-        inc += warp_sum(lane < w ? ws : 0ull);
-        const Gather *got = exchange(Gather{all, 0u, 0u});
-        u64 at = above + inc - sum, total = 0;
+        u64 ws = lane < NW ? S.wsum[lane] : 0, wi = ws;
 #pragma unroll
-        for (int r = 0; r < C; ++r) {
-            if (r < rank) at += got[r].a;
-            total += got[r].a;
+        for (int o = 1; o < 32; o <<= 1) {
+            const u64 y = __shfl_up_sync(0xffffffffu, wi, o);
+            if (lane >= o) wi += y;
         }
-        if (frac >= 0.f) {
-            if (tid == 0) S.target = max(1ull, (u64)ceil((double)frac * (double)total));
-            __syncthreads();
-            target = S.target;
+        u64 total = __shfl_sync(0xffffffffu, wi, 31);
+        u64 at = above + inc - sum + __shfl_sync(0xffffffffu, wi - ws, w);
+        if constexpr (G > 1) {
+            const Gather *got = exchange(Gather{total, 0u, 0u});
+            total = 0;
+#pragma unroll
+            for (int r = 0; r < G; ++r) {
+                if (r < rank) at += got[r].a;
+                total += got[r].a;
+            }
         }
+        if (frac >= 0.f) target = max(1ull, scaled(frac, total, true));
 #pragma unroll
         for (int i = 0; i < PT; ++i) {
             if (at < target && target <= at + v[i]) {
                 S.found = 1;
-                S.found_bin = (uint32_t)(rank * SL + b0 + i);
+                S.found_bin = (uint32_t)(part * SL + b0 + i);
                 S.found_before = at;
             }
             at += v[i];
         }
         __syncthreads();
-        got = exchange(Gather{S.found_before, S.found_bin, (uint32_t)S.found});
         int bin = F_BINS - 1;
         before = above;
+        if constexpr (G > 1) {
+            const Gather *got = exchange(Gather{S.found_before, S.found_bin, (uint32_t)S.found});
 #pragma unroll
-        for (int r = 0; r < C; ++r)
-            if (got[r].c) {
-                bin = (int)got[r].b;
-                before = got[r].a;
-            }
+            for (int r = 0; r < G; ++r)
+                if (got[r].c) {
+                    bin = (int)got[r].b;
+                    before = got[r].a;
+                }
+        } else if (S.found) {
+            bin = (int)S.found_bin;
+            before = S.found_before;
+        }
         return bin;
     }
 
@@ -346,9 +387,39 @@ struct Row {
         return total;
     }
 
-    // Among the m gathered values: the key of the value at which the count of
-    // values at or above it reaches k.
-    __device__ uint32_t rank_count(int m, int k) {
+    // The border among the keys of [kmin, kmax] over the logits (LIST: over the
+    // m gathered ones, in this CTA alone): 2048 equal runs of keys a level, until
+    // one key is left.  (11 bits a level: at most 3 levels.)
+    template <bool MASS, bool LIST>
+    __device__ uint32_t refine(uint32_t kmin, uint32_t kmax, u64 above, u64 target, int m) {
+        while (kmin < kmax) {
+            int shift = 0;
+            while (((kmax - kmin) >> shift) >= (uint32_t)F_BINS) ++shift;
+            clear_hist();
+            auto take = [&](float x) {
+                const uint32_t key = key_of(x);
+                if (key < kmin || key > kmax) return;
+                const u64 wt = MASS ? weight_of(x) : 1ull;
+                if (wt) hist_add(S, (int)((kmax - key) >> shift), wt);
+            };
+            if constexpr (LIST) {
+                for (int i = tid; i < m; i += NT) take(S.all[i]);
+            } else {
+                each(take);
+            }
+            u64 before = 0;
+            const uint32_t bin = (uint32_t)find_bin<LIST ? 1 : C>(above, target, -1.f, before);
+            above = before;
+            kmax -= min(bin << shift, kmax - kmin);
+            kmin = max(kmin, kmax - min(kmax, (1u << shift) - 1u));
+        }
+        return kmax;
+    }
+
+    // Among the m gathered values, all keys in [kmin, kmax]: the key of the
+    // value at which the count of values at or above it reaches k.
+    __device__ uint32_t list_count(int m, int k, uint32_t kmin, uint32_t kmax) {
+        if (m > F_RANK) return refine<false, true>(kmin, kmax, 0ull, (u64)k, m);
         if (tid < m) {
             const float x = S.all[tid];
             int gt = 0, ge = 0;
@@ -363,22 +434,24 @@ struct Row {
         return S.key;
     }
     // The same by mass, over the values at or above `floor`: above + their
-    // mass reaches the target (or, with frac >= 0, ceil(frac * their mass)).
-    __device__ uint32_t rank_mass(int m, float floor, u64 above, u64 target, float frac) {
-        u64 mine = 0;
-        if (tid < m && S.all[tid] >= floor) mine = weight_of(S.all[tid]);
-        if (tid < m) S.mass[tid] = mine;
+    // mass reaches the target (or, with frac >= 0, that share of their mass).
+    __device__ uint32_t list_mass(int m, float floor, u64 above, u64 target, float frac, uint32_t kmin, uint32_t kmax) {
         if (frac >= 0.f) {
-            const u64 sum = warp_sum(mine);
+            u64 sum = 0;
+            for (int i = tid; i < m; i += NT)
+                if (S.all[i] >= floor) sum += weight_of(S.all[i]);
+            sum = warp_sum(sum);
             if (lane == 0) S.wsum[w] = sum;
             __syncthreads();
-            if (w == 0) {
-                const u64 all = warp_sum(lane < NW ? S.wsum[lane] : 0ull);
-                if (lane == 0) S.target = max(1ull, (u64)ceil((double)frac * (double)all));
-            }
+            target = max(1ull, scaled(frac, warp_sum(lane < NW ? S.wsum[lane] : 0ull), true));
+        }
+        if (m > F_RANK) return refine<true, true>(max(kmin, key_of(floor)), kmax, above, target, m);
+        u64 mine = 0;
+        if (tid < m) {
+            if (S.all[tid] >= floor) mine = weight_of(S.all[tid]);
+            S.mass[tid] = mine;
         }
         __syncthreads();
-        if (frac >= 0.f) target = S.target;
         if (mine) {
             const float x = S.all[tid];
             u64 gt = above, eq = 0;
@@ -394,65 +467,56 @@ struct Row {
         return S.key;
     }
 
-    // The border among the keys of [kmin, kmax], which hold every candidate and
-    // nothing else from `floor` on: 1024 equal runs of keys a level, until one
-    // key is left.  (10 bits a level: at most 4 levels.)
-    template <bool MASS>
-    __device__ uint32_t refine(uint32_t kmin, uint32_t kmax, u64 above, u64 target) {
-        while (kmin < kmax) {
-            int shift = 0;
-            while (((kmax - kmin) >> shift) >= (uint32_t)F_BINS) ++shift;
+    // The lower bounds that top-k (off: k = 0) and top-p (off: 1) put on the logit.
+    __device__ float bounds(int k, float top_p, float thread_max) {
+        float floor = -INFINITY;
+        uint32_t kmin, kmax;
+        if (k > 0) {
+            clear_hist();
+            // (the padding behind the vocabulary is -inf, the same as a masked logit:
+            // it lies below every logit or equals the smallest, so it changes no bound above -inf)
+            if (2 * k <= NT * C) {
+                hist_add(S, step(thread_max), 1ull);
+            } else {
+                each([&](float x) { hist_add(S, step(x), 1ull); });
+            }
+            u64 target = (u64)k, before = 0;
+            const int last = find_bin<C>(0ull, target, -1.f, before);
+            const int m = collect([&](float x) { return step(x) <= last; }, kmin, kmax);
+            if (m <= F_LIST) {  // the list holds the whole top-k set
+                floor = of_key(list_count(m, k, kmin, kmax));
+                if (top_p < 1.f) floor = fmaxf(floor, of_key(list_mass(m, floor, 0ull, 0ull, top_p, kmin, kmax)));
+                return floor;
+            }
+            floor = of_key(refine<false, false>(kmin, kmax, 0ull, (u64)k, 0));
+        }
+        if (top_p < 1.f) {
             clear_hist();
             each([&](float x) {
-                const uint32_t key = key_of(x);
-                if (key < kmin || key > kmax) return;
-                const u64 wt = MASS ? weight_of(x) : 1ull;
-                if (wt) hist_add(S, (int)((kmax - key) >> shift), wt);
+                if (!(x >= floor)) return;
+                const u64 wt = weight_of(x);
+                if (wt) hist_add(S, step(x), wt);
             });
-            u64 before = 0;
-            const uint32_t bin = (uint32_t)find_bin(above, target, -1.f, before);
-            above = before;
-            kmax -= min(bin << shift, kmax - kmin);
-            kmin = max(kmin, kmax - min(kmax, (1u << shift) - 1u));
+            u64 target = 0, before = 0;
+            const int border = find_bin<C>(0ull, target, top_p, before);
+            const int m = collect([&](float x) { return x >= floor && step(x) == border; }, kmin, kmax);
+            uint32_t key = kmax;
+            if (kmin != kmax)
+                key = m <= F_LIST ? list_mass(m, floor, before, target, -1.f, kmin, kmax)
+                                  : refine<true, false>(kmin, kmax, before, target, 0);
+            floor = fmaxf(floor, of_key(key));
         }
-        return kmax;
+        return floor;
     }
 
-    // The key of the k-th largest logit, 0 < k < vocabulary.  `m` gets the
-    // number of gathered values if they hold the whole top-k set, else 0.
-    __device__ uint32_t top_k_key(int k, int vocab, float thread_max, int &m) {
-        clear_hist();
-        // (the padding behind the vocabulary is -inf, the same as a masked logit:
-        // it lies below every logit or equals the smallest, so it changes no bound above -inf)
-        if (2 * k <= NT * C) {
-            hist_add(S, step(thread_max), 1ull);
-        } else {
-            each([&](float x) { hist_add(S, step(x), 1ull); });
-        }
-        u64 target = (u64)k, before = 0;
-        const int last = find_bin(0ull, target, -1.f, before);
-        uint32_t kmin, kmax;
-        const int total = collect([&](float x) { return step(x) <= last; }, kmin, kmax);
-        m = total <= F_LIST ? total : 0;
-        if (m) return rank_count(m, k);
-        return refine<false>(kmin, kmax, 0ull, (u64)k);
-    }
-
-    // The key of the nucleus border over the logits at or above `floor`.
-    __device__ uint32_t top_p_key(float floor, float top_p) {
-        clear_hist();
-        each([&](float x) {
-            if (!(x >= floor)) return;
-            const u64 wt = weight_of(x);
-            if (wt) hist_add(S, step(x), wt);
-        });
-        u64 target = 0, before = 0;
-        const int border = find_bin(0ull, target, top_p, before);
-        uint32_t kmin, kmax;
-        const int total = collect([&](float x) { return x >= floor && step(x) == border; }, kmin, kmax);
-        if (kmin == kmax) return kmax;
-        if (total <= F_LIST) return rank_mass(total, floor, before, target, -1.f);
-        return refine<true>(kmin, kmax, before, target);
+    // The smallest float at or above max + T ln(p), by one thread: with p = m 2^e,
+    // ln m = g + ln(m e^-g) for g near it, and m e^-g - 1 from the exact weight.
+    __device__ float min_p_floor(float p, float t) const {
+        int e;
+        const float m = frexpf(p, &e), g = logf(m);
+        const u64 we = weight(g, 0.f, 1.44269502162933349609375f, 1.92596299112661746887e-8f, S.pow2);
+        const float rest = (float)((long long)((u64)(m * 16777216.f) << (F_FRAC - 24)) - (long long)we) / (float)we;
+        return __double2float_ru((double)rs.mx + (double)t * ((double)e * 0.69314718055994530942 + (double)g + (double)rest));
     }
 };
 
@@ -530,14 +594,6 @@ __global__ void __launch_bounds__(NT) sample_filtered_kernel(const FilterArgs a)
                          : a.dtype == LF_F16
                              ? load_row<__half, NT>(static_cast<const __half *>(a.logits) + at, n, z, nan, kmin)
                              : load_row<__nv_bfloat16, NT>(static_cast<const __nv_bfloat16 *>(a.logits) + at, n, z, nan, kmin);
-    // 64-bit arithmetic is slow (and the same for every thread): one thread of
-    // the last warp does the row's
-    if (tid == NT - 32 && t > 0.f) {
-        const double cd = 1.4426950408889634074 / (double)t;
-        S.ch = (float)cd;
-        S.cl = (float)(cd - (double)S.ch);
-        if (min_p > 0.f) S.ln_min_p = (double)t * log((double)min_p);
-    }
     uint32_t kmax = own;
     nan = __syncthreads_or(nan);
     R.block_minmax(kmin, kmax);
@@ -574,22 +630,19 @@ __global__ void __launch_bounds__(NT) sample_filtered_kernel(const FilterArgs a)
         return;
     }
 
+    // log2(e) / T as a pair: the quotient and what its product with T leaves
+    constexpr float kLog2eHi = 1.44269502162933349609375f, kLog2eLo = 1.92596299112661746887e-8f;
     R.rs.mx = mx;
-    R.rs.ch = S.ch;
-    R.rs.cl = S.cl;
-    // 16 steps per factor of 2 in weight, finer where the whole row spans less
-    R.rs.step = fmaxf(16.f * S.ch, (float)(F_BINS - 1) / (mx - of_key(kmin)));
+    R.rs.ch = __fdiv_rn(kLog2eHi, t);
+    R.rs.cl = __fdiv_rn(__fmaf_rn(-R.rs.ch, t, kLog2eHi) + kLog2eLo, t);
+    // 32 steps per factor of 2 in weight, finer where the whole row spans less
+    R.rs.step = fmaxf(32.f * R.rs.ch, (float)(F_BINS - 1) / (mx - of_key(kmin)));
 
-    float floor = -INFINITY;
-    int m = 0;
-    if (top_k > 0 && top_k < a.vocab)
-        floor = of_key(R.top_k_key(top_k, a.vocab, own ? of_key(own) : -INFINITY, m));
-    if (top_p < 1.f)
-        floor = fmaxf(floor, of_key(m ? R.rank_mass(m, floor, 0ull, 0ull, top_p) : R.top_p_key(floor, top_p)));
+    float floor = R.bounds(top_k > 0 && top_k < a.vocab ? top_k : 0, top_p, own ? of_key(own) : -INFINITY);
     if (min_p > 0.f) {
-        if (tid == 0) S.floor = __double2float_ru((double)mx + S.ln_min_p);
+        if (tid == 0) S.floor = R.min_p_floor(min_p, t);
         __syncthreads();
-        floor = fmaxf(floor, S.floor);
+        floor = fmaxf(floor, fminf(S.floor, mx));  // (min_p 1: the maxima stay whatever the last bit of the sum)
     }
 
     // the kept mass: each warp owns a contiguous range of the CTA's
@@ -608,17 +661,21 @@ __global__ void __launch_bounds__(NT) sample_filtered_kernel(const FilterArgs a)
     if (lane == 0) S.wsum[w] = mine;
     __syncthreads();
     const u64 ws = lane < NW ? S.wsum[lane] : 0;
-    u64 before = warp_sum(lane < w ? ws : 0ull);
-    got = R.exchange(Gather{warp_sum(ws), 0u, 0u});
+    u64 wi = ws;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const u64 y = __shfl_up_sync(0xffffffffu, wi, o);
+        if (lane >= o) wi += y;
+    }
+    u64 before = __shfl_sync(0xffffffffu, wi - ws, w);
+    got = R.exchange(Gather{__shfl_sync(0xffffffffu, wi, 31), 0u, 0u});
     u64 total = 0;
 #pragma unroll
     for (int r = 0; r < C; ++r) {
         if (r < rank) before += got[r].a;
         total += got[r].a;
     }
-    if (tid == 0) S.target = (u64)((double)u * (double)total);  // running > u * total <=> running > that
-    __syncthreads();
-    const u64 goal = S.target;
+    const u64 goal = scaled(u, total, false);  // running > u * total <=> running > that
     if (before > goal || goal >= before + mine) return;
     // this warp's range holds the crossing
     for (int c0 = 4 * q0; c0 < 4 * q1; c0 += 32) {
@@ -634,9 +691,10 @@ __global__ void __launch_bounds__(NT) sample_filtered_kernel(const FilterArgs a)
         if (hit) {
             if (lane == __ffs(hit) - 1) {
                 a.token[row] = i0 + i;
-                if (a.logprob) {  // from the logit, not from its rounded weight
-                    const double d = x == mx ? 0.0 : ((double)x - (double)mx) / (double)t;
-                    a.logprob[row] = (float)(d - log((double)total * 5.684341886080801e-14));  // 2^-44
+                // from the logit, not from its rounded weight; the mass is 1 + something (the maximum is kept)
+                if (a.logprob) {
+                    const float more = (float)(total - (1ull << F_FRAC)) * 5.684341886080801e-14f;  // 2^-44
+                    a.logprob[row] = (x == mx ? 0.f : (x - mx) / t) - log1pf(more);
                 }
             }
             return;
