@@ -18,12 +18,13 @@
 //
 // A row belongs to a cluster of 1, 2, 4 or 8 CTAs, each with a contiguous
 // range of the vocabulary in shared memory as fp32: the logits are read from
-// HBM once.  A bound is found in two stages.  First a histogram over 2048
-// equal steps of the logit below the maximum, summed over the cluster through
-// distributed shared memory, leaves few candidates:
-//   top-k: the threads' own maxima are counted; k of them at or above a step
-//          mean that the k-th largest logit is there too, so everything below
-//          drops out (for k above half the threads: every logit is counted);
+// HBM once.  A bound is found in two stages.  First a cheap bound
+// leaves few candidates (histograms: 2048 equal steps of the logit below the
+// maximum, summed over the cluster through distributed shared memory):
+//   top-k: of C CTAs, each takes the ceil(k / C)-th largest of its thread
+//          groups' maxima; at least k logits reach the smallest of those, so
+//          everything below drops out (for k above half the threads every
+//          logit is counted in the histogram instead);
 //   top-p: the masses of all logits (64 bits as two 32-bit shared atomics, the
 //          second only on a carry) name the step that holds the border.
 // The candidates' values (up to 1024) are then gathered in every CTA and told
@@ -196,6 +197,7 @@ __device__ __forceinline__ float of_key(uint32_t k) {
 template <int NT, int C>
 struct Row {
     static constexpr int NW = NT / 32;
+    static constexpr int RT = NT / F_RANK;  // threads to a candidate that is ranked pairwise
     FilterShared &S;
     const float4 *z4;  // this CTA's logits, -inf past n up to a multiple of 4
     int n4, rank, tid, lane, w;
@@ -420,16 +422,20 @@ struct Row {
     // value at which the count of values at or above it reaches k.
     __device__ uint32_t list_count(int m, int k, uint32_t kmin, uint32_t kmax) {
         if (m > F_RANK) return refine<false, true>(kmin, kmax, 0ull, (u64)k, m);
-        if (tid < m) {
-            const float x = S.all[tid];
-            int gt = 0, ge = 0;
-            for (int j = 0; j < m; ++j) {
-                const float y = S.all[j];
-                gt += y > x ? 1 : 0;
-                ge += y >= x ? 1 : 0;
-            }
-            if (gt < k && k <= ge) S.key = key_of(x);
+        const int i = tid / RT;  // RT neighbouring threads share candidate i
+        const float x = i < m ? S.all[i] : 0.f;
+        int gt = 0, ge = 0;
+        for (int j = tid % RT; j < m; j += RT) {
+            const float y = S.all[j];
+            gt += y > x ? 1 : 0;
+            ge += y >= x ? 1 : 0;
         }
+#pragma unroll
+        for (int o = 1; o < RT; o <<= 1) {
+            gt += __shfl_xor_sync(0xffffffffu, gt, o);
+            ge += __shfl_xor_sync(0xffffffffu, ge, o);
+        }
+        if (i < m && gt < k && k <= ge) S.key = key_of(x);
         __syncthreads();
         return S.key;
     }
@@ -446,43 +452,77 @@ struct Row {
             target = max(1ull, scaled(frac, warp_sum(lane < NW ? S.wsum[lane] : 0ull), true));
         }
         if (m > F_RANK) return refine<true, true>(max(kmin, key_of(floor)), kmax, above, target, m);
-        u64 mine = 0;
-        if (tid < m) {
-            if (S.all[tid] >= floor) mine = weight_of(S.all[tid]);
-            S.mass[tid] = mine;
-        }
+        if (tid < m) S.mass[tid] = S.all[tid] >= floor ? weight_of(S.all[tid]) : 0ull;
         __syncthreads();
-        if (mine) {
-            const float x = S.all[tid];
-            u64 gt = above, eq = 0;
-            for (int j = 0; j < m; ++j) {
-                const float y = S.all[j];
-                const u64 wj = S.mass[j];
-                gt += y > x ? wj : 0ull;
-                eq += y == x ? wj : 0ull;
+        const int i = tid / RT;
+        const float x = i < m ? S.all[i] : 0.f;
+        u64 gt = 0, eq = 0;
+        for (int j = tid % RT; j < m; j += RT) {
+            const float y = S.all[j];
+            const u64 wj = S.mass[j];
+            gt += y > x ? wj : 0ull;
+            eq += y == x ? wj : 0ull;
+        }
+#pragma unroll
+        for (int o = 1; o < RT; o <<= 1) {
+            gt += __shfl_xor_sync(0xffffffffu, gt, o);
+            eq += __shfl_xor_sync(0xffffffffu, eq, o);
+        }
+        gt += above;
+        if (i < m && gt < target && target <= gt + eq) S.key = key_of(x);
+        __syncthreads();
+        return S.key;
+    }
+
+    // A key that at least ceil(k / C) of this CTA's logits reach, so that k of
+    // the row's reach the smallest of the CTAs' keys: the ceil(k / C)-th largest of
+    // the maxima of groups of 32, 8 or 2 threads, at least twice as many groups
+    // as that.  0 where that is more than every thread's share (then the row's
+    // histogram finds the bound).  `own` is the thread's largest key.
+    __device__ uint32_t group_bound(uint32_t own, int k) {
+        const int need = (k + C - 1) / C;
+        const int size = 2 * need <= NT / 32 ? 32 : 2 * need <= NT / 8 ? 8 : 2 * need <= NT / 2 ? 2 : 0;
+        if (size == 0) return 0;
+        for (int o = 1; o < size; o <<= 1) own = max(own, __shfl_xor_sync(0xffffffffu, own, o));
+        const int groups = NT / size;
+        if (tid % size == 0) S.lo[tid / size] = own;
+        __syncthreads();
+        if (tid < groups) {  // (at most NT / 2 = 512 of them; equal keys rank alike, so one of the k-th's equals writes)
+            const uint32_t x = S.lo[tid];
+            int gt = 0, ge = 0;
+            for (int j = 0; j < groups; ++j) {
+                const uint32_t y = S.lo[j];
+                gt += y > x ? 1 : 0;
+                ge += y >= x ? 1 : 0;
             }
-            if (gt < target && target <= gt + eq) S.key = key_of(x);
+            if (gt < need && need <= ge) S.key = x;
         }
         __syncthreads();
         return S.key;
     }
 
-    // The lower bounds that top-k (off: k = 0) and top-p (off: 1) put on the logit.
-    __device__ float bounds(int k, float top_p, float thread_max) {
+    // The lower bounds that top-k (off: k = 0) and top-p (off: 1) put on the
+    // logit.  bound: a key that at least k logits reach, or 0.
+    __device__ float bounds(int k, float top_p, uint32_t bound) {
         float floor = -INFINITY;
         uint32_t kmin, kmax;
-        if (k > 0) {
+        if (k == 1) {
+            floor = rs.mx;
+            top_p = 1.f;  // the maxima are the nucleus too
+        } else if (k > 0) {
             clear_hist();
             // (the padding behind the vocabulary is -inf, the same as a masked logit:
             // it lies below every logit or equals the smallest, so it changes no bound above -inf)
-            if (2 * k <= NT * C) {
-                hist_add(S, step(thread_max), 1ull);
+            int m;
+            if (bound) {
+                const float least = of_key(bound);
+                m = collect([&](float x) { return x >= least; }, kmin, kmax);
             } else {
                 each([&](float x) { hist_add(S, step(x), 1ull); });
+                u64 target = (u64)k, before = 0;
+                const int last = find_bin<C>(0ull, target, -1.f, before);
+                m = collect([&](float x) { return step(x) <= last; }, kmin, kmax);
             }
-            u64 target = (u64)k, before = 0;
-            const int last = find_bin<C>(0ull, target, -1.f, before);
-            const int m = collect([&](float x) { return step(x) <= last; }, kmin, kmax);
             if (m <= F_LIST) {  // the list holds the whole top-k set
                 floor = of_key(list_count(m, k, kmin, kmax));
                 if (top_p < 1.f) floor = fmaxf(floor, of_key(list_mass(m, floor, 0ull, 0ull, top_p, kmin, kmax)));
@@ -595,12 +635,15 @@ __global__ void __launch_bounds__(NT) sample_filtered_kernel(const FilterArgs a)
                              ? load_row<__half, NT>(static_cast<const __half *>(a.logits) + at, n, z, nan, kmin)
                              : load_row<__nv_bfloat16, NT>(static_cast<const __nv_bfloat16 *>(a.logits) + at, n, z, nan, kmin);
     uint32_t kmax = own;
+    const int k = top_k > 0 && top_k < a.vocab ? top_k : 0;
     nan = __syncthreads_or(nan);
     R.block_minmax(kmin, kmax);
-    const Gather *got = R.exchange(Gather{nan ? 1ull : 0ull, kmin, kmax});
+    uint32_t bound = k > 1 && t > 0.f ? R.group_bound(own, k) : 0u;
+    const Gather *got = R.exchange(Gather{(u64)bound << 32 | (nan ? 1u : 0u), kmin, kmax});
 #pragma unroll
     for (int r = 0; r < C; ++r) {
-        nan |= got[r].a != 0;
+        nan |= (got[r].a & 1) != 0;
+        bound = min(bound, (uint32_t)(got[r].a >> 32));
         kmin = min(kmin, got[r].b);
         kmax = max(kmax, got[r].c);
     }
@@ -638,7 +681,7 @@ __global__ void __launch_bounds__(NT) sample_filtered_kernel(const FilterArgs a)
     // 32 steps per factor of 2 in weight, finer where the whole row spans less
     R.rs.step = fmaxf(32.f * R.rs.ch, (float)(F_BINS - 1) / (mx - of_key(kmin)));
 
-    float floor = R.bounds(top_k > 0 && top_k < a.vocab ? top_k : 0, top_p, own ? of_key(own) : -INFINITY);
+    float floor = R.bounds(k, top_p, bound);
     if (min_p > 0.f) {
         if (tid == 0) S.floor = R.min_p_floor(min_p, t);
         __syncthreads();
@@ -703,8 +746,8 @@ __global__ void __launch_bounds__(NT) sample_filtered_kernel(const FilterArgs a)
     }
 }
 
-constexpr int kMaxPer = 49152;  // logits of one CTA: 192 KB
-constexpr int kWidePer = 26624;  // above it (one CTA per SM by its shared memory): 1024 threads, else 512
+constexpr int kMaxPer = 49152;   // logits of one CTA: 192 KB
+constexpr int kPairPer = 20480;  // up to here two CTAs fit an SM's shared memory
 
 template <int NT, int C>
 lf_status launch_row(const FilterArgs &a, cudaStream_t st) {
@@ -716,8 +759,9 @@ lf_status launch_row(const FilterArgs &a, cudaStream_t st) {
 }
 
 template <int C>
-lf_status launch_cluster(const FilterArgs &a, cudaStream_t st) {
-    return a.per > kWidePer ? launch_row<1024, C>(a, st) : launch_row<512, C>(a, st);
+lf_status launch_cluster(const FilterArgs &a, int n_sm, cudaStream_t st) {
+    // 1024 threads where a CTA has its SM to itself
+    return a.per > kPairPer || a.rows * C <= n_sm ? launch_row<1024, C>(a, st) : launch_row<512, C>(a, st);
 }
 
 lf_status launch_filtered(FilterArgs a, cudaStream_t st) {
@@ -727,14 +771,18 @@ lf_status launch_filtered(FilterArgs a, cudaStream_t st) {
         (void)cudaGetLastError();
         return LF_ERR_CUDA;
     }
+    // CTAs per row: what the shared memory asks for, and more while the grid has at
+    // most one CTA per SM and a CTA at least 4096 logits.  Measured (us, c = 1 | 2 | 4
+    // | 8): 1 x 32000 17.4 | 14.8 | 12.2 | 9.9, 16 x 32000 39 | 30 | 23 | 20, 64 x
+    // 32000 39 | 32 | 29 | 34, 256 x 32000 58 | 57 | 69 | 107, 1 x 4000 7.3 | 7.6 | 8.0 | 8.9.
     int c = 1;
-    while (c < F_MAX_CLUSTER && ((a.vocab + c - 1) / c > kMaxPer || (a.rows * c < n_sm && a.vocab / c > 2048))) c *= 2;
+    while (c < F_MAX_CLUSTER && ((a.vocab + c - 1) / c > kMaxPer || (a.rows * c <= n_sm && a.vocab / c > 4096))) c *= 2;
     a.per = ((a.vocab + c - 1) / c + 7) / 8 * 8;
     switch (c) {
-        case 1: return launch_cluster<1>(a, st);
-        case 2: return launch_cluster<2>(a, st);
-        case 4: return launch_cluster<4>(a, st);
-        default: return launch_cluster<8>(a, st);
+        case 1: return launch_cluster<1>(a, n_sm, st);
+        case 2: return launch_cluster<2>(a, n_sm, st);
+        case 4: return launch_cluster<4>(a, n_sm, st);
+        default: return launch_cluster<8>(a, n_sm, st);
     }
 }
 
