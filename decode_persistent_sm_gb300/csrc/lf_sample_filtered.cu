@@ -126,11 +126,10 @@ __device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162flo
 // 2^-y = 2^(-j / 256) (1 - q), q = 1 - e^(-t), t = r ln 2 = th + tl, |t| < 0.0014:
 // q = th + (tl - th^2 (1/2 - th / 6)), the rest below 2^-42.  Sums of a large and a
 // small integer are taken after their conversions (the small one by adding 1.5 * 2^23).
+// mx is finite.
 __device__ __forceinline__ u64 weight(float z, float mx, float ch, float cl, const u64 *pow2) {
-    if (z == mx) return 1ull << F_FRAC;  // (also +inf)
     const float s = mx - z;
     const float yh = __fmul_rn(s, ch);
-    if (!(yh < F_MAX_Y)) return 0;
     constexpr float kRound = 12582912.f;  // 1.5 * 2^23: adding it leaves the integer part in the low mantissa bits
     constexpr int kRoundBits = 0x4B400000;
     const float bb = __fsub_rn(s, mx);  // mx - z = s + e exactly
@@ -148,7 +147,8 @@ __device__ __forceinline__ u64 weight(float z, float mx, float ch, float cl, con
     const u64 t = pow2[j & 255];
     const u64 w61 = t - (u64)(((long long)(int)(t >> 31) * q) >> 8);
     const int sh = 61 - F_FRAC + (j >> 8);
-    return ((w61 >> (sh - 1)) + 1) >> 1;
+    const u64 v = ((w61 >> ((sh - 1) & 63)) + 1) >> 1;
+    return yh < F_MAX_Y ? v : 0ull;  // (a select: what was computed for a far or infinite z is dropped)
 }
 
 // floor(f * s), or (up) its ceiling, exactly, for 0 <= f < 1.
@@ -476,27 +476,31 @@ struct Row {
 
     // A key that at least ceil(k / C) of this CTA's logits reach, so that k of
     // the row's reach the smallest of the CTAs' keys: the ceil(k / C)-th largest of
-    // the maxima of groups of 32, 8 or 2 threads, at least twice as many groups
-    // as that.  0 where that is more than every thread's share (then the row's
+    // the maxima of groups of threads (32, 8 or 2 to 4 of them), at least twice as
+    // many groups as that.  0 where 256 groups are too few for it (then the row's
     // histogram finds the bound).  `own` is the thread's largest key.
     __device__ uint32_t group_bound(uint32_t own, int k) {
         const int need = (k + C - 1) / C;
-        const int size = 2 * need <= NT / 32 ? 32 : 2 * need <= NT / 8 ? 8 : 2 * need <= NT / 2 ? 2 : 0;
+        const int size = 2 * need <= NT / 32 ? 32 : 2 * need <= NT / 8 ? 8 : 2 * need <= F_RANK ? RT : 0;
         if (size == 0) return 0;
         for (int o = 1; o < size; o <<= 1) own = max(own, __shfl_xor_sync(0xffffffffu, own, o));
-        const int groups = NT / size;
+        const int groups = NT / size;  // at most F_RANK
         if (tid % size == 0) S.lo[tid / size] = own;
         __syncthreads();
-        if (tid < groups) {  // (at most NT / 2 = 512 of them; equal keys rank alike, so one of the k-th's equals writes)
-            const uint32_t x = S.lo[tid];
-            int gt = 0, ge = 0;
-            for (int j = 0; j < groups; ++j) {
-                const uint32_t y = S.lo[j];
-                gt += y > x ? 1 : 0;
-                ge += y >= x ? 1 : 0;
-            }
-            if (gt < need && need <= ge) S.key = x;
+        const int i = tid / RT;  // RT neighbouring threads rank group i
+        const uint32_t x = i < groups ? S.lo[i] : 0u;
+        int gt = 0, ge = 0;
+        for (int j = tid % RT; j < groups; j += RT) {
+            const uint32_t y = S.lo[j];
+            gt += y > x ? 1 : 0;
+            ge += y >= x ? 1 : 0;
         }
+#pragma unroll
+        for (int o = 1; o < RT; o <<= 1) {
+            gt += __shfl_xor_sync(0xffffffffu, gt, o);
+            ge += __shfl_xor_sync(0xffffffffu, ge, o);
+        }
+        if (i < groups && gt < need && need <= ge) S.key = x;
         __syncthreads();
         return S.key;
     }
@@ -647,7 +651,7 @@ __global__ void __launch_bounds__(NT) sample_filtered_kernel(const FilterArgs a)
         kmin = min(kmin, got[r].b);
         kmax = max(kmax, got[r].c);
     }
-    const float mx = of_key(kmax);
+    float mx = of_key(kmax);
     if (nan || !(mx > -INFINITY)) {
         if (rank == 0 && tid == 0) {
             a.token[row] = -1;
@@ -673,6 +677,14 @@ __global__ void __launch_bounds__(NT) sample_filtered_kernel(const FilterArgs a)
         return;
     }
 
+    const bool infinite = mx == INFINITY;
+    if (infinite) {  // the infinite logits hold all the mass, equally, under any filter: 0 there and -inf elsewhere
+        for (int i = tid; i < 4 * R.n4; i += NT) z[i] = z[i] == INFINITY ? 0.f : -INFINITY;
+        mx = 0.f;
+        kmin = key_of(0.f);
+        __syncthreads();
+    }
+
     // log2(e) / T as a pair: the quotient and what its product with T leaves
     constexpr float kLog2eHi = 1.44269502162933349609375f, kLog2eLo = 1.92596299112661746887e-8f;
     R.rs.mx = mx;
@@ -681,8 +693,8 @@ __global__ void __launch_bounds__(NT) sample_filtered_kernel(const FilterArgs a)
     // 32 steps per factor of 2 in weight, finer where the whole row spans less
     R.rs.step = fmaxf(32.f * R.rs.ch, (float)(F_BINS - 1) / (mx - of_key(kmin)));
 
-    float floor = R.bounds(k, top_p, bound);
-    if (min_p > 0.f) {
+    float floor = infinite ? 0.f : R.bounds(k, top_p, bound);
+    if (min_p > 0.f && !infinite) {
         if (tid == 0) S.floor = R.min_p_floor(min_p, t);
         __syncthreads();
         floor = fmaxf(floor, fminf(S.floor, mx));  // (min_p 1: the maxima stay whatever the last bit of the sum)
@@ -694,10 +706,10 @@ __global__ void __launch_bounds__(NT) sample_filtered_kernel(const FilterArgs a)
 #pragma unroll 2
     for (int i = q0 + lane; i < q1; i += 32) {
         const float4 x = R.z4[i];
-        if (x.x >= floor) mine += R.weight_of(x.x);
-        if (x.y >= floor) mine += R.weight_of(x.y);
-        if (x.z >= floor) mine += R.weight_of(x.z);
-        if (x.w >= floor) mine += R.weight_of(x.w);
+        if (!(fmaxf(fmaxf(x.x, x.y), fmaxf(x.z, x.w)) >= floor)) continue;
+        const u64 wx = R.weight_of(x.x), wy = R.weight_of(x.y), wz = R.weight_of(x.z), ww = R.weight_of(x.w);
+        mine += (x.x >= floor ? wx : 0ull) + (x.y >= floor ? wy : 0ull) + (x.z >= floor ? wz : 0ull) +
+                (x.w >= floor ? ww : 0ull);
     }
     mine = warp_sum(mine);
     __syncthreads();
