@@ -43,6 +43,7 @@
 
 #include "laneformer.h"
 #include "lf_paged.h"
+#include "lf_ptx.cuh"
 
 namespace cg = cooperative_groups;
 
@@ -87,7 +88,7 @@ struct FilterArgs {
     float *logprob;
 };
 
-struct Gather {  // one CTA's contribution to a cluster-wide exchange
+struct __align__(16) Gather {  // one CTA's contribution to a cluster-wide exchange
     u64 a;
     uint32_t b, c;
 };
@@ -102,7 +103,8 @@ struct FilterShared {
     float cand[F_LIST];      // this CTA's candidates
     float all[F_LIST];       // the cluster's
     u64 mass[F_RANK];        // weights of those ranked pairwise
-    Gather slot[2][F_MAX_CLUSTER];
+    Gather slot[2][F_MAX_CLUSTER], said, heard[F_MAX_CLUSTER];
+    uint64_t bar[2];
     u64 wsum[32];
     uint32_t wmin[32], wmax[32];
     u64 found_before;
@@ -151,8 +153,13 @@ __device__ __forceinline__ u64 weight(float z, float mx, float ch, float cl, con
     return yh < F_MAX_Y ? v : 0ull;  // (a select: what was computed for a far or infinite z is dropped)
 }
 
+// The same as a call, for the places that are not loops over the row.
+__device__ __noinline__ u64 weight_call(float z, float mx, float ch, float cl, const u64 *pow2) {
+    return weight(z, mx, ch, cl, pow2);
+}
+
 // floor(f * s), or (up) its ceiling, exactly, for 0 <= f < 1.
-__device__ __forceinline__ u64 scaled(float f, u64 s, bool up) {
+__device__ __noinline__ u64 scaled(float f, u64 s, bool up) {
     const uint32_t bits = __float_as_uint(f);
     const int e = (int)(bits >> 23);
     const u64 m = e ? (bits & 0x7fffffu) | 0x800000u : bits;  // f = m 2^-k
@@ -194,6 +201,24 @@ __device__ __forceinline__ float of_key(uint32_t k) {
     return __uint_as_float((k & 0x80000000u) ? k & 0x7fffffffu : ~k);
 }
 
+// Phase wait whose acquire covers stores from other CTAs of the cluster.
+__device__ __forceinline__ bool wait_cluster(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "n"(kWaitHintNs)
+        : "memory");
+    return ok != 0;
+}
+
+__device__ __forceinline__ void no_draw(int32_t *token, float *logprob) {
+    *token = -1;
+    if (logprob) *logprob = __int_as_float(0x7fffffff);
+}
+
 template <int NT, int C>
 struct Row {
     static constexpr int NW = NT / 32;
@@ -202,16 +227,18 @@ struct Row {
     const float4 *z4;  // this CTA's logits, -inf past n up to a multiple of 4
     int n4, rank, tid, lane, w;
     int turn = 0;
+    int32_t *token;
+    float *logprob;
     RowScale rs;
 
-    __device__ Row(FilterShared &s, const float *z, int n, int r)
+    __device__ Row(FilterShared &s, const float *z, int n, int r, int32_t *tok, float *lp)
         : S(s), z4(reinterpret_cast<const float4 *>(z)), n4((n + 3) / 4), rank(r), tid(threadIdx.x),
-          lane(threadIdx.x & 31), w(threadIdx.x >> 5) {}
+          lane(threadIdx.x & 31), w(threadIdx.x >> 5), token(tok), logprob(lp) {}
 
     // f(value) for every logit of this CTA
     template <class F>
     __device__ __forceinline__ void each(F f) const {
-#pragma unroll 2
+#pragma unroll 1
         for (int i = tid; i < n4; i += NT) {
             const float4 x = z4[i];
             f(x.x);
@@ -221,19 +248,37 @@ struct Row {
         }
     }
 
-    // Every CTA of the cluster gets every CTA's Gather.  `turn` alternates the
-    // buffers: a CTA can write the next but one exchange only after every CTA
-    // has passed the next, and so has read this one.
+    // Every CTA of the cluster gets every CTA's Gather: one 16-byte store into
+    // each CTA's shared memory, counted there on a barrier (about 1 us less than a
+    // store and a cluster barrier).  g is the same in threads 0 .. C - 1; a
+    // __syncthreads lies between two exchanges, so a CTA has read the buffer of
+    // one before its message of the next lets anyone write the one after
+    // (`turn` alternates two buffers).  The wait is bounded: a thread whose wait
+    // runs out reports the row as one without a draw and ends.
     __device__ __forceinline__ const Gather *exchange(const Gather &g) {
-        Gather *mine = S.slot[turn & 1];
+        const int b = turn & 1, parity = (turn >> 1) & 1;
+        Gather *mine = S.slot[b];
         ++turn;
         if constexpr (C == 1) {
             if (tid == 0) mine[0] = g;
             __syncthreads();
         } else {
-            cg::cluster_group cl = cg::this_cluster();
-            if (tid < C) cl.map_shared_rank(mine, tid)[rank] = g;
-            cl.sync();
+            if (tid == 0) mbar_arrive_expect_tx(&S.bar[b], C * (uint32_t)sizeof(Gather));
+            if (tid < C) {
+                uint32_t dst, bar;
+                asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(dst) : "r"(smem_u32(mine + rank)), "r"(tid));
+                asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(bar) : "r"(smem_u32(&S.bar[b])), "r"(tid));
+                asm volatile(
+                    "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(dst),
+                    "r"((uint32_t)g.a), "r"((uint32_t)(g.a >> 32)), "r"(g.b), "r"(g.c), "r"(bar)
+                    : "memory");
+            }
+            const uint64_t give_up = global_timer_ns() + 2000000000ull;
+            while (!wait_cluster(&S.bar[b], parity))
+                if (global_timer_ns() > give_up) {
+                    no_draw(token, logprob);
+                    asm volatile("exit;");
+                }
         }
         return mine;
     }
@@ -256,6 +301,7 @@ struct Row {
     }
 
     __device__ __forceinline__ u64 weight_of(float x) const { return weight(x, rs.mx, rs.ch, rs.cl, S.pow2); }
+    __device__ __forceinline__ u64 weight_cold(float x) const { return weight_call(x, rs.mx, rs.ch, rs.cl, S.pow2); }
     __device__ __forceinline__ int step(float x) const { return step_of(x, rs.mx, rs.step); }
 
     __device__ void clear_hist() {
@@ -366,51 +412,61 @@ struct Row {
             }
         });
         block_minmax(kmin, kmax);
-        const int mine = S.n_cand;
-        const Gather *got = exchange(Gather{(u64)mine, kmin, kmax});
-        int total = 0, count[C], first[C];
+        // the lists and what each CTA says of its own are read from its shared memory
+        if (tid == 0) S.said = Gather{(u64)S.n_cand, kmin, kmax};
+        sync();
+        const Gather *got = &S.said;
+        if constexpr (C > 1) {
+            if (tid < C) S.heard[tid] = *cg::this_cluster().map_shared_rank(&S.said, tid);
+            __syncthreads();
+            got = S.heard;
+        }
+        int total = 0, first[C];
 #pragma unroll
         for (int r = 0; r < C; ++r) {
             kmin = min(kmin, got[r].b);
             kmax = max(kmax, got[r].c);
             first[r] = total;
-            count[r] = (int)got[r].a;
-            total += count[r];
+            total += (int)got[r].a;
         }
         if (total <= F_LIST) {
+            for (int i = tid; i < total; i += NT) {
+                int r = 0, at = i;  // entry `at` of CTA r's list
 #pragma unroll
-            for (int r = 0; r < C; ++r) {
+                for (int x = 1; x < C; ++x)
+                    if (i >= first[x]) r = x, at = i - first[x];
                 const float *src = S.cand;
                 if constexpr (C > 1) src = cg::this_cluster().map_shared_rank(S.cand, r);
-                for (int i = tid; i < count[r]; i += NT) S.all[first[r] + i] = src[i];
+                S.all[i] = src[at];
             }
             __syncthreads();
         }
         return total;
     }
 
-    // The border among the keys of [kmin, kmax] over the logits (LIST: over the
-    // m gathered ones, in this CTA alone): 2048 equal runs of keys a level, until
-    // one key is left.  (11 bits a level: at most 3 levels.)
-    template <bool MASS, bool LIST>
-    __device__ uint32_t refine(uint32_t kmin, uint32_t kmax, u64 above, u64 target, int m) {
+    __device__ __forceinline__ u64 share(float x, bool mass) const { return mass ? weight_cold(x) : 1ull; }
+
+    // The border among the keys of [kmin, kmax] over the row's logits (list:
+    // over the m gathered ones, in this CTA alone), by mass or by count: 2048 equal
+    // runs of keys a level, until one key is left.  (11 bits a level: at most 3.)
+    __device__ uint32_t refine(bool mass, bool list, int m, uint32_t kmin, uint32_t kmax, u64 above, u64 target) {
+        const float *src = list ? S.all : reinterpret_cast<const float *>(z4);
+        const int n = list ? m : 4 * n4;
         while (kmin < kmax) {
             int shift = 0;
             while (((kmax - kmin) >> shift) >= (uint32_t)F_BINS) ++shift;
             clear_hist();
-            auto take = [&](float x) {
+#pragma unroll 1
+            for (int i = tid; i < n; i += NT) {
+                const float x = src[i];
                 const uint32_t key = key_of(x);
-                if (key < kmin || key > kmax) return;
-                const u64 wt = MASS ? weight_of(x) : 1ull;
+                if (key < kmin || key > kmax) continue;
+                const u64 wt = share(x, mass);
                 if (wt) hist_add(S, (int)((kmax - key) >> shift), wt);
-            };
-            if constexpr (LIST) {
-                for (int i = tid; i < m; i += NT) take(S.all[i]);
-            } else {
-                each(take);
             }
             u64 before = 0;
-            const uint32_t bin = (uint32_t)find_bin<LIST ? 1 : C>(above, target, -1.f, before);
+            const uint32_t bin = (uint32_t)(list ? find_bin<1>(above, target, -1.f, before)
+                                                 : find_bin<C>(above, target, -1.f, before));
             above = before;
             kmax -= min(bin << shift, kmax - kmin);
             kmin = max(kmin, kmax - min(kmax, (1u << shift) - 1u));
@@ -418,45 +474,51 @@ struct Row {
         return kmax;
     }
 
-    // Among the m gathered values, all keys in [kmin, kmax]: the key of the
-    // value at which the count of values at or above it reaches k.
-    __device__ uint32_t list_count(int m, int k, uint32_t kmin, uint32_t kmax) {
-        if (m > F_RANK) return refine<false, true>(kmin, kmax, 0ull, (u64)k, m);
-        const int i = tid / RT;  // RT neighbouring threads share candidate i
-        const float x = i < m ? S.all[i] : 0.f;
-        int gt = 0, ge = 0;
-        for (int j = tid % RT; j < m; j += RT) {
-            const float y = S.all[j];
-            gt += y > x ? 1 : 0;
-            ge += y >= x ? 1 : 0;
-        }
+    // Among the m gathered values from `floor` on, all keys in [kmin, kmax]: the
+    // key of the value at which above + the values at or above it, by their mass
+    // or (MASS false: above 0, no floor) counted, reach the target; with frac >= 0
+    // that is frac of them all.
+    template <bool MASS>
+    __device__ uint32_t border(int m, float floor, u64 above, u64 target, float frac, uint32_t kmin,
+                                            uint32_t kmax) {
+        if constexpr (!MASS) {
+            if (m > F_RANK) return refine(false, true, m, kmin, kmax, above, target);
+            const int i = tid / RT, k = (int)target;  // RT neighbouring threads share candidate i
+            const float x = i < m ? S.all[i] : 0.f;
+            int gt = 0, ge = 0;
+            for (int j = tid % RT; j < m; j += RT) {
+                const float y = S.all[j];
+                gt += y > x ? 1 : 0;
+                ge += y >= x ? 1 : 0;
+            }
 #pragma unroll
-        for (int o = 1; o < RT; o <<= 1) {
-            gt += __shfl_xor_sync(0xffffffffu, gt, o);
-            ge += __shfl_xor_sync(0xffffffffu, ge, o);
+            for (int o = 1; o < RT; o <<= 1) {
+                gt += __shfl_xor_sync(0xffffffffu, gt, o);
+                ge += __shfl_xor_sync(0xffffffffu, ge, o);
+            }
+            if (i < m && gt < k && k <= ge) S.key = key_of(x);
+            __syncthreads();
+            return S.key;
         }
-        if (i < m && gt < k && k <= ge) S.key = key_of(x);
-        __syncthreads();
-        return S.key;
-    }
-    // The same by mass, over the values at or above `floor`: above + their
-    // mass reaches the target (or, with frac >= 0, that share of their mass).
-    __device__ uint32_t list_mass(int m, float floor, u64 above, u64 target, float frac, uint32_t kmin, uint32_t kmax) {
+        u64 own = 0;
+#pragma unroll 1
+        for (int i = tid; i < m; i += NT) {
+            const u64 v = S.all[i] >= floor ? weight_cold(S.all[i]) : 0ull;
+            if (i < F_RANK) S.mass[i] = v;
+            own += v;
+        }
         if (frac >= 0.f) {
-            u64 sum = 0;
-            for (int i = tid; i < m; i += NT)
-                if (S.all[i] >= floor) sum += weight_of(S.all[i]);
-            sum = warp_sum(sum);
-            if (lane == 0) S.wsum[w] = sum;
+            own = warp_sum(own);
+            if (lane == 0) S.wsum[w] = own;
             __syncthreads();
             target = max(1ull, scaled(frac, warp_sum(lane < NW ? S.wsum[lane] : 0ull), true));
         }
-        if (m > F_RANK) return refine<true, true>(max(kmin, key_of(floor)), kmax, above, target, m);
-        if (tid < m) S.mass[tid] = S.all[tid] >= floor ? weight_of(S.all[tid]) : 0ull;
+        if (m > F_RANK) return refine(true, true, m, max(kmin, key_of(floor)), kmax, above, target);
         __syncthreads();
         const int i = tid / RT;
         const float x = i < m ? S.all[i] : 0.f;
         u64 gt = 0, eq = 0;
+#pragma unroll 1
         for (int j = tid % RT; j < m; j += RT) {
             const float y = S.all[j];
             const u64 wj = S.mass[j];
@@ -476,12 +538,13 @@ struct Row {
 
     // A key that at least ceil(k / C) of this CTA's logits reach, so that k of
     // the row's reach the smallest of the CTAs' keys: the ceil(k / C)-th largest of
-    // the maxima of groups of threads (32, 8 or 2 to 4 of them), at least twice as
-    // many groups as that.  0 where 256 groups are too few for it (then the row's
+    // the maxima of groups of threads (32, 8 or 2 to 4 of them).  0 where 256 groups are too few for it (then the row's
     // histogram finds the bound).  `own` is the thread's largest key.
     __device__ uint32_t group_bound(uint32_t own, int k) {
         const int need = (k + C - 1) / C;
-        const int size = 2 * need <= NT / 32 ? 32 : 2 * need <= NT / 8 ? 8 : 2 * need <= F_RANK ? RT : 0;
+        // (at 4/5 of the groups, twice as many logits as wanted reach the bound)
+        const int most = 5 * need / 4;
+        const int size = most <= NT / 32 ? 32 : most <= NT / 8 ? 8 : most <= F_RANK ? RT : 0;
         if (size == 0) return 0;
         for (int o = 1; o < size; o <<= 1) own = max(own, __shfl_xor_sync(0xffffffffu, own, o));
         const int groups = NT / size;  // at most F_RANK
@@ -517,22 +580,22 @@ struct Row {
             clear_hist();
             // (the padding behind the vocabulary is -inf, the same as a masked logit:
             // it lies below every logit or equals the smallest, so it changes no bound above -inf)
-            int m;
+            u64 target = (u64)k, before = 0;
+            float least = -INFINITY;
+            int last = F_BINS;
             if (bound) {
-                const float least = of_key(bound);
-                m = collect([&](float x) { return x >= least; }, kmin, kmax);
+                least = of_key(bound);
             } else {
                 each([&](float x) { hist_add(S, step(x), 1ull); });
-                u64 target = (u64)k, before = 0;
-                const int last = find_bin<C>(0ull, target, -1.f, before);
-                m = collect([&](float x) { return step(x) <= last; }, kmin, kmax);
+                last = find_bin<C>(0ull, target, -1.f, before);
             }
+            const int m = collect([&](float x) { return x >= least && (last == F_BINS || step(x) <= last); }, kmin, kmax);
             if (m <= F_LIST) {  // the list holds the whole top-k set
-                floor = of_key(list_count(m, k, kmin, kmax));
-                if (top_p < 1.f) floor = fmaxf(floor, of_key(list_mass(m, floor, 0ull, 0ull, top_p, kmin, kmax)));
+                floor = of_key(border<false>(m, -INFINITY, 0ull, target, -1.f, kmin, kmax));
+                if (top_p < 1.f) floor = fmaxf(floor, of_key(border<true>(m, floor, 0ull, 0ull, top_p, kmin, kmax)));
                 return floor;
             }
-            floor = of_key(refine<false, false>(kmin, kmax, 0ull, (u64)k, 0));
+            floor = of_key(refine(false, false, 0, kmin, kmax, 0ull, target));
         }
         if (top_p < 1.f) {
             clear_hist();
@@ -542,12 +605,12 @@ struct Row {
                 if (wt) hist_add(S, step(x), wt);
             });
             u64 target = 0, before = 0;
-            const int border = find_bin<C>(0ull, target, top_p, before);
-            const int m = collect([&](float x) { return x >= floor && step(x) == border; }, kmin, kmax);
+            const int at = find_bin<C>(0ull, target, top_p, before);
+            const int m = collect([&](float x) { return x >= floor && step(x) == at; }, kmin, kmax);
             uint32_t key = kmax;
             if (kmin != kmax)
-                key = m <= F_LIST ? list_mass(m, floor, before, target, -1.f, kmin, kmax)
-                                  : refine<true, false>(kmin, kmax, before, target, 0);
+                key = m <= F_LIST ? border<true>(m, floor, before, target, -1.f, kmin, kmax)
+                                  : refine(true, false, 0, kmin, kmax, before, target);
             floor = fmaxf(floor, of_key(key));
         }
         return floor;
@@ -558,7 +621,7 @@ struct Row {
     __device__ float min_p_floor(float p, float t) const {
         int e;
         const float m = frexpf(p, &e), g = logf(m);
-        const u64 we = weight(g, 0.f, 1.44269502162933349609375f, 1.92596299112661746887e-8f, S.pow2);
+        const u64 we = weight_call(g, 0.f, 1.44269502162933349609375f, 1.92596299112661746887e-8f, S.pow2);
         const float rest = (float)((long long)((u64)(m * 16777216.f) << (F_FRAC - 24)) - (long long)we) / (float)we;
         return __double2float_ru((double)rs.mx + (double)t * ((double)e * 0.69314718055994530942 + (double)g + (double)rest));
     }
@@ -607,15 +670,24 @@ __device__ __forceinline__ uint32_t load_row(const T *src, int n, float *z, bool
 }
 
 template <int NT, int C>
-__global__ void __launch_bounds__(NT) sample_filtered_kernel(const FilterArgs a) {
+__global__ void __launch_bounds__(NT, 1024 / NT) sample_filtered_kernel(const FilterArgs a) {
     extern __shared__ __align__(16) float z[];  // this CTA's logits
     __shared__ FilterShared S;
     constexpr int NW = NT / 32;
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     const int row = blockIdx.x / C, rank = blockIdx.x % C;
     const int i0 = rank * a.per, n = max(0, min(a.per, a.vocab - i0));
-    Row<NT, C> R(S, z, n, rank);
+    float *logprob = a.logprob ? a.logprob + row : nullptr;
+    Row<NT, C> R(S, z, n, rank, a.token + row, logprob);
     for (int i = tid; i < 256; i += NT) S.pow2[i] = kPow2.v[i];
+    if constexpr (C > 1) {
+        if (tid == 0) {
+            mbar_init(&S.bar[0], 1);
+            mbar_init(&S.bar[1], 1);
+            fence_barrier_init();
+        }
+        R.sync();  // no message comes before the barriers are there
+    }
     pdl_wait();
     pdl_trigger();
 
@@ -625,10 +697,7 @@ __global__ void __launch_bounds__(NT) sample_filtered_kernel(const FilterArgs a)
     const bool fine = (t == 0.f || (t >= 1e-30f && t <= 1e30f)) && top_p > 0.f && top_p <= 1.f && min_p >= 0.f &&
                       min_p <= 1.f && u >= 0.f && u < 1.f;
     if (!fine) {  // every CTA of the row sees the same
-        if (rank == 0 && tid == 0) {
-            a.token[row] = -1;
-            if (a.logprob) a.logprob[row] = __int_as_float(0x7fffffff);
-        }
+        if (rank == 0 && tid == 0) no_draw(a.token + row, logprob);
         return;
     }
     const long long at = (long long)row * a.ld + i0;
@@ -653,10 +722,7 @@ __global__ void __launch_bounds__(NT) sample_filtered_kernel(const FilterArgs a)
     }
     float mx = of_key(kmax);
     if (nan || !(mx > -INFINITY)) {
-        if (rank == 0 && tid == 0) {
-            a.token[row] = -1;
-            if (a.logprob) a.logprob[row] = __int_as_float(0x7fffffff);
-        }
+        if (rank == 0 && tid == 0) no_draw(a.token + row, logprob);
         return;
     }
     if (t == 0.f) {  // greedy
@@ -672,7 +738,7 @@ __global__ void __launch_bounds__(NT) sample_filtered_kernel(const FilterArgs a)
         for (int r = 0; r < C; ++r) first = min(first, got[r].b);
         if (rank == 0 && tid == 0) {
             a.token[row] = (int)first;
-            if (a.logprob) a.logprob[row] = 0.f;
+            if (logprob) *logprob = 0.f;
         }
         return;
     }
@@ -703,7 +769,7 @@ __global__ void __launch_bounds__(NT) sample_filtered_kernel(const FilterArgs a)
     // the kept mass: each warp owns a contiguous range of the CTA's
     const int per_w = ((R.n4 + NW - 1) / NW), q0 = min(R.n4, w * per_w), q1 = min(R.n4, q0 + per_w);
     u64 mine = 0;
-#pragma unroll 2
+#pragma unroll 1
     for (int i = q0 + lane; i < q1; i += 32) {
         const float4 x = R.z4[i];
         if (!(fmaxf(fmaxf(x.x, x.y), fmaxf(x.z, x.w)) >= floor)) continue;
@@ -736,7 +802,7 @@ __global__ void __launch_bounds__(NT) sample_filtered_kernel(const FilterArgs a)
     for (int c0 = 4 * q0; c0 < 4 * q1; c0 += 32) {
         const int i = c0 + lane;
         const float x = i < 4 * q1 ? z[i] : -INFINITY;
-        u64 inc = x >= floor ? R.weight_of(x) : 0ull;
+        u64 inc = x >= floor ? R.weight_cold(x) : 0ull;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const u64 y = __shfl_up_sync(0xffffffffu, inc, o);
@@ -747,9 +813,9 @@ __global__ void __launch_bounds__(NT) sample_filtered_kernel(const FilterArgs a)
             if (lane == __ffs(hit) - 1) {
                 a.token[row] = i0 + i;
                 // from the logit, not from its rounded weight; the mass is 1 + something (the maximum is kept)
-                if (a.logprob) {
+                if (logprob) {
                     const float more = (float)(total - (1ull << F_FRAC)) * 5.684341886080801e-14f;  // 2^-44
-                    a.logprob[row] = (x == mx ? 0.f : (x - mx) / t) - log1pf(more);
+                    *logprob = (x == mx ? 0.f : (x - mx) / t) - log1pf(more);
                 }
             }
             return;
