@@ -59,6 +59,8 @@ _SIGS = {
     "lf_set_idle_prefetch": (_ci, [_vp, ctypes.c_uint32, ctypes.c_uint32]),
     "lf_debug_read_trace": (_ci, [_vp, _vp, ctypes.c_size_t, _vp]),
     "lf_batch_begin": (_ci, [_vp, _ci]),
+    "lf_batch_begin_shared": (_ci, [_vp, _ci]),
+    "lf_batch_generate_filtered": (_ci, [_vp, _vp, _ci, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
     "lf_batch_end": (_ci, [_vp]),
     "lf_batch_info": (_ci, [_vp, ctypes.POINTER(_ci), ctypes.POINTER(_ci)]),
     "lf_batch_step": (_ci, [_vp, _vp, _vp, _vp]),
@@ -342,6 +344,11 @@ class Engine:
         together (each with a copy of its KV cache so far)."""
         _check("lf_batch_begin", self._lib.lf_batch_begin(self._h, int(n_batch)))
 
+    def batch_begin_shared(self, n_batch: int):
+        """lf_batch_begin_shared: the same, with the cache so far kept once for
+        all samples and read once per step."""
+        _check("lf_batch_begin_shared", self._lib.lf_batch_begin_shared(self._h, int(n_batch)))
+
     def batch_end(self):
         _check("lf_batch_end", self._lib.lf_batch_end(self._h))
 
@@ -370,6 +377,27 @@ class Engine:
                                          int(seed) & (2 ** 64 - 1), out.ctypes.data)
         _check("lf_batch_generate", rc)
         return out
+
+    def batch_generate_filtered(self, first_tokens: Sequence[int], u, temperature=None, top_k=None, top_p=None,
+                                min_p=None):
+        """lf_batch_generate_filtered: u [B][n] uniform numbers, one per draw;
+        temperature, top_k, top_p, min_p one value for all samples, one per
+        sample, or None.  Returns (tokens [B][n], logprobs [B][n])."""
+        t = np.ascontiguousarray(np.asarray(first_tokens, dtype=np.int32))
+        u = np.ascontiguousarray(np.asarray(u, dtype=np.float32))
+        if u.ndim != 2 or u.shape[0] != t.size:
+            raise ValueError(f"u must be [{t.size}][steps], got {u.shape}")
+
+        def each(v, dtype):
+            return None if v is None else np.ascontiguousarray(np.broadcast_to(np.asarray(v, dtype=dtype), (t.size,)))
+
+        par = [each(temperature, np.float32), each(top_k, np.int32), each(top_p, np.float32), each(min_p, np.float32)]
+        out, lp = np.zeros(u.shape, dtype=np.int32), np.zeros(u.shape, dtype=np.float32)
+        rc = self._lib.lf_batch_generate_filtered(self._h, t.ctypes.data, u.shape[1],
+                                                  *[None if p is None else p.ctypes.data for p in par], u.ctypes.data,
+                                                  out.ctypes.data, lp.ctypes.data)
+        _check("lf_batch_generate_filtered", rc)
+        return out, lp
 
     def decode_step_chained(self, token_device_ptr: int, argmax_device_ptr: int):
         """Enqueues one step whose token is read from, and whose argmax goes to,

@@ -18,6 +18,12 @@
 // merges the splits in split order; drain + final norm; LM head; argmax.
 // The step is captured once as a CUDA graph; the kernels read the position
 // from a device word, so the same graph serves every step.
+//
+// A batch with a shared prefix (lf_batch_begin_shared) keeps the positions
+// before the branch once, in a paged cache whose pages all samples name, and
+// gives each sample pages of its own from there on.  Its QKV GEMV leaves fp32
+// rows; lf_kv_append_paged rotates and appends them, and lf_attn_paged_shared
+// reads the prefix once for all samples.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
@@ -41,6 +47,7 @@ constexpr int kBatchAttnSplits = 16;        // most key splits per (sample, KV h
 constexpr int kBatchAttnKeysPerSplit = 128;  // keys per split below that
 constexpr int kBatchAttnThreads = 128;
 constexpr unsigned long long kBatchTimeoutNs = 2000000000ull;
+constexpr int kBatchPage = 64;  // positions per page of a batch with a shared prefix
 
 struct BatchState {
     int B = 0, pos = 0;
@@ -59,6 +66,17 @@ struct BatchState {
     float *q = nullptr, *att_ws = nullptr;                           // [L][B][NQ * DH], [L][...]
     __half *h16 = nullptr, *o16 = nullptr, *u16 = nullptr;          // [2L + 1][B][D], [L][B][NQ * DH], [L][B][F]
     __half *kc = nullptr, *vc = nullptr;
+    // shared prefix: the first `prefix` positions once, kPage positions to a page; one pool of n_pages pages per layer
+    bool shared = false;
+    int prefix = 0, n_pages = 0, max_pages = 0;
+    int *table = nullptr, *spos = nullptr, *slen = nullptr;  // [B][max_pages], [B] positions, [B] lengths
+    float *qkv = nullptr;                                    // [L][B][(NQ + 2 NKV) DH]
+    __half *q16 = nullptr;                                   // [L][B][NQ DH]
+    uint8_t *pws = nullptr;                                  // attention workspace, one per sub-block in flight
+    size_t pws_bytes = 0;
+    // filtered generation: per-sample parameters, one row of u, tokens and log shares per step
+    float *f_t = nullptr, *f_p = nullptr, *f_mp = nullptr, *f_u = nullptr, *f_lp = nullptr;
+    int *f_k = nullptr, *f_tok = nullptr;
     // split-K workspace and counters of each GEMV of the step (QKV, O, gate/up, down per layer, then LM head)
     std::vector<size_t> ws_off;
     std::vector<int> cnt_off;
@@ -344,6 +362,48 @@ __global__ void ba_copy_prefix(const __half *__restrict__ ekc, const __half *__r
     }
 }
 
+// One step further for every sample of a batch with a shared prefix.
+__global__ void ba_bump_each(int *pos, int *len) {
+    pos[threadIdx.x] += 1;
+    len[threadIdx.x] += 1;
+}
+
+// Positions [0, P) of the engine's cache of layer l (blockIdx.x = l * NKV + kv
+// head, blockIdx.y = page) to the pages that sample 0's row of the table names.
+__global__ void ba_copy_prefix_paged(const __half *__restrict__ ekc, const __half *__restrict__ evc,
+                                     __half *__restrict__ pk, __half *__restrict__ pv, const int2 *__restrict__ kvsrc,
+                                     const int *__restrict__ table, int P, int L, int NKV, int HKV_L, int DH, int ctx,
+                                     int n_pages) {
+    const int l = blockIdx.x / NKV, kh = blockIdx.x % NKV, j0 = blockIdx.y * lf::kBatchPage;
+    const int2 src = kvsrc[kh];
+    const size_t from = (((((size_t)src.x * L + l) * HKV_L + src.y) * ctx) + j0) * DH;
+    const size_t to = (((size_t)l * n_pages + table[blockIdx.y]) * NKV + kh) * lf::kBatchPage * DH;
+    const int n16 = min(lf::kBatchPage, P - j0) * DH / 8;
+    const uint4 *sk = reinterpret_cast<const uint4 *>(ekc + from), *sv = reinterpret_cast<const uint4 *>(evc + from);
+    uint4 *dk = reinterpret_cast<uint4 *>(pk + to), *dv = reinterpret_cast<uint4 *>(pv + to);
+    for (int i = threadIdx.x; i < n16; i += blockDim.x) {
+        dk[i] = sk[i];
+        dv[i] = sv[i];
+    }
+}
+
+// The paged cache of layer l.
+lf_paged_kv layer_pages(const BatchState &b, const lf::Shape &s, int l) {
+    lf_paged_kv kv = {};
+    const size_t at = (size_t)l * b.n_pages * s.NKV * lf::kBatchPage * s.DH;
+    kv.k = b.kc + at;
+    kv.v = b.vc + at;
+    kv.page_table = b.table;
+    kv.n_pages = b.n_pages;
+    kv.n_kv_heads = s.NKV;
+    kv.page_size = lf::kBatchPage;
+    kv.head_dim = s.DH;
+    kv.n_seqs = b.B;
+    kv.max_pages = b.max_pages;
+    kv.dtype = LF_F16;
+    return kv;
+}
+
 size_t al256(size_t b) { return (b + 255) & ~size_t(255); }
 
 size_t att_ws_floats(const lf::Shape &s, int B) {
@@ -419,7 +479,8 @@ void carve(BatchState &b, uint8_t *base, const lf::Shape &s, int B) {
         return p;
     };
     const size_t D = s.D, QD = (size_t)s.NQ * s.DH, F = s.F, V = s.V, R = 2 * (size_t)s.delay + 1, L = s.L;
-    const size_t kv = (size_t)B * s.L * s.NKV * s.ctx * s.DH;
+    const size_t kv = b.shared ? (size_t)s.L * b.n_pages * s.NKV * lf::kBatchPage * s.DH
+                               : (size_t)B * s.L * s.NKV * s.ctx * s.DH;
     b.tok = reinterpret_cast<int *>(take(B * sizeof(int)));
     b.gen = reinterpret_cast<int *>(take((size_t)B * s.ctx * sizeof(int)));
     b.am = reinterpret_cast<int *>(take(B * sizeof(int)));
@@ -437,6 +498,21 @@ void carve(BatchState &b, uint8_t *base, const lf::Shape &s, int B) {
     b.h16 = reinterpret_cast<__half *>(take((2 * L + 1) * B * D * 2));
     b.o16 = reinterpret_cast<__half *>(take(L * B * QD * 2));
     b.u16 = reinterpret_cast<__half *>(take(L * B * F * 2));
+    if (b.shared) {
+        b.table = reinterpret_cast<int *>(take((size_t)B * b.max_pages * sizeof(int)));
+        b.spos = reinterpret_cast<int *>(take(B * sizeof(int)));
+        b.slen = reinterpret_cast<int *>(take(B * sizeof(int)));
+        b.qkv = reinterpret_cast<float *>(take(L * B * (QD + 2 * (size_t)s.NKV * s.DH) * 4));
+        b.q16 = reinterpret_cast<__half *>(take(L * B * QD * 2));
+        b.pws = take(R * b.pws_bytes);
+    }
+    b.f_t = reinterpret_cast<float *>(take(B * 4));
+    b.f_p = reinterpret_cast<float *>(take(B * 4));
+    b.f_mp = reinterpret_cast<float *>(take(B * 4));
+    b.f_k = reinterpret_cast<int *>(take(B * 4));
+    b.f_u = reinterpret_cast<float *>(take((size_t)B * s.ctx * 4));
+    b.f_lp = reinterpret_cast<float *>(take((size_t)B * s.ctx * 4));
+    b.f_tok = reinterpret_cast<int *>(take((size_t)B * s.ctx * 4));
     b.kc = reinterpret_cast<__half *>(take(kv * 2));
     b.vc = reinterpret_cast<__half *>(take(kv * 2));
     b.bytes = at;
@@ -511,6 +587,29 @@ lf_status enqueue_batch_step(lf_engine *e, BatchState &b, cudaStream_t main) {
             float *q = b.q + (size_t)l * B * QD;
             __half *o16 = b.o16 + (size_t)l * B * QD;
             lf::GemvArgs a = gemv_args(4 * l);
+            if (b.shared) {
+                const lf_paged_kv kv = layer_pages(b, s, l);
+                const int64_t ld = QD + 2 * (int64_t)s.NKV * s.DH;
+                float *x = b.qkv + (size_t)l * B * ld;
+                __half *q16 = b.q16 + (size_t)l * B * QD;
+                a.mode = lf::GEMV_F32;
+                a.y = x;
+                a.ldy = (int)ld;
+                if ((gs = lf::gemv_tc(wt(4 * l), h, a, w)) != LF_OK) break;
+                gs = lf_kv_append_paged(&kv, x, x + QD, x + QD + (int64_t)s.NKV * s.DH, LF_F32, ld, ld, ld, s.NQ, q16, QD,
+                                        nullptr, b.spos, B, reinterpret_cast<const float *>(e->rope), s.ctx, b.err, w);
+                if (gs != LF_OK) break;
+                gs = lf_attn_paged_shared(&kv, q16, QD, o16, QD, nullptr, s.NQ, b.slen, s.ctx, b.prefix,
+                                          e->cfg.swa_window[l], scale, b.pws + (size_t)(sb % R) * b.pws_bytes, b.pws_bytes,
+                                          b.err, w);
+                if (gs != LF_OK) break;
+                a = gemv_args(4 * l + 1);
+                a.y = P;
+                a.ldy = D;
+                if ((gs = lf::gemv_tc(wt(4 * l + 1), o16, a, w)) != LF_OK) break;
+                cudaEventRecord(ev_part[sb], w);
+                continue;
+            }
             a.q = q;
             a.rope = e->rope;
             a.kc = b.kc;
@@ -558,6 +657,7 @@ lf_status enqueue_batch_step(lf_engine *e, BatchState &b, cudaStream_t main) {
     // (the argmax runs outside the graph, for lf_batch_step: the generation
     // loop draws its tokens from the logits with the sampler)
     if (gs == LF_OK) ba_bump<<<1, 1, 0, main>>>(b.d_pos);
+    if (gs == LF_OK && b.shared) ba_bump_each<<<1, B, 0, main>>>(b.spos, b.slen);
     destroy();
     if (gs != LF_OK) return gs;
     return cudaGetLastError() == cudaSuccess ? LF_OK : LF_ERR_CUDA;
@@ -592,7 +692,9 @@ void lf_batch_free(lf_engine *e) {
     e->batch = nullptr;
 }
 
-extern "C" lf_status lf_batch_begin(lf_engine *e, int n_batch) {
+namespace {
+
+lf_status batch_begin(lf_engine *e, int n_batch, bool shared) {
     if (!e || n_batch < 1 || n_batch > lf::kGemvMaxBatch) return LF_ERR_INVALID_ARG;
     if (e->poisoned != LF_OK) return e->poisoned;
     if (!e->loaded) return LF_ERR_NOT_LOADED;
@@ -621,6 +723,22 @@ extern "C" lf_status lf_batch_begin(lf_engine *e, int n_batch) {
     }
     b->ws_floats = b->ws_off.back();
     b->n_cnt = b->cnt_off.back();
+    const int whole = e->pos / lf::kBatchPage;  // pages of the prefix that every sample names
+    if (shared) {
+        b->shared = true;
+        b->prefix = e->pos;
+        b->max_pages = (s.ctx + lf::kBatchPage - 1) / lf::kBatchPage;
+        b->n_pages = whole + n_batch * (b->max_pages - whole);
+        b->B = n_batch;
+        lf_paged_kv kv = layer_pages(*b, s, 0);
+        kv.k = kv.v = reinterpret_cast<void *>(uintptr_t(256));  // only the sizes count here
+        kv.page_table = reinterpret_cast<const int32_t *>(uintptr_t(256));
+        b->pws_bytes = al256(lf_attn_paged_shared_workspace(&kv, s.NQ));
+        if (!b->pws_bytes) {
+            batch_release(b);
+            return LF_ERR_UNSUPPORTED;
+        }
+    }
     carve(*b, nullptr, s, n_batch);
     if (cudaMalloc(&b->mem, b->bytes) != cudaSuccess) {
         (void)cudaGetLastError();
@@ -641,7 +759,22 @@ extern "C" lf_status lf_batch_begin(lf_engine *e, int n_batch) {
     if (err == cudaSuccess) err = cudaMemcpyAsync(b->kvsrc, kvsrc.data(), kvsrc.size() * sizeof(int2), cudaMemcpyHostToDevice, st);
     b->pos = e->pos;
     if (err == cudaSuccess) err = cudaMemcpyAsync(b->d_pos, &b->pos, sizeof(int), cudaMemcpyHostToDevice, st);
-    if (err == cudaSuccess && e->pos > 0)
+    if (shared) {
+        // sample i's row: the whole pages of the prefix, then pages of its own; sample 0's first own page also takes
+        // the prefix's last, incomplete one
+        std::vector<int> table((size_t)n_batch * b->max_pages), pos(n_batch, e->pos), len(n_batch, e->pos + 1);
+        for (int i = 0; i < n_batch; ++i)
+            for (int g = 0; g < b->max_pages; ++g)
+                table[(size_t)i * b->max_pages + g] = g < whole ? g : whole + i * (b->max_pages - whole) + g - whole;
+        const size_t nb = (size_t)n_batch * sizeof(int);
+        if (err == cudaSuccess) err = cudaMemcpyAsync(b->table, table.data(), table.size() * sizeof(int), cudaMemcpyHostToDevice, st);
+        if (err == cudaSuccess) err = cudaMemcpyAsync(b->spos, pos.data(), nb, cudaMemcpyHostToDevice, st);
+        if (err == cudaSuccess) err = cudaMemcpyAsync(b->slen, len.data(), nb, cudaMemcpyHostToDevice, st);
+        if (err == cudaSuccess && e->pos > 0)
+            ba_copy_prefix_paged<<<dim3(s.L * s.NKV, (e->pos + lf::kBatchPage - 1) / lf::kBatchPage), 256, 0, st>>>(
+                e->kc, e->vc, b->kc, b->vc, b->kvsrc, b->table, e->pos, s.L, s.NKV, s.HKV_L, s.DH, s.ctx, b->n_pages);
+        if (err == cudaSuccess) err = cudaStreamSynchronize(st);  // the host arrays go out of scope
+    } else if (err == cudaSuccess && e->pos > 0)
         ba_copy_prefix<<<dim3(s.L * s.NKV, n_batch), 256, 0, st>>>(e->kc, e->vc, b->kc, b->vc, b->kvsrc, e->pos, s.L,
                                                                   s.NKV, s.HKV_L, s.DH, s.ctx);
     if (err == cudaSuccess) err = cudaStreamSynchronize(st);
@@ -674,6 +807,12 @@ extern "C" lf_status lf_batch_begin(lf_engine *e, int n_batch) {
     b->ready = true;
     return LF_OK;
 }
+
+}  // namespace
+
+extern "C" lf_status lf_batch_begin(lf_engine *e, int n_batch) { return batch_begin(e, n_batch, false); }
+
+extern "C" lf_status lf_batch_begin_shared(lf_engine *e, int n_batch) { return batch_begin(e, n_batch, true); }
 
 extern "C" lf_status lf_batch_end(lf_engine *e) {
     if (!e) return LF_ERR_INVALID_ARG;
@@ -751,4 +890,73 @@ extern "C" lf_status lf_batch_generate(lf_engine *e, const int32_t *first_tokens
     const lf_status r = batch_finish(e, b);
     if (r == LF_OK) b.pos += n_steps;
     return r;
+}
+
+extern "C" lf_status lf_batch_generate_filtered(lf_engine *e, const int32_t *first_tokens, int n_steps,
+                                                const float *temperature, const int32_t *top_k, const float *top_p,
+                                                const float *min_p, const float *u, int32_t *tokens_out,
+                                                float *logprobs_out) {
+    if (!e || !first_tokens || !u || !tokens_out || n_steps < 1) return LF_ERR_INVALID_ARG;
+    if (e->poisoned != LF_OK) return e->poisoned;
+    if (!e->batch || !e->batch->ready) return LF_ERR_NOT_LOADED;
+    BatchState &b = *e->batch;
+    const lf::Shape &s = e->plan.sh;
+    if ((long long)b.pos + n_steps > s.ctx) return LF_ERR_CTX_OVERFLOW;
+    if (s.V > 262144) return LF_ERR_UNSUPPORTED;
+    const int B = b.B;
+    for (int i = 0; i < B; ++i) {
+        if (first_tokens[i] < 0 || first_tokens[i] >= s.V) return LF_ERR_INVALID_ARG;
+        if (temperature && !(temperature[i] == 0.f || (temperature[i] >= 1e-30f && temperature[i] <= 1e30f)))
+            return LF_ERR_INVALID_ARG;
+        if (top_p && !(top_p[i] > 0.f && top_p[i] <= 1.f)) return LF_ERR_INVALID_ARG;
+        if (min_p && !(min_p[i] >= 0.f && min_p[i] <= 1.f)) return LF_ERR_INVALID_ARG;
+    }
+    const size_t n = (size_t)B * n_steps, nb = (size_t)B * 4;
+    for (size_t i = 0; i < n; ++i)
+        if (!(u[i] >= 0.f && u[i] < 1.f)) return LF_ERR_INVALID_ARG;
+    std::vector<float> rows(n), lp(logprobs_out ? n : 0);  // step by step on the device, sample by sample for the caller
+    std::vector<int32_t> tok(n);
+    for (int i = 0; i < B; ++i)
+        for (int t = 0; t < n_steps; ++t) rows[(size_t)t * B + i] = u[(size_t)i * n_steps + t];
+    cudaStream_t st = e->stream;
+    cudaError_t err = cudaMemcpyAsync(b.tok, first_tokens, nb, cudaMemcpyHostToDevice, st);
+    auto up = [&](void *dst, const void *src, size_t bytes) {
+        if (err == cudaSuccess && src) err = cudaMemcpyAsync(dst, src, bytes, cudaMemcpyHostToDevice, st);
+    };
+    up(b.f_t, temperature, nb);
+    up(b.f_k, top_k, nb);
+    up(b.f_p, top_p, nb);
+    up(b.f_mp, min_p, nb);
+    up(b.f_u, rows.data(), n * 4);
+    for (int i = 0; i < n_steps && err == cudaSuccess; ++i) {
+        err = cudaGraphLaunch(b.graph, st);
+        if (err != cudaSuccess) break;
+        int *drawn = b.f_tok + (size_t)i * B;
+        const lf_status ls = lf_sample_filtered(b.logits, LF_F32, B, s.V, s.V, temperature ? b.f_t : nullptr,
+                                                top_k ? b.f_k : nullptr, top_p ? b.f_p : nullptr, min_p ? b.f_mp : nullptr,
+                                                b.f_u + (size_t)i * B, drawn, b.f_lp + (size_t)i * B, st);
+        if (ls != LF_OK) {
+            (void)cudaStreamSynchronize(st);  // the copies from this call's arrays
+            return batch_fail(e, ls);
+        }
+        err = cudaMemcpyAsync(b.tok, drawn, nb, cudaMemcpyDeviceToDevice, st);
+    }
+    if (err == cudaSuccess) err = cudaMemcpyAsync(tok.data(), b.f_tok, n * 4, cudaMemcpyDeviceToHost, st);
+    if (err == cudaSuccess && logprobs_out) err = cudaMemcpyAsync(lp.data(), b.f_lp, n * 4, cudaMemcpyDeviceToHost, st);
+    if (err != cudaSuccess) {
+        (void)cudaGetLastError();
+        (void)cudaStreamSynchronize(st);
+        return batch_fail(e, LF_ERR_CUDA);
+    }
+    const lf_status r = batch_finish(e, b);
+    if (r != LF_OK) return r;
+    b.pos += n_steps;
+    bool drawn = true;
+    for (int i = 0; i < B; ++i)
+        for (int t = 0; t < n_steps; ++t) {
+            tokens_out[(size_t)i * n_steps + t] = tok[(size_t)t * B + i];
+            drawn &= tok[(size_t)t * B + i] >= 0;
+            if (logprobs_out) logprobs_out[(size_t)i * n_steps + t] = lp[(size_t)t * B + i];
+        }
+    return drawn ? LF_OK : batch_fail(e, LF_ERR_INVALID_ARG);  // the last step's logits held a NaN
 }

@@ -383,6 +383,17 @@ lf_status lf_matmul_f16_async(const void *a_device, const void *b_device, float 
  * of head_dim, more than 8 query heads per KV head); LF_ERR_OOM. */
 lf_status lf_batch_begin(lf_engine *e, int n_batch);
 lf_status lf_batch_end(lf_engine *e);
+
+/* lf_batch_begin with the positions before the branch kept once: the samples
+ * name the same pages of a paged cache up to there and own pages of it from
+ * there on, so the batch state holds (and each step reads) the prefix once
+ * instead of n_batch times (lf_kv_append_paged and lf_attn_paged_shared run
+ * the layers' attention).  The same function as lf_batch_begin's batch up to
+ * rounding: the rotated queries and the softmax weights enter the tensor
+ * cores as FP16.  Pays with a long prefix and several samples; a short batch
+ * is a little slower.  The other batch calls serve both kinds.  Errors as
+ * lf_batch_begin. */
+lf_status lf_batch_begin_shared(lf_engine *e, int n_batch);
 /* *n_batch and *position of the current batch (0 and 0 when there is none). */
 lf_status lf_batch_info(const lf_engine *e, int *n_batch, int *position);
 
@@ -406,6 +417,21 @@ lf_status lf_batch_step(lf_engine *e, const int32_t *tokens, float *logits, int3
  * LF_ERR_UNSUPPORTED for a vocabulary above 51200. */
 lf_status lf_batch_generate(lf_engine *e, const int32_t *first_tokens, int n_steps, float temperature, float top_p,
                             uint64_t seed, int32_t *tokens_out);
+
+/* n_steps steps of every sample with the draw of lf_sample_filtered: per
+ * sample a temperature, top_k, top_p and min_p (host arrays of n_batch; NULL:
+ * 1, all, 1 and 0), and u (host, n_batch x n_steps fp32 in [0, 1), row b =
+ * sample b) one number per draw, so a caller that keeps its own random
+ * numbers can repeat or vary a single sample.  tokens_out (host, n_batch x
+ * n_steps int32) receives the drawn tokens, logprobs_out (the same shape,
+ * fp32, nullable) the log of each one's share of what was kept.  Synchronous;
+ * advances the batch position by n_steps.  Errors as lf_batch_step, plus
+ * LF_ERR_INVALID_ARG for parameters outside the ranges of lf_sample_filtered
+ * (nothing run) and, ending the batch, for logits that allow no draw (NaN);
+ * LF_ERR_UNSUPPORTED for a vocabulary above 262144. */
+lf_status lf_batch_generate_filtered(lf_engine *e, const int32_t *first_tokens, int n_steps, const float *temperature,
+                                     const int32_t *top_k, const float *top_p, const float *min_p, const float *u,
+                                     int32_t *tokens_out, float *logprobs_out);
 
 /* The tensor-core GEMV of the batched decode, exported for tests:
  * y[b][r] = sum_k w[r][k] * x[b][k] for b < batch (1..16), r < n, with w
