@@ -108,7 +108,8 @@ class Walker {
 
     // The plan from the lengths: the common range and the own tiles before
     // each sequence.  Every warp works it out for itself, so that only the
-    // table waits for a barrier; CTA 0 leaves it for the join.
+    // table waits for a barrier; CTA 0 leaves the common range for
+    // the join.
     __device__ void plan() {
         const int n = a.kv.n_seqs;
         com = Common(a, __reduce_max_sync(0xffffffffu, latest_start(a, lane)));
@@ -127,21 +128,15 @@ class Walker {
                 const int y = __shfl_up_sync(0xffffffffu, inc, o);
                 if (lane >= o) inc += y;
             }
-            if (warp == 0 && b < n) {
-                cum[b] = at + inc - t;
-                if (blockIdx.x == 0) a.plan[kPlanWords + b] = at + inc - t;
-            }
+            if (warp == 0 && b < n) cum[b] = at + inc - t;
             at += __shfl_sync(0xffffffffu, inc, 31);
         }
         if (tid == 0) cum[n] = at;
-        const int all_c = a.kv.n_kv * a.row_tiles * tiles_c;
-        common_total = a.tc ? 0 : all_c;
+        common_total = a.tc ? 0 : a.kv.n_kv * a.row_tiles * tiles_c;
         total = common_total + a.kv.n_kv * at;
         if (blockIdx.x == 0 && tid == 0) {
-            a.plan[0] = tiles_c;
-            a.plan[1] = total;
-            a.plan[2] = a.tc ? all_c : total;
-            a.plan[kPlanWords + n] = at;
+            a.plan[0] = com.lo;
+            a.plan[1] = com.hi;
         }
         __syncthreads();
     }
@@ -173,6 +168,11 @@ class Walker {
             asm volatile("cp.async.wait_group %0;" ::"n"(L::STAGES - 1) : "memory");
             __syncthreads();
             const bool last = i + 1 == n || work.tile + 1 == work.tiles;
+            if (tid == 0) {  // for the join
+                int2 *sp = a.span + (work.common ? work.item : a.items_c + work.item);
+                if (work.tile == 0) sp->x = blockIdx.x;
+                if (work.tile + 1 == work.tiles) sp->y = blockIdx.x;
+            }
             if (work.common) {
                 const int rows = min(PA_ROWS, a.kv.n_seqs * a.group - work.rt * PA_ROWS);
                 if (rows <= 16)
@@ -231,10 +231,10 @@ class Walker {
         Place p;
         if (u < common_total) {
             p.common = true;
-            p.item = u / tiles_c;
+            p.item = quotient(u, tiles_c);
             p.tile = u - p.item * tiles_c;
             p.tiles = tiles_c;
-            p.h = p.item / a.row_tiles;
+            p.h = quotient(p.item, a.row_tiles);
             p.rt = p.item - p.h * a.row_tiles;
             p.b = 0;
         } else {
@@ -251,7 +251,7 @@ class Walker {
             p.b = lo;
             p.tiles = cum[lo + 1] - cum[lo];
             const int r = v - a.kv.n_kv * cum[lo];
-            p.h = r / p.tiles;
+            p.h = quotient(r, p.tiles);
             p.tile = r - p.h * p.tiles;
             p.rt = 0;
             p.item = p.b * a.kv.n_kv + p.h;
@@ -533,28 +533,23 @@ template <typename T, int DH>
 __global__ void __launch_bounds__(PA_MERGE_THREADS) paged_attn_join(const AttnArgs a) {
     constexpr int V = DH / 32;  // values per lane
     constexpr int U = 8;        // partials in flight
+    const int x = (int)((blockIdx.x * (long long)PA_MERGE_THREADS + threadIdx.x) >> 5), lane = threadIdx.x & 31;
+    const int b = x / a.n_q, hq = x - b * a.n_q, h = hq / a.group, r = hq - h * a.group;
+    const int row = b * a.group + r, item = h * a.row_tiles + row / a.rows_c, own = b * a.kv.n_kv + h;
+    const bool active = x < a.kv.n_seqs * a.n_q;
     pdl_wait();
     pdl_trigger();
-    const int x = (int)((blockIdx.x * (long long)PA_MERGE_THREADS + threadIdx.x) >> 5), lane = threadIdx.x & 31;
-    if (x >= a.kv.n_seqs * a.n_q) return;
-    const int b = x / a.n_q, hq = x % a.n_q, h = hq / a.group, r = hq % a.group;
-    const int tiles_c = a.plan[0], total = a.plan[1], t0 = a.plan[kPlanWords + b];
-    const int tiles = a.plan[kPlanWords + b + 1] - t0, common_total = a.tc ? 0 : a.kv.n_kv * a.row_tiles * tiles_c;
-    const Shares sh(total, a.grid), sh_c(a.plan[2], a.grid_c);
+    if (!active) return;
+    const int2 at_c = a.span[item], at_o = a.span[a.items_c + own];  // (of earlier calls where this one has no tiles)
+    Common com(a, -1);
+    com.lo = a.plan[0];
+    com.hi = a.plan[1];
+    const Span s = span_of(a, b);
     // partial k < n_c of the common item, then n_o of the own one: their rows in the workspace
-    long long row_c = 0, row_o = 0;
-    int n_c = 0, n_o = 0;
-    if (span_of(a, b).member && tiles_c > 0) {
-        const int row = b * a.group + r, item = h * a.row_tiles + row / a.rows_c, u = item * tiles_c;
-        const int c0 = sh_c.owner(u);
-        n_c = sh_c.owner(u + tiles_c - 1) - c0 + 1;
-        row_c = (long long)(item + c0) * a.rows_c + row % a.rows_c;
-    }
-    if (tiles > 0) {
-        const int u = common_total + a.kv.n_kv * t0 + h * tiles, c0 = sh.owner(u);
-        n_o = sh.owner(u + tiles - 1) - c0 + 1;
-        row_o = (long long)a.slots_c * a.rows_c + (long long)(b * a.kv.n_kv + h + c0) * a.group + r;
-    }
+    const int n_c = s.member && com.lo < com.hi ? at_c.y - at_c.x + 1 : 0;
+    const int n_o = own_count(s, com) > 0 ? at_o.y - at_o.x + 1 : 0;
+    const long long row_c = (long long)(item + at_c.x) * a.rows_c + row % a.rows_c;
+    const long long row_o = (long long)a.slots_c * a.rows_c + (long long)(own + at_o.x) * a.group + r;
     auto row_of = [&](int k) {
         return k < n_c ? row_c + (long long)k * a.rows_c : row_o + (long long)(k - n_c) * a.group;
     };
@@ -641,17 +636,18 @@ void common_shape(AttnArgs &a, bool tc, int n_sm) {
     a.grid = n_sm * PA_CTAS_PER_SM;
     a.grid_c = tc ? n_sm : a.grid;
     a.page_align = tc ? 1 << a.kv.ps_log2 : 1;
-    a.slots_c = a.kv.n_kv * a.row_tiles + a.grid_c;
+    a.items_c = a.kv.n_kv * a.row_tiles;
+    a.slots_c = a.items_c + a.grid_c;
 }
 
 struct WsLayout {
-    size_t plan, ml, o, bytes;
+    size_t span, ml, o, bytes;
 };
 WsLayout ws_layout(const AttnArgs &a) {
     WsLayout w;
     const size_t rows = (size_t)a.slots_c * a.rows_c + ((size_t)a.kv.n_seqs * a.kv.n_kv + a.grid) * a.group;
-    w.plan = 0;
-    w.ml = al256((size_t)(kPlanWords + a.kv.n_seqs + 1) * sizeof(int));
+    w.span = 256;  // behind the plan
+    w.ml = w.span + al256(((size_t)a.items_c + (size_t)a.kv.n_seqs * a.kv.n_kv) * sizeof(int2));
     w.o = w.ml + al256(rows * sizeof(float2));
     w.bytes = w.o + rows * a.kv.head_dim * sizeof(float);
     return w;
@@ -762,7 +758,8 @@ extern "C" lf_status lf_attn_paged_shared(const lf_paged_kv *kv, const void *q_d
     lf::common_shape(a, lf::tc_possible(a.kv) && lf::tc_pays(a), n_sm);
     const lf::WsLayout w = lf::ws_layout(a);
     uint8_t *ws = static_cast<uint8_t *>(workspace_device);
-    a.plan = reinterpret_cast<int *>(ws + w.plan);
+    a.plan = reinterpret_cast<int *>(ws);
+    a.span = reinterpret_cast<int2 *>(ws + w.span);
     a.part_ml = reinterpret_cast<float2 *>(ws + w.ml);
     a.part_o = reinterpret_cast<float *>(ws + w.o);
     a.q = q_device;

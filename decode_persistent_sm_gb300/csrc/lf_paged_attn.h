@@ -17,13 +17,15 @@ struct AttnArgs {
     const int32_t *lens;
     int max_len, shared, window;
     float scale_log2;  // scale * log2 e
-    // common items: rows_c rows of a KV head (row = sequence * group + head), row_tiles of them, tiles of keys_c keys,
+    // common items: rows_c rows of a KV head (row = sequence * group + head), row_tiles of them, items_c = n_kv * row_tiles
+    // items, tiles of keys_c keys,
     // shares of the first grid_c CTAs; page_align: 1, or the page size when the common range is cut to whole pages
-    int rows_c, row_tiles, keys_c, grid_c, page_align;
+    int rows_c, row_tiles, items_c, keys_c, grid_c, page_align;
     bool tc;           // the common items run in paged_attn_tc_kernel, not in the list below
     int grid;          // CTAs that share the list
     // workspace
-    int *plan;         // kPlanWords, then the own tiles before each sequence [n_seqs + 1]
+    int *plan;         // the common range [lo, hi)
+    int2 *span;        // first and last CTA of each item: common items [n_kv][row_tiles], then own ones [n_seqs][n_kv]
     // partials, common items' slots first: slots_c = n_kv * row_tiles + grid_c of rows_c rows, then n_seqs * n_kv + grid
     // of `group` rows
     int slots_c;
@@ -32,8 +34,6 @@ struct AttnArgs {
     uint32_t *err;
 };
 
-// Head of the plan: tiles per common item, tiles of the list, tiles of all common items, unused.
-constexpr int kPlanWords = 4;
 
 // What one sequence sees.
 struct Span {
@@ -72,20 +72,26 @@ __device__ __forceinline__ int own_count(const Span &s, const Common &c) {
     return s.member ? max(0, c.lo - s.lo) + (s.len - c.hi) : s.len - s.lo;
 }
 
+// u / d for u >= 0, d > 0.  The compiler's integer division is a call of some
+// hundred cycles, which the start of a short kernel feels; below 2^20 a
+// reciprocal is off by less than one.
+__device__ __forceinline__ int quotient(int u, int d) {
+    if (u >= 1 << 20) return u / d;
+    int q = (int)((float)u * __fdividef(1.f, (float)d));
+    const int r = u - q * d;
+    q += (r >= d) - (r < 0);
+    return q;
+}
+
 // The list's shares: the first total % ctas CTAs take one tile more.  No share
 // is empty (a list shorter than the grid goes to its first tiles' CTAs).
 struct Shares {
     int q, r;
     __device__ Shares(int total, int grid) {
-        const int ctas = min(total, grid);
-        q = ctas ? total / ctas : 0;
-        r = ctas ? total - q * ctas : 0;
+        q = total < grid ? 1 : quotient(total, grid);
+        r = total < grid ? 0 : total - q * grid;
     }
     __device__ int begin(int c) const { return c * q + min(c, r); }
-    __device__ int owner(int u) const {
-        const int head = r * (q + 1);
-        return u < head ? u / (q + 1) : r + (u - head) / q;
-    }
 };
 
 template <typename T>

@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(T_THREADS, 1)
     const Shares sh(total, gridDim.x);
     if ((int)blockIdx.x >= min(total, (int)gridDim.x)) return;
     const int u0 = sh.begin(blockIdx.x), n = sh.begin(blockIdx.x + 1) - u0;
-    const int item0 = u0 / tiles, tile0 = u0 - item0 * tiles;
+    const int item0 = quotient(u0, tiles), tile0 = u0 - item0 * tiles;
     const int all_rows = a.kv.n_seqs * a.group;
     // row tiles in use of an item
     auto row_tiles_of = [&](int item) {
@@ -303,6 +303,10 @@ __global__ void __launch_bounds__(T_THREADS, 1)
         bool ok = true;
         while (ok && left > 0) {
             const int count = min(left, tiles - tile);  // tiles of this item in this CTA
+            if (x == 0 && row == 0) {  // for the join
+                if (tile == 0) a.span[item].x = blockIdx.x;
+                if (tile + count == tiles) a.span[item].y = blockIdx.x;
+            }
             if (x < row_tiles_of(item)) {
                 const int rt = item % a.row_tiles, h = item / a.row_tiles;
                 const int at = rt * kTcRows + x * 128 + row;  // (sequence, head) row of the KV head
