@@ -396,21 +396,29 @@ struct Row {
         return bin;
     }
 
-    // Collects the logits for which take(value) holds: up to F_LIST of them in
+    // Collects the logits from `floor` on for which take(value) holds: up to F_LIST of them in
     // S.all of every CTA.  Returns how many there are in the cluster (above
     // F_LIST: not collected) and their smallest and largest keys.
     template <class Take>
-    __device__ int collect(Take take, uint32_t &kmin, uint32_t &kmax) {
+    __device__ int collect(float floor, Take take, uint32_t &kmin, uint32_t &kmax) {
         kmin = 0xffffffffu, kmax = 0;
-        each([&](float x) {
-            if (take(x)) {
+        auto one = [&](float x) {
+            if (x >= floor && take(x)) {
                 const uint32_t k = key_of(x);
                 kmin = min(kmin, k);
                 kmax = max(kmax, k);
                 const int at = atomicAdd(&S.n_cand, 1);
                 if (at < F_LIST) S.cand[at] = x;
             }
-        });
+        };
+        for (int i = tid; i < n4; i += NT) {
+            const float4 x = z4[i];
+            if (!(fmaxf(fmaxf(x.x, x.y), fmaxf(x.z, x.w)) >= floor)) continue;
+            one(x.x);
+            one(x.y);
+            one(x.z);
+            one(x.w);
+        }
         block_minmax(kmin, kmax);
         // the lists and what each CTA says of its own are read from its shared memory
         if (tid == 0) S.said = Gather{(u64)S.n_cand, kmin, kmax};
@@ -589,7 +597,7 @@ struct Row {
                 each([&](float x) { hist_add(S, step(x), 1ull); });
                 last = find_bin<C>(0ull, target, -1.f, before);
             }
-            const int m = collect([&](float x) { return x >= least && (last == F_BINS || step(x) <= last); }, kmin, kmax);
+            const int m = collect(least, [&](float x) { return last == F_BINS || step(x) <= last; }, kmin, kmax);
             if (m <= F_LIST) {  // the list holds the whole top-k set
                 floor = of_key(border<false>(m, -INFINITY, 0ull, target, -1.f, kmin, kmax));
                 if (top_p < 1.f) floor = fmaxf(floor, of_key(border<true>(m, floor, 0ull, 0ull, top_p, kmin, kmax)));
@@ -606,7 +614,7 @@ struct Row {
             });
             u64 target = 0, before = 0;
             const int at = find_bin<C>(0ull, target, top_p, before);
-            const int m = collect([&](float x) { return x >= floor && step(x) == at; }, kmin, kmax);
+            const int m = collect(floor, [&](float x) { return step(x) == at; }, kmin, kmax);
             uint32_t key = kmax;
             if (kmin != kmax)
                 key = m <= F_LIST ? border<true>(m, floor, before, target, -1.f, kmin, kmax)
@@ -627,18 +635,23 @@ struct Row {
     }
 };
 
+// The larger, NaN if either is.
+__device__ __forceinline__ float max_or_nan(float a, float b) {
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
+}
+
 // Reads n logits as fp32 into shared memory (16-byte loads where the row is
-// aligned for them); returns the thread's largest key, and through nan and kmin
-// whether it saw a NaN and its smallest key above -inf.
+// aligned for them); returns the thread's largest (NaN if there is one, -inf if
+// it read none), and through least its smallest above -inf.
 template <typename T, int NT>
-__device__ __forceinline__ uint32_t load_row(const T *src, int n, float *z, bool &nan, uint32_t &kmin) {
+__device__ __forceinline__ float load_row(const T *src, int n, float *z, float &least) {
     constexpr int V = 16 / sizeof(T);
-    uint32_t kmax = 0;
+    float most = -INFINITY;
     auto take = [&](float x) {
-        nan |= x != x;
-        const uint32_t k = key_of(x);
-        kmax = max(kmax, k);
-        if (x > -INFINITY) kmin = min(kmin, k);
+        most = max_or_nan(most, x);
+        if (x > -INFINITY) least = fminf(least, x);
     };
     int done = 0;
     if ((reinterpret_cast<uintptr_t>(src) & 15u) == 0) {
@@ -666,7 +679,7 @@ __device__ __forceinline__ uint32_t load_row(const T *src, int n, float *z, bool
         take(x);
     }
     if (threadIdx.x < ((4 - n % 4) & 3)) z[n + threadIdx.x] = -INFINITY;
-    return kmax;
+    return most;
 }
 
 template <int NT, int C>
@@ -701,15 +714,14 @@ __global__ void __launch_bounds__(NT, 1024 / NT) sample_filtered_kernel(const Fi
         return;
     }
     const long long at = (long long)row * a.ld + i0;
-    uint32_t kmin = 0xffffffffu;
-    bool nan = false;
-    const uint32_t own = a.dtype == LF_F32 ? load_row<float, NT>(static_cast<const float *>(a.logits) + at, n, z, nan, kmin)
-                         : a.dtype == LF_F16
-                             ? load_row<__half, NT>(static_cast<const __half *>(a.logits) + at, n, z, nan, kmin)
-                             : load_row<__nv_bfloat16, NT>(static_cast<const __nv_bfloat16 *>(a.logits) + at, n, z, nan, kmin);
-    uint32_t kmax = own;
+    float least = INFINITY;
+    const float most = a.dtype == LF_F32   ? load_row<float, NT>(static_cast<const float *>(a.logits) + at, n, z, least)
+                       : a.dtype == LF_F16 ? load_row<__half, NT>(static_cast<const __half *>(a.logits) + at, n, z, least)
+                                           : load_row<__nv_bfloat16, NT>(static_cast<const __nv_bfloat16 *>(a.logits) + at, n, z, least);
+    bool nan = __syncthreads_or(most != most);
+    const uint32_t own = key_of(most);
+    uint32_t kmax = own, kmin = key_of(least);  // (least +inf: no logit above -inf, or only infinite ones)
     const int k = top_k > 0 && top_k < a.vocab ? top_k : 0;
-    nan = __syncthreads_or(nan);
     R.block_minmax(kmin, kmax);
     uint32_t bound = k > 1 && t > 0.f ? R.group_bound(own, k) : 0u;
     const Gather *got = R.exchange(Gather{(u64)bound << 32 | (nan ? 1u : 0u), kmin, kmax});
