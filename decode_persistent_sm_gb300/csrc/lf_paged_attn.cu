@@ -455,6 +455,7 @@ class Walker {
                                          : (long long)a.slots_c * a.rows_c + (long long)(p.item + blockIdx.x) * a.group;
         float *dst = a.part_o + slot0 * DH;
         float2 *dst_ml = a.part_ml + slot0;
+        const uint64_t keep = policy_evict_last();  // the keys and values that stream by shall not push it out of L2
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
             l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
@@ -468,7 +469,7 @@ class Walker {
                 float *d = dst + row * DH;
 #pragma unroll
                 for (int i = 0; i < DH / 8; ++i)
-                    *reinterpret_cast<float2 *>(d + 8 * i + 2 * t) = make_float2(o[i][2 * r], o[i][2 * r + 1]);
+                    st_hint(reinterpret_cast<float2 *>(d + 8 * i + 2 * t), make_float2(o[i][2 * r], o[i][2 * r + 1]), keep);
                 if (t == 0) dst_ml[row] = make_float2(m[r], l[r]);
             }
         } else {
@@ -504,7 +505,7 @@ class Walker {
                     sl += f * w.y;
                 }
                 float *d = dst + row * DH;
-                *reinterpret_cast<float2 *>(d + c) = make_float2(sx, sy);
+                st_hint(reinterpret_cast<float2 *>(d + c), make_float2(sx, sy), keep);
                 if (c == 0) dst_ml[row] = make_float2(mx, sl);
             }
         }

@@ -401,6 +401,7 @@ __global__ void __launch_bounds__(T_THREADS, 1)
                     tc_fence_after();
                     const long long slot = (long long)(item + blockIdx.x) * kTcRows + x * 128 + row;
                     float *dst = a.part_o + slot * DH;
+                    const uint64_t keep = policy_evict_last();
 #pragma unroll 1
                     for (int c0 = 0; c0 < DH; c0 += 32) {
                         float v[32];
@@ -408,7 +409,7 @@ __global__ void __launch_bounds__(T_THREADS, 1)
                         if (at < all_rows) {
 #pragma unroll
                             for (int i = 0; i < 32; i += 4)
-                                *reinterpret_cast<float4 *>(dst + c0 + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                                st_hint(reinterpret_cast<float4 *>(dst + c0 + i), make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]), keep);
                         }
                     }
                     if (at < all_rows) a.part_ml[slot] = make_float2(m2, l);

@@ -106,6 +106,10 @@ __device__ __forceinline__ void st_hint(float4 *dst, float4 v, uint64_t policy) 
                  "f"(v.z), "f"(v.w), "l"(policy)
                  : "memory");
 }
+__device__ __forceinline__ void st_hint(float2 *dst, float2 v, uint64_t policy) {
+    asm volatile("st.global.L2::cache_hint.v2.f32 [%0], {%1, %2}, %3;" ::"l"(dst), "f"(v.x), "f"(v.y), "l"(policy)
+                 : "memory");
+}
 __device__ __forceinline__ void st_hint(float *dst, float v, uint64_t policy) {
     asm volatile("st.global.L2::cache_hint.f32 [%0], %1, %2;" ::"l"(dst), "f"(v), "l"(policy) : "memory");
 }
