@@ -518,13 +518,13 @@ __global__ void __launch_bounds__(PA_THREADS, PA_CTAS_PER_SM) paged_attn_kernel(
     Walker<T, DH> w(a, pa_smem);
     // With the tensor-core kernel in front, which triggers this one after its own
     // wait, all that is read here is already there and what is written is apart
-    // from that kernel's partials: this one runs beside it and waits at its end,
-    // so that the join behind it finds both done.
+    // from that kernel's partials: this one runs beside it, and its last CTA waits
+    // at its end, so that the join behind it finds both done.
     if (!a.tc) pdl_wait();
     pdl_trigger();
     w.plan();
     w.run();
-    if (a.tc) pdl_wait();
+    if (a.tc && blockIdx.x == gridDim.x - 1) pdl_wait();
 }
 
 
