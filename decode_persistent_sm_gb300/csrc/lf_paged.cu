@@ -18,7 +18,7 @@
 namespace lf {
 namespace {
 
-constexpr int kAppendThreads = 256;
+constexpr int kAppendThreads = 128;
 constexpr long long kAppendManyUnits = 1 << 18;
 struct AppendArgs {
     PagedView kv;
@@ -100,7 +100,6 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendA
     pdl_trigger();
     const int seq = a.seq ? a.seq[t] : t;
     const int p = a.pos[t];
-    if (seq < 0) return;  // padding
     Eight<TI> lo[U], hi[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -117,6 +116,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendA
             hi[u].load(src + half + c0);
         }
     }
+    if (seq < 0) return;  // padding
     int page = -1;
     if (seq < a.kv.n_seqs && p >= 0 && (p >> a.kv.ps_log2) < a.kv.max_pages && (!a.rope || p < a.rope_len))
         page = a.kv.table[(long long)seq * a.kv.max_pages + (p >> a.kv.ps_log2)];

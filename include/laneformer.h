@@ -493,7 +493,7 @@ typedef struct {
  *   for position p; NULL appends without a rotation.
  * Pointers and row strides are multiples of 16 bytes.  The rotation is
  * computed in fp32 and rounded once.  A token whose sequence is negative is
- * padding: nothing is read for it and nothing is written.  A sequence, position
+ * padding: nothing is written for it.  A sequence, position
  * or page outside the cache (or a position outside rope_device) skips the
  * token and sets *err_device (DEVICE word, cleared by the caller) to 1.  The
  * tokens of one call name different slots: of two that name the same slot
