@@ -33,6 +33,7 @@
 #include <climits>
 #include <cmath>
 #include <mutex>
+#include <new>
 #include <vector>
 
 #include "laneformer.h"
@@ -812,7 +813,13 @@ lf_status batch_begin(lf_engine *e, int n_batch, bool shared) {
 
 extern "C" lf_status lf_batch_begin(lf_engine *e, int n_batch) { return batch_begin(e, n_batch, false); }
 
-extern "C" lf_status lf_batch_begin_shared(lf_engine *e, int n_batch) { return batch_begin(e, n_batch, true); }
+extern "C" lf_status lf_batch_begin_shared(lf_engine *e, int n_batch) {
+    try {
+        return batch_begin(e, n_batch, true);
+    } catch (const std::bad_alloc &) {
+        return LF_ERR_OOM;
+    }
+}
 
 extern "C" lf_status lf_batch_end(lf_engine *e) {
     if (!e) return LF_ERR_INVALID_ARG;
@@ -914,8 +921,15 @@ extern "C" lf_status lf_batch_generate_filtered(lf_engine *e, const int32_t *fir
     const size_t n = (size_t)B * n_steps, nb = (size_t)B * 4;
     for (size_t i = 0; i < n; ++i)
         if (!(u[i] >= 0.f && u[i] < 1.f)) return LF_ERR_INVALID_ARG;
-    std::vector<float> rows(n), lp(logprobs_out ? n : 0);  // step by step on the device, sample by sample for the caller
-    std::vector<int32_t> tok(n);
+    std::vector<float> rows, lp;  // step by step on the device, sample by sample for the caller
+    std::vector<int32_t> tok;
+    try {
+        rows.resize(n);
+        lp.resize(logprobs_out ? n : 0);
+        tok.resize(n);
+    } catch (const std::bad_alloc &) {
+        return LF_ERR_OOM;
+    }
     for (int i = 0; i < B; ++i)
         for (int t = 0; t < n_steps; ++t) rows[(size_t)t * B + i] = u[(size_t)i * n_steps + t];
     cudaStream_t st = e->stream;

@@ -12,7 +12,11 @@
 // takes U heads of it, so its cos and sin are read once and U units' loads are
 // in flight together, started before the position, the table entry and the
 // rotation's row (three loads that wait for each other) are looked up.  The
-// bound is HBM: every value is read and written once.
+// bound is HBM: every value is read and written once.  Measured: 3584 tokens of
+// 32 + 2 x 16 heads of 128, FP16: 22.5 us, 5.3 TB/s (79 % of the copy rate;
+// 35.9 us with one unit a thread loaded after the page lookup); 8191 tokens of 24
+// + 2 x 8 heads of 64, BF16: 16.6 us, 5.2 TB/s; 16 tokens: 5.2 us, the time
+// of the call itself.
 #include "lf_paged.h"
 
 namespace lf {
@@ -174,8 +178,9 @@ bool launch_units(const AppendArgs &a, cudaStream_t st) {
 
 template <typename TI, typename TO>
 bool launch_append(const AppendArgs &a, cudaStream_t st) {
-    // four units a thread once that still leaves a few blocks per SM, one unit
-    // for the few tokens of a decode step (a shorter chain in each thread)
+    // four units a thread once that still leaves a few blocks per SM (3584 tokens: 4
+    // 22.5 us, 2 22.1, 8 22.3; 8191 of head_dim 64: 16.6, 18.1, 18.7), one unit for
+    // the few tokens of a decode step (a shorter chain in each thread)
     const long long units = (long long)a.n_tokens * (a.n_q + 2 * a.kv.n_kv) * (a.kv.head_dim / 16);
     return units >= kAppendManyUnits ? launch_units<TI, TO, 4>(a, st) : launch_units<TI, TO, 1>(a, st);
 }

@@ -19,6 +19,12 @@
 // tensor, which reads as zeros, so that no value that is not to be seen enters
 // a product.
 //
+// Measured: 64 sequences x 8 heads per KV head (512 rows), 8 KV heads of 128, 16384
+// common positions, BF16: 39 us, 880 TFLOP/s (46 % of the measured dense rate; the
+// tensor pipe is active 36 % of the time: a row tile's softmax, 128 values a thread,
+// takes longer than the other's two products).  The whole call 78.6 us, of which
+// the sequences' own positions take 31 (142 MB); on warp-level MMAs alone 161.
+//
 // Every wait is bounded; a CTA that ran out of time flags it, lets its copies
 // and products finish (bounded), frees its TMEM and exits.
 #include <cuda.h>

@@ -522,7 +522,7 @@ lf_status lf_kv_append_paged(const lf_paged_kv *kv, const void *q_in, const void
  *   lens_device: DEVICE int32 [n_seqs]; a sequence of length 0 gets zeros and
  *   lse -inf;
  *   max_len: upper bound of the lengths (sizes nothing but the check of them);
- *   scale: finite, above 0;
+ *   scale: above 0, scale * log2(e) finite;
  *   workspace_device: DEVICE scratch of at least
  *   lf_attn_paged_shared_workspace bytes, 256-byte aligned; it needs no
  *   initial content, holds nothing between calls, and belongs to one call (or
@@ -531,7 +531,8 @@ lf_status lf_kv_append_paged(const lf_paged_kv *kv, const void *q_in, const void
  * second product rounded to the cache's type.  The result does not depend on
  * timing (sums in a fixed order), only on the arguments and the SM count.  A
  * length outside [0, max_len] (taken as 0) or a page outside the cache (the
- * result is then undefined) sets *err_device to 1.
+ * result is then undefined) sets *err_device (DEVICE word, cleared by the
+ * caller) to 1, a device-side wait that ran out (2 s) to 2.
  * LF_ERR_INVALID_ARG for bad sizes, pointers, strides or types, shared_len or
  * max_len above max_pages * page_size, or a workspace too small;
  * LF_ERR_UNSUPPORTED for head_dim other than 32, 64 or 128, more than 16
@@ -543,7 +544,8 @@ lf_status lf_attn_paged_shared(const lf_paged_kv *kv, const void *q_device, int6
                                size_t workspace_bytes, uint32_t *err_device, void *cuda_stream);
 
 /* Workspace bytes of lf_attn_paged_shared for this cache on the current
- * device, whatever the lengths; 0 where that call would refuse the sizes. */
+ * device, whatever the lengths; 0 where that call would refuse the sizes (or
+ * there is no device). */
 size_t lf_attn_paged_shared_workspace(const lf_paged_kv *kv, int n_q_heads);
 
 /* One draw per row of logits under temperature, top-k, top-p and min-p, from

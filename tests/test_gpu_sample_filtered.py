@@ -98,6 +98,7 @@ def test_edges_of_u():
     z = np.log(np.array([[0.25, 0.25, 0.25, 0.25]], dtype=np.float32)).repeat(6, 0)
     tok = check(z, "f32", u=[0.0, 0.25, 0.5, 0.75, 1 - 2.0 ** -24, 0.24999])
     assert list(tok) == [0, 1, 2, 3, 3, 0]
+    assert list(check(z, "f32", t=[-0.0, 1, 1, 1, 1, 1], mp=-0.0, u=[-0.0, -0.0, 1e-45, 1e-38, 2.0 ** -149, 1e-20])) == [0] * 6
 
 
 def test_equal_logits():
@@ -127,6 +128,10 @@ def test_masked_logits():
     z[g.random(z.shape) < 0.95] = -np.inf
     z[:, 4321] = 0.5
     check(z, "f32", **params(g, 40))
+    few = np.full((24, 40000), -np.inf, dtype=np.float32)  # fewer tokens than top_k, all in one part of the row or spread
+    few[:12, 39000:39030] = g.standard_normal((12, 30))
+    few[12:, ::1300] = g.standard_normal((12, 31))
+    check(few, "f32", t=0.8, k=np.tile([5, 30, 31, 50, 400, 39999], 4), p=np.tile([1.0, 0.9, 0.6], 8), u=g.random(24, dtype=np.float32))
     only = np.full((3, 20000), -np.inf, dtype=np.float32)
     only[0, 0] = only[1, 19999] = only[2, 777] = -5.0
     assert list(check(only, "f32", t=[1.0, 0.0, 0.7], k=[50, 0, 2], p=0.9, u=0.999)) == [0, 19999, 777]

@@ -90,7 +90,8 @@ def test_append_of_nothing_is_accepted(lib):
                                  dict(q=A + 8), dict(out=A + 4), dict(lse=A + 2), dict(lens=A + 1), dict(ws=A + 128),
                                  dict(ldq=504), dict(ldo=504), dict(ldq=516), dict(ldo=516), dict(max_len=-1),
                                  dict(max_len=81), dict(shared=-1), dict(shared=81), dict(max_len=10), dict(window=-1),
-                                 dict(scale=0.0), dict(scale=-1.0), dict(scale=float("inf")), dict(scale=float("nan"))])
+                                 dict(scale=0.0), dict(scale=-1.0), dict(scale=float("inf")), dict(scale=float("nan")),
+                                 dict(scale=3e38)])
 def test_attention_refusals(lib, bad):
     assert attend(lib, **bad) == INVALID
 
