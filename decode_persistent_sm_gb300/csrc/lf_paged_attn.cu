@@ -19,7 +19,9 @@
 // partial (unnormalised o, max, sum) per item it touches: slot item + CTA,
 // which is unique because both only grow along the list.  A second kernel,
 // launched to overlap the first one's end, joins each row's partials in list
-// order.
+// order.  A call of few keys does without the list: a cluster of up to 8 CTAs
+// per (sequence, KV head) reads all that the sequence sees and joins through
+// distributed shared memory, in one launch.
 //
 // One tile: S = Q K^T and O += P V on warp-level MMAs (m16n8k16, fp32
 // accumulators), softmax statistics in registers.  The four warps take 16-row
@@ -30,17 +32,21 @@
 //
 // Measured (us per call, both launches; in brackets the bytes it cannot do
 // without at the copy rate): 8 sequences x 512 common + 40 .. 130 own positions, 32 / 16
-// heads of 128: 10.0 (1.5); 16 x 3584 + 100 .. 512: 24.0 (10.4); 24 windowed
-// sequences, 24 / 8 heads of 64: 15.3 (2.9); 2 short ones: 6.5, the time of two
-// launches.  Between 2 and 3 us go to working out the list (lengths, then page
+// heads of 128: 9.8 (1.5); 16 x 3584 + 100 .. 512: 24.0 (10.4); 24 windowed
+// sequences, 24 / 8 heads of 64: 15.5 (2.9); 2 short ones, by the direct kernel:
+// 4.7 (6.5 by the list), the time of the call.  Between 2 and 3 us go to working out the list (lengths, then page
 // numbers, then the first keys: three trips to L2), as much to the join; in
 // between the keys and values stream at 5.7 TB/s.
+#include <cooperative_groups.h>
+
 #include <algorithm>
 #include <climits>
 #include <type_traits>
 
 #include "lf_paged_attn.h"
 #include "lf_ptx.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace lf {
 namespace {
@@ -99,7 +105,11 @@ struct Smem {
     static constexpr int BYTES = STAGES * (2 * TILE + Q) + ML + CUM;
     // the join of the warps' rows uses the stage of the item's last tile
     static_assert(4 * 16 * DH * 4 <= 2 * TILE, "the joined rows fit the stage");
+    static_assert(PA_MAX_GROUP * DH * 4 <= STAGES * Q, "a cluster's partial fits the query rows' buffers");
 };
+
+// 1 / sum, 0 for a row that saw nothing (a NaN stays one).
+__device__ __forceinline__ float inverse(float sum) { return sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum); }
 
 template <typename T, int DH>
 class Walker {
@@ -196,6 +206,86 @@ class Walker {
             fresh = last;
             if (i + 1 < n) advance(work);
         }
+    }
+
+    // One (sequence, KV head) by the CTAs of a cluster, result and all: each takes
+    // an equal share of its tiles, and all join the partials through
+    // distributed shared memory.
+    __device__ void run_direct() {
+        cg::cluster_group cl = cg::this_cluster();
+        const int parts = (int)cl.num_blocks(), part = (int)cl.block_rank();
+        Place p;
+        p.common = false;
+        p.item = quotient(blockIdx.x, parts);
+        p.b = quotient(p.item, a.kv.n_kv);
+        p.h = p.item - p.b * a.kv.n_kv;
+        p.rt = 0;
+        if (p.h == 0 && part == 0 && tid == 0 && (a.lens[p.b] < 0 || a.lens[p.b] > a.max_len)) atomicExch(a.err, 1u);
+        set_keys(p);  // (com is empty: all that the sequence sees is its own)
+        p.tiles = (p.keys + KT - 1) / KT;
+        const Shares sh(p.tiles, parts);
+        const bool some = part < p.tiles;
+        const int t0 = some ? sh.begin(part) : 0, n = some ? sh.begin(part + 1) - t0 : 0;
+        p.tile = t0;
+        Place load = p;
+        auto fetch_next = [&](int i) {
+            if (i < n) {
+                prepare(load);
+                fetch(i % L::STAGES, load, i == 0);
+                ++load.tile;
+            }
+            cp_async_commit();
+        };
+        for (int i = 0; i < L::STAGES - 1; ++i) fetch_next(i);
+        for (int i = 0; i != n; ++i) {
+            fetch_next(i + L::STAGES - 1);
+            asm volatile("cp.async.wait_group %0;" ::"n"(L::STAGES - 1) : "memory");
+            __syncthreads();
+            tile<1, true>(p, a.group, i == 0, i + 1 == n, i % L::STAGES);
+            __syncthreads();
+            ++p.tile;
+        }
+        // this CTA's partial lies in shared memory (finish); an empty share leaves nothing
+        float *mine = direct_o();
+        float2 *stat = direct_ml();
+        if (n == 0) {
+            for (int x = tid; x < a.group * DH; x += PA_THREADS) mine[x] = 0.f;
+            if (tid < a.group) stat[tid] = make_float2(-INFINITY, 0.f);
+        }
+        if (parts > 1)
+            cl.sync();
+        else
+            __syncthreads();
+        const int pairs = a.group * (DH / 2), per = (pairs + parts - 1) / parts;
+        for (int x = part * per + tid; x < min(pairs, (part + 1) * per); x += PA_THREADS) {
+            const int row = x / (DH / 2), c = (x % (DH / 2)) * 2;
+            float2 w[8], v[8];
+            float mx = -INFINITY;
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (k < parts) {
+                    w[k] = parts > 1 ? *cl.map_shared_rank(stat + row, k) : stat[row];
+                    v[k] = *reinterpret_cast<const float2 *>(parts > 1 ? cl.map_shared_rank(mine + row * DH + c, k)
+                                                                       : mine + row * DH + c);
+                    mx = fmaxf(mx, w[k].x);
+                }
+            const float off = mx == -INFINITY ? 0.f : mx;
+            float sx = 0.f, sy = 0.f, sl = 0.f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (k < parts) {
+                    const float f = ex2(w[k].x - off);
+                    sx += f * v[k].x;
+                    sy += f * v[k].y;
+                    sl += f * w[k].y;
+                }
+            const float inv = inverse(sl);
+            *reinterpret_cast<uint32_t *>(static_cast<T *>(a.out) + (long long)p.b * a.ld_out +
+                                          (long long)(p.h * a.group + row) * DH + c) = pack2<T>(sx * inv, sy * inv);
+            if (c == 0 && a.lse)
+                a.lse[(long long)p.b * a.n_q + p.h * a.group + row] = mx * 0.69314718055994530942f + logf(sl);
+        }
+        if (parts > 1) cl.sync();  // nobody leaves while its partial is read
     }
 
   private:
@@ -336,8 +426,15 @@ class Walker {
         }
     }
 
+    // Where a CTA of run_direct leaves its partial, the same place in all: o in the
+    // query rows' buffers (the queries are in registers by then), the statistics
+    // where the list's table would be.
+    __device__ float *direct_o() const { return reinterpret_cast<float *>(q0); }
+    __device__ float2 *direct_ml() const { return reinterpret_cast<float2 *>(cum); }
+
     // One tile of an item's rows: WR warps side by side in rows, 4 / WR in keys.
-    template <int WR>
+    // DIRECT: the item's end is the result, not a partial.
+    template <int WR, bool DIRECT = false>
     __device__ void tile(const Place &p, int rows, bool fresh, bool last, int s) {
         constexpr int WK = 4 / WR, NB = KT / (16 * WK);  // NB blocks of 16 keys per warp
         const int wr = warp % WR, wk = warp / WR, t = lane & 3;
@@ -426,7 +523,7 @@ class Walker {
                 mma<T>(o[2 * d + 1], pf, r[2], r[3]);
             }
         }
-        if (last) finish<WR>(p, wr, rows, s);
+        if (last) finish<WR, DIRECT>(p, wr, rows, s);
     }
 
     // Q fragments of this warp's 16 rows of a common item, straight from global
@@ -455,7 +552,7 @@ class Walker {
     }
 
     // The item's partial: (o, max, sum) per row, warps with the same rows joined.
-    template <int WR>
+    template <int WR, bool DIRECT>
     __device__ void finish(const Place &p, int wr, int rows, int s) {
         constexpr int WK = 4 / WR;
         const int g = lane >> 2, t = lane & 3;
@@ -512,9 +609,13 @@ class Walker {
                     sy += f * v.y;
                     sl += f * w.y;
                 }
-                float *d = dst + row * DH;
-                st_hint(reinterpret_cast<float2 *>(d + c), make_float2(sx, sy), keep);
-                if (c == 0) dst_ml[row] = make_float2(mx, sl);
+                if constexpr (DIRECT) {
+                    *reinterpret_cast<float2 *>(direct_o() + row * DH + c) = make_float2(sx, sy);
+                    if (c == 0) direct_ml()[row] = make_float2(mx, sl);
+                } else {
+                    st_hint(reinterpret_cast<float2 *>(dst + row * DH + c), make_float2(sx, sy), keep);
+                    if (c == 0) dst_ml[row] = make_float2(mx, sl);
+                }
             }
         }
     }
@@ -538,6 +639,15 @@ __global__ void __launch_bounds__(PA_THREADS, PA_CTAS_PER_SM) paged_attn_kernel(
     if (a.tc && blockIdx.x == gridDim.x - 1) pdl_wait();
 }
 
+
+// A cluster per (sequence, KV head) and no other launch: for few keys.
+template <typename T, int DH>
+__global__ void __launch_bounds__(PA_THREADS, PA_CTAS_PER_SM) paged_attn_direct(const AttnArgs a) {
+    extern __shared__ __align__(128) uint8_t pa_smem[];
+    pdl_wait();
+    pdl_trigger();
+    Walker<T, DH>(a, pa_smem).run_direct();
+}
 
 // One warp per (sequence, query head): the row's partials joined in list
 // order (common item first), normalised and rounded once.
@@ -613,7 +723,7 @@ __global__ void __launch_bounds__(PA_MERGE_THREADS) paged_attn_join(const AttnAr
             }
         }
     }
-    const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);  // (a NaN stays one)
+    const float inv = inverse(sum);
     T *dst = static_cast<T *>(a.out) + (long long)b * a.ld_out + (long long)hq * DH + lane * V;
     if constexpr (V == 1) {
         dst[0] = (T)(acc[0] * inv);
@@ -650,6 +760,37 @@ void common_shape(AttnArgs &a, bool tc, int n_sm) {
     a.page_align = tc ? 1 << a.kv.ps_log2 : 1;
     a.items_c = a.kv.n_kv * a.row_tiles;
     a.slots_c = a.items_c + a.grid_c;
+}
+
+// CTAs to a (sequence, KV head) of the direct kernel, 0 for the list and its
+// join.  Without the list, its table and the second launch a call of few keys
+// is 3 to 5 us shorter, but every sequence reads the common positions itself and a
+// CTA's tiles follow one another (0.7 us each).  As many CTAs as there are tiles
+// and as two per SM allow; then at most 512 keys a CTA, fewer where the grid
+// takes more than one wave.  Measured (us, list | direct by 1, 2, 4, 8), head_dim 128, n
+// (sequence, KV head) items x keys:
+//    16 x 160   6.2 | 4.7 4.9 4.3 4.4       128 x 160   8.5 | 4.9 5.9 9.1 16.7
+//    16 x 1000  7.4 | 14.2 9.1 6.5 5.3      128 x 512   9.5 | 8.6 7.9 11.4 18.4
+//    16 x 4096 12.5 | 49.6 27.0 15.3 11.0   128 x 1000 11.9 | 14.5 11.5 14.3 21.5
+//    64 x 2048 11.0 | 26.3 15.3 11.4 14.8   128 x 2048 14.1 | 26.5 19.0 22.4 29.0
+//   256 x 512  12.6 | 10.9 15.3 21.8        512 x 160  11.0 | 10.6 20.1
+//   256 x 1000 14.6 | 18.1 21.5 27.3        512 x 256  11.3 | 12.9 21.9
+// (over 252 such sizes, 64 wide heads too, the rule is 1 % off the best choice).
+// Not where the common positions read once more by every sequence make over 16
+// MB: alone that is L2's to give (64 x 1000 at 4 sequences: 10.4 | 7.7), but in a
+// step that streams weights beside it the list is faster (the batched decode of 4
+// and 8 samples, 3584 common positions: 0.868 | 0.876 and 0.890 | 0.905 ms a step).
+int direct_parts(const AttnArgs &a, int n_sm) {
+    const int bound = a.window > 0 ? std::min(a.window, a.max_len) : a.max_len, kt = tile_keys(a.kv.head_dim);
+    const int tiles = bound / kt + (bound % kt != 0);
+    const long long items = (long long)a.kv.n_seqs * a.kv.n_kv;
+    if (items > 6 * n_sm) return 0;
+    if ((items - a.kv.n_kv) * std::min(a.shared, bound) * a.kv.head_dim * 4 > (16 << 20)) return 0;
+    int parts = 1;
+    while (parts < 8 && parts < tiles && items * parts * 2 <= 2 * n_sm) parts *= 2;
+    const long long waves = (items * parts + 2 * n_sm - 1) / (2 * n_sm);
+    const int each = (tiles + parts - 1) / parts;
+    return waves * each <= (waves == 1 ? 512 / kt : 6) ? parts : 0;
 }
 
 struct WsLayout {
@@ -708,8 +849,14 @@ lf_status check_shape(const lf_paged_kv *kv, int n_q_heads, PagedView *v) {
 }
 
 template <typename T, int DH>
-lf_status launch_attn(const AttnArgs &a, cudaStream_t st) {
+lf_status launch_attn(const AttnArgs &a, int direct, cudaStream_t st) {
     constexpr int smem = Smem<T, DH>::BYTES;
+    if (direct)
+        return set_smem_once<paged_attn_direct<T, DH>>(smem) &&
+                       launch_pdl_cluster(paged_attn_direct<T, DH>, (unsigned)direct,
+                                          dim3((unsigned)(a.kv.n_seqs * a.kv.n_kv * direct)), PA_THREADS, smem, st, a)
+                   ? LF_OK
+                   : LF_ERR_CUDA;
     if (!set_smem_once<paged_attn_kernel<T, DH>>(smem)) return LF_ERR_CUDA;
     if constexpr (DH >= 64) {
         if (a.tc) {
@@ -724,10 +871,10 @@ lf_status launch_attn(const AttnArgs &a, cudaStream_t st) {
 }
 
 template <typename T>
-lf_status launch_attn_dim(const AttnArgs &a, cudaStream_t st) {
-    return a.kv.head_dim == 32   ? launch_attn<T, 32>(a, st)
-           : a.kv.head_dim == 64 ? launch_attn<T, 64>(a, st)
-                                 : launch_attn<T, 128>(a, st);
+lf_status launch_attn_dim(const AttnArgs &a, int direct, cudaStream_t st) {
+    return a.kv.head_dim == 32   ? launch_attn<T, 32>(a, direct, st)
+           : a.kv.head_dim == 64 ? launch_attn<T, 64>(a, direct, st)
+                                 : launch_attn<T, 128>(a, direct, st);
 }
 
 }  // namespace
@@ -784,6 +931,7 @@ extern "C" lf_status lf_attn_paged_shared(const lf_paged_kv *kv, const void *q_d
     a.max_len = max_len;
     a.scale_log2 = scale * lf::kLog2e;
     a.err = err_device;
+    const int direct = lf::direct_parts(a, n_sm);
     cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
-    return kv->dtype == LF_F16 ? lf::launch_attn_dim<__half>(a, st) : lf::launch_attn_dim<__nv_bfloat16>(a, st);
+    return kv->dtype == LF_F16 ? lf::launch_attn_dim<__half>(a, direct, st) : lf::launch_attn_dim<__nv_bfloat16>(a, direct, st);
 }

@@ -510,9 +510,10 @@ lf_status lf_kv_append_paged(const lf_paged_kv *kv, const void *q_in, const void
  * 0: all j < len_b), len_b = lens_device[b] counting the current token; query
  * head h reads KV head h / (n_q_heads / n_kv_heads).  The first `shared_len`
  * positions are common to the batch and always read through sequence 0's row
- * of the page table; they are read once for all sequences that reach them
- * (len_b >= shared_len, and a window that starts before it), each sequence's
- * other positions through its own row.  shared_len 0 is plain paged
+ * of the page table, each sequence's other positions through its own row.
+ * Where it pays (more than a few hundred positions, by max_len and window) the
+ * common ones are read once for all sequences that reach them (len_b >=
+ * shared_len, and a window that starts before it).  shared_len 0 is plain paged
  * attention.  A position that a sequence does not see never reaches its
  * result, whatever the cache holds there (NaN included).
  *   q_device, out_device: DEVICE [n_seqs][n_q_heads][head_dim] of the cache's
@@ -521,7 +522,8 @@ lf_status lf_kv_append_paged(const lf_paged_kv *kv, const void *q_in, const void
  *   softmax's denominator (of sum_j exp(scale * q . k_j)); NULL: not wanted;
  *   lens_device: DEVICE int32 [n_seqs]; a sequence of length 0 gets zeros and
  *   lse -inf;
- *   max_len: upper bound of the lengths (sizes nothing but the check of them);
+ *   max_len: upper bound of the lengths (a tight one lets a short batch take the
+ *   shortest way);
  *   scale: above 0, scale * log2(e) finite;
  *   workspace_device: DEVICE scratch of at least
  *   lf_attn_paged_shared_workspace bytes, 256-byte aligned; it needs no

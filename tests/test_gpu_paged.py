@@ -136,7 +136,7 @@ class Case:
     """A batch over a paged cache in which only the positions that some
     sequence sees hold numbers; everything else is NaN."""
 
-    def __init__(self, lens, shared, nq, nkv, dim, page, dtype, window=0, seed=0, stride_extra=0, spare=2):
+    def __init__(self, lens, shared, nq, nkv, dim, page, dtype, window=0, seed=0, stride_extra=0, spare=2, wide=False):
         import torch
         g = np.random.default_rng(seed + dim + page + shared)
         gen = torch.Generator(device="cuda").manual_seed(seed + dim + page + shared)
@@ -144,6 +144,8 @@ class Case:
         self.lens, self.shared, self.window, self.page, self.dtype, self.nq = lens, shared, window, page, dtype, nq
         max_pages = max(1, -(-(max(max(lens), shared)) // page)) + spare
         self.table, n_pages = ref.page_tables(g, n, max_pages, shared // page)
+        if wide:  # room for 2^17 positions that no sequence reaches: the bound of the lengths is far above them
+            self.table = np.concatenate([self.table, np.full((n, (1 << 17) // page - max_pages), -1, dtype=np.int32)], 1)
         dt = ref.torch_dtype(dtype)
         per = nkv * page * dim
         # K and V interleaved page by page in one pool when stride_extra is set
@@ -284,18 +286,33 @@ def test_attention_of_many_rows_strided_flagged_and_replayed():
     assert c.err.item() == 1
 
 
+# with a tight bound of the lengths a short batch takes the direct kernel, with a far one the list and the join
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("case", range(len(CASES)))
-def test_attention(case):
+def test_attention(case, wide):
     lens, shared, nq, nkv, dim, page, dtype, window = CASES[case]
-    c = Case(lens, shared, nq, nkv, dim, page, dtype, window, seed=case)
+    c = Case(lens, shared, nq, nkv, dim, page, dtype, window, seed=case, wide=wide)
     c.check(*c.run())
 
 
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("dim", [32, 64, 128])
 @pytest.mark.parametrize("group", [1, 2, 3, 7, 8, 16])
-def test_attention_groups(dim, group):
-    c = Case(lens_of(77, [1, 9, 150]), 77, 2 * group, 2, dim, 8, "f16" if group % 2 else "bf16")
+def test_attention_groups(dim, group, wide):
+    c = Case(lens_of(77, [1, 9, 150]), 77, 2 * group, 2, dim, 8, "f16" if group % 2 else "bf16", wide=wide)
     c.check(*c.run())
+
+
+@pytest.mark.parametrize("n_seqs,nkv,keys", [(1, 1, 64), (1, 1, 65), (1, 1, 513), (1, 2, 4096), (5, 8, 2000), (3, 21, 300),
+                                             (10, 16, 700), (38, 8, 500), (80, 8, 190), (100, 8, 129)])
+def test_attention_direct_cluster_sizes(n_seqs, nkv, keys):
+    # 1, 2, 4 and 8 CTAs to a sequence and head; some sequences so short that CTAs of the cluster have nothing
+    g = np.random.default_rng(keys)
+    lens = [keys] + [int(x) for x in g.integers(0, keys + 1, n_seqs - 1)]
+    c = Case(lens, min(lens) // 2, 2 * nkv, nkv, 128, 16, "f16", spare=0)
+    c.check(*c.run(max_len=keys))
+    c = Case(lens, keys // 3, 3 * nkv, nkv, 64, 32, "bf16", window=keys // 2 + 1, spare=0)
+    c.check(*c.run(max_len=keys))
 
 
 def test_attention_of_1024_sequences():
@@ -304,9 +321,10 @@ def test_attention_of_1024_sequences():
     c.check(*c.run())
 
 
-def test_attention_strides_interleaved_pool_and_no_lse():
+@pytest.mark.parametrize("wide", [False, True])
+def test_attention_strides_interleaved_pool_and_no_lse(wide):
     import torch
-    c = Case(lens_of(100, [1, 50, 90]), 100, 4, 2, 64, 16, "bf16", stride_extra=24)
+    c = Case(lens_of(100, [1, 50, 90]), 100, 4, 2, 64, 16, "bf16", stride_extra=24, wide=wide)
     out = torch.full((3, 4 * 64 + 40), 9.0, dtype=torch.bfloat16, device="cuda")
     got, _ = c.run(out=out, lse=False, ld=4 * 64 + 40)
     c.check(got, None)
@@ -323,11 +341,12 @@ def test_attention_is_repeatable_and_independent_of_the_workspace():
     c.check(a, la)
 
 
-def test_attention_captured_and_replayed_as_it_grows():
+@pytest.mark.parametrize("wide", [False, True])
+def test_attention_captured_and_replayed_as_it_grows(wide):
     # one graph, the lengths changed between replays; another graph with its own workspace on another stream
     import torch
     full = lens_of(120, [40, 64, 1])
-    c = Case(full, 120, 8, 4, 64, 16, "f16")
+    c = Case(full, 120, 8, 4, 64, 16, "f16", wide=wide)
     n, nq, d = c.q.shape
     graphs = []
     for _ in range(2):
@@ -353,9 +372,10 @@ def test_attention_captured_and_replayed_as_it_grows():
             c.check(out, lse)
 
 
-def test_attention_and_append_on_another_stream():
+@pytest.mark.parametrize("wide", [False, True])
+def test_attention_and_append_on_another_stream(wide):
     import torch
-    c = Case(lens_of(60, [5, 9]), 60, 4, 2, 64, 16, "f16")
+    c = Case(lens_of(60, [5, 9]), 60, 4, 2, 64, 16, "f16", wide=wide)
     s = torch.cuda.Stream()
     torch.cuda.synchronize()
     ws = c.workspace()
@@ -366,23 +386,25 @@ def test_attention_and_append_on_another_stream():
     c.check(*got)
 
 
-@pytest.mark.parametrize("bad_len", [-1, 97, 1 << 30])
-def test_attention_flags_a_length_out_of_range(bad_len):
+@pytest.mark.parametrize("most", [96, 30000])
+@pytest.mark.parametrize("bad_len", [-1, 30001, 1 << 30])
+def test_attention_flags_a_length_out_of_range(bad_len, most):
     import torch
-    c = Case([40, 60], 20, 4, 2, 64, 16, "f16")
+    c = Case([40, 60], 20, 4, 2, 64, 16, "f16", wide=True)
     c.ln.copy_(torch.tensor([bad_len, 60], dtype=torch.int32))
     c.lens = [0, 60]
-    out, lse = c.run(max_len=96)
+    out, lse = c.run(max_len=most)
     torch.cuda.synchronize()
     assert c.err.item() == 1
     c.err.zero_()
     c.check(out, lse)
 
 
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("bad_page", [-1, 1 << 30, 1000])
-def test_attention_flags_a_page_out_of_range(bad_page):
+def test_attention_flags_a_page_out_of_range(bad_page, wide):
     import torch
-    c = Case([40, 60], 0, 4, 2, 64, 16, "f16")
+    c = Case([40, 60], 0, 4, 2, 64, 16, "f16", wide=wide)
     c.tb[0, 1] = bad_page
     out, _ = c.run()
     torch.cuda.synchronize()
