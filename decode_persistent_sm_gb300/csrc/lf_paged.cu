@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendA
         const float4 *r = reinterpret_cast<const float4 *>(a.rope + ((long long)p * half + c0) * 2);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const float4 y = __ldg(r + i);
+            const float4 y = r[i];
             cs[2 * i] = y.x, sn[2 * i] = y.y, cs[2 * i + 1] = y.z, sn[2 * i + 1] = y.w;
         }
     }

@@ -48,9 +48,11 @@ inline lf_status paged_view(const lf_paged_kv *kv, PagedView *out) {
 // Programmatic dependent launch.  The kernels of these calls are launched so
 // that they may become resident before the stream's previous kernel has
 // finished; pdl_wait is the first thing they do, and returns when that kernel's
-// results are visible.  pdl_trigger lets the next such kernel become resident
-// in turn.  (A kernel launched without the attribute still waits for all of
-// this one.)  It hides about 2 us of launch latency between these kernels.
+// results are visible.  What any kernel may have written is therefore read by
+// plain loads: a read-only one (__ldg) may be moved above the wait.  pdl_trigger
+// lets the next such kernel become resident in turn.  (A kernel launched without
+// the attribute still waits for all of this one.)  It hides about 2 us of launch
+// latency between these kernels.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 

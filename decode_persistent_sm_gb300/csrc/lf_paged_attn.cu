@@ -384,21 +384,25 @@ class Walker {
 
     // Looks up the pages of p's tile.
     __device__ void prepare(const Place &p) {
+        int page[KT / 32], pos[KT / 32];
+#pragma unroll
+        for (int i = 0; i < KT / 32; ++i) {  // (the loads first: none of them may pass the flag's atomic)
+            const int k = p.tile * KT + lane + 32 * i, j = p.first + k + (k >= p.gap_at ? p.gap : 0);
+            const int row = j < a.shared ? 0 : p.b;
+            pos[i] = j;
+            page[i] = 0;
+            if (k < p.keys) page[i] = a.kv.table[(long long)row * a.kv.max_pages + (j >> a.kv.ps_log2)];
+        }
+        bool bad = false;
 #pragma unroll
         for (int i = 0; i < KT / 32; ++i) {
-            const int k = p.tile * KT + lane + 32 * i;
-            row_off[i] = -1;
-            if (k < p.keys) {
-                const int j = p.first + k + (k >= p.gap_at ? p.gap : 0);
-                const int row = j < a.shared ? 0 : p.b;
-                const int page = __ldg(a.kv.table + (long long)row * a.kv.max_pages + (j >> a.kv.ps_log2));
-                if (page >= 0 && page < a.kv.n_pages)
-                    row_off[i] = page * a.kv.page_stride +
-                                 ((((long long)p.h << a.kv.ps_log2) + (j & ((1 << a.kv.ps_log2) - 1))) * DH);
-                else
-                    atomicExch(a.err, 1u);
-            }
+            const bool key = p.tile * KT + lane + 32 * i < p.keys, in = page[i] >= 0 && page[i] < a.kv.n_pages;
+            bad |= key && !in;
+            row_off[i] = key && in ? page[i] * a.kv.page_stride +
+                                         ((((long long)p.h << a.kv.ps_log2) + (pos[i] & ((1 << a.kv.ps_log2) - 1))) * DH)
+                                   : -1;
         }
+        if (bad) atomicExch(a.err, 1u);
     }
 
     // Starts the copies of the prepared tile into stage s
@@ -547,7 +551,7 @@ class Walker {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const T *q = base[i & 1];
-                qf[kk][i] = q ? __ldg(reinterpret_cast<const uint32_t *>(q + kk * 16 + (i >> 1) * 8 + 2 * t)) : 0u;
+                qf[kk][i] = q ? *reinterpret_cast<const uint32_t *>(q + kk * 16 + (i >> 1) * 8 + 2 * t) : 0u;
             }
     }
 
@@ -662,7 +666,11 @@ __global__ void __launch_bounds__(PA_MERGE_THREADS) paged_attn_join(const AttnAr
     pdl_wait();
     pdl_trigger();
     if (!active) return;
-    const int2 at_c = a.span[item], at_o = a.span[a.items_c + own];  // (of earlier calls where this one has no tiles)
+    // (of earlier calls, or anything, where this one has no tiles or gave up)
+    int2 at_c = a.span[item];
+    const int2 at_o = a.span[a.items_c + own];
+    at_c.x = max(0, min(at_c.x, a.grid_c - 1));
+    at_c.y = max(at_c.x, min(at_c.y, a.grid_c - 1));
     Common com(a, -1);
     com.lo = a.plan[0];
     com.hi = a.plan[1];

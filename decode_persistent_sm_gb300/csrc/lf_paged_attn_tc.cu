@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(T_THREADS, 1)
             page = a.kv.n_pages;  // outside the tensor: zeros
             row = at & ((1 << a.kv.ps_log2) - 1);
             if (lane < boxes && at < com.hi) {
-                const int p = __ldg(a.kv.table + (at >> a.kv.ps_log2));  // sequence 0's row of the table
+                const int p = a.kv.table[at >> a.kv.ps_log2];  // sequence 0's row of the table
                 if (p >= 0 && p < a.kv.n_pages)
                     page = p;
                 else
@@ -324,12 +324,13 @@ __global__ void __launch_bounds__(T_THREADS, 1)
                         src = static_cast<const T *>(a.q) + (long long)b * a.ld_q +
                               (long long)(h * a.group + at - b * a.group) * DH;
                     }
+                    uint4 v[DH / 8];  // (all loads before the first store)
 #pragma unroll
-                    for (int c = 0; c < DH / 8; ++c) {
-                        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                        if (src) v = __ldg(reinterpret_cast<const uint4 *>(src) + c);
-                        *reinterpret_cast<uint4 *>(qs + (c >> 3) * T_HALF + sw128_offset(row, (c & 7) * 8)) = v;
-                    }
+                    for (int c = 0; c < DH / 8; ++c)
+                        v[c] = src ? reinterpret_cast<const uint4 *>(src)[c] : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+                    for (int c = 0; c < DH / 8; ++c)
+                        *reinterpret_cast<uint4 *>(qs + (c >> 3) * T_HALF + sw128_offset(row, (c & 7) * 8)) = v[c];
                     fence_proxy_async_shared();
                     mbar_arrive(&S.bq[x]);
                 }

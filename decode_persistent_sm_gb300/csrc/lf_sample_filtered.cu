@@ -669,7 +669,7 @@ __device__ __forceinline__ float load_row(const T *src, int n, float *z, float &
         done = nv * V;
 #pragma unroll 4
         for (int i = threadIdx.x; i < nv; i += NT) {
-            const uint4 raw = __ldg(reinterpret_cast<const uint4 *>(src) + i);
+            const uint4 raw = reinterpret_cast<const uint4 *>(src)[i];
             const T *t = reinterpret_cast<const T *>(&raw);
             float x[V];
 #pragma unroll
