@@ -63,6 +63,7 @@ struct TcShared {
 
 __device__ __forceinline__ bool await_phase(TcShared &S, uint64_t *bar, uint32_t parity, uint64_t deadline,
                                             uint32_t *err) {
+    if (mbar_test_wait(bar, parity)) return true;
     while (!mbar_try_wait(bar, parity)) {
         if (S.abort_) return false;
         if (global_timer_ns() > deadline) {
