@@ -20,10 +20,18 @@
 // a product.
 //
 // Measured: 64 sequences x 8 heads per KV head (512 rows), 8 KV heads of 128, 16384
-// common positions, BF16: 39 us, 880 TFLOP/s (46 % of the measured dense rate; the
-// tensor pipe is active 36 % of the time: a row tile's softmax, 128 values a thread,
-// takes longer than the other's two products).  The whole call 78.6 us, of which
-// the sequences' own positions take 31 (142 MB); on warp-level MMAs alone 161.
+// common positions, BF16: 35 us, 980 TFLOP/s (51 % of the measured dense rate; the
+// tensor pipe is active 41 % of the time).  The whole call 74.0 us, of which the
+// sequences' own positions take 31 (142 MB); on warp-level MMAs alone 161.  A step
+// (128 keys, both row tiles) takes 3700 cycles for 2048 of products.  Its chain is
+// softmax (1400: load 100, max 200, exponentials 800, store and fence 160), then P V
+// and Q K^T (512 each, and 340 until the result is seen).  Around the products the
+// issuing thread's own instructions count, some 300 cycles for a wait even when it
+// is over: so one wait for V and the next K, counters and descriptors in
+// registers, no barrier that nobody waits for (79.2 -> 74.0 us).  Slower: a thread
+// per half row (16 softmax warps, +8 %), an issuing warp per row tile (their products
+// interleave and delay both, +2 %), tiles of 64 keys with two buffers of S (+30 %: twice
+// as many waits).
 //
 // Every wait is bounded; a CTA that ran out of time flags it, lets its copies
 // and products finish (bounded), frees its TMEM and exits.
@@ -48,13 +56,12 @@ constexpr unsigned long long kTimeoutNs = 2000000000ull;
 // fall two phases behind, so parity waits are unambiguous.
 struct TcShared {
     uint64_t bq[2];   // Q of row tile x written (128 arrivals)
-    uint64_t bk[2];   // K buffer b loaded (tiles b, b + 2, ...)
-    uint64_t bkf[2];  // K buffer b read by the S products of its tile
-    uint64_t bv[2];   // V buffer b loaded
-    uint64_t bvf[2];  // V buffer b read by the P V products of its tile
+    uint64_t bk0;     // K of the first tile loaded
+    uint64_t bl[2];   // V of tile p and K of tile p + 1 loaded (p = 0, 2, .. and 1, 3, ..)
+    uint64_t bf[2];   // done: the S products of tile p and the P V products of tile p - 1 (p = 0, 2, .. and 1, 3, ..)
     uint64_t bs[2];   // row tile x: S of the next tile computed (and its earlier P V done)
     uint64_t bp[2];   // row tile x: P written to TMEM (128 arrivals)
-    uint64_t bo[2];   // row tile x: P V done
+    uint64_t bo[2];   // row tile x: the last P V of an item done
     uint64_t bdone;   // every product this CTA issued is done (one commit at the end)
     uint32_t tmem;
     volatile int abort_;
@@ -145,14 +152,13 @@ __global__ void __launch_bounds__(T_THREADS, 1)
     if (threadIdx.x == 0) {
         for (int b = 0; b < 2; ++b) {
             mbar_init(&S.bq[b], 128);
-            mbar_init(&S.bk[b], 1);
-            mbar_init(&S.bkf[b], 1);
-            mbar_init(&S.bv[b], 1);
-            mbar_init(&S.bvf[b], 1);
+            mbar_init(&S.bl[b], 1);
+            mbar_init(&S.bf[b], 1);
             mbar_init(&S.bs[b], 1);
             mbar_init(&S.bp[b], 128);
             mbar_init(&S.bo[b], 1);
         }
+        mbar_init(&S.bk0, 1);
         mbar_init(&S.bdone, 1);
         S.abort_ = 0;
         S.issued_ = 0;
@@ -169,85 +175,90 @@ __global__ void __launch_bounds__(T_THREADS, 1)
     if (warp == 0) {
         // copies: lane i < pages looks up and loads the tile's i-th box
         const int box = min(1 << a.kv.ps_log2, kTcKeys), boxes = kTcKeys / box;
-        int nk[2] = {0, 0}, nv[2] = {0, 0};
-        int tile = tile0, item = item0;
-        auto lookup = [&](int tl, int &page, int &row) {
-            const int at = com.lo + tl * kTcKeys + lane * box;
-            page = a.kv.n_pages;  // outside the tensor: zeros
-            row = at & ((1 << a.kv.ps_log2) - 1);
+        struct Box {
+            int h, page, row;
+        };
+        int tile = tile0, item = item0, started = 0;  // loads on bl so far
+        auto next = [&] {  // this lane's box of the next tile of the list
+            const int at = com.lo + tile * kTcKeys + lane * box;
+            Box x;
+            x.h = item / a.row_tiles;
+            x.page = a.kv.n_pages;  // outside the tensor: zeros
+            x.row = at & ((1 << a.kv.ps_log2) - 1);
             if (lane < boxes && at < com.hi) {
                 const int p = a.kv.table[at >> a.kv.ps_log2];  // sequence 0's row of the table
                 if (p >= 0 && p < a.kv.n_pages)
-                    page = p;
+                    x.page = p;
                 else
                     atomicExch(a.err, 1u);
             }
-        };
-        int page, row;
-        lookup(tile, page, row);
-        bool ok = true;
-        for (int j = 0; j < n; ++j) {
-            const int b = j & 1, h = item / a.row_tiles, cur_page = page, cur_row = row;
             if (++tile == tiles) {
                 tile = 0;
                 ++item;
             }
-            if (j + 1 < n) lookup(tile, page, row);
-            // buffer b is free once the products of tile j - 2 have read it
-            if (j >= 2) ok = await_phase(S, &S.bkf[b], ((j - 2) >> 1) & 1u, deadline, a.err);
-            if (!__all_sync(0xffffffffu, ok)) break;
-            uint8_t *kb = t + L::K + b * L::TILE + lane * box * 128;
-            if (lane == 0) mbar_arrive_expect_tx(&S.bk[b], L::TILE);
-            __syncwarp();
+            return x;
+        };
+        auto load = [&](int tile_at, const CUtensorMap *map, const Box &x, uint64_t *bar) {
             if (lane < boxes)
-                for (int x = 0; x < L::HALVES; ++x)
-                    tma_load_4d(kb + x * T_HALF, &tmK, 64 * x, cur_row, h, cur_page, &S.bk[b]);
-            ++nk[b];
-            if (j >= 2) ok = await_phase(S, &S.bvf[b], ((j - 2) >> 1) & 1u, deadline, a.err);
+                for (int i = 0; i < L::HALVES; ++i)
+                    tma_load_4d(t + tile_at + lane * box * 128 + i * T_HALF, map, 64 * i, x.row, x.h, x.page, bar);
+        };
+        Box now = next(), then = now;
+        if (lane == 0) mbar_arrive_expect_tx(&S.bk0, L::TILE);
+        __syncwarp();
+        load(L::K, &tmK, now, &S.bk0);
+        bool ok = true;
+        for (int j = 0; j < n; ++j) {  // V of tile j and K of the next
+            if (j + 1 < n) then = next();
+            // their buffers are free once the S products of tile j - 1 and the P V products of tile j - 2 are done
+            if (j >= 1) ok = await_phase(S, &S.bf[(j - 1) & 1], ((j - 1) >> 1) & 1u, deadline, a.err);
             if (!__all_sync(0xffffffffu, ok)) break;
-            uint8_t *vb = t + L::V + b * L::TILE + lane * box * 128;
-            if (lane == 0) mbar_arrive_expect_tx(&S.bv[b], L::TILE);
+            uint64_t *bar = &S.bl[j & 1];
+            if (lane == 0) mbar_arrive_expect_tx(bar, j + 1 < n ? 2 * L::TILE : L::TILE);
             __syncwarp();
-            if (lane < boxes)
-                for (int x = 0; x < L::HALVES; ++x)
-                    tma_load_4d(vb + x * T_HALF, &tmV, 64 * x, cur_row, h, cur_page, &S.bv[b]);
-            ++nv[b];
+            load(L::V + (j & 1) * L::TILE, &tmV, now, bar);
+            if (j + 1 < n) load(L::K + ((j + 1) & 1) * L::TILE, &tmK, then, bar);
+            ++started;
+            now = then;
         }
         if (S.abort_ && lane == 0) {  // let the copies in flight land
             const uint64_t dl = global_timer_ns() + 1000000000ull;
-            for (int b = 0; b < 2; ++b) {
-                if (nk[b] > 0)
-                    while (!mbar_try_wait(&S.bk[b], (nk[b] - 1) & 1u) && global_timer_ns() < dl) {
-                    }
-                if (nv[b] > 0)
-                    while (!mbar_try_wait(&S.bv[b], (nv[b] - 1) & 1u) && global_timer_ns() < dl) {
-                    }
+            while (!mbar_try_wait(&S.bk0, 0) && global_timer_ns() < dl) {
             }
+            for (int i = max(0, started - 2); i < started; ++i)
+                while (!mbar_try_wait(&S.bl[i & 1], (i >> 1) & 1u) && global_timer_ns() < dl) {
+                }
         }
     } else if (warp == 1) {
         if (lane == 0) {  // products, issued in order by this one thread
             constexpr uint32_t kIdescS = idesc<T>(128, kTcKeys, false), kIdescO = idesc<T>(128, DH, true);
-            const uint32_t q0 = smem_u32(t + L::Q), k0 = smem_u32(t + L::K), v0 = smem_u32(t + L::V);
+            // (descriptors of what lies `bytes` further: the address is in the low word)
+            auto on = [](uint64_t d, uint32_t bytes) {
+                return (d & 0xffffffff00000000ull) | (uint32_t)((uint32_t)d + (bytes >> 4));
+            };
+            const uint64_t q0 = smem_desc_sw128(smem_u32(t + L::Q)), k0 = smem_desc_sw128(smem_u32(t + L::K)),
+                           v0 = desc_mn_sw128(smem_u32(t + L::V));
             auto qk = [&](int x, int j) {
-                const uint32_t q = q0 + (uint32_t)x * L::TILE, k = k0 + (uint32_t)(j & 1) * L::TILE;
+                const uint64_t q = on(q0, (uint32_t)x * L::TILE), k = on(k0, (uint32_t)(j & 1) * L::TILE);
 #pragma unroll
                 for (int kk = 0; kk < DH / 16; ++kk) {
                     const uint32_t off = (uint32_t)(kk >> 2) * T_HALF + (uint32_t)(kk & 3) * 32;
-                    tc_mma(tmem + (uint32_t)x * kTcKeys, smem_desc_sw128(q + off), smem_desc_sw128(k + off), kIdescS,
-                           kk > 0);
+                    tc_mma(tmem + (uint32_t)x * kTcKeys, on(q, off), on(k, off), kIdescS, kk > 0);
                 }
             };
             auto pv = [&](int x, int j, bool first) {
-                const uint32_t v = v0 + (uint32_t)(j & 1) * L::TILE;
+                const uint64_t v = on(v0, (uint32_t)(j & 1) * L::TILE);
 #pragma unroll
                 for (int kk = 0; kk < kTcKeys / 16; ++kk)
                     tc_mma_tmem_a(tmem + T_O + (uint32_t)x * 128, tmem + (uint32_t)x * kTcKeys + (uint32_t)kk * 8,
-                                  desc_mn_sw128(v + (uint32_t)kk * 16 * 128), kIdescO, (!first || kk > 0) ? 1u : 0u);
+                                  on(v, (uint32_t)kk * 16 * 128), kIdescO, (!first || kk > 0) ? 1u : 0u);
             };
             int np[2] = {0, 0}, nq[2] = {0, 0};  // uses of bp and bq so far
             int tile = tile0, item = item0, nx = row_tiles_of(item0);
-            bool first = true, ok = await_phase(S, &S.bk[0], 0, deadline, a.err);
-            for (int x = 0; ok && x < nx; ++x) {
+            bool first = true, ok = await_phase(S, &S.bk0, 0, deadline, a.err);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {  // (unrolled: the issuing thread's own instructions are on the critical path)
+                if (!ok || x >= nx) break;
                 ok = await_phase(S, &S.bq[x], nq[x]++ & 1u, deadline, a.err);
                 if (!ok) break;
                 tc_fence_after();
@@ -255,27 +266,25 @@ __global__ void __launch_bounds__(T_THREADS, 1)
                 S.issued_ = 1;
                 tc_commit(&S.bs[x]);
             }
-            if (ok) tc_commit(&S.bkf[0]);
+            if (ok) tc_commit(&S.bf[0]);
             for (int j = 0; ok && j < n; ++j) {
                 const int b = j & 1, b1 = (j + 1) & 1;
                 const bool ends = tile + 1 == tiles;  // the next tile belongs to another item
-                ok = await_phase(S, &S.bv[b], (j >> 1) & 1u, deadline, a.err);
-                for (int x = 0; ok && x < nx; ++x) {
+                ok = await_phase(S, &S.bl[b], (j >> 1) & 1u, deadline, a.err);
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    if (!ok || x >= nx) break;
                     ok = await_phase(S, &S.bp[x], np[x]++ & 1u, deadline, a.err);
                     if (!ok) break;
                     tc_fence_after();
                     pv(x, j, first);
-                    tc_commit(&S.bo[x]);
+                    if (ends || j + 1 == n) tc_commit(&S.bo[x]);
                     if (j + 1 < n && !ends) {  // after the P V that read P from the same columns
-                        if (x == 0) ok = await_phase(S, &S.bk[b1], ((j + 1) >> 1) & 1u, deadline, a.err);
-                        if (!ok) break;
-                        tc_fence_after();
                         qk(x, j + 1);
                         tc_commit(&S.bs[x]);
                     }
                 }
                 if (!ok) break;
-                tc_commit(&S.bvf[b]);
                 first = false;
                 if (ends) {
                     tile = 0;
@@ -283,8 +292,9 @@ __global__ void __launch_bounds__(T_THREADS, 1)
                     first = true;
                     if (j + 1 < n) {  // both row tiles are on their way out; the next item's Q follows
                         nx = row_tiles_of(item);
-                        ok = await_phase(S, &S.bk[b1], ((j + 1) >> 1) & 1u, deadline, a.err);
-                        for (int x = 0; ok && x < nx; ++x) {
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            if (!ok || x >= nx) break;
                             ok = await_phase(S, &S.bq[x], nq[x]++ & 1u, deadline, a.err);
                             if (!ok) break;
                             tc_fence_after();
@@ -296,7 +306,7 @@ __global__ void __launch_bounds__(T_THREADS, 1)
                 } else {
                     ++tile;
                 }
-                if (j + 1 < n) tc_commit(&S.bkf[b1]);
+                tc_commit(&S.bf[b1]);
             }
             if (S.issued_) tc_commit(&S.bdone);  // tracks everything issued above
         }
@@ -306,7 +316,7 @@ __global__ void __launch_bounds__(T_THREADS, 1)
         const uint32_t ts = trow + (uint32_t)x * kTcKeys, to = trow + T_O + (uint32_t)x * 128;
         const float sc2 = a.scale_log2;
         constexpr float kLazy = 8.f;  // log2 of the largest P before the max moves
-        int item = item0, tile = tile0, left = n, ns = 0;  // ns: uses of bs (and bo) so far
+        int item = item0, tile = tile0, left = n, ns = 0, no = 0;  // ns, no: uses of bs and bo so far
         bool ok = true;
         while (ok && left > 0) {
             const int count = min(left, tiles - tile);  // tiles of this item in this CTA
@@ -404,7 +414,7 @@ __global__ void __launch_bounds__(T_THREADS, 1)
                     mbar_arrive(&S.bp[x]);
                 }
                 // the partial of this row, once the last P V is done
-                if (ok) ok = __all_sync(0xffffffffu, await_phase(S, &S.bo[x], (ns - 1) & 1u, deadline, a.err));
+                if (ok) ok = __all_sync(0xffffffffu, await_phase(S, &S.bo[x], no++ & 1u, deadline, a.err));
                 if (ok) {
                     tc_fence_after();
                     const long long slot = (long long)(item + blockIdx.x) * kTcRows + x * 128 + row;
