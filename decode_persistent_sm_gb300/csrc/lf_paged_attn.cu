@@ -821,11 +821,13 @@ bool tc_possible(const PagedView &v) { return v.head_dim >= 64 && v.ps_log2 >= 3
 // its 128-row tiles idle where there are few rows; it gains as the common
 // products grow.  Both measured (us, warp-level MMAs | tensor cores), 64 own
 // positions at most, by rows of a KV head x common positions:
-//   head_dim 128, 8 KV heads:   64 x 4096 20.9 | 22.9   64 x 16384 36.2 | 30.7
-//                              128 x 4096 25.3 | 28.1  128 x 16384 47.7 | 39.5
-//   head_dim 128, 16 KV heads: 128 x 2048 28.5 | 29.4  128 x 4096  36.9 | 34.6
-//                               32 x 16384 39.8 | 39.5 256 x 16384 132 | 69
-//   head_dim 64, 16 KV heads:   64 x 16384 34.8 | 37.9 128 x 16384 57.1 | 43.3
+//   head_dim 128, 8 KV heads:   64 x 4096 19.5 | 21.5   64 x 16384 30.9 | 26.2
+//                              128 x 4096 21.9 | 23.3  128 x 6000  25.3 | 24.8
+//                              128 x 16384 42.3 | 29.6  33 x 16384 28.8 | 22.3
+//   head_dim 128, 16 KV heads:  64 x 4096 23.0 | 23.3   64 x 8192  30.4 | 29.0
+//                               32 x 16384 37.4 | 38.6 256 x 16384 127 | 53
+//   head_dim 64, 16 KV heads:   64 x 16384 30.1 | 32.8 128 x 8192  30.1 | 26.2
+//   head_dim 64, 8 KV heads:   128 x 11500 23.5 | 22.4  96 x 16384 28.6 | 23.4
 // so: by the size of the common products, and not where half of a row tile (a
 // quarter at head_dim 128) would be empty.  With a window at most that many
 // positions are common.
