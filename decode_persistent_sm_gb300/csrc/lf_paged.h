@@ -36,8 +36,8 @@ inline lf_status paged_view(const lf_paged_kv *kv, PagedView *out) {
     if (kv->head_dim < 16 || kv->head_dim > 256 || kv->head_dim % 16) return LF_ERR_INVALID_ARG;
     const long long dense = (long long)kv->n_kv_heads * kv->page_size * kv->head_dim;
     if (kv->page_stride != 0 && (kv->page_stride < dense || kv->page_stride % 8)) return LF_ERR_INVALID_ARG;
-    // positions are 32-bit
-    if ((long long)kv->max_pages * kv->page_size > 0x7fffffffLL) return LF_ERR_INVALID_ARG;
+    // positions are 32-bit, and the last tile may run past the last one (by 4096: 32 TMA boxes)
+    if ((long long)kv->max_pages * kv->page_size > 0x7fff0000LL) return LF_ERR_INVALID_ARG;
     int lg = 0;
     while ((1 << lg) < kv->page_size) ++lg;
     *out = PagedView{kv->k,         kv->v,        kv->page_table, kv->n_pages, kv->n_kv_heads, lg, kv->head_dim,

@@ -468,7 +468,8 @@ typedef enum { LF_F32 = 0, LF_F16 = 1, LF_BF16 = 2 } lf_dtype;
  * may name the same page (a shared prompt).
  *   k, v: DEVICE arrays of dtype (LF_F16 or LF_BF16), 16-byte aligned;
  *   page_table: DEVICE int32 [n_seqs][max_pages];
- *   page_size: a power of two, 1 .. 1024; head_dim: a multiple of 16, 16 .. 256;
+ *   page_size: a power of two, 1 .. 1024; max_pages * page_size at most
+ *   2^31 - 2^16; head_dim: a multiple of 16, 16 .. 256;
  *   page_stride: elements from one page to the next, a multiple of 8 and at
  *   least n_kv_heads * page_size * head_dim; 0 = exactly that. */
 typedef struct {

@@ -64,6 +64,15 @@ def test_bad_cache_descriptions_are_refused(lib, bad):
     assert lib.lf_attn_paged_shared_workspace(ctypes.byref(kv), 8) == 0
 
 
+def test_positions_that_a_last_tile_would_carry_past_32_bits_are_refused(lib):
+    most = (1 << 31) - (1 << 16)
+    assert append(lib, cache(page_size=1, max_pages=most), n=0) == OK
+    assert append(lib, cache(page_size=1, max_pages=most + 1), n=0) == INVALID
+    assert append(lib, cache(page_size=1024, max_pages=most // 1024), n=0) == OK
+    assert append(lib, cache(page_size=1024, max_pages=most // 1024 + 1), n=0) == INVALID
+    assert attend(lib, cache(page_size=1024, max_pages=most // 1024 + 1)) == INVALID
+
+
 def test_no_cache_is_refused(lib):
     assert lib.lf_attn_paged_shared_workspace(None, 8) == 0
     assert lib.lf_kv_append_paged(None, A, A, A, 0, 512, 256, 256, 8, A, 512, A, A, 1, A, 9, A, None) == INVALID
