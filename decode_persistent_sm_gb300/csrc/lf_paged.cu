@@ -172,7 +172,7 @@ bool launch_units(const AppendArgs &a, cudaStream_t st) {
     const int slots = min((heads + U - 1) / U, kAppendThreads / pieces);
     const int tokens = kAppendThreads / (pieces * slots);  // per block
     const int y = (heads + slots * U - 1) / (slots * U);
-    return launch_pdl(kv_append_kernel<TI, TO, U>, dim3((unsigned)((a.n_tokens + tokens - 1) / tokens), (unsigned)y),
+    return launch_pdl(kv_append_kernel<TI, TO, U>, dim3((unsigned)((a.n_tokens - 1) / tokens + 1), (unsigned)y),
                       (unsigned)(pieces * slots * tokens), 0, st, a, slots);
 }
 
