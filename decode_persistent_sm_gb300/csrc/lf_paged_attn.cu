@@ -32,9 +32,9 @@
 //
 // Measured (us per call, both launches; in brackets the bytes it cannot do
 // without at the copy rate): 8 sequences x 512 common + 40 .. 130 own positions, 32 / 16
-// heads of 128: 9.8 (1.5); 16 x 3584 + 100 .. 512: 23.8 (10.4); 24 windowed
+// heads of 128: 10.0 (1.5); 16 x 3584 + 100 .. 512: 23.8 (10.4); 24 windowed
 // sequences, 24 / 8 heads of 64: 15.0 (2.9); 2 short ones, by the direct kernel:
-// 4.7 (6.5 by the list), the time of the call.  Between 2 and 3 us go to working out the list (lengths, then page
+// 4.7 to 5.2 (6.5 by the list), the time of the call.  Between 2 and 3 us go to working out the list (lengths, then page
 // numbers, then the first keys: three trips to L2), as much to the join; in
 // between the keys and values stream at 5.7 TB/s.
 #include <cooperative_groups.h>

@@ -37,7 +37,7 @@
 // products, log2(e) / T and ln(min_p) come as pairs of floats.
 //
 // Measured (us per call; rows of mixed filters, a fifth greedy; in brackets the
-// bytes at the copy rate): 1 x 32000 fp32 6 - 10 (0.02), 16 x 32000 18 - 20 (0.3),
+// bytes at the copy rate): 1 x 32000 fp32 5 - 11 (0.02), 16 x 32000 18 - 20 (0.3),
 // 100 x 50257 39 (3), 256 x 131072 bf16 152 (10).  A single row is a chain of three
 // to six exchanges between CTAs (about 1 us each) and passes over 4000 logits; many rows
 // are bound by instructions: 76 per logit on average, two thirds of them the exact
