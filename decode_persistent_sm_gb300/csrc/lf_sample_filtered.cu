@@ -861,8 +861,12 @@ lf_status launch_row(const FilterArgs &a, cudaStream_t st) {
 
 template <int C>
 lf_status launch_cluster(const FilterArgs &a, int n_sm, cudaStream_t st) {
-    // 1024 threads where a CTA has its SM to itself
-    return a.per > kPairPer || a.rows * C <= n_sm ? launch_row<1024, C>(a, st) : launch_row<512, C>(a, st);
+    // 1024 threads where a CTA has its SM to itself, or nearly all do: 512, two CTAs
+    // to an SM, win with more of them or few logits (us, 512 | 1024 threads; CTAs x logits
+    // of one: 160 x 10000 30.6 | 24.6, 200 x 10000 30.2 | 26.5, 200 x 4000 21.6 | 20.8,
+    // 300 x 10000 31.7 | 35.4, 200 x 37 10.6 | 12.9)
+    const int wide = a.per > 2048 ? n_sm + n_sm / 3 : n_sm;
+    return a.per > kPairPer || a.rows <= wide / C ? launch_row<1024, C>(a, st) : launch_row<512, C>(a, st);
 }
 
 lf_status launch_filtered(FilterArgs a, cudaStream_t st) {
@@ -872,12 +876,18 @@ lf_status launch_filtered(FilterArgs a, cudaStream_t st) {
         (void)cudaGetLastError();
         return LF_ERR_CUDA;
     }
-    // CTAs per row: what the shared memory asks for, and more while the grid has at
-    // most one CTA per SM and a CTA at least 4096 logits.  Measured (us, c = 1 | 2 | 4
-    // | 8): 1 x 32000 17.4 | 14.8 | 12.2 | 9.9, 16 x 32000 39 | 30 | 23 | 20, 64 x
-    // 32000 39 | 32 | 29 | 34, 256 x 32000 58 | 57 | 69 | 107, 1 x 4000 7.3 | 7.6 | 8.0 | 8.9.
+    // CTAs per row: what the shared memory asks for, and more while a CTA has at least
+    // 4096 logits and the grid fits the SMs, or overflows them by a third at 12000 logits
+    // and more.  Measured (us, c = 1 | 2 | 4 | 8): 1 x 32000 17.1 | 12.9 | 10.1 | 9.4,
+    // 16 x 32000 38 | 26 | 20 | 19, 40 x 32000 37 | 27 | 23 | 38, 70 x 32000 37 | 28 | 33 | 59,
+    // 100 x 32000 39 | 33 | 43 | 79, 100 x 10000 20 | 30 | 42 | 86, 150 x 10000 21 | 40 | 59 |
+    // 132, 256 x 32000 57 | 65 | 94 | 185, 1 x 4000 7.3 | 7.6 | 8.0 | 8.9.
     int c = 1;
-    while (c < F_MAX_CLUSTER && ((a.vocab + c - 1) / c > kMaxPer || (a.rows * c <= n_sm && a.vocab / c > 4096))) c *= 2;
+    auto more = [&] {
+        const int per = a.vocab / c, room = per > 12000 ? n_sm + n_sm / 3 : n_sm;
+        return (a.vocab + c - 1) / c > kMaxPer || (per > 4096 && a.rows <= room / (2 * c));
+    };
+    while (c < F_MAX_CLUSTER && more()) c *= 2;
     a.per = ((a.vocab + c - 1) / c + 7) / 8 * 8;
     switch (c) {
         case 1: return launch_cluster<1>(a, n_sm, st);
