@@ -9,12 +9,16 @@
 // the kept set is z >= the largest of the three, and the token is the first
 // kept index whose running kept mass exceeds u times the kept mass.
 //
-// The answer is a whole number that sums decide, so the sums are exact: a
-// weight is a 64-bit integer, 2^44 w rounded, from an exponential whose
-// argument is carried as a pair of floats (error about 2^-40 of the weight:
-// the fp32 exponential's 2^-22 would put one row in ten of a flat 131072-token
-// row on the wrong side of some border).  Integer sums come out the same in
-// any order, atomics included.
+// The answer is a whole number that sums decide, so the sums are integers: a
+// weight is 2^58 w rounded up, from an exponential whose argument is carried as a
+// pair of floats (error about 2^-40 of the weight: the fp32 exponential's 2^-22
+// would put one row in ten of a flat 131072-token row on the wrong side of some
+// border).  The largest weight is 1 and a row has at most 2^18 logits, so all
+// that is rounded up is below 2^-40 of the mass (units of 2^-44 would lose 2^-27 in
+// a long tail of equal weights).  Rounded up and not to nearest: a weight that 64
+// bits can hold counts, if only by a unit, and u = 0 draws the first kept
+// index.  A thread's sum fits 64 bits (at most 48 logits), what is summed further
+// has 128.  Integer sums come out the same in any order, atomics included.
 //
 // A row belongs to a cluster of 1, 2, 4 or 8 CTAs, each with a contiguous
 // range of the vocabulary in shared memory as fp32: the logits are read from
@@ -26,7 +30,9 @@
 //          everything below drops out (for k above half the threads every
 //          logit is counted in the histogram instead);
 //   top-p: the masses of all logits (64 bits as two 32-bit shared atomics, the
-//          second only on a carry) name the step that holds the border.
+//          second where the high word changes) name the step that holds the border.
+//          A step's unit is 2^-44 of the largest weight that can lie in it, down to
+//          2^-58: a sum of 2^18 weights of one step fits 64 bits at full precision.
 // The candidates' values (up to 1024) are then gathered in every CTA and told
 // apart there, up to 256 by ranking them pairwise, more by their float's bits,
 // 11 a level; a top-k set that was gathered serves top-p as well.  More
@@ -62,10 +68,13 @@ constexpr int F_LIST = 1024;  // candidates that every CTA of the row gathers
 constexpr int F_RANK = 256;   // candidates that are ranked pairwise
 constexpr int F_MAX_CLUSTER = 8;
 constexpr int F_MAX_VOCAB = 262144;
-constexpr int F_FRAC = 44;          // weights are integers in units of 2^-44
-constexpr float F_MAX_Y = 45.f;     // below 2^-45 a weight rounds to nothing
+constexpr int F_FRAC = 58;          // weights are integers in units of 2^-58: 48 of them fit 64 bits
+constexpr int F_STEP_FRAC = 44;     // in a step of the histogram: 2^-44 of its largest weight, at least 2^-58
+constexpr int F_LIST_FRAC = 53;     // among the candidates of a list: F_LIST of them fit 64 bits
+constexpr float F_ZERO_Y = 1075.f;  // a weight below 2^-1075 is zero, as in 64-bit arithmetic
 
 using u64 = unsigned long long;
+using u128 = unsigned __int128;
 
 // 2^61 * 2^(-f / 256), f = 0 .. 255 (Taylor series of the exponential).
 struct Pow2Table {
@@ -102,6 +111,7 @@ struct __align__(16) Gather {  // one CTA's contribution to a cluster-wide excha
 
 struct RowScale {
     float mx, ch, cl, step;  // the maximum, log2(e) / T as a pair, histogram steps per unit of logit
+    int oct;                 // log2 of the steps to a factor of 2 in weight
 };
 
 struct FilterShared {
@@ -112,12 +122,11 @@ struct FilterShared {
     u64 mass[F_RANK];        // weights of those ranked pairwise
     Gather slot[2][F_MAX_CLUSTER], said, heard[F_MAX_CLUSTER];
     uint64_t bar[2];
-    u64 wsum[32];
+    u128 wsum[32], found_before;
     uint32_t wmin[32], wmax[32];
-    u64 found_before;
     float floor;
-    uint32_t found_bin, key;
-    int found, n_cand;
+    uint32_t found_bin, key;  // found_bin: the step and 1, 0 for none
+    int n_cand;
 };
 
 // Order-preserving bits of a float (no NaN; -0 was made +0).
@@ -130,13 +139,14 @@ __device__ __forceinline__ float to_f32(float x) { return x; }
 __device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
 
-// round(2^44 exp((z - max) / T)), (ch, cl) = log2(e) / T as a pair of floats.
+// ceil(2^frac exp((z - max) / T)), (ch, cl) = log2(e) / T as a pair of floats.
 // y = (max - z) log2(e) / T as a pair (error 2^-46 of it); y = j / 256 + r, |r| <= 1 / 512;
 // 2^-y = 2^(-j / 256) (1 - q), q = 1 - e^(-t), t = r ln 2 = th + tl, |t| < 0.0014:
 // q = th + (tl - th^2 (1/2 - th / 6)), the rest below 2^-42.  Sums of a large and a
 // small integer are taken after their conversions (the small one by adding 1.5 * 2^23).
-// mx is finite.
-__device__ __forceinline__ u64 weight(float z, float mx, float ch, float cl, const u64 *pow2) {
+// From `far` <= frac on (in y) the weight is one unit, from F_ZERO_Y on 0 (a masked
+// logit's).  mx is finite.
+__device__ __forceinline__ u64 weight(float z, float mx, float ch, float cl, const u64 *pow2, int frac, float far) {
     const float s = mx - z;
     const float yh = __fmul_rn(s, ch);
     constexpr float kRound = 12582912.f;  // 1.5 * 2^23: adding it leaves the integer part in the low mantissa bits
@@ -155,33 +165,23 @@ __device__ __forceinline__ u64 weight(float z, float mx, float ch, float cl, con
     const int q = __float2int_rn(th * kScale) + (__float_as_int(__fmaf_rn(c, kScale, kRound)) - kRoundBits);
     const u64 t = pow2[j & 255];
     const u64 w61 = t - (u64)(((long long)(int)(t >> 31) * q) >> 8);
-    const int sh = 61 - F_FRAC + (j >> 8);
-    const u64 v = ((w61 >> ((sh - 1) & 63)) + 1) >> 1;
-    return yh < F_MAX_Y ? v : 0ull;  // (a select: what was computed for a far or infinite z is dropped)
+    const u64 v = ((w61 - 1) >> ((61 - frac + (j >> 8)) & 63)) + 1;
+    return yh < far ? v : (yh < F_ZERO_Y ? 1ull : 0ull);  // (selects: what was computed for a far or infinite z is dropped)
 }
 
 // The same as a call, for the places that are not loops over the row.
-__device__ __noinline__ u64 weight_call(float z, float mx, float ch, float cl, const u64 *pow2) {
-    return weight(z, mx, ch, cl, pow2);
+__device__ __noinline__ u64 weight_call(float z, float mx, float ch, float cl, const u64 *pow2, int frac) {
+    return weight(z, mx, ch, cl, pow2, frac, (float)frac);
 }
 
-// floor(f * s), or (up) its ceiling, exactly, for 0 <= f < 1.
-__device__ __noinline__ u64 scaled(float f, u64 s, bool up) {
+// floor(f * s), or (up) its ceiling, exactly, for 0 <= f < 1 and s < 2^104.
+__device__ __noinline__ u128 scaled(float f, u128 s, bool up) {
     const uint32_t bits = __float_as_uint(f) & 0x7fffffffu;  // (f may be -0)
     const int e = (int)(bits >> 23);
-    const u64 m = e ? (bits & 0x7fffffu) | 0x800000u : bits;  // f = m 2^-k
-    const int k = 150 - (e ? e : 1);                          // 24 ..
-    const u64 lo = m * s, hi = __umul64hi(m, s);
-    u64 v = 0;
-    bool rest;
-    if (k < 64) {
-        v = (hi << (64 - k)) | (lo >> k);
-        rest = (lo & ((1ull << k) - 1)) != 0;
-    } else {
-        const int d = k - 64;
-        v = d < 64 ? hi >> d : 0;
-        rest = lo != 0 || (d < 64 ? (hi & ((1ull << d) - 1)) != 0 : hi != 0);
-    }
+    const u128 p = s * (e ? (bits & 0x7fffffu) | 0x800000u : bits);  // f = m 2^-k
+    const int k = 150 - (e ? e : 1);                                 // 24 ..
+    const u128 v = k < 128 ? p >> k : 0;
+    const bool rest = k < 128 ? (v << k) != p : p != 0;
     return v + (up && rest ? 1 : 0);
 }
 
@@ -198,11 +198,37 @@ __device__ __forceinline__ void hist_add(FilterShared &S, int bin, u64 w) {
     if (wh) atomicAdd(&S.hi[bin], wh);
 }
 
-__device__ __forceinline__ u64 warp_sum(u64 v) {
+// The warp's sum, in pieces of 22 bits.
+__device__ __forceinline__ u128 warp_sum(u64 v) {
+    const uint32_t a = __reduce_add_sync(0xffffffffu, (uint32_t)v & 0x3fffffu),
+                   b = __reduce_add_sync(0xffffffffu, (uint32_t)(v >> 22) & 0x3fffffu),
+                   c = __reduce_add_sync(0xffffffffu, (uint32_t)(v >> 44));
+    return ((u128)c << 44) + ((u64)b << 22) + a;
+}
+
+__device__ __forceinline__ u64 shfl(u64 v, int lane) { return __shfl_sync(0xffffffffu, v, lane); }
+__device__ __forceinline__ u128 shfl(u128 v, int lane) {
+    return (u128)shfl((u64)(v >> 64), lane) << 64 | shfl((u64)v, lane);
+}
+// Inclusive sum over the lanes.
+__device__ __forceinline__ u64 warp_scan(u64 v, int lane) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    for (int o = 1; o < 32; o <<= 1) {
+        const u64 y = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += y;
+    }
     return v;
 }
+__device__ __forceinline__ u128 warp_scan(u128 v, int lane) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const u64 lo = __shfl_up_sync(0xffffffffu, (u64)v, o), hi = __shfl_up_sync(0xffffffffu, (u64)(v >> 64), o);
+        if (lane >= o) v += (u128)hi << 64 | lo;
+    }
+    return v;
+}
+// A sum of a Gather's a (low 64 bits) and b (the rest).
+__device__ __forceinline__ u128 wide(const Gather &g) { return (u128)g.b << 64 | g.a; }
 
 __device__ __forceinline__ float of_key(uint32_t k) {
     return __uint_as_float((k & 0x80000000u) ? k & 0x7fffffffu : ~k);
@@ -307,9 +333,19 @@ struct Row {
         mx = __reduce_max_sync(0xffffffffu, lane < NW ? S.wmax[lane] : 0u);
     }
 
-    __device__ __forceinline__ u64 weight_of(float x) const { return weight(x, rs.mx, rs.ch, rs.cl, S.pow2); }
-    __device__ __forceinline__ u64 weight_cold(float x) const { return weight_call(x, rs.mx, rs.ch, rs.cl, S.pow2); }
+    __device__ __forceinline__ u64 weight_of(float x) const {
+        return weight(x, rs.mx, rs.ch, rs.cl, S.pow2, F_FRAC, (float)F_FRAC);
+    }
+    // in units of x's step (where the unit is above 2^-58, y stays far below 58)
+    __device__ __forceinline__ u64 weight_in_step(float x, int step) const {
+        return weight(x, rs.mx, rs.ch, rs.cl, S.pow2, step_frac(step), (float)F_FRAC);
+    }
+    __device__ __forceinline__ u64 weight_cold(float x, int frac) const {
+        return weight_call(x, rs.mx, rs.ch, rs.cl, S.pow2, frac);
+    }
     __device__ __forceinline__ int step(float x) const { return step_of(x, rs.mx, rs.step); }
+    // weights of step s are at most 2^-(s >> oct)
+    __device__ __forceinline__ int step_frac(int s) const { return min(F_STEP_FRAC + (s >> rs.oct), F_FRAC); }
 
     __device__ void clear_hist() {
         for (int i = tid; i < F_BINS; i += NT) S.lo[i] = S.hi[i] = 0;
@@ -321,9 +357,11 @@ struct Row {
     // bin where `above` + the running sum reaches the target, and `before`,
     // above + the sum of the bins before it.  With frac >= 0 the target is first
     // set to frac of the total, rounded up.  G = C: the sum of the cluster's
-    // histograms; G = 1: this CTA's alone.
-    template <int G>
-    __device__ int find_bin(u64 above, u64 &target, float frac, u64 &before) {
+    // histograms; G = 1: this CTA's alone.  Sum u128: bins hold masses in their
+    // steps' units, the sums are in units of 2^-58.
+    template <int G, typename Sum>
+    __device__ int find_bin(Sum above, Sum &target, float frac, Sum &before) {
+        constexpr bool MASS = sizeof(Sum) > sizeof(u64);
         constexpr int SL = F_BINS / G;            // bins of this CTA's slice
         constexpr int PT = (SL + NT - 1) / NT;    // bins per thread
         const int part = G == 1 ? 0 : rank;
@@ -331,12 +369,13 @@ struct Row {
             sync();  // every CTA's histogram is complete
         else
             __syncthreads();
-        u64 v[PT], sum = 0;
+        Sum v[PT], sum = 0;
         const int b0 = tid * PT;
 #pragma unroll
         for (int i = 0; i < PT; ++i) {
             v[i] = 0;
             if (b0 + i < SL) {
+                u64 in_bin = 0;
 #pragma unroll
                 for (int r = 0; r < G; ++r) {
                     const uint32_t *lo = S.lo, *hi = S.hi;
@@ -344,43 +383,37 @@ struct Row {
                         lo = cg::this_cluster().map_shared_rank(S.lo, r);
                         hi = cg::this_cluster().map_shared_rank(S.hi, r);
                     }
-                    v[i] += ((u64)hi[part * SL + b0 + i] << 32) + lo[part * SL + b0 + i];
+                    in_bin += ((u64)hi[part * SL + b0 + i] << 32) + lo[part * SL + b0 + i];
                 }
+                v[i] = in_bin;
+                if constexpr (MASS) v[i] <<= F_FRAC - step_frac(part * SL + b0 + i);
             }
             sum += v[i];
         }
-        u64 inc = sum;  // inclusive scan over the slice
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const u64 y = __shfl_up_sync(0xffffffffu, inc, o);
-            if (lane >= o) inc += y;
-        }
+        const Sum inc = warp_scan(sum, lane);  // inclusive over the slice
         if (lane == 31) S.wsum[w] = inc;
-        if (tid == 0) S.found = 0;
+        if (tid == 0) S.found_bin = 0;
         __syncthreads();
-        u64 ws = lane < NW ? S.wsum[lane] : 0, wi = ws;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const u64 y = __shfl_up_sync(0xffffffffu, wi, o);
-            if (lane >= o) wi += y;
-        }
-        u64 total = __shfl_sync(0xffffffffu, wi, 31);
-        u64 at = above + inc - sum + __shfl_sync(0xffffffffu, wi - ws, w);
+        const Sum ws = lane < NW ? (Sum)S.wsum[lane] : 0, wi = warp_scan(ws, lane);
+        Sum total = shfl(wi, 31);
+        Sum at = above + inc - sum + shfl(wi - ws, w);
         if constexpr (G > 1) {
-            const Gather *got = exchange(Gather{total, 0u, 0u});
+            const Gather *got = exchange(Gather{(u64)total, (uint32_t)((u128)total >> 64), 0u});
             total = 0;
 #pragma unroll
             for (int r = 0; r < G; ++r) {
-                if (r < rank) at += got[r].a;
-                total += got[r].a;
+                if (r < rank) at += (Sum)wide(got[r]);
+                total += (Sum)wide(got[r]);
             }
         }
-        if (frac >= 0.f) target = max(1ull, scaled(frac, total, true));
+        if (frac >= 0.f) {
+            target = (Sum)scaled(frac, total, true);
+            if (target == 0) target = 1;
+        }
 #pragma unroll
         for (int i = 0; i < PT; ++i) {
             if (at < target && target <= at + v[i]) {
-                S.found = 1;
-                S.found_bin = (uint32_t)(part * SL + b0 + i);
+                S.found_bin = (uint32_t)(part * SL + b0 + i) + 1;
                 S.found_before = at;
             }
             at += v[i];
@@ -389,16 +422,16 @@ struct Row {
         int bin = F_BINS - 1;
         before = above;
         if constexpr (G > 1) {
-            const Gather *got = exchange(Gather{S.found_before, S.found_bin, (uint32_t)S.found});
+            const Gather *got = exchange(Gather{(u64)S.found_before, (uint32_t)(S.found_before >> 64), S.found_bin});
 #pragma unroll
             for (int r = 0; r < G; ++r)
                 if (got[r].c) {
-                    bin = (int)got[r].b;
-                    before = got[r].a;
+                    bin = (int)got[r].c - 1;
+                    before = (Sum)wide(got[r]);
                 }
-        } else if (S.found) {
-            bin = (int)S.found_bin;
-            before = S.found_before;
+        } else if (S.found_bin) {
+            bin = (int)S.found_bin - 1;
+            before = (Sum)S.found_before;
         }
         return bin;
     }
@@ -459,14 +492,14 @@ struct Row {
         return total;
     }
 
-    __device__ __forceinline__ u64 share(float x, bool mass) const { return mass ? weight_cold(x) : 1ull; }
-
     // The border among the keys of [kmin, kmax] over the row's logits (list:
-    // over the m gathered ones, in this CTA alone), by mass or by count: 2048 equal
-    // runs of keys a level, until one key is left.  (11 bits a level: at most 3.)
-    __device__ uint32_t refine(bool mass, bool list, int m, uint32_t kmin, uint32_t kmax, u64 above, u64 target) {
+    // over the m gathered ones, in this CTA alone), by mass in units of 2^-frac or
+    // (frac 0) by count: 2048 equal runs of keys a level, until one key is left.
+    // (11 bits a level: at most 3.)
+    __device__ uint32_t refine(int frac, bool list, int m, uint32_t kmin, uint32_t kmax, u64 target) {
         const float *src = list ? S.all : reinterpret_cast<const float *>(z4);
         const int n = list ? m : 4 * n4;
+        u64 above = 0;
         while (kmin < kmax) {
             int shift = 0;
             while (((kmax - kmin) >> shift) >= (uint32_t)F_BINS) ++shift;
@@ -476,12 +509,12 @@ struct Row {
                 const float x = src[i];
                 const uint32_t key = key_of(x);
                 if (key < kmin || key > kmax) continue;
-                const u64 wt = share(x, mass);
+                const u64 wt = frac ? weight_cold(x, frac) : 1ull;
                 if (wt) hist_add(S, (int)((kmax - key) >> shift), wt);
             }
             u64 before = 0;
-            const uint32_t bin = (uint32_t)(list ? find_bin<1>(above, target, -1.f, before)
-                                                 : find_bin<C>(above, target, -1.f, before));
+            const uint32_t bin = (uint32_t)(list ? find_bin<1, u64>(above, target, -1.f, before)
+                                                 : find_bin<C, u64>(above, target, -1.f, before));
             above = before;
             kmax -= min(bin << shift, kmax - kmin);
             kmin = max(kmin, kmax - min(kmax, (1u << shift) - 1u));
@@ -490,14 +523,13 @@ struct Row {
     }
 
     // Among the m gathered values from `floor` on, all keys in [kmin, kmax]: the
-    // key of the value at which above + the values at or above it, by their mass
-    // or (MASS false: above 0, no floor) counted, reach the target; with frac >= 0
-    // that is frac of them all.
+    // key of the value at which the values at or above it, by their mass in units
+    // of 2^-units or (MASS false: no floor) counted, reach the target; with
+    // part >= 0 that is this part of them all.
     template <bool MASS>
-    __device__ uint32_t border(int m, float floor, u64 above, u64 target, float frac, uint32_t kmin,
-                                            uint32_t kmax) {
+    __device__ uint32_t border(int m, float floor, int units, u64 target, float part, uint32_t kmin, uint32_t kmax) {
         if constexpr (!MASS) {
-            if (m > F_RANK) return refine(false, true, m, kmin, kmax, above, target);
+            if (m > F_RANK) return refine(0, true, m, kmin, kmax, target);
             const int i = tid / RT, k = (int)target;  // RT neighbouring threads share candidate i
             const float x = i < m ? S.all[i] : 0.f;
             int gt = 0, ge = 0;
@@ -518,17 +550,17 @@ struct Row {
         u64 own = 0;
 #pragma unroll 1
         for (int i = tid; i < m; i += NT) {
-            const u64 v = S.all[i] >= floor ? weight_cold(S.all[i]) : 0ull;
+            const u64 v = S.all[i] >= floor ? weight_cold(S.all[i], units) : 0ull;
             if (i < F_RANK) S.mass[i] = v;
             own += v;
         }
-        if (frac >= 0.f) {
-            own = warp_sum(own);
-            if (lane == 0) S.wsum[w] = own;
+        if (part >= 0.f) {
+            const u128 all = warp_sum(own);
+            if (lane == 0) S.wsum[w] = all;
             __syncthreads();
-            target = max(1ull, scaled(frac, warp_sum(lane < NW ? S.wsum[lane] : 0ull), true));
+            target = max((u64)1, (u64)scaled(part, warp_sum(lane < NW ? (u64)S.wsum[lane] : 0ull), true));
         }
-        if (m > F_RANK) return refine(true, true, m, max(kmin, key_of(floor)), kmax, above, target);
+        if (m > F_RANK) return refine(units, true, m, max(kmin, key_of(floor)), kmax, target);
         __syncthreads();
         const int i = tid / RT;
         const float x = i < m ? S.all[i] : 0.f;
@@ -545,7 +577,6 @@ struct Row {
             gt += __shfl_xor_sync(0xffffffffu, gt, o);
             eq += __shfl_xor_sync(0xffffffffu, eq, o);
         }
-        gt += above;
         if (i < m && gt < target && target <= gt + eq) S.key = key_of(x);
         __syncthreads();
         return S.key;
@@ -602,16 +633,17 @@ struct Row {
                 least = of_key(bound);
             } else {
                 each([&](float x) { hist_add(S, step(x), 1ull); });
-                last = find_bin<C>(0ull, target, -1.f, before);
+                last = find_bin<C, u64>(0ull, target, -1.f, before);
             }
             const int m = collect(least, [&](float x) { return last == F_BINS || step(x) <= last; }, kmin, kmax);
             if (m <= k)
                 floor = of_key(kmin);  // (fewer: there are no more above -inf)
             else
-                floor = of_key(m <= F_LIST ? border<false>(m, -INFINITY, 0ull, target, -1.f, kmin, kmax)
-                                           : refine(false, false, 0, kmin, kmax, 0ull, target));
+                floor = of_key(m <= F_LIST ? border<false>(m, -INFINITY, 0, target, -1.f, kmin, kmax)
+                                           : refine(0, false, 0, kmin, kmax, target));
             if (m <= F_LIST) {  // the list holds the whole top-k set
-                if (top_p < 1.f) floor = fmaxf(floor, of_key(border<true>(m, floor, 0ull, 0ull, top_p, kmin, kmax)));
+                if (top_p < 1.f)
+                    floor = fmaxf(floor, of_key(border<true>(m, floor, F_LIST_FRAC, 0ull, top_p, kmin, kmax)));
                 return floor;
             }
         }
@@ -619,16 +651,19 @@ struct Row {
             clear_hist();
             each([&](float x) {
                 if (!(x >= floor)) return;
-                const u64 wt = weight_of(x);
-                if (wt) hist_add(S, step(x), wt);
+                const int s = step(x);
+                const u64 wt = weight_in_step(x, s);
+                if (wt) hist_add(S, s, wt);
             });
-            u64 target = 0, before = 0;
-            const int at = find_bin<C>(0ull, target, top_p, before);
+            u128 target = 0, before = 0;
+            const int at = find_bin<C, u128>(0, target, top_p, before), units = step_frac(at);
+            // what is wanted of the step, in its units, rounded up
+            const u64 rest = (u64)((target - before + (1ull << (F_FRAC - units)) - 1) >> (F_FRAC - units));
             const int m = collect(floor, [&](float x) { return step(x) == at; }, kmin, kmax);
             uint32_t key = kmax;
             if (kmin != kmax)
-                key = m <= F_LIST ? border<true>(m, floor, before, target, -1.f, kmin, kmax)
-                                  : refine(true, false, 0, kmin, kmax, before, target);
+                key = m <= F_LIST ? border<true>(m, floor, units, rest, -1.f, kmin, kmax)
+                                  : refine(units, false, 0, kmin, kmax, rest);
             floor = fmaxf(floor, of_key(key));
         }
         return floor;
@@ -639,7 +674,7 @@ struct Row {
     __device__ float min_p_floor(float p, float t) const {
         int e;
         const float m = frexpf(p, &e), g = logf(m);
-        const u64 we = weight_call(g, 0.f, 1.44269502162933349609375f, 1.92596299112661746887e-8f, S.pow2);
+        const u64 we = weight_call(g, 0.f, 1.44269502162933349609375f, 1.92596299112661746887e-8f, S.pow2, F_FRAC);
         const float rest = (float)((long long)((u64)(m * 16777216.f) << (F_FRAC - 24)) - (long long)we) / (float)we;
         return __double2float_ru((double)rs.mx + (double)t * ((double)e * 0.69314718055994530942 + (double)g + (double)rest));
     }
@@ -779,8 +814,10 @@ __global__ void __launch_bounds__(NT, 1024 / NT) sample_filtered_kernel(const Fi
     R.rs.mx = mx;
     R.rs.ch = __fdiv_rn(kLog2eHi, t);
     R.rs.cl = __fdiv_rn(__fmaf_rn(-R.rs.ch, t, kLog2eHi) + kLog2eLo, t);
-    // 32 steps per factor of 2 in weight, finer where the whole row spans less
-    R.rs.step = fmaxf(32.f * R.rs.ch, (float)(F_BINS - 1) / (mx - of_key(kmin)));
+    // 32 steps per factor of 2 in weight, more (a power of two) where the whole row spans less
+    const float fit = (float)(F_BINS - 1) / ((mx - of_key(kmin)) * R.rs.ch);
+    R.rs.oct = fit >= 64.f ? min((int)(__float_as_uint(fit) >> 23) - 127, 30) : 5;
+    R.rs.step = R.rs.ch * (float)(1 << R.rs.oct);
 
     float floor = infinite ? 0.f : R.bounds(k, top_p, bound);
     if (min_p > 0.f && !infinite) {
@@ -800,55 +837,48 @@ __global__ void __launch_bounds__(NT, 1024 / NT) sample_filtered_kernel(const Fi
         mine += (x.x >= floor ? wx : 0ull) + (x.y >= floor ? wy : 0ull) + (x.z >= floor ? wz : 0ull) +
                 (x.w >= floor ? ww : 0ull);
     }
-    mine = warp_sum(mine);
+    const u128 own_mass = warp_sum(mine);
     __syncthreads();
-    if (lane == 0) S.wsum[w] = mine;
+    if (lane == 0) S.wsum[w] = own_mass;
     __syncthreads();
-    const u64 ws = lane < NW ? S.wsum[lane] : 0;
-    u64 wi = ws;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const u64 y = __shfl_up_sync(0xffffffffu, wi, o);
-        if (lane >= o) wi += y;
-    }
-    u64 before = __shfl_sync(0xffffffffu, wi - ws, w);
-    got = R.exchange(Gather{__shfl_sync(0xffffffffu, wi, 31), 0u, 0u});
-    u64 total = 0;
+    const u128 ws = lane < NW ? S.wsum[lane] : 0, wi = warp_scan(ws, lane), all = shfl(wi, 31);
+    u128 before = shfl(wi - ws, w);
+    got = R.exchange(Gather{(u64)all, (uint32_t)(all >> 64), 0u});
+    u128 total = 0;
 #pragma unroll
     for (int r = 0; r < C; ++r) {
-        if (r < rank) before += got[r].a;
-        total += got[r].a;
+        if (r < rank) before += wide(got[r]);
+        total += wide(got[r]);
     }
-    const u64 goal = scaled(u, total, false);  // running > u * total <=> running > that
-    if (before > goal || goal >= before + mine) return;
+    const u128 goal = scaled(u, total, false);  // running > u * total <=> running > that
+    if (before > goal || goal >= before + own_mass) return;
     // this warp's range holds the crossing
+    u128 left = goal - before;
     for (int c0 = 4 * q0; c0 < 4 * q1; c0 += 32) {
         const int i = c0 + lane;
         const float x = i < 4 * q1 ? z[i] : -INFINITY;
-        u64 inc = x >= floor ? R.weight_cold(x) : 0ull;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const u64 y = __shfl_up_sync(0xffffffffu, inc, o);
-            if (lane >= o) inc += y;
-        }
-        const unsigned hit = __ballot_sync(0xffffffffu, before + inc > goal);
+        const u64 inc = warp_scan(x >= floor ? R.weight_cold(x, F_FRAC) : 0ull, lane);  // (32 of them fit 64 bits)
+        const unsigned hit = __ballot_sync(0xffffffffu, inc > left);
         if (hit) {
             if (lane == __ffs(hit) - 1) {
                 a.token[row] = i0 + i;
                 // from the logit, not from its rounded weight; the mass is 1 + something (the maximum is kept)
                 if (logprob) {
-                    const float more = (float)(total - (1ull << F_FRAC)) * 5.684341886080801e-14f;  // 2^-44
+                    const u128 rest = total - ((u128)1 << F_FRAC);
+                    const float more = (rest >> 64) == 0 ? (float)(u64)rest * 0x1p-58f : (float)(u64)(rest >> 20) * 0x1p-38f;
                     *logprob = (x == mx ? 0.f : (x - mx) / t) - log1pf(more);
                 }
             }
             return;
         }
-        before += __shfl_sync(0xffffffffu, inc, 31);
+        left -= shfl(inc, 31);
     }
 }
 
 constexpr int kMaxPer = 49152;   // logits of one CTA: 192 KB
 constexpr int kPairPer = 20480;  // up to here two CTAs fit an SM's shared memory
+// a lane's weights (rounded up, so at most 2^58 each) in the kept mass fit 64 bits
+static_assert((kMaxPer / 4 / 32 + 31) / 32 * 4 < 64 && (kPairPer / 4 / 16 + 31) / 32 * 4 < 64, "sums of a lane");
 
 template <int NT, int C>
 lf_status launch_row(const FilterArgs &a, cudaStream_t st) {

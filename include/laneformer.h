@@ -570,8 +570,11 @@ size_t lf_attn_paged_shared_workspace(const lf_paged_kv *kv, int n_q_heads);
  *   NULL: 1, all, 1 and 0 for every row; u: DEVICE fp32 [rows], in [0, 1);
  *   token_device: DEVICE int32 [rows]; logprob_device: DEVICE fp32 [rows] or
  *   NULL.
- * Masses are 64-bit fixed-point sums of weights that are exact to about 2^-40,
- * so the draw is the definition's unless u lies that close to a border.  A row
+ * Masses are integer sums of weights in units of 2^-58 (the largest weight is
+ * 1), each off by less than a unit and 2^-40 of itself: together by less than
+ * about 2^-39 of the mass, so the draw is the definition's unless u (or top_p, the
+ * nucleus) lies that close to a border.  u = 0 draws the first kept index; a weight
+ * below 2^-1075 is zero, as in 64-bit arithmetic, and never drawn.  A row
  * with a NaN, without a logit above -inf, or with a parameter outside its range
  * (T neither 0 nor in [1e-30, 1e30], top_p outside (0, 1], min_p outside [0, 1],
  * u outside [0, 1)) gets token -1 and logprob NaN.  rows 0 does nothing.
