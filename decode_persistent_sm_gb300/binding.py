@@ -75,6 +75,7 @@ _SIGS = {
     "lf_sample_filtered": (_ci, [_vp, _ci, _ci, _ci, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
     "lf_debug_canaries": (_ci, [_vp, ctypes.POINTER(_ci)]),
     "lf_debug_corrupt_canary": (_ci, [_vp, _ci, _ci]),
+    "lf_debug_sample_wait": (_ci, [ctypes.c_uint64, _ci, _ci]),
 }
 
 

@@ -946,9 +946,9 @@ extern "C" lf_status lf_batch_generate_filtered(lf_engine *e, const int32_t *fir
         err = cudaGraphLaunch(b.graph, st);
         if (err != cudaSuccess) break;
         int *drawn = b.f_tok + (size_t)i * B;
-        const lf_status ls = lf_sample_filtered(b.logits, LF_F32, B, s.V, s.V, temperature ? b.f_t : nullptr,
-                                                top_k ? b.f_k : nullptr, top_p ? b.f_p : nullptr, min_p ? b.f_mp : nullptr,
-                                                b.f_u + (size_t)i * B, drawn, b.f_lp + (size_t)i * B, st);
+        const lf_status ls = lf::launch_sample_filtered(
+            b.logits, LF_F32, B, s.V, s.V, temperature ? b.f_t : nullptr, top_k ? b.f_k : nullptr, top_p ? b.f_p : nullptr,
+            min_p ? b.f_mp : nullptr, b.f_u + (size_t)i * B, drawn, b.f_lp + (size_t)i * B, b.err, st);
         if (ls != LF_OK) {
             (void)cudaStreamSynchronize(st);  // the copies from this call's arrays
             return batch_fail(e, ls);

@@ -22,4 +22,10 @@ lf_status launch_sample_batch(const float *logits, int vocab, int rows, float te
                               cudaStream_t stream);
 size_t sample_smem_bytes(int vocab);
 
+// lf_sample_filtered with its checks; *err (device, nullable) becomes 2, if it
+// was 0, when a wait between the CTAs of a row ran out.
+lf_status launch_sample_filtered(const void *logits, int dtype, int rows, int vocab, int64_t ld, const float *temperature,
+                                 const int32_t *top_k, const float *top_p, const float *min_p, const float *u,
+                                 int32_t *token, float *logprob, uint32_t *err, cudaStream_t stream);
+
 }  // namespace lf

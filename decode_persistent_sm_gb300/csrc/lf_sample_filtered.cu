@@ -51,12 +51,14 @@
 
 #include <cooperative_groups.h>
 
+#include <atomic>
 #include <cfloat>
 #include <climits>
 
 #include "laneformer.h"
 #include "lf_paged.h"
 #include "lf_ptx.cuh"
+#include "lf_sample.h"
 
 namespace cg = cooperative_groups;
 
@@ -72,6 +74,7 @@ constexpr int F_FRAC = 58;          // weights are integers in units of 2^-58: 4
 constexpr int F_STEP_FRAC = 44;     // in a step of the histogram: 2^-44 of its largest weight, at least 2^-58
 constexpr int F_LIST_FRAC = 53;     // among the candidates of a list: F_LIST of them fit 64 bits
 constexpr float F_ZERO_Y = 1075.f;  // a weight below 2^-1075 is zero, as in 64-bit arithmetic
+constexpr long long F_WAIT_CYCLES = 4000000000ll;  // 2 s
 
 using u64 = unsigned long long;
 using u128 = unsigned __int128;
@@ -102,6 +105,11 @@ struct FilterArgs {
     const float *top_p, *min_p, *u;
     int32_t *token;
     float *logprob;
+    uint32_t *err;           // nullable: 2 when a wait ran out
+    long long wait_cycles;   // limit of a wait between CTAs
+#ifdef LF_DEBUG
+    int lose_rank, lose_wait;  // the CTA of this rank (-1: each) gives up in its lose_wait-th wait (0: none)
+#endif
 };
 
 struct __align__(16) Gather {  // one CTA's contribution to a cluster-wide exchange
@@ -121,8 +129,12 @@ struct FilterShared {
     float all[F_LIST];       // the cluster's
     u64 mass[F_RANK];        // weights of those ranked pairwise
     Gather slot[2][F_MAX_CLUSTER], said, heard[F_MAX_CLUSTER];
-    uint64_t bar[2];
+    uint64_t bar[2], ready;
     u128 wsum[32], found_before;
+    // what warp 0 makes of an exchange
+    u128 base, target, before, total, left;
+    uint32_t kmin, kmax, bound, first, bin;
+    int nan, winner, lost;
     uint32_t wmin[32], wmax[32];
     float floor;
     uint32_t found_bin, key;  // found_bin: the step and 1, 0 for none
@@ -234,8 +246,9 @@ __device__ __forceinline__ float of_key(uint32_t k) {
     return __uint_as_float((k & 0x80000000u) ? k & 0x7fffffffu : ~k);
 }
 
-// Phase wait whose acquire covers stores from other CTAs of the cluster.
-__device__ __forceinline__ bool wait_cluster(uint64_t *bar, uint32_t parity) {
+// Phase wait, suspended for kWaitHintNs at most, whose acquire covers stores from
+// other CTAs of the cluster.
+__device__ __forceinline__ bool try_cluster(uint64_t *bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
@@ -245,6 +258,16 @@ __device__ __forceinline__ bool wait_cluster(uint64_t *bar, uint32_t parity) {
         : "r"(smem_u32(bar)), "r"(parity), "n"(kWaitHintNs)
         : "memory");
     return ok != 0;
+}
+
+// A warp's wait for a phase, of about `cycles` at most; the same answer in every
+// lane.  (The lanes stay together: after a loop of one lane the warp goes on in two
+// parts, and every shuffle costs a hundred cycles: 3 us for the sums of an exchange.)
+__device__ __forceinline__ bool wait_cluster(uint64_t *bar, uint32_t parity, long long cycles) {
+    const long long since = clock64();
+    while (!__all_sync(0xffffffffu, try_cluster(bar, parity)))
+        if (__any_sync(0xffffffffu, clock64() - since > cycles)) return false;
+    return true;
 }
 
 __device__ __forceinline__ void no_draw(int32_t *token, float *logprob) {
@@ -259,14 +282,18 @@ struct Row {
     FilterShared &S;
     const float4 *z4;  // this CTA's logits, -inf past n up to a multiple of 4
     int n4, rank, tid, lane, w;
-    int turn = 0;
-    int32_t *token;
-    float *logprob;
+    int turn = 0, published = 0;
+    bool lost = false;  // a wait of this CTA ran out: the same in all its threads
+    bool met = false;   // past meet()
+    const FilterArgs &a;
     RowScale rs;
+#ifdef LF_DEBUG
+    int waits = 0;
+#endif
 
-    __device__ Row(FilterShared &s, const float *z, int n, int r, int32_t *tok, float *lp)
+    __device__ Row(FilterShared &s, const float *z, int n, int r, const FilterArgs &args)
         : S(s), z4(reinterpret_cast<const float4 *>(z)), n4((n + 3) / 4), rank(r), tid(threadIdx.x),
-          lane(threadIdx.x & 31), w(threadIdx.x >> 5), token(tok), logprob(lp) {}
+          lane(threadIdx.x & 31), w(threadIdx.x >> 5), a(args) {}
 
     // f(value) for every logit of this CTA
     template <class F>
@@ -281,45 +308,129 @@ struct Row {
         }
     }
 
-    // Every CTA of the cluster gets every CTA's Gather: one 16-byte store into
-    // each CTA's shared memory, counted there on a barrier (about 1 us less than a
-    // store and a cluster barrier).  g is the same in threads 0 .. C - 1; a
-    // __syncthreads lies between two exchanges, so a CTA has read the buffer of
-    // one before its message of the next lets anyone write the one after
-    // (`turn` alternates two buffers).  The wait is bounded: a thread whose wait
-    // runs out reports the row as one without a draw and ends.
-    __device__ __forceinline__ const Gather *exchange(const Gather &g) {
-        const int b = turn & 1, parity = (turn >> 1) & 1;
-        Gather *mine = S.slot[b];
-        ++turn;
-        if constexpr (C == 1) {
-            if (tid == 0) mine[0] = g;
+    // Warp 0's bounded wait for a phase; its answer holds for the CTA.
+    __device__ __forceinline__ bool await(uint64_t *bar, uint32_t parity) {
+#ifdef LF_DEBUG
+        if (++waits == a.lose_wait && (a.lose_rank < 0 || a.lose_rank == rank)) return false;
+#endif
+        __syncwarp();
+        return wait_cluster(bar, parity, a.wait_cycles);
+    }
+
+    // A Gather from each of G CTAs (all of the cluster, or 1: this one alone) to all
+    // of them: one 16-byte store into each CTA's shared memory, counted there on a
+    // barrier (about 1 us less than a store and a cluster barrier).  g counts in
+    // warp 0, which passes what arrived to digest(lane r: the Gather of CTA r) and
+    // leaves what that makes of it in shared memory for the others.  A CTA has
+    // digested one exchange before its message of the next lets anyone write the
+    // one after (`turn` alternates two buffers).
+    // The wait is bounded.  A CTA whose wait ran out takes part in nothing more but
+    // leave(), so the row's other CTAs run out of theirs; nobody goes on with numbers
+    // that did not arrive.
+    template <int G, class D>
+    __device__ __forceinline__ void exchange(const Gather &g, D digest) {
+        if (lost) return;
+        if constexpr (G == 1) {
+            if (w == 0) digest(g);
             __syncthreads();
         } else {
-            if (tid == 0) mbar_arrive_expect_tx(&S.bar[b], C * (uint32_t)sizeof(Gather));
-            if (tid < C) {
-                uint32_t dst, bar;
-                asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(dst) : "r"(smem_u32(mine + rank)), "r"(tid));
-                asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(bar) : "r"(smem_u32(&S.bar[b])), "r"(tid));
-                asm volatile(
-                    "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(dst),
-                    "r"((uint32_t)g.a), "r"((uint32_t)(g.a >> 32)), "r"(g.b), "r"(g.c), "r"(bar)
-                    : "memory");
-            }
-            const uint64_t give_up = global_timer_ns() + 2000000000ull;
-            while (!wait_cluster(&S.bar[b], parity))
-                if (global_timer_ns() > give_up) {
-                    no_draw(token, logprob);
-                    asm volatile("exit;");
+            const int b = turn & 1, parity = (turn >> 1) & 1;
+            ++turn;
+            if (w == 0) {
+                if (tid == 0) mbar_arrive_expect_tx(&S.bar[b], G * (uint32_t)sizeof(Gather));
+                if (tid < G) {
+                    uint32_t dst, bar;
+                    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                                 : "=r"(dst)
+                                 : "r"(smem_u32(&S.slot[b][rank])), "r"(tid));
+                    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(bar) : "r"(smem_u32(&S.bar[b])), "r"(tid));
+                    asm volatile(
+                        "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(dst),
+                        "r"((uint32_t)g.a), "r"((uint32_t)(g.a >> 32)), "r"(g.b), "r"(g.c), "r"(bar)
+                        : "memory");
                 }
-        }
-        return mine;
-    }
-    __device__ __forceinline__ void sync() const {
-        if constexpr (C == 1)
+                if (await(&S.bar[b], parity))
+                    digest(S.slot[b][lane % G]);
+                else if (lane == 0)
+                    S.lost = 1;
+            }
             __syncthreads();
-        else
-            cg::this_cluster().sync();
+            lost = S.lost != 0;
+        }
+    }
+
+    // The row's last exchange.  Who has its messages needs nothing more of the
+    // others, nor they of it.  A CTA whose wait ran out looks again when all others
+    // have ended or given up: either every CTA had sent its message, then it goes
+    // on; or one had given up before, then no CTA of the row has them all and
+    // none writes a token.
+    template <class D>
+    __device__ __forceinline__ void last_exchange(const Gather &g, D digest) {
+        exchange<C>(g, digest);
+        if constexpr (C > 1) {
+            if (lost) {
+                meet();
+                if (w == 0 && landed(turn - 1)) {
+                    digest(S.slot[(turn - 1) & 1][lane % C]);
+                    if (lane == 0) S.lost = 0;
+                }
+                __syncthreads();
+                lost = S.lost != 0;
+            }
+        }
+    }
+
+    // Every CTA's shared memory as it was at this call may be read by the others
+    // behind it.  (Not a cluster barrier: a CTA that gave up has to leave those
+    // that wait here waiting, not let them pass.)
+    __device__ __forceinline__ void publish() {
+        __syncthreads();
+        if constexpr (C > 1) {
+            if (lost) return;
+            const int parity = published++ & 1;
+            if (w == 0) {
+                if (tid < C) {
+                    uint32_t bar;
+                    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(bar) : "r"(smem_u32(&S.ready)), "r"(tid));
+                    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+                }
+                if (!await(&S.ready, parity) && lane == 0) S.lost = 1;
+            }
+            __syncthreads();
+            lost = S.lost != 0;
+        }
+    }
+
+    // The messages of exchange i, waited for about a millisecond (warp 0).
+    __device__ bool landed(int i) { return wait_cluster(&S.bar[i & 1], (i >> 1) & 1, 2000000); }
+    // Where CTAs that gave up wait until the row's others are here or have ended (an
+    // exited thread counts as arrived).  All waits being bounded, they do.
+    __device__ __forceinline__ void meet() {
+        __syncwarp();
+        cg::this_cluster().sync();
+        met = true;
+    }
+
+    // The end of a row that exchanged anything: no CTA ends while another may still
+    // read or write its shared memory.  A CTA that received all it waited for may
+    // end: the others sent it nothing else, and what they read of it they
+    // had read before they sent the last message.  One that gave up waits for the
+    // others and (a millisecond) for what they sent to it, its last exchange's
+    // messages and those of CTAs one exchange further, and reports the row.
+    __device__ __forceinline__ void leave(int row) {
+        if constexpr (C > 1) {
+            if (!lost) return;
+            if (!met) meet();
+            if (w == 0) {
+                if (turn > 0) (void)landed(turn - 1);
+                if (lane == 0) mbar_arrive_expect_tx(&S.bar[turn & 1], C * (uint32_t)sizeof(Gather));
+                (void)landed(turn);
+                if (lane == 0) {
+                    no_draw(a.token + row, a.logprob ? a.logprob + row : nullptr);
+                    if (a.err) atomicCAS(a.err, 0u, 2u);
+                }
+            }
+        }
     }
 
     // Block-wide (min, max); every thread gets it.
@@ -366,9 +477,10 @@ struct Row {
         constexpr int PT = (SL + NT - 1) / NT;    // bins per thread
         const int part = G == 1 ? 0 : rank;
         if constexpr (G > 1)
-            sync();  // every CTA's histogram is complete
+            publish();  // every CTA's histogram is complete
         else
             __syncthreads();
+        if (lost) return F_BINS - 1;
         Sum v[PT], sum = 0;
         const int b0 = tid * PT;
 #pragma unroll
@@ -394,22 +506,26 @@ struct Row {
         if (lane == 31) S.wsum[w] = inc;
         if (tid == 0) S.found_bin = 0;
         __syncthreads();
-        const Sum ws = lane < NW ? (Sum)S.wsum[lane] : 0, wi = warp_scan(ws, lane);
-        Sum total = shfl(wi, 31);
-        Sum at = above + inc - sum + shfl(wi - ws, w);
-        if constexpr (G > 1) {
-            const Gather *got = exchange(Gather{(u64)total, (uint32_t)((u128)total >> 64), 0u});
-            total = 0;
-#pragma unroll
-            for (int r = 0; r < G; ++r) {
-                if (r < rank) at += (Sum)wide(got[r]);
-                total += (Sum)wide(got[r]);
+        Sum total = 0;
+        if (w == 0) {  // what lies before each warp's bins
+            const Sum ws = lane < NW ? (Sum)S.wsum[lane] : 0, wi = warp_scan(ws, lane);
+            if (lane < NW) S.wsum[lane] = wi - ws;
+            total = shfl(wi, 31);
+        }
+        exchange<G>(Gather{(u64)total, (uint32_t)((u128)total >> 64), 0u}, [&](const Gather &got) {
+            const Sum x = lane < G ? (Sum)wide(got) : 0, xi = warp_scan(x, lane);
+            const Sum base = shfl(xi - x, part), all = shfl(xi, 31);
+            if (lane == 0) {
+                S.base = base;
+                if (frac >= 0.f) {
+                    const Sum want = (Sum)scaled(frac, all, true);
+                    S.target = want == 0 ? 1 : want;
+                }
             }
-        }
-        if (frac >= 0.f) {
-            target = (Sum)scaled(frac, total, true);
-            if (target == 0) target = 1;
-        }
+        });
+        if (lost) return F_BINS - 1;
+        if (frac >= 0.f) target = (Sum)S.target;
+        Sum at = above + (Sum)S.base + (Sum)S.wsum[w] + inc - sum;
 #pragma unroll
         for (int i = 0; i < PT; ++i) {
             if (at < target && target <= at + v[i]) {
@@ -419,21 +535,19 @@ struct Row {
             at += v[i];
         }
         __syncthreads();
-        int bin = F_BINS - 1;
-        before = above;
         if constexpr (G > 1) {
-            const Gather *got = exchange(Gather{(u64)S.found_before, (uint32_t)(S.found_before >> 64), S.found_bin});
-#pragma unroll
-            for (int r = 0; r < G; ++r)
-                if (got[r].c) {
-                    bin = (int)got[r].c - 1;
-                    before = (Sum)wide(got[r]);
+            exchange<G>(Gather{(u64)S.found_before, (uint32_t)(S.found_before >> 64), S.found_bin}, [&](const Gather &got) {
+                const unsigned in = __ballot_sync(0xffffffffu, lane < G && got.c != 0);
+                if (lane == (in ? __ffs(in) - 1 : 0)) {
+                    S.bin = got.c;
+                    S.before = wide(got);
                 }
-        } else if (S.found_bin) {
-            bin = (int)S.found_bin - 1;
-            before = (Sum)S.found_before;
+            });
+            if (lost) return F_BINS - 1;
         }
-        return bin;
+        const uint32_t bin = G > 1 ? S.bin : S.found_bin;
+        before = bin ? (Sum)(G > 1 ? S.before : S.found_before) : above;
+        return bin ? (int)bin - 1 : F_BINS - 1;
     }
 
     // Collects the logits from `floor` on for which take(value) holds: up to F_LIST of them in
@@ -462,7 +576,8 @@ struct Row {
         block_minmax(kmin, kmax);
         // the lists and what each CTA says of its own are read from its shared memory
         if (tid == 0) S.said = Gather{(u64)S.n_cand, kmin, kmax};
-        sync();
+        publish();
+        if (lost) return 0;
         const Gather *got = &S.said;
         if constexpr (C > 1) {
             if (tid < C) S.heard[tid] = *cg::this_cluster().map_shared_rank(&S.said, tid);
@@ -500,7 +615,7 @@ struct Row {
         const float *src = list ? S.all : reinterpret_cast<const float *>(z4);
         const int n = list ? m : 4 * n4;
         u64 above = 0;
-        while (kmin < kmax) {
+        while (kmin < kmax && !lost) {
             int shift = 0;
             while (((kmax - kmin) >> shift) >= (uint32_t)F_BINS) ++shift;
             clear_hist();
@@ -634,8 +749,10 @@ struct Row {
             } else {
                 each([&](float x) { hist_add(S, step(x), 1ull); });
                 last = find_bin<C, u64>(0ull, target, -1.f, before);
+                if (lost) return floor;
             }
             const int m = collect(least, [&](float x) { return last == F_BINS || step(x) <= last; }, kmin, kmax);
+            if (lost) return floor;
             if (m <= k)
                 floor = of_key(kmin);  // (fewer: there are no more above -inf)
             else
@@ -657,9 +774,11 @@ struct Row {
             });
             u128 target = 0, before = 0;
             const int at = find_bin<C, u128>(0, target, top_p, before), units = step_frac(at);
+            if (lost) return floor;
             // what is wanted of the step, in its units, rounded up
             const u64 rest = (u64)((target - before + (1ull << (F_FRAC - units)) - 1) >> (F_FRAC - units));
             const int m = collect(floor, [&](float x) { return step(x) == at; }, kmin, kmax);
+            if (lost) return floor;
             uint32_t key = kmax;
             if (kmin != kmax)
                 key = m <= F_LIST ? border<true>(m, floor, units, rest, -1.f, kmin, kmax)
@@ -727,28 +846,13 @@ __device__ __forceinline__ float load_row(const T *src, int n, float *z, float &
     return most;
 }
 
+// The row's draw, by all threads of its CTAs.  false: nothing was exchanged.
 template <int NT, int C>
-__global__ void __launch_bounds__(NT, 1024 / NT) sample_filtered_kernel(const FilterArgs a) {
-    extern __shared__ __align__(16) float z[];  // this CTA's logits
-    __shared__ FilterShared S;
+__device__ __forceinline__ bool draw_row(const FilterArgs &a, Row<NT, C> &R, FilterShared &S, float *z, int row, int i0,
+                                         int n) {
     constexpr int NW = NT / 32;
-    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
-    const int row = blockIdx.x / C, rank = blockIdx.x % C;
-    const int i0 = rank * a.per, n = max(0, min(a.per, a.vocab - i0));
+    const int tid = R.tid, lane = R.lane, w = R.w, rank = R.rank;
     float *logprob = a.logprob ? a.logprob + row : nullptr;
-    Row<NT, C> R(S, z, n, rank, a.token + row, logprob);
-    for (int i = tid; i < 256; i += NT) S.pow2[i] = kPow2.v[i];
-    if constexpr (C > 1) {
-        if (tid == 0) {
-            mbar_init(&S.bar[0], 1);
-            mbar_init(&S.bar[1], 1);
-            fence_barrier_init();
-        }
-        R.sync();  // no message comes before the barriers are there
-    }
-    pdl_wait();
-    pdl_trigger();
-
     const float t = a.temperature ? a.temperature[row] : 1.f, top_p = a.top_p ? a.top_p[row] : 1.f;
     const float min_p = a.min_p ? a.min_p[row] : 0.f, u = a.u[row];
     const int top_k = a.top_k ? a.top_k[row] : 0;
@@ -756,7 +860,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) sample_filtered_kernel(const Fi
                       min_p <= 1.f && u >= 0.f && u < 1.f;
     if (!fine) {  // every CTA of the row sees the same
         if (rank == 0 && tid == 0) no_draw(a.token + row, logprob);
-        return;
+        return false;
     }
     const long long at = (long long)row * a.ld + i0;
     float least = INFINITY;
@@ -769,19 +873,19 @@ __global__ void __launch_bounds__(NT, 1024 / NT) sample_filtered_kernel(const Fi
     const int k = top_k > 0 && top_k < a.vocab ? top_k : 0;
     R.block_minmax(kmin, kmax);
     uint32_t bound = k > 1 && t > 0.f ? R.group_bound(own, k) : 0u;
-    const Gather *got = R.exchange(Gather{(u64)bound << 32 | (nan ? 1u : 0u), kmin, kmax});
-#pragma unroll
-    for (int r = 0; r < C; ++r) {
-        nan |= (got[r].a & 1) != 0;
-        bound = min(bound, (uint32_t)(got[r].a >> 32));
-        kmin = min(kmin, got[r].b);
-        kmax = max(kmax, got[r].c);
-    }
+    R.template exchange<C>(Gather{(u64)bound << 32 | (nan ? 1u : 0u), kmin, kmax}, [&](const Gather &got) {
+        const uint32_t lo = __reduce_min_sync(0xffffffffu, got.b), hi = __reduce_max_sync(0xffffffffu, got.c),
+                       bd = __reduce_min_sync(0xffffffffu, (uint32_t)(got.a >> 32));
+        const int bad = __any_sync(0xffffffffu, (got.a & 1) != 0);
+        if (lane == 0) S.kmin = lo, S.kmax = hi, S.bound = bd, S.nan = bad;
+    });
+    if (R.lost) return true;
+    kmin = S.kmin, kmax = S.kmax, bound = S.bound, nan = S.nan != 0;
     if (bound && bound <= key_of(-INFINITY)) bound = kmin;  // a CTA with few logits above -inf: then all of those
     float mx = of_key(kmax);
     if (nan || !(mx > -INFINITY)) {
         if (rank == 0 && tid == 0) no_draw(a.token + row, logprob);
-        return;
+        return true;
     }
     if (t == 0.f) {  // greedy
         uint32_t first = 0xffffffffu, unused = 0;
@@ -791,14 +895,15 @@ __global__ void __launch_bounds__(NT, 1024 / NT) sample_filtered_kernel(const Fi
                 break;
             }
         R.block_minmax(first, unused);
-        got = R.exchange(Gather{0ull, first, 0u});
-#pragma unroll
-        for (int r = 0; r < C; ++r) first = min(first, got[r].b);
-        if (rank == 0 && tid == 0) {
-            a.token[row] = (int)first;
+        R.last_exchange(Gather{0ull, first, 0u}, [&](const Gather &got) {
+            const uint32_t least_index = __reduce_min_sync(0xffffffffu, got.b);
+            if (lane == 0) S.first = least_index;
+        });
+        if (rank == 0 && tid == 0 && !R.lost) {
+            a.token[row] = (int)S.first;
             if (logprob) *logprob = 0.f;
         }
-        return;
+        return true;
     }
 
     const bool infinite = mx == INFINITY;
@@ -820,6 +925,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) sample_filtered_kernel(const Fi
     R.rs.step = R.rs.ch * (float)(1 << R.rs.oct);
 
     float floor = infinite ? 0.f : R.bounds(k, top_p, bound);
+    if (R.lost) return true;
     if (min_p > 0.f && !infinite) {
         if (tid == 0) S.floor = R.min_p_floor(min_p, t);
         __syncthreads();
@@ -841,19 +947,27 @@ __global__ void __launch_bounds__(NT, 1024 / NT) sample_filtered_kernel(const Fi
     __syncthreads();
     if (lane == 0) S.wsum[w] = own_mass;
     __syncthreads();
-    const u128 ws = lane < NW ? S.wsum[lane] : 0, wi = warp_scan(ws, lane), all = shfl(wi, 31);
-    u128 before = shfl(wi - ws, w);
-    got = R.exchange(Gather{(u64)all, (uint32_t)(all >> 64), 0u});
-    u128 total = 0;
-#pragma unroll
-    for (int r = 0; r < C; ++r) {
-        if (r < rank) before += wide(got[r]);
-        total += wide(got[r]);
+    // warp 0 finds the warp, if it is one of this CTA, whose range holds the crossing
+    u128 ws = 0, wi = 0, all = 0;
+    if (w == 0) {
+        ws = lane < NW ? S.wsum[lane] : 0;
+        wi = warp_scan(ws, lane);
+        all = shfl(wi, 31);
     }
-    const u128 goal = scaled(u, total, false);  // running > u * total <=> running > that
-    if (before > goal || goal >= before + own_mass) return;
-    // this warp's range holds the crossing
-    u128 left = goal - before;
+    R.last_exchange(Gather{(u64)all, (uint32_t)(all >> 64), 0u}, [&](const Gather &got) {
+        const u128 x = lane < C ? wide(got) : 0, xi = warp_scan(x, lane), total = shfl(xi, 31);
+        const u128 before = shfl(xi - x, rank) + wi - ws, goal = scaled(u, total, false);  // running > u * total <=> running > that
+        const bool mine_is_it = before <= goal && goal - before < ws;
+        const unsigned in = __ballot_sync(0xffffffffu, mine_is_it);
+        if (lane == 0) S.winner = in ? __ffs(in) - 1 : -1;
+        if (mine_is_it) {
+            S.left = goal - before;
+            S.total = total;
+        }
+    });
+    if (R.lost || w != S.winner) return true;
+    const u128 total = S.total;
+    u128 left = S.left;
     for (int c0 = 4 * q0; c0 < 4 * q1; c0 += 32) {
         const int i = c0 + lane;
         const float x = i < 4 * q1 ? z[i] : -INFINITY;
@@ -869,10 +983,34 @@ __global__ void __launch_bounds__(NT, 1024 / NT) sample_filtered_kernel(const Fi
                     *logprob = (x == mx ? 0.f : (x - mx) / t) - log1pf(more);
                 }
             }
-            return;
+            break;
         }
         left -= shfl(inc, 31);
     }
+    return true;
+}
+
+template <int NT, int C>
+__global__ void __launch_bounds__(NT, 1024 / NT) sample_filtered_kernel(const FilterArgs a) {
+    extern __shared__ __align__(16) float z[];  // this CTA's logits
+    __shared__ FilterShared S;
+    const int row = blockIdx.x / C, rank = blockIdx.x % C;
+    const int i0 = rank * a.per, n = max(0, min(a.per, a.vocab - i0));
+    Row<NT, C> R(S, z, n, rank, a);
+    for (int i = threadIdx.x; i < 256; i += NT) S.pow2[i] = kPow2.v[i];
+    if constexpr (C > 1) {
+        if (threadIdx.x == 0) {
+            mbar_init(&S.bar[0], 1);
+            mbar_init(&S.bar[1], 1);
+            mbar_init(&S.ready, C);
+            S.lost = 0;
+            fence_barrier_init();
+        }
+        cg::this_cluster().sync();  // no message comes before the barriers are there
+    }
+    pdl_wait();
+    pdl_trigger();
+    if (draw_row(a, R, S, z, row, i0, n)) R.leave(row);
 }
 
 constexpr int kMaxPer = 49152;   // logits of one CTA: 192 KB
@@ -927,34 +1065,67 @@ lf_status launch_filtered(FilterArgs a, cudaStream_t st) {
     }
 }
 
+#ifdef LF_DEBUG
+std::atomic<long long> g_wait_cycles{F_WAIT_CYCLES};
+std::atomic<int> g_lose_rank{-1}, g_lose_wait{0};
+#endif
+
 }  // namespace
+
+lf_status launch_sample_filtered(const void *logits, int dtype, int rows, int vocab, int64_t ld, const float *temperature,
+                                 const int32_t *top_k, const float *top_p, const float *min_p, const float *u,
+                                 int32_t *token, float *logprob, uint32_t *err, cudaStream_t stream) {
+    const int bytes = dtype_bytes(dtype);
+    auto off = [](const void *p, int b) { return (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(b - 1)) != 0; };
+    if (!bytes || !logits || !u || !token || rows < 0 || vocab < 1 || ld < vocab || off(logits, bytes) ||
+        off(temperature, 4) || off(top_k, 4) || off(top_p, 4) || off(min_p, 4) || off(u, 4) || off(token, 4) ||
+        off(logprob, 4))
+        return LF_ERR_INVALID_ARG;
+    if (vocab > F_MAX_VOCAB) return LF_ERR_UNSUPPORTED;
+    if (rows > (1 << 24)) return LF_ERR_INVALID_ARG;
+    if (rows == 0) return LF_OK;
+    FilterArgs a = {};
+    a.logits = logits;
+    a.dtype = dtype;
+    a.rows = rows;
+    a.vocab = vocab;
+    a.ld = ld;
+    a.temperature = temperature;
+    a.top_k = top_k;
+    a.top_p = top_p;
+    a.min_p = min_p;
+    a.u = u;
+    a.token = token;
+    a.logprob = logprob;
+    a.err = err;
+    a.wait_cycles = F_WAIT_CYCLES;
+#ifdef LF_DEBUG
+    a.wait_cycles = g_wait_cycles;
+    a.lose_rank = g_lose_rank;
+    a.lose_wait = g_lose_wait;
+#endif
+    return launch_filtered(a, stream);
+}
+
 }  // namespace lf
 
 extern "C" lf_status lf_sample_filtered(const void *logits_device, int dtype, int rows, int vocab, int64_t ld,
                                         const float *temperature_device, const int32_t *top_k_device,
                                         const float *top_p_device, const float *min_p_device, const float *u_device,
                                         int32_t *token_device, float *logprob_device, void *cuda_stream) {
-    const int bytes = lf::dtype_bytes(dtype);
-    auto off = [](const void *p, int b) { return (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(b - 1)) != 0; };
-    if (!bytes || !logits_device || !u_device || !token_device || rows < 0 || vocab < 1 || ld < vocab ||
-        off(logits_device, bytes) || off(temperature_device, 4) || off(top_k_device, 4) || off(top_p_device, 4) ||
-        off(min_p_device, 4) || off(u_device, 4) || off(token_device, 4) || off(logprob_device, 4))
-        return LF_ERR_INVALID_ARG;
-    if (vocab > lf::F_MAX_VOCAB) return LF_ERR_UNSUPPORTED;
-    if (rows > (1 << 24)) return LF_ERR_INVALID_ARG;
-    if (rows == 0) return LF_OK;
-    lf::FilterArgs a = {};
-    a.logits = logits_device;
-    a.dtype = dtype;
-    a.rows = rows;
-    a.vocab = vocab;
-    a.ld = ld;
-    a.temperature = temperature_device;
-    a.top_k = top_k_device;
-    a.top_p = top_p_device;
-    a.min_p = min_p_device;
-    a.u = u_device;
-    a.token = token_device;
-    a.logprob = logprob_device;
-    return lf::launch_filtered(a, static_cast<cudaStream_t>(cuda_stream));
+    return lf::launch_sample_filtered(logits_device, dtype, rows, vocab, ld, temperature_device, top_k_device, top_p_device,
+                                      min_p_device, u_device, token_device, logprob_device, nullptr,
+                                      static_cast<cudaStream_t>(cuda_stream));
+}
+
+extern "C" lf_status lf_debug_sample_wait(uint64_t limit_ns, int rank, int nth) {
+    if (limit_ns > 2000000000ull || rank < -1 || nth < 0) return LF_ERR_INVALID_ARG;
+#ifdef LF_DEBUG
+    lf::g_wait_cycles = (long long)limit_ns * 2;
+    lf::g_lose_rank = rank;
+    lf::g_lose_wait = nth;
+    return LF_OK;
+#else
+    return LF_ERR_UNSUPPORTED;
+#endif
 }

@@ -577,7 +577,9 @@ size_t lf_attn_paged_shared_workspace(const lf_paged_kv *kv, int n_q_heads);
  * below 2^-1075 is zero, as in 64-bit arithmetic, and never drawn.  A row
  * with a NaN, without a logit above -inf, or with a parameter outside its range
  * (T neither 0 nor in [1e-30, 1e30], top_p outside (0, 1], min_p outside [0, 1],
- * u outside [0, 1)) gets token -1 and logprob NaN.  rows 0 does nothing.
+ * u outside [0, 1)) gets token -1 and logprob NaN, and so does a row one of whose
+ * device-side waits ran out (2 s; they are between the CTAs that share a row of a
+ * large vocabulary).  rows 0 does nothing.
  * LF_ERR_INVALID_ARG for bad sizes, types or pointers; LF_ERR_UNSUPPORTED for
  * a vocabulary above 262144. */
 lf_status lf_sample_filtered(const void *logits_device, int dtype, int rows, int vocab, int64_t ld,
@@ -601,11 +603,16 @@ lf_status lf_sample_filtered(const void *logits_device, int dtype, int rows, int
  * number of guarded buffers to *n_guarded (nullable): LF_OK, or
  * LF_ERR_BOUNDS for an overwritten canary.  lf_debug_corrupt_canary writes
  * one word into the front (back = 0) or back canary of guarded buffer i,
- * from the host, so that a test can see the check fire.  Both return
- * LF_ERR_UNSUPPORTED in the release library.
+ * from the host, so that a test can see the check fire.
+ *
+ * lf_debug_sample_wait sets, for this process, the limit of the waits of
+ * lf_sample_filtered (at most 2 s, the usual one) and has the CTA `rank` of each row (-1: every CTA) give up
+ * in its nth wait (0: in none), so that a test can see a wait run out.
+ * The three return LF_ERR_UNSUPPORTED in the release library.
  */
 lf_status lf_debug_canaries(lf_engine *e, int *n_guarded);
 lf_status lf_debug_corrupt_canary(lf_engine *e, int i, int back);
+lf_status lf_debug_sample_wait(uint64_t limit_ns, int rank, int nth);
 
 /* Measurement call, not a step of the decode: one read of `bytes` of device
  * memory at `src_device` in the decode kernel's weight-copy pattern (one CTA
