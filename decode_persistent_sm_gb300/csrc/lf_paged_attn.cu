@@ -629,20 +629,14 @@ template <typename T, int DH>
 __global__ void __launch_bounds__(PA_THREADS, PA_CTAS_PER_SM) paged_attn_kernel(const AttnArgs a) {
     extern __shared__ __align__(128) uint8_t pa_smem[];
     Walker<T, DH> w(a, pa_smem);
-    // With the tensor-core kernel in front, which triggers this one after its own
-    // wait, all that is read here is already there and what is written is apart
-    // from that kernel's partials: this one runs beside it, and its last CTA waits
-    // at its end, so that the join behind it finds both done.
-    if (!a.tc)
-        pdl_wait();
-    else
-        __threadfence();  // nothing older than that kernel's wait out of this SM's L1
+    // (Behind the tensor-core kernel too.  Its trigger lets these CTAs become
+    // resident as its own leave, but only the wait makes visible what the kernels
+    // before it wrote.)
+    pdl_wait();
     pdl_trigger();
     w.plan();
     w.run();
-    if (a.tc && blockIdx.x == gridDim.x - 1) pdl_wait();
 }
-
 
 // A cluster per (sequence, KV head) and no other launch: for few keys.
 template <typename T, int DH>
@@ -817,24 +811,27 @@ WsLayout ws_layout(const AttnArgs &a) {
 // The tensor-core kernel takes head_dim 64 and 128, pages of at least 8 positions
 // (a TMA box) and page strides that a tensor map can hold (2^40 bytes).
 bool tc_possible(const PagedView &v) { return v.head_dim >= 64 && v.ps_log2 >= 3 && v.page_stride < (1ll << 38); }
-// It costs one more launch, which leaves the other kernel about 4 us later, and
-// its 128-row tiles idle where there are few rows; it gains as the common
-// products grow.  Both measured (us, warp-level MMAs | tensor cores), 64 own
-// positions at most, by rows of a KV head x common positions:
-//   head_dim 128, 8 KV heads:   64 x 4096 19.5 | 21.5   64 x 16384 30.9 | 26.2
-//                              128 x 4096 21.9 | 23.3  128 x 6000  25.3 | 24.8
-//                              128 x 16384 42.3 | 29.6  33 x 16384 28.8 | 22.3
-//   head_dim 128, 16 KV heads:  64 x 4096 23.0 | 23.3   64 x 8192  30.4 | 29.0
-//                               32 x 16384 37.4 | 38.6 256 x 16384 127 | 53
-//   head_dim 64, 16 KV heads:   64 x 16384 30.1 | 32.8 128 x 8192  30.1 | 26.2
-//   head_dim 64, 8 KV heads:   128 x 11500 23.5 | 22.4  96 x 16384 28.6 | 23.4
-// so: by the size of the common products, and not where half of a row tile (a
-// quarter at head_dim 128) would be empty.  With a window at most that many
-// positions are common.
-bool tc_pays(const AttnArgs &a) {
+// It costs one more launch and a second start (8 to 10 us; the own items wait for
+// all of it), its 128-row tiles idle where there are few rows, and each CTA leaves a
+// partial of up to 256 rows; it gains as the common products grow.  Both measured
+// (us, warp-level MMAs | tensor cores), 64 own positions, common ones in whole
+// pages, by rows of a KV head x common positions:
+//   head_dim 128, 8 KV heads:   64 x 15232 31.4 | 29.3   64 x 25920 41.8 | 39.9   33 x 29568 42.4 | 40.1
+//                              128 x 4544  22.3 | 23.3  128 x 7616  28.0 | 25.3  128 x 18304 45.8 | 36.6
+//                              256 x 3813  27.5 | 30.1  256 x 9189  43.3 | 33.5  512 x 3200 37.3 | 39.2
+//   head_dim 128, 16 KV heads:  64 x 9856  34.4 | 34.6  128 x 3776  28.3 | 30.4  128 x 6464 37.8 | 33.4
+//                              256 x 3237  37.3 | 41.8  256 x 4581  45.8 | 35.6   32 x 16384 37.3 | 42.2
+//   head_dim 64, 8 KV heads:    64 x 39616 35.1 | 38.5  128 x 15232 28.3 | 26.4  256 x 7653 27.3 | 24.6
+//   head_dim 64, 16 KV heads:  128 x 9856  33.0 | 30.1  512 x 3776 28.4 | 29.7 (8 KV heads), 512 x 2432 38.9 | 34.3
+// so: by the size of the common products, not where half of a row tile (a quarter at
+// head_dim 128) would be empty, and from three key tiles a CTA on, which pay for its
+// partial.  With a window at most that many positions are common.  (Over 150
+// such sizes from 0.5e9 to 2.4e9 the rule is 1 % off the better choice, 10 % at most.)
+bool tc_pays(const AttnArgs &a, int n_sm) {
     const long long rows = (long long)a.kv.n_seqs * a.group, keys = a.window > 0 ? std::min(a.window, a.shared) : a.shared;
-    return rows > (a.kv.head_dim == 128 ? 32 : 64) &&
-           (double)rows * (double)keys * a.kv.n_kv * a.kv.head_dim >= 7.5e8;
+    const long long tiles = keys / kTcKeys * ((rows + kTcRows - 1) / kTcRows) * a.kv.n_kv;
+    return rows > (a.kv.head_dim == 128 ? 32 : 64) && tiles >= 3 * n_sm &&
+           (double)rows * (double)keys * a.kv.n_kv * a.kv.head_dim >= 9.5e8;
 }
 
 size_t ws_bytes(AttnArgs a, int n_sm) {
@@ -924,7 +921,7 @@ extern "C" lf_status lf_attn_paged_shared(const lf_paged_kv *kv, const void *q_d
     if (workspace_bytes < lf::ws_bytes(a, n_sm)) return LF_ERR_INVALID_ARG;
     a.shared = shared_len;
     a.window = window;
-    lf::common_shape(a, lf::tc_possible(a.kv) && lf::tc_pays(a), n_sm);
+    lf::common_shape(a, lf::tc_possible(a.kv) && lf::tc_pays(a, n_sm), n_sm);
     const lf::WsLayout w = lf::ws_layout(a);
     uint8_t *ws = static_cast<uint8_t *>(workspace_device);
     a.plan = reinterpret_cast<int *>(ws);

@@ -21,14 +21,15 @@
 //
 // Measured: 64 sequences x 8 heads per KV head (512 rows), 8 KV heads of 128, 16384
 // common positions, BF16: 35 us, 980 TFLOP/s (51 % of the measured dense rate; the
-// tensor pipe is active 41 % of the time).  The whole call 74.0 us, of which the
-// sequences' own positions take 31 (142 MB); on warp-level MMAs alone 161.  A step
+// tensor pipe is active 41 % of the time).  The whole call 85 us: behind it the
+// kernel of the sequences' own positions starts (6 to 8 us) and reads them (31 us,
+// 142 MB); on warp-level MMAs alone 161.  A step
 // (128 keys, both row tiles) takes 3700 cycles for 2048 of products.  Its chain is
 // softmax (1400: load 100, max 200, exponentials 800, store and fence 160), then P V
 // and Q K^T (512 each, and 340 until the result is seen).  Around the products the
 // issuing thread's own instructions count, some 300 cycles for a wait even when it
 // is over: so one wait for V and the next K, counters and descriptors in
-// registers, no barrier that nobody waits for (79.2 -> 74.0 us).  Slower: a thread
+// registers, no barrier that nobody waits for (-5 us).  Slower: a thread
 // per half row (16 softmax warps, +8 %), an issuing warp per row tile (their products
 // interleave and delay both, +2 %), tiles of 64 keys with two buffers of S (+30 %: twice
 // as many waits).
