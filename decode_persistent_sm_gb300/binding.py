@@ -243,6 +243,14 @@ def sample_filtered(logits_ptr: int, dtype: str, rows: int, vocab: int, ld: int,
         _check("lf_sample_filtered", rc)
 
 
+def _round_down(u) -> np.ndarray:
+    """u as fp32, each value the largest that is not above it."""
+    u = np.asarray(u)
+    with np.errstate(over="ignore"):
+        r = np.ascontiguousarray(u, dtype=np.float32)
+    return np.ascontiguousarray(np.where(r > u, np.nextafter(r, np.float32(-np.inf)), r))
+
+
 def validate_config(cfg: LfConfig) -> int:
     return load_library().lf_validate_config(ctypes.byref(cfg))
 
@@ -381,11 +389,12 @@ class Engine:
 
     def batch_generate_filtered(self, first_tokens: Sequence[int], u, temperature=None, top_k=None, top_p=None,
                                 min_p=None):
-        """lf_batch_generate_filtered: u [B][n] uniform numbers, one per draw;
-        temperature, top_k, top_p, min_p one value for all samples, one per
-        sample, or None.  Returns (tokens [B][n], logprobs [B][n])."""
+        """lf_batch_generate_filtered: u [B][n] uniform numbers in [0, 1), one per
+        draw (rounded down to fp32, so that none becomes 1); temperature,
+        top_k, top_p, min_p one value for all samples, one per sample, or None.
+        Returns (tokens [B][n], logprobs [B][n])."""
         t = np.ascontiguousarray(np.asarray(first_tokens, dtype=np.int32))
-        u = np.ascontiguousarray(np.asarray(u, dtype=np.float32))
+        u = _round_down(u)
         if u.ndim != 2 or u.shape[0] != t.size:
             raise ValueError(f"u must be [{t.size}][steps], got {u.shape}")
 
