@@ -367,10 +367,19 @@ class Engine:
         _check("lf_batch_info", self._lib.lf_batch_info(self._h, ctypes.byref(nb), ctypes.byref(pos)))
         return nb.value, pos.value
 
+    def _batch_tokens(self, tokens: Sequence[int]) -> np.ndarray:
+        """One token per sample of the batch: the library reads, and writes its
+        results, for as many as there are."""
+        t = np.ascontiguousarray(np.asarray(tokens, dtype=np.int32))
+        n, _ = self.batch_info()
+        if n and t.shape != (n,):
+            raise ValueError(f"{t.size} tokens for a batch of {n} samples")
+        return t
+
     def batch_step(self, tokens: Sequence[int], logits: bool = True):
         """lf_batch_step: one step of every sample; returns (logits [B][vocab]
         or None, argmax [B])."""
-        t = np.ascontiguousarray(np.asarray(tokens, dtype=np.int32))
+        t = self._batch_tokens(tokens)
         am = np.full(t.size, -1, dtype=np.int32)
         out = np.empty((t.size, self.vocab), dtype=np.float32) if logits else None
         rc = self._lib.lf_batch_step(self._h, t.ctypes.data, out.ctypes.data if logits else None, am.ctypes.data)
@@ -380,7 +389,7 @@ class Engine:
     def batch_generate(self, first_tokens: Sequence[int], n: int, temperature: float, top_p: float, seed: int):
         """lf_batch_generate: n sampled steps of every sample (sample b draws
         from Philox stream (seed, position, b)); returns tokens [B][n]."""
-        t = np.ascontiguousarray(np.asarray(first_tokens, dtype=np.int32))
+        t = self._batch_tokens(first_tokens)
         out = np.zeros((t.size, int(n)), dtype=np.int32)
         rc = self._lib.lf_batch_generate(self._h, t.ctypes.data, int(n), float(temperature), float(top_p),
                                          int(seed) & (2 ** 64 - 1), out.ctypes.data)
@@ -393,7 +402,7 @@ class Engine:
         draw (rounded down to fp32, so that none becomes 1); temperature,
         top_k, top_p, min_p one value for all samples, one per sample, or None.
         Returns (tokens [B][n], logprobs [B][n])."""
-        t = np.ascontiguousarray(np.asarray(first_tokens, dtype=np.int32))
+        t = self._batch_tokens(first_tokens)
         u = _round_down(u)
         if u.ndim != 2 or u.shape[0] != t.size:
             raise ValueError(f"u must be [{t.size}][steps], got {u.shape}")

@@ -1,6 +1,7 @@
 """What the binding hands to the batch calls (no GPU needed: a stand-in for the
 library records the arguments): uniform numbers rounded to fp32 stay below what they
-were, so a valid one is never refused."""
+were, so a valid one is never refused; and a call with more or fewer tokens than
+the batch has samples does not reach the library."""
 import ctypes
 
 import numpy as np
@@ -20,6 +21,14 @@ class Library:
     def lf_batch_generate_filtered(self, h, first, steps, t, k, p, mp, u, out, lp):
         assert self.n > 0
         self.calls.append(np.ctypeslib.as_array(ctypes.cast(u, ctypes.POINTER(ctypes.c_float)), (self.n, steps)).copy())
+        return 0
+
+    def lf_batch_step(self, *a):
+        self.calls.append("step")
+        return 0
+
+    def lf_batch_generate(self, *a):
+        self.calls.append("generate")
         return 0
 
     def lf_destroy(self, h):
@@ -67,3 +76,24 @@ def test_any_layout_of_u():
         e.batch_generate_filtered([1] * 7, view)
         got = e._lib.calls[0].astype(np.float64)
         assert (got <= view).all() and np.abs(got - view).max() < 2.0 ** -23
+
+
+@pytest.mark.parametrize("have,given", [(3, 2), (3, 4), (1, 0), (16, 1)])
+def test_a_token_for_each_sample_of_the_batch(have, given):
+    # the library reads and writes as many as the batch has samples
+    tokens = [1] * given
+    for call in (lambda e: e.batch_step(tokens), lambda e: e.batch_step(tokens, logits=False),
+                 lambda e: e.batch_generate(tokens, 4, 0.8, 0.9, 1),
+                 lambda e: e.batch_generate_filtered(tokens, np.full((given, 4), 0.5))):
+        e = engine(have)
+        with pytest.raises(ValueError, match=f"{have} samples"):
+            call(e)
+        assert not e._lib.calls
+
+
+def test_without_a_batch_the_library_answers():
+    from decode_persistent_sm_gb300 import LaneformerError
+    e = engine(0)
+    e._lib.lf_batch_step = lambda *a: 4
+    with pytest.raises(LaneformerError, match="NOT_LOADED"):
+        e.batch_step([1, 2])
