@@ -32,6 +32,7 @@
 #include <cfloat>
 #include <climits>
 #include <cmath>
+#include <memory>
 #include <mutex>
 #include <new>
 #include <vector>
@@ -519,6 +520,17 @@ void carve(BatchState &b, uint8_t *base, const lf::Shape &s, int B) {
     b.bytes = at;
 }
 
+// Where lf_batch_begin allocates on the host; lf_debug_fail_alloc lets one of
+// these places run out of memory.
+#ifdef LF_DEBUG
+int g_fail_alloc = 0;
+void alloc_point() {
+    if (g_fail_alloc > 0 && --g_fail_alloc == 0) throw std::bad_alloc();
+}
+#else
+inline void alloc_point() {}
+#endif
+
 void batch_release(BatchState *b) {
     if (!b) return;
     if (b->graph) cudaGraphExecDestroy(b->graph);
@@ -528,6 +540,43 @@ void batch_release(BatchState *b) {
     if (b->mem) cudaFree(b->mem);
     delete b;
 }
+struct BatchRelease {
+    void operator()(BatchState *b) const { batch_release(b); }
+};
+
+// Events and an open capture, ended whichever way their scope is left.
+struct Events {
+    std::vector<cudaEvent_t> v;
+    explicit Events(size_t n) : v(n, nullptr) {}
+    ~Events() {
+        for (cudaEvent_t e : v)
+            if (e) cudaEventDestroy(e);
+    }
+    bool create() {
+        for (cudaEvent_t &e : v)
+            if (cudaEventCreateWithFlags(&e, cudaEventDisableTiming) != cudaSuccess) {
+                e = nullptr;
+                return false;
+            }
+        return true;
+    }
+    cudaEvent_t operator[](size_t i) const { return v[i]; }
+};
+struct Capture {
+    cudaStream_t stream;
+    bool open = true;
+    cudaError_t end(cudaGraph_t *g) {
+        open = false;
+        return cudaStreamEndCapture(stream, g);
+    }
+    ~Capture() {
+        cudaGraph_t g = nullptr;
+        if (!open) return;
+        (void)end(&g);
+        if (g) cudaGraphDestroy(g);
+        (void)cudaGetLastError();
+    }
+};
 
 // Every kernel of one step, captured from `main` into the graph.  Under the
 // delayed sum, sub-block s reads only the partials of sub-blocks up to
@@ -559,23 +608,14 @@ lf_status enqueue_batch_step(lf_engine *e, BatchState &b, cudaStream_t main) {
         a.timeout_ns = kBatchTimeoutNs;
         return a;
     };
-    std::vector<cudaEvent_t> ev_norm(2 * L), ev_part(2 * L);
-    auto destroy = [&] {
-        for (cudaEvent_t v : ev_norm)
-            if (v) cudaEventDestroy(v);
-        for (cudaEvent_t v : ev_part)
-            if (v) cudaEventDestroy(v);
-    };
-    for (int i = 0; i < 2 * L; ++i)
-        if (cudaEventCreateWithFlags(&ev_norm[i], cudaEventDisableTiming) != cudaSuccess ||
-            cudaEventCreateWithFlags(&ev_part[i], cudaEventDisableTiming) != cudaSuccess) {
-            destroy();
-            return LF_ERR_CUDA;
-        }
+    alloc_point();
+    Events ev_norm(2 * L), ev_part(2 * L);
+    if (!ev_norm.create() || !ev_part.create()) return LF_ERR_CUDA;
     lf_status gs = LF_OK;
     ba_embed<<<B, 256, 0, main>>>(e->emb, b.tok, b.x, D, s.V, b.err);
     for (int sb = 0; sb < 2 * L && gs == LF_OK; ++sb) {
         const int l = sb / 2, ua = sb - 1 - 2 * s.delay;
+        alloc_point();
         __half *h = b.h16 + (size_t)sb * BD;
         const __half *gain = e->gains + (size_t)(sb % 2 == 0 ? l : L + l) * D;
         if (ua >= 0) cudaStreamWaitEvent(main, ev_part[ua], 0);
@@ -659,7 +699,6 @@ lf_status enqueue_batch_step(lf_engine *e, BatchState &b, cudaStream_t main) {
     // loop draws its tokens from the logits with the sampler)
     if (gs == LF_OK) ba_bump<<<1, 1, 0, main>>>(b.d_pos);
     if (gs == LF_OK && b.shared) ba_bump_each<<<1, B, 0, main>>>(b.spos, b.slen);
-    destroy();
     if (gs != LF_OK) return gs;
     return cudaGetLastError() == cudaSuccess ? LF_OK : LF_ERR_CUDA;
 }
@@ -709,10 +748,13 @@ lf_status batch_begin(lf_engine *e, int n_batch, bool shared) {
     if (lf::gemv_tc_prepare() != LF_OK) return LF_ERR_CUDA;
     const lf_status ts = ensure_tiled(e);
     if (ts != LF_OK) return ts == LF_ERR_CUDA ? (e->poisoned = LF_ERR_CUDA) : ts;
-    BatchState *b = new BatchState();
+    alloc_point();
+    std::unique_ptr<BatchState, BatchRelease> own(new BatchState());
+    BatchState *b = own.get();
     b->B = n_batch;
     // split-K workspace and counters: a region per GEMV of the step
     const std::vector<std::array<int, 3>> shapes = gemv_shapes(s);
+    alloc_point();
     b->ws_off.assign(1, 0);
     b->cnt_off.assign(1, 0);
     for (auto &sh : shapes) {
@@ -735,22 +777,32 @@ lf_status batch_begin(lf_engine *e, int n_batch, bool shared) {
         kv.k = kv.v = reinterpret_cast<void *>(uintptr_t(256));  // only the sizes count here
         kv.page_table = reinterpret_cast<const int32_t *>(uintptr_t(256));
         b->pws_bytes = al256(lf_attn_paged_shared_workspace(&kv, s.NQ));
-        if (!b->pws_bytes) {
-            batch_release(b);
-            return LF_ERR_UNSUPPORTED;
-        }
+        if (!b->pws_bytes) return LF_ERR_UNSUPPORTED;
+    }
+    // what the host copies from below is all there before the first copy
+    alloc_point();
+    b->work.assign(2 * s.delay + 1, nullptr);
+    std::vector<int2> kvsrc(s.NKV);
+    std::vector<int> table, pos, len;
+    if (shared) {
+        // sample i's row: the whole pages of the prefix, then pages of its own; sample 0's first own page also takes
+        // the prefix's last, incomplete one
+        table.resize((size_t)n_batch * b->max_pages);
+        pos.assign(n_batch, e->pos);
+        len.assign(n_batch, e->pos + 1);
+        for (int i = 0; i < n_batch; ++i)
+            for (int g = 0; g < b->max_pages; ++g)
+                table[(size_t)i * b->max_pages + g] = g < whole ? g : whole + i * (b->max_pages - whole) + g - whole;
     }
     carve(*b, nullptr, s, n_batch);
     if (cudaMalloc(&b->mem, b->bytes) != cudaSuccess) {
         (void)cudaGetLastError();
         b->mem = nullptr;
-        batch_release(b);
         return LF_ERR_OOM;
     }
     carve(*b, static_cast<uint8_t *>(b->mem), s, n_batch);
-    e->batch = b;
+    e->batch = own.release();
 
-    std::vector<int2> kvsrc(s.NKV);
     for (int kh = 0; kh < s.NKV; ++kh)
         for (int lam = s.NL - 1; lam >= 0; --lam)
             if (s.kv_first[lam] <= kh && kh < s.kv_first[lam] + s.HKV_L) kvsrc[kh] = make_int2(lam, kh - s.kv_first[lam]);
@@ -761,12 +813,6 @@ lf_status batch_begin(lf_engine *e, int n_batch, bool shared) {
     b->pos = e->pos;
     if (err == cudaSuccess) err = cudaMemcpyAsync(b->d_pos, &b->pos, sizeof(int), cudaMemcpyHostToDevice, st);
     if (shared) {
-        // sample i's row: the whole pages of the prefix, then pages of its own; sample 0's first own page also takes
-        // the prefix's last, incomplete one
-        std::vector<int> table((size_t)n_batch * b->max_pages), pos(n_batch, e->pos), len(n_batch, e->pos + 1);
-        for (int i = 0; i < n_batch; ++i)
-            for (int g = 0; g < b->max_pages; ++g)
-                table[(size_t)i * b->max_pages + g] = g < whole ? g : whole + i * (b->max_pages - whole) + g - whole;
         const size_t nb = (size_t)n_batch * sizeof(int);
         if (err == cudaSuccess) err = cudaMemcpyAsync(b->table, table.data(), table.size() * sizeof(int), cudaMemcpyHostToDevice, st);
         if (err == cudaSuccess) err = cudaMemcpyAsync(b->spos, pos.data(), nb, cudaMemcpyHostToDevice, st);
@@ -774,7 +820,6 @@ lf_status batch_begin(lf_engine *e, int n_batch, bool shared) {
         if (err == cudaSuccess && e->pos > 0)
             ba_copy_prefix_paged<<<dim3(s.L * s.NKV, (e->pos + lf::kBatchPage - 1) / lf::kBatchPage), 256, 0, st>>>(
                 e->kc, e->vc, b->kc, b->vc, b->kvsrc, b->table, e->pos, s.L, s.NKV, s.HKV_L, s.DH, s.ctx, b->n_pages);
-        if (err == cudaSuccess) err = cudaStreamSynchronize(st);  // the host arrays go out of scope
     } else if (err == cudaSuccess && e->pos > 0)
         ba_copy_prefix<<<dim3(s.L * s.NKV, n_batch), 256, 0, st>>>(e->kc, e->vc, b->kc, b->vc, b->kvsrc, e->pos, s.L,
                                                                   s.NKV, s.HKV_L, s.DH, s.ctx);
@@ -784,16 +829,16 @@ lf_status batch_begin(lf_engine *e, int n_batch, bool shared) {
 
     // capture one step
     if (cudaStreamCreateWithFlags(&b->cap, cudaStreamNonBlocking) != cudaSuccess) return batch_fail(e, LF_ERR_CUDA);
-    b->work.assign(2 * s.delay + 1, nullptr);
     for (cudaStream_t &w : b->work)
         if (cudaStreamCreateWithFlags(&w, cudaStreamNonBlocking) != cudaSuccess) {
             w = nullptr;
             return batch_fail(e, LF_ERR_CUDA);
         }
     if (cudaStreamBeginCapture(b->cap, cudaStreamCaptureModeRelaxed) != cudaSuccess) return batch_fail(e, LF_ERR_CUDA);
+    Capture capture{b->cap};
     const lf_status qs = enqueue_batch_step(e, *b, b->cap);
     cudaGraph_t g = nullptr;
-    const cudaError_t ce = cudaStreamEndCapture(b->cap, &g);
+    const cudaError_t ce = capture.end(&g);
     if (qs != LF_OK || ce != cudaSuccess) {
         if (g) cudaGraphDestroy(g);
         (void)cudaGetLastError();
@@ -809,16 +854,31 @@ lf_status batch_begin(lf_engine *e, int n_batch, bool shared) {
     return LF_OK;
 }
 
-}  // namespace
-
-extern "C" lf_status lf_batch_begin(lf_engine *e, int n_batch) { return batch_begin(e, n_batch, false); }
-
-extern "C" lf_status lf_batch_begin_shared(lf_engine *e, int n_batch) {
+// Without host memory there is no batch, and nothing of one is left.
+lf_status begin(lf_engine *e, int n_batch, bool shared) {
     try {
-        return batch_begin(e, n_batch, true);
+        return batch_begin(e, n_batch, shared);
     } catch (const std::bad_alloc &) {
+        if (e->stream) cudaStreamSynchronize(e->stream);
+        lf_batch_free(e);
         return LF_ERR_OOM;
     }
+}
+
+}  // namespace
+
+extern "C" lf_status lf_batch_begin(lf_engine *e, int n_batch) { return begin(e, n_batch, false); }
+
+extern "C" lf_status lf_batch_begin_shared(lf_engine *e, int n_batch) { return begin(e, n_batch, true); }
+
+extern "C" lf_status lf_debug_fail_alloc(int nth) {
+    if (nth < 0) return LF_ERR_INVALID_ARG;
+#ifdef LF_DEBUG
+    g_fail_alloc = nth;
+    return LF_OK;
+#else
+    return LF_ERR_UNSUPPORTED;
+#endif
 }
 
 extern "C" lf_status lf_batch_end(lf_engine *e) {

@@ -608,11 +608,15 @@ lf_status lf_sample_filtered(const void *logits_device, int dtype, int rows, int
  * lf_debug_sample_wait sets, for this process, the limit of the waits of
  * lf_sample_filtered (at most 2 s, the usual one) and has the CTA `rank` of each row (-1: every CTA) give up
  * in its nth wait (0: in none), so that a test can see a wait run out.
- * The three return LF_ERR_UNSUPPORTED in the release library.
+ *
+ * lf_debug_fail_alloc lets the nth (0: none) of the places where the next
+ * lf_batch_begin or lf_batch_begin_shared allocates host memory find none.
+ * These calls return LF_ERR_UNSUPPORTED in the release library.
  */
 lf_status lf_debug_canaries(lf_engine *e, int *n_guarded);
 lf_status lf_debug_corrupt_canary(lf_engine *e, int i, int back);
 lf_status lf_debug_sample_wait(uint64_t limit_ns, int rank, int nth);
+lf_status lf_debug_fail_alloc(int nth);
 
 /* Measurement call, not a step of the decode: one read of `bytes` of device
  * memory at `src_device` in the decode kernel's weight-copy pattern (one CTA
