@@ -77,6 +77,7 @@ _SIGS = {
     "lf_debug_corrupt_canary": (_ci, [_vp, _ci, _ci]),
     "lf_debug_sample_wait": (_ci, [ctypes.c_uint64, _ci, _ci]),
     "lf_debug_fail_alloc": (_ci, [_ci]),
+    "lf_debug_batch_error": (_ci, [_vp, ctypes.c_uint32]),
 }
 
 

@@ -705,7 +705,7 @@ lf_status enqueue_batch_step(lf_engine *e, BatchState &b, cudaStream_t main) {
 
 lf_status batch_fail(lf_engine *e, lf_status st) {
     if (e->batch) e->batch->ready = false;
-    if (st == LF_ERR_CUDA || st == LF_ERR_TIMEOUT) e->poisoned = st;
+    if (st == LF_ERR_CUDA || st == LF_ERR_TIMEOUT || st == LF_ERR_BOUNDS) e->poisoned = st;
     return st;
 }
 
@@ -720,6 +720,7 @@ lf_status batch_finish(lf_engine *e, BatchState &b) {
         return batch_fail(e, LF_ERR_CUDA);
     }
     if (werr == 6) return batch_fail(e, LF_ERR_INVALID_ARG);
+    if (werr == 1) return batch_fail(e, LF_ERR_BOUNDS);  // a page, length or position outside the batch's paged cache
     if (werr) return batch_fail(e, LF_ERR_TIMEOUT);
     return LF_OK;
 }
@@ -877,6 +878,19 @@ extern "C" lf_status lf_debug_fail_alloc(int nth) {
     g_fail_alloc = nth;
     return LF_OK;
 #else
+    return LF_ERR_UNSUPPORTED;
+#endif
+}
+
+extern "C" lf_status lf_debug_batch_error(lf_engine *e, uint32_t word) {
+    if (!e) return LF_ERR_INVALID_ARG;
+#ifdef LF_DEBUG
+    if (!e->batch || !e->batch->ready) return LF_ERR_NOT_LOADED;
+    const cudaError_t err = cudaMemcpy(e->batch->err, &word, sizeof(word), cudaMemcpyHostToDevice);
+    if (err != cudaSuccess) (void)cudaGetLastError();
+    return err == cudaSuccess ? LF_OK : LF_ERR_CUDA;
+#else
+    (void)word;
     return LF_ERR_UNSUPPORTED;
 #endif
 }

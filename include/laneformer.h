@@ -42,8 +42,9 @@ typedef enum {
     LF_ERR_CTX_OVERFLOW = 5,  /* the position would reach ctx_cap */
     LF_ERR_TIMEOUT = 6,       /* a bounded device-side wait ran out */
     LF_ERR_UNSUPPORTED = 7,   /* a valid config this build has no kernel for */
-    LF_ERR_BOUNDS = 8         /* debug build only: a device-side bounds check or a
-                                 canary around an engine buffer failed */
+    LF_ERR_BOUNDS = 8         /* a device-side bounds check (the debug build's, or the
+                                 paged cache's of a batch) or a canary around an
+                                 engine buffer (debug build) failed */
 } lf_status;
 
 /*
@@ -403,7 +404,8 @@ lf_status lf_batch_info(const lf_engine *e, int *n_batch, int *position);
  * sample.  Synchronous; advances the batch position by one.
  * LF_ERR_NOT_LOADED without lf_batch_begin; LF_ERR_INVALID_ARG for a token
  * outside [0, vocab); LF_ERR_CTX_OVERFLOW at position == ctx_cap;
- * LF_ERR_TIMEOUT / LF_ERR_CUDA poison the engine (and end the batch). */
+ * LF_ERR_TIMEOUT / LF_ERR_CUDA (and LF_ERR_BOUNDS: the batch's own pages or
+ * lengths are damaged) poison the engine and end the batch. */
 lf_status lf_batch_step(lf_engine *e, const int32_t *tokens, float *logits, int32_t *argmax);
 
 /* n_steps sampled steps of every sample, the draw of lf_generate_sampled:
@@ -611,12 +613,15 @@ lf_status lf_sample_filtered(const void *logits_device, int dtype, int rows, int
  *
  * lf_debug_fail_alloc lets the nth (0: none) of the places where the next
  * lf_batch_begin or lf_batch_begin_shared allocates host memory find none.
+ * lf_debug_batch_error writes the error word of the current batch, as its kernels
+ * do, for the next batch call to find.
  * These calls return LF_ERR_UNSUPPORTED in the release library.
  */
 lf_status lf_debug_canaries(lf_engine *e, int *n_guarded);
 lf_status lf_debug_corrupt_canary(lf_engine *e, int i, int back);
 lf_status lf_debug_sample_wait(uint64_t limit_ns, int rank, int nth);
 lf_status lf_debug_fail_alloc(int nth);
+lf_status lf_debug_batch_error(lf_engine *e, uint32_t word);
 
 /* Measurement call, not a step of the decode: one read of `bytes` of device
  * memory at `src_device` in the decode kernel's weight-copy pattern (one CTA

@@ -16,3 +16,9 @@ def test_allocation_failure(libs):
     assert rel.lf_debug_fail_alloc(1) == 7  # LF_ERR_UNSUPPORTED
     assert rel.lf_debug_fail_alloc(-1) == dbg.lf_debug_fail_alloc(-1) == 1
     assert dbg.lf_debug_fail_alloc(3) == dbg.lf_debug_fail_alloc(0) == 0
+
+
+def test_batch_error_word(libs):
+    # (no engine needed: a null engine is refused first)
+    for lib in libs:
+        assert lib.lf_debug_batch_error(None, 1) == 1
