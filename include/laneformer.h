@@ -526,7 +526,8 @@ lf_status lf_kv_append_paged(const lf_paged_kv *kv, const void *q_in, const void
  *   lens_device: DEVICE int32 [n_seqs]; a sequence of length 0 gets zeros and
  *   lse -inf;
  *   max_len: upper bound of the lengths (a tight one lets a short batch take the
- *   shortest way);
+ *   shortest way), at least shared_len; where every sequence ends inside the
+ *   common positions, max_len is as good a shared_len;
  *   scale: above 0, scale * log2(e) finite;
  *   workspace_device: DEVICE scratch of at least
  *   lf_attn_paged_shared_workspace bytes, 256-byte aligned; it needs no
@@ -538,8 +539,8 @@ lf_status lf_kv_append_paged(const lf_paged_kv *kv, const void *q_in, const void
  * length outside [0, max_len] (taken as 0) or a page outside the cache (the
  * result is then undefined) sets *err_device (DEVICE word, cleared by the
  * caller) to 1, a device-side wait that ran out (2 s) to 2.
- * LF_ERR_INVALID_ARG for bad sizes, pointers, strides or types, shared_len or
- * max_len above max_pages * page_size, or a workspace too small;
+ * LF_ERR_INVALID_ARG for bad sizes, pointers, strides or types, max_len above
+ * max_pages * page_size, shared_len above max_len, or a workspace too small;
  * LF_ERR_UNSUPPORTED for head_dim other than 32, 64 or 128, more than 16
  * query heads per KV head, more than 1024 sequences, or max_len * n_seqs *
  * n_kv_heads above about 2^37. */

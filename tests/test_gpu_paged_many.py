@@ -59,3 +59,16 @@ def test_repeatable_and_independent_of_the_workspace():
     torch.cuda.synchronize()
     assert torch.equal(a, b) and torch.equal(la, lb)
     c.check(a, la)
+
+
+@pytest.mark.parametrize("lens", [[50, 20, 99], [0, 7, 8], [300, 299, 1]])
+def test_tight_bound_where_every_sequence_ends_inside_the_prefix(lens):
+    # the bound as the number of common positions: the same positions through the same row of the table
+    shared = max(lens) + 30
+    c = Case(lens, shared, 4, 2, 64, 16, "f16", seed=3)
+    want, wl = c.run()
+    c.shared = max(lens)
+    got, gl = c.run(max_len=max(lens))
+    c.shared = shared
+    c.check(got, gl)
+    c.check(want, wl)
