@@ -23,7 +23,7 @@ namespace lf {
 namespace {
 
 constexpr int kAppendThreads = 128;
-constexpr long long kAppendManyUnits = 1 << 18;
+constexpr long long kAppendManyUnits = 1 << 17;
 struct AppendArgs {
     PagedView kv;
     const void *q, *k, *v;
@@ -178,9 +178,13 @@ bool launch_units(const AppendArgs &a, cudaStream_t st) {
 
 template <typename TI, typename TO>
 bool launch_append(const AppendArgs &a, cudaStream_t st) {
-    // four units a thread once that still leaves a few blocks per SM (3584 tokens: 4
-    // 22.5 us, 2 22.1, 8 22.3; 8191 of head_dim 64: 16.6, 18.1, 18.7), one unit for
-    // the few tokens of a decode step (a shorter chain in each thread)
+    // four units a thread once that still leaves a few blocks per SM, one for the few
+    // tokens of a decode step (a shorter chain in each thread).  Measured on the device
+    // (us, 1 | 4 units), 32 + 2 x 16 heads of 128, FP16: 64 tokens 1.9 | 2.3, 128 2.3 | 2.3,
+    // 181 2.5 | 2.6, 256 (2^17 units) 3.3 | 2.7, 512 4.4 | 4.0, 2048 15.1 | 14.3; 24 + 2 x 8 heads
+    // of 64, BF16: 409 2.6 | 2.4, 819 (2^17) 3.1 | 2.6, 3276 9.8 | 7.8, 11410 30.9 | 21.5.  From
+    // FP32 four are slower again with many tokens of the larger heads (2048 18.4 | 20.0),
+    // faster with the smaller (6553 22.0 | 20.3); two would do as well there (18.5, 18.4).
     const long long units = (long long)a.n_tokens * (a.n_q + 2 * a.kv.n_kv) * (a.kv.head_dim / 16);
     return units >= kAppendManyUnits ? launch_units<TI, TO, 4>(a, st) : launch_units<TI, TO, 1>(a, st);
 }
