@@ -27,13 +27,16 @@
 // accumulators), softmax statistics in registers.  The four warps take 16-row
 // blocks (rows > 16) and 16-key blocks (what is left), each warp its own
 // running maximum; warps that shared rows join in shared memory at the item's
-// end.  P is rounded to the cache's type for the second product (as the other
-// operand is); its sum is taken before the rounding.
+// end.  P is rounded to the cache's type for the second product: both operands of
+// an MMA have one type, and a second product with what the rounding leaves would
+// double the work.  Its sum is taken before the rounding.  Against 64 bits the
+// output's error (mostly its own rounding) grows by 8 to 14 % on the timed cases, from
+// 1.66e-3 to 2.31e-3 at the largest in BF16.
 //
 // Measured (us per call, both launches; in brackets the bytes it cannot do
 // without at the copy rate): 8 sequences x 512 common + 40 .. 130 own positions, 32 / 16
 // heads of 128: 10.0 (1.5); 16 x 3584 + 100 .. 512: 23.8 (10.4); 24 windowed
-// sequences, 24 / 8 heads of 64: 15.0 (2.9); 2 short ones, by the direct kernel:
+// sequences, 24 / 8 heads of 64: 15.1 (2.9); 2 short ones, by the direct kernel:
 // 4.7 to 5.2 (6.5 by the list), the time of the call.  Between 2 and 3 us go to working out the list (lengths, then page
 // numbers, then the first keys: three trips to L2), as much to the join; in
 // between the keys and values stream at 5.7 TB/s.
@@ -777,7 +780,8 @@ void common_shape(AttnArgs &a, bool tc, int n_sm) {
 //    64 x 2048 11.0 | 26.3 15.3 11.4 14.8   128 x 2048 14.1 | 26.5 19.0 22.4 29.0
 //   256 x 512  12.6 | 10.9 15.3 21.8        512 x 160  11.0 | 10.6 20.1
 //   256 x 1000 14.6 | 18.1 21.5 27.3        512 x 256  11.3 | 12.9 21.9
-// (over 252 such sizes, 64 wide heads too, the rule is 1 % off the best choice).
+// (over 179 such sizes, 64 wide heads too, the rule is 1.2 % off the best choice, 21 %
+// at most).
 // Not where the common positions read once more by every sequence make over 16
 // MB: alone that is L2's to give (64 x 1000 at 4 sequences: 10.4 | 7.7), but in a
 // step that streams weights beside it the list is faster (the batched decode of 4

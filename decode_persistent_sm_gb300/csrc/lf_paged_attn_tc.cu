@@ -23,7 +23,7 @@
 // common positions, BF16: 35 us, 980 TFLOP/s (51 % of the measured dense rate; the
 // tensor pipe is active 41 % of the time).  The whole call 85 us: behind it the
 // kernel of the sequences' own positions starts (6 to 8 us) and reads them (31 us,
-// 142 MB); on warp-level MMAs alone 161.  A step
+// 135 MB); on warp-level MMAs alone 161.  A step
 // (128 keys, both row tiles) takes 3700 cycles for 2048 of products.  Its chain is
 // softmax (1400: load 100, max 200, exponentials 800, store and fence 160), then P V
 // and Q K^T (512 each, and 340 until the result is seen).  Around the products the

@@ -27,8 +27,8 @@
 // maximum, summed over the cluster through distributed shared memory):
 //   top-k: of C CTAs, each takes the ceil(k / C)-th largest of its thread
 //          groups' maxima; at least k logits reach the smallest of those, so
-//          everything below drops out (for k above half the threads every
-//          logit is counted in the histogram instead);
+//          everything below drops out (for k above 204 C every logit is counted
+//          in the histogram instead);
 //   top-p: the masses of all logits (64 bits as two 32-bit shared atomics, the
 //          second where the high word changes) name the step that holds the border.
 //          A step's unit is 2^-44 of the largest weight that can lie in it, down to
@@ -42,12 +42,13 @@
 // of fp32's: a logarithm and a division cost 2 us): targets are exact integer
 // products, log2(e) / T and ln(min_p) come as pairs of floats.
 //
-// Measured (us per call; rows of mixed filters, a fifth greedy; in brackets the
-// bytes at the copy rate): 1 x 32000 fp32 5 - 11 (0.02), 16 x 32000 18 - 20 (0.3),
-// 100 x 50257 39 (3), 256 x 131072 bf16 152 (10).  A single row is a chain of three
-// to six exchanges between CTAs (about 1 us each) and passes over 4000 logits; many rows
-// are bound by instructions: 76 per logit on average, two thirds of them the exact
-// weights of the rows that need the mass of their whole vocabulary (no top-k).
+// Measured (us per call; in brackets the bytes at the copy rate): 1 x 32000 fp32 6.5
+// without a filter, 14 under top-p, 10 under top-k 50, 15 under both, 3 greedy (0.02);
+// rows of mixed filters, a fifth greedy: 16 x 32000 20 (0.3), 100 x 50257 42 - 47 (3), 256
+// x 131072 bf16 151 - 156 (10).  A single row is a chain of two to six exchanges
+// between CTAs (about 1 us each) and passes over 4000 logits; many rows are bound by
+// instructions: 73 per logit on average, two thirds of them the exact weights of the
+// rows that need the mass of their whole vocabulary (no top-k).
 
 #include <cooperative_groups.h>
 
@@ -1031,8 +1032,9 @@ template <int C>
 lf_status launch_cluster(const FilterArgs &a, int n_sm, cudaStream_t st) {
     // 1024 threads where a CTA has its SM to itself, or nearly all do: 512, two CTAs
     // to an SM, win with more of them or few logits (us, 512 | 1024 threads; CTAs x logits
-    // of one: 160 x 10000 30.6 | 24.6, 200 x 10000 30.2 | 26.5, 200 x 4000 21.6 | 20.8,
-    // 300 x 10000 31.7 | 35.4, 200 x 37 10.6 | 12.9)
+    // of one: 160 x 10000 31.1 | 24.9, 200 x 10000 31.1 | 27.4, 240 x 10000 32.2 | 31.7, 300 x
+    // 10000 32.4 | 35.9, 200 x 4000 22.7 | 21.1, 260 x 4000 23.0 | 23.9, 200 x 37 10.6 | 13.0;
+    // it takes the slower one, 1024, at 120 x 37: 8.8 | 9.8)
     const int wide = a.per > 2048 ? n_sm + n_sm / 3 : n_sm;
     return a.per > kPairPer || a.rows <= wide / C ? launch_row<1024, C>(a, st) : launch_row<512, C>(a, st);
 }
@@ -1046,10 +1048,11 @@ lf_status launch_filtered(FilterArgs a, cudaStream_t st) {
     }
     // CTAs per row: what the shared memory asks for, and more while a CTA has at least
     // 4096 logits and the grid fits the SMs, or overflows them by a third at 12000 logits
-    // and more.  Measured (us, c = 1 | 2 | 4 | 8): 1 x 32000 17.1 | 12.9 | 10.1 | 9.4,
-    // 16 x 32000 38 | 26 | 20 | 19, 40 x 32000 37 | 27 | 23 | 38, 70 x 32000 37 | 28 | 33 | 59,
-    // 100 x 32000 39 | 33 | 43 | 79, 100 x 10000 20 | 30 | 42 | 86, 150 x 10000 21 | 40 | 59 |
-    // 132, 256 x 32000 57 | 65 | 94 | 185, 1 x 4000 7.3 | 7.6 | 8.0 | 8.9.
+    // and more.  Measured (us, c = 1 | 2 | 4 | 8): 1 x 32000 17.0 | 12.1 | 9.1 | 7.4,
+    // 16 x 32000 42 | 27 | 20 | 18, 40 x 32000 40 | 27 | 23 | 31, 70 x 32000 41 | 28 | 32 | 40,
+    // 100 x 32000 42 | 33 | 36 | 51, 100 x 10000 23 | 26 | 29 | 46, 150 x 20000 29 | 34 | 41 | 64,
+    // 256 x 32000 58 | 58 | 72 | 109, 1 x 4000 5.9 | 6.4 | 6.1 | 6.4.  Not the best choice at 32 x
+    // 131072, where 4 take 43.6 and 8 would 40.0, and at 20 x 20000 (4: 20.6, 8: 19.5).
     int c = 1;
     auto more = [&] {
         const int per = a.vocab / c, room = per > 12000 ? n_sm + n_sm / 3 : n_sm;
