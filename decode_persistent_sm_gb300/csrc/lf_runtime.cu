@@ -145,7 +145,7 @@ const char *lf_status_string(lf_status s) {
         case LF_ERR_CTX_OVERFLOW: return "context capacity reached";
         case LF_ERR_TIMEOUT: return "device wait timed out";
         case LF_ERR_UNSUPPORTED: return "unsupported configuration";
-        case LF_ERR_BOUNDS: return "debug check failed (device bounds check or buffer canary)";
+        case LF_ERR_BOUNDS: return "bounds check failed on the device (a batch's paged cache, or a debug check or buffer canary)";
     }
     return "unknown status";
 }
