@@ -73,6 +73,12 @@ _SIGS = {
                                    _vp, _vp]),
     "lf_attn_paged_shared_workspace": (ctypes.c_size_t, [_vp, _ci]),
     "lf_sample_filtered": (_ci, [_vp, _ci, _ci, _ci, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "lf_add_rmsnorm": (_ci, [_vp, _ci, _i64, _vp, _vp, _ci, _i64, _i64, _vp, _ci, _ci, _ci, _f32, _vp, _ci, _i64, _vp, _vp]),
+    "lf_matmul_f8": (_ci, [_vp, _vp, _vp, _vp, _vp, _ci, _ci, _ci, _ci, _vp, _vp]),
+    "lf_attn_paged_chunk": (_ci, [_vp, _vp, _i64, _vp, _i64, _vp, _ci, _vp, _ci, _vp, _ci, _ci, _f32, _vp, ctypes.c_size_t,
+                                  _vp, _vp]),
+    "lf_attn_paged_chunk_workspace": (ctypes.c_size_t, [_vp, _ci, _ci]),
+    "lf_token_logprobs": (_ci, [_vp, _ci, _ci, _ci, _i64, _vp, _vp, _ci, _vp, _vp, _vp, _vp, _vp, _vp]),
     "lf_debug_canaries": (_ci, [_vp, ctypes.POINTER(_ci)]),
     "lf_debug_corrupt_canary": (_ci, [_vp, _ci, _ci]),
     "lf_debug_sample_wait": (_ci, [ctypes.c_uint64, _ci, _ci]),
@@ -90,7 +96,7 @@ class LfConfig(ctypes.Structure):
     ]
 
 
-DTYPES = {"f32": 0, "f16": 1, "bf16": 2}  # lf_dtype
+DTYPES = {"f32": 0, "f16": 1, "bf16": 2, "e4m3": 3}  # lf_dtype
 
 
 class LfPagedKV(ctypes.Structure):
@@ -243,6 +249,59 @@ def sample_filtered(logits_ptr: int, dtype: str, rows: int, vocab: int, ld: int,
                                            top_p_ptr, min_p_ptr, u_ptr, token_ptr, logprob_ptr, stream)
     if rc:
         _check("lf_sample_filtered", rc)
+
+
+def add_rmsnorm(x_ptr: int, x_dtype: str, ld_x: int, residual_ptr: Optional[int], sum_ptr: Optional[int],
+                residual_dtype: str, ld_residual: int, ld_sum: int, gain_ptr: Optional[int], gain_dtype: str, rows: int,
+                cols: int, eps: float, out_ptr: int, out_dtype: str, ld_out: int, scale_ptr: Optional[int] = None,
+                stream: Optional[int] = None):
+    """lf_add_rmsnorm: enqueue RMSNorm of x + residual, the sum written beside it;
+    out_dtype "e4m3" leaves 8 bits and a scale per row."""
+    rc = load_library().lf_add_rmsnorm(x_ptr, DTYPES[x_dtype], ld_x, residual_ptr, sum_ptr, DTYPES[residual_dtype],
+                                       ld_residual, ld_sum, gain_ptr, DTYPES[gain_dtype], rows, cols, eps, out_ptr,
+                                       DTYPES[out_dtype], ld_out, scale_ptr, stream)
+    if rc:
+        _check("lf_add_rmsnorm", rc)
+
+
+def matmul_f8(a_ptr: int, a_scale_ptr: Optional[int], b_ptr: int, b_scale_ptr: Optional[int], c_ptr: int, c_dtype: str,
+              m: int, n: int, k: int, err_ptr: int, stream: Optional[int] = None):
+    """lf_matmul_f8: enqueue c = (a . b^T) * a_scale * b_scale of e4m3 operands."""
+    rc = load_library().lf_matmul_f8(a_ptr, a_scale_ptr, b_ptr, b_scale_ptr, c_ptr, DTYPES[c_dtype], m, n, k, err_ptr,
+                                     stream)
+    if rc:
+        _check("lf_matmul_f8", rc)
+
+
+def attn_paged_chunk_workspace(kv: LfPagedKV, n_q_heads: int, n_tokens: int) -> int:
+    """lf_attn_paged_chunk_workspace: bytes of scratch one call of up to n_tokens
+    rows needs on the current device (0: the call would refuse the sizes)."""
+    return load_library().lf_attn_paged_chunk_workspace(ctypes.byref(kv), n_q_heads, n_tokens)
+
+
+def attn_paged_chunk(kv: LfPagedKV, q_ptr: int, ld_q: int, out_ptr: int, ld_out: int, lse_ptr: Optional[int],
+                     n_q_heads: int, starts_ptr: int, n_tokens: int, lens_ptr: int, max_len: int, window: int,
+                     scale: float, workspace_ptr: int, workspace_bytes: int, err_ptr: int,
+                     stream: Optional[int] = None):
+    """lf_attn_paged_chunk: enqueue the attention of each sequence's new tokens
+    (rows starts[b] .. starts[b + 1] - 1) over a paged cache that holds them."""
+    rc = load_library().lf_attn_paged_chunk(ctypes.byref(kv), q_ptr, ld_q, out_ptr, ld_out, lse_ptr, n_q_heads,
+                                            starts_ptr, n_tokens, lens_ptr, max_len, window, scale, workspace_ptr,
+                                            workspace_bytes, err_ptr, stream)
+    if rc:
+        _check("lf_attn_paged_chunk", rc)
+
+
+def token_logprobs(logits_ptr: int, dtype: str, rows: int, vocab: int, ld: int, temperature_ptr: Optional[int],
+                   token_ptr: Optional[int], top_n: int, logprob_ptr: Optional[int], rank_ptr: Optional[int] = None,
+                   entropy_ptr: Optional[int] = None, top_token_ptr: Optional[int] = None,
+                   top_logprob_ptr: Optional[int] = None, stream: Optional[int] = None):
+    """lf_token_logprobs: enqueue, per row of device logits, the log probability
+    and rank of a given token, the entropy and the top_n most probable tokens."""
+    rc = load_library().lf_token_logprobs(logits_ptr, DTYPES[dtype], rows, vocab, ld, temperature_ptr, token_ptr, top_n,
+                                          logprob_ptr, rank_ptr, entropy_ptr, top_token_ptr, top_logprob_ptr, stream)
+    if rc:
+        _check("lf_token_logprobs", rc)
 
 
 def _round_down(u) -> np.ndarray:

@@ -1,0 +1,322 @@
+// Product of 8-bit operands with a scale per row of each (sm_103a, tcgen05 + TMA):
+//   C[m][n] = sa[m] sb[n] sum_k A[m][k] B[n][k],  A (M x K) and B (N x K) e4m3, row-major.
+//
+// A persistent CTA per SM walks 128 x BN tiles of C: a copy warp streams 128 x
+// 128 and BN x 128 byte tiles of A and B into a shared-memory ring with TMA
+// (128-byte swizzle; zeros past K, M and N), one thread issues tcgen05.mma
+// (kind::f8f6f4, 32 values of K each, fp32 accumulators in one of two TMEM
+// buffers), and four warps read a finished accumulator back, scale it and store
+// it while the next tile's products run.
+//
+// BN is 256 where there are tiles enough for every SM (the products are the
+// bound: an MMA of 128 x 256 reads 384 bytes of shared memory for each 32 x 32
+// of K, one of 128 x 128 a third more), and less where the weights' stream is the
+// bound and has to be spread over the SMs (few rows of A).
+//
+// Every wait is bounded: on a timeout the CTA records an error, lets its copies
+// and MMAs in flight finish (bounded), frees TMEM and exits.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <mutex>
+
+#include "lf_paged.h"
+#include "lf_tc.cuh"
+
+namespace lf {
+namespace {
+
+constexpr int F8_BM = 128, F8_BK = 128;  // 128 values of K = 128 bytes = one swizzle row
+constexpr int F8_THREADS = 192;          // warp 0 copies, warp 1 MMA + TMEM owner, warps 2-5 epilogue
+constexpr int F8_GROUP_M = 32;           // M-tiles that take each B tile in turn
+constexpr unsigned long long kF8TimeoutNs = 2000000000ull;
+
+template <int BN>
+struct F8Tile {
+    static constexpr int A = F8_BM * F8_BK, B = BN * F8_BK, STAGE = A + B;
+    static constexpr int STAGES = 196608 / STAGE;  // 192 KB: 4, 6, 8
+    static constexpr uint32_t COLS = 2 * BN;       // two accumulators (a power of two, at least 32)
+    static constexpr int SMEM = STAGES * STAGE + 1024 + 256;
+};
+
+template <int STAGES>
+struct F8Shared {
+    uint64_t full[STAGES], empty[STAGES];
+    uint64_t acc_full[2], acc_empty[2];  // accumulator b computed / read back (128 arrivals)
+    uint32_t tmem;
+    volatile int abort_;
+    volatile int n_acc_[2];  // commits issued on acc_full[b]
+};
+
+struct F8Args {
+    const float *sa, *sb;
+    void *c;
+    int m, n, k, c_dtype, rows_a;  // rows_a: rows of A's box
+    uint32_t *err;
+};
+
+template <typename S>
+__device__ __forceinline__ bool f8_wait(S &s, uint64_t *bar, uint32_t parity, uint64_t deadline, uint32_t *err) {
+    while (!mbar_try_wait(bar, parity)) {
+        if (s.abort_) return false;
+        if (global_timer_ns() > deadline) {
+            atomicExch(err, 2u);
+            s.abort_ = 1;
+            return false;
+        }
+    }
+    return true;
+}
+
+__device__ __forceinline__ void tc_mma_f8(uint32_t tmem_d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ void f8_tile_of(int t, int mt, int nt, int &m, int &n) {
+    const int per_group = F8_GROUP_M * nt, group = t / per_group, first = group * F8_GROUP_M;
+    const int gm = min(F8_GROUP_M, mt - first), r = t - group * per_group;
+    m = first + r % gm;
+    n = r / gm;
+}
+
+template <typename T>
+__device__ __forceinline__ T f8_round(float v) {
+    if constexpr (sizeof(T) == 4)
+        return v;
+    else
+        return (T)v;
+}
+
+// 32 columns of one row, from column `col` on.
+template <typename T>
+__device__ __forceinline__ void f8_store(T *dst, const float *v, int left) {
+    __align__(16) T o[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) o[i] = f8_round<T>(v[i]);
+    if (left >= 32 && (reinterpret_cast<uintptr_t>(dst) & 15) == 0) {
+#pragma unroll
+        for (int i = 0; i < 32 * (int)sizeof(T) / 16; ++i)
+            reinterpret_cast<uint4 *>(dst)[i] = reinterpret_cast<const uint4 *>(o)[i];
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (i < left) dst[i] = o[i];
+    }
+}
+
+template <int BN>
+__global__ void __launch_bounds__(F8_THREADS, 1)
+    matmul_f8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const F8Args a) {
+    using L = F8Tile<BN>;
+    constexpr int ST = L::STAGES;
+    extern __shared__ __align__(1024) uint8_t f8_raw[];
+    uint8_t *tiles = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(f8_raw) + 1023) & ~uintptr_t(1023));
+    auto &S = *reinterpret_cast<F8Shared<ST> *>(tiles + ST * L::STAGE);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int mt = (a.m + F8_BM - 1) / F8_BM, nt = (a.n + BN - 1) / BN, ntiles = mt * nt;
+    const int nk = (a.k + F8_BK - 1) / F8_BK;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < ST; ++s) {
+            mbar_init(&S.full[s], 1);
+            mbar_init(&S.empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&S.acc_full[b], 1);
+            mbar_init(&S.acc_empty[b], 128);
+            S.n_acc_[b] = 0;
+        }
+        S.abort_ = 0;
+        fence_barrier_init();
+        tma_prefetch_map(&tmA);
+        tma_prefetch_map(&tmB);
+    }
+    if (warp == 1) tc_alloc(&S.tmem, L::COLS);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = S.tmem;
+    pdl_wait();
+    pdl_trigger();
+    const uint64_t deadline = global_timer_ns() + kF8TimeoutNs;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int kbg = 0;  // k-blocks issued so far (all tiles)
+            for (int t = blockIdx.x; t < ntiles && !S.abort_; t += gridDim.x) {
+                int m, n;
+                f8_tile_of(t, mt, nt, m, n);
+                for (int kb = 0; kb < nk; ++kb, ++kbg) {
+                    const int s = kbg % ST;
+                    if (kbg >= ST && !f8_wait(S, &S.empty[s], ((kbg / ST) - 1) & 1u, deadline, a.err)) break;
+                    uint8_t *st = tiles + s * L::STAGE;
+                    mbar_arrive_expect_tx(&S.full[s], a.rows_a * F8_BK + L::B);
+                    tma_load_2d(st, &tmA, kb * F8_BK, m * F8_BM, &S.full[s]);
+                    tma_load_2d(st + L::A, &tmB, kb * F8_BK, n * BN, &S.full[s]);
+                }
+            }
+            if (S.abort_) {  // let the copies in flight land before the CTA exits
+                const uint64_t dl = global_timer_ns() + 1000000000ull;
+                for (int k = kbg > ST ? kbg - ST : 0; k < kbg; ++k)
+                    while (!mbar_try_wait(&S.full[k % ST], (k / ST) & 1u) && global_timer_ns() < dl) {
+                    }
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            // e4m3 operands (type 0), fp32 accumulators, both K-major
+            constexpr uint32_t kIdesc = idesc_f16(F8_BM, BN);
+            int kbg = 0, lt = 0;
+            bool ok = true;
+            for (int t = blockIdx.x; ok && t < ntiles; t += gridDim.x, ++lt) {
+                const int b = lt & 1;
+                const uint32_t acc = tmem + (uint32_t)b * BN;
+                if (lt >= 2 && !f8_wait(S, &S.acc_empty[b], ((lt >> 1) - 1) & 1u, deadline, a.err)) break;
+                tc_fence_after();
+                for (int kb = 0; kb < nk; ++kb, ++kbg) {
+                    const int s = kbg % ST;
+                    if (!f8_wait(S, &S.full[s], (kbg / ST) & 1u, deadline, a.err)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t at = smem_u32(tiles + s * L::STAGE), bt = at + L::A;
+#pragma unroll
+                    for (int kk = 0; kk < F8_BK / 32; ++kk)  // 32 values = 32 bytes along K per instruction
+                        tc_mma_f8(acc, smem_desc_sw128(at + 32 * kk), smem_desc_sw128(bt + 32 * kk), kIdesc, (kb | kk) != 0);
+                    tc_commit(&S.empty[s]);
+                }
+                tc_commit(&S.acc_full[b]);
+                S.n_acc_[b] = (lt >> 1) + 1;
+            }
+        }
+    } else {  // warp w reads TMEM lanes 32 * (w % 4) .. + 31
+        const int q = warp & 3;
+        int lt = 0;
+        for (int t = blockIdx.x; t < ntiles; t += gridDim.x, ++lt) {
+            int m, n;
+            f8_tile_of(t, mt, nt, m, n);
+            const int b = lt & 1, row = m * F8_BM + 32 * q + lane;
+            const float ra = row < a.m && a.sa ? a.sa[row] : 1.f;
+            if (!__all_sync(0xffffffffu, f8_wait(S, &S.acc_full[b], (lt >> 1) & 1u, deadline, a.err))) break;
+            tc_fence_after();
+            const uint32_t tacc = tmem + (uint32_t)b * BN + ((uint32_t)(32 * q) << 16);
+#pragma unroll 1
+            for (int c0 = 0; c0 < BN; c0 += 32) {
+                const int col = n * BN + c0, left = a.n - col;
+                if (left <= 0 || m * F8_BM + 32 * q >= a.m) break;  // (the whole warp)
+                float v[32];
+                tc_ld32(tacc + (uint32_t)c0, v);
+                const float sc = a.sb && lane < left ? a.sb[col + lane] : 1.f;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] = v[i] * ra * __shfl_sync(0xffffffffu, sc, i);
+                if (row < a.m) {
+                    const long long at = (long long)row * a.n + col;
+                    if (a.c_dtype == LF_F32)
+                        f8_store(static_cast<float *>(a.c) + at, v, left);
+                    else if (a.c_dtype == LF_F16)
+                        f8_store(static_cast<__half *>(a.c) + at, v, left);
+                    else
+                        f8_store(static_cast<__nv_bfloat16 *>(a.c) + at, v, left);
+                }
+                __syncwarp();
+            }
+            tc_fence_before();
+            mbar_arrive(&S.acc_empty[b]);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        if (S.abort_ && lane == 0) {  // MMAs may still run: wait (bounded) for their last commits
+            const uint64_t dl = global_timer_ns() + 1000000000ull;
+            for (int b = 0; b < 2; ++b)
+                if (S.n_acc_[b] > 0)
+                    while (!mbar_try_wait(&S.acc_full[b], (S.n_acc_[b] - 1) & 1u) && global_timer_ns() < dl) {
+                    }
+        }
+        __syncwarp();
+        tc_fence_after();
+        tc_dealloc(tmem, L::COLS);
+    }
+}
+
+using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                 const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encoder() {
+    static EncodeTiled fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
+                cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<EncodeTiled>(p);
+    });
+    return fn;
+}
+
+// Row-major [rows][k] bytes, boxes of box_rows x 128, 128-byte swizzle, zeros outside.
+bool f8_map(CUtensorMap *map, const void *p, int rows, int k, int box_rows) {
+    EncodeTiled enc = encoder();
+    if (!enc) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)k, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)k};
+    const cuuint32_t box[2] = {F8_BK, (cuuint32_t)box_rows}, one[2] = {1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(p), dims, strides, box, one,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int BN>
+lf_status launch_f8(const void *A, const void *B, F8Args a, int n_sm, cudaStream_t st) {
+    using L = F8Tile<BN>;
+    // a short A is not copied as 128 rows (the products of the rows behind it, whatever they hold, are not stored)
+    a.rows_a = a.m >= F8_BM ? F8_BM : (a.m + 7) / 8 * 8;
+    CUtensorMap ma, mb;
+    if (!set_smem_once<matmul_f8_kernel<BN>>(L::SMEM) || !f8_map(&ma, A, a.m, a.k, a.rows_a) ||
+        !f8_map(&mb, B, a.n, a.k, BN))
+        return LF_ERR_CUDA;
+    const long long tiles = (((long long)a.m + F8_BM - 1) / F8_BM) * (((long long)a.n + BN - 1) / BN);
+    const unsigned grid = (unsigned)(tiles < n_sm ? tiles : n_sm);
+    return launch_pdl(matmul_f8_kernel<BN>, grid, F8_THREADS, L::SMEM, st, ma, mb, a) ? LF_OK : LF_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace lf
+
+extern "C" lf_status lf_matmul_f8(const void *a_device, const float *a_scale_device, const void *b_device,
+                                  const float *b_scale_device, void *c_device, int c_dtype, int m, int n, int k,
+                                  uint32_t *err_device, void *cuda_stream) {
+    const int bytes = lf::dtype_bytes(c_dtype);
+    auto off = [](const void *p, int by) { return reinterpret_cast<uintptr_t>(p) % (unsigned)by != 0; };
+    if (!bytes || m < 0 || n < 0 || k < 16 || k % 16 || !a_device || !b_device || !c_device || !err_device ||
+        !lf::aligned16(a_device) || !lf::aligned16(b_device) || off(c_device, bytes) || off(a_scale_device, 4) ||
+        off(b_scale_device, 4) || off(err_device, 4))
+        return LF_ERR_INVALID_ARG;
+    // coordinates and tile numbers are 32-bit (the narrowest tiles are 64 wide)
+    if (m > INT32_MAX - 128 || n > INT32_MAX - 256 || k > INT32_MAX - 128 ||
+        ((long long)m / 128 + 1) * ((long long)n / 64 + 1) + 4096 > INT32_MAX)
+        return LF_ERR_UNSUPPORTED;
+    if (m == 0 || n == 0) return LF_OK;
+    int dev = 0, n_sm = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n_sm < 1) {
+        (void)cudaGetLastError();
+        return LF_ERR_CUDA;
+    }
+    const lf::F8Args a = {a_scale_device, b_scale_device, c_device, m, n, k, c_dtype, 0, err_device};
+    cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
+    const long long mt = ((long long)m + 127) / 128;
+    if (mt * ((n + 255) / 256) >= n_sm) return lf::launch_f8<256>(a_device, b_device, a, n_sm, st);
+    if (mt * ((n + 127) / 128) >= n_sm) return lf::launch_f8<128>(a_device, b_device, a, n_sm, st);
+    return lf::launch_f8<64>(a_device, b_device, a, n_sm, st);
+}

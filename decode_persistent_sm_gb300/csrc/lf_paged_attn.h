@@ -1,7 +1,8 @@
-// What the kernels of the paged attention share (private to the library).
+// What the kernels of the paged attentions share (private to the library).
 #pragma once
 
 #include "lf_paged.h"
+#include "lf_ptx.cuh"
 
 namespace lf {
 
@@ -112,6 +113,38 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+
+// keys per tile: 32 KB of K and V at head_dim 64 and 128 (a 16 KB tile's barriers and softmax statistics cost more than its copy)
+__host__ __device__ constexpr int tile_keys(int dim) { return dim == 128 ? 64 : 128; }
+
+template <typename T>
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1);
+template <>
+__device__ __forceinline__ void mma<__half>(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    mma_16816(c, a, b0, b1);
+}
+template <>
+__device__ __forceinline__ void mma<__nv_bfloat16>(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// 16 bytes global -> shared, or 16 zero bytes.
+__device__ __forceinline__ void cp16_or_zero(uint32_t dst, const void *src, bool valid) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
+}
+
+// Byte offset of 16-byte chunk c of row r of a tile: the chunk index is
+// permuted by the row so that the 8 rows of a matrix load lie in 8 different
+// 16-byte bank groups.
+template <int DH>
+__device__ __forceinline__ uint32_t tile_off(int r, int c) {
+    return (uint32_t)(r * DH * 2 + ((c ^ (DH >= 64 ? (r & 7) : ((r >> 1) & 3))) << 4));
+}
+
+// 1 / sum, 0 for a row that saw nothing (a NaN stays one).
+__device__ __forceinline__ float inverse(float sum) { return sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum); }
 
 // The common items on the 5th-generation tensor cores (lf_paged_attn_tc.cu).
 constexpr int kTcRows = 256, kTcKeys = 128;

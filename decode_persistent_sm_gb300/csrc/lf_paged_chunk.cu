@@ -1,0 +1,577 @@
+// Attention of each sequence's new tokens over a paged cache that holds them:
+// o = softmax(scale q K^T) V per query head, causal (and windowed) by position.
+//
+// The rows (token, head of the group) of a few tokens are the M side of a product
+// with a tile of keys (the list of such items: lf_paged_chunk.h).  Here: warp-level
+// MMAs (m16n8k16, fp32 accumulators), 16, 32 or 64 rows an item, K and V tiles of 64
+// or 128 keys through a cp.async ring that runs on across item borders, softmax
+// statistics in registers.  Warps take 16-row blocks, and 16-key blocks where the
+// rows are fewer; warps that shared rows join in shared memory at the item's end.
+// An item that one CTA sees whole is written out at once; one that several share
+// leaves partials (unnormalised o, max, sum) and a second launch joins them.
+//
+// Masks.  Only a tile that some row of the item does not see whole is masked, by
+// position, scores set to -inf.  A weight of 0 times a value that is not finite
+// would still be NaN, so in such a tile those values are taken out of the product
+// and added to the rows that do see them.
+//
+// P is rounded to the cache's type for the second product: both operands of an MMA
+// have one type.  Its sum is taken before the rounding.
+#include <algorithm>
+#include <climits>
+#include <type_traits>
+
+#include "lf_paged_chunk.h"
+
+namespace lf {
+namespace {
+
+constexpr int CK_THREADS = 128, CK_CTAS_PER_SM = 2, CK_MAX_SEQS = 1024, CK_MAX_GROUP = 16;
+constexpr int CK_MAX_TOKENS = 1 << 26;
+
+template <typename T, int DH>
+struct CkSmem {
+    static constexpr int KT = tile_keys(DH);
+    static constexpr int TILE = KT * DH * 2;  // bytes of K (or V) of one tile
+    static constexpr int STAGES = DH == 32 ? 6 : 3;
+    static constexpr int ML = 4 * 16 * 2 * 4;  // max and sum of the rows that the warps join
+    static constexpr int CUM = (CK_MAX_SEQS + 4) * 4;
+    static constexpr int BYTES = STAGES * 2 * TILE + ML + CUM;
+    static_assert(4 * 16 * DH * 4 <= 2 * TILE, "the joined rows fit the stage");
+};
+
+// A 16-bit value is infinite or NaN.
+template <typename T>
+__device__ __forceinline__ bool odd_one(uint32_t h) {
+    constexpr uint32_t e = std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u;
+    return (h & e) == e;
+}
+
+// WR warps side by side in rows, 4 / WR in keys: items of up to 16 WR rows.
+template <typename T, int DH, int WR>
+class ChunkWalker {
+  public:
+    __device__ ChunkWalker(const ChunkArgs &args, uint8_t *smem) : a(args) {
+        stage0 = smem;
+        ml = reinterpret_cast<float2 *>(smem + L::STAGES * 2 * L::TILE);
+        cum = reinterpret_cast<int *>(smem + L::STAGES * 2 * L::TILE + L::ML);
+        tid = threadIdx.x;
+        warp = tid >> 5;
+        lane = tid & 31;
+    }
+
+    __device__ void run() {
+        const int total = chunk_plan(a, cum);
+        const Shares sh(total, gridDim.x);
+        const int cta = blockIdx.x;
+        if (tid == 0) a.joins[cta].parts = 0;
+        if (cta >= min(total, (int)gridDim.x)) return;
+        const int u0 = sh.begin(cta), u1 = sh.begin(cta + 1), n = u1 - u0;
+        ChunkWork work = chunk_place(a, cum, u0), load = work;
+        prepare(load);
+        int loaded = 0;
+        auto fetch_next = [&] {
+            if (loaded < n) {
+                fetch(loaded % L::STAGES);
+                if (loaded + 1 < n) {
+                    chunk_advance(a, cum, load);
+                    prepare(load);
+                }
+            }
+            ++loaded;
+            cp_async_commit();
+        };
+        for (int i = 0; i < L::STAGES - 1; ++i) fetch_next();
+        bool fresh = true, whole = work.tile == 0;  // whole: this CTA has begun the item
+        for (int i = 0; i < n; ++i) {
+            if (fresh) begin(work);
+            fetch_next();
+            asm volatile("cp.async.wait_group %0;" ::"n"(L::STAGES - 1) : "memory");
+            __syncthreads();
+            const bool ends = work.tile + 1 == work.tiles, last = i + 1 == n || ends;
+            tile(work, last, i % L::STAGES, whole && ends, 2 * cta + (whole ? 1 : 0));
+            __syncthreads();  // the stage may be written again
+            if (i + 1 == n) {
+                if (tid == 0) a.joins[cta] = chunk_join(a, work, sh, cta, u1, work.tile + 1, whole);
+            } else {
+                fresh = chunk_advance(a, cum, work);
+                if (fresh) whole = true;
+            }
+        }
+    }
+
+  private:
+    using L = CkSmem<T, DH>;
+    static constexpr int KT = L::KT, WK = 4 / WR, NB = KT / (16 * WK);  // NB blocks of 16 keys per warp
+    const ChunkArgs &a;
+    uint8_t *stage0;
+    float2 *ml;
+    int *cum;
+    int tid, warp, lane;
+    // the tile to be fetched next: element offsets of rows lane + 32 i (-1: no such key)
+    long long row_off[KT / 32];
+    // running state of this warp's 16 rows (lane 4 g + t: rows g and g + 8)
+    uint32_t qf[DH / 16][4];
+    float o[DH / 8][4];
+    float m[2], l[2];
+    int pos[2];  // their tokens' positions; INT_MIN: no such row
+
+    // element offset of position j of w's KV head in K and V, -1 for a page outside the cache
+    __device__ long long offset_of(const ChunkWork &w, int j) const {
+        const int page = a.kv.table[(long long)w.b * a.kv.max_pages + (j >> a.kv.ps_log2)];
+        return page >= 0 && page < a.kv.n_pages
+                   ? page * a.kv.page_stride +
+                         ((((long long)w.h << a.kv.ps_log2) + (j & ((1 << a.kv.ps_log2) - 1))) * DH)
+                   : -1;
+    }
+
+    // Looks up the pages of w's tile.
+    __device__ void prepare(const ChunkWork &w) {
+        bool bad = false;
+#pragma unroll
+        for (int i = 0; i < KT / 32; ++i) {
+            const int j = (w.kt0 + w.tile) * KT + lane + 32 * i;
+            const bool key = j >= w.k.lo && j < w.k.hi;
+            row_off[i] = -1;
+            if (key) {
+                row_off[i] = offset_of(w, j);
+                bad |= row_off[i] < 0;
+            }
+        }
+        if (bad) atomicExch(a.err, 1u);
+    }
+
+    // Starts the copies of the prepared tile into stage s; keys outside the item are zeros.
+    __device__ void fetch(int s) {
+        constexpr int CH = DH / 8;           // 16-byte chunks per row
+        constexpr int RP = CK_THREADS / CH;  // rows per pass
+        const int c = tid % CH, r0 = tid / CH;
+        const uint32_t ks = smem_u32(stage0 + (size_t)s * 2 * L::TILE), vs = ks + L::TILE;
+        const T *k = static_cast<const T *>(a.kv.k), *v = static_cast<const T *>(a.kv.v);
+#pragma unroll
+        for (int i = 0; i < KT / RP; ++i) {
+            const int r = i * RP + r0;
+            // (the RP rows of a pass lie in one group of 32: RP divides 32)
+            const long long off = __shfl_sync(0xffffffffu, row_off[i * RP / 32], r & 31);
+            const long long at = off < 0 ? 0 : off + c * 8;
+            cp16_or_zero(ks + tile_off<DH>(r, c), k + at, off >= 0);
+            cp16_or_zero(vs + tile_off<DH>(r, c), v + at, off >= 0);
+        }
+    }
+
+    // A new item: its queries, straight from global memory (rows past the item's are zero).
+    __device__ void begin(const ChunkWork &w) {
+        const int rows = w.toks * a.group, wr = warp % WR, g = lane >> 2, t = lane & 3;
+        const T *base[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int row = wr * 16 + g + 8 * r;
+            base[r] = nullptr;
+            pos[r] = INT_MIN;
+            if (row < rows) {
+                const int tok = row / a.group;
+                base[r] = static_cast<const T *>(a.q) + (long long)(w.ch.row0 + w.tok + tok) * a.ld_q +
+                          (long long)(w.h * a.group + row - tok * a.group) * DH;
+                pos[r] = w.ch.base + w.tok + tok;
+            }
+        }
+#pragma unroll
+        for (int kk = 0; kk < DH / 16; ++kk)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const T *q = base[i & 1];
+                qf[kk][i] = q ? *reinterpret_cast<const uint32_t *>(q + kk * 16 + (i >> 1) * 8 + 2 * t) : 0u;
+            }
+#pragma unroll
+        for (int i = 0; i < DH / 8; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
+        m[0] = m[1] = -INFINITY;
+        l[0] = l[1] = 0.f;
+    }
+
+    // This lane's row r sees position j.
+    __device__ bool sees(int r, int j) const {
+        return j <= pos[r] && (a.window == 0 || j > (long long)pos[r] - a.window);
+    }
+
+    // One tile of the item.
+    __device__ void tile(const ChunkWork &w, bool last, int s, bool whole, int slot) {
+        const int wk = warp / WR, t = lane & 3;
+        const int j0 = (w.kt0 + w.tile) * KT;  // position of the tile's first key
+        const uint32_t ks = smem_u32(stage0 + (size_t)s * 2 * L::TILE), vs = ks + L::TILE;
+        // every row sees every key: up to the first token, from the last one's window on
+        const int first = w.ch.base + w.tok, end = first + w.toks - 1;
+        const bool full = j0 + KT - 1 <= first && j0 >= w.k.lo && (a.window == 0 || j0 > (long long)end - a.window);
+        bool odd = false;
+        if (!full) {  // values that are not finite leave the product
+            uint8_t *v = stage0 + (size_t)s * 2 * L::TILE + L::TILE;
+            for (int x = tid; x < L::TILE / 16; x += CK_THREADS) {
+                uint4 y = reinterpret_cast<uint4 *>(v)[x];
+                uint32_t *p = reinterpret_cast<uint32_t *>(&y);
+                bool found = false;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (odd_one<T>(p[i] & 0xffffu)) p[i] &= 0xffff0000u, found = true;
+                    if (odd_one<T>(p[i] >> 16)) p[i] &= 0xffffu, found = true;
+                }
+                if (found) reinterpret_cast<uint4 *>(v)[x] = y;
+                odd |= found;
+            }
+            odd = __syncthreads_or(odd);
+        }
+        float sc[2 * NB][4];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+            const int key0 = (nb * WK + wk) * 16;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) sc[2 * nb][j] = sc[2 * nb + 1][j] = 0.f;
+#pragma unroll
+            for (int kk = 0; kk < DH / 16; ++kk) {
+                // matrices: keys 0-7 | dims 0-7, keys 0-7 | dims 8-15, keys 8-15 | dims 0-7, keys 8-15 | dims 8-15
+                uint32_t r[4];
+                ldsm_x4(ks + tile_off<DH>(key0 + (lane & 7) + ((lane >> 4) << 3), 2 * kk + ((lane >> 3) & 1)), r);
+                mma<T>(sc[2 * nb], qf[kk], r[0], r[1]);
+                mma<T>(sc[2 * nb + 1], qf[kk], r[2], r[3]);
+            }
+        }
+        if (!full) {
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (!sees(i >> 1, j0 + (nb * WK + wk) * 16 + x * 8 + 2 * t + (i & 1))) sc[2 * nb + x][i] = -INFINITY;
+        }
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {  // rows g, g + 8
+            float mx = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < 2 * NB; ++i) mx = fmaxf(mx, fmaxf(sc[i][2 * r], sc[i][2 * r + 1]));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+            const float mn = fmaxf(m[r], mx * a.scale_log2);
+            const float off = mn == -INFINITY ? 0.f : mn;
+            const float fac = ex2(m[r] - off);
+            m[r] = mn;
+            l[r] *= fac;
+#pragma unroll
+            for (int i = 0; i < DH / 8; ++i) {
+                o[i][2 * r] *= fac;
+                o[i][2 * r + 1] *= fac;
+            }
+            float sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < 2 * NB; ++i)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const float e = ex2(fmaf(sc[i][2 * r + x], a.scale_log2, -off));
+                    sc[i][2 * r + x] = e;
+                    sum += e;
+                }
+            l[r] += sum;  // this lane's keys only: joined at the end
+        }
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+            const int key0 = (nb * WK + wk) * 16;
+            uint32_t pf[4];
+            pf[0] = pack2<T>(sc[2 * nb][0], sc[2 * nb][1]);
+            pf[1] = pack2<T>(sc[2 * nb][2], sc[2 * nb][3]);
+            pf[2] = pack2<T>(sc[2 * nb + 1][0], sc[2 * nb + 1][1]);
+            pf[3] = pack2<T>(sc[2 * nb + 1][2], sc[2 * nb + 1][3]);
+#pragma unroll
+            for (int d = 0; d < DH / 16; ++d) {
+                // transposed matrices: keys 0-7 | dims 0-7, keys 8-15 | dims 0-7, then dims 8-15
+                uint32_t r[4];
+                ldsm_x4_trans(vs + tile_off<DH>(key0 + (lane & 15), 2 * d + (lane >> 4)), r);
+                mma<T>(o[2 * d], pf, r[0], r[1]);
+                mma<T>(o[2 * d + 1], pf, r[2], r[3]);
+            }
+        }
+        if (odd) add_odd(w, j0, wk, t);
+        if (last) finish(w, s, whole, slot);
+    }
+
+    // Adds the tile's values that are not finite to the rows that see them.
+    __device__ __forceinline__ void add_odd(const ChunkWork &w, int j0, int wk, int t) {
+#pragma unroll 1
+        for (int key = 0; key < KT; ++key) {
+            const int j = j0 + key;
+            if ((key / 16) % WK != wk || j < w.k.lo || j >= w.k.hi) continue;
+            const long long off = offset_of(w, j);
+            if (off < 0) continue;
+            const uint16_t *v = static_cast<const uint16_t *>(a.kv.v) + off;
+#pragma unroll
+            for (int i = 0; i < DH / 8; ++i)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const uint16_t h = v[8 * i + 2 * t + x];
+                    if (!odd_one<T>(h)) continue;
+                    const float f = (float)*reinterpret_cast<const T *>(&h);
+                    if (sees(0, j)) o[i][x] += f;
+                    if (sees(1, j)) o[i][2 + x] += f;
+                }
+        }
+    }
+
+    // The item's end in this CTA: the result where it has seen all of it, a partial otherwise; warps with the same rows
+    // joined.
+    __device__ void finish(const ChunkWork &w, int s, bool whole, int slot) {
+        const int wr = warp % WR, g = lane >> 2, t = lane & 3, rows = w.toks * a.group;
+        const long long at = (long long)slot * a.slot_rows;
+        float *dst = a.part_o + at * DH;
+        float2 *dst_ml = a.part_ml + at;
+        auto result = [&](int row, int c, float x, float y, float mx, float sum) {  // dims c, c + 1
+            if (whole) {
+                const int tok = row / a.group, head = w.h * a.group + row - tok * a.group;
+                const long long q = w.ch.row0 + w.tok + tok;
+                const float inv = inverse(sum);
+                *reinterpret_cast<uint32_t *>(static_cast<T *>(a.out) + q * a.ld_out + (long long)head * DH + c) =
+                    pack2<T>(x * inv, y * inv);
+                if (c == 0 && a.lse) a.lse[q * a.n_q + head] = mx * 0.69314718055994530942f + logf(sum);
+            } else {
+                *reinterpret_cast<float2 *>(dst + (long long)row * DH + c) = make_float2(x, y);
+                if (c == 0) dst_ml[row] = make_float2(mx, sum);
+            }
+        };
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+        }
+        if constexpr (WK == 1) {
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const int row = wr * 16 + g + 8 * r;
+                if (row >= rows) continue;
+#pragma unroll
+                for (int i = 0; i < DH / 8; ++i) result(row, 8 * i + 2 * t, o[i][2 * r], o[i][2 * r + 1], m[r], l[r]);
+            }
+        } else {
+            __syncthreads();  // every warp has read this stage's keys and values
+            // row r of warp w at (w * 16 + r) * DH, its columns permuted by the row (8 rows of a warp write 8 bank groups)
+            float *red = reinterpret_cast<float *>(stage0 + (size_t)s * 2 * L::TILE);
+            auto col = [](int row, int c) { return c ^ ((row & (DH / 8 - 1) & 7) << 3); };
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const int row = g + 8 * r;
+                float *d = red + (warp * 16 + row) * DH;
+#pragma unroll
+                for (int i = 0; i < DH / 8; ++i)
+                    *reinterpret_cast<float2 *>(d + col(row, 8 * i) + 2 * t) = make_float2(o[i][2 * r], o[i][2 * r + 1]);
+                if (t == 0) ml[warp * 16 + row] = make_float2(m[r], l[r]);
+            }
+            __syncthreads();
+            for (int x = tid; x < rows * (DH / 2); x += CK_THREADS) {
+                const int row = x / (DH / 2), c = (x % (DH / 2)) * 2;
+                float mx = -INFINITY;  // over the key shares k: warp row / 16 + k * WR
+#pragma unroll
+                for (int k = 0; k < WK; ++k) mx = fmaxf(mx, ml[row + k * WR * 16].x);
+                const float off = mx == -INFINITY ? 0.f : mx;
+                float sx = 0.f, sy = 0.f, sl = 0.f;
+#pragma unroll
+                for (int k = 0; k < WK; ++k) {
+                    const float2 y = ml[row + k * WR * 16];
+                    const float f = ex2(y.x - off);
+                    const float2 v = *reinterpret_cast<const float2 *>(red + (row + k * WR * 16) * DH +
+                                                                       col(row, c & ~7) + (c & 7));
+                    sx += f * v.x;
+                    sy += f * v.y;
+                    sl += f * y.y;
+                }
+                result(row, c, sx, sy, mx, sl);
+            }
+        }
+    }
+};
+
+template <typename T, int DH, int WR>
+__global__ void __launch_bounds__(CK_THREADS, CK_CTAS_PER_SM) paged_chunk_kernel(const ChunkArgs a) {
+    extern __shared__ __align__(128) uint8_t ck_smem[];
+    pdl_wait();
+    pdl_trigger();
+    ChunkWalker<T, DH, WR>(a, ck_smem).run();
+}
+
+// The items that several CTAs share, one warp to a row: block (c, y) takes rows 4 y ..
+// of the item that CTA c began and did not end, its partials in the list's order.
+template <typename T, int DH>
+__global__ void __launch_bounds__(CK_THREADS) paged_chunk_join(const ChunkArgs a) {
+    constexpr int V = DH / 32;  // values per lane
+    const int c = blockIdx.x, lane = threadIdx.x & 31;
+    pdl_wait();
+    pdl_trigger();
+    const ChunkArgs::Join j = a.joins[c];
+    for (int row = blockIdx.y * 4 + (threadIdx.x >> 5); j.parts > 0 && row < j.rows; row += gridDim.y * 4) {
+        // partial p of the item: the CTA that begins it leaves it second, those behind first
+        auto at = [&](int p) { return (long long)(p == 0 ? 2 * c + 1 : 2 * (c + p)) * a.slot_rows + row; };
+        float mx = -INFINITY;
+        for (int p = lane; p < j.parts; p += 32) mx = fmaxf(mx, a.part_ml[at(p)].x);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        const float off = mx == -INFINITY ? 0.f : mx;
+        float acc[V], sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[i] = 0.f;
+#pragma unroll 4
+        for (int p = 0; p < j.parts; ++p) {
+            const long long s = at(p);
+            const float2 y = a.part_ml[s];
+            const float f = ex2(y.x - off);
+            sum += f * y.y;
+#pragma unroll
+            for (int i = 0; i < V; ++i) acc[i] += f * a.part_o[s * DH + lane * V + i];
+        }
+        const int tok = row / a.group, head = j.head * a.group + row - tok * a.group;
+        const long long q = j.row0 + tok;
+        const float inv = inverse(sum);
+        T *dst = static_cast<T *>(a.out) + q * a.ld_out + (long long)head * DH + lane * V;
+        if constexpr (V == 1) {
+            dst[0] = (T)(acc[0] * inv);
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; i += 2)
+                *reinterpret_cast<uint32_t *>(dst + i) = pack2<T>(acc[i] * inv, acc[i + 1] * inv);
+        }
+        if (a.lse && lane == 0) a.lse[q * a.n_q + head] = mx * 0.69314718055994530942f + logf(sum);
+    }
+}
+
+int sm_count() {
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return 0;
+    }
+    return n;
+}
+
+size_t al256(size_t n) { return (n + 255) & ~size_t(255); }
+
+// Rows of an item: 16, 32 or 64, as the sequences have on average.
+int warp_rows(const ChunkArgs &a) {
+    const long long rows = ((long long)a.n_tokens * a.group + a.kv.n_seqs - 1) / a.kv.n_seqs;
+    return rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
+}
+
+void shape(ChunkArgs &a, int n_sm) {
+    a.slot_rows = 16 * warp_rows(a);
+    a.keys = tile_keys(a.kv.head_dim);
+    a.toks = a.slot_rows / a.group;
+    a.grid = n_sm * CK_CTAS_PER_SM;
+}
+
+struct CkWs {
+    size_t ml, o, bytes;
+};
+CkWs ck_layout(const ChunkArgs &a) {
+    CkWs w;
+    const size_t rows = 2 * (size_t)a.grid * a.slot_rows;
+    w.ml = al256((size_t)a.grid * sizeof(ChunkArgs::Join));
+    w.o = w.ml + al256(rows * sizeof(float2));
+    w.bytes = w.o + rows * a.kv.head_dim * sizeof(float);
+    return w;
+}
+
+lf_status check_chunk(const lf_paged_kv *kv, int n_q_heads, int n_tokens, PagedView *v) {
+    const lf_status st = paged_view(kv, v);
+    if (st != LF_OK) return st;
+    if (n_q_heads < 1 || n_q_heads % v->n_kv || n_tokens < 0) return LF_ERR_INVALID_ARG;
+    if ((v->head_dim != 32 && v->head_dim != 64 && v->head_dim != 128) || n_q_heads / v->n_kv > CK_MAX_GROUP ||
+        v->n_seqs > CK_MAX_SEQS || n_tokens > CK_MAX_TOKENS)
+        return LF_ERR_UNSUPPORTED;
+    return LF_OK;
+}
+
+// The largest a call of up to this many tokens needs (fewer tokens may take smaller items, never larger ones).
+size_t ck_bytes(ChunkArgs a, int n_sm) {
+    shape(a, n_sm);
+    return ck_layout(a).bytes;
+}
+
+template <typename T, int DH>
+lf_status launch_chunk(const ChunkArgs &a, cudaStream_t st) {
+    constexpr int smem = CkSmem<T, DH>::BYTES;
+    bool ok = false;
+    if (a.slot_rows == 16)
+        ok = set_smem_once<paged_chunk_kernel<T, DH, 1>>(smem) &&
+             launch_pdl(paged_chunk_kernel<T, DH, 1>, a.grid, CK_THREADS, smem, st, a);
+    else if (a.slot_rows == 32)
+        ok = set_smem_once<paged_chunk_kernel<T, DH, 2>>(smem) &&
+             launch_pdl(paged_chunk_kernel<T, DH, 2>, a.grid, CK_THREADS, smem, st, a);
+    else
+        ok = set_smem_once<paged_chunk_kernel<T, DH, 4>>(smem) &&
+             launch_pdl(paged_chunk_kernel<T, DH, 4>, a.grid, CK_THREADS, smem, st, a);
+    return ok && launch_pdl(paged_chunk_join<T, DH>, dim3((unsigned)a.grid, (unsigned)((a.slot_rows + 15) / 16)),
+                            CK_THREADS, 0, st, a)
+               ? LF_OK
+               : LF_ERR_CUDA;
+}
+
+template <typename T>
+lf_status launch_chunk_dim(const ChunkArgs &a, cudaStream_t st) {
+    return a.kv.head_dim == 32   ? launch_chunk<T, 32>(a, st)
+           : a.kv.head_dim == 64 ? launch_chunk<T, 64>(a, st)
+                                 : launch_chunk<T, 128>(a, st);
+}
+
+}  // namespace
+}  // namespace lf
+
+extern "C" size_t lf_attn_paged_chunk_workspace(const lf_paged_kv *kv, int n_q_heads, int n_tokens) {
+    lf::ChunkArgs a = {};
+    if (lf::check_chunk(kv, n_q_heads, n_tokens, &a.kv) != LF_OK) return 0;
+    a.group = n_q_heads / a.kv.n_kv;
+    a.n_tokens = n_tokens;
+    const int n_sm = lf::sm_count();
+    return n_sm ? lf::ck_bytes(a, n_sm) : 0;
+}
+
+extern "C" lf_status lf_attn_paged_chunk(const lf_paged_kv *kv, const void *q_device, int64_t ld_q, void *out_device,
+                                         int64_t ld_out, float *lse_device, int n_q_heads,
+                                         const int32_t *starts_device, int n_tokens, const int32_t *lens_device,
+                                         int max_len, int window, float scale, void *workspace_device,
+                                         size_t workspace_bytes, uint32_t *err_device, void *cuda_stream) {
+    lf::ChunkArgs a = {};
+    const lf_status cs = lf::check_chunk(kv, n_q_heads, n_tokens, &a.kv);
+    if (cs != LF_OK) return cs;
+    const int64_t row = (int64_t)n_q_heads * kv->head_dim, cap = (int64_t)kv->max_pages * kv->page_size;
+    auto off4 = [](const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; };
+    if (!q_device || !out_device || !starts_device || !lens_device || !workspace_device || !err_device ||
+        !lf::aligned16(q_device) || !lf::aligned16(out_device) || off4(lse_device) || off4(starts_device) ||
+        off4(lens_device) || off4(err_device) || (reinterpret_cast<uintptr_t>(workspace_device) & 255u) || ld_q < row ||
+        ld_out < row || ld_q % 8 || ld_out % 8 || (q_device == out_device && ld_q != ld_out) || max_len < 0 ||
+        max_len > cap || window < 0 || !(scale > 0.f && scale * lf::kLog2e < INFINITY))
+        return LF_ERR_INVALID_ARG;
+    a.group = n_q_heads / a.kv.n_kv;
+    a.n_tokens = n_tokens;
+    const int n_sm = lf::sm_count();
+    if (!n_sm) return LF_ERR_CUDA;
+    lf::shape(a, n_sm);
+    // tiles are counted in 32 bits
+    if (((long long)n_tokens / a.toks + kv->n_seqs) * ((long long)max_len / a.keys + 2) * kv->n_kv_heads > INT_MAX)
+        return LF_ERR_UNSUPPORTED;
+    if (workspace_bytes < lf::ck_bytes(a, n_sm)) return LF_ERR_INVALID_ARG;
+    if (n_tokens == 0) return LF_OK;
+    const lf::CkWs w = lf::ck_layout(a);
+    uint8_t *ws = static_cast<uint8_t *>(workspace_device);
+    a.joins = reinterpret_cast<lf::ChunkArgs::Join *>(ws);
+    a.part_ml = reinterpret_cast<float2 *>(ws + w.ml);
+    a.part_o = reinterpret_cast<float *>(ws + w.o);
+    a.q = q_device;
+    a.out = out_device;
+    a.lse = lse_device;
+    a.ld_q = ld_q;
+    a.ld_out = ld_out;
+    a.n_q = n_q_heads;
+    a.starts = starts_device;
+    a.lens = lens_device;
+    a.max_len = max_len;
+    a.window = window >= max_len ? 0 : window;  // (every position lies less than max_len back)
+    a.scale_log2 = scale * lf::kLog2e;
+    a.err = err_device;
+    cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
+    return kv->dtype == LF_F16 ? lf::launch_chunk_dim<__half>(a, st) : lf::launch_chunk_dim<__nv_bfloat16>(a, st);
+}

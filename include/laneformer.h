@@ -461,7 +461,12 @@ lf_status lf_gemv_f16(const void *w_device, const void *x_device, float *y_devic
  * graph.  What a kernel can only see on the device (a page number, a length,
  * a position, a filter's value) is checked there, never trusted as an index.
  */
-typedef enum { LF_F32 = 0, LF_F16 = 1, LF_BF16 = 2 } lf_dtype;
+typedef enum {
+    LF_F32 = 0,
+    LF_F16 = 1,
+    LF_BF16 = 2,
+    LF_E4M3 = 3 /* 8 bits, finite, at most 448: lf_add_rmsnorm's output and lf_matmul_f8's operands only */
+} lf_dtype;
 
 /* A paged KV cache (one layer).  Page g of K holds page_size positions of
  * every KV head, [n_kv_heads][page_size][head_dim] from k + g * page_stride
@@ -589,6 +594,128 @@ lf_status lf_sample_filtered(const void *logits_device, int dtype, int rows, int
                              const float *temperature_device, const int32_t *top_k_device, const float *top_p_device,
                              const float *min_p_device, const float *u_device, int32_t *token_device,
                              float *logprob_device, void *cuda_stream);
+
+/*
+ * Operators of a pass over several new tokens per sequence (a chunk of a
+ * prompt, drafted tokens to check, a continuation to score), for callers that
+ * build their own passes beside the calls above: the norm with the residual's
+ * addition, the product of 8-bit operands, the attention of the new tokens over
+ * the paged cache that lf_kv_append_paged has put them into, and the log
+ * probabilities of given tokens.  They are asynchronous and work on
+ * `cuda_stream` as the three above do: nothing is allocated, graphs may capture
+ * them, and what only the device can see is checked there.
+ */
+
+/* RMSNorm with the residual's addition: per row
+ *   s = x + residual,   y = gain * s / sqrt(mean(s^2) + eps).
+ *   x_device: DEVICE [rows][cols] of x_dtype, row stride ld_x; residual_device:
+ *   the same of residual_dtype, row stride ld_residual (NULL: s = x);
+ *   sum_device: s rounded to residual_dtype, row stride ld_sum (NULL: not wanted);
+ *   gain_device: DEVICE [cols] of gain_dtype (NULL: 1);
+ *   out_device: y in out_dtype (LF_F32, LF_F16, LF_BF16 or LF_E4M3), row stride
+ *   ld_out; for LF_E4M3 what is stored is y / scale, scale_device[r] (DEVICE
+ *   fp32 [rows], unused otherwise) = max |y| of row r / 448, or 1 where that is not
+ *   a finite number above 0, so that y is out * scale.
+ * Types are LF_F32, LF_F16 or LF_BF16 where nothing else is said; every pointer is
+ * aligned to its type (rows of 16-byte multiples, cols a multiple of 8, are the
+ * fast way).  s and the sum of its squares are fp32 (a row whose squares pass
+ * 3e38 gets zeros), y is taken of s before its rounding and rounded once
+ * itself.  sum_device may be x_device or residual_device, and out_device too (but
+ * not sum_device), where types and strides are equal; arrays overlap in no other way.  A
+ * NaN or infinity stays in its row.  rows 0 does nothing.
+ * LF_ERR_INVALID_ARG for bad sizes, pointers, strides or types and eps not
+ * finite and above 0; LF_ERR_UNSUPPORTED for cols above 32768. */
+lf_status lf_add_rmsnorm(const void *x_device, int x_dtype, int64_t ld_x, const void *residual_device,
+                         void *sum_device, int residual_dtype, int64_t ld_residual, int64_t ld_sum,
+                         const void *gain_device, int gain_dtype, int rows, int cols, float eps, void *out_device,
+                         int out_dtype, int64_t ld_out, float *scale_device, void *cuda_stream);
+
+/* Tensor-core product of 8-bit operands with a scale per row of each:
+ *   c[m][n] = a_scale[m] * b_scale[n] * sum_k a[m][k] * b[n][k],
+ * a (m x k) and b (n x k) row-major LF_E4M3 DEVICE arrays (16-byte aligned; what
+ * lf_add_rmsnorm leaves, and a weight matrix in its [out][in] layout), the scales
+ * DEVICE fp32 [m] and [n] (NULL: 1), c an m x n row-major DEVICE array of c_dtype
+ * (LF_F32, LF_F16 or LF_BF16).  k is a multiple of 16; m or n 0 does nothing.  The
+ * products are summed in fp32 by the tensor core, scaled and rounded once; a value
+ * beyond c_dtype's range becomes infinite.  *err_device (DEVICE word, cleared by the
+ * caller) becomes non-zero if a device-side wait ran out (2 s).
+ * LF_ERR_INVALID_ARG for bad sizes, pointers or types; LF_ERR_UNSUPPORTED where
+ * m + 128 or n + 256 pass 2^31 or c has more than 2^31 tiles. */
+lf_status lf_matmul_f8(const void *a_device, const float *a_scale_device, const void *b_device,
+                       const float *b_scale_device, void *c_device, int c_dtype, int m, int n, int k,
+                       uint32_t *err_device, void *cuda_stream);
+
+/* Attention of each sequence's new tokens over the paged cache, which holds their
+ * keys and values already.  The new tokens of sequence b are rows starts[b] ..
+ * starts[b + 1] - 1 of q and out, and the last ones of its lens[b] cached positions:
+ * the i-th of c is position p = lens[b] - c + i and sees the positions j <= p, with a
+ * window only those with j > p - window (window 0: all):
+ *   out[t][h] = sum_j w_j v_j,  w = softmax_j(scale * q[t][h] . k_j),
+ * query head h reading KV head h / (n_q_heads / n_kv_heads).  One new token per
+ * sequence is plain decode attention; lens equal to the chunks is a prompt's causal
+ * attention; sequences of both kinds, and without a new token, may mix.
+ *   q_device, out_device: DEVICE [n_tokens][n_q_heads][head_dim] of the cache's
+ *   dtype, row strides ld_q and ld_out elements (16-byte multiples); out may be q
+ *   itself where the strides are equal, and otherwise does not overlap it;
+ *   lse_device: DEVICE [n_tokens][n_q_heads] fp32, the natural log of the softmax's
+ *   denominator; NULL: not wanted;
+ *   starts_device: DEVICE int32 [n_seqs + 1], non-decreasing, 0 .. n_tokens; rows
+ *   before starts[0] and from starts[n_seqs] on are not touched (a batch padded to
+ *   n_tokens rows);
+ *   lens_device: DEVICE int32 [n_seqs], counting the new tokens; a token that is
+ *   left with a position below 0 (a chunk longer than its sequence) sees nothing
+ *   and gets zeros and lse -inf;
+ *   max_len: upper bound of the lengths; scale: above 0, scale * log2(e) finite;
+ *   workspace_device: DEVICE scratch of at least lf_attn_paged_chunk_workspace bytes
+ *   for this n_tokens or more, 256-byte aligned; no initial content, nothing
+ *   held between calls, one call (or one replayed graph) at a time.
+ * What a token does not see never reaches its result, whatever the cache holds
+ * there (NaN included), in its own chunk too.  Scores, softmax statistics and sums
+ * are fp32; the softmax weights enter the second product rounded to the cache's
+ * type.  The result does not depend on timing, only on the arguments and the SM
+ * count.  A length outside [0, max_len] (taken as 0), a start outside its bounds
+ * (that sequence is taken as without new tokens) or a page outside the cache (the
+ * result is then undefined) sets *err_device (DEVICE word, cleared by the caller) to
+ * 1, a device-side wait that ran out (2 s) to 2.  n_tokens 0 does nothing.
+ * LF_ERR_INVALID_ARG for bad sizes, pointers, strides or types, max_len above
+ * max_pages * page_size, or a workspace too small; LF_ERR_UNSUPPORTED for head_dim
+ * other than 32, 64 or 128, more than 16 query heads per KV head, more than 1024
+ * sequences, or n_tokens * max_len * n_q_heads above about 2^41. */
+lf_status lf_attn_paged_chunk(const lf_paged_kv *kv, const void *q_device, int64_t ld_q, void *out_device,
+                              int64_t ld_out, float *lse_device, int n_q_heads, const int32_t *starts_device,
+                              int n_tokens, const int32_t *lens_device, int max_len, int window, float scale,
+                              void *workspace_device, size_t workspace_bytes, uint32_t *err_device, void *cuda_stream);
+
+/* Workspace bytes of lf_attn_paged_chunk for this cache and up to n_tokens rows on
+ * the current device, whatever the chunks and lengths; 0 where that call would
+ * refuse the sizes (or there is no device). */
+size_t lf_attn_paged_chunk_workspace(const lf_paged_kv *kv, int n_q_heads, int n_tokens);
+
+/* Log probabilities of given tokens, with the distribution's entropy and its most
+ * probable tokens.  For row r with z = its logits, T = temperature[r] and
+ * p = softmax(z / T):
+ *   logprob[r] = ln p[token[r]];   entropy[r] = -sum_i p_i ln p_i;
+ *   rank[r] = how many tokens come before token[r] when all are ordered by logit,
+ *   the lower index first among equal ones (0: it is the greedy token);
+ *   top_token[r][0 .. top_n - 1]: the first of that order, top_logprob their ln p.
+ *   logits_device: DEVICE [rows] rows of vocab values of dtype (LF_F32, LF_F16 or
+ *   LF_BF16), ld elements apart (ld >= vocab), aligned to the type;
+ *   temperature_device: DEVICE fp32 [rows], in [1e-30, 1e30]; NULL: 1 for every row;
+ *   token_device: DEVICE int32 [rows]; a token outside [0, vocab) asks for nothing:
+ *   logprob NaN, rank -1; NULL: logprob and rank are not wanted and must be NULL too;
+ *   top_n: 0 .. 32 and at most vocab; top_token_device, top_logprob_device: DEVICE
+ *   [rows][top_n] int32 and fp32; each of the five results may be NULL: not wanted.
+ * Sums are fp32 and in a fixed order.  A logit of -inf has probability 0 and is
+ * never among the most probable: places left over get token -1, logprob -inf.  If
+ * some logits are +inf, those alone hold the mass, equally.  A row with a NaN,
+ * without a logit above -inf, or with T outside its range gets logprob and
+ * entropy NaN, rank -1, tokens -1 and top_logprob NaN.  rows 0 does nothing.
+ * LF_ERR_INVALID_ARG for bad sizes, types or pointers; LF_ERR_UNSUPPORTED for a
+ * vocabulary above 262144. */
+lf_status lf_token_logprobs(const void *logits_device, int dtype, int rows, int vocab, int64_t ld,
+                            const float *temperature_device, const int32_t *token_device, int top_n,
+                            float *logprob_device, int32_t *rank_device, float *entropy_device,
+                            int32_t *top_token_device, float *top_logprob_device, void *cuda_stream);
 
 /*
  * Debug build.  liblaneformer_debug.so is the same library compiled with
