@@ -26,7 +26,7 @@ LIB_DEBUG = os.path.join(PKG, "liblaneformer_debug.so")
 SOURCES = ["lf_plan.cpp", "lf_kernel.cu", "lf_runtime.cu", "lf_noalloc.cu", "lf_tc_gemm.cu", "lf_prefill.cu",
            "lf_pf_attn_tc.cu", "lf_sample.cu", "lf_gemv_tc.cu", "lf_batch.cu", "lf_stream.cu",
            "lf_paged.cu", "lf_paged_attn.cu", "lf_paged_attn_tc.cu", "lf_sample_filtered.cu", "lf_norm.cu",
-           "lf_matmul_f8.cu", "lf_logprobs.cu", "lf_paged_chunk.cu"]
+           "lf_matmul_f8.cu", "lf_logprobs.cu", "lf_paged_chunk.cu", "lf_paged_chunk_tc.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

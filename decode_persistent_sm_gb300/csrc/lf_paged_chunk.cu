@@ -450,17 +450,18 @@ int sm_count() {
 
 size_t al256(size_t n) { return (n + 255) & ~size_t(255); }
 
-// Rows of an item: 16, 32 or 64, as the sequences have on average.
-int warp_rows(const ChunkArgs &a) {
-    const long long rows = ((long long)a.n_tokens * a.group + a.kv.n_seqs - 1) / a.kv.n_seqs;
-    return rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
-}
+// The tensor-core kernel takes head_dim 64 and 128, pages of at least 8 positions
+// (a TMA box) and page strides that a tensor map can hold (2^40 bytes).
+bool tc_fits(const PagedView &v) { return v.head_dim >= 64 && v.ps_log2 >= 3 && v.page_stride < (1ll << 38); }
 
+// Rows of an item: 16, 32 or 64, as the sequences have on average; beyond 64 the tensor cores' 256.
 void shape(ChunkArgs &a, int n_sm) {
-    a.slot_rows = 16 * warp_rows(a);
-    a.keys = tile_keys(a.kv.head_dim);
-    a.toks = a.slot_rows / a.group;
-    a.grid = n_sm * CK_CTAS_PER_SM;
+    const long long rows = ((long long)a.n_tokens * a.group + a.kv.n_seqs - 1) / a.kv.n_seqs;
+    a.tc = rows > 64 && tc_fits(a.kv);
+    a.slot_rows = a.tc ? kTcRows : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+    a.keys = a.tc ? kTcKeys : tile_keys(a.kv.head_dim);
+    a.toks = a.tc ? 2 * (128 / a.group) : a.slot_rows / a.group;  // (a 128-row tile holds whole tokens)
+    a.grid = a.tc ? n_sm : n_sm * CK_CTAS_PER_SM;
 }
 
 struct CkWs {
@@ -495,7 +496,15 @@ template <typename T, int DH>
 lf_status launch_chunk(const ChunkArgs &a, cudaStream_t st) {
     constexpr int smem = CkSmem<T, DH>::BYTES;
     bool ok = false;
-    if (a.slot_rows == 16)
+    if constexpr (DH >= 64) {
+        if (a.tc) {
+            const lf_status ts = paged_chunk_tc(a, std::is_same<T, __half>::value ? LF_F16 : LF_BF16, st);
+            if (ts != LF_OK) return ts;
+            ok = true;
+        }
+    }
+    if (a.tc) {
+    } else if (a.slot_rows == 16)
         ok = set_smem_once<paged_chunk_kernel<T, DH, 1>>(smem) &&
              launch_pdl(paged_chunk_kernel<T, DH, 1>, a.grid, CK_THREADS, smem, st, a);
     else if (a.slot_rows == 32)

@@ -23,6 +23,7 @@ struct ChunkArgs {
     const int32_t *starts, *lens;
     int n_tokens, max_len, window;  // window 0: none
     float scale_log2;
+    bool tc;                    // the tensor cores' kernel
     int keys, toks, slot_rows;  // rows of a partial in the workspace: at least toks * group
     int grid;                   // CTAs that share the list
     // A CTA works on at most two items that it does not see whole: one that an
@@ -225,7 +226,8 @@ __device__ __forceinline__ ChunkArgs::Join chunk_join(const ChunkArgs &a, const 
     return j;
 }
 
-// The join of the items that several CTAs share (lf_paged_chunk.cu).
-lf_status paged_chunk_join(const ChunkArgs &a, int dtype, cudaStream_t st);
+// The list's kernel on the 5th-generation tensor cores (lf_paged_chunk_tc.cu): head_dim 64 and 128, keys = kTcKeys,
+// toks even, slot_rows = kTcRows.
+lf_status paged_chunk_tc(const ChunkArgs &a, int dtype, cudaStream_t st);
 
 }  // namespace lf

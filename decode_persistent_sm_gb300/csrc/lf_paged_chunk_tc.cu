@@ -1,0 +1,523 @@
+// lf_attn_paged_chunk on the 5th-generation tensor cores (tcgen05 + TMA + TMEM), for
+// chunks whose rows (token, query head) of one KV head are many.
+//
+// An item is two M = 128 row tiles of consecutive tokens of one sequence and KV head;
+// the list of its tiles of 128 keys and its shares are lf_paged_chunk.h's, one
+// CTA per SM.  Per key tile and row tile x:
+//   S = Q K^T into TMEM; the row tile's softmax warpgroup, a row per thread,
+//   reads S, moves the row's running max (only when it grows by more than 2^8,
+//   so P stays below 256), and writes P in the cache's type back over S;
+//   O += P V with P as the A operand from TMEM.
+// The two row tiles take turns: one's softmax runs under the other's products.  P is
+// handed over in two pieces: the products with its first 96 keys run while the
+// exponentials of the last 32 are still computed.
+//
+// K and V pages come by TMA (one box of min(page size, 128) positions x 64 dims
+// each), double-buffered; V is read as it lies, [key][dim], as an MN-major B
+// operand.  Tiles are cut at multiples of 128 positions, so boxes never cross a page;
+// pages without a key of the item are loaded from outside the tensor, as zeros.
+//
+// Masks.  A tile that some row does not see whole has its scores masked by position.
+// What lies behind the sequence's end in the last page, before a window's start, or
+// is not finite would still reach the product as 0 times itself: in such a tile
+// the first warpgroup zeroes those values in shared memory (a thread per key, before
+// it hands over P), and at the item's end the values that are not finite are
+// added to the rows that do see them.
+//
+// Every wait is bounded; a CTA that ran out of time flags it, lets its copies
+// and products finish (bounded), frees its TMEM and exits.
+#include <climits>
+
+#include "lf_paged_chunk.h"
+#include "lf_paged_tc.cuh"
+
+namespace lf {
+namespace {
+
+constexpr int C_THREADS = 320;         // copy warp, MMA warp, 2 x 4 softmax warps
+constexpr uint32_t C_TMEM_COLS = 512;  // S / P of row tile x at 128 x, O at 256 + 128 x
+constexpr uint32_t C_O = 256;
+constexpr int C_FIRST = 96;            // keys of P's first piece (a multiple of 32)
+constexpr unsigned long long kChunkTimeoutNs = 2000000000ull;
+
+// Every barrier completes once per use of what it guards, and no waiter can
+// fall two phases behind, so parity waits are unambiguous.
+struct CtShared {
+    uint64_t bq[2];     // Q of row tile x written (128 arrivals)
+    uint64_t bk0;       // K of the first tile loaded
+    uint64_t bl[2];     // V of tile p and K of tile p + 1 loaded (p = 0, 2, .. and 1, 3, ..)
+    uint64_t bf[2];     // done: the S products of tile p and the P V products of tile p - 1 (p = 0, 2, .. and 1, 3, ..)
+    uint64_t bs[2];     // row tile x: S of the next tile computed (and its earlier P V done)
+    uint64_t bp[2][2];  // row tile x: first and last piece of P written to TMEM (128 arrivals)
+    uint64_t bo[2];     // row tile x: the last P V of an item done
+    uint64_t bdone;     // every product this CTA issued is done (one commit at the end)
+    uint32_t tmem;
+    volatile int abort_;
+    volatile int issued_;   // 1 once any product was issued (then bdone gets its commit)
+    volatile int odd_[4];   // an item's masked tiles hold values that are not finite (items in turn)
+};
+
+__device__ __forceinline__ bool await_phase(CtShared &S, uint64_t *bar, uint32_t parity, uint64_t deadline,
+                                            uint32_t *err) {
+    if (mbar_test_wait(bar, parity)) return true;
+    while (!mbar_try_wait(bar, parity)) {
+        if (S.abort_) return false;
+        if (global_timer_ns() > deadline) {
+            atomicExch(err, 2u);
+            S.abort_ = 1;
+            return false;
+        }
+    }
+    return true;
+}
+
+// (x, y) * c + d and x + y, two values to an instruction
+__device__ __forceinline__ float2 fma2(float2 x, float2 c, float2 d) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(r)
+        : "l"(*reinterpret_cast<const uint64_t *>(&x)), "l"(*reinterpret_cast<const uint64_t *>(&c)),
+          "l"(*reinterpret_cast<const uint64_t *>(&d)));
+    return *reinterpret_cast<float2 *>(&r);
+}
+__device__ __forceinline__ float2 add2(float2 x, float2 y) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(r)
+        : "l"(*reinterpret_cast<const uint64_t *>(&x)), "l"(*reinterpret_cast<const uint64_t *>(&y)));
+    return *reinterpret_cast<float2 *>(&r);
+}
+
+// Two 16-bit values of a word: those that are infinite or NaN become 0; true if there was one.
+template <typename T>
+__device__ __forceinline__ bool drop_odd(uint32_t &w) {
+    constexpr uint32_t e = std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u;
+    bool found = false;
+    if ((w & e) == e) w &= 0xffff0000u, found = true;
+    if ((w & (e << 16)) == (e << 16)) w &= 0xffffu, found = true;
+    return found;
+}
+
+template <int DH>
+struct CtSmem {
+    static constexpr int HALVES = DH / 64;
+    static constexpr int TILE = HALVES * T_HALF;  // one row tile of Q, one buffer of K or V
+    static constexpr int Q = 0, K = 2 * TILE, V = 4 * TILE, TILES = 6 * TILE;
+    static constexpr int CUM = TILES + 256;
+    static constexpr int BYTES = CUM + (1024 + 4) * 4 + 1024;
+    static_assert(sizeof(CtShared) <= 256, "the barriers' place");
+};
+
+template <typename T, int DH>
+__global__ void __launch_bounds__(C_THREADS, 1)
+    paged_chunk_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                          const ChunkArgs a) {
+    using L = CtSmem<DH>;
+    extern __shared__ __align__(1024) uint8_t ct_raw[];
+    uint8_t *t = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(ct_raw) + 1023) & ~uintptr_t(1023));
+    CtShared &S = *reinterpret_cast<CtShared *>(t + L::TILES);
+    int *cum = reinterpret_cast<int *>(t + L::CUM);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x;
+
+    if (threadIdx.x == 0) {
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&S.bq[b], 128);
+            mbar_init(&S.bl[b], 1);
+            mbar_init(&S.bf[b], 1);
+            mbar_init(&S.bs[b], 1);
+            mbar_init(&S.bp[b][0], 128);
+            mbar_init(&S.bp[b][1], 128);
+            mbar_init(&S.bo[b], 1);
+            S.odd_[b] = S.odd_[2 + b] = 0;
+        }
+        mbar_init(&S.bk0, 1);
+        mbar_init(&S.bdone, 1);
+        S.abort_ = 0;
+        S.issued_ = 0;
+        fence_barrier_init();
+        tma_prefetch_map(&tmK);
+        tma_prefetch_map(&tmV);
+    }
+    pdl_wait();
+    pdl_trigger();
+    const int total = chunk_plan(a, cum);
+    const Shares sh(total, gridDim.x);
+    if (threadIdx.x == 0) a.joins[cta].parts = 0;
+    if (cta >= min(total, (int)gridDim.x)) return;  // (the whole block, before it holds any TMEM)
+    const int u0 = sh.begin(cta), u1 = sh.begin(cta + 1), n = u1 - u0;
+    const uint64_t deadline = global_timer_ns() + kChunkTimeoutNs;
+    const int tx = a.toks / 2;  // tokens of a row tile
+    ChunkWork w = chunk_place(a, cum, u0);  // every warp walks the list for itself
+    if (warp == 1) tc_alloc(&S.tmem, C_TMEM_COLS);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = S.tmem;
+
+    if (warp == 0) {
+        // copies: lane i < boxes looks up and loads the tile's i-th box
+        const int box = min(1 << a.kv.ps_log2, kTcKeys), boxes = kTcKeys / box;
+        struct Box {
+            int h, page, row;
+        };
+        int started = 0;  // loads on bl so far
+        auto place = [&] {  // this lane's box of w's tile
+            const int at = (w.kt0 + w.tile) * kTcKeys + lane * box;
+            Box x;
+            x.h = w.h;
+            x.page = a.kv.n_pages;  // outside the tensor: zeros
+            x.row = at & ((1 << a.kv.ps_log2) - 1);
+            if (lane < boxes && at < w.k.hi && at + box > w.k.lo) {
+                const int p = a.kv.table[(long long)w.b * a.kv.max_pages + (at >> a.kv.ps_log2)];
+                if (p >= 0 && p < a.kv.n_pages)
+                    x.page = p;
+                else
+                    atomicExch(a.err, 1u);
+            }
+            return x;
+        };
+        auto load = [&](int tile_at, const CUtensorMap *map, const Box &x, uint64_t *bar) {
+            if (lane < boxes)
+                for (int i = 0; i < L::HALVES; ++i)
+                    tma_load_4d(t + tile_at + lane * box * 128 + i * T_HALF, map, 64 * i, x.row, x.h, x.page, bar);
+        };
+        Box now = place(), then = now;
+        if (lane == 0) mbar_arrive_expect_tx(&S.bk0, L::TILE);
+        __syncwarp();
+        load(L::K, &tmK, now, &S.bk0);
+        bool ok = true;
+        for (int j = 0; j < n; ++j) {  // V of tile j and K of the next
+            if (j + 1 < n) {
+                chunk_advance(a, cum, w);
+                then = place();
+            }
+            // their buffers are free once the S products of tile j - 1 and the P V products of tile j - 2 are done
+            if (j >= 1) ok = await_phase(S, &S.bf[(j - 1) & 1], ((j - 1) >> 1) & 1u, deadline, a.err);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            uint64_t *bar = &S.bl[j & 1];
+            if (lane == 0) mbar_arrive_expect_tx(bar, j + 1 < n ? 2 * L::TILE : L::TILE);
+            __syncwarp();
+            load(L::V + (j & 1) * L::TILE, &tmV, now, bar);
+            if (j + 1 < n) load(L::K + ((j + 1) & 1) * L::TILE, &tmK, then, bar);
+            ++started;
+            now = then;
+        }
+        if (S.abort_ && lane == 0) {  // let the copies in flight land
+            const uint64_t dl = global_timer_ns() + 1000000000ull;
+            while (!mbar_try_wait(&S.bk0, 0) && global_timer_ns() < dl) {
+            }
+            for (int i = max(0, started - 2); i < started; ++i)
+                while (!mbar_try_wait(&S.bl[i & 1], (i >> 1) & 1u) && global_timer_ns() < dl) {
+                }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {  // products, issued in order by this one thread
+            constexpr uint32_t kIdescS = idesc<T>(128, kTcKeys, false), kIdescO = idesc<T>(128, DH, true);
+            // (descriptors of what lies `bytes` further: the address is in the low word)
+            auto on = [](uint64_t d, uint32_t bytes) {
+                return (d & 0xffffffff00000000ull) | (uint32_t)((uint32_t)d + (bytes >> 4));
+            };
+            const uint64_t q0 = smem_desc_sw128(smem_u32(t + L::Q)), k0 = smem_desc_sw128(smem_u32(t + L::K)),
+                           v0 = desc_mn_sw128(smem_u32(t + L::V));
+            auto qk = [&](int x, int j) {
+                const uint64_t q = on(q0, (uint32_t)x * L::TILE), k = on(k0, (uint32_t)(j & 1) * L::TILE);
+#pragma unroll
+                for (int kk = 0; kk < DH / 16; ++kk) {
+                    const uint32_t off = (uint32_t)(kk >> 2) * T_HALF + (uint32_t)(kk & 3) * 32;
+                    tc_mma(tmem + (uint32_t)x * kTcKeys, on(q, off), on(k, off), kIdescS, kk > 0);
+                }
+            };
+            auto pv = [&](int x, int j, bool first, int kk0, int kk1) {  // steps of 16 keys
+                const uint64_t v = on(v0, (uint32_t)(j & 1) * L::TILE);
+#pragma unroll
+                for (int kk = kk0; kk < kk1; ++kk)
+                    tc_mma_tmem_a(tmem + C_O + (uint32_t)x * 128, tmem + (uint32_t)x * kTcKeys + (uint32_t)kk * 8,
+                                  on(v, (uint32_t)kk * 16 * 128), kIdescO, (!first || kk > 0) ? 1u : 0u);
+            };
+            int np[2] = {0, 0}, nq[2] = {0, 0};  // uses of bp and bq so far
+            int nx = w.toks > tx ? 2 : 1;        // row tiles in use
+            bool first = true, ok = await_phase(S, &S.bk0, 0, deadline, a.err);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {  // (unrolled: the issuing thread's own instructions are on the critical path)
+                if (!ok || x >= nx) break;
+                ok = await_phase(S, &S.bq[x], nq[x]++ & 1u, deadline, a.err);
+                if (!ok) break;
+                tc_fence_after();
+                qk(x, 0);
+                S.issued_ = 1;
+                tc_commit(&S.bs[x]);
+            }
+            if (ok) tc_commit(&S.bf[0]);
+            for (int j = 0; ok && j < n; ++j) {
+                const int b = j & 1, b1 = (j + 1) & 1;
+                const bool ends = w.tile + 1 == w.tiles;  // the next tile belongs to another item
+                ok = await_phase(S, &S.bl[b], (j >> 1) & 1u, deadline, a.err);
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    if (!ok || x >= nx) break;
+                    const uint32_t ph = np[x]++ & 1u;
+                    ok = await_phase(S, &S.bp[x][0], ph, deadline, a.err);
+                    if (!ok) break;
+                    tc_fence_after();
+                    pv(x, j, first, 0, C_FIRST / 16);
+                    ok = await_phase(S, &S.bp[x][1], ph, deadline, a.err);
+                    if (!ok) break;
+                    tc_fence_after();
+                    pv(x, j, false, C_FIRST / 16, kTcKeys / 16);
+                    if (ends || j + 1 == n) tc_commit(&S.bo[x]);
+                    if (j + 1 < n && !ends) {  // after the P V that read P from the same columns
+                        qk(x, j + 1);
+                        tc_commit(&S.bs[x]);
+                    }
+                }
+                if (!ok) break;
+                first = false;
+                if (j + 1 < n) chunk_advance(a, cum, w);
+                if (ends && j + 1 < n) {  // both row tiles are on their way out; the next item's Q follows
+                    first = true;
+                    nx = w.toks > tx ? 2 : 1;
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        if (!ok || x >= nx) break;
+                        ok = await_phase(S, &S.bq[x], nq[x]++ & 1u, deadline, a.err);
+                        if (!ok) break;
+                        tc_fence_after();
+                        qk(x, j + 1);
+                        tc_commit(&S.bs[x]);
+                    }
+                    if (!ok) break;
+                }
+                tc_commit(&S.bf[b1]);
+            }
+            if (S.issued_) tc_commit(&S.bdone);  // tracks everything issued above
+        }
+    } else {  // softmax warpgroup x: warp w owns TMEM lanes (rows) 32 * (w % 4) .. + 31
+        const int x = (warp - 2) >> 2, quarter = warp & 3, row = 32 * quarter + lane;
+        const uint32_t trow = tmem + ((uint32_t)(32 * quarter) << 16);
+        const uint32_t ts = trow + (uint32_t)x * kTcKeys, to = trow + C_O + (uint32_t)x * 128;
+        const float sc2 = a.scale_log2;
+        constexpr float kLazy = 8.f;  // log2 of the largest P before the max moves
+        int left = n, at_tile = 0, ns = 0, no = 0;  // ns, no: uses of bs and bo so far
+        bool ok = true, whole = w.tile == 0;        // whole: this CTA has begun the item
+        for (int it = 0; ok && left > 0; ++it) {
+            const int count = min(left, w.tiles - w.tile);  // tiles of this item in this CTA
+            const bool ends = w.tile + count == w.tiles;
+            if (x == 0 && row == 0 && count == left) a.joins[cta] = chunk_join(a, w, sh, cta, u1, w.tile + count, whole);
+            const int toks = min(tx, w.toks - x * tx), rows = toks * a.group;
+            if (toks > 0) {
+                const int tok = min(row, rows - 1) / a.group;
+                const bool mine = row < rows, warp_used = 32 * quarter < rows;
+                const long long q_row = (long long)w.ch.row0 + w.tok + x * tx + tok;
+                const int head = w.h * a.group + (row - tok * a.group);
+                const int pos = mine ? w.ch.base + w.tok + x * tx + tok : INT_MIN;
+                {  // Q of this row into the swizzled tile; the item before is done with it (its last P V was awaited)
+                    uint8_t *qs = t + L::Q + x * L::TILE;
+                    const T *src = mine ? static_cast<const T *>(a.q) + q_row * a.ld_q + (long long)head * DH : nullptr;
+                    uint4 v[DH / 8];  // (all loads before the first store)
+#pragma unroll
+                    for (int c = 0; c < DH / 8; ++c)
+                        v[c] = src ? reinterpret_cast<const uint4 *>(src)[c] : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+                    for (int c = 0; c < DH / 8; ++c)
+                        *reinterpret_cast<uint4 *>(qs + (c >> 3) * T_HALF + sw128_offset(row, (c & 7) * 8)) = v[c];
+                    fence_proxy_async_shared();
+                    mbar_arrive(&S.bq[x]);
+                }
+                // what every row of the item sees: up to its first token, from its last one's window on
+                const int first_pos = w.ch.base + w.tok, last_pos = first_pos + w.toks - 1;
+                float m2 = -INFINITY, l = 0.f;
+                for (int j = 0; j < count; ++j, ++ns) {
+                    const int j0 = (w.kt0 + w.tile + j) * kTcKeys;
+                    const bool full = j0 + kTcKeys - 1 <= first_pos && (a.window == 0 || j0 > (long long)last_pos - a.window);
+                    if (!full && x == 0) {  // V of this tile: a key per thread
+                        const int vj = at_tile + j;
+                        ok = ok && await_phase(S, &S.bl[vj & 1], (vj >> 1) & 1u, deadline, a.err);
+                        if (ok) {
+                            const bool none = j0 + row < w.k.lo || j0 + row >= w.k.hi;
+                            uint8_t *v = t + L::V + (vj & 1) * L::TILE + row * 128;
+                            bool odd = false;
+#pragma unroll 4
+                            for (int i = 0; i < DH / 8; ++i) {  // (lanes begin at different pieces: different banks)
+                                uint4 *p = reinterpret_cast<uint4 *>(v + (i >> 3) * T_HALF + (((i & 7) ^ (lane & 7)) << 4));
+                                uint4 y = none ? make_uint4(0u, 0u, 0u, 0u) : *p;
+                                const bool found = drop_odd<T>(y.x) | drop_odd<T>(y.y) | drop_odd<T>(y.z) | drop_odd<T>(y.w);
+                                if (none || found) *p = y;
+                                odd |= found;
+                            }
+                            if (odd) S.odd_[it & 3] = 1;
+                            fence_proxy_async_shared();
+                        }
+                    }
+                    ok = __all_sync(0xffffffffu, ok && await_phase(S, &S.bs[x], ns & 1u, deadline, a.err));
+                    if (!ok) break;
+                    tc_fence_after();
+                    // (every thread has left the item before the last one: its flag serves the next but one)
+                    if (j == 0 && x == 0 && row == 0) S.odd_[(it + 2) & 3] = 0;
+                    if (!warp_used) {  // (rows of nobody: whatever their P is)
+                        tc_fence_before();
+                        mbar_arrive(&S.bp[x][0]);
+                        mbar_arrive(&S.bp[x][1]);
+                        continue;
+                    }
+                    float2 r[kTcKeys / 2];
+                    uint32_t *ri = reinterpret_cast<uint32_t *>(r);
+                    float *rf = reinterpret_cast<float *>(r);
+#pragma unroll
+                    for (int c0 = 0; c0 < kTcKeys; c0 += 32) tc_ld32_nowait(ts + (uint32_t)c0, ri + c0);
+#pragma unroll
+                    for (int c0 = 0; c0 < kTcKeys; c0 += 32) tc_wait_ld32(ri + c0);
+                    if (!full) {  // this row sees keys c with clo < c <= chi
+                        const int chi = pos < j0 ? -1 : min(pos - j0, kTcKeys);
+                        const int clo = a.window == 0 ? -1 : (int)max(-1ll, min((long long)kTcKeys, (long long)pos - a.window - j0));
+#pragma unroll
+                        for (int c = 0; c < kTcKeys; ++c) ri[c] = c <= chi && c > clo ? ri[c] : 0xff800000u;  // -inf
+                    }
+                    // the tile's max of the row in eight independent chains of three-input maxima
+                    float mp[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) mp[i] = rf[i];
+#pragma unroll
+                    for (int c = 8; c < kTcKeys; c += 16)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            mp[i] = c + 8 + i < kTcKeys ? max3(mp[i], rf[c + i], rf[c + 8 + i]) : fmaxf(mp[i], rf[c + i]);
+                    const float mr = max3(max3(mp[0], mp[1], mp[2]), max3(mp[3], mp[4], mp[5]), fmaxf(mp[6], mp[7]));
+                    float fac = 1.f;
+                    if (mr != -INFINITY && mr * sc2 > m2 + kLazy) {
+                        const float mn = mr * sc2;
+                        fac = ex2(m2 - mn);  // 0 while the row had no key yet (O and l are 0 then)
+                        l *= fac;
+                        m2 = mn;
+                    }
+                    if (j > 0 && __any_sync(0xffffffffu, fac != 1.f)) {
+                        // the commit that published S of this tile covers the row tile's
+                        // previous P V, and this tile's waits for the arrivals below: O is idle
+#pragma unroll 1
+                        for (int c0 = 0; c0 < DH; c0 += 16) {
+                            float o[16];
+                            tc_ld16(to + (uint32_t)c0, o);
+                            uint32_t ob[16];
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) ob[i] = __float_as_uint(o[i] * fac);
+                            tc_st16_nowait(to + (uint32_t)c0, ob);
+                        }
+                    }
+                    // P over the first 64 columns of S (S is in registers now)
+                    const float neg = m2 == -INFINITY ? 0.f : -m2;
+                    const float2 neg2 = make_float2(neg, neg), scale2 = make_float2(sc2, sc2);
+                    float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+                    for (int c0 = 0; c0 < kTcKeys; c0 += 32) {
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const float2 d = fma2(r[c0 / 2 + i], scale2, neg2);
+                            const float2 p = make_float2(ex2(d.x), ex2(d.y));
+                            ls[i & 1] = add2(ls[i & 1], p);
+                            pk[i] = pack2<T>(p.x, p.y);
+                        }
+                        tc_st16_nowait(ts + (uint32_t)(c0 / 2), pk);
+                        if (c0 + 32 == C_FIRST || c0 + 32 == kTcKeys) {
+                            tc_wait_st();
+                            tc_fence_before();
+                            mbar_arrive(&S.bp[x][c0 + 32 == kTcKeys]);
+                        }
+                    }
+                    const float2 s2 = add2(ls[0], ls[1]);
+                    l += s2.x + s2.y;
+                }
+                // the row's result or partial, once the last P V is done
+                if (ok) ok = __all_sync(0xffffffffu, await_phase(S, &S.bo[x], no++ & 1u, deadline, a.err));
+                if (ok && warp_used) {
+                    tc_fence_after();
+                    const bool odd = S.odd_[it & 3] != 0, result = whole && ends;
+                    const float inv = inverse(l);
+                    const long long slot = (long long)(2 * cta + (whole ? 1 : 0)) * a.slot_rows + x * tx * a.group + row;
+                    const uint64_t keep = policy_evict_last();
+#pragma unroll 1
+                    for (int c0 = 0; c0 < DH; c0 += 32) {
+                        float v[32];
+                        tc_ld32(to + (uint32_t)c0, v);
+                        if (odd && mine) {  // what is not finite reaches those who see it
+                            for (int j = 0; j < count * kTcKeys; ++j) {
+                                const int p = (w.kt0 + w.tile) * kTcKeys + j, p0 = p & ~(kTcKeys - 1);
+                                if (p0 + kTcKeys - 1 <= first_pos && (a.window == 0 || p0 > (long long)last_pos - a.window)) continue;
+                                if (p > pos || p < w.k.lo || (a.window > 0 && p <= (long long)pos - a.window)) continue;
+                                const int page = a.kv.table[(long long)w.b * a.kv.max_pages + (p >> a.kv.ps_log2)];
+                                if (page < 0 || page >= a.kv.n_pages) continue;
+                                const T *src = static_cast<const T *>(a.kv.v) + page * a.kv.page_stride +
+                                               ((((long long)w.h << a.kv.ps_log2) + (p & ((1 << a.kv.ps_log2) - 1))) * DH) + c0;
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) {
+                                    const float f = (float)src[i];
+                                    if (!(fabsf(f) < INFINITY)) v[i] += f;
+                                }
+                            }
+                        }
+                        if (!mine) {
+                        } else if (result) {
+                            uint32_t h[16];
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) h[i] = pack2<T>(v[2 * i] * inv, v[2 * i + 1] * inv);
+                            uint4 *dst = reinterpret_cast<uint4 *>(static_cast<T *>(a.out) + q_row * a.ld_out + (long long)head * DH + c0);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) dst[i] = make_uint4(h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]);
+                        } else {
+                            float *dst = a.part_o + slot * DH + c0;
+#pragma unroll
+                            for (int i = 0; i < 32; i += 4)
+                                st_hint(reinterpret_cast<float4 *>(dst + i), make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]), keep);
+                        }
+                        __syncwarp();
+                    }
+                    if (mine) {
+                        if (!result)
+                            a.part_ml[slot] = make_float2(m2, l);
+                        else if (a.lse)
+                            a.lse[q_row * a.n_q + head] = m2 * 0.69314718055994530942f + logf(l);
+                    }
+                    tc_fence_before();
+                }
+            }
+            left -= count;
+            at_tile += count;
+            whole = true;
+            if (left > 0) {  // on to the next item
+                w.tile = w.tiles - 1;
+                chunk_advance(a, cum, w);
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        if (lane == 0 && S.issued_) {  // the products may still run after an error: wait (bounded)
+            const uint64_t dl = global_timer_ns() + 1000000000ull;
+            while (!mbar_try_wait(&S.bdone, 0) && global_timer_ns() < dl) {
+            }
+        }
+        __syncwarp();
+        tc_fence_after();
+        tc_dealloc(tmem, C_TMEM_COLS);
+    }
+}
+
+template <typename T, int DH>
+lf_status launch_chunk_tc(const ChunkArgs &a, int dtype, cudaStream_t st) {
+    constexpr int smem = CtSmem<DH>::BYTES;
+    if (!set_smem_once<paged_chunk_tc_kernel<T, DH>>(smem)) return LF_ERR_CUDA;
+    CUtensorMap mk, mv;
+    if (!cache_map(&mk, a.kv.k, a.kv, dtype) || !cache_map(&mv, a.kv.v, a.kv, dtype)) return LF_ERR_CUDA;
+    return launch_pdl(paged_chunk_tc_kernel<T, DH>, a.grid, C_THREADS, smem, st, mk, mv, a) ? LF_OK : LF_ERR_CUDA;
+}
+
+}  // namespace
+
+lf_status paged_chunk_tc(const ChunkArgs &a, int dtype, cudaStream_t st) {
+    if (dtype == LF_F16)
+        return a.kv.head_dim == 64 ? launch_chunk_tc<__half, 64>(a, dtype, st) : launch_chunk_tc<__half, 128>(a, dtype, st);
+    return a.kv.head_dim == 64 ? launch_chunk_tc<__nv_bfloat16, 64>(a, dtype, st)
+                               : launch_chunk_tc<__nv_bfloat16, 128>(a, dtype, st);
+}
+
+}  // namespace lf
