@@ -20,6 +20,7 @@
 #include <cooperative_groups.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "lf_paged.h"
 #include "lf_ptx.cuh"
@@ -30,6 +31,8 @@ namespace lf {
 namespace {
 
 constexpr int LP_THREADS = 256, LP_WARPS = LP_THREADS / 32, LP_TOP = 32, LP_LIST = 512, LP_PARTS = 8;
+constexpr int LP_U = 4, LP_STAGES = 3;  // 16-byte pieces of a thread's batch, batches on their way
+constexpr int LP_RING = LP_STAGES * LP_U * LP_THREADS * 16;
 constexpr int LP_MAX_VOCAB = 1 << 18;
 constexpr float kLog2E = 1.4426950408889634f, kLn2 = 0.69314718055994530942f;
 
@@ -48,12 +51,6 @@ __device__ __forceinline__ float lp_ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-__device__ __forceinline__ float lp_max_nan(float a, float b) {
-    float y;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
-    return y;
-}
-
 // A running maximum with the sums below it, in units of log2: s = sum 2^d, e = sum d 2^d, d = (z - m) c.
 struct Sums {
     float m, s, e;
@@ -92,7 +89,7 @@ struct LpPart {
 };
 
 struct LpShared {
-    LpPart part;
+    LpPart part, all[LP_PARTS];  // all: of the CTAs of the row, in its first
     Sums warp_sums[LP_WARPS];
     int warp_count[LP_WARPS][3];
     float best[LP_WARPS][LP_TOP];  // each warp's maxima in descending order
@@ -119,9 +116,16 @@ __device__ __forceinline__ void unpack(const uint4 &q, float *f) {
     if constexpr (sizeof(T) == 4) {
         f[0] = __uint_as_float(q.x), f[1] = __uint_as_float(q.y), f[2] = __uint_as_float(q.z), f[3] = __uint_as_float(q.w);
     } else {
-        const T *t = reinterpret_cast<const T *>(&q);
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = (float)t[i];
+        for (int i = 0; i < 4; ++i) {
+            float2 y;
+            if constexpr (std::is_same<T, __half>::value)
+                y = __half22float2(*reinterpret_cast<const __half2 *>(w + i));
+            else  // (a bf16 is an fp32's upper half)
+                y = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+            f[2 * i] = y.x, f[2 * i + 1] = y.y;
+        }
     }
 }
 
@@ -150,32 +154,193 @@ struct Share {
     __device__ int index(int piece) const { return head + piece * Vec<T>::N; }
 };
 
+// The next value of the type above z, for which y > z says y >= it; a NaN (never
+// reached) above +inf and for a NaN.
+__device__ __forceinline__ float next_above(float z) {
+    if (!(z < INFINITY)) return NAN;
+    const int i = __float_as_int(z + 0.f);  // (no -0)
+    return i == 0x80000000 || i == 0 ? __int_as_float(1) : __int_as_float(i + (i > 0 ? 1 : -1));
+}
+template <typename T>
+__device__ __forceinline__ T next_above16(T z) {  // the same for 16 bits
+    uint16_t i = *reinterpret_cast<const uint16_t *>(&z);
+    if (!((float)z < INFINITY))
+        i = 0x7fff;
+    else if ((i & 0x7fff) == 0)
+        i = 1;
+    else
+        i += i & 0x8000 ? -1 : 1;
+    return *reinterpret_cast<const T *>(&i);
+}
+
+// Two values to an instruction.
+__device__ __forceinline__ float2 lp_fma2(float2 x, float2 y, float2 z) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(r)
+        : "l"(*reinterpret_cast<const uint64_t *>(&x)), "l"(*reinterpret_cast<const uint64_t *>(&y)),
+          "l"(*reinterpret_cast<const uint64_t *>(&z)));
+    return *reinterpret_cast<float2 *>(&r);
+}
+__device__ __forceinline__ float2 lp_add2(float2 x, float2 y) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(r)
+        : "l"(*reinterpret_cast<const uint64_t *>(&x)), "l"(*reinterpret_cast<const uint64_t *>(&y)));
+    return *reinterpret_cast<float2 *>(&r);
+}
+__device__ __forceinline__ float2 lp_mul2(float2 x, float2 y) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;"
+        : "=l"(r)
+        : "l"(*reinterpret_cast<const uint64_t *>(&x)), "l"(*reinterpret_cast<const uint64_t *>(&y)));
+    return *reinterpret_cast<float2 *>(&r);
+}
+
+// What a token's logit is compared with: pieces before its own count equal logits too.
+template <typename T>
+struct Before {
+    float z, above;
+    uint32_t z2, above2;  // both halves, 16-bit types
+    int token, piece;     // its piece (below all, above all: in the single logits)
+    int own;              // its index from the first piece on
+    __device__ Before(float zt, int tok, const Share<T> &sh) {
+        z = tok < 0 ? NAN : zt;
+        above = next_above(z);
+        token = tok;
+        own = tok - sh.head;
+        piece = tok < sh.head ? -1 : tok >= sh.tail_at ? INT32_MAX : (tok - sh.head) / Vec<T>::N;
+        z2 = above2 = 0;
+        if constexpr (sizeof(T) == 2) {
+            const T t = (T)z, u = next_above16<T>(t);
+            z2 = *reinterpret_cast<const uint16_t *>(&t) * 0x10001u;
+            above2 = *reinterpret_cast<const uint16_t *>(&u) * 0x10001u;
+        }
+    }
+};
+
 // One thread's walk over its pieces.
 template <typename T>
 struct Walk {
-    Sums t;
+    static constexpr int N = Vec<T>::N;
+    using T2 = std::conditional_t<std::is_same<T, __half>::value, __half2, __nv_bfloat162>;
+    Sums t;       // (below a maximum that follows `best` at a distance of at most kLag)
+    float best;
     int before, bad, infs;
-    template <int N>
-    __device__ __forceinline__ void add(const float *f, const int *at, float c, float zt, int token) {
-        float lm = f[0];
-#pragma unroll
-        for (int i = 1; i < N; ++i) lm = lp_max_nan(lm, f[i]);
+
+    // The maximum that the sums are taken below moves when a larger one is over 2^3 of it: sums stay as exact, and
+    // few threads ever move.
+    static constexpr float kLag = 3.f;
+    template <int U>
+    __device__ __forceinline__ void add(const uint4 *q, const int *v, float c, const Before<T> &b) {
+        float lm = largest<U>(q);
         bad |= lm != lm;
-        if (lm > t.m) t.move(lm, c);
-        if (t.m > -INFINITY && t.m < INFINITY) {
+        best = fmaxf(best, lm);
+        if ((lm - t.m) * c > kLag) t.move(lm, c);
+        const Sums was = t;
+        sums<U, false>(q, c);
+        if (!(fabsf(t.e) < INFINITY)) {  // a masked logit (0 times an infinite d is none), or one that is not finite
+            t = was;
+            uint4 again[U];  // (unpacked anew: kept values would cost the common way its registers)
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const float d = fmaxf((f[i] - t.m) * c, -1e30f), p = lp_ex2(d);  // (0 times an infinite d is none)
-                t.s += p;
-                t.e = fmaf(d, p, t.e);
+            for (int u = 0; u < U; ++u) {
+                again[u] = q[u];
+                asm volatile("" : "+r"(again[u].x), "+r"(again[u].y), "+r"(again[u].z), "+r"(again[u].w));
+            }
+            if (fabsf(t.m) < INFINITY) sums<U, true>(again, c);  // (no sums without a finite maximum)
+            if (lm == INFINITY) {
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    float f[N];
+                    unpack<T>(again[u], f);
+#pragma unroll
+                    for (int i = 0; i < N; ++i) infs += f[i] == INFINITY;
+                }
             }
         }
-        if (lm == INFINITY) {
+        if constexpr (sizeof(T) == 4) {
 #pragma unroll
-            for (int i = 0; i < N; ++i) infs += f[i] == INFINITY;
+            for (int u = 0; u < U; ++u) {
+                float f[N];
+                unpack<T>(q[u], f);
+                const float to = v[u] < b.piece ? b.z : b.above;
+#pragma unroll
+                for (int i = 0; i < N; ++i) before += f[i] >= to;
+            }
+        } else {
+            uint32_t none = 0;
+            T2 n = *reinterpret_cast<T2 *>(&none);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const uint32_t to = v[u] < b.piece ? b.z2 : b.above2, *w = reinterpret_cast<const uint32_t *>(&q[u]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    n = __hadd2(n, __hge2(*reinterpret_cast<const T2 *>(w + i), *reinterpret_cast<const T2 *>(&to)));
+            }
+            before += (int)((float)n.x + (float)n.y);  // (at most 16 each: exact)
         }
 #pragma unroll
-        for (int i = 0; i < N; ++i) before += precedes(f[i], at[i], zt, token);
+        for (int u = 0; u < U; ++u)
+            if (v[u] == b.piece) {  // equal logits before the token in its own piece
+                uint4 own = q[u];
+                asm volatile("" : "+r"(own.x), "+r"(own.y), "+r"(own.z), "+r"(own.w));
+                float f[N];
+                unpack<T>(own, f);
+#pragma unroll
+                for (int i = 0; i < N; ++i) before += v[u] * N + i < b.own && f[i] == b.z;
+            }
+    }
+    // The largest of the pieces' values; a NaN if there is one.
+    template <int U>
+    __device__ __forceinline__ float largest(const uint4 *q) {
+        const uint32_t *w = reinterpret_cast<const uint32_t *>(q);
+        if constexpr (sizeof(T) == 4) {
+            float m = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < 4 * U; i += 2)
+                asm("max.NaN.f32 %0, %0, %1, %2;" : "+f"(m) : "f"(__uint_as_float(w[i])), "f"(__uint_as_float(w[i + 1])));
+            return m;
+        } else {
+            T2 m = *reinterpret_cast<const T2 *>(w);
+#pragma unroll
+            for (int i = 1; i < 4 * U; ++i) m = __hmax2_nan(m, *reinterpret_cast<const T2 *>(w + i));
+            float y;
+            asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"((float)m.x), "f"((float)m.y));
+            return y;
+        }
+    }
+    // Adds the pieces' terms below t.m.  CLAMP: a term of an infinite distance adds nothing.
+    template <int U, bool CLAMP>
+    __device__ __forceinline__ void sums(const uint4 *q, float c) {
+        const float2 m2 = make_float2(-t.m, -t.m), c2 = make_float2(c, c);
+        float2 s = make_float2(t.s, 0.f), e = make_float2(t.e, 0.f);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            float2 f[N / 2];
+            unpack<T>(q[u], reinterpret_cast<float *>(f));
+#pragma unroll
+            for (int i = 0; i < N / 2; ++i) {
+                float2 d = lp_mul2(lp_add2(f[i], m2), c2);
+                if (CLAMP) d = make_float2(fmaxf(d.x, -1e30f), fmaxf(d.y, -1e30f));
+                const float2 p = make_float2(lp_ex2(d.x), lp_ex2(d.y));
+                s = lp_add2(s, p);
+                e = lp_fma2(d, p, e);
+            }
+        }
+        t.s = s.x + s.y;
+        t.e = e.x + e.y;
+    }
+    __device__ __forceinline__ void add_one(float f, int at, float c, const Before<T> &b) {
+        best = fmaxf(best, f);
+        bad |= f != f;
+        if ((f - t.m) * c > kLag) t.move(f, c);
+        infs += f == INFINITY;
+        if (fabsf(t.m) < INFINITY) {
+            const float d = fmaxf((f - t.m) * c, -1e30f), p = lp_ex2(d);
+            t.s += p;
+            t.e = fmaf(d, p, t.e);
+        }
+        before += precedes(f, at, b.z, b.token);
     }
 };
 
@@ -242,70 +407,83 @@ __device__ __forceinline__ float merge_desc(float a, float b_reversed, int lane)
 }
 
 template <typename T>
-__global__ void __launch_bounds__(LP_THREADS) token_logprobs_kernel(const LpArgs a) {
+__global__ void __launch_bounds__(LP_THREADS, 4) token_logprobs_kernel(const LpArgs a) {
     __shared__ LpShared S;
-    constexpr int N = Vec<T>::N, U = 4;  // pieces in flight
+    constexpr int N = Vec<T>::N, U = LP_U;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const long long r = blockIdx.x / (unsigned)a.parts;
     const int part = (int)(blockIdx.x - r * a.parts);
+    cg::cluster_group cl = cg::this_cluster();
     pdl_wait();
     pdl_trigger();
+    if (a.parts > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;");  // (every CTA of the row has begun: below)
     const Share<T> sh(a, r, part);
     const float temp = a.temperature ? a.temperature[r] : 1.f;
     const int token = a.token ? a.token[r] : -1;
     const bool asked = token >= 0 && token < a.vocab;
-    const float zt = asked ? (float)sh.row[token] : INFINITY;  // (nothing comes before an infinity that is not there)
-    const int tok = asked ? token : -1;
+    const float zt = asked ? (float)sh.row[token] : NAN;
     const bool warm = temp >= 1e-30f && temp <= 1e30f;
     const float c = warm ? kLog2E / temp : 1.f;
+    const Before<T> b(zt, asked ? token : -1, sh);
 
     Walk<T> w;
     w.t = Sums{-INFINITY, 0.f, 0.f};
+    w.best = -INFINITY;
     w.before = w.bad = w.infs = 0;
-    for (int v = sh.v0 + tid; v < sh.v1; v += U * LP_THREADS) {
+    // Each thread copies its own pieces, a batch of U at a time, into its own places of a ring and reads them back:
+    // enough on their way for HBM without holding registers, and no barrier.
+    const uint4 *body = reinterpret_cast<const uint4 *>(sh.body);
+    extern __shared__ __align__(16) uint4 ring[];  // [LP_STAGES][U][LP_THREADS]
+    const int pieces = sh.v1 - sh.v0, mine = pieces <= tid ? 0 : (pieces - tid + LP_THREADS - 1) / LP_THREADS;
+    auto place = [&](int i) { return ring + ((i / U) % LP_STAGES * U + i % U) * LP_THREADS + tid; };
+    auto fetch = [&](int i0) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (i0 + u < mine) cp_async16(place(i0 + u), body + sh.v0 + tid + (i0 + u) * LP_THREADS);
+        cp_async_commit();
+    };
+#pragma unroll
+    for (int k = 0; k < LP_STAGES - 1; ++k) fetch(k * U);
+    for (int i = 0; i < mine; i += U) {
+        fetch(i + (LP_STAGES - 1) * U);
+        asm volatile("cp.async.wait_group %0;" ::"n"(LP_STAGES - 1) : "memory");
         uint4 q[U];
+        int at[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (v + u * LP_THREADS < sh.v1) q[u] = reinterpret_cast<const uint4 *>(sh.body)[v + u * LP_THREADS];
+        for (int u = 0; u < U; ++u) at[u] = sh.v0 + tid + (i + u) * LP_THREADS, q[u] = *place(i + u);
+        if (i + U <= mine) {
+            w.template add<U>(q, at, c, b);
+        } else {
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (v + u * LP_THREADS < sh.v1) {
-                float f[N];
-                int at[N];
-                unpack<T>(q[u], f);
-#pragma unroll
-                for (int i = 0; i < N; ++i) at[i] = sh.index(v + u * LP_THREADS) + i;
-                w.template add<N>(f, at, c, zt, tok);
-            }
+            for (int u = 0; u < U - 1; ++u)
+                if (i + u < mine) w.template add<1>(q + u, at + u, c, b);
+        }
     }
-    for (int i = tid; i < sh.extras; i += LP_THREADS) {
-        const int at = sh.extra(i);
-        const float f = (float)sh.row[at];
-        w.template add<1>(&f, &at, c, zt, tok);
-    }
-    // the CTA's sums
-    const float mine = w.t.m;
+    if (tid < sh.extras) w.add_one((float)sh.row[sh.extra(tid)], sh.extra(tid), c, b);
+    // the CTA's sums, below its maximum
+    float m = w.best;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const int n_bad = __reduce_or_sync(0xffffffffu, w.bad), n_inf = __reduce_add_sync(0xffffffffu, w.infs),
+              n_before = __reduce_add_sync(0xffffffffu, w.before);
+    w.t.move(m, c);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
-        Sums y;
-        y.m = __shfl_xor_sync(0xffffffffu, w.t.m, o);
-        y.s = __shfl_xor_sync(0xffffffffu, w.t.s, o);
-        y.e = __shfl_xor_sync(0xffffffffu, w.t.e, o);
-        w.t.join(y, c);
+        w.t.s += __shfl_xor_sync(0xffffffffu, w.t.s, o);
+        w.t.e += __shfl_xor_sync(0xffffffffu, w.t.e, o);
     }
-    w.before = __reduce_add_sync(0xffffffffu, w.before);
-    w.bad = __reduce_or_sync(0xffffffffu, w.bad);
-    w.infs = __reduce_add_sync(0xffffffffu, w.infs);
     if (lane == 0) {
         S.warp_sums[warp] = w.t;
-        S.warp_count[warp][0] = w.before, S.warp_count[warp][1] = w.bad, S.warp_count[warp][2] = w.infs;
+        S.warp_count[warp][0] = n_before, S.warp_count[warp][1] = n_bad, S.warp_count[warp][2] = n_inf;
     }
-    if (a.top > 0) S.best[warp][lane] = sort_desc(mine, lane);
+    float x = 0.f;
+    if (a.top > 0) S.best[warp][lane] = x = sort_desc(w.best, lane);
     if (tid == 0) S.n_list = S.n_hold = 0;
     __syncthreads();
     if (tid == 0) {
         Sums t = S.warp_sums[0];
         int before = S.warp_count[0][0], bad = S.warp_count[0][1], infs = S.warp_count[0][2];
+#pragma unroll
         for (int k = 1; k < LP_WARPS; ++k) {
             t.join(S.warp_sums[k], c);
             before += S.warp_count[k][0], bad |= S.warp_count[k][1], infs += S.warp_count[k][2];
@@ -314,15 +492,18 @@ __global__ void __launch_bounds__(LP_THREADS) token_logprobs_kernel(const LpArgs
         S.part.before = before, S.part.bad = bad, S.part.infs = infs, S.part.n = 0;
     }
     if (a.top > 0) {
-        if (warp == LP_WARPS - 1) {  // the top_n-th largest of the threads' maxima
-            float x = S.best[0][lane];
+        // the top_n-th largest of the threads' maxima: the warps' lists in pairs (the last warps, beside the sums)
 #pragma unroll
-            for (int k = 1; k < LP_WARPS; ++k) x = merge_desc(x, S.best[k][31 - lane], lane);
-            if (lane == a.top - 1) S.bound = x;
+        for (int half = LP_WARPS / 2; half > 0; half /= 2) {
+            if (warp >= LP_WARPS - half) {
+                x = merge_desc(x, S.best[warp - half][31 - lane], lane);
+                if (half > 1) S.best[warp][lane] = x;
+                if (half == 1 && lane == a.top - 1) S.bound = x;
+            }
+            __syncthreads();
         }
-        __syncthreads();
         const float bound = S.bound;
-        if (mine >= bound && mine > -INFINITY) S.hold[atomicAdd(&S.n_hold, 1)] = tid;
+        if (w.best >= bound && w.best > -INFINITY) S.hold[atomicAdd(&S.n_hold, 1)] = tid;
         __syncthreads();
         // every piece of the threads that hold candidates, spread over the CTA
         const int hold = S.n_hold, steps = (sh.v1 - sh.v0 + LP_THREADS - 1) / LP_THREADS;
@@ -332,46 +513,60 @@ __global__ void __launch_bounds__(LP_THREADS) token_logprobs_kernel(const LpArgs
                 if (i < LP_LIST) S.list_z[i] = z, S.list_at[i] = at;
             }
         };
-        for (int x = tid; x < hold * steps; x += LP_THREADS) {
-            const int v = sh.v0 + x / hold * LP_THREADS + S.hold[x % hold];
-            if (v >= sh.v1) continue;
+        for (int y = tid; y < hold * steps; y += LP_THREADS) {
+            const int p = sh.v0 + y / hold * LP_THREADS + S.hold[y % hold];
+            if (p >= sh.v1) continue;
             float f[N];
-            unpack<T>(reinterpret_cast<const uint4 *>(sh.body)[v], f);
+            unpack<T>(body[p], f);
 #pragma unroll
-            for (int i = 0; i < N; ++i) keep(f[i], sh.index(v) + i);
+            for (int i = 0; i < N; ++i) keep(f[i], sh.index(p) + i);
         }
-        for (int i = tid; i < sh.extras; i += LP_THREADS) keep((float)sh.row[sh.extra(i)], sh.extra(i));
+        if (tid < sh.extras) keep((float)sh.row[sh.extra(tid)], sh.extra(tid));
         __syncthreads();
         const int n = S.n_list;
         if (n > LP_LIST) {
             pick_slowly<T>(a, sh, S);
         } else {
-            for (int x = tid; x < n; x += LP_THREADS) {
-                const float z = S.list_z[x];
-                const int at = S.list_at[x];
+            for (int y = tid; y < n; y += LP_THREADS) {
+                const float z = S.list_z[y];
+                const int at = S.list_at[y];
                 int ahead = 0;
-                for (int y = 0; y < n; ++y) ahead += precedes(S.list_z[y], S.list_at[y], z, at);
+                for (int o = 0; o < n; ++o) ahead += precedes(S.list_z[o], S.list_at[o], z, at);
                 if (ahead < a.top) S.part.top[ahead] = z, S.part.at[ahead] = at;
             }
             if (tid == 0) S.part.n = min(n, a.top);
         }
     }
-    // the row, by its first CTA
-    cg::cluster_group cl = cg::this_cluster();
-    if (a.parts > 1)
+    __syncthreads();
+    // every CTA's part into the shared memory of the row's first
+    if (a.parts > 1) {
+        asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+        const uint32_t *src = reinterpret_cast<const uint32_t *>(&S.part);
+        uint32_t *dst = reinterpret_cast<uint32_t *>(cl.map_shared_rank(&S.all[part], 0));
+        if (tid < (int)(sizeof(LpPart) / 4)) dst[tid] = src[tid];
         cl.sync();
-    else
-        __syncthreads();
-    if (part == 0) {
-        auto of = [&](int k) { return a.parts > 1 ? cl.map_shared_rank(&S.part, k) : &S.part; };
-        if (tid == 0) {
-            Sums t = S.part.sums;
-            int before = S.part.before, bad = S.part.bad, infs = S.part.infs;
-            for (int k = 1; k < a.parts; ++k) {
-                const LpPart *p = of(k);
-                t.join(p->sums, c);
-                before += p->before, bad |= p->bad, infs += p->infs;
-            }
+        if (part > 0) return;
+    }
+    const LpPart *all = a.parts > 1 ? S.all : &S.part;
+    if (warp == 0) {
+        Sums t = {-INFINITY, 0.f, 0.f};
+        int before = 0, bad = 0, infs = 0;
+        if (lane < a.parts) {
+            t = all[lane].sums;
+            before = all[lane].before, bad = all[lane].bad, infs = all[lane].infs;
+        }
+#pragma unroll
+        for (int o = LP_PARTS / 2; o > 0; o >>= 1) {
+            Sums y;
+            y.m = __shfl_xor_sync(0xffffffffu, t.m, o);
+            y.s = __shfl_xor_sync(0xffffffffu, t.s, o);
+            y.e = __shfl_xor_sync(0xffffffffu, t.e, o);
+            t.join(y, c);
+            before += __shfl_xor_sync(0xffffffffu, before, o);
+            bad |= __shfl_xor_sync(0xffffffffu, bad, o);
+            infs += __shfl_xor_sync(0xffffffffu, infs, o);
+        }
+        if (lane == 0) {
             const bool ok = warm && !bad && t.m > -INFINITY;
             const bool inf = t.m == INFINITY;
             const float norm = logf(inf ? (float)infs : t.s);
@@ -381,40 +576,33 @@ __global__ void __launch_bounds__(LP_THREADS) token_logprobs_kernel(const LpArgs
             if (a.rank) a.rank[r] = !ok || !asked ? -1 : before;
             S.row_m = t.m, S.row_norm = norm, S.row_ok = ok;
         }
-        __syncthreads();
-        if (a.top > 0 && (a.top_token || a.top_logprob)) {
-            // candidates of all parts, a thread to each place
-            int total = 0;
-            for (int k = 0; k < a.parts; ++k) total += of(k)->n;
-            const int k = tid / LP_TOP, i = tid % LP_TOP;
-            const float m = S.row_m, norm = S.row_norm;
-            auto put = [&](int place, int at, float lp) {
-                if (a.top_token) a.top_token[r * a.top + place] = at;
-                if (a.top_logprob) a.top_logprob[r * a.top + place] = lp;
-            };
-            if (!S.row_ok) {
-                if (tid < a.top) put(tid, -1, NAN);
-            } else {
-                if (k < a.parts && i < of(k)->n) {
-                    const float z = of(k)->top[i];
-                    const int at = of(k)->at[i];
-                    int ahead = i;
-                    for (int o = 0; o < a.parts; ++o)
-                        if (o != k) {
-                            const LpPart *p = of(o);
-                            const int n = p->n;
-                            int x = 0;
-                            while (x < n && precedes(p->top[x], p->at[x], z, at)) ++x;
-                            ahead += x;
-                        }
-                    if (ahead < a.top)
-                        put(ahead, at, m == INFINITY ? (z == INFINITY ? -norm : -INFINITY) : (z - m) / temp - norm);
-                }
-                if (tid < a.top && tid >= total) put(tid, -1, -INFINITY);
-            }
-        }
     }
-    if (a.parts > 1) cl.sync();  // nobody leaves while its part is read
+    if (a.top == 0) return;
+    __syncthreads();
+    // the most probable tokens of all parts, a thread to each place of each part's list
+    const int k = tid / LP_TOP, i = tid % LP_TOP;
+    const float norm = S.row_norm, row_m = S.row_m;
+    auto put = [&](int place, int at, float lp) {
+        if (a.top_token) a.top_token[r * a.top + place] = at;
+        if (a.top_logprob) a.top_logprob[r * a.top + place] = lp;
+    };
+    if (!S.row_ok) {
+        if (tid < a.top) put(tid, -1, NAN);
+        return;
+    }
+    int total = 0;
+    for (int o = 0; o < a.parts; ++o) total += all[o].n;
+    if (k < a.parts && i < all[k].n) {
+        const float z = all[k].top[i];
+        const int at = all[k].at[i];
+        int ahead = i;
+        for (int o = 0; o < a.parts; ++o)
+            if (o != k)
+                for (int y = 0; y < all[o].n; ++y) ahead += precedes(all[o].top[y], all[o].at[y], z, at);
+        if (ahead < a.top)
+            put(ahead, at, row_m == INFINITY ? (z == INFINITY ? -norm : -INFINITY) : (z - row_m) / temp - norm);
+    }
+    if (tid < a.top && tid >= total) put(tid, -1, -INFINITY);
 }
 
 // CTAs to a row: as many as leave each a few thousand logits, where the rows do not
@@ -427,8 +615,9 @@ int parts_of(int rows, int vocab, int n_sm) {
 
 template <typename T>
 bool launch_logprobs(const LpArgs &a, cudaStream_t st) {
-    return launch_pdl_cluster(token_logprobs_kernel<T>, (unsigned)a.parts, dim3((unsigned)a.rows * (unsigned)a.parts),
-                              LP_THREADS, 0, st, a);
+    return set_smem_once<token_logprobs_kernel<T>>(LP_RING) &&
+           launch_pdl_cluster(token_logprobs_kernel<T>, (unsigned)a.parts, dim3((unsigned)a.rows * (unsigned)a.parts),
+                              LP_THREADS, LP_RING, st, a);
 }
 
 }  // namespace

@@ -169,7 +169,8 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
             }
         }
     } else if (warp == 1) {
-        if (lane == 0) {
+        {  // (the whole warp walks the loop, one lane issues: what the instructions take stays in uniform registers)
+            const bool leader = elect_one();
             // e4m3 operands (type 0), fp32 accumulators, both K-major
             constexpr uint32_t kIdesc = idesc_f16(F8_BM, BN);
             int kbg = 0, lt = 0;
@@ -177,23 +178,29 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
             for (int t = blockIdx.x; ok && t < ntiles; t += gridDim.x, ++lt) {
                 const int b = lt & 1;
                 const uint32_t acc = tmem + (uint32_t)b * BN;
-                if (lt >= 2 && !f8_wait(S, &S.acc_empty[b], ((lt >> 1) - 1) & 1u, deadline, a.err)) break;
+                if (lt >= 2 && !__all_sync(0xffffffffu, f8_wait(S, &S.acc_empty[b], ((lt >> 1) - 1) & 1u, deadline, a.err))) break;
                 tc_fence_after();
                 for (int kb = 0; kb < nk; ++kb, ++kbg) {
                     const int s = kbg % ST;
-                    if (!f8_wait(S, &S.full[s], (kbg / ST) & 1u, deadline, a.err)) {
+                    if (!__all_sync(0xffffffffu, f8_wait(S, &S.full[s], (kbg / ST) & 1u, deadline, a.err))) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t at = smem_u32(tiles + s * L::STAGE), bt = at + L::A;
+                    if (leader) {
+                        const uint32_t at = smem_u32(tiles + s * L::STAGE), bt = at + L::A;
 #pragma unroll
-                    for (int kk = 0; kk < F8_BK / 32; ++kk)  // 32 values = 32 bytes along K per instruction
-                        tc_mma_f8(acc, smem_desc_sw128(at + 32 * kk), smem_desc_sw128(bt + 32 * kk), kIdesc, (kb | kk) != 0);
-                    tc_commit(&S.empty[s]);
+                        for (int kk = 0; kk < F8_BK / 32; ++kk)  // 32 values = 32 bytes along K per instruction
+                            tc_mma_f8(acc, smem_desc_sw128(at + 32 * kk), smem_desc_sw128(bt + 32 * kk), kIdesc, (kb | kk) != 0);
+                        tc_commit(&S.empty[s]);
+                    }
+                    __syncwarp();
                 }
-                tc_commit(&S.acc_full[b]);
-                S.n_acc_[b] = (lt >> 1) + 1;
+                if (leader) {
+                    tc_commit(&S.acc_full[b]);
+                    S.n_acc_[b] = (lt >> 1) + 1;
+                }
+                __syncwarp();
             }
         }
     } else {  // warp w reads TMEM lanes 32 * (w % 4) .. + 31

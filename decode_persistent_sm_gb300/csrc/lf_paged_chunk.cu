@@ -61,20 +61,20 @@ class ChunkWalker {
     }
 
     __device__ void run() {
-        const int total = chunk_plan(a, cum);
+        const int total = chunk_plan<KT>(a, cum);
         const Shares sh(total, gridDim.x);
         const int cta = blockIdx.x;
         if (tid == 0) a.joins[cta].parts = 0;
         if (cta >= min(total, (int)gridDim.x)) return;
         const int u0 = sh.begin(cta), u1 = sh.begin(cta + 1), n = u1 - u0;
-        ChunkWork work = chunk_place(a, cum, u0), load = work;
+        ChunkWork work = chunk_place<KT>(a, cum, u0), load = work;
         prepare(load);
         int loaded = 0;
         auto fetch_next = [&] {
             if (loaded < n) {
                 fetch(loaded % L::STAGES);
                 if (loaded + 1 < n) {
-                    chunk_advance(a, cum, load);
+                    chunk_advance<KT>(a, cum, load);
                     prepare(load);
                 }
             }
@@ -94,7 +94,7 @@ class ChunkWalker {
             if (i + 1 == n) {
                 if (tid == 0) a.joins[cta] = chunk_join(a, work, sh, cta, u1, work.tile + 1, whole);
             } else {
-                fresh = chunk_advance(a, cum, work);
+                fresh = chunk_advance<KT>(a, cum, work);
                 if (fresh) whole = true;
             }
         }
@@ -394,48 +394,73 @@ __global__ void __launch_bounds__(CK_THREADS, CK_CTAS_PER_SM) paged_chunk_kernel
     ChunkWalker<T, DH, WR>(a, ck_smem).run();
 }
 
-// The items that several CTAs share, one warp to a row: block (c, y) takes rows 4 y ..
-// of the item that CTA c began and did not end, its partials in the list's order.
+// The items that several CTAs share, half a warp to a row: block (c, y) takes rows
+// 16 y .. 16 y + 15 of the item that CTA c began and did not end, its partials in the
+// list's order, several in flight.
+constexpr int CJ_THREADS = 256, CJ_ROWS = CJ_THREADS / 16;
 template <typename T, int DH>
-__global__ void __launch_bounds__(CK_THREADS) paged_chunk_join(const ChunkArgs a) {
-    constexpr int V = DH / 32;  // values per lane
-    const int c = blockIdx.x, lane = threadIdx.x & 31;
+__global__ void __launch_bounds__(CJ_THREADS) paged_chunk_join(const ChunkArgs a) {
+    constexpr int V = DH / 16, U = 4;  // values per lane; partials in flight
+    const int c = blockIdx.x, lane = threadIdx.x & 15, row = blockIdx.y * CJ_ROWS + (threadIdx.x >> 4);
     pdl_wait();
     pdl_trigger();
     const ChunkArgs::Join j = a.joins[c];
-    for (int row = blockIdx.y * 4 + (threadIdx.x >> 5); j.parts > 0 && row < j.rows; row += gridDim.y * 4) {
-        // partial p of the item: the CTA that begins it leaves it second, those behind first
-        auto at = [&](int p) { return (long long)(p == 0 ? 2 * c + 1 : 2 * (c + p)) * a.slot_rows + row; };
-        float mx = -INFINITY;
-        for (int p = lane; p < j.parts; p += 32) mx = fmaxf(mx, a.part_ml[at(p)].x);
+    if (j.parts == 0 || row >= j.rows) return;
+    // partial p of the item: the CTA that begins it leaves it second, those behind first
+    auto at = [&](int p) { return (long long)(p == 0 ? 2 * c + 1 : 2 * (c + p)) * a.slot_rows + row; };
+    float acc[V], mx = -INFINITY, sum = 0.f;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        const float off = mx == -INFINITY ? 0.f : mx;
-        float acc[V], sum = 0.f;
+    for (int i = 0; i < V; ++i) acc[i] = 0.f;
+    for (int p0 = 0; p0 < j.parts; p0 += U) {
+        float2 y[U];
+        float v[U][V];
 #pragma unroll
-        for (int i = 0; i < V; ++i) acc[i] = 0.f;
-#pragma unroll 4
-        for (int p = 0; p < j.parts; ++p) {
-            const long long s = at(p);
-            const float2 y = a.part_ml[s];
-            const float f = ex2(y.x - off);
-            sum += f * y.y;
+        for (int u = 0; u < U; ++u) {
+            const long long s = at(min(p0 + u, j.parts - 1));
+            y[u] = a.part_ml[s];
+            const float *d = a.part_o + s * DH + lane * V;
 #pragma unroll
-            for (int i = 0; i < V; ++i) acc[i] += f * a.part_o[s * DH + lane * V + i];
+            for (int i = 0; i < V; i += V >= 4 ? 4 : V) {
+                if constexpr (V >= 4)
+                    *reinterpret_cast<float4 *>(v[u] + i) = *reinterpret_cast<const float4 *>(d + i);
+                else
+                    *reinterpret_cast<float2 *>(v[u] + i) = *reinterpret_cast<const float2 *>(d + i);
+            }
         }
-        const int tok = row / a.group, head = j.head * a.group + row - tok * a.group;
-        const long long q = j.row0 + tok;
-        const float inv = inverse(sum);
-        T *dst = static_cast<T *>(a.out) + q * a.ld_out + (long long)head * DH + lane * V;
-        if constexpr (V == 1) {
-            dst[0] = (T)(acc[0] * inv);
-        } else {
+        float mn = mx;
 #pragma unroll
-            for (int i = 0; i < V; i += 2)
-                *reinterpret_cast<uint32_t *>(dst + i) = pack2<T>(acc[i] * inv, acc[i + 1] * inv);
+        for (int u = 0; u < U; ++u) {
+            if (p0 + u >= j.parts) y[u] = make_float2(-INFINITY, 0.f);
+            mn = fmaxf(mn, y[u].x);
         }
-        if (a.lse && lane == 0) a.lse[q * a.n_q + head] = mx * 0.69314718055994530942f + logf(sum);
+        const float off = mn == -INFINITY ? 0.f : mn, f0 = ex2(mx - off);
+        mx = mn;
+        sum *= f0;
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[i] *= f0;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (p0 + u >= j.parts) break;
+            const float f = ex2(y[u].x - off);
+            sum += f * y[u].y;
+#pragma unroll
+            for (int i = 0; i < V; ++i) acc[i] += f * v[u][i];
+        }
     }
+    const int tok = row / a.group, head = j.head * a.group + row - tok * a.group;
+    const long long q = j.row0 + tok;
+    const float inv = inverse(sum);
+    uint32_t h[V / 2];
+#pragma unroll
+    for (int i = 0; i < V; i += 2) h[i / 2] = pack2<T>(acc[i] * inv, acc[i + 1] * inv);
+    uint32_t *dst = reinterpret_cast<uint32_t *>(static_cast<T *>(a.out) + q * a.ld_out + (long long)head * DH + lane * V);
+    if constexpr (V == 8)
+        *reinterpret_cast<uint4 *>(dst) = make_uint4(h[0], h[1], h[2], h[3]);
+    else if constexpr (V == 4)
+        *reinterpret_cast<uint2 *>(dst) = make_uint2(h[0], h[1]);
+    else
+        *dst = h[0];
+    if (a.lse && lane == 0) a.lse[q * a.n_q + head] = mx * 0.69314718055994530942f + logf(sum);
 }
 
 int sm_count() {
@@ -459,7 +484,6 @@ void shape(ChunkArgs &a, int n_sm) {
     const long long rows = ((long long)a.n_tokens * a.group + a.kv.n_seqs - 1) / a.kv.n_seqs;
     a.tc = rows > 64 && tc_fits(a.kv);
     a.slot_rows = a.tc ? kTcRows : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
-    a.keys = a.tc ? kTcKeys : tile_keys(a.kv.head_dim);
     a.toks = a.tc ? 2 * (128 / a.group) : a.slot_rows / a.group;  // (a 128-row tile holds whole tokens)
     a.grid = a.tc ? n_sm : n_sm * CK_CTAS_PER_SM;
 }
@@ -513,8 +537,8 @@ lf_status launch_chunk(const ChunkArgs &a, cudaStream_t st) {
     else
         ok = set_smem_once<paged_chunk_kernel<T, DH, 4>>(smem) &&
              launch_pdl(paged_chunk_kernel<T, DH, 4>, a.grid, CK_THREADS, smem, st, a);
-    return ok && launch_pdl(paged_chunk_join<T, DH>, dim3((unsigned)a.grid, (unsigned)((a.slot_rows + 15) / 16)),
-                            CK_THREADS, 0, st, a)
+    return ok && launch_pdl(paged_chunk_join<T, DH>, dim3((unsigned)a.grid, (unsigned)(a.slot_rows / CJ_ROWS)), CJ_THREADS,
+                            0, st, a)
                ? LF_OK
                : LF_ERR_CUDA;
 }
@@ -560,7 +584,8 @@ extern "C" lf_status lf_attn_paged_chunk(const lf_paged_kv *kv, const void *q_de
     if (!n_sm) return LF_ERR_CUDA;
     lf::shape(a, n_sm);
     // tiles are counted in 32 bits
-    if (((long long)n_tokens / a.toks + kv->n_seqs) * ((long long)max_len / a.keys + 2) * kv->n_kv_heads > INT_MAX)
+    const int kt = a.tc ? lf::kTcKeys : lf::tile_keys(kv->head_dim);
+    if (((long long)n_tokens / a.toks + kv->n_seqs) * ((long long)max_len / kt + 2) * kv->n_kv_heads > INT_MAX)
         return LF_ERR_UNSUPPORTED;
     if (workspace_bytes < lf::ck_bytes(a, n_sm)) return LF_ERR_INVALID_ARG;
     if (n_tokens == 0) return LF_OK;

@@ -2,8 +2,8 @@
 //
 // An item is (sequence, KV head, row tile): `toks` consecutive new tokens with all
 // query heads of the KV head, row = token * group + head of the group.  It reads
-// the keys that any of its tokens sees in tiles of `keys` positions, cut at
-// multiples of `keys` of the sequence's positions, so a tile lies in whole pages or
+// the keys that any of its tokens sees in tiles of KT positions, cut at
+// multiples of KT of the sequence's positions, so a tile lies in whole pages or
 // a page in whole tiles.  The tiles of all items, in the order sequence, head, row
 // tile, key, form one list that is cut into equal contiguous shares, one per CTA.
 // Everything is worked out on the device from starts and lens.
@@ -24,7 +24,7 @@ struct ChunkArgs {
     int n_tokens, max_len, window;  // window 0: none
     float scale_log2;
     bool tc;                    // the tensor cores' kernel
-    int keys, toks, slot_rows;  // rows of a partial in the workspace: at least toks * group
+    int toks, slot_rows;        // tokens of a row tile; rows of a partial in the workspace: at least toks * group
     int grid;                   // CTAs that share the list
     // A CTA works on at most two items that it does not see whole: one that an
     // earlier CTA began (partial 2 c), and one that it begins and does not
@@ -58,20 +58,26 @@ __device__ __forceinline__ Chunk chunk_of(const ChunkArgs &a, int b) {
     return k;
 }
 
-// sum_{i < n} floor((a i + b) / m) for a, b >= 0, m > 0, a n + b < 2^32, by the
-// Euclidean reduction of the lattice points under a line (each step swaps a and m).
-__host__ __device__ inline long long floor_sum(unsigned n, unsigned m, unsigned a, unsigned b) {
+// sum_{i < n} floor((a i + b) / M) for a, b >= 0, M a power of two, a n + b < 2^32, by
+// the Euclidean reduction of the lattice points under a line (each step swaps a and m).
+template <unsigned M>
+__host__ __device__ inline long long floor_sum(unsigned n, unsigned a, unsigned b) {
     long long sum = 0;
+    unsigned m = M;
+    bool power = true;  // (the first step divides by M: shifts)
     while (n) {
-        sum += (long long)n * (n - 1) / 2 * (a / m) + (long long)n * (b / m);
-        a %= m;
-        b %= m;
+        const unsigned qa = power ? a / M : a / m, qb = power ? b / M : b / m;
+        sum += (long long)n * (n - 1) / 2 * qa + (long long)n * qb;
+        a -= qa * m;
+        b -= qb * m;
+        if (a == 0) break;  // (what is left lies below one step)
         const unsigned y = a * n + b;
-        n = y / m;
-        b = y % m;
+        n = power ? y / M : y / m;
+        b = y - n * m;
         const unsigned t = m;
         m = a;
         a = t;
+        power = false;
     }
     return sum;
 }
@@ -89,25 +95,27 @@ __host__ __device__ inline Keys keys_of(int base, int c, int window, int toks, i
     return k;
 }
 // Key tiles of a row tile: at least one (a row tile that sees nothing writes zeros).
-__host__ __device__ inline int key_tiles(const Keys &k, int keys) {
-    return k.hi <= 0 ? 1 : (k.hi + keys - 1) / keys - k.lo / keys;
+template <int KT>
+__host__ __device__ inline int key_tiles(const Keys &k) {
+    return k.hi <= 0 ? 1 : (int)((unsigned)(k.hi + KT - 1) / KT - (unsigned)k.lo / KT);
 }
 // Key tiles of the first n row tiles of a chunk, n at most ceil(c / toks).
-__host__ __device__ inline long long tiles_before(int base, int c, int window, int toks, int keys, int n) {
+template <int KT>
+__host__ __device__ inline long long tiles_before(int base, int c, int window, int toks, int n) {
     if (n <= 0) return 0;
     const int full = c / toks < n ? c / toks : n;  // row tiles of `toks` tokens; one more is shorter
     // those that end before position 1 have one tile without keys
     int none = base < 0 ? -base / toks : 0;
     if (none > full) none = full;
-    long long sum = none + floor_sum((unsigned)(full - none), (unsigned)keys, (unsigned)toks,
-                                     full > none ? (unsigned)(base + (none + 1) * toks + keys - 1) : 0u);
-    if (n > full) sum += base + c <= 0 ? 1 : (base + c + keys - 1) / keys;
+    long long sum = none + floor_sum<KT>((unsigned)(full - none), (unsigned)toks,
+                                         full > none ? (unsigned)(base + (none + 1) * toks + KT - 1) : 0u);
+    if (n > full) sum += base + c <= 0 ? 1 : (unsigned)(base + c + KT - 1) / KT;
     if (window > 0) {  // less the tiles before each one's first key; none before token window - 1 - base
         const long long from = (long long)window - 1 - base;
         const long long z = from < 0 ? 0 : from / toks + 1;
         if (z < n) {
             const int f = (int)z;
-            sum -= floor_sum((unsigned)(n - f), (unsigned)keys, (unsigned)toks, (unsigned)(base + f * toks - window + 1));
+            sum -= floor_sum<KT>((unsigned)(n - f), (unsigned)toks, (unsigned)(base + f * toks - window + 1));
         }
     }
     return sum;
@@ -119,18 +127,20 @@ struct ChunkWork {
     Chunk ch;
     int tok, toks;           // first token of the row tile, tokens
     Keys k;
-    int kt0, tile, tiles;    // first key tile (key / keys); this tile, and how many the item has
+    int kt0, tile, tiles;    // first key tile (key / KT); this tile, and how many the item has
+    template <int KT>
     __device__ void set(const ChunkArgs &a) {
         tok = r * a.toks;
         toks = min(a.toks, ch.c - tok);
         k = keys_of(ch.base, ch.c, a.window, a.toks, tok);
-        kt0 = k.lo / a.keys;
-        tiles = key_tiles(k, a.keys);
+        kt0 = (unsigned)k.lo / KT;
+        tiles = key_tiles<KT>(k);
     }
 };
 
 // Fills cum[b] = key tiles per KV head of the sequences before b (cum[n_seqs]: of
 // all); a whole block calls it.  Returns the list's length.
+template <int KT>
 __device__ __forceinline__ int chunk_plan(const ChunkArgs &a, int *cum) {
     const int n = a.kv.n_seqs, lane = threadIdx.x & 31;
     int at = 0;
@@ -139,7 +149,7 @@ __device__ __forceinline__ int chunk_plan(const ChunkArgs &a, int *cum) {
         int t = 0;
         if (b < n) {
             const Chunk k = chunk_of(a, b);
-            t = (int)tiles_before(k.base, k.c, a.window, a.toks, a.keys, (k.c + a.toks - 1) / a.toks);
+            t = (int)tiles_before<KT>(k.base, k.c, a.window, a.toks, (k.c + a.toks - 1) / a.toks);
             if (k.bad && blockIdx.x == 0 && threadIdx.x < 32) atomicExch(a.err, 1u);
         }
         int inc = t;
@@ -157,6 +167,7 @@ __device__ __forceinline__ int chunk_plan(const ChunkArgs &a, int *cum) {
 }
 
 // The place of tile u; whole warps call it together.
+template <int KT>
 __device__ __forceinline__ ChunkWork chunk_place(const ChunkArgs &a, const int *cum, int u) {
     ChunkWork w;
     const int lane = threadIdx.x & 31;
@@ -179,18 +190,19 @@ __device__ __forceinline__ ChunkWork chunk_place(const ChunkArgs &a, const int *
     lo = 0, hi = w.row_tiles;
     while (hi - lo > 1) {
         const int step = (hi - lo + 31) / 32, x = lo + lane * step;
-        const bool in = x < hi && tiles_before(w.ch.base, w.ch.c, a.window, a.toks, a.keys, x) <= u;
+        const bool in = x < hi && tiles_before<KT>(w.ch.base, w.ch.c, a.window, a.toks, x) <= u;
         const int last = 31 - __clz(__ballot_sync(0xffffffffu, in));  // (lane 0 always is)
         lo += last * step;
         hi = min(hi, lo + step);
     }
     w.r = lo;
-    w.set(a);
-    w.tile = u - (int)tiles_before(w.ch.base, w.ch.c, a.window, a.toks, a.keys, lo);
+    w.set<KT>(a);
+    w.tile = u - (int)tiles_before<KT>(w.ch.base, w.ch.c, a.window, a.toks, lo);
     return w;
 }
 
 // The next tile of the list; true if it begins another item.
+template <int KT>
 __device__ __forceinline__ bool chunk_advance(const ChunkArgs &a, const int *cum, ChunkWork &w) {
     if (++w.tile < w.tiles) return false;
     w.tile = 0;
@@ -205,7 +217,7 @@ __device__ __forceinline__ bool chunk_advance(const ChunkArgs &a, const int *cum
             w.row_tiles = (w.ch.c + a.toks - 1) / a.toks;
         }
     }
-    w.set(a);
+    w.set<KT>(a);
     return true;
 }
 
@@ -226,7 +238,7 @@ __device__ __forceinline__ ChunkArgs::Join chunk_join(const ChunkArgs &a, const 
     return j;
 }
 
-// The list's kernel on the 5th-generation tensor cores (lf_paged_chunk_tc.cu): head_dim 64 and 128, keys = kTcKeys,
+// The list's kernel on the 5th-generation tensor cores (lf_paged_chunk_tc.cu): head_dim 64 and 128,
 // toks even, slot_rows = kTcRows.
 lf_status paged_chunk_tc(const ChunkArgs &a, int dtype, cudaStream_t st);
 

@@ -54,7 +54,7 @@ struct CtShared {
     uint32_t tmem;
     volatile int abort_;
     volatile int issued_;   // 1 once any product was issued (then bdone gets its commit)
-    volatile int odd_[4];   // an item's masked tiles hold values that are not finite (items in turn)
+    volatile int odd_[8];   // item it's masked tiles hold values that are not finite: odd_[it & 7] is it + 1
 };
 
 __device__ __forceinline__ bool await_phase(CtShared &S, uint64_t *bar, uint32_t parity, uint64_t deadline,
@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(C_THREADS, 1)
             mbar_init(&S.bp[b][0], 128);
             mbar_init(&S.bp[b][1], 128);
             mbar_init(&S.bo[b], 1);
-            S.odd_[b] = S.odd_[2 + b] = 0;
+            for (int i = 0; i < 4; ++i) S.odd_[4 * b + i] = 0;
         }
         mbar_init(&S.bk0, 1);
         mbar_init(&S.bdone, 1);
@@ -140,14 +140,14 @@ __global__ void __launch_bounds__(C_THREADS, 1)
     }
     pdl_wait();
     pdl_trigger();
-    const int total = chunk_plan(a, cum);
+    const int total = chunk_plan<kTcKeys>(a, cum);
     const Shares sh(total, gridDim.x);
     if (threadIdx.x == 0) a.joins[cta].parts = 0;
     if (cta >= min(total, (int)gridDim.x)) return;  // (the whole block, before it holds any TMEM)
     const int u0 = sh.begin(cta), u1 = sh.begin(cta + 1), n = u1 - u0;
     const uint64_t deadline = global_timer_ns() + kChunkTimeoutNs;
     const int tx = a.toks / 2;  // tokens of a row tile
-    ChunkWork w = chunk_place(a, cum, u0);  // every warp walks the list for itself
+    ChunkWork w = chunk_place<kTcKeys>(a, cum, u0);  // every warp walks the list for itself
     if (warp == 1) tc_alloc(&S.tmem, C_TMEM_COLS);
     tc_fence_before();
     __syncthreads();
@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(C_THREADS, 1)
         bool ok = true;
         for (int j = 0; j < n; ++j) {  // V of tile j and K of the next
             if (j + 1 < n) {
-                chunk_advance(a, cum, w);
+                chunk_advance<kTcKeys>(a, cum, w);
                 then = place();
             }
             // their buffers are free once the S products of tile j - 1 and the P V products of tile j - 2 are done
@@ -211,86 +211,96 @@ __global__ void __launch_bounds__(C_THREADS, 1)
                 }
         }
     } else if (warp == 1) {
-        if (lane == 0) {  // products, issued in order by this one thread
-            constexpr uint32_t kIdescS = idesc<T>(128, kTcKeys, false), kIdescO = idesc<T>(128, DH, true);
-            // (descriptors of what lies `bytes` further: the address is in the low word)
-            auto on = [](uint64_t d, uint32_t bytes) {
-                return (d & 0xffffffff00000000ull) | (uint32_t)((uint32_t)d + (bytes >> 4));
-            };
-            const uint64_t q0 = smem_desc_sw128(smem_u32(t + L::Q)), k0 = smem_desc_sw128(smem_u32(t + L::K)),
-                           v0 = desc_mn_sw128(smem_u32(t + L::V));
-            auto qk = [&](int x, int j) {
-                const uint64_t q = on(q0, (uint32_t)x * L::TILE), k = on(k0, (uint32_t)(j & 1) * L::TILE);
+        // products, issued in order by one lane (the whole warp walks along: what the instructions take stays in uniform
+        // registers, and nothing but them stands between two of them)
+        const bool leader = elect_one();
+        constexpr uint32_t kIdescS = idesc<T>(128, kTcKeys, false), kIdescO = idesc<T>(128, DH, true);
+        // (descriptors of what lies `bytes` further: the address is in the low word)
+        auto on = [](uint64_t d, uint32_t bytes) {
+            return (d & 0xffffffff00000000ull) | (uint32_t)((uint32_t)d + (bytes >> 4));
+        };
+        const uint64_t q0 = smem_desc_sw128(smem_u32(t + L::Q)), k0 = smem_desc_sw128(smem_u32(t + L::K)),
+                       v0 = desc_mn_sw128(smem_u32(t + L::V));
+        auto qk = [&](int x, int j) {
+            const uint64_t q = on(q0, (uint32_t)x * L::TILE), k = on(k0, (uint32_t)(j & 1) * L::TILE);
 #pragma unroll
-                for (int kk = 0; kk < DH / 16; ++kk) {
-                    const uint32_t off = (uint32_t)(kk >> 2) * T_HALF + (uint32_t)(kk & 3) * 32;
-                    tc_mma(tmem + (uint32_t)x * kTcKeys, on(q, off), on(k, off), kIdescS, kk > 0);
-                }
-            };
-            auto pv = [&](int x, int j, bool first, int kk0, int kk1) {  // steps of 16 keys
-                const uint64_t v = on(v0, (uint32_t)(j & 1) * L::TILE);
+            for (int kk = 0; kk < DH / 16; ++kk) {
+                const uint32_t off = (uint32_t)(kk >> 2) * T_HALF + (uint32_t)(kk & 3) * 32;
+                tc_mma(tmem + (uint32_t)x * kTcKeys, on(q, off), on(k, off), kIdescS, kk > 0);
+            }
+            tc_commit(&S.bs[x]);
+        };
+        auto pv = [&](int x, int j, bool first, int kk0, int kk1) {  // steps of 16 keys
+            const uint64_t v = on(v0, (uint32_t)(j & 1) * L::TILE);
 #pragma unroll
-                for (int kk = kk0; kk < kk1; ++kk)
-                    tc_mma_tmem_a(tmem + C_O + (uint32_t)x * 128, tmem + (uint32_t)x * kTcKeys + (uint32_t)kk * 8,
-                                  on(v, (uint32_t)kk * 16 * 128), kIdescO, (!first || kk > 0) ? 1u : 0u);
-            };
-            int np[2] = {0, 0}, nq[2] = {0, 0};  // uses of bp and bq so far
-            int nx = w.toks > tx ? 2 : 1;        // row tiles in use
-            bool first = true, ok = await_phase(S, &S.bk0, 0, deadline, a.err);
+            for (int kk = kk0; kk < kk1; ++kk)
+                tc_mma_tmem_a(tmem + C_O + (uint32_t)x * 128, tmem + (uint32_t)x * kTcKeys + (uint32_t)kk * 8,
+                              on(v, (uint32_t)kk * 16 * 128), kIdescO, (!first || kk > 0) ? 1u : 0u);
+        };
+        auto await = [&](uint64_t *bar, uint32_t parity) {
+            const bool got = __all_sync(0xffffffffu, await_phase(S, bar, parity, deadline, a.err));
+            tc_fence_after();
+            return got;
+        };
+        uint32_t np[2] = {0, 0}, nq[2] = {0, 0};  // uses of bp and bq so far
+        int nx = w.toks > tx ? 2 : 1;             // row tiles in use
+        int to_go = w.tiles - w.tile;             // tiles of the item from this one on
+        bool first = true, ok = await(&S.bk0, 0);
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {  // (unrolled: the issuing thread's own instructions are on the critical path)
-                if (!ok || x >= nx) break;
-                ok = await_phase(S, &S.bq[x], nq[x]++ & 1u, deadline, a.err);
-                if (!ok) break;
-                tc_fence_after();
+        for (int x = 0; x < 2; ++x) {
+            if (!ok || x >= nx) break;
+            ok = await(&S.bq[x], nq[x]++ & 1u);
+            if (ok && leader) {
                 qk(x, 0);
                 S.issued_ = 1;
-                tc_commit(&S.bs[x]);
             }
-            if (ok) tc_commit(&S.bf[0]);
-            for (int j = 0; ok && j < n; ++j) {
-                const int b = j & 1, b1 = (j + 1) & 1;
-                const bool ends = w.tile + 1 == w.tiles;  // the next tile belongs to another item
-                ok = await_phase(S, &S.bl[b], (j >> 1) & 1u, deadline, a.err);
+            __syncwarp();
+        }
+        if (ok && leader) tc_commit(&S.bf[0]);
+        ok = ok && await(&S.bl[0], 0);
+        for (int j = 0; ok && j < n; ++j) {
+            const bool ends = to_go == 1, more = j + 1 < n;  // ends: the next tile belongs to another item
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                if (!ok || x >= nx) break;
+                const uint32_t ph = np[x]++ & 1u;
+                ok = await(&S.bp[x][0], ph);
+                if (!ok) break;
+                if (leader) pv(x, j, first, 0, C_FIRST / 16);
+                __syncwarp();
+                ok = await(&S.bp[x][1], ph);
+                if (!ok) break;
+                if (leader) {
+                    pv(x, j, false, C_FIRST / 16, kTcKeys / 16);
+                    if (ends || !more) tc_commit(&S.bo[x]);
+                    if (more && !ends) qk(x, j + 1);  // after the P V that read P from the same columns
+                    if (x + 1 == nx && more && !ends) tc_commit(&S.bf[(j + 1) & 1]);
+                }
+                __syncwarp();
+            }
+            if (!ok) break;
+            first = false;
+            --to_go;
+            if (ends && more) {  // both row tiles are on their way out; the next item's Q follows
+                w.tile = w.tiles - 1;
+                chunk_advance<kTcKeys>(a, cum, w);
+                first = true;
+                nx = w.toks > tx ? 2 : 1;
+                to_go = w.tiles;
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     if (!ok || x >= nx) break;
-                    const uint32_t ph = np[x]++ & 1u;
-                    ok = await_phase(S, &S.bp[x][0], ph, deadline, a.err);
-                    if (!ok) break;
-                    tc_fence_after();
-                    pv(x, j, first, 0, C_FIRST / 16);
-                    ok = await_phase(S, &S.bp[x][1], ph, deadline, a.err);
-                    if (!ok) break;
-                    tc_fence_after();
-                    pv(x, j, false, C_FIRST / 16, kTcKeys / 16);
-                    if (ends || j + 1 == n) tc_commit(&S.bo[x]);
-                    if (j + 1 < n && !ends) {  // after the P V that read P from the same columns
-                        qk(x, j + 1);
-                        tc_commit(&S.bs[x]);
-                    }
+                    ok = await(&S.bq[x], nq[x]++ & 1u);
+                    if (ok && leader) qk(x, j + 1);
+                    __syncwarp();
                 }
-                if (!ok) break;
-                first = false;
-                if (j + 1 < n) chunk_advance(a, cum, w);
-                if (ends && j + 1 < n) {  // both row tiles are on their way out; the next item's Q follows
-                    first = true;
-                    nx = w.toks > tx ? 2 : 1;
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        if (!ok || x >= nx) break;
-                        ok = await_phase(S, &S.bq[x], nq[x]++ & 1u, deadline, a.err);
-                        if (!ok) break;
-                        tc_fence_after();
-                        qk(x, j + 1);
-                        tc_commit(&S.bs[x]);
-                    }
-                    if (!ok) break;
-                }
-                tc_commit(&S.bf[b1]);
+                if (ok && leader) tc_commit(&S.bf[(j + 1) & 1]);
+                __syncwarp();
             }
-            if (S.issued_) tc_commit(&S.bdone);  // tracks everything issued above
+            if (more) ok = ok && await(&S.bl[(j + 1) & 1], ((j + 1) >> 1) & 1u);
         }
+        if (leader && S.issued_) tc_commit(&S.bdone);  // tracks everything issued above
+        __syncwarp();
     } else {  // softmax warpgroup x: warp w owns TMEM lanes (rows) 32 * (w % 4) .. + 31
         const int x = (warp - 2) >> 2, quarter = warp & 3, row = 32 * quarter + lane;
         const uint32_t trow = tmem + ((uint32_t)(32 * quarter) << 16);
@@ -299,6 +309,26 @@ __global__ void __launch_bounds__(C_THREADS, 1)
         constexpr float kLazy = 8.f;  // log2 of the largest P before the max moves
         int left = n, at_tile = 0, ns = 0, no = 0;  // ns, no: uses of bs and bo so far
         bool ok = true, whole = w.tile == 0;        // whole: this CTA has begun the item
+        // Q of this thread's row of an item into the swizzled tile
+        auto load_q = [&](const ChunkWork &y) {
+            const int rows = min(tx, y.toks - x * tx) * a.group;
+            if (rows <= 0) return;
+            uint8_t *qs = t + L::Q + x * L::TILE;
+            const int tok = row / a.group;
+            const T *src = row < rows ? static_cast<const T *>(a.q) + ((long long)y.ch.row0 + y.tok + x * tx + tok) * a.ld_q +
+                                            (long long)(y.h * a.group + row - tok * a.group) * DH
+                                      : nullptr;
+            uint4 v[DH / 8];  // (all loads before the first store)
+#pragma unroll
+            for (int c = 0; c < DH / 8; ++c)
+                v[c] = src ? reinterpret_cast<const uint4 *>(src)[c] : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+            for (int c = 0; c < DH / 8; ++c)
+                *reinterpret_cast<uint4 *>(qs + (c >> 3) * T_HALF + sw128_offset(row, (c & 7) * 8)) = v[c];
+            fence_proxy_async_shared();
+            mbar_arrive(&S.bq[x]);
+        };
+        load_q(w);
         for (int it = 0; ok && left > 0; ++it) {
             const int count = min(left, w.tiles - w.tile);  // tiles of this item in this CTA
             const bool ends = w.tile + count == w.tiles;
@@ -310,19 +340,6 @@ __global__ void __launch_bounds__(C_THREADS, 1)
                 const long long q_row = (long long)w.ch.row0 + w.tok + x * tx + tok;
                 const int head = w.h * a.group + (row - tok * a.group);
                 const int pos = mine ? w.ch.base + w.tok + x * tx + tok : INT_MIN;
-                {  // Q of this row into the swizzled tile; the item before is done with it (its last P V was awaited)
-                    uint8_t *qs = t + L::Q + x * L::TILE;
-                    const T *src = mine ? static_cast<const T *>(a.q) + q_row * a.ld_q + (long long)head * DH : nullptr;
-                    uint4 v[DH / 8];  // (all loads before the first store)
-#pragma unroll
-                    for (int c = 0; c < DH / 8; ++c)
-                        v[c] = src ? reinterpret_cast<const uint4 *>(src)[c] : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-                    for (int c = 0; c < DH / 8; ++c)
-                        *reinterpret_cast<uint4 *>(qs + (c >> 3) * T_HALF + sw128_offset(row, (c & 7) * 8)) = v[c];
-                    fence_proxy_async_shared();
-                    mbar_arrive(&S.bq[x]);
-                }
                 // what every row of the item sees: up to its first token, from its last one's window on
                 const int first_pos = w.ch.base + w.tok, last_pos = first_pos + w.toks - 1;
                 float m2 = -INFINITY, l = 0.f;
@@ -344,15 +361,13 @@ __global__ void __launch_bounds__(C_THREADS, 1)
                                 if (none || found) *p = y;
                                 odd |= found;
                             }
-                            if (odd) S.odd_[it & 3] = 1;
+                            if (odd) S.odd_[it & 7] = it + 1;
                             fence_proxy_async_shared();
                         }
                     }
                     ok = __all_sync(0xffffffffu, ok && await_phase(S, &S.bs[x], ns & 1u, deadline, a.err));
                     if (!ok) break;
                     tc_fence_after();
-                    // (every thread has left the item before the last one: its flag serves the next but one)
-                    if (j == 0 && x == 0 && row == 0) S.odd_[(it + 2) & 3] = 0;
                     if (!warp_used) {  // (rows of nobody: whatever their P is)
                         tc_fence_before();
                         mbar_arrive(&S.bp[x][0]);
@@ -426,11 +441,19 @@ __global__ void __launch_bounds__(C_THREADS, 1)
                     const float2 s2 = add2(ls[0], ls[1]);
                     l += s2.x + s2.y;
                 }
+                // the next item's queries: the products with this one's are done (S of its last tile was awaited), and
+                // O is not written again before this thread hands over the next item's first P
+                if (ok && left > count) {
+                    ChunkWork y = w;
+                    y.tile = y.tiles - 1;
+                    chunk_advance<kTcKeys>(a, cum, y);
+                    load_q(y);
+                }
                 // the row's result or partial, once the last P V is done
                 if (ok) ok = __all_sync(0xffffffffu, await_phase(S, &S.bo[x], no++ & 1u, deadline, a.err));
                 if (ok && warp_used) {
                     tc_fence_after();
-                    const bool odd = S.odd_[it & 3] != 0, result = whole && ends;
+                    const bool odd = S.odd_[it & 7] == it + 1, result = whole && ends;
                     const float inv = inverse(l);
                     const long long slot = (long long)(2 * cta + (whole ? 1 : 0)) * a.slot_rows + x * tx * a.group + row;
                     const uint64_t keep = policy_evict_last();
@@ -484,7 +507,8 @@ __global__ void __launch_bounds__(C_THREADS, 1)
             whole = true;
             if (left > 0) {  // on to the next item
                 w.tile = w.tiles - 1;
-                chunk_advance(a, cum, w);
+                chunk_advance<kTcKeys>(a, cum, w);
+                if (toks <= 0) load_q(w);  // (this warpgroup had no part in the last one)
             }
         }
     }
