@@ -31,7 +31,7 @@ namespace lf {
 namespace {
 
 constexpr int LP_THREADS = 256, LP_WARPS = LP_THREADS / 32, LP_TOP = 32, LP_LIST = 512, LP_PARTS = 8;
-constexpr int LP_U = 4, LP_STAGES = 3;  // 16-byte pieces of a thread's batch, batches on their way
+constexpr int LP_U = 2, LP_STAGES = 4;  // 16-byte pieces of a thread's batch, batches on their way
 constexpr int LP_RING = LP_STAGES * LP_U * LP_THREADS * 16;
 constexpr int LP_MAX_VOCAB = 1 << 18;
 constexpr float kLog2E = 1.4426950408889634f, kLn2 = 0.69314718055994530942f;
@@ -224,30 +224,55 @@ template <typename T>
 struct Walk {
     static constexpr int N = Vec<T>::N;
     using T2 = std::conditional_t<std::is_same<T, __half>::value, __half2, __nv_bfloat162>;
-    Sums t;       // (below a maximum that follows `best` at a distance of at most kLag)
-    float best;
-    int before, bad, infs;
-
-    // The maximum that the sums are taken below moves when a larger one is over 2^3 of it: sums stay as exact, and
-    // few threads ever move.
+    // The sums are taken below m, which moves when a larger logit lies over 2^kLag above it: they stay as exact, and few
+    // threads ever move.
     static constexpr float kLag = 3.f;
+    float m, limit, c;  // limit: what a logit must pass for m to move
+    float2 s, e;        // (in two halves)
+    float best;
+    uint32_t before, masks;  // masks: of 16-bit comparisons, L of lower and H of upper halves as 65536 (L - H) - L
+    int bad, infs;
+    bool masked;
+
+    __device__ __forceinline__ Walk(float c_) : c(c_), masked(false) {
+        m = limit = best = -INFINITY;
+        s = e = make_float2(0.f, 0.f);
+        before = masks = 0;
+        bad = infs = 0;
+    }
+    __device__ __forceinline__ Sums sums() const { return Sums{m, s.x + s.y, e.x + e.y}; }
+    __device__ __forceinline__ int count() const {
+        const int low = (int)((0u - masks) & 0xffffu);  // L
+        return (int)before + low + (low - (int16_t)((masks + (uint32_t)low) >> 16));
+    }
+    __device__ __forceinline__ void move(float to) {
+        Sums t = sums();
+        t.move(to, c);
+        m = to;
+        limit = to + kLag / c;
+        s = make_float2(t.s, 0.f), e = make_float2(t.e, 0.f);
+    }
+
     template <int U>
-    __device__ __forceinline__ void add(const uint4 *q, const int *v, float c, const Before<T> &b) {
-        float lm = largest<U>(q);
-        bad |= lm != lm;
+    __device__ __forceinline__ void add(const uint4 *q, int v, const Before<T> &b) {  // pieces v, v + LP_THREADS, ..
+        const float lm = largest<U>(q);
         best = fmaxf(best, lm);
-        if ((lm - t.m) * c > kLag) t.move(lm, c);
-        const Sums was = t;
-        sums<U, false>(q, c);
-        if (!(fabsf(t.e) < INFINITY)) {  // a masked logit (0 times an infinite d is none), or one that is not finite
-            t = was;
+        if (lm > limit) move(lm);
+        if (!masked) {
+            const float2 was_s = s, was_e = e;
+            terms<U, false>(q);
+            // a masked logit (0 times an infinite d is none), or one that is not finite: from here on the other way
+            if (!(fabsf(e.x + e.y) < INFINITY)) masked = true, s = was_s, e = was_e;
+        }
+        if (masked) {
             uint4 again[U];  // (unpacked anew: kept values would cost the common way its registers)
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 again[u] = q[u];
                 asm volatile("" : "+r"(again[u].x), "+r"(again[u].y), "+r"(again[u].z), "+r"(again[u].w));
             }
-            if (fabsf(t.m) < INFINITY) sums<U, true>(again, c);  // (no sums without a finite maximum)
+            bad |= lm != lm;
+            if (fabsf(m) < INFINITY) terms<U, true>(again);  // (no sums without a finite maximum)
             if (lm == INFINITY) {
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
@@ -258,62 +283,55 @@ struct Walk {
                 }
             }
         }
-        if constexpr (sizeof(T) == 4) {
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
+        for (int u = 0; u < U; ++u) {
+            const int at = v + u * LP_THREADS;
+            if constexpr (sizeof(T) == 4) {
                 float f[N];
                 unpack<T>(q[u], f);
-                const float to = v[u] < b.piece ? b.z : b.above;
+                const float to = at < b.piece ? b.z : b.above;
 #pragma unroll
                 for (int i = 0; i < N; ++i) before += f[i] >= to;
-            }
-        } else {
-            uint32_t none = 0;
-            T2 n = *reinterpret_cast<T2 *>(&none);
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const uint32_t to = v[u] < b.piece ? b.z2 : b.above2, *w = reinterpret_cast<const uint32_t *>(&q[u]);
+            } else {
+                const uint32_t to = at < b.piece ? b.z2 : b.above2, *w = reinterpret_cast<const uint32_t *>(&q[u]);
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    n = __hadd2(n, __hge2(*reinterpret_cast<const T2 *>(w + i), *reinterpret_cast<const T2 *>(&to)));
+                    masks += __hge2_mask(*reinterpret_cast<const T2 *>(w + i), *reinterpret_cast<const T2 *>(&to));
             }
-            before += (int)((float)n.x + (float)n.y);  // (at most 16 each: exact)
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (v[u] == b.piece) {  // equal logits before the token in its own piece
+            if (at == b.piece) {  // equal logits before the token in its own piece
                 uint4 own = q[u];
                 asm volatile("" : "+r"(own.x), "+r"(own.y), "+r"(own.z), "+r"(own.w));
                 float f[N];
                 unpack<T>(own, f);
 #pragma unroll
-                for (int i = 0; i < N; ++i) before += v[u] * N + i < b.own && f[i] == b.z;
+                for (int i = 0; i < N; ++i) before += at * N + i < b.own && f[i] == b.z;
             }
+        }
     }
     // The largest of the pieces' values; a NaN if there is one.
     template <int U>
     __device__ __forceinline__ float largest(const uint4 *q) {
         const uint32_t *w = reinterpret_cast<const uint32_t *>(q);
         if constexpr (sizeof(T) == 4) {
-            float m = -INFINITY;
+            float y = __uint_as_float(w[0]);
+            asm("max.NaN.f32 %0, %0, %1;" : "+f"(y) : "f"(__uint_as_float(w[1])));
 #pragma unroll
-            for (int i = 0; i < 4 * U; i += 2)
-                asm("max.NaN.f32 %0, %0, %1, %2;" : "+f"(m) : "f"(__uint_as_float(w[i])), "f"(__uint_as_float(w[i + 1])));
-            return m;
-        } else {
-            T2 m = *reinterpret_cast<const T2 *>(w);
-#pragma unroll
-            for (int i = 1; i < 4 * U; ++i) m = __hmax2_nan(m, *reinterpret_cast<const T2 *>(w + i));
-            float y;
-            asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"((float)m.x), "f"((float)m.y));
+            for (int i = 2; i < 4 * U; i += 2)
+                asm("max.NaN.f32 %0, %0, %1, %2;" : "+f"(y) : "f"(__uint_as_float(w[i])), "f"(__uint_as_float(w[i + 1])));
             return y;
+        } else {
+            T2 y = *reinterpret_cast<const T2 *>(w);
+#pragma unroll
+            for (int i = 1; i < 4 * U; ++i) y = __hmax2_nan(y, *reinterpret_cast<const T2 *>(w + i));
+            float z;
+            asm("max.NaN.f32 %0, %1, %2;" : "=f"(z) : "f"((float)y.x), "f"((float)y.y));
+            return z;
         }
     }
-    // Adds the pieces' terms below t.m.  CLAMP: a term of an infinite distance adds nothing.
+    // Adds the pieces' terms below m.  CLAMP: a term of an infinite distance adds nothing (a NaN stays one).
     template <int U, bool CLAMP>
-    __device__ __forceinline__ void sums(const uint4 *q, float c) {
-        const float2 m2 = make_float2(-t.m, -t.m), c2 = make_float2(c, c);
-        float2 s = make_float2(t.s, 0.f), e = make_float2(t.e, 0.f);
+    __device__ __forceinline__ void terms(const uint4 *q) {
+        const float2 m2 = make_float2(-m, -m), c2 = make_float2(c, c);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             float2 f[N / 2];
@@ -321,24 +339,25 @@ struct Walk {
 #pragma unroll
             for (int i = 0; i < N / 2; ++i) {
                 float2 d = lp_mul2(lp_add2(f[i], m2), c2);
-                if (CLAMP) d = make_float2(fmaxf(d.x, -1e30f), fmaxf(d.y, -1e30f));
+                if (CLAMP) {
+                    asm("max.NaN.f32 %0, %0, %1;" : "+f"(d.x) : "f"(-1e30f));
+                    asm("max.NaN.f32 %0, %0, %1;" : "+f"(d.y) : "f"(-1e30f));
+                }
                 const float2 p = make_float2(lp_ex2(d.x), lp_ex2(d.y));
                 s = lp_add2(s, p);
                 e = lp_fma2(d, p, e);
             }
         }
-        t.s = s.x + s.y;
-        t.e = e.x + e.y;
     }
-    __device__ __forceinline__ void add_one(float f, int at, float c, const Before<T> &b) {
+    __device__ __forceinline__ void add_one(float f, int at, const Before<T> &b) {
         best = fmaxf(best, f);
         bad |= f != f;
-        if ((f - t.m) * c > kLag) t.move(f, c);
         infs += f == INFINITY;
-        if (fabsf(t.m) < INFINITY) {
-            const float d = fmaxf((f - t.m) * c, -1e30f), p = lp_ex2(d);
-            t.s += p;
-            t.e = fmaf(d, p, t.e);
+        if (f > limit) move(f);
+        if (fabsf(m) < INFINITY) {
+            const float d = fmaxf((f - m) * c, -1e30f), p = lp_ex2(d);
+            s.x += p;
+            e.x = fmaf(d, p, e.x);
         }
         before += precedes(f, at, b.z, b.token);
     }
@@ -418,6 +437,25 @@ __global__ void __launch_bounds__(LP_THREADS, 4) token_logprobs_kernel(const LpA
     pdl_trigger();
     if (a.parts > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;");  // (every CTA of the row has begun: below)
     const Share<T> sh(a, r, part);
+    // Each thread copies its own pieces, a batch of U at a time, into its own places of a ring and reads them back:
+    // enough on their way for HBM without holding registers, and no barrier.
+    const uint4 *body = reinterpret_cast<const uint4 *>(sh.body);
+    extern __shared__ __align__(16) uint4 ring[];  // [LP_STAGES][U][LP_THREADS]
+    const int pieces = sh.v1 - sh.v0 - tid, batches = pieces <= 0 ? 0 : (pieces + LP_THREADS - 1) / LP_THREADS / U;
+    const uint4 *from = body + sh.v0 + tid;
+    uint4 *const mine = ring + tid;
+    int in = 0;  // copies: the stage they go to
+    auto fetch = [&](int k) {
+        if (k < batches) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) cp_async16(mine + in + u * LP_THREADS, from + u * LP_THREADS);
+            from += U * LP_THREADS;
+            in = in + U * LP_THREADS == LP_STAGES * U * LP_THREADS ? 0 : in + U * LP_THREADS;
+        }
+        cp_async_commit();
+    };
+#pragma unroll
+    for (int k = 0; k < LP_STAGES - 1; ++k) fetch(k);
     const float temp = a.temperature ? a.temperature[r] : 1.f;
     const int token = a.token ? a.token[r] : -1;
     const bool asked = token >= 0 && token < a.vocab;
@@ -425,55 +463,39 @@ __global__ void __launch_bounds__(LP_THREADS, 4) token_logprobs_kernel(const LpA
     const bool warm = temp >= 1e-30f && temp <= 1e30f;
     const float c = warm ? kLog2E / temp : 1.f;
     const Before<T> b(zt, asked ? token : -1, sh);
-
-    Walk<T> w;
-    w.t = Sums{-INFINITY, 0.f, 0.f};
-    w.best = -INFINITY;
-    w.before = w.bad = w.infs = 0;
-    // Each thread copies its own pieces, a batch of U at a time, into its own places of a ring and reads them back:
-    // enough on their way for HBM without holding registers, and no barrier.
-    const uint4 *body = reinterpret_cast<const uint4 *>(sh.body);
-    extern __shared__ __align__(16) uint4 ring[];  // [LP_STAGES][U][LP_THREADS]
-    const int pieces = sh.v1 - sh.v0, mine = pieces <= tid ? 0 : (pieces - tid + LP_THREADS - 1) / LP_THREADS;
-    auto place = [&](int i) { return ring + ((i / U) % LP_STAGES * U + i % U) * LP_THREADS + tid; };
-    auto fetch = [&](int i0) {
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (i0 + u < mine) cp_async16(place(i0 + u), body + sh.v0 + tid + (i0 + u) * LP_THREADS);
-        cp_async_commit();
-    };
-#pragma unroll
-    for (int k = 0; k < LP_STAGES - 1; ++k) fetch(k * U);
-    for (int i = 0; i < mine; i += U) {
-        fetch(i + (LP_STAGES - 1) * U);
+    Walk<T> w(c);
+    int v = sh.v0 + tid;
+    for (int k = 0, out = 0; k < batches; ++k, v += U * LP_THREADS) {
+        fetch(k + LP_STAGES - 1);
         asm volatile("cp.async.wait_group %0;" ::"n"(LP_STAGES - 1) : "memory");
         uint4 q[U];
-        int at[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) at[u] = sh.v0 + tid + (i + u) * LP_THREADS, q[u] = *place(i + u);
-        if (i + U <= mine) {
-            w.template add<U>(q, at, c, b);
-        } else {
-#pragma unroll
-            for (int u = 0; u < U - 1; ++u)
-                if (i + u < mine) w.template add<1>(q + u, at + u, c, b);
-        }
+        for (int u = 0; u < U; ++u) q[u] = mine[out + u * LP_THREADS];
+        out = out + U * LP_THREADS == LP_STAGES * U * LP_THREADS ? 0 : out + U * LP_THREADS;
+        w.template add<U>(q, v, b);
     }
-    if (tid < sh.extras) w.add_one((float)sh.row[sh.extra(tid)], sh.extra(tid), c, b);
+#pragma unroll
+    for (int u = 0; u < U - 1; ++u, v += LP_THREADS)  // less than a batch is left
+        if (v < sh.v1) {
+            const uint4 q = body[v];
+            w.template add<1>(&q, v, b);
+        }
+    if (tid < sh.extras) w.add_one((float)sh.row[sh.extra(tid)], sh.extra(tid), b);
     // the CTA's sums, below its maximum
     float m = w.best;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     const int n_bad = __reduce_or_sync(0xffffffffu, w.bad), n_inf = __reduce_add_sync(0xffffffffu, w.infs),
-              n_before = __reduce_add_sync(0xffffffffu, w.before);
-    w.t.move(m, c);
+              n_before = __reduce_add_sync(0xffffffffu, w.count());
+    Sums t0 = w.sums();
+    t0.move(m, c);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
-        w.t.s += __shfl_xor_sync(0xffffffffu, w.t.s, o);
-        w.t.e += __shfl_xor_sync(0xffffffffu, w.t.e, o);
+        t0.s += __shfl_xor_sync(0xffffffffu, t0.s, o);
+        t0.e += __shfl_xor_sync(0xffffffffu, t0.e, o);
     }
     if (lane == 0) {
-        S.warp_sums[warp] = w.t;
+        S.warp_sums[warp] = t0;
         S.warp_count[warp][0] = n_before, S.warp_count[warp][1] = n_bad, S.warp_count[warp][2] = n_inf;
     }
     float x = 0.f;

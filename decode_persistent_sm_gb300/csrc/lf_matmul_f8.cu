@@ -32,12 +32,14 @@ constexpr int F8_THREADS = 192;          // warp 0 copies, warp 1 MMA + TMEM own
 constexpr int F8_GROUP_M = 32;           // M-tiles that take each B tile in turn
 constexpr unsigned long long kF8TimeoutNs = 2000000000ull;
 
-template <int BN>
+// AR: rows of A that a stage holds.  With fewer than 128 the products read on into what lies behind (the rows of
+// their result that come of it are not stored), and more stages fit.
+template <int BN, int AR>
 struct F8Tile {
-    static constexpr int A = F8_BM * F8_BK, B = BN * F8_BK, STAGE = A + B;
-    static constexpr int STAGES = 196608 / STAGE;  // 192 KB: 4, 6, 8
+    static constexpr int A = AR * F8_BK, B = BN * F8_BK, STAGE = A + B;
+    static constexpr int STAGES = 196608 / STAGE;  // 192 KB: 4, 6, 8, or 16 with short A
     static constexpr uint32_t COLS = 2 * BN;       // two accumulators (a power of two, at least 32)
-    static constexpr int SMEM = STAGES * STAGE + 1024 + 256;
+    static constexpr int SMEM = STAGES * STAGE + 1024 + 512 + (F8_BM - AR) * F8_BK;
 };
 
 template <int STAGES>
@@ -110,10 +112,10 @@ __device__ __forceinline__ void f8_store(T *dst, const float *v, int left) {
     }
 }
 
-template <int BN>
+template <int BN, int AR>
 __global__ void __launch_bounds__(F8_THREADS, 1)
     matmul_f8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const F8Args a) {
-    using L = F8Tile<BN>;
+    using L = F8Tile<BN, AR>;
     constexpr int ST = L::STAGES;
     extern __shared__ __align__(1024) uint8_t f8_raw[];
     uint8_t *tiles = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(f8_raw) + 1023) & ~uintptr_t(1023));
@@ -283,18 +285,17 @@ bool f8_map(CUtensorMap *map, const void *p, int rows, int k, int box_rows) {
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int BN>
+template <int BN, int AR>
 lf_status launch_f8(const void *A, const void *B, F8Args a, int n_sm, cudaStream_t st) {
-    using L = F8Tile<BN>;
-    // a short A is not copied as 128 rows (the products of the rows behind it, whatever they hold, are not stored)
-    a.rows_a = a.m >= F8_BM ? F8_BM : (a.m + 7) / 8 * 8;
+    using L = F8Tile<BN, AR>;
+    a.rows_a = a.m >= AR ? AR : (a.m + 7) / 8 * 8;
     CUtensorMap ma, mb;
-    if (!set_smem_once<matmul_f8_kernel<BN>>(L::SMEM) || !f8_map(&ma, A, a.m, a.k, a.rows_a) ||
+    if (!set_smem_once<matmul_f8_kernel<BN, AR>>(L::SMEM) || !f8_map(&ma, A, a.m, a.k, a.rows_a) ||
         !f8_map(&mb, B, a.n, a.k, BN))
         return LF_ERR_CUDA;
     const long long tiles = (((long long)a.m + F8_BM - 1) / F8_BM) * (((long long)a.n + BN - 1) / BN);
     const unsigned grid = (unsigned)(tiles < n_sm ? tiles : n_sm);
-    return launch_pdl(matmul_f8_kernel<BN>, grid, F8_THREADS, L::SMEM, st, ma, mb, a) ? LF_OK : LF_ERR_CUDA;
+    return launch_pdl(matmul_f8_kernel<BN, AR>, grid, F8_THREADS, L::SMEM, st, ma, mb, a) ? LF_OK : LF_ERR_CUDA;
 }
 
 }  // namespace
@@ -323,7 +324,7 @@ extern "C" lf_status lf_matmul_f8(const void *a_device, const float *a_scale_dev
     const lf::F8Args a = {a_scale_device, b_scale_device, c_device, m, n, k, c_dtype, 0, err_device};
     cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
     const long long mt = ((long long)m + 127) / 128;
-    if (mt * ((n + 255) / 256) >= n_sm) return lf::launch_f8<256>(a_device, b_device, a, n_sm, st);
-    if (mt * ((n + 127) / 128) >= n_sm) return lf::launch_f8<128>(a_device, b_device, a, n_sm, st);
-    return lf::launch_f8<64>(a_device, b_device, a, n_sm, st);
+    if (mt * ((n + 255) / 256) >= n_sm) return lf::launch_f8<256, 128>(a_device, b_device, a, n_sm, st);
+    if (mt * ((n + 127) / 128) >= n_sm) return lf::launch_f8<128, 128>(a_device, b_device, a, n_sm, st);
+    return m <= 32 ? lf::launch_f8<64, 32>(a_device, b_device, a, n_sm, st) : lf::launch_f8<64, 128>(a_device, b_device, a, n_sm, st);
 }

@@ -17,11 +17,15 @@
 //
 // P is rounded to the cache's type for the second product: both operands of an MMA
 // have one type.  Its sum is taken before the rounding.
+#include <cooperative_groups.h>
+
 #include <algorithm>
 #include <climits>
 #include <type_traits>
 
 #include "lf_paged_chunk.h"
+
+namespace cg = cooperative_groups;
 
 namespace lf {
 namespace {
@@ -38,6 +42,7 @@ struct CkSmem {
     static constexpr int CUM = (CK_MAX_SEQS + 4) * 4;
     static constexpr int BYTES = STAGES * 2 * TILE + ML + CUM;
     static_assert(4 * 16 * DH * 4 <= 2 * TILE, "the joined rows fit the stage");
+    static_assert(STAGES >= 2 && 64 * 8 <= CUM, "a cluster's partials have their places");
 };
 
 // A 16-bit value is infinite or NaN.
@@ -98,6 +103,108 @@ class ChunkWalker {
                 if (fresh) whole = true;
             }
         }
+    }
+
+    // One item by the CTAs of a cluster, result and all: each takes an equal share of its
+    // tiles, and all join the partials through distributed shared memory.
+    __device__ void run_direct() {
+        cg::cluster_group cl = cg::this_cluster();
+        const int parts = (int)cl.num_blocks(), part = (int)cl.block_rank();
+        const int id = quotient(blockIdx.x, parts), g = quotient(id, a.kv.n_kv);  // row tile g of all sequences
+        ChunkWork w;
+        w.h = id - g * a.kv.n_kv;
+        w.b = -1;
+        for (int b0 = 0, at = 0; b0 < a.kv.n_seqs; b0 += 32) {
+            const int b = b0 + lane;
+            Chunk k = {0, 0, 0, false};
+            if (b < a.kv.n_seqs) k = chunk_of(a, b);
+            if (k.bad && blockIdx.x == 0 && warp == 0) atomicExch(a.err, 1u);
+            const int rt = row_tiles_of(k.c, a.toks);
+            int inc = rt;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += y;
+            }
+            const unsigned hit = __ballot_sync(0xffffffffu, at + inc > g);
+            if (hit && w.b < 0) {
+                const int who = __ffs(hit) - 1;
+                w.b = b0 + who;
+                w.r = g - at - __shfl_sync(0xffffffffu, inc - rt, who);
+                w.ch.row0 = __shfl_sync(0xffffffffu, k.row0, who);
+                w.ch.c = __shfl_sync(0xffffffffu, k.c, who);
+                w.ch.base = __shfl_sync(0xffffffffu, k.base, who);
+                if (blockIdx.x > 0) break;
+            }
+            at += __shfl_sync(0xffffffffu, inc, 31);
+        }
+        if (w.b < 0) return;  // (the whole cluster: there are fewer row tiles than the grid allows for)
+        w.set<KT>(a);
+        const Shares sh(w.tiles, parts);
+        const int t0 = part < w.tiles ? sh.begin(part) : 0, n = part < w.tiles ? sh.begin(part + 1) - t0 : 0;
+        w.tile = t0;
+        ChunkWork load = w;
+        auto fetch_next = [&](int i) {
+            if (i < n) {
+                prepare(load);
+                fetch(i % L::STAGES);
+                ++load.tile;
+            }
+            cp_async_commit();
+        };
+        for (int i = 0; i < L::STAGES - 1; ++i) fetch_next(i);
+        if (n > 0) begin(w);
+        for (int i = 0; i < n; ++i) {
+            fetch_next(i + L::STAGES - 1);
+            asm volatile("cp.async.wait_group %0;" ::"n"(L::STAGES - 1) : "memory");
+            __syncthreads();
+            tile<true>(w, i + 1 == n, i % L::STAGES, false, 0);
+            __syncthreads();
+            ++w.tile;
+        }
+        // this CTA's partial lies in shared memory (finish); an empty share leaves nothing
+        const int rows = w.toks * a.group;
+        float *mine = direct_o();
+        float2 *stat = direct_ml();
+        if (n == 0) {
+            for (int x = tid; x < rows * DH; x += CK_THREADS) mine[x] = 0.f;
+            for (int x = tid; x < rows; x += CK_THREADS) stat[x] = make_float2(-INFINITY, 0.f);
+        }
+        if (parts > 1)
+            cl.sync();
+        else
+            __syncthreads();
+        const int pairs = rows * (DH / 2), per = (pairs + parts - 1) / parts;
+        for (int x = part * per + tid; x < min(pairs, (part + 1) * per); x += CK_THREADS) {
+            const int row = x / (DH / 2), c = (x % (DH / 2)) * 2;
+            float2 y[8], v[8];
+            float mx = -INFINITY;
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (k < parts) {
+                    y[k] = parts > 1 ? *cl.map_shared_rank(stat + row, k) : stat[row];
+                    v[k] = *reinterpret_cast<const float2 *>(parts > 1 ? cl.map_shared_rank(mine + row * DH + c, k)
+                                                                       : mine + row * DH + c);
+                    mx = fmaxf(mx, y[k].x);
+                }
+            const float off = mx == -INFINITY ? 0.f : mx;
+            float sx = 0.f, sy = 0.f, sl = 0.f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (k < parts) {
+                    const float f = ex2(y[k].x - off);
+                    sx += f * v[k].x;
+                    sy += f * v[k].y;
+                    sl += f * y[k].y;
+                }
+            const float inv = inverse(sl);
+            const int tok = quotient(row, a.group), head = w.h * a.group + row - tok * a.group;
+            const long long q = w.ch.row0 + w.tok + tok;
+            *reinterpret_cast<uint32_t *>(static_cast<T *>(a.out) + q * a.ld_out + (long long)head * DH + c) =
+                pack2<T>(sx * inv, sy * inv);
+            if (c == 0 && a.lse) a.lse[q * a.n_q + head] = mx * 0.69314718055994530942f + logf(sl);
+        }
+        if (parts > 1) cl.sync();  // nobody leaves while its partial is read
     }
 
   private:
@@ -169,7 +276,7 @@ class ChunkWalker {
             base[r] = nullptr;
             pos[r] = INT_MIN;
             if (row < rows) {
-                const int tok = row / a.group;
+                const int tok = quotient(row, a.group);
                 base[r] = static_cast<const T *>(a.q) + (long long)(w.ch.row0 + w.tok + tok) * a.ld_q +
                           (long long)(w.h * a.group + row - tok * a.group) * DH;
                 pos[r] = w.ch.base + w.tok + tok;
@@ -195,7 +302,13 @@ class ChunkWalker {
         return j <= pos[r] && (a.window == 0 || j > (long long)pos[r] - a.window);
     }
 
-    // One tile of the item.
+    // Where a CTA of run_direct leaves its partial, the same place in all: o in the ring's first stage (no copy is under
+    // way by then), the statistics where the list's table would be.
+    __device__ float *direct_o() const { return reinterpret_cast<float *>(stage0); }
+    __device__ float2 *direct_ml() const { return reinterpret_cast<float2 *>(cum); }
+
+    // One tile of the item.  DIRECT: the item's end is a partial in shared memory.
+    template <bool DIRECT = false>
     __device__ void tile(const ChunkWork &w, bool last, int s, bool whole, int slot) {
         const int wk = warp / WR, t = lane & 3;
         const int j0 = (w.kt0 + w.tile) * KT;  // position of the tile's first key
@@ -290,7 +403,7 @@ class ChunkWalker {
             }
         }
         if (odd) add_odd(w, j0, wk, t);
-        if (last) finish(w, s, whole, slot);
+        if (last) finish<DIRECT>(w, s, whole, slot);
     }
 
     // Adds the tile's values that are not finite to the rows that see them.
@@ -317,13 +430,17 @@ class ChunkWalker {
 
     // The item's end in this CTA: the result where it has seen all of it, a partial otherwise; warps with the same rows
     // joined.
+    template <bool DIRECT>
     __device__ void finish(const ChunkWork &w, int s, bool whole, int slot) {
         const int wr = warp % WR, g = lane >> 2, t = lane & 3, rows = w.toks * a.group;
         const long long at = (long long)slot * a.slot_rows;
         float *dst = a.part_o + at * DH;
         float2 *dst_ml = a.part_ml + at;
         auto result = [&](int row, int c, float x, float y, float mx, float sum) {  // dims c, c + 1
-            if (whole) {
+            if constexpr (DIRECT) {
+                *reinterpret_cast<float2 *>(direct_o() + row * DH + c) = make_float2(x, y);
+                if (c == 0) direct_ml()[row] = make_float2(mx, sum);
+            } else if (whole) {
                 const int tok = row / a.group, head = w.h * a.group + row - tok * a.group;
                 const long long q = w.ch.row0 + w.tok + tok;
                 const float inv = inverse(sum);
@@ -341,6 +458,7 @@ class ChunkWalker {
             l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
         }
         if constexpr (WK == 1) {
+            if (DIRECT) __syncthreads();  // every warp has read the keys and values
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
                 const int row = wr * 16 + g + 8 * r;
@@ -351,7 +469,7 @@ class ChunkWalker {
         } else {
             __syncthreads();  // every warp has read this stage's keys and values
             // row r of warp w at (w * 16 + r) * DH, its columns permuted by the row (8 rows of a warp write 8 bank groups)
-            float *red = reinterpret_cast<float *>(stage0 + (size_t)s * 2 * L::TILE);
+            float *red = reinterpret_cast<float *>(stage0 + (size_t)(DIRECT ? 1 : s) * 2 * L::TILE);
             auto col = [](int row, int c) { return c ^ ((row & (DH / 8 - 1) & 7) << 3); };
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
@@ -392,6 +510,15 @@ __global__ void __launch_bounds__(CK_THREADS, CK_CTAS_PER_SM) paged_chunk_kernel
     pdl_wait();
     pdl_trigger();
     ChunkWalker<T, DH, WR>(a, ck_smem).run();
+}
+
+// A cluster per item and no other launch: for few keys.
+template <typename T, int DH, int WR>
+__global__ void __launch_bounds__(CK_THREADS, CK_CTAS_PER_SM) paged_chunk_direct(const ChunkArgs a) {
+    extern __shared__ __align__(128) uint8_t ck_smem[];
+    pdl_wait();
+    pdl_trigger();
+    ChunkWalker<T, DH, WR>(a, ck_smem).run_direct();
 }
 
 // The items that several CTAs share, half a warp to a row: block (c, y) takes rows
@@ -488,6 +615,21 @@ void shape(ChunkArgs &a, int n_sm) {
     a.grid = a.tc ? n_sm : n_sm * CK_CTAS_PER_SM;
 }
 
+// CTAs to an item of the direct kernel, 0 for the list and its join.
+int chunk_direct_parts(const ChunkArgs &a, int n_sm) {
+    if (a.tc) return 0;
+    const int kt = tile_keys(a.kv.head_dim), rts = (a.n_tokens + a.kv.n_seqs - 1) / a.kv.n_seqs;  // tokens of a sequence
+    const int bound = a.window > 0 ? std::min(a.window + a.toks, a.max_len) : a.max_len;
+    const int tiles = bound / kt + 1;
+    const long long items = (long long)a.kv.n_seqs * a.kv.n_kv * ((rts + a.toks - 1) / a.toks);
+    if (items > 6 * n_sm) return 0;
+    int parts = 1;
+    while (parts < 8 && parts < tiles && items * parts * 2 <= 2 * n_sm) parts *= 2;
+    const long long waves = (items * parts + 2 * n_sm - 1) / (2 * n_sm);
+    const int each = (tiles + parts - 1) / parts;
+    return waves * each <= (waves == 1 ? 512 / kt : 6) ? parts : 0;
+}
+
 struct CkWs {
     size_t ml, o, bytes;
 };
@@ -516,9 +658,20 @@ size_t ck_bytes(ChunkArgs a, int n_sm) {
     return ck_layout(a).bytes;
 }
 
-template <typename T, int DH>
-lf_status launch_chunk(const ChunkArgs &a, cudaStream_t st) {
+template <typename T, int DH, int WR>
+bool launch_rows(const ChunkArgs &a, int direct, cudaStream_t st) {
     constexpr int smem = CkSmem<T, DH>::BYTES;
+    if (!direct)
+        return set_smem_once<paged_chunk_kernel<T, DH, WR>>(smem) &&
+               launch_pdl(paged_chunk_kernel<T, DH, WR>, a.grid, CK_THREADS, smem, st, a);
+    // (a cluster for each row tile that the chunks can have; those without one leave at once)
+    const unsigned clusters = (unsigned)(a.kv.n_kv * (a.kv.n_seqs + a.n_tokens / a.toks));
+    return set_smem_once<paged_chunk_direct<T, DH, WR>>(smem) &&
+           launch_pdl_cluster(paged_chunk_direct<T, DH, WR>, (unsigned)direct, dim3(clusters * direct), CK_THREADS, smem, st, a);
+}
+
+template <typename T, int DH>
+lf_status launch_chunk(const ChunkArgs &a, int direct, cudaStream_t st) {
     bool ok = false;
     if constexpr (DH >= 64) {
         if (a.tc) {
@@ -527,27 +680,20 @@ lf_status launch_chunk(const ChunkArgs &a, cudaStream_t st) {
             ok = true;
         }
     }
-    if (a.tc) {
-    } else if (a.slot_rows == 16)
-        ok = set_smem_once<paged_chunk_kernel<T, DH, 1>>(smem) &&
-             launch_pdl(paged_chunk_kernel<T, DH, 1>, a.grid, CK_THREADS, smem, st, a);
-    else if (a.slot_rows == 32)
-        ok = set_smem_once<paged_chunk_kernel<T, DH, 2>>(smem) &&
-             launch_pdl(paged_chunk_kernel<T, DH, 2>, a.grid, CK_THREADS, smem, st, a);
-    else
-        ok = set_smem_once<paged_chunk_kernel<T, DH, 4>>(smem) &&
-             launch_pdl(paged_chunk_kernel<T, DH, 4>, a.grid, CK_THREADS, smem, st, a);
-    return ok && launch_pdl(paged_chunk_join<T, DH>, dim3((unsigned)a.grid, (unsigned)(a.slot_rows / CJ_ROWS)), CJ_THREADS,
-                            0, st, a)
-               ? LF_OK
-               : LF_ERR_CUDA;
+    if (!a.tc)
+        ok = a.slot_rows == 16   ? launch_rows<T, DH, 1>(a, direct, st)
+             : a.slot_rows == 32 ? launch_rows<T, DH, 2>(a, direct, st)
+                                 : launch_rows<T, DH, 4>(a, direct, st);
+    if (ok && !direct)
+        ok = launch_pdl(paged_chunk_join<T, DH>, dim3((unsigned)a.grid, (unsigned)(a.slot_rows / CJ_ROWS)), CJ_THREADS, 0, st, a);
+    return ok ? LF_OK : LF_ERR_CUDA;
 }
 
 template <typename T>
-lf_status launch_chunk_dim(const ChunkArgs &a, cudaStream_t st) {
-    return a.kv.head_dim == 32   ? launch_chunk<T, 32>(a, st)
-           : a.kv.head_dim == 64 ? launch_chunk<T, 64>(a, st)
-                                 : launch_chunk<T, 128>(a, st);
+lf_status launch_chunk_dim(const ChunkArgs &a, int direct, cudaStream_t st) {
+    return a.kv.head_dim == 32   ? launch_chunk<T, 32>(a, direct, st)
+           : a.kv.head_dim == 64 ? launch_chunk<T, 64>(a, direct, st)
+                                 : launch_chunk<T, 128>(a, direct, st);
 }
 
 }  // namespace
@@ -606,6 +752,8 @@ extern "C" lf_status lf_attn_paged_chunk(const lf_paged_kv *kv, const void *q_de
     a.window = window >= max_len ? 0 : window;  // (every position lies less than max_len back)
     a.scale_log2 = scale * lf::kLog2e;
     a.err = err_device;
+    const int direct = lf::chunk_direct_parts(a, n_sm);
     cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
-    return kv->dtype == LF_F16 ? lf::launch_chunk_dim<__half>(a, st) : lf::launch_chunk_dim<__nv_bfloat16>(a, st);
+    return kv->dtype == LF_F16 ? lf::launch_chunk_dim<__half>(a, direct, st)
+                               : lf::launch_chunk_dim<__nv_bfloat16>(a, direct, st);
 }

@@ -58,30 +58,6 @@ __device__ __forceinline__ Chunk chunk_of(const ChunkArgs &a, int b) {
     return k;
 }
 
-// sum_{i < n} floor((a i + b) / M) for a, b >= 0, M a power of two, a n + b < 2^32, by
-// the Euclidean reduction of the lattice points under a line (each step swaps a and m).
-template <unsigned M>
-__host__ __device__ inline long long floor_sum(unsigned n, unsigned a, unsigned b) {
-    long long sum = 0;
-    unsigned m = M;
-    bool power = true;  // (the first step divides by M: shifts)
-    while (n) {
-        const unsigned qa = power ? a / M : a / m, qb = power ? b / M : b / m;
-        sum += (long long)n * (n - 1) / 2 * qa + (long long)n * qb;
-        a -= qa * m;
-        b -= qb * m;
-        if (a == 0) break;  // (what is left lies below one step)
-        const unsigned y = a * n + b;
-        n = power ? y / M : y / m;
-        b = y - n * m;
-        const unsigned t = m;
-        m = a;
-        a = t;
-        power = false;
-    }
-    return sum;
-}
-
 // Keys [lo, hi) that the row tile from token `tok` on sees.
 struct Keys {
     int lo, hi;
@@ -99,26 +75,12 @@ template <int KT>
 __host__ __device__ inline int key_tiles(const Keys &k) {
     return k.hi <= 0 ? 1 : (int)((unsigned)(k.hi + KT - 1) / KT - (unsigned)k.lo / KT);
 }
-// Key tiles of the first n row tiles of a chunk, n at most ceil(c / toks).
+// Row tiles of a chunk of c tokens.
+__device__ __forceinline__ int row_tiles_of(int c, int toks) { return c <= toks ? (c > 0) : quotient(c + toks - 1, toks); }
+// Key tiles of row tile r.
 template <int KT>
-__host__ __device__ inline long long tiles_before(int base, int c, int window, int toks, int n) {
-    if (n <= 0) return 0;
-    const int full = c / toks < n ? c / toks : n;  // row tiles of `toks` tokens; one more is shorter
-    // those that end before position 1 have one tile without keys
-    int none = base < 0 ? -base / toks : 0;
-    if (none > full) none = full;
-    long long sum = none + floor_sum<KT>((unsigned)(full - none), (unsigned)toks,
-                                         full > none ? (unsigned)(base + (none + 1) * toks + KT - 1) : 0u);
-    if (n > full) sum += base + c <= 0 ? 1 : (unsigned)(base + c + KT - 1) / KT;
-    if (window > 0) {  // less the tiles before each one's first key; none before token window - 1 - base
-        const long long from = (long long)window - 1 - base;
-        const long long z = from < 0 ? 0 : from / toks + 1;
-        if (z < n) {
-            const int f = (int)z;
-            sum -= floor_sum<KT>((unsigned)(n - f), (unsigned)toks, (unsigned)(base + f * toks - window + 1));
-        }
-    }
-    return sum;
+__device__ __forceinline__ int key_tiles_of(const ChunkArgs &a, const Chunk &k, int r) {
+    return key_tiles<KT>(keys_of(k.base, k.c, a.window, a.toks, r * a.toks));
 }
 
 // The list as one CTA walks it.
@@ -139,18 +101,32 @@ struct ChunkWork {
 };
 
 // Fills cum[b] = key tiles per KV head of the sequences before b (cum[n_seqs]: of
-// all); a whole block calls it.  Returns the list's length.
+// all); a whole block calls it.  Returns the list's length.  A lane adds up the few
+// row tiles of its sequence, the warp together those of a long chunk.
 template <int KT>
 __device__ __forceinline__ int chunk_plan(const ChunkArgs &a, int *cum) {
+    constexpr int kFew = 4;
     const int n = a.kv.n_seqs, lane = threadIdx.x & 31;
     int at = 0;
     for (int b0 = 0; b0 < n; b0 += 32) {  // (every warp for itself; the first fills the table)
         const int b = b0 + lane;
-        int t = 0;
+        Chunk k = {0, 0, 0, false};
         if (b < n) {
-            const Chunk k = chunk_of(a, b);
-            t = (int)tiles_before<KT>(k.base, k.c, a.window, a.toks, (k.c + a.toks - 1) / a.toks);
+            k = chunk_of(a, b);
             if (k.bad && blockIdx.x == 0 && threadIdx.x < 32) atomicExch(a.err, 1u);
+        }
+        const int rt = row_tiles_of(k.c, a.toks);
+        int t = 0;
+        for (int r = 0; r < min(rt, kFew); ++r) t += key_tiles_of<KT>(a, k, r);
+        for (unsigned left = __ballot_sync(0xffffffffu, rt > kFew); left; left &= left - 1) {
+            const int who = __ffs(left) - 1, rts = __shfl_sync(0xffffffffu, rt, who);
+            Chunk y;
+            y.base = __shfl_sync(0xffffffffu, k.base, who);
+            y.c = __shfl_sync(0xffffffffu, k.c, who);
+            int sum = 0;
+            for (int r = kFew + lane; r < rts; r += 32) sum += key_tiles_of<KT>(a, y, r);
+            sum = __reduce_add_sync(0xffffffffu, sum);
+            if (lane == who) t += sum;
         }
         int inc = t;
 #pragma unroll
@@ -185,19 +161,26 @@ __device__ __forceinline__ ChunkWork chunk_place(const ChunkArgs &a, const int *
     w.h = quotient(u, per_head);
     u -= w.h * per_head;
     w.ch = chunk_of(a, lo);
-    w.row_tiles = (w.ch.c + a.toks - 1) / a.toks;
-    // the row tile with before(r) <= u < before(r + 1): 32 places at a time
-    lo = 0, hi = w.row_tiles;
-    while (hi - lo > 1) {
-        const int step = (hi - lo + 31) / 32, x = lo + lane * step;
-        const bool in = x < hi && tiles_before<KT>(w.ch.base, w.ch.c, a.window, a.toks, x) <= u;
-        const int last = 31 - __clz(__ballot_sync(0xffffffffu, in));  // (lane 0 always is)
-        lo += last * step;
-        hi = min(hi, lo + step);
+    w.row_tiles = row_tiles_of(w.ch.c, a.toks);
+    w.r = 0;
+    w.tile = u;
+    for (int r0 = 0; w.row_tiles > 1 && r0 < w.row_tiles; r0 += 32) {  // 32 row tiles at a time: how many end at or before u
+        const int t = r0 + lane < w.row_tiles ? key_tiles_of<KT>(a, w.ch, r0 + lane) : 0;
+        int inc = t;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += y;
+        }
+        const int ended = __popc(__ballot_sync(0xffffffffu, r0 + lane < w.row_tiles && inc <= u));
+        if (ended < 32) {
+            w.r = r0 + ended;
+            w.tile = u - __shfl_sync(0xffffffffu, inc - t, ended);
+            break;
+        }
+        u -= __shfl_sync(0xffffffffu, inc, 31);
     }
-    w.r = lo;
     w.set<KT>(a);
-    w.tile = u - (int)tiles_before<KT>(w.ch.base, w.ch.c, a.window, a.toks, lo);
     return w;
 }
 
@@ -214,7 +197,7 @@ __device__ __forceinline__ bool chunk_advance(const ChunkArgs &a, const int *cum
                 ++w.b;
             } while (w.b < a.kv.n_seqs - 1 && cum[w.b + 1] == cum[w.b]);
             w.ch = chunk_of(a, w.b);
-            w.row_tiles = (w.ch.c + a.toks - 1) / a.toks;
+            w.row_tiles = row_tiles_of(w.ch.c, a.toks);
         }
     }
     w.set<KT>(a);
