@@ -33,11 +33,11 @@ constexpr int F8_GROUP_M = 32;           // M-tiles that take each B tile in tur
 constexpr unsigned long long kF8TimeoutNs = 2000000000ull;
 
 // AR: rows of A that a stage holds.  With fewer than 128 the products read on into what lies behind (the rows of
-// their result that come of it are not stored), and more stages fit.
-template <int BN, int AR>
+// their result that come of it are not stored), and more fits.  KS: blocks of 128 along K to a stage, i.e. to a wait.
+template <int BN, int AR, int KS>
 struct F8Tile {
-    static constexpr int A = AR * F8_BK, B = BN * F8_BK, STAGE = A + B;
-    static constexpr int STAGES = 196608 / STAGE;  // 192 KB: 4, 6, 8, or 16 with short A
+    static constexpr int A = AR * F8_BK, B = BN * F8_BK, BLOCK = A + B, STAGE = KS * BLOCK;
+    static constexpr int STAGES = 196608 / STAGE;  // 192 KB
     static constexpr uint32_t COLS = 2 * BN;       // two accumulators (a power of two, at least 32)
     static constexpr int SMEM = STAGES * STAGE + 1024 + 512 + (F8_BM - AR) * F8_BK;
 };
@@ -60,6 +60,7 @@ struct F8Args {
 
 template <typename S>
 __device__ __forceinline__ bool f8_wait(S &s, uint64_t *bar, uint32_t parity, uint64_t deadline, uint32_t *err) {
+    if (mbar_test_wait(bar, parity)) return true;
     while (!mbar_try_wait(bar, parity)) {
         if (s.abort_) return false;
         if (global_timer_ns() > deadline) {
@@ -112,17 +113,17 @@ __device__ __forceinline__ void f8_store(T *dst, const float *v, int left) {
     }
 }
 
-template <int BN, int AR>
+template <int BN, int AR, int KS>
 __global__ void __launch_bounds__(F8_THREADS, 1)
     matmul_f8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const F8Args a) {
-    using L = F8Tile<BN, AR>;
+    using L = F8Tile<BN, AR, KS>;
     constexpr int ST = L::STAGES;
     extern __shared__ __align__(1024) uint8_t f8_raw[];
     uint8_t *tiles = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(f8_raw) + 1023) & ~uintptr_t(1023));
     auto &S = *reinterpret_cast<F8Shared<ST> *>(tiles + ST * L::STAGE);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int mt = (a.m + F8_BM - 1) / F8_BM, nt = (a.n + BN - 1) / BN, ntiles = mt * nt;
-    const int nk = (a.k + F8_BK - 1) / F8_BK;
+    const int nk = (a.k + KS * F8_BK - 1) / (KS * F8_BK);  // stages of a tile
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < ST; ++s) {
@@ -150,17 +151,22 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
 
     if (warp == 0) {
         if (lane == 0) {
-            int kbg = 0;  // k-blocks issued so far (all tiles)
+            int kbg = 0, s = 0;  // stages filled so far (all tiles), and the next one's place
+            uint32_t ph = 1;     // its parity while it is being emptied
             for (int t = blockIdx.x; t < ntiles && !S.abort_; t += gridDim.x) {
                 int m, n;
                 f8_tile_of(t, mt, nt, m, n);
                 for (int kb = 0; kb < nk; ++kb, ++kbg) {
-                    const int s = kbg % ST;
-                    if (kbg >= ST && !f8_wait(S, &S.empty[s], ((kbg / ST) - 1) & 1u, deadline, a.err)) break;
+                    if (kbg >= ST && !f8_wait(S, &S.empty[s], ph, deadline, a.err)) break;
                     uint8_t *st = tiles + s * L::STAGE;
-                    mbar_arrive_expect_tx(&S.full[s], a.rows_a * F8_BK + L::B);
-                    tma_load_2d(st, &tmA, kb * F8_BK, m * F8_BM, &S.full[s]);
-                    tma_load_2d(st + L::A, &tmB, kb * F8_BK, n * BN, &S.full[s]);
+                    mbar_arrive_expect_tx(&S.full[s], KS * (a.rows_a * F8_BK + L::B));
+#pragma unroll
+                    for (int i = 0; i < KS; ++i) {  // (a block past K is zeros)
+                        const int x = (kb * KS + i) * F8_BK;
+                        tma_load_2d(st + i * L::BLOCK, &tmA, x, m * F8_BM, &S.full[s]);
+                        tma_load_2d(st + i * L::BLOCK + L::A, &tmB, x, n * BN, &S.full[s]);
+                    }
+                    if (++s == ST) s = 0, ph ^= 1u;
                 }
             }
             if (S.abort_) {  // let the copies in flight land before the CTA exits
@@ -171,39 +177,40 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
             }
         }
     } else if (warp == 1) {
-        {  // (the whole warp walks the loop, one lane issues: what the instructions take stays in uniform registers)
-            const bool leader = elect_one();
-            // e4m3 operands (type 0), fp32 accumulators, both K-major
-            constexpr uint32_t kIdesc = idesc_f16(F8_BM, BN);
-            int kbg = 0, lt = 0;
-            bool ok = true;
-            for (int t = blockIdx.x; ok && t < ntiles; t += gridDim.x, ++lt) {
-                const int b = lt & 1;
-                const uint32_t acc = tmem + (uint32_t)b * BN;
-                if (lt >= 2 && !__all_sync(0xffffffffu, f8_wait(S, &S.acc_empty[b], ((lt >> 1) - 1) & 1u, deadline, a.err))) break;
+        // The whole warp walks the loop and one lane issues: what the instructions take stays in uniform registers.  What
+        // stands between two blocks' products counts (32 to 128 cycles each): one wait a stage, descriptors by addition.
+        const bool leader = elect_one();
+        // e4m3 operands (type 0), fp32 accumulators, both K-major
+        constexpr uint32_t kIdesc = idesc_f16(F8_BM, BN);
+        const uint64_t desc = smem_desc_sw128(smem_u32(tiles));
+        auto on = [&](uint32_t bytes) { return (desc & 0xffffffff00000000ull) | (uint32_t)((uint32_t)desc + (bytes >> 4)); };
+        int lt = 0, s = 0;
+        uint32_t ph = 0;
+        bool ok = true;
+        for (int t = blockIdx.x; ok && t < ntiles; t += gridDim.x, ++lt) {
+            const int b = lt & 1;
+            const uint32_t acc = tmem + (uint32_t)b * BN;
+            if (lt >= 2 && !__all_sync(0xffffffffu, f8_wait(S, &S.acc_empty[b], ((lt >> 1) - 1) & 1u, deadline, a.err))) break;
+            for (int kb = 0; kb < nk; ++kb) {
+                ok = __all_sync(0xffffffffu, f8_wait(S, &S.full[s], ph, deadline, a.err));
+                if (!ok) break;
                 tc_fence_after();
-                for (int kb = 0; kb < nk; ++kb, ++kbg) {
-                    const int s = kbg % ST;
-                    if (!__all_sync(0xffffffffu, f8_wait(S, &S.full[s], (kbg / ST) & 1u, deadline, a.err))) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    if (leader) {
-                        const uint32_t at = smem_u32(tiles + s * L::STAGE), bt = at + L::A;
-#pragma unroll
-                        for (int kk = 0; kk < F8_BK / 32; ++kk)  // 32 values = 32 bytes along K per instruction
-                            tc_mma_f8(acc, smem_desc_sw128(at + 32 * kk), smem_desc_sw128(bt + 32 * kk), kIdesc, (kb | kk) != 0);
-                        tc_commit(&S.empty[s]);
-                    }
-                    __syncwarp();
-                }
                 if (leader) {
-                    tc_commit(&S.acc_full[b]);
-                    S.n_acc_[b] = (lt >> 1) + 1;
+#pragma unroll
+                    for (int kk = 0; kk < KS * F8_BK / 32; ++kk) {  // 32 values = 32 bytes along K per instruction
+                        const uint32_t at = (uint32_t)(s * L::STAGE + kk / 4 * L::BLOCK + kk % 4 * 32);
+                        tc_mma_f8(acc, on(at), on(at + L::A), kIdesc, (kb | kk) != 0);
+                    }
+                    tc_commit(&S.empty[s]);
                 }
                 __syncwarp();
+                if (++s == ST) s = 0, ph ^= 1u;
             }
+            if (ok && leader) {
+                tc_commit(&S.acc_full[b]);
+                S.n_acc_[b] = (lt >> 1) + 1;
+            }
+            __syncwarp();
         }
     } else {  // warp w reads TMEM lanes 32 * (w % 4) .. + 31
         const int q = warp & 3;
@@ -285,17 +292,17 @@ bool f8_map(CUtensorMap *map, const void *p, int rows, int k, int box_rows) {
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int BN, int AR>
+template <int BN, int AR, int KS>
 lf_status launch_f8(const void *A, const void *B, F8Args a, int n_sm, cudaStream_t st) {
-    using L = F8Tile<BN, AR>;
+    using L = F8Tile<BN, AR, KS>;
     a.rows_a = a.m >= AR ? AR : (a.m + 7) / 8 * 8;
     CUtensorMap ma, mb;
-    if (!set_smem_once<matmul_f8_kernel<BN, AR>>(L::SMEM) || !f8_map(&ma, A, a.m, a.k, a.rows_a) ||
+    if (!set_smem_once<matmul_f8_kernel<BN, AR, KS>>(L::SMEM) || !f8_map(&ma, A, a.m, a.k, a.rows_a) ||
         !f8_map(&mb, B, a.n, a.k, BN))
         return LF_ERR_CUDA;
     const long long tiles = (((long long)a.m + F8_BM - 1) / F8_BM) * (((long long)a.n + BN - 1) / BN);
     const unsigned grid = (unsigned)(tiles < n_sm ? tiles : n_sm);
-    return launch_pdl(matmul_f8_kernel<BN, AR>, grid, F8_THREADS, L::SMEM, st, ma, mb, a) ? LF_OK : LF_ERR_CUDA;
+    return launch_pdl(matmul_f8_kernel<BN, AR, KS>, grid, F8_THREADS, L::SMEM, st, ma, mb, a) ? LF_OK : LF_ERR_CUDA;
 }
 
 }  // namespace
@@ -324,7 +331,7 @@ extern "C" lf_status lf_matmul_f8(const void *a_device, const float *a_scale_dev
     const lf::F8Args a = {a_scale_device, b_scale_device, c_device, m, n, k, c_dtype, 0, err_device};
     cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
     const long long mt = ((long long)m + 127) / 128;
-    if (mt * ((n + 255) / 256) >= n_sm) return lf::launch_f8<256, 128>(a_device, b_device, a, n_sm, st);
-    if (mt * ((n + 127) / 128) >= n_sm) return lf::launch_f8<128, 128>(a_device, b_device, a, n_sm, st);
-    return m <= 32 ? lf::launch_f8<64, 32>(a_device, b_device, a, n_sm, st) : lf::launch_f8<64, 128>(a_device, b_device, a, n_sm, st);
+    if (mt * ((n + 255) / 256) >= n_sm) return lf::launch_f8<256, 128, 1>(a_device, b_device, a, n_sm, st);
+    if (mt * ((n + 127) / 128) >= n_sm) return lf::launch_f8<128, 128, 2>(a_device, b_device, a, n_sm, st);
+    return m <= 32 ? lf::launch_f8<64, 32, 2>(a_device, b_device, a, n_sm, st) : lf::launch_f8<64, 128, 2>(a_device, b_device, a, n_sm, st);
 }
