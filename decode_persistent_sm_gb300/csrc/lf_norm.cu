@@ -14,11 +14,13 @@
 #include <type_traits>
 
 #include "lf_paged.h"
+#include "lf_ptx.cuh"
 
 namespace lf {
 namespace {
 
 constexpr int kNormMaxThreads = 1024, kNormMaxVecs = 4;  // so at most 32768 columns
+constexpr int kNormWalkRows = 8;
 constexpr float kE4m3Max = 448.f;
 
 struct NormArgs {
@@ -78,6 +80,39 @@ __device__ __forceinline__ void store8(T *p, int n, const float *f) {
         for (int i = 0; i < 8; ++i)
             if (i < n) p[i] = t[i];
     }
+}
+
+// y of one vector of g s, in the output's type.
+template <bool VEC>
+__device__ __forceinline__ void put8(const NormArgs &a, long long at, int n, const float *s, float inv, float scale) {
+    float y[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = s[i] * inv;
+    if (a.out_dtype == LF_E4M3) {
+        if (scale >= 1e-30f) {  // (the scale of a row of tiny values may have no reciprocal)
+            const float per = 1.f / scale;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[i] *= per;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[i] /= scale;
+        }
+        store8<__nv_fp8_e4m3, VEC>(static_cast<__nv_fp8_e4m3 *>(a.out) + at, n, y);
+    } else if (a.out_dtype == LF_F32) {
+        store8<float, VEC>(static_cast<float *>(a.out) + at, n, y);
+    } else if (a.out_dtype == LF_F16) {
+        store8<__half, VEC>(static_cast<__half *>(a.out) + at, n, y);
+    } else {
+        store8<__nv_bfloat16, VEC>(static_cast<__nv_bfloat16 *>(a.out) + at, n, y);
+    }
+}
+
+// The row's 1 / rms and 8-bit scale from its sum of squares and max |g s|.
+__device__ __forceinline__ float2 row_scales(const NormArgs &a, float sq, float mx) {
+    const float rms = sqrtf(sq / (float)a.cols + a.eps), inv = 1.f / rms;
+    float scale = mx * inv / kE4m3Max;
+    if (!(scale > 0.f && scale < INFINITY)) scale = 1.f;  // nothing but zeros, or a NaN or infinity somewhere
+    return make_float2(inv, scale);
 }
 
 // A NaN among the values is the maximum.
@@ -158,55 +193,154 @@ __global__ void __launch_bounds__(kNormMaxThreads) add_rmsnorm_kernel(const Norm
         }
     }
     if (!live) return;
-    const float rms = sqrtf(sq / (float)a.cols + a.eps), inv = 1.f / rms;
-    float scale = mx * inv / kE4m3Max;
-    if (!(scale > 0.f && scale < INFINITY)) scale = 1.f;  // nothing but zeros, or a NaN or infinity somewhere
-    if (a.out_dtype == LF_E4M3 && t == 0) a.scale[row] = scale;
+    const float2 by = row_scales(a, sq, mx);
+    if (a.out_dtype == LF_E4M3 && t == 0) a.scale[row] = by.y;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+        if (left(v) > 0) put8<VEC>(a, row * a.ld_out + 8 * (t + v * a.tpr), left(v), s[v], by.x, by.y);
+}
+
+// The same for many rows of whole vectors: a block walks its rows with the next two on
+// their way.  Each thread copies its own vectors into its own places of shared memory
+// and reads them back, so that enough is in flight without registers and a
+// row costs one barrier; the gain stays in registers.
+constexpr int kNormStages = 2;
+template <typename TX, typename TR, int V>
+__global__ void __launch_bounds__(kNormMaxThreads) add_rmsnorm_rows_kernel(const NormArgs a) {
+    constexpr int PX = sizeof(TX) / 2, PR = sizeof(TR) / 2, SLOT = V * (PX + PR);  // 16-byte pieces
+    extern __shared__ __align__(16) uint4 norm_ring[];                            // [stage][SLOT][threads]
+    __shared__ float2 part[2][kNormMaxThreads / 32];
+    const int t = threadIdx.x, warps = a.tpr >> 5;
+    pdl_wait();
+    pdl_trigger();
+    auto fetch = [&](long long row, int stage) {
+        if (row < a.rows) {
+            uint4 *to = norm_ring + (stage * SLOT) * a.tpr + t;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const int at = 8 * (t + v * a.tpr);
+                if (at >= a.cols) continue;
+                const TX *x = static_cast<const TX *>(a.x) + row * a.ld_x + at;
+                const TR *r = static_cast<const TR *>(a.res) + row * a.ld_res + at;
+#pragma unroll
+                for (int i = 0; i < PX; ++i) cp_async16(to + (v * (PX + PR) + i) * a.tpr, reinterpret_cast<const uint4 *>(x) + i);
+                if (a.res) {
+#pragma unroll
+                    for (int i = 0; i < PR; ++i)
+                        cp_async16(to + (v * (PX + PR) + PX + i) * a.tpr, reinterpret_cast<const uint4 *>(r) + i);
+                }
+            }
+        }
+        cp_async_commit();
+    };
+#pragma unroll
+    for (int k = 0; k < kNormStages - 1; ++k) fetch(blockIdx.x + (long long)k * gridDim.x, k);
+    float g[V][8];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        const int n = left(v);
-        if (n <= 0) continue;
-        const long long at = row * a.ld_out + 8 * (t + v * a.tpr);
-        float y[8];
+        const int at = 8 * (t + v * a.tpr);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = s[v][i] * inv;
-        if (a.out_dtype == LF_E4M3) {
-            // (a division: the scale of a row of tiny values has no reciprocal)
+        for (int i = 0; i < 8; ++i) g[v][i] = 1.f;
+        if (at >= a.cols || !a.gain) continue;
+        auto take = [&](auto *p) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] /= scale;
-            store8<__nv_fp8_e4m3, VEC>(static_cast<__nv_fp8_e4m3 *>(a.out) + at, n, y);
-        } else if (a.out_dtype == LF_F32) {
-            store8<float, VEC>(static_cast<float *>(a.out) + at, n, y);
-        } else if (a.out_dtype == LF_F16) {
-            store8<__half, VEC>(static_cast<__half *>(a.out) + at, n, y);
-        } else {
-            store8<__nv_bfloat16, VEC>(static_cast<__nv_bfloat16 *>(a.out) + at, n, y);
+            for (int i = 0; i < 8; ++i) g[v][i] = to_f(p[at + i]);
+        };
+        if (a.gain_dtype == LF_F32)
+            take(static_cast<const float *>(a.gain));
+        else if (a.gain_dtype == LF_F16)
+            take(static_cast<const __half *>(a.gain));
+        else
+            take(static_cast<const __nv_bfloat16 *>(a.gain));
+    }
+    int stage = 0, turn = 0;
+    for (long long row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
+        fetch(row + (long long)(kNormStages - 1) * gridDim.x, stage == 0 ? kNormStages - 1 : stage - 1);
+        asm volatile("cp.async.wait_group %0;" ::"n"(kNormStages - 1) : "memory");
+        const uint4 *from = norm_ring + (stage * SLOT) * a.tpr + t;
+        stage = stage + 1 == kNormStages ? 0 : stage + 1;
+        float s[V][8], sq = 0.f, mx = 0.f;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int at = 8 * (t + v * a.tpr);
+            __align__(16) TX x[8];
+            __align__(16) TR r[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s[v][i] = 0.f;
+            if (at >= a.cols) continue;
+#pragma unroll
+            for (int i = 0; i < PX; ++i) reinterpret_cast<uint4 *>(x)[i] = from[(v * (PX + PR) + i) * a.tpr];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s[v][i] = to_f(x[i]);
+            if (a.res) {
+#pragma unroll
+                for (int i = 0; i < PR; ++i) reinterpret_cast<uint4 *>(r)[i] = from[(v * (PX + PR) + PX + i) * a.tpr];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) s[v][i] += to_f(r[i]);
+            }
+            if (a.sum) store8<TR, true>(static_cast<TR *>(a.sum) + row * a.ld_sum + at, 8, s[v]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                sq += s[v][i] * s[v][i];
+                s[v][i] *= g[v][i];
+                mx = max_nan(mx, fabsf(s[v][i]));
+            }
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            sq += __shfl_xor_sync(0xffffffffu, sq, o);
+            mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        }
+        if ((t & 31) == 0) part[turn][t >> 5] = make_float2(sq, mx);
+        __syncthreads();  // (the other half of `part` is free: whoever read it has passed this row's barrier's predecessor)
+        sq = mx = 0.f;
+        for (int w = 0; w < warps; ++w) {
+            const float2 p = part[turn][w];
+            sq += p.x;
+            mx = max_nan(mx, p.y);
+        }
+        const float2 by = row_scales(a, sq, mx);
+        if (a.out_dtype == LF_E4M3 && t == 0) a.scale[row] = by.y;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int at = 8 * (t + v * a.tpr);
+            if (at < a.cols) put8<true>(a, row * a.ld_out + at, 8, s[v], by.x, by.y);
         }
     }
 }
 
 template <typename TX, typename TR, bool VEC>
-bool launch_norm(NormArgs a, cudaStream_t st) {
+bool launch_norm(NormArgs a, int n_sm, cudaStream_t st) {
     const int vecs = (a.cols + 7) / 8;
     // two vectors a thread, four where a block of 1024 threads needs them
     const int v = vecs > 2 * kNormMaxThreads ? 4 : 2;
     a.tpr = ((vecs + v - 1) / v + 31) / 32 * 32;
     a.rpb = std::max(1, 128 / a.tpr);
+    if constexpr (VEC && sizeof(TX) == 2 && sizeof(TR) == 2) {
+        // from a few rows per SM on the walk that keeps rows on their way, where a block of at most 512 threads holds a row
+        if (v == 2 && a.rpb == 1 && a.tpr <= 512 && a.rows >= kNormWalkRows * n_sm) {
+            const int smem = kNormStages * a.tpr * 2 * 8 * (int)(sizeof(TX) + sizeof(TR));
+            const int ctas = std::max(1, std::min(227 * 1024 / (smem + 2048), 1024 / a.tpr));
+            return set_smem_once<add_rmsnorm_rows_kernel<TX, TR, 2>>(kNormStages * 512 * 2 * 8 * (int)(sizeof(TX) + sizeof(TR))) &&
+                   launch_pdl(add_rmsnorm_rows_kernel<TX, TR, 2>, (unsigned)std::min<long long>(a.rows, (long long)ctas * n_sm),
+                              (unsigned)a.tpr, (size_t)smem, st, a);
+        }
+    }
     const unsigned grid = (unsigned)(((long long)a.rows + a.rpb - 1) / a.rpb), threads = (unsigned)(a.tpr * a.rpb);
     return v == 2 ? launch_pdl(add_rmsnorm_kernel<TX, TR, 2, VEC>, grid, threads, 0, st, a)
                   : launch_pdl(add_rmsnorm_kernel<TX, TR, 4, VEC>, grid, threads, 0, st, a);
 }
 
 template <typename TX, typename TR>
-bool launch_norm_vec(const NormArgs &a, bool vec, cudaStream_t st) {
-    return vec ? launch_norm<TX, TR, true>(a, st) : launch_norm<TX, TR, false>(a, st);
+bool launch_norm_vec(const NormArgs &a, bool vec, int n_sm, cudaStream_t st) {
+    return vec ? launch_norm<TX, TR, true>(a, n_sm, st) : launch_norm<TX, TR, false>(a, n_sm, st);
 }
 
 template <typename TX>
-bool launch_norm_res(const NormArgs &a, int res_dtype, bool vec, cudaStream_t st) {
-    return res_dtype == LF_F32   ? launch_norm_vec<TX, float>(a, vec, st)
-           : res_dtype == LF_F16 ? launch_norm_vec<TX, __half>(a, vec, st)
-                                 : launch_norm_vec<TX, __nv_bfloat16>(a, vec, st);
+bool launch_norm_res(const NormArgs &a, int res_dtype, bool vec, int n_sm, cudaStream_t st) {
+    return res_dtype == LF_F32   ? launch_norm_vec<TX, float>(a, vec, n_sm, st)
+           : res_dtype == LF_F16 ? launch_norm_vec<TX, __half>(a, vec, n_sm, st)
+                                 : launch_norm_vec<TX, __nv_bfloat16>(a, vec, n_sm, st);
 }
 
 }  // namespace
@@ -236,6 +370,12 @@ extern "C" lf_status lf_add_rmsnorm(const void *x_device, int x_dtype, int64_t l
     if (out_device == residual_device && (residual_dtype != out_dtype || ld_residual != ld_out)) return LF_ERR_INVALID_ARG;
     if (cols > lf::kNormMaxThreads * lf::kNormMaxVecs * 8) return LF_ERR_UNSUPPORTED;
     if (rows == 0) return LF_OK;
+    int dev = 0, n_sm = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n_sm < 1) {
+        (void)cudaGetLastError();
+        return LF_ERR_CUDA;
+    }
     lf::NormArgs a = {x_device, residual_device, gain_device, sum_device, out_device, scale_device, ld_x, ld_residual,
                       ld_sum,   ld_out,          gain_dtype,  out_dtype,  rows,       cols,         eps,  0, 0};
     // 16-byte accesses (8 bytes of an 8-bit output) where every row allows them
@@ -245,8 +385,8 @@ extern "C" lf_status lf_add_rmsnorm(const void *x_device, int x_dtype, int64_t l
     const bool vec = cols % 8 == 0 && fits(x_device, ld_x, bx) && fits(residual_device, ld_residual, br) &&
                      fits(sum_device, ld_sum, br) && fits(gain_device, 0, bg) && fits(out_device, ld_out, bo);
     cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
-    const bool ok = x_dtype == LF_F32   ? lf::launch_norm_res<float>(a, residual_dtype, vec, st)
-                    : x_dtype == LF_F16 ? lf::launch_norm_res<__half>(a, residual_dtype, vec, st)
-                                        : lf::launch_norm_res<__nv_bfloat16>(a, residual_dtype, vec, st);
+    const bool ok = x_dtype == LF_F32   ? lf::launch_norm_res<float>(a, residual_dtype, vec, n_sm, st)
+                    : x_dtype == LF_F16 ? lf::launch_norm_res<__half>(a, residual_dtype, vec, n_sm, st)
+                                        : lf::launch_norm_res<__nv_bfloat16>(a, residual_dtype, vec, n_sm, st);
     return ok ? LF_OK : LF_ERR_CUDA;
 }

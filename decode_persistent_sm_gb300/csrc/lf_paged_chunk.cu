@@ -51,6 +51,12 @@ __device__ __forceinline__ bool odd_one(uint32_t h) {
     constexpr uint32_t e = std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u;
     return (h & e) == e;
 }
+// One of a word's two is.
+template <typename T>
+__device__ __forceinline__ bool odd_word(uint32_t w) {
+    constexpr uint32_t one = std::is_same<T, __half>::value ? 0x04000400u : 0x00800080u;  // (carries out of a full exponent)
+    return (((w & 0x7fff7fffu) + one) & 0x80008000u) != 0;
+}
 
 // WR warps side by side in rows, 4 / WR in keys: items of up to 16 WR rows.
 template <typename T, int DH, int WR>
@@ -321,15 +327,15 @@ class ChunkWalker {
             uint8_t *v = stage0 + (size_t)s * 2 * L::TILE + L::TILE;
             for (int x = tid; x < L::TILE / 16; x += CK_THREADS) {
                 uint4 y = reinterpret_cast<uint4 *>(v)[x];
+                if (!(odd_word<T>(y.x) | odd_word<T>(y.y) | odd_word<T>(y.z) | odd_word<T>(y.w))) continue;
                 uint32_t *p = reinterpret_cast<uint32_t *>(&y);
-                bool found = false;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    if (odd_one<T>(p[i] & 0xffffu)) p[i] &= 0xffff0000u, found = true;
-                    if (odd_one<T>(p[i] >> 16)) p[i] &= 0xffffu, found = true;
+                    if (odd_one<T>(p[i] & 0xffffu)) p[i] &= 0xffff0000u;
+                    if (odd_one<T>(p[i] >> 16)) p[i] &= 0xffffu;
                 }
-                if (found) reinterpret_cast<uint4 *>(v)[x] = y;
-                odd |= found;
+                reinterpret_cast<uint4 *>(v)[x] = y;
+                odd = true;
             }
             odd = __syncthreads_or(odd);
         }

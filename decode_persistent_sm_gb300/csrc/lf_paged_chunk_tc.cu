@@ -37,13 +37,14 @@ namespace {
 constexpr int C_THREADS = 320;         // copy warp, MMA warp, 2 x 4 softmax warps
 constexpr uint32_t C_TMEM_COLS = 512;  // S / P of row tile x at 128 x, O at 256 + 128 x
 constexpr uint32_t C_O = 256;
+constexpr int kLeast = 2;              // key tiles of a CTA, at least
 constexpr int C_FIRST = 96;            // keys of P's first piece (a multiple of 32)
 constexpr unsigned long long kChunkTimeoutNs = 2000000000ull;
 
 // Every barrier completes once per use of what it guards, and no waiter can
 // fall two phases behind, so parity waits are unambiguous.
 struct CtShared {
-    uint64_t bq[2];     // Q of row tile x written (128 arrivals)
+    uint64_t bq[2];     // Q of row tile x loaded
     uint64_t bk0;       // K of the first tile loaded
     uint64_t bl[2];     // V of tile p and K of tile p + 1 loaded (p = 0, 2, .. and 1, 3, ..)
     uint64_t bf[2];     // done: the S products of tile p and the P V products of tile p - 1 (p = 0, 2, .. and 1, 3, ..)
@@ -57,9 +58,10 @@ struct CtShared {
     volatile int odd_[8];   // item it's masked tiles hold values that are not finite: odd_[it & 7] is it + 1
 };
 
-__device__ __forceinline__ bool await_phase(CtShared &S, uint64_t *bar, uint32_t parity, uint64_t deadline,
-                                            uint32_t *err) {
+// (The limit counts from the first probe that fails: a wait that is over costs no look at the clock.)
+__device__ __forceinline__ bool await_phase(CtShared &S, uint64_t *bar, uint32_t parity, uint32_t *err) {
     if (mbar_test_wait(bar, parity)) return true;
+    const uint64_t deadline = global_timer_ns() + kChunkTimeoutNs;
     while (!mbar_try_wait(bar, parity)) {
         if (S.abort_) return false;
         if (global_timer_ns() > deadline) {
@@ -88,14 +90,11 @@ __device__ __forceinline__ float2 add2(float2 x, float2 y) {
     return *reinterpret_cast<float2 *>(&r);
 }
 
-// Two 16-bit values of a word: those that are infinite or NaN become 0; true if there was one.
+// Bits 15 and 31: of the two 16-bit values of a word, those that are infinite or NaN.
 template <typename T>
-__device__ __forceinline__ bool drop_odd(uint32_t &w) {
-    constexpr uint32_t e = std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u;
-    bool found = false;
-    if ((w & e) == e) w &= 0xffff0000u, found = true;
-    if ((w & (e << 16)) == (e << 16)) w &= 0xffffu, found = true;
-    return found;
+__device__ __forceinline__ uint32_t odd_bits(uint32_t w) {
+    constexpr uint32_t one = std::is_same<T, __half>::value ? 0x04000400u : 0x00800080u;  // (carries out of a full exponent)
+    return ((w & 0x7fff7fffu) + one) & 0x80008000u;
 }
 
 template <int DH>
@@ -104,14 +103,17 @@ struct CtSmem {
     static constexpr int TILE = HALVES * T_HALF;  // one row tile of Q, one buffer of K or V
     static constexpr int Q = 0, K = 2 * TILE, V = 4 * TILE, TILES = 6 * TILE;
     static constexpr int CUM = TILES + 256;
-    static constexpr int BYTES = CUM + (1024 + 4) * 4 + 1024;
+    static constexpr int OUT = CUM + (1024 + 4) * 4;  // 32 rows of 64 bytes of each softmax warp, on their way out
+    static constexpr int OUT_ROW = 80;                // (apart so that 8 rows lie in 8 different groups of banks)
+    static constexpr int WORK = OUT + 8 * 32 * OUT_ROW;  // two items of each softmax warp
+    static constexpr int BYTES = WORK + 16 * (int)sizeof(ChunkWork) + 1024;
     static_assert(sizeof(CtShared) <= 256, "the barriers' place");
 };
 
 template <typename T, int DH>
 __global__ void __launch_bounds__(C_THREADS, 1)
     paged_chunk_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                          const ChunkArgs a) {
+                          const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ ChunkArgs a) {
     using L = CtSmem<DH>;
     extern __shared__ __align__(1024) uint8_t ct_raw[];
     uint8_t *t = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(ct_raw) + 1023) & ~uintptr_t(1023));
@@ -121,7 +123,7 @@ __global__ void __launch_bounds__(C_THREADS, 1)
 
     if (threadIdx.x == 0) {
         for (int b = 0; b < 2; ++b) {
-            mbar_init(&S.bq[b], 128);
+            mbar_init(&S.bq[b], 1);
             mbar_init(&S.bl[b], 1);
             mbar_init(&S.bf[b], 1);
             mbar_init(&S.bs[b], 1);
@@ -137,15 +139,17 @@ __global__ void __launch_bounds__(C_THREADS, 1)
         fence_barrier_init();
         tma_prefetch_map(&tmK);
         tma_prefetch_map(&tmV);
+        tma_prefetch_map(&tmQ);
     }
     pdl_wait();
     pdl_trigger();
     const int total = chunk_plan<kTcKeys>(a, cum);
-    const Shares sh(total, gridDim.x);
+    // (a share is at least kLeast tiles: below, the partials would cost more than the tiles)
+    const int ctas = min((int)gridDim.x, max(1, (total + kLeast - 1) / kLeast));
+    const Shares sh(total, ctas);
     if (threadIdx.x == 0) a.joins[cta].parts = 0;
-    if (cta >= min(total, (int)gridDim.x)) return;  // (the whole block, before it holds any TMEM)
+    if (cta >= min(total, ctas)) return;  // (the whole block, before it holds any TMEM)
     const int u0 = sh.begin(cta), u1 = sh.begin(cta + 1), n = u1 - u0;
-    const uint64_t deadline = global_timer_ns() + kChunkTimeoutNs;
     const int tx = a.toks / 2;  // tokens of a row tile
     ChunkWork w = chunk_place<kTcKeys>(a, cum, u0);  // every warp walks the list for itself
     if (warp == 1) tc_alloc(&S.tmem, C_TMEM_COLS);
@@ -181,19 +185,44 @@ __global__ void __launch_bounds__(C_THREADS, 1)
                 for (int i = 0; i < L::HALVES; ++i)
                     tma_load_4d(t + tile_at + lane * box * 128 + i * T_HALF, map, 64 * i, x.row, x.h, x.page, bar);
         };
+        // An item's queries, a box of (64 dims, heads of the group, tokens) for each half of a row tile: its rows lie as the
+        // products want them (rows of tokens behind the item's are of others, or zeros past the last: nobody reads their
+        // results).
+        struct Queries {
+            int head, row, nx;
+        };
+        auto queries_of = [&] { return Queries{w.h * a.group, w.ch.row0 + w.tok, w.toks > tx ? 2 : 1}; };
+        auto load_queries = [&](const Queries &q) {
+            if (lane < q.nx) {
+                mbar_arrive_expect_tx(&S.bq[lane], L::HALVES * 64 * 2 * a.group * tx);
+                for (int i = 0; i < L::HALVES; ++i)
+                    tma_load_3d(t + L::Q + lane * L::TILE + i * T_HALF, &tmQ, 64 * i, q.head, q.row + lane * tx, &S.bq[lane]);
+            }
+            __syncwarp();
+        };
         Box now = place(), then = now;
+        Queries q_now = queries_of(), q_then = q_now;
+        bool fresh_now = true, fresh_then = false;  // tile j, tile j + 1 begin an item
+        int loads[2] = {0, 0};                      // on bq so far
         if (lane == 0) mbar_arrive_expect_tx(&S.bk0, L::TILE);
         __syncwarp();
         load(L::K, &tmK, now, &S.bk0);
         bool ok = true;
         for (int j = 0; j < n; ++j) {  // V of tile j and K of the next
             if (j + 1 < n) {
-                chunk_advance<kTcKeys>(a, cum, w);
+                fresh_then = chunk_advance<kTcKeys>(a, cum, w);
                 then = place();
+                if (fresh_then) q_then = queries_of();
             }
-            // their buffers are free once the S products of tile j - 1 and the P V products of tile j - 2 are done
-            if (j >= 1) ok = await_phase(S, &S.bf[(j - 1) & 1], ((j - 1) >> 1) & 1u, deadline, a.err);
+            // their buffers are free once the S products of tile j - 1 and the P V products of tile j - 2 are done, and so
+            // are the queries of the item before
+            if (j >= 1) ok = await_phase(S, &S.bf[(j - 1) & 1], ((j - 1) >> 1) & 1u, a.err);
             if (!__all_sync(0xffffffffu, ok)) break;
+            if (fresh_now) {
+                load_queries(q_now);
+                ++loads[0];
+                loads[1] += q_now.nx > 1;
+            }
             uint64_t *bar = &S.bl[j & 1];
             if (lane == 0) mbar_arrive_expect_tx(bar, j + 1 < n ? 2 * L::TILE : L::TILE);
             __syncwarp();
@@ -201,11 +230,16 @@ __global__ void __launch_bounds__(C_THREADS, 1)
             if (j + 1 < n) load(L::K + ((j + 1) & 1) * L::TILE, &tmK, then, bar);
             ++started;
             now = then;
+            q_now = q_then;
+            fresh_now = fresh_then;
         }
         if (S.abort_ && lane == 0) {  // let the copies in flight land
             const uint64_t dl = global_timer_ns() + 1000000000ull;
             while (!mbar_try_wait(&S.bk0, 0) && global_timer_ns() < dl) {
             }
+            for (int x = 0; x < 2; ++x)
+                while (loads[x] > 0 && !mbar_try_wait(&S.bq[x], (loads[x] - 1) & 1u) && global_timer_ns() < dl) {
+                }
             for (int i = max(0, started - 2); i < started; ++i)
                 while (!mbar_try_wait(&S.bl[i & 1], (i >> 1) & 1u) && global_timer_ns() < dl) {
                 }
@@ -238,7 +272,7 @@ __global__ void __launch_bounds__(C_THREADS, 1)
                               on(v, (uint32_t)kk * 16 * 128), kIdescO, (!first || kk > 0) ? 1u : 0u);
         };
         auto await = [&](uint64_t *bar, uint32_t parity) {
-            const bool got = __all_sync(0xffffffffu, await_phase(S, bar, parity, deadline, a.err));
+            const bool got = __all_sync(0xffffffffu, await_phase(S, bar, parity, a.err));
             tc_fence_after();
             return got;
         };
@@ -307,65 +341,71 @@ __global__ void __launch_bounds__(C_THREADS, 1)
         const uint32_t ts = trow + (uint32_t)x * kTcKeys, to = trow + C_O + (uint32_t)x * 128;
         const float sc2 = a.scale_log2;
         constexpr float kLazy = 8.f;  // log2 of the largest P before the max moves
+        // this item and the next one, in shared memory: the row's scores need the registers
+        ChunkWork *const works = reinterpret_cast<ChunkWork *>(t + L::WORK) + 2 * (warp - 2);
+        if (lane == 0) works[0] = w;
+        __syncwarp();
         int left = n, at_tile = 0, ns = 0, no = 0;  // ns, no: uses of bs and bo so far
         bool ok = true, whole = w.tile == 0;        // whole: this CTA has begun the item
-        // Q of this thread's row of an item into the swizzled tile
-        auto load_q = [&](const ChunkWork &y) {
-            const int rows = min(tx, y.toks - x * tx) * a.group;
-            if (rows <= 0) return;
-            uint8_t *qs = t + L::Q + x * L::TILE;
-            const int tok = row / a.group;
-            const T *src = row < rows ? static_cast<const T *>(a.q) + ((long long)y.ch.row0 + y.tok + x * tx + tok) * a.ld_q +
-                                            (long long)(y.h * a.group + row - tok * a.group) * DH
-                                      : nullptr;
-            uint4 v[DH / 8];  // (all loads before the first store)
-#pragma unroll
-            for (int c = 0; c < DH / 8; ++c)
-                v[c] = src ? reinterpret_cast<const uint4 *>(src)[c] : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-            for (int c = 0; c < DH / 8; ++c)
-                *reinterpret_cast<uint4 *>(qs + (c >> 3) * T_HALF + sw128_offset(row, (c & 7) * 8)) = v[c];
-            fence_proxy_async_shared();
-            mbar_arrive(&S.bq[x]);
-        };
-        load_q(w);
         for (int it = 0; ok && left > 0; ++it) {
-            const int count = min(left, w.tiles - w.tile);  // tiles of this item in this CTA
-            const bool ends = w.tile + count == w.tiles;
-            if (x == 0 && row == 0 && count == left) a.joins[cta] = chunk_join(a, w, sh, cta, u1, w.tile + count, whole);
-            const int toks = min(tx, w.toks - x * tx), rows = toks * a.group;
-            if (toks > 0) {
-                const int tok = min(row, rows - 1) / a.group;
-                const bool mine = row < rows, warp_used = 32 * quarter < rows;
-                const long long q_row = (long long)w.ch.row0 + w.tok + x * tx + tok;
-                const int head = w.h * a.group + (row - tok * a.group);
-                const int pos = mine ? w.ch.base + w.tok + x * tx + tok : INT_MIN;
-                // what every row of the item sees: up to its first token, from its last one's window on
-                const int first_pos = w.ch.base + w.tok, last_pos = first_pos + w.toks - 1;
+            const ChunkWork &y = works[it & 1];
+            auto next_item = [&] {
+                if (lane == 0) {
+                    ChunkWork z = y;
+                    z.tile = z.tiles - 1;
+                    chunk_advance<kTcKeys>(a, cum, z);
+                    works[(it + 1) & 1] = z;
+                }
+                __syncwarp();
+            };
+            const int count = min(left, y.tiles - y.tile);  // tiles of this item in this CTA
+            if (x == 0 && row == 0 && count == left) a.joins[cta] = chunk_join(a, y, sh, cta, u1, y.tile + count, whole);
+            const int rows = min(tx, y.toks - x * tx) * a.group;
+            const bool warp_used = 32 * quarter < rows;
+            if (rows > 0) {
+                const int j00 = (y.kt0 + y.tile) * kTcKeys;  // the first tile's first position
+                // tiles that every row of the item sees whole: up to its first token, from its last one's window on
+                const int first_pos = y.ch.base + y.tok, last_pos = first_pos + y.toks - 1;
+                const int full_to = (max(first_pos + 1, 0) >> 7) - (j00 >> 7);
+                const int full_from = a.window == 0 || last_pos < a.window ? 0 : ((last_pos - a.window) >> 7) + 1 - (j00 >> 7);
+                static_assert(kTcKeys == 128, "shifts above");
+                const int pos = row < rows ? first_pos + x * tx + quotient(row, a.group) - j00 : INT_MIN;  // from there on
+                const int lo = y.k.lo - j00, hi = y.k.hi - j00;
                 float m2 = -INFINITY, l = 0.f;
                 for (int j = 0; j < count; ++j, ++ns) {
-                    const int j0 = (w.kt0 + w.tile + j) * kTcKeys;
-                    const bool full = j0 + kTcKeys - 1 <= first_pos && (a.window == 0 || j0 > (long long)last_pos - a.window);
+                    const bool full = j >= full_from && j < full_to;
                     if (!full && x == 0) {  // V of this tile: a key per thread
-                        const int vj = at_tile + j;
-                        ok = ok && await_phase(S, &S.bl[vj & 1], (vj >> 1) & 1u, deadline, a.err);
+                        const int vj = at_tile + j, key = j * kTcKeys + row;
+                        ok = ok && await_phase(S, &S.bl[vj & 1], (vj >> 1) & 1u, a.err);
                         if (ok) {
-                            const bool none = j0 + row < w.k.lo || j0 + row >= w.k.hi;
+                            const bool none = key < lo || key >= hi;
                             uint8_t *v = t + L::V + (vj & 1) * L::TILE + row * 128;
-                            bool odd = false;
-#pragma unroll 4
-                            for (int i = 0; i < DH / 8; ++i) {  // (lanes begin at different pieces: different banks)
-                                uint4 *p = reinterpret_cast<uint4 *>(v + (i >> 3) * T_HALF + (((i & 7) ^ (lane & 7)) << 4));
-                                uint4 y = none ? make_uint4(0u, 0u, 0u, 0u) : *p;
-                                const bool found = drop_odd<T>(y.x) | drop_odd<T>(y.y) | drop_odd<T>(y.z) | drop_odd<T>(y.w);
-                                if (none || found) *p = y;
-                                odd |= found;
+                            uint32_t odd = 0;
+                            if (none) {
+#pragma unroll
+                                for (int i = 0; i < DH / 8; ++i)  // (lanes begin at different pieces: different banks)
+                                    *reinterpret_cast<uint4 *>(v + (i >> 3) * T_HALF + (((i & 7) ^ (lane & 7)) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+                            } else {
+                                uint4 z[DH / 8];
+#pragma unroll
+                                for (int i = 0; i < DH / 8; ++i)
+                                    z[i] = *reinterpret_cast<const uint4 *>(v + (i >> 3) * T_HALF + (((i & 7) ^ (lane & 7)) << 4));
+#pragma unroll
+                                for (int i = 0; i < DH / 8; ++i)
+                                    odd |= odd_bits<T>(z[i].x) | odd_bits<T>(z[i].y) | odd_bits<T>(z[i].z) | odd_bits<T>(z[i].w);
+                                if (odd) {
+                                    uint16_t *h = reinterpret_cast<uint16_t *>(v);
+                                    for (int i = 0; i < DH; ++i) {
+                                        uint16_t &e = h[(i >> 6) * (T_HALF / 2) + (i & 63)];
+                                        if (odd_bits<T>(e)) e = 0;
+                                    }
+                                }
                             }
                             if (odd) S.odd_[it & 7] = it + 1;
                             fence_proxy_async_shared();
                         }
                     }
-                    ok = __all_sync(0xffffffffu, ok && await_phase(S, &S.bs[x], ns & 1u, deadline, a.err));
+                    ok = __all_sync(0xffffffffu, ok && await_phase(S, &S.bs[x], ns & 1u, a.err));
                     if (!ok) break;
                     tc_fence_after();
                     if (!warp_used) {  // (rows of nobody: whatever their P is)
@@ -382,10 +422,14 @@ __global__ void __launch_bounds__(C_THREADS, 1)
 #pragma unroll
                     for (int c0 = 0; c0 < kTcKeys; c0 += 32) tc_wait_ld32(ri + c0);
                     if (!full) {  // this row sees keys c with clo < c <= chi
-                        const int chi = pos < j0 ? -1 : min(pos - j0, kTcKeys);
-                        const int clo = a.window == 0 ? -1 : (int)max(-1ll, min((long long)kTcKeys, (long long)pos - a.window - j0));
+                        const int chi = pos < j * kTcKeys ? -1 : min(pos - j * kTcKeys, kTcKeys);
 #pragma unroll
-                        for (int c = 0; c < kTcKeys; ++c) ri[c] = c <= chi && c > clo ? ri[c] : 0xff800000u;  // -inf
+                        for (int c = 0; c < kTcKeys; ++c) ri[c] = c <= chi ? ri[c] : 0xff800000u;  // -inf
+                        if (a.window > 0) {
+                            const int clo = (int)max(-1ll, min((long long)kTcKeys, (long long)pos - a.window - j * kTcKeys));
+#pragma unroll
+                            for (int c = 0; c < kTcKeys; ++c) ri[c] = c > clo ? ri[c] : 0xff800000u;
+                        }
                     }
                     // the tile's max of the row in eight independent chains of three-input maxima
                     float mp[8];
@@ -441,75 +485,92 @@ __global__ void __launch_bounds__(C_THREADS, 1)
                     const float2 s2 = add2(ls[0], ls[1]);
                     l += s2.x + s2.y;
                 }
-                // the next item's queries: the products with this one's are done (S of its last tile was awaited), and
-                // O is not written again before this thread hands over the next item's first P
-                if (ok && left > count) {
-                    ChunkWork y = w;
-                    y.tile = y.tiles - 1;
-                    chunk_advance<kTcKeys>(a, cum, y);
-                    load_q(y);
-                }
-                // the row's result or partial, once the last P V is done
-                if (ok) ok = __all_sync(0xffffffffu, await_phase(S, &S.bo[x], no++ & 1u, deadline, a.err));
+                // the rows' result or partial, once the last P V is done; what needs no wait first
+                const bool odd = S.odd_[it & 7] == it + 1, result = whole && y.tile + count == y.tiles;
+                const int tok = quotient(min(row, rows - 1), a.group);
+                const bool mine = row < rows;
+                const long long q_row = (long long)y.ch.row0 + y.tok + x * tx + tok;
+                const int head = y.h * a.group + (row - tok * a.group);
+                const long long at = (long long)(2 * cta + (whole ? 1 : 0)) * a.slot_rows + x * tx * a.group + row;
+                const long long dst = !mine ? -1 : result ? q_row * a.ld_out + (long long)head * DH : at * DH;
+                // rows leave through shared memory: 64 bytes of a row to four neighbouring lanes
+                long long to4[4];  // of the rows 8 k + lane / 4
+#pragma unroll
+                for (int k = 0; k < 4; ++k) to4[k] = __shfl_sync(0xffffffffu, dst, 8 * k + lane / 4);
+                if (left > count) next_item();
+                if (ok) ok = __all_sync(0xffffffffu, await_phase(S, &S.bo[x], no++ & 1u, a.err));
                 if (ok && warp_used) {
                     tc_fence_after();
-                    const bool odd = S.odd_[it & 7] == it + 1, result = whole && ends;
-                    const float inv = inverse(l);
-                    const long long slot = (long long)(2 * cta + (whole ? 1 : 0)) * a.slot_rows + x * tx * a.group + row;
-                    const uint64_t keep = policy_evict_last();
-#pragma unroll 1
-                    for (int c0 = 0; c0 < DH; c0 += 32) {
-                        float v[32];
-                        tc_ld32(to + (uint32_t)c0, v);
-                        if (odd && mine) {  // what is not finite reaches those who see it
-                            for (int j = 0; j < count * kTcKeys; ++j) {
-                                const int p = (w.kt0 + w.tile) * kTcKeys + j, p0 = p & ~(kTcKeys - 1);
-                                if (p0 + kTcKeys - 1 <= first_pos && (a.window == 0 || p0 > (long long)last_pos - a.window)) continue;
-                                if (p > pos || p < w.k.lo || (a.window > 0 && p <= (long long)pos - a.window)) continue;
-                                const int page = a.kv.table[(long long)w.b * a.kv.max_pages + (p >> a.kv.ps_log2)];
-                                if (page < 0 || page >= a.kv.n_pages) continue;
-                                const T *src = static_cast<const T *>(a.kv.v) + page * a.kv.page_stride +
-                                               ((((long long)w.h << a.kv.ps_log2) + (p & ((1 << a.kv.ps_log2) - 1))) * DH) + c0;
+                    float v[DH];
+                    uint32_t *vi = reinterpret_cast<uint32_t *>(v);
 #pragma unroll
-                                for (int i = 0; i < 32; ++i) {
-                                    const float f = (float)src[i];
-                                    if (!(fabsf(f) < INFINITY)) v[i] += f;
-                                }
+                    for (int c0 = 0; c0 < DH; c0 += 32) tc_ld32_nowait(to + (uint32_t)c0, vi + c0);
+#pragma unroll
+                    for (int c0 = 0; c0 < DH; c0 += 32) tc_wait_ld32(vi + c0);
+                    tc_fence_before();
+                    if (odd && mine) {  // what is not finite reaches those who see it
+                        const int my_pos = y.ch.base + y.tok + x * tx + tok;
+                        for (int j = 0; j < count * kTcKeys; ++j) {
+                            const int p = (y.kt0 + y.tile) * kTcKeys + j, p0 = p & ~(kTcKeys - 1);
+                            if (p0 + kTcKeys - 1 <= first_pos && (a.window == 0 || p0 > (long long)last_pos - a.window)) continue;
+                            if (p > my_pos || p < y.k.lo || (a.window > 0 && p <= (long long)my_pos - a.window)) continue;
+                            const int page = a.kv.table[(long long)y.b * a.kv.max_pages + (p >> a.kv.ps_log2)];
+                            if (page < 0 || page >= a.kv.n_pages) continue;
+                            const T *src = static_cast<const T *>(a.kv.v) + page * a.kv.page_stride +
+                                           ((((long long)y.h << a.kv.ps_log2) + (p & ((1 << a.kv.ps_log2) - 1))) * DH);
+#pragma unroll
+                            for (int i = 0; i < DH; ++i) {
+                                const float f = (float)src[i];
+                                if (!(fabsf(f) < INFINITY)) v[i] += f;
                             }
                         }
-                        if (!mine) {
-                        } else if (result) {
-                            uint32_t h[16];
+                    }
+                    uint8_t *stage = t + L::OUT + (warp - 2) * 32 * L::OUT_ROW;
+                    uint4 *own = reinterpret_cast<uint4 *>(stage + lane * L::OUT_ROW);
+                    const uint4 *theirs = reinterpret_cast<const uint4 *>(stage + (lane / 4) * L::OUT_ROW + (lane & 3) * 16);
+                    if (result) {
+                        const float inv = inverse(l);
+                        T *out = static_cast<T *>(a.out) + (lane & 3) * 8;
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) h[i] = pack2<T>(v[2 * i] * inv, v[2 * i + 1] * inv);
-                            uint4 *dst = reinterpret_cast<uint4 *>(static_cast<T *>(a.out) + q_row * a.ld_out + (long long)head * DH + c0);
+                        for (int c0 = 0; c0 < DH; c0 += 32) {
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) dst[i] = make_uint4(h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]);
-                        } else {
-                            float *dst = a.part_o + slot * DH + c0;
+                            for (int i = 0; i < 4; ++i) {
+                                const float *f = v + c0 + 8 * i;
+                                own[i] = make_uint4(pack2<T>(f[0] * inv, f[1] * inv), pack2<T>(f[2] * inv, f[3] * inv),
+                                                    pack2<T>(f[4] * inv, f[5] * inv), pack2<T>(f[6] * inv, f[7] * inv));
+                            }
+                            __syncwarp();
 #pragma unroll
-                            for (int i = 0; i < 32; i += 4)
-                                st_hint(reinterpret_cast<float4 *>(dst + i), make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]), keep);
+                            for (int k = 0; k < 4; ++k)
+                                if (to4[k] >= 0) *reinterpret_cast<uint4 *>(out + to4[k] + c0) = theirs[k * 8 * L::OUT_ROW / 16];
+                            __syncwarp();
                         }
-                        __syncwarp();
+                        if (mine && a.lse) a.lse[q_row * a.n_q + head] = m2 * 0.69314718055994530942f + logf(l);
+                    } else {
+                        const uint64_t keep = policy_evict_last();
+                        float *out = a.part_o + (lane & 3) * 4;
+#pragma unroll
+                        for (int c0 = 0; c0 < DH; c0 += 16) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                own[i] = make_uint4(vi[c0 + 4 * i], vi[c0 + 4 * i + 1], vi[c0 + 4 * i + 2], vi[c0 + 4 * i + 3]);
+                            __syncwarp();
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                if (to4[k] >= 0)
+                                    st_hint(reinterpret_cast<float4 *>(out + to4[k] + c0),
+                                            *reinterpret_cast<const float4 *>(theirs + k * 8 * L::OUT_ROW / 16), keep);
+                            __syncwarp();
+                        }
+                        if (mine) a.part_ml[at] = make_float2(m2, l);
                     }
-                    if (mine) {
-                        if (!result)
-                            a.part_ml[slot] = make_float2(m2, l);
-                        else if (a.lse)
-                            a.lse[q_row * a.n_q + head] = m2 * 0.69314718055994530942f + logf(l);
-                    }
-                    tc_fence_before();
                 }
+            } else if (left > count) {  // (this warpgroup has no part in this item)
+                next_item();
             }
             left -= count;
             at_tile += count;
             whole = true;
-            if (left > 0) {  // on to the next item
-                w.tile = w.tiles - 1;
-                chunk_advance<kTcKeys>(a, cum, w);
-                if (toks <= 0) load_q(w);  // (this warpgroup had no part in the last one)
-            }
         }
     }
     tc_fence_before();
@@ -526,13 +587,26 @@ __global__ void __launch_bounds__(C_THREADS, 1)
     }
 }
 
+// The queries as a 3-D tensor (dim, head, token), boxes of 64 dims x a group's heads x a row tile's tokens, swizzled.
+bool query_map(CUtensorMap *map, const ChunkArgs &a, int dtype) {
+    PagedEncode enc = paged_encoder();
+    if (!enc) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)a.kv.head_dim, (cuuint64_t)a.n_q, (cuuint64_t)a.n_tokens};
+    const cuuint64_t str[2] = {(cuuint64_t)a.kv.head_dim * 2, (cuuint64_t)a.ld_q * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)a.group, (cuuint32_t)(a.toks / 2)}, one[3] = {1, 1, 1};
+    return enc(map, dtype == LF_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+               const_cast<void *>(a.q), dims, str, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <typename T, int DH>
 lf_status launch_chunk_tc(const ChunkArgs &a, int dtype, cudaStream_t st) {
     constexpr int smem = CtSmem<DH>::BYTES;
     if (!set_smem_once<paged_chunk_tc_kernel<T, DH>>(smem)) return LF_ERR_CUDA;
-    CUtensorMap mk, mv;
-    if (!cache_map(&mk, a.kv.k, a.kv, dtype) || !cache_map(&mv, a.kv.v, a.kv, dtype)) return LF_ERR_CUDA;
-    return launch_pdl(paged_chunk_tc_kernel<T, DH>, a.grid, C_THREADS, smem, st, mk, mv, a) ? LF_OK : LF_ERR_CUDA;
+    CUtensorMap mk, mv, mq;
+    if (!cache_map(&mk, a.kv.k, a.kv, dtype) || !cache_map(&mv, a.kv.v, a.kv, dtype) || !query_map(&mq, a, dtype))
+        return LF_ERR_CUDA;
+    return launch_pdl(paged_chunk_tc_kernel<T, DH>, a.grid, C_THREADS, smem, st, mk, mv, mq, a) ? LF_OK : LF_ERR_CUDA;
 }
 
 }  // namespace
