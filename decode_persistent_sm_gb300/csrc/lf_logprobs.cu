@@ -627,11 +627,12 @@ __global__ void __launch_bounds__(LP_THREADS, 4) token_logprobs_kernel(const LpA
     if (tid < a.top && tid >= total) put(tid, -1, -INFINITY);
 }
 
-// CTAs to a row: as many as leave each a few thousand logits, where the rows do not
-// fill the SMs by themselves.
+// CTAs to a row: with few rows as many as there are SMs for, each of 4000 logits at least; two CTAs an SM still pay for
+// two to a row.
 int parts_of(int rows, int vocab, int n_sm) {
     int parts = 1;
-    while (parts < LP_PARTS && (long long)rows * parts * 2 <= 4ll * n_sm && vocab / (parts * 2) >= 2048) parts *= 2;
+    while (parts < LP_PARTS && (long long)rows * parts * 2 <= (parts == 1 ? 2 * n_sm : n_sm + n_sm / 16) && vocab / (parts * 2) >= 4000)
+        parts *= 2;
     return parts;
 }
 

@@ -20,7 +20,7 @@ namespace lf {
 namespace {
 
 constexpr int kNormMaxThreads = 1024, kNormMaxVecs = 4;  // so at most 32768 columns
-constexpr int kNormWalkRows = 8;
+constexpr int kNormWalkRows = 4;
 constexpr float kE4m3Max = 448.f;
 
 struct NormArgs {
@@ -318,7 +318,7 @@ bool launch_norm(NormArgs a, int n_sm, cudaStream_t st) {
     a.rpb = std::max(1, 128 / a.tpr);
     if constexpr (VEC && sizeof(TX) == 2 && sizeof(TR) == 2) {
         // from a few rows per SM on the walk that keeps rows on their way, where a block of at most 512 threads holds a row
-        if (v == 2 && a.rpb == 1 && a.tpr <= 512 && a.rows >= kNormWalkRows * n_sm) {
+        if (v == 2 && a.tpr <= 512 && (a.tpr > 256 || (a.tpr == 256 && a.out_dtype == LF_E4M3)) && a.rows >= kNormWalkRows * n_sm) {
             const int smem = kNormStages * a.tpr * 2 * 8 * (int)(sizeof(TX) + sizeof(TR));
             const int ctas = std::max(1, std::min(227 * 1024 / (smem + 2048), 1024 / a.tpr));
             return set_smem_once<add_rmsnorm_rows_kernel<TX, TR, 2>>(kNormStages * 512 * 2 * 8 * (int)(sizeof(TX) + sizeof(TR))) &&

@@ -180,34 +180,38 @@ class ChunkWalker {
             cl.sync();
         else
             __syncthreads();
-        const int pairs = rows * (DH / 2), per = (pairs + parts - 1) / parts;
-        for (int x = part * per + tid; x < min(pairs, (part + 1) * per); x += CK_THREADS) {
-            const int row = x / (DH / 2), c = (x % (DH / 2)) * 2;
-            float2 y[8], v[8];
+        const int quads = rows * (DH / 4), per = (quads + parts - 1) / parts;
+        for (int x = part * per + tid; x < min(quads, (part + 1) * per); x += CK_THREADS) {
+            const int row = x / (DH / 4), c = (x % (DH / 4)) * 4;
+            float2 y[8];
+            float4 v[8];
             float mx = -INFINITY;
 #pragma unroll
             for (int k = 0; k < 8; ++k)
                 if (k < parts) {
                     y[k] = parts > 1 ? *cl.map_shared_rank(stat + row, k) : stat[row];
-                    v[k] = *reinterpret_cast<const float2 *>(parts > 1 ? cl.map_shared_rank(mine + row * DH + c, k)
+                    v[k] = *reinterpret_cast<const float4 *>(parts > 1 ? cl.map_shared_rank(mine + row * DH + c, k)
                                                                        : mine + row * DH + c);
                     mx = fmaxf(mx, y[k].x);
                 }
             const float off = mx == -INFINITY ? 0.f : mx;
-            float sx = 0.f, sy = 0.f, sl = 0.f;
+            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+            float sl = 0.f;
 #pragma unroll
             for (int k = 0; k < 8; ++k)
                 if (k < parts) {
                     const float f = ex2(y[k].x - off);
-                    sx += f * v[k].x;
-                    sy += f * v[k].y;
+                    s.x += f * v[k].x;
+                    s.y += f * v[k].y;
+                    s.z += f * v[k].z;
+                    s.w += f * v[k].w;
                     sl += f * y[k].y;
                 }
             const float inv = inverse(sl);
             const int tok = quotient(row, a.group), head = w.h * a.group + row - tok * a.group;
             const long long q = w.ch.row0 + w.tok + tok;
-            *reinterpret_cast<uint32_t *>(static_cast<T *>(a.out) + q * a.ld_out + (long long)head * DH + c) =
-                pack2<T>(sx * inv, sy * inv);
+            *reinterpret_cast<uint2 *>(static_cast<T *>(a.out) + q * a.ld_out + (long long)head * DH + c) =
+                make_uint2(pack2<T>(s.x * inv, s.y * inv), pack2<T>(s.z * inv, s.w * inv));
             if (c == 0 && a.lse) a.lse[q * a.n_q + head] = mx * 0.69314718055994530942f + logf(sl);
         }
         if (parts > 1) cl.sync();  // nobody leaves while its partial is read
@@ -612,28 +616,58 @@ size_t al256(size_t n) { return (n + 255) & ~size_t(255); }
 // (a TMA box) and page strides that a tensor map can hold (2^40 bytes).
 bool tc_fits(const PagedView &v) { return v.head_dim >= 64 && v.ps_log2 >= 3 && v.page_stride < (1ll << 38); }
 
-// Rows of an item: 16, 32 or 64, as the sequences have on average; beyond 64 the tensor cores' 256.
-void shape(ChunkArgs &a, int n_sm) {
-    const long long rows = ((long long)a.n_tokens * a.group + a.kv.n_seqs - 1) / a.kv.n_seqs;
-    a.tc = rows > 64 && tc_fits(a.kv);
-    a.slot_rows = a.tc ? kTcRows : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
-    a.toks = a.tc ? 2 * (128 / a.group) : a.slot_rows / a.group;  // (a 128-row tile holds whole tokens)
-    a.grid = a.tc ? n_sm : n_sm * CK_CTAS_PER_SM;
+// Rows of a sequence and KV head, on average.
+long long rows_of(const ChunkArgs &a) { return ((long long)a.n_tokens * a.group + a.kv.n_seqs - 1) / a.kv.n_seqs; }
+
+// Items of 16, 32 or 64 rows on warp-level MMAs, as the sequences have, or of 256 on the tensor cores.
+void shape(ChunkArgs &a, bool tc, int n_sm) {
+    const long long rows = rows_of(a);
+    a.tc = tc;
+    a.slot_rows = tc ? kTcRows : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+    a.toks = tc ? 2 * (128 / a.group) : a.slot_rows / a.group;  // (a 128-row tile holds whole tokens)
+    a.grid = tc ? n_sm : n_sm * CK_CTAS_PER_SM;
 }
 
-// CTAs to an item of the direct kernel, 0 for the list and its join.
-int chunk_direct_parts(const ChunkArgs &a, int n_sm) {
-    if (a.tc) return 0;
-    const int kt = tile_keys(a.kv.head_dim), rts = (a.n_tokens + a.kv.n_seqs - 1) / a.kv.n_seqs;  // tokens of a sequence
+// How a call on warp-level MMAs would run: items, tiles of keys each, and the CTAs to an item that take the fewest tiles
+// one after another (every further wave of CTAs costs its start, about six tiles).
+struct MmaPlan {
+    long long items, tiles, each;  // each: tiles one after another of the direct kernel, starts of further waves included
+    int parts;
+    bool one_wave;
+};
+MmaPlan mma_plan(const ChunkArgs &a, int n_sm) {
+    MmaPlan p;
+    const int kt = tile_keys(a.kv.head_dim), toks = (a.n_tokens + a.kv.n_seqs - 1) / a.kv.n_seqs;  // tokens of a sequence
     const int bound = a.window > 0 ? std::min(a.window + a.toks, a.max_len) : a.max_len;
-    const int tiles = bound / kt + 1;
-    const long long items = (long long)a.kv.n_seqs * a.kv.n_kv * ((rts + a.toks - 1) / a.toks);
-    if (items > 6 * n_sm) return 0;
-    int parts = 1;
-    while (parts < 8 && parts < tiles && items * parts * 2 <= 2 * n_sm) parts *= 2;
-    const long long waves = (items * parts + 2 * n_sm - 1) / (2 * n_sm);
-    const int each = (tiles + parts - 1) / parts;
-    return waves * each <= (waves == 1 ? 512 / kt : 6) ? parts : 0;
+    const long long ctas = (long long)n_sm * CK_CTAS_PER_SM;
+    p.tiles = bound / kt + 1;
+    p.items = (long long)a.kv.n_seqs * a.kv.n_kv * ((toks + a.toks - 1) / a.toks);
+    p.each = LLONG_MAX;
+    for (int k = 1; k <= 8; k *= 2) {
+        const long long room = k > 2 ? ctas * 7 / 8 : ctas;  // (larger clusters do not fill every SM of a GPC)
+        const long long waves = (p.items * k + room - 1) / room, t = waves * ((p.tiles + k - 1) / k + 6) - 6;
+        if (t < p.each) p.each = t, p.parts = k, p.one_wave = waves == 1;
+    }
+    return p;
+}
+
+// CTAs to an item of the direct kernel, 0 for the list and its join.  The list is even however the lengths are, but its
+// table, its partials and the second launch take longer than six key tiles of a CTA, and the more CTAs share an item, the
+// longer its join: about 0.3 tiles for each.
+int direct_parts(const ChunkArgs &a, const MmaPlan &p, int n_sm) {
+    const long long ctas = (long long)n_sm * CK_CTAS_PER_SM;
+    return p.each * 10 <= p.items * p.tiles * 10 / ctas + 60 + 3 * std::min(p.tiles, ctas / p.items) ? p.parts : 0;
+}
+
+// The tensor cores pay beyond 64 rows of a sequence and KV head, with many sequences from 41 on, but not where one wave of
+// the direct kernel has three key tiles to a CTA at most (two where an item has one CTA).
+bool tc_pays(const ChunkArgs &a, int n_sm) {
+    const long long rows = rows_of(a);
+    if (!tc_fits(a.kv) || rows <= 40 || (rows <= 64 && (long long)a.kv.n_seqs * a.kv.n_kv < 48)) return false;
+    ChunkArgs m = a;
+    shape(m, false, n_sm);
+    const MmaPlan p = mma_plan(m, n_sm);
+    return !(p.one_wave && (p.parts > 1 ? (p.tiles + p.parts - 1) / p.parts <= 3 : p.tiles <= 2));
 }
 
 struct CkWs {
@@ -660,8 +694,13 @@ lf_status check_chunk(const lf_paged_kv *kv, int n_q_heads, int n_tokens, PagedV
 
 // The largest a call of up to this many tokens needs (fewer tokens may take smaller items, never larger ones).
 size_t ck_bytes(ChunkArgs a, int n_sm) {
-    shape(a, n_sm);
-    return ck_layout(a).bytes;
+    shape(a, false, n_sm);
+    size_t n = ck_layout(a).bytes;
+    if (tc_fits(a.kv) && rows_of(a) > 40) {
+        shape(a, true, n_sm);
+        n = std::max(n, ck_layout(a).bytes);
+    }
+    return n;
 }
 
 template <typename T, int DH, int WR>
@@ -734,12 +773,14 @@ extern "C" lf_status lf_attn_paged_chunk(const lf_paged_kv *kv, const void *q_de
     a.n_tokens = n_tokens;
     const int n_sm = lf::sm_count();
     if (!n_sm) return LF_ERR_CUDA;
-    lf::shape(a, n_sm);
+    if (workspace_bytes < lf::ck_bytes(a, n_sm)) return LF_ERR_INVALID_ARG;
+    a.max_len = max_len;
+    a.window = window >= max_len ? 0 : window;  // (every position lies less than max_len back)
+    lf::shape(a, lf::tc_pays(a, n_sm), n_sm);
     // tiles are counted in 32 bits
     const int kt = a.tc ? lf::kTcKeys : lf::tile_keys(kv->head_dim);
     if (((long long)n_tokens / a.toks + kv->n_seqs) * ((long long)max_len / kt + 2) * kv->n_kv_heads > INT_MAX)
         return LF_ERR_UNSUPPORTED;
-    if (workspace_bytes < lf::ck_bytes(a, n_sm)) return LF_ERR_INVALID_ARG;
     if (n_tokens == 0) return LF_OK;
     const lf::CkWs w = lf::ck_layout(a);
     uint8_t *ws = static_cast<uint8_t *>(workspace_device);
@@ -754,11 +795,9 @@ extern "C" lf_status lf_attn_paged_chunk(const lf_paged_kv *kv, const void *q_de
     a.n_q = n_q_heads;
     a.starts = starts_device;
     a.lens = lens_device;
-    a.max_len = max_len;
-    a.window = window >= max_len ? 0 : window;  // (every position lies less than max_len back)
     a.scale_log2 = scale * lf::kLog2e;
     a.err = err_device;
-    const int direct = lf::chunk_direct_parts(a, n_sm);
+    const int direct = a.tc ? 0 : lf::direct_parts(a, lf::mma_plan(a, n_sm), n_sm);
     cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
     return kv->dtype == LF_F16 ? lf::launch_chunk_dim<__half>(a, direct, st)
                                : lf::launch_chunk_dim<__nv_bfloat16>(a, direct, st);

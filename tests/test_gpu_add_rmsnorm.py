@@ -190,3 +190,39 @@ def test_rows_past_32_bits():
     x[-1] = 2.0
     _, y, _ = run(x, None, None, ("f16", "f16", "f16"), "f16")
     assert (y[-1] == 1.0).all() and not y[-2].any()
+
+
+@pytest.mark.parametrize("dtypes", [("f16", "f16", "f16"), ("bf16", "bf16", "f32"), ("f16", "bf16", "bf16")])
+@pytest.mark.parametrize("rows,cols,out_dtype", [(1300, 4096, "e4m3"), (1301, 8192, "f16"), (700, 7168, "bf16"),
+                                                 (640, 4104, "e4m3"), (2000, 5000, "f32")])
+def test_many_rows_of_16_bits(rows, cols, out_dtype, dtypes):
+    x, res, gain = inputs(rows, cols, dtypes, cols)
+    check(x, res, gain, dtypes, out_dtype, 1e-5, *run(x, res, gain, dtypes, out_dtype))
+    check(x, None, None, dtypes, out_dtype, 1e-5, *run(x, None, None, dtypes, out_dtype))
+
+
+def test_many_rows_in_place_strided_and_not_finite():
+    import torch
+    dtypes = ("f16", "f16", "f16")
+    x, res, gain = inputs(1000, 4608, dtypes, 5, ld=24)
+    s, y, scale = run(x, res, gain, dtypes, "e4m3")
+    a, b = x.clone(), res.clone()
+    s2, y2, scale2 = run(a, b, gain, dtypes, "e4m3", sum_to=b)
+    assert torch.equal(s, s2) and torch.equal(y.view(torch.uint8), y2.view(torch.uint8)) and torch.equal(scale, scale2)
+    s3, y3, _ = run(a, res, gain, dtypes, "f16", sum_to=a, out=res.clone())
+    assert torch.equal(s, s3)
+    x[999, 7] = math.nan
+    _, y4, scale4 = run(x, res, gain, dtypes, "e4m3")
+    assert torch.equal(y4[:999].view(torch.uint8), y[:999].view(torch.uint8)) and torch.isnan(y4[999].float()).all() and scale4[999] == 1
+
+
+@pytest.mark.parametrize("rows", [607, 608, 609])
+def test_both_ways_agree_at_their_border(rows):
+    import torch
+    dtypes = ("bf16", "bf16", "bf16")
+    x, res, gain = inputs(rows, 6144, dtypes, 9)
+    s, y, _ = run(x, res, gain, dtypes, "bf16")
+    s2, y2, _ = run(x[:100], res[:100], gain, dtypes, "bf16")
+    assert torch.equal(s[:100], s2)
+    check(x, res, gain, dtypes, "bf16", 1e-5, s, y, torch.ones(rows))
+    assert (y[:100] != y2).float().mean() < 1e-3  # the sums of squares may differ in their last bit

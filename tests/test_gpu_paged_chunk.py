@@ -370,3 +370,58 @@ def test_offsets_past_32_bits():
             assert err.item() == 0
             outs.append(out)
         assert torch.equal(*outs)
+
+
+def drawn(seed):
+    """A batch of any kind: few or many sequences, chunks short, long, mixed and
+    missing, windows, padding."""
+    g = np.random.default_rng(seed)
+    log = lambda a, b: int(round(math.exp(g.uniform(math.log(a), math.log(b)))))  # noqa: E731
+    n, most, ctx = log(1, 30), log(1, 400), log(1, 1500)
+    new = [int(g.integers(0, most + 1)) for _ in range(n)]
+    if g.random() < 0.3:  # one chunk beside single tokens
+        new = [most] + [1] * (n - 1)
+    if g.random() < 0.3:  # drafted tokens
+        new = [int(g.integers(1, 9)) for _ in range(n)]
+    before = [int(g.integers(0, ctx + 1)) for _ in range(n)]
+    if g.random() < 0.1:
+        before[0] = -int(g.integers(0, new[0] + 1))
+    nkv = int(g.choice([1, 2, 4, 8]))
+    group = int(g.choice([1, 2, 3, 4, 5, 8, 16]))
+    return Case(new, before, nkv * group, nkv, int(g.choice([32, 64, 128])), int(g.choice([2, 8, 16, 64, 256])),
+                str(g.choice(["f16", "bf16"])), int(g.choice([0, 0, 0, 1, 60, 500])), seed=seed, pad=int(g.integers(0, 4)),
+                lead=int(g.integers(0, 3)), stride_extra=int(g.choice([0, 16])))
+
+
+@pytest.mark.parametrize("seed", range(60))
+def test_drawn_batches(seed):
+    import torch
+    c = drawn(seed)
+    if c.rows == 0:
+        pytest.skip("nobody has a token")
+    ws = c.workspace()
+    for bound in (max(0, max(c.lens)), c.table.shape[1] * c.page):  # a tight bound and a loose one take other ways
+        c.check(*c.run(ws=ws, max_len=bound))
+    again, _ = c.run(ws=ws, max_len=max(0, max(c.lens)))
+    first, _ = c.run(max_len=max(0, max(c.lens)))
+    torch.cuda.synchronize()
+    assert torch.equal(first, again)
+
+
+@pytest.mark.parametrize("new,ctx,nq,nkv,dim", [([1], [300], 2, 2, 128), ([4], [1500], 8, 4, 128), ([20], [700], 8, 4, 64),
+                                                ([30] * 2, [500, 900], 16, 4, 32), ([5] * 8, [400] * 8, 32, 16, 128),
+                                                ([3] * 5, [60] * 5, 64, 4, 64), ([8] * 30, [700] * 30, 16, 8, 128),
+                                                ([2] * 70, [90] * 70, 8, 8, 64), ([64] * 20, [20] * 20, 16, 8, 128),
+                                                ([40] * 12, [2000] * 12, 8, 8, 64)])
+def test_clusters_of_every_size(new, ctx, nq, nkv, dim):
+    # few keys by 1, 2, 4 or 8 CTAs to an item, the list, and both sides of where the tensor cores begin
+    c = Case(new, ctx, nq, nkv, dim, 16, "f16", seed=sum(new))
+    c.check(*c.run(max_len=max(c.lens)))
+
+
+def test_a_row_tile_longer_than_a_warps_prefix_sum():
+    # more than 32 row tiles to a sequence, on warp-level MMAs (head_dim 32) and on the tensor cores
+    c = Case([1500], [100], 4, 1, 32, 16, "f16", seed=1)
+    c.check(*c.run())
+    c = Case([2300, 3], [50, 9], 16, 1, 64, 32, "bf16", seed=2)
+    c.check(*c.run())

@@ -229,3 +229,25 @@ def test_rows_past_32_bits():
     lp, rank, ent, _, _ = definition(z[-1].double().cpu().numpy(), 8, np.float32(1), 0)
     assert abs(r["logprob"][-1].item() - lp) < 1e-4 and r["rank"][-1] == rank and abs(r["entropy"][-1].item() - ent) < 1e-4
     assert (r["rank"][:-1] == 8).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16"])
+@pytest.mark.parametrize("rows,vocab", [(1, 8001), (19, 32003), (20, 64000), (38, 20000), (40, 16001), (76, 9000), (77, 33000),
+                                        (152, 8000), (153, 8000)])
+def test_rows_of_1_2_4_and_8_ctas(dtype, rows, vocab):
+    z, token = logits(rows, vocab, dtype, rows, masked=0.3)
+    z[0, ::7] = -math.inf
+    z[rows // 2, :] = -math.inf
+    z[rows // 2, vocab - 1] = 0.5
+    check(z, token, None, 32, call(z, dtype, token, None, 32), rows=range(0, rows, max(1, rows // 8)))
+
+
+def test_a_masked_value_after_clean_ones_and_before():
+    # a thread goes over to the masked way in the middle of its walk
+    import torch
+    z, token = logits(4, 40000, "f32", 3)
+    z[0, 39000:] = -math.inf
+    z[1, :1000] = -math.inf
+    z[2, 20000] = torch.finfo(torch.float32).min
+    z[3, 20000] = math.nan
+    check(z, token, None, 5, call(z, "f32", token, None, 5))
