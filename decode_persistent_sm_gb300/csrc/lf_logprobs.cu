@@ -31,7 +31,7 @@ namespace lf {
 namespace {
 
 constexpr int LP_THREADS = 256, LP_WARPS = LP_THREADS / 32, LP_TOP = 32, LP_LIST = 512, LP_PARTS = 8;
-constexpr int LP_U = 2, LP_STAGES = 4;  // 16-byte pieces of a thread's batch, batches on their way
+constexpr int LP_U = 3, LP_STAGES = 3;  // 16-byte pieces of a thread's batch, batches on their way
 constexpr int LP_RING = LP_STAGES * LP_U * LP_THREADS * 16;
 constexpr int LP_MAX_VOCAB = 1 << 18;
 constexpr float kLog2E = 1.4426950408889634f, kLn2 = 0.69314718055994530942f;
