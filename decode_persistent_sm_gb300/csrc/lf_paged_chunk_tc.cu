@@ -486,7 +486,7 @@ __global__ void __launch_bounds__(C_THREADS, 1)
                     l += s2.x + s2.y;
                 }
                 // the rows' result or partial, once the last P V is done; what needs no wait first
-                const bool odd = S.odd_[it & 7] == it + 1, result = whole && y.tile + count == y.tiles;
+                const bool result = whole && y.tile + count == y.tiles;
                 const int tok = quotient(min(row, rows - 1), a.group);
                 const bool mine = row < rows;
                 const long long q_row = (long long)y.ch.row0 + y.tok + x * tx + tok;
@@ -499,6 +499,8 @@ __global__ void __launch_bounds__(C_THREADS, 1)
                 for (int k = 0; k < 4; ++k) to4[k] = __shfl_sync(0xffffffffu, dst, 8 * k + lane / 4);
                 if (left > count) next_item();
                 if (ok) ok = __all_sync(0xffffffffu, await_phase(S, &S.bo[x], no++ & 1u, a.err));
+                // (the products behind bo waited for every cleaned tile of the item: its flag is final from here on)
+                const bool odd = S.odd_[it & 7] == it + 1;
                 if (ok && warp_used) {
                     tc_fence_after();
                     float v[DH];
