@@ -8,10 +8,20 @@
 // buffers), and four warps read a finished accumulator back, scale it and store
 // it while the next tile's products run.
 //
-// BN is 256 where there are tiles enough for every SM (the products are the
-// bound: an MMA of 128 x 256 reads 384 bytes of shared memory for each 32 x 32
-// of K, one of 128 x 128 a third more), and less where the weights' stream is the
-// bound and has to be spread over the SMs (few rows of A).
+// What bounds it: with many rows the operands' way from shared memory into the
+// products (a block of 128 x 256 x 128 reads 48 KB in the 256 cycles that its
+// products take; a narrower tile reads more per product), 3584 x 8192 x 4096 in 90 us,
+// 2660 TFLOP/s; with few rows the weights' stream, 16 x 8192 x 4096 in 10.0 us, of
+// which 5 are the call (6.7 TB/s per further byte).  So BN is 256 where the tiles
+// fill the SMs, and less where they do not or the stream has to be spread over them.
+//
+// With few rows a block of 128 along K is over in less time than a barrier's round
+// trip: two blocks to a stage (KS) took 16 x 8192 x 4096 from 12.9 us to 10.1.  A stage
+// that holds 32 rows of A instead of 128 (AR) leaves room for more of them:
+// 14.2 us where 15.5 at 16 x 14336 x 4096.
+//
+// The accumulators are full fp32: a sum of 4096 products that spread over 2^30 in
+// size comes out to 2^-23 of its terms' magnitude.
 //
 // Every wait is bounded: on a timeout the CTA records an error, lets its copies
 // and MMAs in flight finish (bounded), frees TMEM and exits.
@@ -330,7 +340,11 @@ extern "C" lf_status lf_matmul_f8(const void *a_device, const float *a_scale_dev
     }
     const lf::F8Args a = {a_scale_device, b_scale_device, c_device, m, n, k, c_dtype, 0, err_device};
     cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
-    // the width whose waves over the SMs take the least: a tile of 256, 128 and 64 columns takes as 12 : 7.2 : 5
+    // The width whose waves over the SMs take the least: a tile of 256, 128 and 64 columns takes as 12 : 7.2 : 5.
+    // us by width 64 | 128 | 256, K 4096:
+    //   n  8192, m  128  10.4 | 12.4 | 17.6    200  15.0 | 12.6 | 17.6     384  20.6 | 19.5 | 17.8    1024  43.0 | 34.0 | 29.4
+    //   n 14336, m   16  14.2 | 14.2 | 17.8    384  32.3 | 27.9 | 31.0     512  38.7 | 29.1 | 31.5    1024  72.6 | 52.0 | 44.5
+    //   n  1024, m   16   8.1 |  8.9 | 13.2
     const long long mt = ((long long)m + 127) / 128;
     auto cost = [&](int bn, int weight) { return (mt * (((long long)n + bn - 1) / bn) + n_sm - 1) / n_sm * weight; };
     const long long c256 = cost(256, 120), c128 = cost(128, 72), c64 = cost(64, 50);

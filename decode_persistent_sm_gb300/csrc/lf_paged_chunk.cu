@@ -8,7 +8,16 @@
 // statistics in registers.  Warps take 16-row blocks, and 16-key blocks where the
 // rows are fewer; warps that shared rows join in shared memory at the item's end.
 // An item that one CTA sees whole is written out at once; one that several share
-// leaves partials (unnormalised o, max, sum) and a second launch joins them.
+// leaves partials (unnormalised o, max, sum) and a second launch joins them.  With
+// few keys there is neither list nor second launch: a cluster of CTAs takes an
+// item and joins it through distributed shared memory.  Many rows go to the
+// tensor cores (lf_paged_chunk_tc.cu).
+//
+// What bounds it: with few tokens the cache's bytes and, for short ones, the call's
+// fixed parts: 8 sequences of 5 new tokens at 512 positions (32 heads on 16 of
+// 128) move 38 MB in 14.1 us, 5.7 of them the bytes; one launch in a cluster took
+// the place of list and join at 17.9.  8 sequences of one token at 4096 positions:
+// 268 MB in 46.6 us, 85 % of the copy rate.
 //
 // Masks.  Only a tile that some row of the item does not see whole is masked, by
 // position, scores set to -inf.  A weight of 0 times a value that is not finite
@@ -653,14 +662,26 @@ MmaPlan mma_plan(const ChunkArgs &a, int n_sm) {
 
 // CTAs to an item of the direct kernel, 0 for the list and its join.  The list is even however the lengths are, but its
 // table, its partials and the second launch take longer than six key tiles of a CTA, and the more CTAs share an item, the
-// longer its join: about 0.3 tiles for each.
+// longer its join: about 0.3 tiles for each.  us, list | clusters of 1, 2, 4, 8, 32 heads on 16 of 128, one new token:
+//   1 sequence   512 keys  10.2 | 13.1  9.8  8.2  7.7    4096 keys  22.9 | 63.8 35.3 21.0 15.7
+//   8 sequences  512 keys  15.8 | 15.3 13.4 18.4 27.3    4096 keys  49.4 | 70.9 46.6 52.3 61.2
+// and 16 rows (8 new tokens), 32 sequences: 512 keys 39.7 | 39.0 51.0 70.8 124, 4096 keys 171 | 176 190 189 236.
+// Over 404 sizes this rule and tc_pays' together lose 2 % to the best choice of each.
 int direct_parts(const ChunkArgs &a, const MmaPlan &p, int n_sm) {
     const long long ctas = (long long)n_sm * CK_CTAS_PER_SM;
     return p.each * 10 <= p.items * p.tiles * 10 / ctas + 60 + 3 * std::min(p.tiles, ctas / p.items) ? p.parts : 0;
 }
 
 // The tensor cores pay beyond 64 rows of a sequence and KV head, with many sequences from 41 on, but not where one wave of
-// the direct kernel has three key tiles to a CTA at most (two where an item has one CTA).
+// the direct kernel has three key tiles to a CTA at most (two where an item has one CTA).  us, the better of list and
+// clusters | tensor cores, 32 heads on 16 of 128:
+//   1 sequence,    64 rows   512 keys  12.2 | 17.5   4096  26.7 | 25.0     128 rows  512  12.7 | 18.6   4096  26.9 | 26.1
+//   8 sequences,   16 rows   512 keys  15.3 | 21.9   4096  48.4 | 57.2      64 rows  512  22.8 | 23.7   4096  74.7 | 59.5
+//                 128 rows   512 keys  33.7 | 26.2   4096 130.7 | 63.8
+//   32 sequences,  16 rows   512 keys  39.0 | 50.0   4096 171   | 180       32 rows  512  48.3 | 51.5   4096 187   | 184
+//                  64 rows   512 keys  58.9 | 52.1   4096 246   | 187
+// and 24 on 8 of 64: 1 sequence, 96 rows, 512 keys 10.0 | 13.8; 8 sequences, 48 rows, 4096 keys 28.9 | 28.4, 512 keys
+// 11.1 | 15.5; 32 sequences, 48 rows, 4096 keys 81.8 | 74.1, 512 keys 22.8 | 26.3.
 bool tc_pays(const ChunkArgs &a, int n_sm) {
     const long long rows = rows_of(a);
     if (!tc_fits(a.kv) || rows <= 40 || (rows <= 64 && (long long)a.kv.n_seqs * a.kv.n_kv < 48)) return false;

@@ -24,6 +24,22 @@
 // it hands over P), and at the item's end the values that are not finite are
 // added to the rows that do see them.
 //
+// Q comes by TMA, a box of (64 dims, the group's heads, tokens): its rows lie as the
+// products want them, and it loads under the item before.  Rows leave through
+// shared memory, 64 bytes of a row to four lanes.  Both together took 512 new tokens
+// at 3584 from 54 us to 45.
+//
+// What bounds it: over long keys the tensor cores (2 x 2048 new tokens at 14336, 32
+// heads on 16 of 128, bf16: 961 us, 1672 TFLOP/s, their pipe 72 % full; in calls back to
+// back the board's power, 1133 to 1150 us), else the items' starts, ends and joins
+// (512 at 3584: 44 us, 11 of them the join of 215 pieces, its products 17).  Of a
+// softmax warp's 168 registers 128 hold a row's scores.
+//
+// Tried: P's first piece of 64 or 32 keys, no better; shares of at least four tiles
+// instead of two, slower for short keys; the key tiles of an item of one row tile in
+// turn on both warpgroups, with a join of their sums at the end (36 us to 56 for
+// a mixed batch, 1 to 9 us more for short keys).
+//
 // Every wait is bounded; a CTA that ran out of time flags it, lets its copies
 // and products finish (bounded), frees its TMEM and exits.
 #include <climits>

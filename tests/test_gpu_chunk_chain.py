@@ -107,7 +107,13 @@ def test_steps_against_plain_torch():
         m.step(s, b, None)
     torch.cuda.synchronize()
     assert m.err.item() == 0
-    # the same pass from the library's 8-bit rows on, in 64 bits with its roundings
+    # The same pass from the library's 8-bit rows on, in 64 bits with its roundings.  The tolerances:
+    #   y8    half a step of 4 bits, 2^-4 of the value (1 % for the fp32 before it), or of the subnormals, 2^-10 of the scale
+    #   qkv   the rounding to 11 bits, and fp32 sums of 512 terms
+    #   att   P and o rounded to 11 bits: 2^-11 (sum p |v| + |o|), with sum p |v| below 7 times the largest |o| of all rows
+    #   res   fp32 sums of 512 products (their expected error is sqrt(512) 2^-24 = 1.3e-6 of the terms' size)
+    #   y     the rounding to 11 bits, and res's 1e-5 of the largest value, which is below 10 times the rms
+    #   lp    fp32: differences and logarithms below 16, each to 2^-21, a handful of them
     ks = [torch.zeros(0, NKV, DH, dtype=torch.float64, device="cuda") for _ in range(3)]
     vs = [k.clone() for k in ks]
     for s, b in zip(steps, bufs):
