@@ -425,3 +425,20 @@ def test_a_row_tile_longer_than_a_warps_prefix_sum():
     c.check(*c.run())
     c = Case([2300, 3], [50, 9], 16, 1, 64, 32, "bf16", seed=2)
     c.check(*c.run())
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_values_that_are_not_finite_and_come_late_reach_every_row(dim):
+    # one masked tile to an item of two row tiles, its scores ready before its values: these alone come from far memory
+    import torch
+    c = Case([100 + i % 28 for i in range(60)], [0] * 60, 8, 4, dim, 64, "f16", seed=3)
+    page = torch.from_numpy(c.table[:, 0]).cuda().long()
+    c.v[page, :, 3, 7] = float("inf")
+    want, lse = c.run()
+    c.check(want, lse)
+    far = torch.empty(1 << 26, dtype=torch.float32, device="cuda")
+    for _ in range(20):
+        far.zero_()
+        c.k.sum(), c.q.sum()
+        out, again = c.run()
+        assert torch.equal(out, want) and torch.equal(again, lse)
