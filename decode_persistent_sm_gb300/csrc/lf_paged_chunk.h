@@ -102,11 +102,14 @@ struct ChunkWork {
 
 // Fills cum[b] = key tiles per KV head of the sequences before b (cum[n_seqs]: of
 // all); a whole block calls it.  Returns the list's length.  A lane adds up the few
-// row tiles of its sequence, the warp together those of a long chunk.
+// row tiles of its sequence, the warp together those of a long chunk.  Starts that
+// decrease (bad where they do) can claim rows more than once: beyond n_tokens in all,
+// which is what the host bounds the list by, there is no list.
 template <int KT>
 __device__ __forceinline__ int chunk_plan(const ChunkArgs &a, int *cum) {
     constexpr int kFew = 4;
     const int n = a.kv.n_seqs, lane = threadIdx.x & 31;
+    long long claimed = 0;
     int at = 0;
     for (int b0 = 0; b0 < n; b0 += 32) {  // (every warp for itself; the first fills the table)
         const int b = b0 + lane;
@@ -115,6 +118,8 @@ __device__ __forceinline__ int chunk_plan(const ChunkArgs &a, int *cum) {
             k = chunk_of(a, b);
             if (k.bad && blockIdx.x == 0 && threadIdx.x < 32) atomicExch(a.err, 1u);
         }
+        claimed += __reduce_add_sync(0xffffffffu, (unsigned)k.c);  // (32 times 2^26 at most)
+        if (claimed > a.n_tokens) break;
         const int rt = row_tiles_of(k.c, a.toks);
         int t = 0;
         for (int r = 0; r < min(rt, kFew); ++r) t += key_tiles_of<KT>(a, k, r);
@@ -137,6 +142,7 @@ __device__ __forceinline__ int chunk_plan(const ChunkArgs &a, int *cum) {
         if (threadIdx.x < 32 && b < n) cum[b] = at + inc - t;
         at += __shfl_sync(0xffffffffu, inc, 31);
     }
+    if (claimed > a.n_tokens) at = 0;
     if (threadIdx.x == 0) cum[n] = at;
     __syncthreads();
     return at * a.kv.n_kv;

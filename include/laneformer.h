@@ -673,9 +673,10 @@ lf_status lf_matmul_f8(const void *a_device, const float *a_scale_device, const 
  * there (NaN included), in its own chunk too.  Scores, softmax statistics and sums
  * are fp32; the softmax weights enter the second product rounded to the cache's
  * type.  The result does not depend on timing, only on the arguments and the SM
- * count.  A length outside [0, max_len] (taken as 0), a start outside its bounds
- * (that sequence is taken as without new tokens) or a page outside the cache (the
- * result is then undefined) sets *err_device (DEVICE word, cleared by the caller) to
+ * count.  A length outside [0, max_len] (taken as 0), a start outside its bounds or
+ * above the next one (that sequence is taken as without new tokens; rows that
+ * several others then claim are undefined, and all rows if more are claimed than
+ * there are) or a page outside the cache (the result is then undefined) sets *err_device (DEVICE word, cleared by the caller) to
  * 1, a device-side wait that ran out (2 s) to 2.  n_tokens 0 does nothing.
  * LF_ERR_INVALID_ARG for bad sizes, pointers, strides or types, max_len above
  * max_pages * page_size, or a workspace too small; LF_ERR_UNSUPPORTED for head_dim

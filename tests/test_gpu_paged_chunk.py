@@ -442,3 +442,23 @@ def test_values_that_are_not_finite_and_come_late_reach_every_row(dim):
         c.k.sum(), c.q.sum()
         out, again = c.run()
         assert torch.equal(out, want) and torch.equal(again, lse)
+
+
+@pytest.mark.parametrize("tokens", [1 << 14, 1 << 18])
+def test_starts_that_claim_all_rows_many_times_over(tokens):
+    # every second sequence claims every row, 2^32 key tiles in all: refused on the device, no row touched
+    import torch
+    import decode_persistent_sm_gb300 as lf
+    n, page, pages, dim = 1024, 1024, 1024, 64
+    e = lambda *s, dt=torch.float16, v=0: torch.full(s, v, dtype=dt, device="cuda")  # noqa: E731
+    k, v, table = e(1, 1, page, dim), e(1, 1, page, dim), e(n, pages, dt=torch.int32)
+    q, out, err = e(tokens, dim), e(tokens, dim, v=9.0), e(1, dt=torch.int32)
+    starts = (torch.arange(n + 1, device="cuda") % 2 * tokens).int()
+    lens = e(n, dt=torch.int32, v=page * pages)
+    kv = lf.paged_kv(k.data_ptr(), v.data_ptr(), table.data_ptr(), n_pages=1, n_kv_heads=1, page_size=page, head_dim=dim,
+                     n_seqs=n, max_pages=pages, dtype="f16")
+    ws = e(lf.attn_paged_chunk_workspace(kv, 1, tokens), dt=torch.uint8, v=255)
+    lf.attn_paged_chunk(kv, q.data_ptr(), dim, out.data_ptr(), dim, None, 1, starts.data_ptr(), tokens, lens.data_ptr(),
+                        page * pages, 0, 0.125, ws.data_ptr(), ws.numel(), err.data_ptr())
+    torch.cuda.synchronize()
+    assert err.item() == 1 and (out == 9.0).all()
