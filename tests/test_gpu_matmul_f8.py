@@ -130,3 +130,14 @@ def test_chained_on_a_stream_captured_and_repeated():
     gr.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(first, o) for o in outs + [third])
+
+
+@pytest.mark.parametrize("m,n,k", [(70001, 65600, 16), (5, 1 << 20, 4224)])
+def test_offsets_past_32_bits(m, n, k):
+    # a result, and a weight matrix, of more than 2^32 places: their last rows and some between
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(11)
+    a, b = (torch.randint(0, 120, (x, k), device="cuda", generator=g, dtype=torch.uint8).view(torch.float8_e4m3fn) for x in (m, n))
+    c = run(a, b, None, None, "bf16")
+    for rows, cols in ((slice(max(0, m - 70), m), slice(n - 300, n)), (slice(m // 2, m // 2 + 9), slice(n // 2, n // 2 + 99))):
+        check(a[rows], b[cols], None, None, "bf16", c[rows, cols])
