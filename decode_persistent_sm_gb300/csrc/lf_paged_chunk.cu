@@ -125,36 +125,8 @@ class ChunkWalker {
     __device__ void run_direct() {
         cg::cluster_group cl = cg::this_cluster();
         const int parts = (int)cl.num_blocks(), part = (int)cl.block_rank();
-        const int id = quotient(blockIdx.x, parts), g = quotient(id, a.kv.n_kv);  // row tile g of all sequences
         ChunkWork w;
-        w.h = id - g * a.kv.n_kv;
-        w.b = -1;
-        for (int b0 = 0, at = 0; b0 < a.kv.n_seqs; b0 += 32) {
-            const int b = b0 + lane;
-            Chunk k = {0, 0, 0, false};
-            if (b < a.kv.n_seqs) k = chunk_of(a, b);
-            if (k.bad && blockIdx.x == 0 && warp == 0) atomicExch(a.err, 1u);
-            const int rt = row_tiles_of(k.c, a.toks);
-            int inc = rt;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int y = __shfl_up_sync(0xffffffffu, inc, o);
-                if (lane >= o) inc += y;
-            }
-            const unsigned hit = __ballot_sync(0xffffffffu, at + inc > g);
-            if (hit && w.b < 0) {
-                const int who = __ffs(hit) - 1;
-                w.b = b0 + who;
-                w.r = g - at - __shfl_sync(0xffffffffu, inc - rt, who);
-                w.ch.row0 = __shfl_sync(0xffffffffu, k.row0, who);
-                w.ch.c = __shfl_sync(0xffffffffu, k.c, who);
-                w.ch.base = __shfl_sync(0xffffffffu, k.base, who);
-                if (blockIdx.x > 0) break;
-            }
-            at += __shfl_sync(0xffffffffu, inc, 31);
-        }
-        if (w.b < 0) return;  // (the whole cluster: there are fewer row tiles than the grid allows for)
-        w.set<KT>(a);
+        if (!chunk_item<KT>(a, quotient(blockIdx.x, parts), w)) return;  // (the whole cluster: fewer row tiles than the grid allows for)
         const Shares sh(w.tiles, parts);
         const int t0 = part < w.tiles ? sh.begin(part) : 0, n = part < w.tiles ? sh.begin(part + 1) - t0 : 0;
         w.tile = t0;
@@ -691,6 +663,28 @@ bool tc_pays(const ChunkArgs &a, int n_sm) {
     return !(p.one_wave && (p.parts > 1 ? (p.tiles + p.parts - 1) / p.parts <= 3 : p.tiles <= 2));
 }
 
+// CTAs to an item of the tensor-core kernel in a cluster, 0 for the list and its join.  A cluster's start, end and join take
+// as long as 8, 9 or 12 key tiles of a CTA with 1, 2 or 4 CTAs, those of the list as 19, and its tiles a tenth longer (their
+// partials go through L2); but the list is even, and a cluster's item with the most keys sets the time.
+int tc_parts(const ChunkArgs &a, int n_sm) {
+    const long long items = chunk_items(a);
+    const int toks = (a.n_tokens + a.kv.n_seqs - 1) / a.kv.n_seqs;  // tokens of a sequence
+    const int bound = a.window > 0 ? std::min(a.window + a.toks, a.max_len) : a.max_len;
+    const long long tiles = bound / kTcKeys + 1, mean = a.window > 0 ? tiles : std::max(1ll, tiles - toks / (2 * kTcKeys));
+    const long long even = (long long)a.kv.n_seqs * a.kv.n_kv * ((toks + a.toks - 1) / a.toks);
+    long long best = 190 + 11 * even * mean / n_sm;
+    int parts = 0;
+    const int fixed[3] = {80, 90, 120};
+    for (int i = 0, k = 1; i < 3; ++i, k *= 2) {
+        const long long room = (k > 1 ? n_sm * 7 / 8 : n_sm) / k;
+        long long t = fixed[i] + 10 * ((tiles + k - 1) / k);
+        if (even > room) continue;
+        if (items > room) t += t / 2;  // (chunks of uneven lengths may take a second wave)
+        if (t < best) best = t, parts = k;
+    }
+    return parts;
+}
+
 struct CkWs {
     size_t ml, o, bytes;
 };
@@ -730,10 +724,8 @@ bool launch_rows(const ChunkArgs &a, int direct, cudaStream_t st) {
     if (!direct)
         return set_smem_once<paged_chunk_kernel<T, DH, WR>>(smem) &&
                launch_pdl(paged_chunk_kernel<T, DH, WR>, a.grid, CK_THREADS, smem, st, a);
-    // (a cluster for each row tile that the chunks can have; those without one leave at once)
-    const unsigned clusters = (unsigned)(a.kv.n_kv * (a.kv.n_seqs + a.n_tokens / a.toks));
     return set_smem_once<paged_chunk_direct<T, DH, WR>>(smem) &&
-           launch_pdl_cluster(paged_chunk_direct<T, DH, WR>, (unsigned)direct, dim3(clusters * direct), CK_THREADS, smem, st, a);
+           launch_pdl_cluster(paged_chunk_direct<T, DH, WR>, (unsigned)direct, dim3((unsigned)(chunk_items(a) * direct)), CK_THREADS, smem, st, a);
 }
 
 template <typename T, int DH>
@@ -741,7 +733,7 @@ lf_status launch_chunk(const ChunkArgs &a, int direct, cudaStream_t st) {
     bool ok = false;
     if constexpr (DH >= 64) {
         if (a.tc) {
-            const lf_status ts = paged_chunk_tc(a, std::is_same<T, __half>::value ? LF_F16 : LF_BF16, st);
+            const lf_status ts = paged_chunk_tc(a, std::is_same<T, __half>::value ? LF_F16 : LF_BF16, direct, st);
             if (ts != LF_OK) return ts;
             ok = true;
         }
@@ -818,7 +810,7 @@ extern "C" lf_status lf_attn_paged_chunk(const lf_paged_kv *kv, const void *q_de
     a.lens = lens_device;
     a.scale_log2 = scale * lf::kLog2e;
     a.err = err_device;
-    const int direct = a.tc ? 0 : lf::direct_parts(a, lf::mma_plan(a, n_sm), n_sm);
+    const int direct = a.tc ? lf::tc_parts(a, n_sm) : lf::direct_parts(a, lf::mma_plan(a, n_sm), n_sm);
     cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
     return kv->dtype == LF_F16 ? lf::launch_chunk_dim<__half>(a, direct, st)
                                : lf::launch_chunk_dim<__nv_bfloat16>(a, direct, st);

@@ -227,8 +227,51 @@ __device__ __forceinline__ ChunkArgs::Join chunk_join(const ChunkArgs &a, const 
     return j;
 }
 
-// The list's kernel on the 5th-generation tensor cores (lf_paged_chunk_tc.cu): head_dim 64 and 128,
-// toks even, slot_rows = kTcRows.
-lf_status paged_chunk_tc(const ChunkArgs &a, int dtype, cudaStream_t st);
+// Without the list: item `id` (row tile id / n_kv of all sequences, KV head id % n_kv); false if there are fewer.
+// Whole warps call it together.
+template <int KT>
+__device__ __forceinline__ bool chunk_item(const ChunkArgs &a, int id, ChunkWork &w) {
+    const int lane = threadIdx.x & 31, g = quotient(id, a.kv.n_kv);
+    w.h = id - g * a.kv.n_kv;
+    w.b = -1;
+    for (int b0 = 0, at = 0; b0 < a.kv.n_seqs; b0 += 32) {
+        const int b = b0 + lane;
+        Chunk k = {0, 0, 0, false};
+        if (b < a.kv.n_seqs) k = chunk_of(a, b);
+        if (k.bad && blockIdx.x == 0 && threadIdx.x < 32) atomicExch(a.err, 1u);
+        const int rt = row_tiles_of(k.c, a.toks);
+        int inc = rt;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += y;
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, at + inc > g);
+        if (hit && w.b < 0) {
+            const int who = __ffs(hit) - 1;
+            w.b = b0 + who;
+            w.r = g - at - __shfl_sync(0xffffffffu, inc - rt, who);
+            w.ch.row0 = __shfl_sync(0xffffffffu, k.row0, who);
+            w.ch.c = __shfl_sync(0xffffffffu, k.c, who);
+            w.ch.base = __shfl_sync(0xffffffffu, k.base, who);
+            if (blockIdx.x > 0) break;
+        }
+        at += __shfl_sync(0xffffffffu, inc, 31);
+    }
+    if (w.b < 0) return false;
+    w.set<KT>(a);
+    return true;
+}
+
+// The items that the chunks can have at most, a cluster to each (a chunk of c tokens has 1 + (c - 1) / toks row tiles; those
+// without an item leave at once).
+inline long long chunk_items(const ChunkArgs &a) {
+    const int some = a.n_tokens < a.kv.n_seqs ? a.n_tokens : a.kv.n_seqs;  // sequences with new tokens
+    return (long long)a.kv.n_kv * (some + (a.n_tokens - some) / a.toks);
+}
+
+// The kernel on the 5th-generation tensor cores (lf_paged_chunk_tc.cu): head_dim 64 and 128, toks even, slot_rows =
+// kTcRows.  direct: CTAs to an item, 0 for the list.
+lf_status paged_chunk_tc(const ChunkArgs &a, int dtype, int direct, cudaStream_t st);
 
 }  // namespace lf

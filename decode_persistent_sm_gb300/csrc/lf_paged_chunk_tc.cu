@@ -113,6 +113,31 @@ __device__ __forceinline__ uint32_t odd_bits(uint32_t w) {
     return ((w & 0x7fff7fffu) + one) & 0x80008000u;
 }
 
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t y;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(y));
+    return y;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+    uint32_t y;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(y));
+    return y;
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+// The place in CTA `rank` of the cluster of a place in this one's shared memory, and stores there.
+__device__ __forceinline__ uint32_t cluster_address(uint32_t mine, int rank) {
+    uint32_t y;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(y) : "r"(mine), "r"(rank));
+    return y;
+}
+__device__ __forceinline__ void cluster_store(uint32_t at, float2 v) {
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(at), "f"(v.x), "f"(v.y) : "memory");
+}
+__device__ __forceinline__ void cluster_store(uint32_t at, float4 v) {
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
+}
+
 template <int DH>
 struct CtSmem {
     static constexpr int HALVES = DH / 64;
@@ -124,9 +149,11 @@ struct CtSmem {
     static constexpr int WORK = OUT + 8 * 32 * OUT_ROW;  // two items of each softmax warp
     static constexpr int BYTES = WORK + 16 * (int)sizeof(ChunkWork) + 1024;
     static_assert(sizeof(CtShared) <= 256, "the barriers' place");
+    static_assert(6 * DH * 128 <= TILES && 6 * 32 * 8 <= 1024 * 4, "a cluster's partials and statistics");
 };
 
-template <typename T, int DH>
+// CL: a cluster to an item instead of the list.
+template <typename T, int DH, bool CL>
 __global__ void __launch_bounds__(C_THREADS, 1)
     paged_chunk_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                           const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ ChunkArgs a) {
@@ -159,15 +186,30 @@ __global__ void __launch_bounds__(C_THREADS, 1)
     }
     pdl_wait();
     pdl_trigger();
-    const int total = chunk_plan<kTcKeys>(a, cum);
-    // (a share is at least kLeast tiles: below, the partials would cost more than the tiles)
-    const int ctas = min((int)gridDim.x, max(1, (total + kLeast - 1) / kLeast));
-    const Shares sh(total, ctas);
-    if (threadIdx.x == 0) a.joins[cta].parts = 0;
-    if (cta >= min(total, ctas)) return;  // (the whole block, before it holds any TMEM)
-    const int u0 = sh.begin(cta), u1 = sh.begin(cta + 1), n = u1 - u0;
     const int tx = a.toks / 2;  // tokens of a row tile
-    ChunkWork w = chunk_place<kTcKeys>(a, cum, u0);  // every warp walks the list for itself
+    int parts = 1, rank = 0, u1 = 0, n;  // n: tiles of this CTA
+    ChunkWork w;                         // every warp walks the list for itself
+    Shares sh(1, 1);
+    if constexpr (CL) {
+        parts = (int)cluster_size();
+        rank = (int)cluster_rank();
+        if (!chunk_item<kTcKeys>(a, quotient(cta, parts), w)) return;  // (the whole cluster, before it holds any TMEM)
+        sh = Shares(w.tiles, parts);
+        w.tile = rank < w.tiles ? sh.begin(rank) : 0;
+        n = rank < w.tiles ? sh.begin(rank + 1) - w.tile : 0;
+    } else {
+        const int total = chunk_plan<kTcKeys>(a, cum);
+        // (a share is at least kLeast tiles: below, the partials would cost more than the tiles)
+        const int ctas = min((int)gridDim.x, max(1, (total + kLeast - 1) / kLeast));
+        sh = Shares(total, ctas);
+        if (threadIdx.x == 0) a.joins[cta].parts = 0;
+        if (cta >= min(total, ctas)) return;  // (the whole block, before it holds any TMEM)
+        const int u0 = sh.begin(cta);
+        u1 = sh.begin(cta + 1);
+        n = u1 - u0;
+        w = chunk_place<kTcKeys>(a, cum, u0);
+    }
+    float cl_m = -INFINITY, cl_l = 0.f;  // CL: the row's max and sum in this CTA
     if (warp == 1) tc_alloc(&S.tmem, C_TMEM_COLS);
     tc_fence_before();
     __syncthreads();
@@ -295,7 +337,7 @@ __global__ void __launch_bounds__(C_THREADS, 1)
         uint32_t np[2] = {0, 0}, nq[2] = {0, 0};  // uses of bp and bq so far
         int nx = w.toks > tx ? 2 : 1;             // row tiles in use
         int to_go = w.tiles - w.tile;             // tiles of the item from this one on
-        bool first = true, ok = await(&S.bk0, 0);
+        bool first = true, ok = await(&S.bk0, 0) && n > 0;  // (CL: a share may be empty)
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
             if (!ok || x >= nx) break;
@@ -375,7 +417,7 @@ __global__ void __launch_bounds__(C_THREADS, 1)
                 __syncwarp();
             };
             const int count = min(left, y.tiles - y.tile);  // tiles of this item in this CTA
-            if (x == 0 && row == 0 && count == left) a.joins[cta] = chunk_join(a, y, sh, cta, u1, y.tile + count, whole);
+            if (!CL && x == 0 && row == 0 && count == left) a.joins[cta] = chunk_join(a, y, sh, cta, u1, y.tile + count, whole);
             const int rows = min(tx, y.toks - x * tx) * a.group;
             const bool warp_used = 32 * quarter < rows;
             if (rows > 0) {
@@ -501,6 +543,12 @@ __global__ void __launch_bounds__(C_THREADS, 1)
                     const float2 s2 = add2(ls[0], ls[1]);
                     l += s2.x + s2.y;
                 }
+                if constexpr (CL) {
+                    if (ok) ok = __all_sync(0xffffffffu, await_phase(S, &S.bo[x], no++ & 1u, a.err));
+                    cl_m = m2;
+                    cl_l = l;
+                    break;
+                }
                 // the rows' result or partial, once the last P V is done; what needs no wait first
                 const bool result = whole && y.tile + count == y.tiles;
                 const int tok = quotient(min(row, rows - 1), a.group);
@@ -591,6 +639,124 @@ __global__ void __launch_bounds__(C_THREADS, 1)
             whole = true;
         }
     }
+    if constexpr (CL) {
+        // The CTAs' partials of the item: each softmax warp's rows belong to one CTA, which the others push theirs to
+        // (where its operands lay: by the first barrier all products are done).
+        __syncwarp();
+        tc_fence_before();
+        cluster_arrive();
+        cluster_wait();
+        tc_fence_after();
+        const int wi = warp - 2, x = wi >> 2, quarter = warp & 3, row = 32 * quarter + lane;
+        const int of = 8 / parts, block = 4 * x + quarter, owner = block / of;  // of: warps' rows of a CTA
+        const ChunkWork &y = reinterpret_cast<const ChunkWork *>(t + L::WORK)[2 * (wi & 7)];
+        const int rows = min(tx, y.toks - x * tx) * a.group;
+        const bool used = wi >= 0 && 32 * quarter < rows, mine = row < rows;
+        const uint32_t to = tmem + ((uint32_t)(32 * quarter) << 16) + C_O + (uint32_t)(x & 1) * 128;
+        const bool odd = S.odd_[0] == 1;
+        const int tok = used ? quotient(min(row, rows - 1), a.group) : 0;
+        auto values = [&](int c0, float *v) {  // 32 dims of the row's unnormalised o here
+            uint32_t *vi = reinterpret_cast<uint32_t *>(v);
+            tc_ld32_nowait(to + (uint32_t)c0, vi);
+            tc_wait_ld32(vi);
+            if (odd && mine) {  // what is not finite reaches those who see it
+                const int first_pos = y.ch.base + y.tok, last_pos = first_pos + y.toks - 1, my_pos = first_pos + x * tx + tok;
+                for (int j = 0; j < n * kTcKeys; ++j) {
+                    const int p = (y.kt0 + y.tile) * kTcKeys + j, p0 = p & ~(kTcKeys - 1);
+                    if (p0 + kTcKeys - 1 <= first_pos && (a.window == 0 || p0 > (long long)last_pos - a.window)) continue;
+                    if (p > my_pos || p < y.k.lo || (a.window > 0 && p <= (long long)my_pos - a.window)) continue;
+                    const int page = a.kv.table[(long long)y.b * a.kv.max_pages + (p >> a.kv.ps_log2)];
+                    if (page < 0 || page >= a.kv.n_pages) continue;
+                    const T *src = static_cast<const T *>(a.kv.v) + page * a.kv.page_stride +
+                                   ((((long long)y.h << a.kv.ps_log2) + (p & ((1 << a.kv.ps_log2) - 1))) * DH) + c0;
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        const float f = (float)src[i];
+                        if (!(fabsf(f) < INFINITY)) v[i] += f;
+                    }
+                }
+            }
+        };
+        // [other CTA][warp's rows][4 dims][row] and [other CTA][warp's rows][row]
+        auto inbox = [&](int from, int to_cta) { return (from < to_cta ? from : from - 1) * of + block % of; };
+        if (used && owner != rank) {
+            const int slot = inbox(rank, owner);
+            cluster_store(cluster_address(smem_u32(cum) + (uint32_t)(slot * 32 + lane) * 8, owner), make_float2(cl_m, cl_l));
+            if (n > 0) {
+                const uint32_t dst = cluster_address(smem_u32(t + L::Q) + (uint32_t)slot * DH * 128 + (uint32_t)lane * 16, owner);
+#pragma unroll 1
+                for (int c0 = 0; c0 < DH; c0 += 32) {
+                    float v[32];
+                    values(c0, v);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        cluster_store(dst + (uint32_t)(c0 / 4 + i) * 512, make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
+                }
+            }
+        }
+        __syncwarp();
+        cluster_arrive();
+        cluster_wait();
+        if (used && owner == rank) {
+            const float2 *stat = reinterpret_cast<const float2 *>(cum);
+            float mx = cl_m;
+            for (int k = 0; k < parts; ++k)
+                if (k != rank) mx = fmaxf(mx, stat[inbox(k, rank) * 32 + lane].x);
+            const float off = mx == -INFINITY ? 0.f : mx, f_own = ex2(cl_m - off);
+            float sum = f_own * cl_l;
+            for (int k = 0; k < parts; ++k)
+                if (k != rank) {
+                    const float2 z = stat[inbox(k, rank) * 32 + lane];
+                    sum += ex2(z.x - off) * z.y;
+                }
+            const float inv = inverse(sum);
+            const long long q_row = (long long)y.ch.row0 + y.tok + x * tx + tok;
+            const int head = y.h * a.group + (row - tok * a.group);
+            const long long dst = mine ? q_row * a.ld_out + (long long)head * DH : -1;
+            long long to4[4];  // of the rows 8 k + lane / 4
+#pragma unroll
+            for (int k = 0; k < 4; ++k) to4[k] = __shfl_sync(0xffffffffu, dst, 8 * k + lane / 4);
+            uint8_t *stage = t + L::OUT + wi * 32 * L::OUT_ROW;
+            uint4 *own = reinterpret_cast<uint4 *>(stage + lane * L::OUT_ROW);
+            const uint4 *theirs = reinterpret_cast<const uint4 *>(stage + (lane / 4) * L::OUT_ROW + (lane & 3) * 16);
+            T *out = static_cast<T *>(a.out) + (lane & 3) * 8;
+#pragma unroll 1
+            for (int c0 = 0; c0 < DH; c0 += 32) {
+                float v[32];
+                if (n > 0) values(c0, v);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] = n > 0 ? v[i] * f_own : 0.f;
+                for (int k = 0; k < parts; ++k) {
+                    if (k == rank) continue;
+                    const int slot = inbox(k, rank);
+                    const float z = stat[slot * 32 + lane].x;
+                    if (__all_sync(0xffffffffu, z == -INFINITY)) continue;  // (a share without tiles leaves no o)
+                    const float f = ex2(z - off);
+                    const float4 *src = reinterpret_cast<const float4 *>(t + L::Q + slot * DH * 128 + lane * 16);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float4 q = src[(c0 / 4 + i) * 32];
+                        v[4 * i] += f * q.x;
+                        v[4 * i + 1] += f * q.y;
+                        v[4 * i + 2] += f * q.z;
+                        v[4 * i + 3] += f * q.w;
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float *f = v + 8 * i;
+                    own[i] = make_uint4(pack2<T>(f[0] * inv, f[1] * inv), pack2<T>(f[2] * inv, f[3] * inv),
+                                        pack2<T>(f[4] * inv, f[5] * inv), pack2<T>(f[6] * inv, f[7] * inv));
+                }
+                __syncwarp();
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (to4[k] >= 0) *reinterpret_cast<uint4 *>(out + to4[k] + c0) = theirs[k * 8 * L::OUT_ROW / 16];
+                __syncwarp();
+            }
+            if (mine && a.lse) a.lse[q_row * a.n_q + head] = mx * 0.69314718055994530942f + logf(sum);
+        }
+    }
     tc_fence_before();
     __syncthreads();
     if (warp == 1) {
@@ -618,22 +784,26 @@ bool query_map(CUtensorMap *map, const ChunkArgs &a, int dtype) {
 }
 
 template <typename T, int DH>
-lf_status launch_chunk_tc(const ChunkArgs &a, int dtype, cudaStream_t st) {
+lf_status launch_chunk_tc(const ChunkArgs &a, int dtype, int direct, cudaStream_t st) {
     constexpr int smem = CtSmem<DH>::BYTES;
-    if (!set_smem_once<paged_chunk_tc_kernel<T, DH>>(smem)) return LF_ERR_CUDA;
+    if (!set_smem_once<paged_chunk_tc_kernel<T, DH, false>>(smem) || !set_smem_once<paged_chunk_tc_kernel<T, DH, true>>(smem))
+        return LF_ERR_CUDA;
     CUtensorMap mk, mv, mq;
     if (!cache_map(&mk, a.kv.k, a.kv, dtype) || !cache_map(&mv, a.kv.v, a.kv, dtype) || !query_map(&mq, a, dtype))
         return LF_ERR_CUDA;
-    return launch_pdl(paged_chunk_tc_kernel<T, DH>, a.grid, C_THREADS, smem, st, mk, mv, mq, a) ? LF_OK : LF_ERR_CUDA;
+    const bool ok = direct ? launch_pdl_cluster(paged_chunk_tc_kernel<T, DH, true>, (unsigned)direct,
+                                                dim3((unsigned)(chunk_items(a) * direct)), C_THREADS, smem, st, mk, mv, mq, a)
+                           : launch_pdl(paged_chunk_tc_kernel<T, DH, false>, a.grid, C_THREADS, smem, st, mk, mv, mq, a);
+    return ok ? LF_OK : LF_ERR_CUDA;
 }
 
 }  // namespace
 
-lf_status paged_chunk_tc(const ChunkArgs &a, int dtype, cudaStream_t st) {
+lf_status paged_chunk_tc(const ChunkArgs &a, int dtype, int direct, cudaStream_t st) {
     if (dtype == LF_F16)
-        return a.kv.head_dim == 64 ? launch_chunk_tc<__half, 64>(a, dtype, st) : launch_chunk_tc<__half, 128>(a, dtype, st);
-    return a.kv.head_dim == 64 ? launch_chunk_tc<__nv_bfloat16, 64>(a, dtype, st)
-                               : launch_chunk_tc<__nv_bfloat16, 128>(a, dtype, st);
+        return a.kv.head_dim == 64 ? launch_chunk_tc<__half, 64>(a, dtype, direct, st) : launch_chunk_tc<__half, 128>(a, dtype, direct, st);
+    return a.kv.head_dim == 64 ? launch_chunk_tc<__nv_bfloat16, 64>(a, dtype, direct, st)
+                               : launch_chunk_tc<__nv_bfloat16, 128>(a, dtype, direct, st);
 }
 
 }  // namespace lf
