@@ -644,9 +644,44 @@ int direct_parts(const ChunkArgs &a, const MmaPlan &p, int n_sm) {
     return p.each * 10 <= p.items * p.tiles * 10 / ctas + 60 + 3 * std::min(p.tiles, ctas / p.items) ? p.parts : 0;
 }
 
+// CTAs to an item of the tensor-core kernel in a cluster, 0 for the list and its join.  A cluster's start, end and join take
+// as long as 8, 9 or 12 key tiles of a CTA with 1, 2 or 4 CTAs; those of the list as 19, and 4 for each item of a CTA, and its
+// tiles a tenth longer (their partials go through L2).  But the list is even, and of clusters the item with the most keys
+// sets the time; several waves come only of CTAs that take an item each, whose ends overlap.  us, list | clusters
+// of 1, 2, 4, one sequence, 32 heads on 16 of 128 (16 items for 128 new tokens):
+//    128 new, 128 keys  18.7 | 10.9 12.7 14.5    640 keys  23.6 | 16.4 15.1 16.3    16128 keys  46.6 | 180 97 58
+//    256 new, 256 keys  21.6 | 12.7 13.0 14.5   3840 keys  34.8 | 50.8 33.3 27.1    16256 keys  66.2 | 178 98 59
+//    512 new, 512 keys  24.6 | 15.2 15.4 29.6   4096 keys  43.8 | 53.8 36.1 52.4    16512 keys   111 | 181 102 117
+//   1024 new, 1024 keys 33.4 | 23.1 32.6 62.2   4608 keys  67.0 | 62.0 70.5 102     17024 keys   207 | 190 205 235
+// Clusters of 8 find room for eight at most and were the best of one size in a hundred.
+int tc_parts(const ChunkArgs &a, int n_sm) {
+    const long long items = chunk_items(a);
+    const int toks = (a.n_tokens + a.kv.n_seqs - 1) / a.kv.n_seqs;  // tokens of a sequence
+    const int bound = a.window > 0 ? std::min(a.window + a.toks, a.max_len) : a.max_len;
+    const long long tiles = bound / kTcKeys + 1, mean = a.window > 0 ? tiles : std::max(1ll, tiles - toks / (2 * kTcKeys));
+    const long long even = (long long)a.kv.n_seqs * a.kv.n_kv * ((toks + a.toks - 1) / a.toks);
+    long long best = 190 + 11 * even * mean / n_sm + 40 * even / n_sm;
+    int parts = 0;
+    const int fixed[3] = {80, 90, 120};
+    for (int i = 0, k = 1; i < 3; ++i, k *= 2) {
+        const long long room = (k > 1 ? n_sm * 7 / 8 : n_sm) / k;
+        long long t = fixed[i] + 10 * ((tiles + k - 1) / k);
+        if (even <= room)
+            t += items > room ? t / 2 : 0;  // (chunks of uneven lengths may take a second wave)
+        else if (k == 1)
+            t = (items + n_sm - 1) / n_sm * fixed[0] + 10 * items * mean / n_sm + 5 * tiles;
+        else
+            continue;
+        if (t < best) best = t, parts = k;
+    }
+    return parts;
+}
+
 // The tensor cores pay beyond 64 rows of a sequence and KV head, with many sequences from 41 on, but not where one wave of
-// the direct kernel has three key tiles to a CTA at most (two where an item has one CTA).  us, the better of list and
-// clusters | tensor cores, 32 heads on 16 of 128:
+// the direct kernel has three key tiles to a CTA at most (two where an item has one CTA); with few sequences and 41 to 64
+// rows from 4096 keys on; and below 256 keys (with over 256 rows 512) wherever clusters take the items (64 rows of one
+// sequence, 32 keys: 9.0 us where the direct kernel takes 13.8; 512 rows, 356 keys: 14.2 and 19.5).  us, the better of list and clusters | tensor cores by their list, 32 heads
+// on 16 of 128:
 //   1 sequence,    64 rows   512 keys  12.2 | 17.5   4096  26.7 | 25.0     128 rows  512  12.7 | 18.6   4096  26.9 | 26.1
 //   8 sequences,   16 rows   512 keys  15.3 | 21.9   4096  48.4 | 57.2      64 rows  512  22.8 | 23.7   4096  74.7 | 59.5
 //                 128 rows   512 keys  33.7 | 26.2   4096 130.7 | 63.8
@@ -656,33 +691,16 @@ int direct_parts(const ChunkArgs &a, const MmaPlan &p, int n_sm) {
 // 11.1 | 15.5; 32 sequences, 48 rows, 4096 keys 81.8 | 74.1, 512 keys 22.8 | 26.3.
 bool tc_pays(const ChunkArgs &a, int n_sm) {
     const long long rows = rows_of(a);
-    if (!tc_fits(a.kv) || rows <= 40 || (rows <= 64 && (long long)a.kv.n_seqs * a.kv.n_kv < 48)) return false;
+    if (!tc_fits(a.kv) || rows <= 40) return false;
+    const int bound = a.window > 0 ? std::min(a.window + a.toks, a.max_len) : a.max_len;
+    ChunkArgs t = a;
+    shape(t, true, n_sm);
+    if (bound < (rows > 256 ? 4 : 2) * kTcKeys && tc_parts(t, n_sm) > 0) return true;
+    if (rows <= 64 && (long long)a.kv.n_seqs * a.kv.n_kv < 48 && bound < 4096) return false;
     ChunkArgs m = a;
     shape(m, false, n_sm);
     const MmaPlan p = mma_plan(m, n_sm);
     return !(p.one_wave && (p.parts > 1 ? (p.tiles + p.parts - 1) / p.parts <= 3 : p.tiles <= 2));
-}
-
-// CTAs to an item of the tensor-core kernel in a cluster, 0 for the list and its join.  A cluster's start, end and join take
-// as long as 8, 9 or 12 key tiles of a CTA with 1, 2 or 4 CTAs, those of the list as 19, and its tiles a tenth longer (their
-// partials go through L2); but the list is even, and a cluster's item with the most keys sets the time.
-int tc_parts(const ChunkArgs &a, int n_sm) {
-    const long long items = chunk_items(a);
-    const int toks = (a.n_tokens + a.kv.n_seqs - 1) / a.kv.n_seqs;  // tokens of a sequence
-    const int bound = a.window > 0 ? std::min(a.window + a.toks, a.max_len) : a.max_len;
-    const long long tiles = bound / kTcKeys + 1, mean = a.window > 0 ? tiles : std::max(1ll, tiles - toks / (2 * kTcKeys));
-    const long long even = (long long)a.kv.n_seqs * a.kv.n_kv * ((toks + a.toks - 1) / a.toks);
-    long long best = 190 + 11 * even * mean / n_sm;
-    int parts = 0;
-    const int fixed[3] = {80, 90, 120};
-    for (int i = 0, k = 1; i < 3; ++i, k *= 2) {
-        const long long room = (k > 1 ? n_sm * 7 / 8 : n_sm) / k;
-        long long t = fixed[i] + 10 * ((tiles + k - 1) / k);
-        if (even > room) continue;
-        if (items > room) t += t / 2;  // (chunks of uneven lengths may take a second wave)
-        if (t < best) best = t, parts = k;
-    }
-    return parts;
 }
 
 struct CkWs {

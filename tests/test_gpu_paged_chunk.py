@@ -462,3 +462,22 @@ def test_starts_that_claim_all_rows_many_times_over(tokens):
                         page * pages, 0, 0.125, ws.data_ptr(), ws.numel(), err.data_ptr())
     torch.cuda.synchronize()
     assert err.item() == 1 and (out == 9.0).all()
+
+
+@pytest.mark.parametrize("far", [0, 640, 4096])
+@pytest.mark.parametrize("new,ctx,nq,nkv,dim,window", [
+    ([120], [30], 4, 2, 64, 0), ([130, 70], [300, 0], 8, 2, 128, 0), ([100, 1, 60], [900, 5, 0], 4, 1, 64, 0),
+    ([90], [700], 6, 2, 128, 300), ([300], [-20], 3, 1, 128, 0), ([257, 0, 128], [1000, 0, 1], 16, 4, 64, 0),
+])
+def test_a_cluster_to_an_item_on_tensor_cores(new, ctx, nq, nkv, dim, window, far):
+    # far: a bound far above the lengths, so that clusters are larger than their items and some CTAs have no keys
+    c = Case(new, ctx, nq, nkv, dim, 64, "bf16" if dim == 64 else "f16", window, seed=far, pad=1, far=far)
+    c.check(*c.run())
+
+
+def test_a_chunk_alone_and_among_sequences_without_new_tokens():
+    # a chunk alone, and beside so many sequences without new tokens that there is no cluster for an item
+    a = Case([200], [500], 8, 2, 128, 64, "f16", seed=4)
+    b = Case([200] + [0] * 200, [500] + [0] * 200, 8, 2, 128, 64, "f16", seed=4)
+    for c in (a, b):
+        c.check(*c.run())
