@@ -1,9 +1,14 @@
 // lf_attn_paged_chunk on the 5th-generation tensor cores (tcgen05 + TMA + TMEM), for
 // chunks whose rows (token, query head) of one KV head are many.
 //
-// An item is two M = 128 row tiles of consecutive tokens of one sequence and KV head;
-// the list of its tiles of 128 keys and its shares are lf_paged_chunk.h's, one
-// CTA per SM.  Per key tile and row tile x:
+// An item is two M = 128 row tiles of consecutive tokens of one sequence and KV head.
+// Many items: the list of their tiles of 128 keys in even shares (lf_paged_chunk.h),
+// one CTA per SM, and a join behind.  Few: a cluster of 1, 2 or 4 CTAs to an item, an
+// equal share of its tiles each; at the end each softmax warp's 32 rows belong to one
+// of the CTAs, which the others push their partials to (shared memory, where Q, K
+// and V lay), so that nothing goes through L2 and nothing is launched behind.  Which
+// of the two is taken, and both sides' times: tc_parts in lf_paged_chunk.cu.
+// Per key tile and row tile x:
 //   S = Q K^T into TMEM; the row tile's softmax warpgroup, a row per thread,
 //   reads S, moves the row's running max (only when it grows by more than 2^8,
 //   so P stays below 256), and writes P in the cache's type back over S;
@@ -31,9 +36,12 @@
 //
 // What bounds it: over long keys the tensor cores (2 x 2048 new tokens at 14336, 32
 // heads on 16 of 128, bf16: 961 us, 1672 TFLOP/s, their pipe 72 % full; in calls back to
-// back the board's power, 1133 to 1150 us), else the items' starts, ends and joins
-// (512 at 3584: 44 us, 11 of them the join of 215 pieces, its products 17).  Of a
-// softmax warp's 168 registers 128 hold a row's scores.
+// back the board's power, 1120 to 1150 us), else the items' starts and ends (512 at
+// 3584: 35 us by clusters of two, 44 by the list, of which 11 were the join of 215
+// pieces; its products take 17) and, with few rows to an item, the way of a tile
+// from one product through the softmax to the next, 1.7 us (a mixed windowed
+// batch, 144 items: 23.5 us by a CTA to each, 36 by the list).  Of a softmax warp's
+// 168 registers 128 hold a row's scores.
 //
 // Tried: P's first piece of 64 or 32 keys, no better; shares of at least four tiles
 // instead of two, slower for short keys; the key tiles of an item of one row tile in
