@@ -11,7 +11,7 @@
 // leaves partials (unnormalised o, max, sum) and a second launch joins them.  With
 // few keys there is neither list nor second launch: a cluster of CTAs takes an
 // item and joins it through distributed shared memory.  Many rows go to the
-// tensor cores (lf_paged_chunk_tc.cu).
+// tensor cores (lf_paged_chunk_tc.cu), which has both ways too.
 //
 // What bounds it: with few tokens the cache's bytes and, for short ones, the call's
 // fixed parts: 8 sequences of 5 new tokens at 512 positions (32 heads on 16 of
