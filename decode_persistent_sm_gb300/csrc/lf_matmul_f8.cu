@@ -29,6 +29,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <atomic>
 #include <mutex>
 
 #include "lf_paged.h"
@@ -56,9 +57,10 @@ template <int STAGES>
 struct F8Shared {
     uint64_t full[STAGES], empty[STAGES];
     uint64_t acc_full[2], acc_empty[2];  // accumulator b computed / read back (128 arrivals)
+    uint64_t done;                       // every product this CTA issued is done (one commit at the end)
     uint32_t tmem;
     volatile int abort_;
-    volatile int n_acc_[2];  // commits issued on acc_full[b]
+    volatile int issued_;  // 1 once any product was issued (then done gets its commit)
 };
 
 struct F8Args {
@@ -66,6 +68,7 @@ struct F8Args {
     void *c;
     int m, n, k, c_dtype, rows_a;  // rows_a: rows of A's box
     uint32_t *err;
+    unsigned long long limit;  // ns
 };
 
 template <typename S>
@@ -143,9 +146,10 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
         for (int b = 0; b < 2; ++b) {
             mbar_init(&S.acc_full[b], 1);
             mbar_init(&S.acc_empty[b], 128);
-            S.n_acc_[b] = 0;
         }
+        mbar_init(&S.done, 1);
         S.abort_ = 0;
+        S.issued_ = 0;
         fence_barrier_init();
         tma_prefetch_map(&tmA);
         tma_prefetch_map(&tmB);
@@ -157,12 +161,13 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
     const uint32_t tmem = S.tmem;
     pdl_wait();
     pdl_trigger();
-    const uint64_t deadline = global_timer_ns() + kF8TimeoutNs;
+    const uint64_t deadline = global_timer_ns() + a.limit;
+    int kbg = 0;  // the copying lane: stages filled so far (all tiles)
 
     if (warp == 0) {
         if (lane == 0) {
-            int kbg = 0, s = 0;  // stages filled so far (all tiles), and the next one's place
-            uint32_t ph = 1;     // its parity while it is being emptied
+            int s = 0;        // the next one's place
+            uint32_t ph = 1;  // its parity while it is being emptied
             for (int t = blockIdx.x; t < ntiles && !S.abort_; t += gridDim.x) {
                 int m, n;
                 f8_tile_of(t, mt, nt, m, n);
@@ -179,12 +184,6 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
                     if (++s == ST) s = 0, ph ^= 1u;
                 }
             }
-            if (S.abort_) {  // let the copies in flight land before the CTA exits
-                const uint64_t dl = global_timer_ns() + 1000000000ull;
-                for (int k = kbg > ST ? kbg - ST : 0; k < kbg; ++k)
-                    while (!mbar_try_wait(&S.full[k % ST], (k / ST) & 1u) && global_timer_ns() < dl) {
-                    }
-            }
         }
     } else if (warp == 1) {
         // The whole warp walks the loop and one lane issues: what the instructions take stays in uniform registers.  What
@@ -196,7 +195,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
         auto on = [&](uint32_t bytes) { return (desc & 0xffffffff00000000ull) | (uint32_t)((uint32_t)desc + (bytes >> 4)); };
         int lt = 0, s = 0;
         uint32_t ph = 0;
-        bool ok = true;
+        bool ok = true, issued = false;
         for (int t = blockIdx.x; ok && t < ntiles; t += gridDim.x, ++lt) {
             const int b = lt & 1;
             const uint32_t acc = tmem + (uint32_t)b * BN;
@@ -214,14 +213,17 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
                     tc_commit(&S.empty[s]);
                 }
                 __syncwarp();
+                issued = true;
                 if (++s == ST) s = 0, ph ^= 1u;
             }
-            if (ok && leader) {
-                tc_commit(&S.acc_full[b]);
-                S.n_acc_[b] = (lt >> 1) + 1;
-            }
+            if (ok && leader) tc_commit(&S.acc_full[b]);
             __syncwarp();
         }
+        if (leader && issued) {
+            tc_commit(&S.done);  // tracks everything issued above
+            S.issued_ = 1;
+        }
+        __syncwarp();
     } else {  // warp w reads TMEM lanes 32 * (w % 4) .. + 31
         const int q = warp & 3;
         int lt = 0;
@@ -259,13 +261,19 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
     }
     tc_fence_before();
     __syncthreads();
+    // A CTA that gave up has copies and products under way, whichever of its warps gave up first, and in the middle of a tile
+    // too: both end (bounded) before it does.
+    if (warp == 0 && lane == 0 && S.abort_) {
+        const uint64_t dl = global_timer_ns() + 1000000000ull;
+        for (int k = kbg > ST ? kbg - ST : 0; k < kbg; ++k)
+            while (!mbar_try_wait(&S.full[k % ST], (k / ST) & 1u) && global_timer_ns() < dl) {
+            }
+    }
     if (warp == 1) {
-        if (S.abort_ && lane == 0) {  // MMAs may still run: wait (bounded) for their last commits
+        if (lane == 0 && S.issued_) {
             const uint64_t dl = global_timer_ns() + 1000000000ull;
-            for (int b = 0; b < 2; ++b)
-                if (S.n_acc_[b] > 0)
-                    while (!mbar_try_wait(&S.acc_full[b], (S.n_acc_[b] - 1) & 1u) && global_timer_ns() < dl) {
-                    }
+            while (!mbar_try_wait(&S.done, 0) && global_timer_ns() < dl) {
+            }
         }
         __syncwarp();
         tc_fence_after();
@@ -276,6 +284,9 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
 using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// The limit of a wait.
+std::atomic<unsigned long long> f8_limit{kF8TimeoutNs};
 
 EncodeTiled encoder() {
     static EncodeTiled fn = nullptr;
@@ -338,7 +349,8 @@ extern "C" lf_status lf_matmul_f8(const void *a_device, const float *a_scale_dev
         (void)cudaGetLastError();
         return LF_ERR_CUDA;
     }
-    const lf::F8Args a = {a_scale_device, b_scale_device, c_device, m, n, k, c_dtype, 0, err_device};
+    const lf::F8Args a = {a_scale_device, b_scale_device, c_device, m, n, k, c_dtype, 0, err_device,
+                          lf::f8_limit.load(std::memory_order_relaxed)};
     cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
     // The width whose waves over the SMs take the least: a tile of 256, 128 and 64 columns takes as 12 : 7.2 : 5.
     // us by width 64 | 128 | 256, K 4096:
@@ -351,4 +363,14 @@ extern "C" lf_status lf_matmul_f8(const void *a_device, const float *a_scale_dev
     if (c256 <= c128 && c256 <= c64) return lf::launch_f8<256, 128, 1>(a_device, b_device, a, n_sm, st);
     if (c128 <= c64) return lf::launch_f8<128, 128, 2>(a_device, b_device, a, n_sm, st);
     return m <= 32 ? lf::launch_f8<64, 32, 2>(a_device, b_device, a, n_sm, st) : lf::launch_f8<64, 128, 2>(a_device, b_device, a, n_sm, st);
+}
+
+extern "C" lf_status lf_debug_matmul_f8_wait(uint64_t limit_ns) {
+    if (limit_ns > lf::kF8TimeoutNs) return LF_ERR_INVALID_ARG;
+#ifdef LF_DEBUG
+    lf::f8_limit.store(limit_ns, std::memory_order_relaxed);
+    return LF_OK;
+#else
+    return LF_ERR_UNSUPPORTED;
+#endif
 }

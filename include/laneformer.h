@@ -740,6 +740,9 @@ lf_status lf_token_logprobs(const void *logits_device, int dtype, int rows, int 
  * lf_sample_filtered (at most 2 s, the usual one) and has the CTA `rank` of each row (-1: every CTA) give up
  * in its nth wait (0: in none), so that a test can see a wait run out.
  *
+ * lf_debug_matmul_f8_wait sets, for this process, the limit of the waits of lf_matmul_f8 (at most 2 s, the usual one), so
+ * that a test can see one run out.
+ *
  * lf_debug_fail_alloc lets the nth (0: none) of the places where the next
  * lf_batch_begin or lf_batch_begin_shared allocates host memory find none.
  * lf_debug_batch_error writes the error word of the current batch, as its kernels
@@ -749,6 +752,7 @@ lf_status lf_token_logprobs(const void *logits_device, int dtype, int rows, int 
 lf_status lf_debug_canaries(lf_engine *e, int *n_guarded);
 lf_status lf_debug_corrupt_canary(lf_engine *e, int i, int back);
 lf_status lf_debug_sample_wait(uint64_t limit_ns, int rank, int nth);
+lf_status lf_debug_matmul_f8_wait(uint64_t limit_ns);
 lf_status lf_debug_fail_alloc(int nth);
 lf_status lf_debug_batch_error(lf_engine *e, uint32_t word);
 
