@@ -23,8 +23,8 @@
 // The accumulators are full fp32: a sum of 4096 products that spread over 2^30 in
 // size comes out to 2^-23 of its terms' magnitude.
 //
-// Every wait is bounded: on a timeout the CTA records an error, lets its copies
-// and MMAs in flight finish (bounded), frees TMEM and exits.
+// Every wait is bounded (2 s without progress): on a timeout the CTA records an error,
+// lets its copies and MMAs in flight finish (bounded), frees TMEM and exits.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -68,16 +68,25 @@ struct F8Args {
     void *c;
     int m, n, k, c_dtype, rows_a;  // rows_a: rows of A's box
     uint32_t *err;
-    unsigned long long limit;  // ns
+    unsigned long long limit;  // of a wait, in ns
 };
 
+// The limit is a wait's, from its first failed try on (of up to 20 us, which costs most waits no look at the clock).
+// `moves`: a barrier whose phases go by while what is waited for comes nearer (a whole tile's products may take longer than
+// the limit): then the limit counts from its last change that was seen.
 template <typename S>
-__device__ __forceinline__ bool f8_wait(S &s, uint64_t *bar, uint32_t parity, uint64_t deadline, uint32_t *err) {
-    if (mbar_test_wait(bar, parity)) return true;
+__device__ __forceinline__ bool f8_wait(S &s, uint64_t *bar, uint32_t parity, const F8Args &a, uint64_t *moves = nullptr) {
+    if (mbar_test_wait(bar, parity) || mbar_try_wait(bar, parity)) return true;
+    uint64_t deadline = global_timer_ns() + a.limit;
+    bool phase = moves && mbar_test_wait(moves, 0);
     while (!mbar_try_wait(bar, parity)) {
         if (s.abort_) return false;
-        if (global_timer_ns() > deadline) {
-            atomicExch(err, 2u);
+        const uint64_t now = global_timer_ns();
+        if (moves && mbar_test_wait(moves, 0) != phase) {
+            phase = !phase;
+            deadline = now + a.limit;
+        } else if (now > deadline) {
+            atomicExch(a.err, 2u);
             s.abort_ = 1;
             return false;
         }
@@ -161,7 +170,6 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
     const uint32_t tmem = S.tmem;
     pdl_wait();
     pdl_trigger();
-    const uint64_t deadline = global_timer_ns() + a.limit;
     int kbg = 0;  // the copying lane: stages filled so far (all tiles)
 
     if (warp == 0) {
@@ -172,7 +180,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
                 int m, n;
                 f8_tile_of(t, mt, nt, m, n);
                 for (int kb = 0; kb < nk; ++kb, ++kbg) {
-                    if (kbg >= ST && !f8_wait(S, &S.empty[s], ph, deadline, a.err)) break;
+                    if (kbg >= ST && !f8_wait(S, &S.empty[s], ph, a)) break;
                     uint8_t *st = tiles + s * L::STAGE;
                     mbar_arrive_expect_tx(&S.full[s], KS * (a.rows_a * F8_BK + L::B));
 #pragma unroll
@@ -199,9 +207,9 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
         for (int t = blockIdx.x; ok && t < ntiles; t += gridDim.x, ++lt) {
             const int b = lt & 1;
             const uint32_t acc = tmem + (uint32_t)b * BN;
-            if (lt >= 2 && !__all_sync(0xffffffffu, f8_wait(S, &S.acc_empty[b], ((lt >> 1) - 1) & 1u, deadline, a.err))) break;
+            if (lt >= 2 && !__all_sync(0xffffffffu, f8_wait(S, &S.acc_empty[b], ((lt >> 1) - 1) & 1u, a))) break;
             for (int kb = 0; kb < nk; ++kb) {
-                ok = __all_sync(0xffffffffu, f8_wait(S, &S.full[s], ph, deadline, a.err));
+                ok = __all_sync(0xffffffffu, f8_wait(S, &S.full[s], ph, a));
                 if (!ok) break;
                 tc_fence_after();
                 if (leader) {
@@ -232,7 +240,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
             f8_tile_of(t, mt, nt, m, n);
             const int b = lt & 1, row = m * F8_BM + 32 * q + lane;
             const float ra = row < a.m && a.sa ? a.sa[row] : 1.f;
-            if (!__all_sync(0xffffffffu, f8_wait(S, &S.acc_full[b], (lt >> 1) & 1u, deadline, a.err))) break;
+            if (!__all_sync(0xffffffffu, f8_wait(S, &S.acc_full[b], (lt >> 1) & 1u, a, &S.empty[0]))) break;
             tc_fence_after();
             const uint32_t tacc = tmem + (uint32_t)b * BN + ((uint32_t)(32 * q) << 16);
 #pragma unroll 1

@@ -638,7 +638,8 @@ lf_status lf_add_rmsnorm(const void *x_device, int x_dtype, int64_t ld_x, const 
  * (LF_F32, LF_F16 or LF_BF16).  k is a multiple of 16; m or n 0 does nothing.  The
  * products are summed in fp32 by the tensor core, scaled and rounded once; a value
  * beyond c_dtype's range becomes infinite.  *err_device (DEVICE word, cleared by the
- * caller) becomes non-zero if a device-side wait ran out (2 s).
+ * caller) becomes 2 if a device-side wait ran out (2 s without progress, however long the
+ * call takes in all); c is then unfinished.
  * LF_ERR_INVALID_ARG for bad sizes, pointers or types; LF_ERR_UNSUPPORTED where
  * m + 128 or n + 256 pass 2^31 or c has more than 2^31 tiles. */
 lf_status lf_matmul_f8(const void *a_device, const float *a_scale_device, const void *b_device,
