@@ -346,8 +346,9 @@ extern "C" lf_status lf_matmul_f8(const void *a_device, const float *a_scale_dev
         !lf::aligned16(a_device) || !lf::aligned16(b_device) || off(c_device, bytes) || off(a_scale_device, 4) ||
         off(b_scale_device, 4) || off(err_device, 4))
         return LF_ERR_INVALID_ARG;
-    // coordinates and tile numbers are 32-bit (the narrowest tiles are 64 wide)
-    if (m > INT32_MAX - 128 || n > INT32_MAX - 256 || k > INT32_MAX - 128 ||
+    // coordinates and tile numbers are 32-bit (the narrowest tiles are 64 wide; the last stage's two blocks end up to 255
+    // values behind K)
+    if (m > INT32_MAX - 128 || n > INT32_MAX - 256 || k > INT32_MAX - 256 ||
         ((long long)m / 128 + 1) * ((long long)n / 64 + 1) + 4096 > INT32_MAX)
         return LF_ERR_UNSUPPORTED;
     if (m == 0 || n == 0) return LF_OK;

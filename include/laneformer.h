@@ -641,7 +641,7 @@ lf_status lf_add_rmsnorm(const void *x_device, int x_dtype, int64_t ld_x, const 
  * caller) becomes 2 if a device-side wait ran out (2 s without progress, however long the
  * call takes in all); c is then unfinished.
  * LF_ERR_INVALID_ARG for bad sizes, pointers or types; LF_ERR_UNSUPPORTED where
- * m + 128 or n + 256 pass 2^31 or c has more than 2^31 tiles. */
+ * m + 128, n + 256 or k + 256 pass 2^31 or c has more than 2^31 tiles. */
 lf_status lf_matmul_f8(const void *a_device, const float *a_scale_device, const void *b_device,
                        const float *b_scale_device, void *c_device, int c_dtype, int m, int n, int k,
                        uint32_t *err_device, void *cuda_stream);
