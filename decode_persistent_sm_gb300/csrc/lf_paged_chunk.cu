@@ -808,10 +808,10 @@ extern "C" lf_status lf_attn_paged_chunk(const lf_paged_kv *kv, const void *q_de
     a.max_len = max_len;
     a.window = window >= max_len ? 0 : window;  // (every position lies less than max_len back)
     lf::shape(a, lf::tc_pays(a, n_sm), n_sm);
-    // tiles are counted in 32 bits
+    // tiles are counted in 32 bits: those of the items that the new tokens can have (a sequence without any has none)
     const int kt = a.tc ? lf::kTcKeys : lf::tile_keys(kv->head_dim);
-    if (((long long)n_tokens / a.toks + kv->n_seqs) * ((long long)max_len / kt + 2) * kv->n_kv_heads > INT_MAX)
-        return LF_ERR_UNSUPPORTED;
+    const long long items = lf::chunk_items(a);
+    if (items > INT_MAX || items * (max_len / kt + 2) > INT_MAX) return LF_ERR_UNSUPPORTED;
     if (n_tokens == 0) return LF_OK;
     const lf::CkWs w = lf::ck_layout(a);
     uint8_t *ws = static_cast<uint8_t *>(workspace_device);

@@ -263,8 +263,8 @@ __device__ __forceinline__ bool chunk_item(const ChunkArgs &a, int id, ChunkWork
     return true;
 }
 
-// The items that the chunks can have at most, a cluster to each (a chunk of c tokens has 1 + (c - 1) / toks row tiles; those
-// without an item leave at once).
+// The items that the chunks can have at most, in the list or a cluster to each (a chunk of c tokens has 1 + (c - 1) / toks
+// row tiles; clusters without an item leave at once).
 inline long long chunk_items(const ChunkArgs &a) {
     const int some = a.n_tokens < a.kv.n_seqs ? a.n_tokens : a.kv.n_seqs;  // sequences with new tokens
     return (long long)a.kv.n_kv * (some + (a.n_tokens - some) / a.toks);

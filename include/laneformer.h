@@ -682,7 +682,8 @@ lf_status lf_matmul_f8(const void *a_device, const float *a_scale_device, const 
  * LF_ERR_INVALID_ARG for bad sizes, pointers, strides or types, max_len above
  * max_pages * page_size, or a workspace too small; LF_ERR_UNSUPPORTED for head_dim
  * other than 32, 64 or 128, more than 16 query heads per KV head, more than 1024
- * sequences, or n_tokens * max_len * n_q_heads above about 2^41. */
+ * sequences, or more than 2^31 key tiles of the items that n_tokens may have (never where
+ * n_tokens * (max_len + 128) * n_kv_heads is below 2^37). */
 lf_status lf_attn_paged_chunk(const lf_paged_kv *kv, const void *q_device, int64_t ld_q, void *out_device,
                               int64_t ld_out, float *lse_device, int n_q_heads, const int32_t *starts_device,
                               int n_tokens, const int32_t *lens_device, int max_len, int window, float scale,
