@@ -765,6 +765,10 @@ lf_status launch_chunk(const ChunkArgs &a, int direct, cudaStream_t st) {
     return ok ? LF_OK : LF_ERR_CUDA;
 }
 
+#ifdef LF_DEBUG
+std::atomic<int> g_lose_cta{-1}, g_lose_warp{0}, g_lose_wait{0};
+#endif
+
 template <typename T>
 lf_status launch_chunk_dim(const ChunkArgs &a, int direct, cudaStream_t st) {
     return a.kv.head_dim == 32   ? launch_chunk<T, 32>(a, direct, st)
@@ -828,8 +832,25 @@ extern "C" lf_status lf_attn_paged_chunk(const lf_paged_kv *kv, const void *q_de
     a.lens = lens_device;
     a.scale_log2 = scale * lf::kLog2e;
     a.err = err_device;
+#ifdef LF_DEBUG
+    a.lose_cta = lf::g_lose_cta;
+    a.lose_warp = lf::g_lose_warp;
+    a.lose_wait = lf::g_lose_wait;
+#endif
     const int direct = a.tc ? lf::tc_parts(a, n_sm) : lf::direct_parts(a, lf::mma_plan(a, n_sm), n_sm);
     cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
     return kv->dtype == LF_F16 ? lf::launch_chunk_dim<__half>(a, direct, st)
                                : lf::launch_chunk_dim<__nv_bfloat16>(a, direct, st);
+}
+
+extern "C" lf_status lf_debug_chunk_wait(int cta, int warp, int nth) {
+    if (cta < -1 || warp < 0 || warp > 9 || nth < 0) return LF_ERR_INVALID_ARG;
+#ifdef LF_DEBUG
+    lf::g_lose_cta = cta;
+    lf::g_lose_warp = warp;
+    lf::g_lose_wait = nth;
+    return LF_OK;
+#else
+    return LF_ERR_UNSUPPORTED;
+#endif
 }

@@ -36,6 +36,9 @@ struct ChunkArgs {
     float *part_o;     // [2 grid][slot_rows][head_dim], unnormalised
     float2 *part_ml;   // [2 grid][slot_rows] (max in the log2 domain, sum)
     uint32_t *err;
+#ifdef LF_DEBUG
+    int lose_cta, lose_warp, lose_wait;  // tensor cores' kernel: this warp of this CTA (-1: of each) gives up in its lose_wait-th wait (0: none)
+#endif
 };
 
 // The new tokens of a sequence.

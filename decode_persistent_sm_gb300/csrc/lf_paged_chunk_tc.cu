@@ -82,20 +82,31 @@ struct CtShared {
     volatile int odd_[8];   // item it's masked tiles hold values that are not finite: odd_[it & 7] is it + 1
 };
 
-// (The limit counts from the first probe that fails: a wait that is over costs no look at the clock.)
-__device__ __forceinline__ bool await_phase(CtShared &S, uint64_t *bar, uint32_t parity, uint32_t *err) {
-    if (mbar_test_wait(bar, parity)) return true;
-    const uint64_t deadline = global_timer_ns() + kChunkTimeoutNs;
-    while (!mbar_try_wait(bar, parity)) {
-        if (S.abort_) return false;
-        if (global_timer_ns() > deadline) {
-            atomicExch(err, 2u);
-            S.abort_ = 1;
-            return false;
+// A thread's waits.  (The limit counts from the first probe that fails: a wait that is over costs no look at the clock.)
+struct CtWaits {
+    CtShared &S;
+    uint32_t *err;
+#ifdef LF_DEBUG
+    int lose;  // it gives up in this wait from here on
+#endif
+    __device__ __forceinline__ bool operator()(uint64_t *bar, uint32_t parity) {
+#ifdef LF_DEBUG
+        if (--lose == 0) return give_up();
+#endif
+        if (mbar_test_wait(bar, parity)) return true;
+        const uint64_t deadline = global_timer_ns() + kChunkTimeoutNs;
+        while (!mbar_try_wait(bar, parity)) {
+            if (S.abort_) return false;
+            if (global_timer_ns() > deadline) return give_up();
         }
+        return true;
     }
-    return true;
-}
+    __device__ __forceinline__ bool give_up() {
+        atomicExch(err, 2u);
+        S.abort_ = 1;
+        return false;
+    }
+};
 
 // (x, y) * c + d and x + y, two values to an instruction
 __device__ __forceinline__ float2 fma2(float2 x, float2 c, float2 d) {
@@ -218,6 +229,11 @@ __global__ void __launch_bounds__(C_THREADS, 1)
         w = chunk_place<kTcKeys>(a, cum, u0);
     }
     float cl_m = -INFINITY, cl_l = 0.f;  // CL: the row's max and sum in this CTA
+    CtWaits waits{S, a.err};
+#ifdef LF_DEBUG
+    waits.lose = (a.lose_cta < 0 || a.lose_cta == cta) && a.lose_warp == warp ? a.lose_wait : 0;
+#endif
+    int started = 0, loads[2] = {0, 0};  // the copying warp: loads on bl and on bq so far
     if (warp == 1) tc_alloc(&S.tmem, C_TMEM_COLS);
     tc_fence_before();
     __syncthreads();
@@ -230,7 +246,6 @@ __global__ void __launch_bounds__(C_THREADS, 1)
         struct Box {
             int h, page, row;
         };
-        int started = 0;  // loads on bl so far
         auto place = [&] {  // this lane's box of w's tile
             const int at = (w.kt0 + w.tile) * kTcKeys + lane * box;
             Box x;
@@ -269,7 +284,6 @@ __global__ void __launch_bounds__(C_THREADS, 1)
         Box now = place(), then = now;
         Queries q_now = queries_of(), q_then = q_now;
         bool fresh_now = true, fresh_then = false;  // tile j, tile j + 1 begin an item
-        int loads[2] = {0, 0};                      // on bq so far
         if (lane == 0) mbar_arrive_expect_tx(&S.bk0, L::TILE);
         __syncwarp();
         load(L::K, &tmK, now, &S.bk0);
@@ -282,7 +296,7 @@ __global__ void __launch_bounds__(C_THREADS, 1)
             }
             // their buffers are free once the S products of tile j - 1 and the P V products of tile j - 2 are done, and so
             // are the queries of the item before
-            if (j >= 1) ok = await_phase(S, &S.bf[(j - 1) & 1], ((j - 1) >> 1) & 1u, a.err);
+            if (j >= 1) ok = waits(&S.bf[(j - 1) & 1], ((j - 1) >> 1) & 1u);
             if (!__all_sync(0xffffffffu, ok)) break;
             if (fresh_now) {
                 load_queries(q_now);
@@ -298,17 +312,6 @@ __global__ void __launch_bounds__(C_THREADS, 1)
             now = then;
             q_now = q_then;
             fresh_now = fresh_then;
-        }
-        if (S.abort_ && lane == 0) {  // let the copies in flight land
-            const uint64_t dl = global_timer_ns() + 1000000000ull;
-            while (!mbar_try_wait(&S.bk0, 0) && global_timer_ns() < dl) {
-            }
-            for (int x = 0; x < 2; ++x)
-                while (loads[x] > 0 && !mbar_try_wait(&S.bq[x], (loads[x] - 1) & 1u) && global_timer_ns() < dl) {
-                }
-            for (int i = max(0, started - 2); i < started; ++i)
-                while (!mbar_try_wait(&S.bl[i & 1], (i >> 1) & 1u) && global_timer_ns() < dl) {
-                }
         }
     } else if (warp == 1) {
         // products, issued in order by one lane (the whole warp walks along: what the instructions take stays in uniform
@@ -338,7 +341,7 @@ __global__ void __launch_bounds__(C_THREADS, 1)
                               on(v, (uint32_t)kk * 16 * 128), kIdescO, (!first || kk > 0) ? 1u : 0u);
         };
         auto await = [&](uint64_t *bar, uint32_t parity) {
-            const bool got = __all_sync(0xffffffffu, await_phase(S, bar, parity, a.err));
+            const bool got = __all_sync(0xffffffffu, waits(bar, parity));
             tc_fence_after();
             return got;
         };
@@ -442,7 +445,7 @@ __global__ void __launch_bounds__(C_THREADS, 1)
                     const bool full = j >= full_from && j < full_to;
                     if (!full && x == 0) {  // V of this tile: a key per thread
                         const int vj = at_tile + j, key = j * kTcKeys + row;
-                        ok = ok && await_phase(S, &S.bl[vj & 1], (vj >> 1) & 1u, a.err);
+                        ok = ok && waits(&S.bl[vj & 1], (vj >> 1) & 1u);
                         if (ok) {
                             const bool none = key < lo || key >= hi;
                             uint8_t *v = t + L::V + (vj & 1) * L::TILE + row * 128;
@@ -471,7 +474,7 @@ __global__ void __launch_bounds__(C_THREADS, 1)
                             fence_proxy_async_shared();
                         }
                     }
-                    ok = __all_sync(0xffffffffu, ok && await_phase(S, &S.bs[x], ns & 1u, a.err));
+                    ok = __all_sync(0xffffffffu, ok && waits(&S.bs[x], ns & 1u));
                     if (!ok) break;
                     tc_fence_after();
                     if (!warp_used) {  // (rows of nobody: whatever their P is)
@@ -552,7 +555,7 @@ __global__ void __launch_bounds__(C_THREADS, 1)
                     l += s2.x + s2.y;
                 }
                 if constexpr (CL) {
-                    if (ok) ok = __all_sync(0xffffffffu, await_phase(S, &S.bo[x], no++ & 1u, a.err));
+                    if (ok) ok = __all_sync(0xffffffffu, waits(&S.bo[x], no++ & 1u));
                     cl_m = m2;
                     cl_l = l;
                     break;
@@ -570,7 +573,7 @@ __global__ void __launch_bounds__(C_THREADS, 1)
 #pragma unroll
                 for (int k = 0; k < 4; ++k) to4[k] = __shfl_sync(0xffffffffu, dst, 8 * k + lane / 4);
                 if (left > count) next_item();
-                if (ok) ok = __all_sync(0xffffffffu, await_phase(S, &S.bo[x], no++ & 1u, a.err));
+                if (ok) ok = __all_sync(0xffffffffu, waits(&S.bo[x], no++ & 1u));
                 // (the products behind bo waited for every cleaned tile of the item: its flag is final from here on)
                 const bool odd = S.odd_[it & 7] == it + 1;
                 if (ok && warp_used) {
@@ -767,6 +770,18 @@ __global__ void __launch_bounds__(C_THREADS, 1)
     }
     tc_fence_before();
     __syncthreads();
+    // After an error copies may be in flight, whichever warp gave up and whenever: they land (bounded) before the CTA ends.
+    if (warp == 0 && lane == 0 && S.abort_) {
+        const uint64_t dl = global_timer_ns() + 1000000000ull;
+        while (!mbar_try_wait(&S.bk0, 0) && global_timer_ns() < dl) {
+        }
+        for (int x = 0; x < 2; ++x)
+            while (loads[x] > 0 && !mbar_try_wait(&S.bq[x], (loads[x] - 1) & 1u) && global_timer_ns() < dl) {
+            }
+        for (int i = max(0, started - 2); i < started; ++i)
+            while (!mbar_try_wait(&S.bl[i & 1], (i >> 1) & 1u) && global_timer_ns() < dl) {
+            }
+    }
     if (warp == 1) {
         if (lane == 0 && S.issued_) {  // the products may still run after an error: wait (bounded)
             const uint64_t dl = global_timer_ns() + 1000000000ull;

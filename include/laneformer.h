@@ -743,7 +743,8 @@ lf_status lf_token_logprobs(const void *logits_device, int dtype, int rows, int 
  * in its nth wait (0: in none), so that a test can see a wait run out.
  *
  * lf_debug_matmul_f8_wait sets, for this process, the limit of the waits of lf_matmul_f8 (at most 2 s, the usual one), so
- * that a test can see one run out.
+ * that a test can see one run out.  lf_debug_chunk_wait has a warp (0 to 9) of one CTA (-1: of each) of
+ * lf_attn_paged_chunk's tensor-core kernel give up in its nth wait (0: in none).
  *
  * lf_debug_fail_alloc lets the nth (0: none) of the places where the next
  * lf_batch_begin or lf_batch_begin_shared allocates host memory find none.
@@ -755,6 +756,7 @@ lf_status lf_debug_canaries(lf_engine *e, int *n_guarded);
 lf_status lf_debug_corrupt_canary(lf_engine *e, int i, int back);
 lf_status lf_debug_sample_wait(uint64_t limit_ns, int rank, int nth);
 lf_status lf_debug_matmul_f8_wait(uint64_t limit_ns);
+lf_status lf_debug_chunk_wait(int cta, int warp, int nth);
 lf_status lf_debug_fail_alloc(int nth);
 lf_status lf_debug_batch_error(lf_engine *e, uint32_t word);
 
