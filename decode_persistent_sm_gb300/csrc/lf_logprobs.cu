@@ -24,7 +24,7 @@
 // What bounds it: HBM for many rows of fp32, the call and the second look for few
 // (300 x 50257, two thirds masked, in 19.9 us, of which 9 are the bytes; 1 x 32000 with
 // five of the most probable tokens in 6.5, 4.3 without), the instructions of a logit for 16
-// bits (2048 x 131072 bf16 in 105.9 us, 75 % of the copy rate; 71 % of the issue
+// bits (2048 x 131072 bf16 in 105.9 us, 75 % of the copy rate; 74 % of the issue
 // slots are taken).  Batches of two pieces took 110.6 us there; one stage more or
 // batches of four pieces took no less.
 #include <cooperative_groups.h>

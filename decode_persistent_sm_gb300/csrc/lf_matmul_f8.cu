@@ -8,12 +8,13 @@
 // buffers), and four warps read a finished accumulator back, scale it and store
 // it while the next tile's products run.
 //
-// What bounds it: with many rows the operands' way from shared memory into the
-// products (a block of 128 x 256 x 128 reads 48 KB in the 256 cycles that its
-// products take; a narrower tile reads more per product), 3584 x 8192 x 4096 in 90 us,
-// 2660 TFLOP/s; with few rows the weights' stream, 16 x 8192 x 4096 in 10.0 us, of
-// which 5 are the call (6.7 TB/s per further byte).  So BN is 256 where the tiles
-// fill the SMs, and less where they do not or the stream has to be spread over them.
+// What bounds it: with many rows no unit is full, 3584 x 8192 x 4096 in 90 us, 2660
+// TFLOP/s (84 alone: tensor pipe 61 % active, shared memory's banks read and written
+// 24 % of their peak each, issue slots 10 %, DRAM 9 %).  With few rows it is a CTA's
+// walk along K, which nobody shares, and the weights' stream: 16 x 8192 x 4096 in 10.0
+// us, but 16 x 1024, an eighth of the weights, from HBM in 4.2, 4.7, 9.4 and 14.5 with K
+// 256 (the call), 1024, 4096 and 8192.  So BN is 256 where the tiles fill the SMs, and less
+// where they do not or the stream has to be spread over them.
 //
 // With few rows a block of 128 along K is over in less time than a barrier's round
 // trip: two blocks to a stage (KS) took 16 x 8192 x 4096 from 12.9 us to 10.1.  A stage
@@ -362,7 +363,7 @@ extern "C" lf_status lf_matmul_f8(const void *a_device, const float *a_scale_dev
                           lf::f8_limit.load(std::memory_order_relaxed)};
     cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
     // The width whose waves over the SMs take the least: a tile of 256, 128 and 64 columns takes as 12 : 7.2 : 5.
-    // us by width 64 | 128 | 256, K 4096:
+    // us by width 64 | 128 | 256, K 4096 (no other K was measured; no K is split):
     //   n  8192, m  128  10.4 | 12.4 | 17.6    200  15.0 | 12.6 | 17.6     384  20.6 | 19.5 | 17.8    1024  43.0 | 34.0 | 29.4
     //   n 14336, m   16  14.2 | 14.2 | 17.8    384  32.3 | 27.9 | 31.0     512  38.7 | 29.1 | 31.5    1024  72.6 | 52.0 | 44.5
     //   n  1024, m   16   8.1 |  8.9 | 13.2

@@ -638,7 +638,8 @@ MmaPlan mma_plan(const ChunkArgs &a, int n_sm) {
 //   1 sequence   512 keys  10.2 | 13.1  9.8  8.2  7.7    4096 keys  22.9 | 63.8 35.3 21.0 15.7
 //   8 sequences  512 keys  15.8 | 15.3 13.4 18.4 27.3    4096 keys  49.4 | 70.9 46.6 52.3 61.2
 // and 16 rows (8 new tokens), 32 sequences: 512 keys 39.7 | 39.0 51.0 70.8 124, 4096 keys 171 | 176 190 189 236.
-// Over 404 sizes this rule and tc_pays' together lose 2 % to the best choice of each.
+// Over 404 sizes this rule and tc_pays' together lose 2 % to the best choice of each.  These were batches of equal chunks and
+// lengths, without windows; all the host knows of others is their mean, see tc_pays.
 int direct_parts(const ChunkArgs &a, const MmaPlan &p, int n_sm) {
     const long long ctas = (long long)n_sm * CK_CTAS_PER_SM;
     return p.each * 10 <= p.items * p.tiles * 10 / ctas + 60 + 3 * std::min(p.tiles, ctas / p.items) ? p.parts : 0;
@@ -653,6 +654,7 @@ int direct_parts(const ChunkArgs &a, const MmaPlan &p, int n_sm) {
 //    256 new, 256 keys  21.6 | 12.7 13.0 14.5   3840 keys  34.8 | 50.8 33.3 27.1    16256 keys  66.2 | 178 98 59
 //    512 new, 512 keys  24.6 | 15.2 15.4 29.6   4096 keys  43.8 | 53.8 36.1 52.4    16512 keys   111 | 181 102 117
 //   1024 new, 1024 keys 33.4 | 23.1 32.6 62.2   4608 keys  67.0 | 62.0 70.5 102     17024 keys   207 | 190 205 235
+// (Equal chunks and lengths: 200 sizes.)
 // Clusters of 8 find room for eight at most and were the best of one size in a hundred.
 int tc_parts(const ChunkArgs &a, int n_sm) {
     const long long items = chunk_items(a);
@@ -689,6 +691,9 @@ int tc_parts(const ChunkArgs &a, int n_sm) {
 //                  64 rows   512 keys  58.9 | 52.1   4096 246   | 187
 // and 24 on 8 of 64: 1 sequence, 96 rows, 512 keys 10.0 | 13.8; 8 sequences, 48 rows, 4096 keys 28.9 | 28.4, 512 keys
 // 11.1 | 15.5; 32 sequences, 48 rows, 4096 keys 81.8 | 74.1, 512 keys 22.8 | 26.3.
+// One choice for the batch, by the mean rows of a sequence, those without new tokens among them: a chunk of 512 at 3584 (35
+// us alone) takes 260 us on warp-level MMAs in a batch of 64 places whose others are without new tokens, and beside 63
+// single tokens at 512 to 3584 (164 us by themselves) 270.
 bool tc_pays(const ChunkArgs &a, int n_sm) {
     const long long rows = rows_of(a);
     if (!tc_fits(a.kv) || rows <= 40) return false;

@@ -34,8 +34,8 @@
 // shared memory, 64 bytes of a row to four lanes.  Both together took 512 new tokens
 // at 3584 from 54 us to 45.
 //
-// What bounds it: over long keys the tensor cores (2 x 2048 new tokens at 14336, 32
-// heads on 16 of 128, bf16: 961 us, 1672 TFLOP/s, their pipe 72 % full; in calls back to
+// What bounds it: over long keys the tensor cores (2 x 2048 new tokens at 14336, 64
+// heads on 8 of 128, bf16: 961 us, 1672 TFLOP/s, their pipe 72 % full; in calls back to
 // back the board's power, 1120 to 1150 us), else the items' starts and ends (512 at
 // 3584: 35 us by clusters of two, 44 by the list, of which 11 were the join of 215
 // pieces; its products take 17) and, with few rows to an item, the way of a tile

@@ -620,9 +620,10 @@ lf_status lf_sample_filtered(const void *logits_device, int dtype, int rows, int
  * aligned to its type (rows of 16-byte multiples, cols a multiple of 8, are the
  * fast way).  s and the sum of its squares are fp32 (a row whose squares pass
  * 3e38 gets zeros), y is taken of s before its rounding and rounded once
- * itself.  sum_device may be x_device or residual_device, and out_device too (but
- * not sum_device), where types and strides are equal; arrays overlap in no other way.  A
- * NaN or infinity stays in its row.  rows 0 does nothing.
+ * itself (gain * s is formed first, in fp32).  sum_device may be x_device or
+ * residual_device, and out_device too (but not sum_device), where types and strides
+ * are equal; arrays overlap in no other way.  A NaN or infinity stays in its row.
+ * rows 0 does nothing.
  * LF_ERR_INVALID_ARG for bad sizes, pointers, strides or types and eps not
  * finite and above 0; LF_ERR_UNSUPPORTED for cols above 32768. */
 lf_status lf_add_rmsnorm(const void *x_device, int x_dtype, int64_t ld_x, const void *residual_device,
@@ -636,8 +637,8 @@ lf_status lf_add_rmsnorm(const void *x_device, int x_dtype, int64_t ld_x, const 
  * lf_add_rmsnorm leaves, and a weight matrix in its [out][in] layout), the scales
  * DEVICE fp32 [m] and [n] (NULL: 1), c an m x n row-major DEVICE array of c_dtype
  * (LF_F32, LF_F16 or LF_BF16).  k is a multiple of 16; m or n 0 does nothing.  The
- * products are summed in fp32 by the tensor core, scaled and rounded once; a value
- * beyond c_dtype's range becomes infinite.  *err_device (DEVICE word, cleared by the
+ * products are summed in fp32 by the tensor core, scaled (by a's scale, then by b's)
+ * and rounded once; a value beyond c_dtype's range becomes infinite.  *err_device (DEVICE word, cleared by the
  * caller) becomes 2 if a device-side wait ran out (2 s without progress, however long the
  * call takes in all); c is then unfinished.
  * LF_ERR_INVALID_ARG for bad sizes, pointers or types; LF_ERR_UNSUPPORTED where
