@@ -58,10 +58,9 @@ template <int STAGES>
 struct F8Shared {
     uint64_t full[STAGES], empty[STAGES];
     uint64_t acc_full[2], acc_empty[2];  // accumulator b computed / read back (128 arrivals)
-    uint64_t done;                       // every product this CTA issued is done (one commit at the end)
+    uint64_t done;                       // after an error: every product this CTA issued is done
     uint32_t tmem;
     volatile int abort_;
-    volatile int issued_;  // 1 once any product was issued (then done gets its commit)
 };
 
 struct F8Args {
@@ -159,7 +158,6 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
         }
         mbar_init(&S.done, 1);
         S.abort_ = 0;
-        S.issued_ = 0;
         fence_barrier_init();
         tma_prefetch_map(&tmA);
         tma_prefetch_map(&tmB);
@@ -171,7 +169,8 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
     const uint32_t tmem = S.tmem;
     pdl_wait();
     pdl_trigger();
-    int kbg = 0;  // the copying lane: stages filled so far (all tiles)
+    int kbg = 0;          // the copying lane: stages filled so far (all tiles)
+    bool issued = false;  // the lane that issues products has done so
 
     if (warp == 0) {
         if (lane == 0) {
@@ -204,7 +203,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
         auto on = [&](uint32_t bytes) { return (desc & 0xffffffff00000000ull) | (uint32_t)((uint32_t)desc + (bytes >> 4)); };
         int lt = 0, s = 0;
         uint32_t ph = 0;
-        bool ok = true, issued = false;
+        bool ok = true;
         for (int t = blockIdx.x; ok && t < ntiles; t += gridDim.x, ++lt) {
             const int b = lt & 1;
             const uint32_t acc = tmem + (uint32_t)b * BN;
@@ -220,19 +219,14 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
                         tc_mma_f8(acc, on(at), on(at + L::A), kIdesc, (kb | kk) != 0);
                     }
                     tc_commit(&S.empty[s]);
+                    issued = true;
                 }
                 __syncwarp();
-                issued = true;
                 if (++s == ST) s = 0, ph ^= 1u;
             }
             if (ok && leader) tc_commit(&S.acc_full[b]);
             __syncwarp();
         }
-        if (leader && issued) {
-            tc_commit(&S.done);  // tracks everything issued above
-            S.issued_ = 1;
-        }
-        __syncwarp();
     } else {  // warp w reads TMEM lanes 32 * (w % 4) .. + 31
         const int q = warp & 3;
         int lt = 0;
@@ -279,7 +273,8 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
             }
     }
     if (warp == 1) {
-        if (lane == 0 && S.issued_) {
+        if (issued && S.abort_) {
+            tc_commit(&S.done);  // (without an error the accumulators' readers have waited for every product)
             const uint64_t dl = global_timer_ns() + 1000000000ull;
             while (!mbar_try_wait(&S.done, 0) && global_timer_ns() < dl) {
             }
